@@ -55,7 +55,8 @@ typedef enum {
     KDA_ERR_ALIGN = -5,       /* a pointer is not 16-byte (workspace: 256-byte) aligned */
     KDA_ERR_WORKSPACE = -6,   /* workspace smaller than kda_chunk_prefill_workspace_size() */
     KDA_ERR_CUDA = -7,        /* a CUDA launch or API call failed */
-    KDA_ERR_DEVICE = -8       /* the device lacks what the kernels need (sm_103a, smem) */
+    KDA_ERR_DEVICE = -8,      /* the device lacks what the kernels need (sm_103a, smem) */
+    KDA_ERR_PAGES = -9        /* a page id outside the cache or the pool */
 } kda_status;
 
 /* Output element type of the prefill. */
@@ -356,6 +357,166 @@ int kda_fused_decode(const uint16_t *x_q, const uint16_t *x_k, const uint16_t *x
                      const float *g, const float *norm_w, float eps_l2, float eps_rms,
                      float *state, float *y,
                      int32_t num_seqs, int32_t num_heads, int32_t d_k, int32_t d_v, void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * Latent attention over a paged cache, for the layers that stand between KDA layers (24
+ * of them beside 69 KDA layers in the pages' model).
+ *
+ * A token keeps one row of KDA_MLA_ROW = 576 bf16 values: the normalised latent c (512)
+ * and the positional key p (64), both shared by all heads. With W_K, W_V the head's
+ * up-projections, the head's key is (W_K c, p) and its value W_V c:
+ *
+ *   expanded   s = scale (q_nope . (W_K c) + q_pe . p),   o = sum_j softmax(s)_j (W_V c_j)
+ *   absorbed   s = scale ((W_K^T q_nope) . c + q_pe . p),  o = W_V (sum_j softmax(s)_j c_j)
+ *
+ * The expanded form (kda_mla_prefill) costs 2 (192 + 128) operations a query, key and
+ * head and reads keys and values that the caller has expanded; the absorbed form
+ * (kda_mla_decode) costs 2 (576 + 512) and reads the cached rows alone, so it is the one
+ * for few queries. The four projections stay with the caller.
+ *
+ * The cache of one layer is num_pages pages of page_size rows; row r of page p starts at
+ * element p * page_stride + r * 576, so pages of several layers may interleave.
+ * page_size is a multiple of 16 (at most 65536); page_stride is a multiple of 8 and at
+ * least page_size * 576. Row i of sequence n is row i % page_size of page
+ * page_table[n * max_pages + i / page_size]. Entries past a sequence's rows are not read.
+ *
+ * 'status' is a device int32 or NULL. The caller sets it to 0 once; a call whose device
+ * tables turn out bad stores a kda_status there (KDA_ERR_SEQLENS for a length or offset,
+ * KDA_ERR_PAGES for a page id, KDA_ERR_CUDA for a bounded wait that gave up), and no call
+ * clears it. No bad table makes a kernel read or write outside the tensors it was given.
+ * kda_workspace_status(status, stream) reads it.
+ * --------------------------------------------------------------------------------- */
+#define KDA_MLA_LATENT 512 /* values of the latent */
+#define KDA_MLA_POS 64     /* values of the positional key */
+#define KDA_MLA_ROW 576    /* a cached row */
+#define KDA_MLA_NOPE 128   /* expanded key without position, and value, of one head */
+#define KDA_MLA_QK 192     /* expanded query of one head */
+
+/*
+ * kda_mla_append - normalise new tokens' latents, rotate their positional keys, and write
+ * both into the pages; rotate their queries' positional part in the same launch.
+ *
+ *   row = ( c / sqrt(mean(c^2) + eps) * norm_w ,  R(pos) k_pe ),   q_out = R(pos) q_pe
+ *
+ * in fp32, rounded once to bf16. R(pos) turns 32 pairs of values by the angles of the
+ * token's position: (a, b) -> (a cos - b sin, b cos + a sin), the pairs being (i, i + 32),
+ * or (2 i, 2 i + 1) with rope_interleaved. Without 'rope' nothing is rotated (the layers of
+ * the pages carry no position), and k_pe is copied.
+ *
+ * The new tokens of sequence n are rows cu_seqlens[n] .. cu_seqlens[n+1]-1; they are its
+ * last ones: row cu_seqlens[n+1] - 1 has position cache_lens[n] - 1. cache_lens thus
+ * counts the new tokens already, as kda_mla_decode() wants it. cu_seqlens == NULL: every
+ * sequence has total_tokens / num_seqs (a whole number) tokens. Rows outside every
+ * sequence's range are left alone.
+ *
+ *   c         device bf16, row t at c + t * c_stride (512 values)
+ *   k_pe      device bf16, row t at k_pe + t * k_pe_stride (64 values)
+ *   norm_w    device fp32 [512] or NULL (no normalisation: c is copied)
+ *   rope      device fp32 [rope_len, 64], 32 cosines then 32 sines a position, or NULL
+ *   q_pe, q_out  device bf16, head h of token t at t * q_token_stride + h * q_head_stride
+ *             (q_out: its own strides; 64 values), or both NULL. q_out may be q_pe itself
+ *             with the same strides. Only with 'rope'.
+ *   cu_seqlens device int32 [num_seqs + 1] or NULL; cache_lens device int32 [num_seqs];
+ *   page_table device int32 [num_seqs, max_pages]; cache device bf16, written
+ * Strides count elements and are multiples of 8; pointers are 16-byte aligned (tables: 4).
+ * The rows written by one call must be distinct. A token whose position or page is bad
+ * (position negative, past the page table, or past rope_len) writes no row and NaN into
+ * q_out, and sets 'status'.
+ */
+int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64_t k_pe_stride,
+                   const float *norm_w, float eps, const float *rope, int32_t rope_len, int32_t rope_interleaved,
+                   const uint16_t *q_pe, int64_t q_token_stride, int64_t q_head_stride,
+                   uint16_t *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t num_heads,
+                   const int32_t *cu_seqlens, const int32_t *cache_lens, const int32_t *page_table, int32_t max_pages,
+                   uint16_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
+                   int64_t total_tokens, int32_t num_seqs, int32_t *status, void *stream);
+
+/*
+ * kda_mla_gather - cached rows of a batch as dense rows, for the expanded form: out row
+ * cu_seqlens[n] + i is row i of sequence n.
+ *
+ *   cu_seqlens device int32 [num_seqs + 1]; page_table device int32 [num_seqs, max_pages];
+ *   out       device bf16 [total_rows, 576]
+ * Rows of out outside every sequence's range are left as they were; a row whose page is
+ * bad becomes NaN and sets 'status'.
+ */
+int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
+                   const int32_t *cu_seqlens, const int32_t *page_table, int32_t max_pages, uint16_t *out,
+                   int64_t total_rows, int32_t num_seqs, int32_t *status, void *stream);
+
+/*
+ * kda_mla_prefill - attention in the expanded form over packed sequences.
+ *
+ * Query row i of sequence n (n_q rows) attends to its n_k keys: all of them, or with
+ * 'causal' keys 0 .. n_k - n_q + i (the queries are the last tokens; n_k > n_q when a
+ * prefix is cached). A row that sees no key gets o = 0 and lse = -inf.
+ *
+ *   q         device bf16 [total_q, H, 192]   128 values without position, then 64 with it
+ *   kv        device bf16 [total_k, H, 256]   a head's key without position (128), then its
+ *             value (128), as one up-projection of the latents gives them
+ *   k_pe      device bf16, row j at k_pe + j * k_pe_stride (64 values): the positional keys
+ *   cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs + 1], rising from 0 or more to
+ *             total_q and total_k at most
+ *   scale     finite and > 0 (KDA_ERR_UNSUPPORTED otherwise)
+ *   o         device bf16 [total_q, H, 128] (written)
+ *   lse       device fp32 [total_q, H] or NULL: log sum_j exp(s_j)
+ * k_pe_stride is a multiple of 8 and at least 64. Rows of o and lse outside every sequence's range are
+ * left as they were. Scores, statistics and sums are fp32; the probabilities are rounded
+ * to bf16 for the product with the values. A sequence whose offsets fall or leave the
+ * tensors is not computed and sets 'status' to KDA_ERR_SEQLENS; its rows are left as they
+ * were.
+ */
+int kda_mla_prefill(const uint16_t *q, const uint16_t *kv, const uint16_t *k_pe, int64_t k_pe_stride,
+                    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int64_t total_q, int64_t total_k,
+                    int32_t num_seqs, int32_t num_heads, int32_t causal, float scale,
+                    uint16_t *o, float *lse, int32_t *status, void *stream);
+
+/* Bytes of device workspace for kda_mla_decode() with these sizes (a bound that depends
+ * on them alone); 0 for a negative argument. */
+size_t kda_mla_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens);
+
+/*
+ * kda_mla_decode - attention in the absorbed form over the paged rows, for one token a
+ * sequence or a window of up to KDA_MAX_REPLAY_TOKENS draft tokens.
+ *
+ * Sequence n has cache_lens[n] rows in the cache, its num_tokens new ones last. Token t of
+ * the window is row n * num_tokens + t and attends to rows 0 .. cache_lens[n] - num_tokens
+ * + t; where that leaves none, o = 0 and lse = -inf.
+ *
+ *   q_lat     device bf16 [N * m, H, 512]   queries carried into the latent space
+ *   q_pe      device bf16 [N * m, H, 64]    their positional part
+ *   cache, page_stride, num_pages, page_size, page_table, max_pages: as above
+ *   cache_lens device int32 [N]
+ *   scale     finite and > 0 (KDA_ERR_UNSUPPORTED otherwise)
+ *   o         device bf16 [N * m, H, 512] (written): sum_j softmax(s)_j c_j
+ *   lse       device fp32 [N * m, H] or NULL
+ *   workspace device scratch, kda_mla_decode_workspace_size() bytes, 256-byte aligned; its
+ *             contents need no initialisation and are dead after the call
+ * Calls that share a workspace must be ordered on one stream. A sequence with a negative
+ * length, one past its page table, or a bad page id gets NaN in o and lse and sets
+ * 'status'.
+ */
+int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *cache, int64_t page_stride,
+                   int32_t num_pages, int32_t page_size, const int32_t *page_table, int32_t max_pages,
+                   const int32_t *cache_lens, int32_t num_seqs, int32_t num_heads, int32_t num_tokens, float scale,
+                   uint16_t *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * kda_pages_copy - copy pages of a pool in every layer: the device side of forking a
+ * sequence (its last page, and its KDA state slot) and of compacting a cache.
+ *
+ * Page p of layer l is the page_bytes bytes at pool + l * layer_stride + p * page_stride
+ * (strides in bytes). For i = 0 .. num_pairs - 1 in order, page dst[i] becomes a copy of
+ * page src[i] in all num_layers layers; a later pair sees what an earlier one wrote.
+ *
+ *   pool      device; src, dst  HOST int32 [num_pairs], read before the call returns (a
+ *             captured call keeps the lists of its capture)
+ * page_bytes, page_stride, layer_stride and the pool's address are multiples of 16; the
+ * pages of all layers are disjoint (KDA_ERR_SHAPE otherwise). A page id outside
+ * [0, num_pages) is refused with KDA_ERR_PAGES before anything is launched.
+ */
+int kda_pages_copy(void *pool, int64_t page_stride, int64_t page_bytes, int32_t num_pages, int64_t layer_stride,
+                   int32_t num_layers, const int32_t *src, const int32_t *dst, int32_t num_pairs, void *stream);
 
 #ifdef __cplusplus
 }

@@ -168,6 +168,7 @@ const char *kda_status_string(int status) {
         case KDA_ERR_WORKSPACE: return "workspace too small";
         case KDA_ERR_CUDA: return "CUDA error";
         case KDA_ERR_DEVICE: return "device unsupported";
+        case KDA_ERR_PAGES: return "a page id outside the cache or the pool";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,157 @@
+// kda_pages_copy: page dst[i] becomes a copy of page src[i] in every layer, in list order.
+//
+// The lists are host memory and travel as kernel parameters, so the call needs no device
+// copy of them and a captured call keeps them. One launch may run its pairs in any order,
+// so the host cuts the list where order matters: a new launch starts before a pair whose
+// source or destination an earlier pair of the same launch writes, or whose destination one
+// reads. A fork or a compaction into free pages has no such pair and is one launch.
+//
+// The work is bytes alone: each moves once in and once out.
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <climits>
+
+#include "kda.h"
+
+namespace kda {
+namespace {
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnits = 4;                                        // 16-byte units a thread
+constexpr int64_t kCopyChunk = (int64_t)kCopyThreads * kCopyUnits;   // units of a block
+
+template <int CAP>
+struct CopyArgs {
+    char *pool;
+    int64_t page_stride, layer_stride;
+    int64_t units;    // 16-byte units of a page
+    int32_t chunks;   // blocks of a page
+    int32_t src[CAP], dst[CAP];
+};
+
+template <int CAP>
+__global__ void __launch_bounds__(kCopyThreads) kda_pages_copy_kernel(const __grid_constant__ CopyArgs<CAP> p) {
+    const int64_t pair = blockIdx.x / p.chunks;
+    const int64_t chunk = blockIdx.x - pair * p.chunks;
+    char *layer = p.pool + (int64_t)blockIdx.y * p.layer_stride;
+    const uint4 *s = reinterpret_cast<const uint4 *>(layer + p.src[pair] * p.page_stride);
+    uint4 *d = reinterpret_cast<uint4 *>(layer + p.dst[pair] * p.page_stride);
+    const int64_t u0 = chunk * kCopyChunk + threadIdx.x;
+    uint4 v[kCopyUnits];
+#pragma unroll
+    for (int i = 0; i < kCopyUnits; ++i)
+        if (u0 + i * kCopyThreads < p.units) v[i] = __ldcs(s + u0 + i * kCopyThreads);
+#pragma unroll
+    for (int i = 0; i < kCopyUnits; ++i)
+        if (u0 + i * kCopyThreads < p.units) __stcs(d + u0 + i * kCopyThreads, v[i]);
+}
+
+// The pages that one launch reads and writes: an open-addressing table on the stack (no
+// allocation at a C entry), at most half full.
+constexpr int kMaxPairs = 2000;
+constexpr int kTable = 8192;
+struct Touched {
+    int32_t page[kTable];
+    uint8_t how[kTable];  // 0 free, 1 read, 2 written, 3 both
+    void clear() {
+        for (int i = 0; i < kTable; ++i) how[i] = 0;
+    }
+    int slot(int32_t p) const {
+        int i = (int)(((uint32_t)p * 2654435761u) >> 19);
+        while (how[i] && page[i] != p) i = (i + 1) & (kTable - 1);
+        return i;
+    }
+    void add(int32_t p, uint8_t h) {
+        const int i = slot(p);
+        page[i] = p;
+        how[i] |= h;
+    }
+};
+
+template <int CAP>
+cudaError_t launch_copy(char *pool, int64_t page_stride, int64_t layer_stride, int64_t units, int32_t layers,
+                        const int32_t *src, const int32_t *dst, int n, cudaStream_t st) {
+    CopyArgs<CAP> a;
+    a.pool = pool;
+    a.page_stride = page_stride;
+    a.layer_stride = layer_stride;
+    a.units = units;
+    a.chunks = (int32_t)((units + kCopyChunk - 1) / kCopyChunk);
+    const int64_t most = INT32_MAX / a.chunks;  // pairs of one grid
+    for (int at = 0; at < n;) {
+        const int k = (int)((n - at) < most ? (n - at) : most);
+        for (int i = 0; i < k; ++i) {
+            a.src[i] = src[at + i];
+            a.dst[i] = dst[at + i];
+        }
+        kda_pages_copy_kernel<CAP><<<dim3((unsigned)(k * (int64_t)a.chunks), (unsigned)layers), kCopyThreads, 0, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        at += k;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" int kda_pages_copy(void *pool, int64_t page_stride, int64_t page_bytes, int32_t num_pages,
+                              int64_t layer_stride, int32_t num_layers, const int32_t *src, const int32_t *dst,
+                              int32_t num_pairs, void *stream) {
+    using namespace kda;
+    if (num_pairs < 0 || num_pages < 0 || num_layers < 0 || num_layers > 65535 || page_bytes < 0) return KDA_ERR_SHAPE;
+    if (page_stride < 0 || layer_stride < 0 || page_bytes % 16 || page_stride % 16 || layer_stride % 16)
+        return KDA_ERR_SHAPE;
+    // the pool's extent stays far inside 64 bits, and a page inside what a grid counts
+    const int64_t most = INT64_MAX >> 3;
+    if (page_bytes > ((int64_t)1 << 40) || (num_pages > 0 && page_stride > most / num_pages) ||
+        (num_layers > 0 && layer_stride > most / num_layers))
+        return KDA_ERR_SHAPE;
+    if (num_pages > 0 && num_layers > 0 && page_bytes > 0) {
+        // pages inside layers, or layers inside pages
+        const bool pages_in = (num_pages == 1 || page_stride >= page_bytes) &&
+                              (num_layers == 1 || layer_stride >= (num_pages - 1) * page_stride + page_bytes);
+        const bool layers_in = (num_layers == 1 || layer_stride >= page_bytes) &&
+                               (num_pages == 1 || page_stride >= (num_layers - 1) * layer_stride + page_bytes);
+        if (!pages_in && !layers_in) return KDA_ERR_SHAPE;
+    }
+    if (num_pairs > 0 && (!src || !dst)) return KDA_ERR_NULL;
+    for (int32_t i = 0; i < num_pairs; ++i)
+        if (src[i] < 0 || src[i] >= num_pages || dst[i] < 0 || dst[i] >= num_pages) return KDA_ERR_PAGES;
+    if (num_pairs == 0 || num_layers == 0 || page_bytes == 0) return KDA_OK;
+    if (!pool) return KDA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(pool) % 16) return KDA_ERR_ALIGN;
+
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Touched seen;
+    seen.clear();
+    int32_t from[kMaxPairs], to[kMaxPairs];
+    int n = 0;
+    const int64_t units = page_bytes / 16;
+    auto flush = [&]() {
+        char *base = static_cast<char *>(pool);
+        // the parameters are copied at every launch: 0.3 KB for the common short list
+        cudaError_t e = n <= 32 ? launch_copy<32>(base, page_stride, layer_stride, units, num_layers, from, to, n, st)
+                                : (n <= 480 ? launch_copy<480>(base, page_stride, layer_stride, units, num_layers, from,
+                                                               to, n, st)
+                                            : launch_copy<kMaxPairs>(base, page_stride, layer_stride, units, num_layers,
+                                                                     from, to, n, st));
+        n = 0;
+        seen.clear();
+        return e;
+    };
+    for (int32_t i = 0; i < num_pairs; ++i) {
+        if (src[i] == dst[i]) continue;
+        if (n == kMaxPairs || (seen.how[seen.slot(src[i])] & 2) || seen.how[seen.slot(dst[i])] != 0)
+            if (flush() != cudaSuccess) return KDA_ERR_CUDA;
+        seen.add(src[i], 1);
+        seen.add(dst[i], 2);
+        from[n] = src[i];
+        to[n] = dst[i];
+        ++n;
+    }
+    if (n > 0 && flush() != cudaSuccess) return KDA_ERR_CUDA;
+    return KDA_OK;
+}

@@ -62,6 +62,20 @@ def library():
         lib.kda_fused_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, i32, i32, i32, i32,
                                          vp]
         lib.kda_fused_decode.restype = ctypes.c_int
+        lib.kda_mla_append.argtypes = [vp, i64, vp, i64, vp, f32, vp, i32, i32, vp, i64, i64, vp, i64, i64, i32,
+                                       vp, vp, vp, i32, vp, i64, i32, i32, i64, i32, vp, vp]
+        lib.kda_mla_append.restype = ctypes.c_int
+        lib.kda_mla_gather.argtypes = [vp, i64, i32, i32, vp, vp, i32, vp, i64, i32, vp, vp]
+        lib.kda_mla_gather.restype = ctypes.c_int
+        lib.kda_mla_prefill.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, i32, i32, i32, f32, vp, vp, vp, vp]
+        lib.kda_mla_prefill.restype = ctypes.c_int
+        lib.kda_mla_decode_workspace_size.argtypes = [i32, i32, i32]
+        lib.kda_mla_decode_workspace_size.restype = ctypes.c_size_t
+        lib.kda_mla_decode.argtypes = [vp, vp, vp, i64, i32, i32, vp, i32, vp, i32, i32, i32, f32, vp, vp, vp,
+                                       ctypes.c_size_t, vp, vp]
+        lib.kda_mla_decode.restype = ctypes.c_int
+        lib.kda_pages_copy.argtypes = [vp, i64, i64, i32, i64, i32, vp, vp, i32, vp]
+        lib.kda_pages_copy.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
@@ -332,3 +346,287 @@ def kda_debug_walk_fault(skip_commit_chunk, wait_limit_ns):
     rc = library().kda_debug_walk_fault(ctypes.c_int32(skip_commit_chunk), ctypes.c_uint64(wait_limit_ns))
     if rc != 0:
         raise KdaError("kda_debug_walk_fault", rc)
+
+
+# ---- latent attention over a paged cache, and the copies of pages (include/kda.h) ----
+MLA_LATENT, MLA_POS, MLA_ROW, MLA_NOPE, MLA_QK = 512, 64, 576, 128, 192
+
+
+def _on(device, stream):
+    """Context of a latent-attention or page call: `device` current, and the given stream (or
+    that device's current one) the one that torch allocates outputs and scratch on, so that
+    their memory is not handed out again before the call's work is done."""
+    if stream is not None and stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+
+
+def _placed(device, stream):
+    """Whether a call may run as it is: `device` is current and no other stream is asked for."""
+    return stream is None and torch.cuda.current_device() == device.index
+
+
+def _mla_tensor(t, name, dtype, dim, device, tail=0):
+    """Type, rank and place of a tensor, and that its last `tail` dimensions are dense."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != dim:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError("%s must be a CUDA tensor%s" % (name, "" if device is None else " on %s" % device))
+    if tail == dim:
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return
+    want = 1
+    for d in range(dim - 1, dim - 1 - tail, -1):
+        if t.shape[d] > 1 and t.stride(d) != want:
+            raise ValueError("%s must be dense in its last %d dimensions" % (name, tail))
+        want *= t.shape[d]
+
+
+def _mla_cache(cache, page_table, num_seqs):
+    """Checks of a paged cache; returns (page_stride, num_pages, page_size, max_pages)."""
+    _mla_tensor(cache, "cache", torch.bfloat16, 3, None, 2)
+    _mla_tensor(page_table, "page_table", torch.int32, 2, cache.device, 2)
+    pages, size, row = cache.shape
+    if row != MLA_ROW:
+        raise ValueError("cache must be [num_pages, page_size, 576]")
+    if page_table.shape[0] != num_seqs:
+        raise ValueError("page_table must have a row for each of %d sequences" % num_seqs)
+    return (cache.stride(0) if pages > 1 else size * row), pages, size, page_table.shape[1]
+
+
+def _mla_ints(t, name, n, device):
+    _mla_tensor(t, name, torch.int32, 1, device, 1)
+    if t.shape[0] != n:
+        raise ValueError("%s must have %d entries, got %d" % (name, n, t.shape[0]))
+
+
+def _mla_status(status, device):
+    if status is not None:
+        _mla_tensor(status, "status", torch.int32, 1, device, 1)
+        if status.shape[0] < 1:
+            raise ValueError("status must hold one int32")
+        return status.data_ptr()
+    return None
+
+
+def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm_w=None, eps=1e-6, rope=None,
+                   rope_interleaved=False, q_pe=None, q_out=None, status=None, stream=None):
+    """Normalise and rotate new tokens' rows into the paged latent cache. Returns q_out, or None.
+
+    c: bf16 [T, 512], k_pe: bf16 [T, 64] (rows may be strided: two slices of one projection);
+    cache: bf16 [num_pages, page_size, 576], written; page_table: int32 [N, max_pages];
+    cache_lens: int32 [N], the lengths with the new tokens; cu_seqlens: int32 [N + 1], or None
+    for T / N tokens each; norm_w: fp32 [512] or None; rope: fp32 [positions, 64] (cosines, then
+    sines) or None; q_pe: bf16 [T, H, 64], rotated into q_out (allocated, dense, when not given;
+    may be q_pe itself).
+    """
+    if c.is_cuda and not _placed(c.device, stream):
+        with _on(c.device, stream):
+            return kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens, norm_w, eps, rope,
+                                  rope_interleaved, q_pe, q_out, status)
+    _mla_tensor(c, "c", torch.bfloat16, 2, None, 1)
+    dev, T = c.device, c.shape[0]
+    _mla_tensor(k_pe, "k_pe", torch.bfloat16, 2, dev, 1)
+    if c.shape[1] != MLA_LATENT or k_pe.shape[0] != T or k_pe.shape[1] != MLA_POS:
+        raise ValueError("c must be [T, 512] and k_pe [T, 64]")
+    N = cache_lens.shape[0]
+    _mla_ints(cache_lens, "cache_lens", N, dev)
+    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N)
+    if cache.device != dev:
+        raise ValueError("cache must be on %s" % dev)
+    if cu_seqlens is not None:
+        _mla_ints(cu_seqlens, "cu_seqlens", N + 1, dev)
+    if norm_w is not None:
+        _mla_tensor(norm_w, "norm_w", torch.float32, 1, dev, 1)
+        if norm_w.shape[0] != MLA_LATENT:
+            raise ValueError("norm_w must be [512]")
+    if rope is not None:
+        _mla_tensor(rope, "rope", torch.float32, 2, dev, 2)
+        if rope.shape[1] != MLA_POS:
+            raise ValueError("rope must be [positions, 64]")
+    H, qs, qos, qp, qop = 0, (0, 0), (0, 0), None, None
+    if q_pe is not None:
+        if rope is None:
+            raise ValueError("q_pe is only rotated: it needs rope")
+        _mla_tensor(q_pe, "q_pe", torch.bfloat16, 3, dev, 1)
+        H = q_pe.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, H, MLA_POS), dtype=torch.bfloat16, device=dev)
+        _mla_tensor(q_out, "q_out", torch.bfloat16, 3, dev, 1)
+        if q_pe.shape != (T, H, MLA_POS) or q_out.shape != q_pe.shape:
+            raise ValueError("q_pe and q_out must be [T, H, 64]")
+        qs, qos, qp, qop = q_pe.stride(), q_out.stride(), q_pe.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out needs q_pe")
+    rc = library().kda_mla_append(
+        c.data_ptr(), c.stride(0) if T > 1 else MLA_LATENT, k_pe.data_ptr(), k_pe.stride(0) if T > 1 else MLA_POS,
+        norm_w.data_ptr() if norm_w is not None else None, eps, rope.data_ptr() if rope is not None else None,
+        rope.shape[0] if rope is not None else 0, 1 if rope_interleaved else 0,
+        qp, qs[0], qs[1], qop, qos[0], qos[1], H,
+        cu_seqlens.data_ptr() if cu_seqlens is not None else None, cache_lens.data_ptr(), page_table.data_ptr(),
+        max_pages, cache.data_ptr(), page_stride, pages, size, T, N, _mla_status(status, dev),
+        torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise KdaError("kda_mla_append", rc)
+    return q_out
+
+
+def kda_mla_gather(cache, page_table, cu_seqlens, total_rows, out=None, status=None, stream=None):
+    """Rows of the paged latent cache as dense rows: out row cu_seqlens[n] + i is row i of
+    sequence n. cu_seqlens: int32 [N + 1] of the lengths to read. Returns out, bf16 [total_rows, 576]."""
+    if cache.is_cuda and not _placed(cache.device, stream):
+        with _on(cache.device, stream):
+            return kda_mla_gather(cache, page_table, cu_seqlens, total_rows, out, status)
+    N, dev, T = page_table.shape[0], cache.device, int(total_rows)
+    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N)
+    _mla_ints(cu_seqlens, "cu_seqlens", N + 1, dev)
+    if out is None:
+        out = torch.empty((T, MLA_ROW), dtype=torch.bfloat16, device=dev)
+    _mla_tensor(out, "out", torch.bfloat16, 2, dev, 2)
+    if out.shape != (T, MLA_ROW):
+        raise ValueError("out must be [total_rows, 576]")
+    rc = library().kda_mla_gather(cache.data_ptr(), page_stride, pages, size, cu_seqlens.data_ptr(),
+                                  page_table.data_ptr(), max_pages, out.data_ptr(), T, N, _mla_status(status, dev),
+                                  torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise KdaError("kda_mla_gather", rc)
+    return out
+
+
+def kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal=True, o=None, lse=None, status=None,
+                    stream=None):
+    """Latent attention in the expanded form over packed sequences. Returns (o, lse).
+
+    q: bf16 [Tq, H, 192]; kv: bf16 [Tk, H, 256], a head's key without position, then its value;
+    k_pe: bf16 [Tk, 64] (rows may be strided); cu_seqlens_q, cu_seqlens_k: int32 [N + 1]. With
+    causal a sequence's queries are its last tokens. o: bf16 [Tq, H, 128]; lse: fp32 [Tq, H].
+    """
+    if q.is_cuda and not _placed(q.device, stream):
+        with _on(q.device, stream):
+            return kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal, o, lse, status)
+    _mla_tensor(q, "q", torch.bfloat16, 3, None, 3)
+    dev, (Tq, H, d) = q.device, q.shape
+    _mla_tensor(kv, "kv", torch.bfloat16, 3, dev, 3)
+    _mla_tensor(k_pe, "k_pe", torch.bfloat16, 2, dev, 1)
+    Tk = kv.shape[0]
+    if d != MLA_QK or kv.shape != (Tk, H, 2 * MLA_NOPE) or k_pe.shape != (Tk, MLA_POS):
+        raise ValueError("q must be [Tq, H, 192], kv [Tk, H, 256] and k_pe [Tk, 64]")
+    N = cu_seqlens_q.shape[0] - 1
+    if N < 0:
+        raise ValueError("cu_seqlens_q must hold num_seqs + 1 offsets")
+    _mla_ints(cu_seqlens_q, "cu_seqlens_q", N + 1, dev)
+    _mla_ints(cu_seqlens_k, "cu_seqlens_k", N + 1, dev)
+    if o is None:
+        o = torch.empty((Tq, H, MLA_NOPE), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+    _mla_tensor(o, "o", torch.bfloat16, 3, dev, 3)
+    _mla_tensor(lse, "lse", torch.float32, 2, dev, 2)
+    if o.shape != (Tq, H, MLA_NOPE) or lse.shape != (Tq, H):
+        raise ValueError("o must be [Tq, H, 128] and lse [Tq, H]")
+    rc = library().kda_mla_prefill(q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), k_pe.stride(0) if Tk > 1 else MLA_POS,
+                                   cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), Tq, Tk, N, H, 1 if causal else 0,
+                                   scale, o.data_ptr(), lse.data_ptr(), _mla_status(status, dev),
+                                   torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise KdaError("kda_mla_prefill", rc)
+    return o, lse
+
+
+def kda_mla_decode_workspace_size(num_seqs, num_heads, num_tokens=1):
+    return int(library().kda_mla_decode_workspace_size(int(num_seqs), int(num_heads), int(num_tokens)))
+
+
+def kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens=1, o=None, lse=None, workspace=None,
+                   status=None, stream=None):
+    """Latent attention in the absorbed form over the paged rows. Returns (o, lse).
+
+    q_lat: bf16 [N * m, H, 512], q_pe: bf16 [N * m, H, 64] (token t of sequence n at row n * m + t,
+    m = num_tokens); cache: bf16 [num_pages, page_size, 576]; page_table: int32 [N, max_pages];
+    cache_lens: int32 [N], the lengths with the m new tokens, of which token t sees all but the
+    last m - 1 - t rows. o: bf16 [N * m, H, 512]; lse: fp32 [N * m, H]. workspace: uint8, at least
+    kda_mla_decode_workspace_size bytes (allocated when not given).
+    """
+    if cache.is_cuda and not _placed(cache.device, stream):
+        with _on(cache.device, stream):
+            return kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse, workspace,
+                                  status)
+    m, N, dev = int(num_tokens), cache_lens.shape[0], cache.device
+    _mla_tensor(q_lat, "q_lat", torch.bfloat16, 3, dev, 3)
+    _mla_tensor(q_pe, "q_pe", torch.bfloat16, 3, dev, 3)
+    rows, H = q_lat.shape[0], q_lat.shape[1]
+    if m < 0 or rows != N * m:
+        raise ValueError("q_lat has %d rows, expected num_seqs * num_tokens = %d" % (rows, N * m))
+    if q_lat.shape[2] != MLA_LATENT or q_pe.shape != (rows, H, MLA_POS):
+        raise ValueError("q_lat must be [N * m, H, 512] and q_pe [N * m, H, 64]")
+    _mla_ints(cache_lens, "cache_lens", N, dev)
+    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N)
+    if o is None:
+        o = torch.empty((rows, H, MLA_LATENT), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+    _mla_tensor(o, "o", torch.bfloat16, 3, dev, 3)
+    _mla_tensor(lse, "lse", torch.float32, 2, dev, 2)
+    if o.shape != (rows, H, MLA_LATENT) or lse.shape != (rows, H):
+        raise ValueError("o must be [N * m, H, 512] and lse [N * m, H]")
+    lib = library()
+    if workspace is None:
+        workspace = torch.empty(lib.kda_mla_decode_workspace_size(N, H, m), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    rc = lib.kda_mla_decode(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), page_stride, pages, size,
+                            page_table.data_ptr(), max_pages, cache_lens.data_ptr(), N, H, m, scale, o.data_ptr(),
+                            lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            _mla_status(status, dev), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise KdaError("kda_mla_decode", rc)
+    return o, lse
+
+
+def _page_ids(ids, name):
+    """A host list of page ids as a contiguous CPU int32 tensor."""
+    if not isinstance(ids, torch.Tensor):
+        ids = torch.tensor(list(ids), dtype=torch.int64)
+    if ids.is_cuda or ids.dim() != 1 or ids.is_floating_point() or ids.dtype == torch.bool:
+        raise ValueError("%s must be a list or a 1-D CPU tensor of page ids" % name)
+    if ids.dtype != torch.int32:
+        if ids.numel() and (int(ids.min()) < 0 or int(ids.max()) > 0x7FFFFFFF):
+            raise KdaError("kda_pages_copy", -9)
+        ids = ids.to(torch.int32)
+    return ids.contiguous()
+
+
+def kda_pages_copy(pool, src, dst, stream=None):
+    """Page dst[i] becomes a copy of page src[i] in every layer, in list order.
+
+    pool: any type, [layers, pages, ...] with each page dense; the first two dimensions may
+    be strided (a pool that keeps a page's layers together is passed transposed). src, dst:
+    lists or CPU tensors of page ids. KDA states [layers, slots, H, 128, 128] and conv states
+    are pools too. Returns pool.
+    """
+    if not pool.is_cuda or pool.dim() < 3:
+        raise ValueError("pool must be a CUDA tensor [layers, pages, ...]")
+    if not _placed(pool.device, stream):
+        with _on(pool.device, stream):
+            return kda_pages_copy(pool, src, dst)
+    want = 1
+    for d in range(pool.dim() - 1, 1, -1):
+        if pool.shape[d] > 1 and pool.stride(d) != want:
+            raise ValueError("pool must be dense within a page")
+        want *= pool.shape[d]
+    src, dst = _page_ids(src, "src"), _page_ids(dst, "dst")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    es = pool.element_size()
+    page_bytes = want * es
+    page_stride = pool.stride(1) * es if pool.shape[1] > 1 else page_bytes
+    layer_stride = pool.stride(0) * es if pool.shape[0] > 1 else page_stride * pool.shape[1]
+    rc = library().kda_pages_copy(pool.data_ptr(), page_stride, page_bytes, pool.shape[1], layer_stride,
+                                  pool.shape[0], src.data_ptr(), dst.data_ptr(), src.numel(),
+                                  torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise KdaError("kda_pages_copy", rc)
+    return pool
