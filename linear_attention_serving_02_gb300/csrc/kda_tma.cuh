@@ -1,0 +1,102 @@
+// Tiled TMA loads into 128-byte-swizzled shared memory, and the matrix descriptors that read
+// them: the operand path of the latent-attention kernels.
+//
+// A tile is cut into chunks of 64 bf16 columns (128 bytes). A chunk of R rows is R * 128
+// bytes, 1024-byte aligned; TMA stores the 16-byte unit u of row r at unit u ^ (r % 8), and
+// the tensor core undoes it. Read with the chunk's columns as the contraction (K-major),
+// 8-row groups are 1024 B apart and a step of 16 columns is 32 B further. Read with the
+// chunk's rows as the contraction (MN-major), 8-row groups are again 1024 B apart, a step of
+// 16 rows is 2048 B further, and the next 64 columns are one chunk further.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace tma {
+
+constexpr int kChunkCols = 64;  // bf16 columns of a chunk: one 128-byte swizzle row
+
+// descriptor of a K-major chunk, 16-column step s
+__device__ __forceinline__ uint64_t desc_k(uint32_t chunk_saddr, int s) {
+    return (uint64_t)(((chunk_saddr + 32u * s) >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// descriptor of an MN-major operand whose 64-column chunks are `chunk_bytes` apart, 16-row step s
+__device__ __forceinline__ uint64_t desc_mn(uint32_t chunk_saddr, uint32_t chunk_bytes, int s) {
+    return (uint64_t)(((chunk_saddr + 2048u * s) >> 4) & 0x3FFF) | ((uint64_t)((chunk_bytes >> 4) & 0x3FFF) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// instruction descriptor: kind::f16, bf16 operands, fp32 accumulator; a_mn / b_mn read that
+// operand MN-major
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, uint64_t *mbar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n" ::
+            "r"(tc::smem_addr(dst)),
+        "l"(map), "r"(tc::smem_addr(mbar)), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, uint64_t *mbar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];\n" ::"r"(tc::smem_addr(dst)),
+        "l"(map), "r"(tc::smem_addr(mbar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+// a wait by a whole warp, whose lanes agree on the outcome (what follows is warp-collective)
+__device__ __forceinline__ bool wait_warp(uint64_t *mbar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc::mbar_wait(mbar, parity));
+}
+__device__ __forceinline__ void arrive(uint64_t *mbar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_addr(mbar)) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+
+// ---- host side ----
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// the driver's encoder, looked up once a process
+inline EncodeFn encoder() {
+    static std::atomic<EncodeFn> kept{nullptr};
+    EncodeFn f = kept.load(std::memory_order_acquire);
+    if (f) return f;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+        got != cudaDriverEntryPointSuccess)
+        return nullptr;
+    f = reinterpret_cast<EncodeFn>(p);
+    kept.store(f, std::memory_order_release);
+    return f;
+}
+
+// Map of a bf16 tensor of `rank` (2 or 3) dimensions, innermost first, whose strides count
+// elements (dims 1 ..), for boxes of {64, box1, box2}. Out-of-range rows load as zeros.
+inline bool encode(CUtensorMap *map, const void *base, int rank, const uint64_t (&dim)[3], const uint64_t (&stride)[3],
+                   uint32_t box1, uint32_t box2) {
+    const EncodeFn f = encoder();
+    if (!f) return false;
+    cuuint64_t d[3], s[2];
+    for (int i = 0; i < rank; ++i) d[i] = dim[i];
+    for (int i = 1; i < rank; ++i) s[i - 1] = stride[i] * 2;
+    const cuuint32_t box[3] = {(cuuint32_t)kChunkCols, box1, box2}, one[3] = {1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, s, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tma
+}  // namespace kda
