@@ -1,74 +1,730 @@
 // Latent attention in the absorbed form over the paged rows: kda_mla_decode.
 //
-//   s_j = scale (q_lat . c_j + q_pe . p_j),  o = sum_j e^{s_j - M} c_j / sum_j e^{s_j - M}
+//   s_rj = scale (q_r . row_j),  o_r = sum_j e^{s_rj - M_r} c_j / sum_j e^{s_rj - M_r}
 //
-// one pass over the rows with a running maximum and sum. One CTA of four warps takes one
-// (token, head); the warps take every fourth row and their parts are joined at the end.
+// A query row r is one (window token, head); all m H rows of a sequence read the same cached
+// rows, and c_j is the first 512 of row_j's 576 values: one read of 1152 B serves the score
+// and the value product of every head. 2176 flop a (row, cached row).
+//
+// Work. The sequences' cached rows are cut into tiles of 64; all tiles of the batch form one
+// list, and each of G groups of CTAs takes an equal run of it, so long and short sequences
+// load every SM alike whatever their lengths. The CTAs of a group take up to 64 query rows
+// each (row tiles) and walk the same tiles at the same time, so all but the first read them
+// from L2. A sequence that a run cuts leaves partial (O, max, sum), joined by a second kernel
+// in list order; the others are finished in place. Nothing waits on another CTA.
+//
+// A tile in a CTA. TMA lays the 64 rows down once as 9 chunks of 64 columns (128-byte
+// swizzle). S = Q K^T: M = 64 query rows, N = 64 cached rows, read K-major. Four softmax warps
+// take S from TMEM, one thread a query row, and write P (bf16) to shared memory. The value
+// product runs transposed, O^T = C^T P^T: M = 128 latents (the same chunks, read MN-major),
+// N = query rows. That way O^T for 64 query rows is 4 x 64 TMEM columns and leaves room for
+// two S tiles, where O itself (64 x 512) would take every column; and a narrow batch pays
+// for its own rows only. Rescaling O^T is rare (rows' maxima must grow by 2^8).
+//
+// Shared memory. Q takes 1152 B a row; the rest is a ring of 16 KB pairs of chunks and a
+// ring of 8 KB positional chunks. The MMA warp issues whatever is ready: the next tile's
+// scores chunk by chunk as they land, or the value product of the tile whose P is written;
+// each pair of chunks is given back as soon as its 128 latents are done.
+//
+// Rows of a tile behind the sequence's length (the rest of a page, or stale shared memory)
+// may hold anything: their scores are replaced by -inf, the product's 16-row steps past the
+// length are left out, and value rows inside the last step are zeroed in shared memory.
 
+#include "kda_common.cuh"
 #include "kda_latent_common.cuh"
+#include "kda_tma.cuh"
 
 namespace kda {
 namespace {
 
+constexpr int kKvTile = 64;                     // cached rows of a tile
+constexpr int kRowTile = 64;                  // query rows of a CTA at most
+constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
+constexpr uint32_t kPairB = 2 * kChunkB;
+constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
+constexpr int kMaxPair = 12, kMaxPos = 4;     // ring slots at most
+constexpr int kDecThreads = 192;              // 4 softmax warps, the MMA warp, the TMA warp
+constexpr int kMaxGroups = 160;               // CTAs that share the list at most
+constexpr float kGrow = 8.0f;
+constexpr int kSoftmaxThreads = 128;
+
+struct DecodeGeom {
+    int32_t R;        // query rows of a sequence: m H
+    int32_t RT, rows; // row tiles and query rows of each (a multiple of 8)
+    int32_t npad;     // MMA columns of O^T: rows rounded up to 16
+    int32_t np, nr;   // ring slots
+    uint32_t smem;    // dynamic shared memory
+};
+
 struct DecodeArgs {
-    const __nv_bfloat16 *q_lat, *q_pe;
-    PagedRows<const __nv_bfloat16> cache;
-    const int32_t *lens;
-    int32_t N, H, m;
+    CUtensorMap q_lat, q_pe, cache;
+    const int32_t *table, *lens;
+    int32_t max_pages, num_pages, page_size, rb;  // rb: rows of a TMA box (64, 32 or 16)
+    int32_t N, H, m, G;
+    DecodeGeom geo;
     float scale;
     __nv_bfloat16 *o;
     float *lse;
+    float *part_o;   // [2 G, RT, rows, 512]
+    float2 *part_ml; // [2 G, RT, rows] reference maximum (raw scores), sum
+    int64_t *head;   // [0]: tiles of the batch; then per group {sequence, first tile, tiles of the sequence}
     int32_t *status;
 };
 
-__global__ void __launch_bounds__(128) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
-    __shared__ float s_o[4][kLatent], s_m[4], s_l[4];
-    __shared__ int s_bad;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x;  // (n m + t) H + h
-    const int64_t nt = row / p.H;
-    const int n = (int)(nt / p.m), t = (int)(nt % p.m);
-    const int64_t len = p.lens[n], size = p.cache.page_size;
-    if (threadIdx.x == 0) s_bad = 0;
+struct DecodeSmem {
+    uint64_t q_full, q_empty, s_full[2], p_full, pv_done, drained;
+    uint64_t pair_full[kMaxPair], pair_empty[kMaxPair], pos_full[kMaxPos], pos_empty[kMaxPos];
+    float factor[kRowTile];
+    float2 ml[kRowTile];
+    uint32_t tmem;
+    int32_t failed, bad[4];
+    int32_t first_seq, first_tile;
+    int64_t begin, end;
+    int32_t pair_issued, pos_issued, q_issued;
+};
+
+__device__ __forceinline__ bool bad_len(const DecodeArgs &p, int64_t len) {
+    return len < 0 || len > (int64_t)p.max_pages * p.page_size;
+}
+// tiles of a sequence in the list: one at least, so that every sequence's output is written
+__device__ __forceinline__ int32_t tiles_of(const DecodeArgs &p, int32_t len) {
+    return bad_len(p, len) || len == 0 ? 1 : (int32_t)(((int64_t)len + kKvTile - 1) / kKvTile);
+}
+
+// A walk over a run of the list, one stretch of tiles of one sequence after the other.
+struct Walk {
+    int32_t n, j0, j1, tiles, len;
+    int64_t left;
+    bool work;  // the sequence has cached rows and a sound length
+    __device__ __forceinline__ void open(const DecodeArgs &p) {
+        len = __ldg(p.lens + n);
+        tiles = tiles_of(p, len);
+        j1 = (int32_t)min((int64_t)tiles, j0 + left);
+        work = len > 0 && !bad_len(p, len);
+    }
+    __device__ __forceinline__ void start(const DecodeArgs &p, const DecodeSmem &sm) {
+        n = sm.first_seq;
+        j0 = sm.first_tile;
+        left = sm.end - sm.begin;
+        if (left > 0) open(p);
+    }
+    __device__ __forceinline__ bool done() const { return left <= 0; }
+    __device__ __forceinline__ void next(const DecodeArgs &p) {
+        left -= j1 - j0;
+        ++n;
+        j0 = 0;
+        if (left > 0) open(p);
+    }
+    __device__ __forceinline__ void skip_idle(const DecodeArgs &p) {
+        while (!done() && !work) next(p);
+    }
+};
+
+__device__ __forceinline__ bool test_warp(uint64_t *mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done)
+                 : "r"(tc::smem_addr(mbar)), "r"(parity)
+                 : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+}
+// barrier of the softmax warps that also tells whether any thread's flag is set
+__device__ __forceinline__ bool softmax_any(bool flag) {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)flag)
+                 : "memory");
+    return r != 0;
+}
+
+__global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const DecodeGeom &geo = p.geo;
+    const uint32_t q_chunk = (uint32_t)geo.rows * 128;
+    uint8_t *s_q = base;                               // 9 chunks of `rows` rows; M = 64 reads run on into what
+    uint8_t *s_p = s_q + 9 * q_chunk;                  // follows, whose rows of S nobody reads
+    uint8_t *s_pair = s_p + (uint32_t)geo.npad * 128;  // P: npad rows of 64 cached rows
+    uint8_t *s_pos = s_pair + (uint32_t)geo.np * kPairB;
+    DecodeSmem &sm = *reinterpret_cast<DecodeSmem *>(s_pos + (uint32_t)geo.nr * kChunkB);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rt = blockIdx.x % geo.RT, g = blockIdx.x / geo.RT;
+
+    // ---- this group's run of the list ----
+    if (warp == 0) {
+        int64_t total = 0;
+        for (int n = lane; n < p.N; n += 32) total += tiles_of(p, __ldg(p.lens + n));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+        const int64_t begin = total * g / p.G, end = total * (g + 1) / p.G;
+        int64_t before = 0;
+        int seq = p.N - 1;
+        int64_t first = 0;
+        int32_t of = 0;
+        for (int n0 = 0; n0 < p.N; n0 += 32) {
+            const int n = n0 + lane;
+            const int32_t t = n < p.N ? tiles_of(p, __ldg(p.lens + n)) : 0;
+            int64_t incl = t;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += x;
+            }
+            const int64_t lo = before + incl - t;
+            const unsigned mine = __ballot_sync(0xffffffffu, begin >= lo && begin < lo + t);
+            if (mine) {
+                const int src = __ffs(mine) - 1;
+                seq = n0 + src;
+                first = begin - __shfl_sync(0xffffffffu, lo, src);
+                of = __shfl_sync(0xffffffffu, t, src);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            sm.first_seq = seq;
+            sm.first_tile = (int32_t)first;
+            sm.begin = begin;
+            sm.end = end;
+            sm.failed = 0;
+            sm.pair_issued = sm.pos_issued = sm.q_issued = 0;
+            for (int i = 0; i < 4; ++i) sm.bad[i] = 0;
+            if (rt == 0) {
+                if (g == 0) p.head[0] = total;
+                int32_t *e = reinterpret_cast<int32_t *>(p.head + 1) + 4 * g;
+                e[0] = seq;
+                e[1] = (int32_t)first;
+                e[2] = of;
+            }
+            tc::mbar_init(&sm.q_full, 1);
+            tc::mbar_init(&sm.q_empty, 1);
+            tc::mbar_init(&sm.s_full[0], 1);
+            tc::mbar_init(&sm.s_full[1], 1);
+            tc::mbar_init(&sm.p_full, kSoftmaxThreads);
+            tc::mbar_init(&sm.pv_done, 1);
+            tc::mbar_init(&sm.drained, 1);
+            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.pair_full[i], 1), tc::mbar_init(&sm.pair_empty[i], 1);
+            for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1);
+            tc::mbar_init_fence();
+        }
+    } else if (warp == 4) {
+        tc::tmem_alloc(&sm.tmem, 512);
+    }
+    tc::fence_before_sync();
     __syncthreads();
-    const bool bad_len = len < 0 || len > (int64_t)p.cache.max_pages * size;
-    const int64_t end = bad_len ? 0 : len - p.m + 1 + t;
-    const int32_t *table = p.cache.table + (int64_t)n * p.cache.max_pages;
-    if (bad_len) {
-        if (threadIdx.x == 0) set_status(p.status, KDA_ERR_SEQLENS), s_bad = 1;
+    tc::fence_after_sync();
+    pdl_trigger();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t t_s = tmem + 256;  // two S tiles of 64 columns behind O^T (4 x npad columns)
+    const int row_first = rt * geo.rows, rows_here = min(geo.rows, geo.R - row_first);
+    bool ok = true;
+
+    if (warp == 5) {
+        // ---- TMA producer: the warp holds the places of the next 32 boxes of rows ----
+        Walk w;
+        w.start(p, sm);
+        w.skip_idle(p);
+        int seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
+        const int sub = kKvTile / p.rb;  // boxes of a tile's chunk
+        while (!w.done() && ok) {
+            const int32_t *table = p.table + (int64_t)w.n * p.max_pages;
+            const int64_t u0 = (int64_t)w.j0 * sub;
+            int32_t page_next = 0;
+            auto look = [&](int64_t u) {  // page of box u, num_pages (loads as zeros) when it is bad, 0 past the end
+                const int64_t row = u * p.rb;
+                if (row >= w.len) return 0;
+                const int32_t pg = __ldg(table + row / p.page_size);
+                return pg < 0 || pg >= p.num_pages ? -1 : pg;
+            };
+            page_next = look(u0 + lane);
+            ok = seg == 0 || tma::wait_warp(&sm.q_empty, (seg - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                sm.bad[seg & 3] = 0;
+                const int row = (int)((int64_t)w.n * geo.R + row_first);
+                tc::mbar_arrive_expect_tx(&sm.q_full, 9 * q_chunk);
+                for (int c = 0; c < 8; ++c) tma::load_2d(s_q + c * q_chunk, &p.q_lat, &sm.q_full, 64 * c, row);
+                tma::load_2d(s_q + 8 * q_chunk, &p.q_pe, &sm.q_full, 0, row);
+                ++sm.q_issued;
+            }
+            int32_t page = 0;
+            for (int j = w.j0; j < w.j1 && ok; ++j) {
+                const int at = (int)(((int64_t)(j - w.j0) * sub) & 31);
+                if (at == 0) {
+                    page = page_next;
+                    if (__any_sync(0xffffffffu, page < 0)) {
+                        // only boxes of this stretch count: another CTA reports its own
+                        const int64_t u = (int64_t)j * sub + lane;
+                        if (__any_sync(0xffffffffu, page < 0 && u < (int64_t)w.j1 * sub) && lane == 0) {
+                            sm.bad[seg & 3] = 1;
+                            set_status(p.status, KDA_ERR_PAGES);
+                        }
+                    }
+                    page_next = look((int64_t)j * sub + 32 + lane);
+                }
+                const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
+                int pg[4], ry[4];
+                for (int b = 0; b < 4; ++b) {
+                    const int x = __shfl_sync(0xffffffffu, page, (at + b) & 31);
+                    pg[b] = x < 0 ? p.num_pages : x;
+                    ry[b] = (int)(((int64_t)j * kKvTile + b * p.rb) % p.page_size);
+                }
+                const uint32_t bytes = (uint32_t)boxes * p.rb * 128;
+                ok = tma::wait_warp(&sm.pos_empty[rs], rph ^ 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(&sm.pos_full[rs], bytes);
+                    for (int b = 0; b < boxes; ++b)
+                        tma::load_3d(s_pos + rs * kChunkB + b * p.rb * 128, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
+                    ++sm.pos_issued;
+                }
+                if (++rs == geo.nr) rs = 0, rph ^= 1;
+                for (int i = 0; i < kPairs && ok; ++i) {
+                    ok = tma::wait_warp(&sm.pair_empty[ps], pph ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        tc::mbar_arrive_expect_tx(&sm.pair_full[ps], 2 * bytes);
+                        for (int c = 0; c < 2; ++c)
+                            for (int b = 0; b < boxes; ++b)
+                                tma::load_3d(s_pair + ps * kPairB + c * kChunkB + b * p.rb * 128, &p.cache,
+                                             &sm.pair_full[ps], 128 * i + 64 * c, ry[b], pg[b]);
+                        ++sm.pair_issued;
+                    }
+                    if (++ps == geo.np) ps = 0, pph ^= 1;
+                }
+            }
+            ++seg;
+            w.next(p);
+            w.skip_idle(p);
+        }
+        if (!ok) sm.failed = 1;
+    } else if (warp == 4) {
+        // ---- MMA issuer: whatever is ready ----
+        const uint32_t idS = tma::idesc(64, kKvTile, 0, 0), idO = tma::idesc(128, geo.npad, 1, 0);
+        Walk ws, wp;  // of the score products, of the value products
+        ws.start(p, sm);
+        ws.skip_idle(p);
+        wp = ws;
+        int js = ws.j0, jp = wp.j0;        // tile of each
+        int sk = 0, pk = 0, sseg = 0;      // tiles issued, score stretches opened
+        int cs = 0;                        // score chunks of the open tile: 0 positional, 1 .. 4 pairs
+        int s_ps = 0, s_pph = 0, s_rs = 0, s_rph = 0, v_ps = 0;
+        bool q_ready = false;
+        uint64_t since = 0;
+        uint32_t idle = 0;
+        while (!wp.done()) {
+            bool moved = false;
+            if (!ws.done() && sk <= pk + 1) {  // the S tile two back has been read
+                if (!q_ready) q_ready = test_warp(&sm.q_full, sseg & 1);
+                if (q_ready) {
+                    const bool ready = cs == 0 ? test_warp(&sm.pos_full[s_rs], s_rph) : test_warp(&sm.pair_full[s_ps], s_pph);
+                    if (ready) {
+                        moved = true;
+                        const uint32_t d = t_s + (sk & 1) * 64;
+                        if (cs == 0) {
+                            if (lane == 0) {
+                                const uint32_t a = tc::smem_addr(s_q + 8 * q_chunk), b = tc::smem_addr(s_pos + s_rs * kChunkB);
+#pragma unroll
+                                for (int s = 0; s < 4; ++s) tc::mma_ss(d, tma::desc_k(a, s), tma::desc_k(b, s), idS, s != 0);
+                                tc::commit(&sm.pos_empty[s_rs]);
+                            }
+                            if (++s_rs == geo.nr) s_rs = 0, s_rph ^= 1;
+                        } else {
+                            if (lane == 0) {
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const uint32_t a = tc::smem_addr(s_q + (2 * (cs - 1) + c) * q_chunk);
+                                    const uint32_t b = tc::smem_addr(s_pair + s_ps * kPairB + c * kChunkB);
+#pragma unroll
+                                    for (int s = 0; s < 4; ++s) tc::mma_ss(d, tma::desc_k(a, s), tma::desc_k(b, s), idS, 1);
+                                }
+                            }
+                            if (++s_ps == geo.np) s_ps = 0, s_pph ^= 1;
+                        }
+                        if (++cs == 1 + kPairs) {
+                            cs = 0;
+                            ++js;
+                            if (lane == 0) {
+                                tc::commit(&sm.s_full[sk & 1]);
+                                if (js == ws.j1) tc::commit(&sm.q_empty);
+                            }
+                            ++sk;
+                            if (js == ws.j1) {
+                                ws.next(p);
+                                ws.skip_idle(p);
+                                js = ws.j0;
+                                ++sseg;
+                                q_ready = false;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (pk < sk && test_warp(&sm.p_full, pk & 1)) {
+                moved = true;
+                tc::fence_after_sync();
+                const int valid = min(kKvTile, wp.len - jp * kKvTile), steps = (valid + 15) / 16;
+                if (valid & 15) {  // value rows behind the sequence in the last step
+                    int slot = v_ps;
+                    const int units = (16 * steps - valid) * 8;
+                    for (int i = 0; i < kPairs; ++i) {
+                        for (int c = 0; c < 2; ++c)
+                            for (int u = lane; u < units; u += 32)
+                                reinterpret_cast<uint4 *>(s_pair + slot * kPairB + c * kChunkB)[valid * 8 + u] =
+                                    make_uint4(0, 0, 0, 0);
+                        if (++slot == geo.np) slot = 0;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+                const uint32_t b = tc::smem_addr(s_p);
+                for (int i = 0; i < kPairs; ++i) {
+                    if (lane == 0) {
+                        const uint32_t a = tc::smem_addr(s_pair + v_ps * kPairB);
+                        for (int s = 0; s < steps; ++s)
+                            tc::mma_ss(tmem + i * geo.npad, tma::desc_mn(a, kChunkB, s), tma::desc_k(b, s), idO,
+                                       (jp != wp.j0) | (s != 0));
+                        tc::commit(&sm.pair_empty[v_ps]);
+                    }
+                    if (++v_ps == geo.np) v_ps = 0;
+                }
+                if (lane == 0) tc::commit(&sm.pv_done);
+                __syncwarp();
+                ++pk;
+                if (++jp == wp.j1) {
+                    wp.next(p);
+                    wp.skip_idle(p);
+                    jp = wp.j0;
+                }
+            }
+            if (moved) {
+                idle = 0;
+            } else if ((++idle & 63) == 0) {
+                const uint64_t now = tc::globaltimer();
+                if (idle == 64)
+                    since = now;
+                else if (__any_sync(0xffffffffu, now - since > tc::kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+            }
+        }
+        if (!ok) sm.failed = 1;
     } else {
-        for (int64_t i = threadIdx.x; i < (len + size - 1) / size; i += blockDim.x)
-            if (table[i] < 0 || table[i] >= p.cache.num_pages) set_status(p.status, KDA_ERR_PAGES), s_bad = 1;
+        // ---- softmax: one thread a query row (16 lanes of each warp), then the output ----
+        const int r = warp * 16 + lane;  // this thread's row, when lane < 16
+        const bool owner = lane < 16 && r < rows_here, warp_rows = warp * 16 < rows_here;
+        const int t = (row_first + (owner ? r : 0)) / p.H;  // its window token
+        const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+        const float c = p.scale * 1.4426950408889634f;
+        const uint64_t c2 = pk2(c, c);
+        int k = 0, seg = 0;  // tiles and stretches worked on
+        Walk w;
+        for (w.start(p, sm); !w.done() && ok; w.next(p)) {
+            float m_ref = -INFINITY, l = 0.f;
+            const int64_t keys = (int64_t)w.len - p.m + 1 + t;  // cached rows that the row sees
+            if (w.work) {
+                for (int j = w.j0; j < w.j1; ++j, ++k) {
+                    ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1);
+                    // a failed wait still meets the barrier below, so that no warp is left in it
+                    if (ok) tc::fence_after_sync();
+                    uint32_t s[2][32];
+                    float mx = -INFINITY;
+                    if (warp_rows && ok) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) tc::tmem_ld32_nowait(t_s + quarter + (k & 1) * 64 + 32 * i, s[i]);
+                        tc::tmem_wait_ld();
+                        const int64_t valid = keys - (int64_t)j * kKvTile;
+                        if (__any_sync(0xffffffffu, valid < kKvTile)) {
+                            const int v = (int)max((int64_t)-1, min((int64_t)kKvTile, valid));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * i + e >= v) s[i][e] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])));
+                    }
+                    bool grown = owner && (mx - m_ref) * c > kGrow;  // also from -inf to a finite maximum
+                    if (j == w.j0) {
+                        m_ref = mx;
+                        grown = false;
+                    }
+                    // one barrier a tile: does any row need its O^T column rescaled, did any wait fail
+                    const bool any = softmax_any(grown || !ok);
+                    const bool wait_pv = k > 0;
+                    if (wait_pv) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                    if (any) {
+                        if (lane < 16) {
+                            const float f = grown ? tc::ex2((m_ref - mx) * c) : 1.0f;
+                            sm.factor[r] = f;
+                            l *= f;
+                            if (grown) m_ref = mx;
+                        }
+                        // the flags again, now that everyone's waits are through: all stop together
+                        if (softmax_any(!ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        for (int i = 0; i < kPairs; ++i)
+                            for (int e = 0; e < geo.npad; e += 16) {
+                                const uint32_t at = tmem + quarter + i * geo.npad + e;
+                                uint32_t x[16];
+                                tc::tmem_ld8_nowait(at, *reinterpret_cast<uint32_t(*)[8]>(&x[0]));
+                                tc::tmem_ld8_nowait(at + 8, *reinterpret_cast<uint32_t(*)[8]>(&x[8]));
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int y = 0; y < 16; ++y)
+                                    x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[e + y]);
+                                tc::tmem_st16(at, x);
+                            }
+                        tc::tmem_wait_st();
+                    }
+                    if (warp_rows && ok) {
+                        const float mb = m_ref == -INFINITY ? 0.f : -m_ref * c;
+                        const uint64_t nmb2 = pk2(mb, mb);
+                        uint64_t l2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+                        uint8_t *row = s_p + r * 128;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {  // eight 16-byte units of the row, swizzled
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t *x = &s[u >> 2][8 * (u & 3) + 2 * e];
+                                const float2 y = upk2(fma2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, nmb2));
+                                const float a = tc::ex2(y.x), b = tc::ex2(y.y);
+                                l2[e & 1] = add2(l2[e & 1], pk2(a, b));
+                                const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
+                                h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                            }
+                            if (lane < 16) *reinterpret_cast<uint4 *>(row + ((u ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                        const float2 ls = upk2(add2(l2[0], l2[1]));
+                        l += ls.x + ls.y;
+                        fence_proxy_async();
+                    }
+                    tc::fence_before_sync();
+                    tma::arrive(&sm.p_full);
+                }
+                if (ok && !w.done()) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
+                if (softmax_any(!ok)) ok = false;
+                tc::fence_after_sync();
+            }
+            // ---- this stretch's part of the sequence: finished, or left for the join ----
+            const bool whole = w.j0 == 0 && w.j1 == w.tiles;
+            const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg & 3] != 0);
+            if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
+            const int64_t row0 = (int64_t)w.n * geo.R + row_first;
+            const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.rows;
+            if (lane < 16 && r < kRowTile) {
+                sm.factor[r] = bad ? NAN : (!whole ? 1.0f : (l == 0.f ? 0.f : 1.0f / l));
+                if (owner) {
+                    if (whole) {
+                        if (p.lse) p.lse[row0 + r] = bad ? NAN : (l == 0.f ? -INFINITY : m_ref * p.scale + logf(l));
+                    } else {
+                        p.part_ml[part0 + r] = make_float2(m_ref, bad ? NAN : l);
+                    }
+                }
+            }
+            named_sync(2, kSoftmaxThreads);
+            for (int i = 0; i < kPairs; ++i)
+                for (int e = 0; e < rows_here; e += 16) {
+                    uint32_t x[16];
+                    if (w.work && ok) {
+                        const uint32_t at = tmem + quarter + i * geo.npad + e;
+                        tc::tmem_ld8_nowait(at, *reinterpret_cast<uint32_t(*)[8]>(&x[0]));
+                        tc::tmem_ld8_nowait(at + 8, *reinterpret_cast<uint32_t(*)[8]>(&x[8]));
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) x[y] = 0;
+                    }
+                    const int lat = 128 * i + 32 * warp + lane;
+                    if (whole) {
+#pragma unroll
+                        for (int y = 0; y < 16; y += 2) {
+                            // neighbouring lanes trade a value: each then holds two latents of one row
+                            const float a = __uint_as_float(x[y]) * sm.factor[e + y];
+                            const float b = __uint_as_float(x[y + 1]) * sm.factor[e + y + 1];
+                            const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+                            const __nv_bfloat162 h = (lane & 1) ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
+                            const int rr = e + y + (lane & 1);
+                            if (rr < rows_here)
+                                *reinterpret_cast<__nv_bfloat162 *>(p.o + (row0 + rr) * kLatent + (lat & ~1)) = h;
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            if (e + y < rows_here) p.part_o[(part0 + e + y) * kLatent + lat] = __uint_as_float(x[y]) * sm.factor[e + y];
+                    }
+                }
+            // O^T has been read: the next stretch's P (all threads arrive) lets the MMA warp write it
+            tc::fence_before_sync();
+            named_sync(2, kSoftmaxThreads);
+            if (w.work) ++seg;
+        }
+        if (!ok) sm.failed = 1;
     }
+    tc::fence_before_sync();
     __syncthreads();
-    const bool bad = s_bad;
-    float q[18], o[16], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < 16; ++i) q[i] = __bfloat162float(p.q_lat[row * kLatent + lane + 32 * i]) * p.scale, o[i] = 0.f;
-    for (int i = 0; i < 2; ++i) q[16 + i] = __bfloat162float(p.q_pe[row * kPos + lane + 32 * i]) * p.scale;
-    for (int64_t j = warp; j < end && !bad; j += 4) {
-        const __nv_bfloat16 *r = p.cache.rows + table[j / size] * p.cache.page_stride + (j % size) * kRow;
-        float x[18], s = 0.f;
-        for (int i = 0; i < 18; ++i) x[i] = __bfloat162float(r[lane + 32 * i]), s += q[i] * x[i];
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float f = expf(m - base), e = expf(s - base);
-        l = l * f + e;
-        for (int i = 0; i < 16; ++i) o[i] = o[i] * f + e * x[i];
-        m = mn;
+    if (sm.failed && warp == 4) {
+        // a wait gave up: report it, and let what is in flight land before the memory goes
+        if (lane == 0) {
+            set_status(p.status, KDA_ERR_CUDA);
+            tc::commit(&sm.drained);
+            tc::mbar_wait(&sm.drained, 0);
+            if (sm.q_issued > 0) tc::mbar_wait(&sm.q_full, (sm.q_issued - 1) & 1);
+            for (int e = max(0, sm.pair_issued - geo.np); e < sm.pair_issued; ++e)
+                tc::mbar_wait(&sm.pair_full[e % geo.np], (e / geo.np) & 1);
+            for (int e = max(0, sm.pos_issued - geo.nr); e < sm.pos_issued; ++e)
+                tc::mbar_wait(&sm.pos_full[e % geo.nr], (e / geo.nr) & 1);
+        }
+        __syncwarp();
     }
-    for (int i = 0; i < 16; ++i) s_o[warp][lane + 32 * i] = o[i];
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    if (warp == 4) tc::tmem_dealloc(tmem, 512);
+}
+
+// The join of the sequences that a run's border cuts. Block x belongs to the border before
+// group x + 1; the first border inside a sequence joins it. W warps share a row's parts,
+// each lane 16 of the 512 latents; the parts are added in list order within a warp and the
+// warps' sums in warp order, so the result does not depend on timing.
+constexpr int kJoinThreads = 512;
+template <int W>
+__global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid_constant__ DecodeArgs p) {
+    constexpr int kRows = kJoinThreads / 32 / W;  // rows of a block
+    __shared__ float s_o[kRows][W][kLatent];
+    __shared__ float s_m[kRows][W], s_l[kRows][W];
+    pdl_wait();
+    const int b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t total = p.head[0];
+    const int32_t *e = reinterpret_cast<const int32_t *>(p.head + 1) + 4 * b;
+    const int64_t at = total * b / p.G;
+    if (at >= total) return;
+    const int32_t n = e[0], inside = e[1], tiles = e[2];
+    const int64_t first = at - inside;  // list index of the sequence's first tile
+    if (inside == 0 || total * (b - 1) / p.G > first) return;
+    const int rl = warp / W, part = warp % W, rr = blockIdx.y * kRows + rl;
+    const bool live = rr < p.geo.R;
+    const int rt = (live ? rr : 0) / p.geo.rows, r = (live ? rr : 0) % p.geo.rows;
+    const float c = p.scale * 1.4426950408889634f;
+    // parts: group b - 1 (slot 1, it holds the sequence's start), then groups b, b + 1, ... while they begin inside
+    int last = b;
+    while (last + 1 < p.G && total * (last + 1) / p.G < first + tiles) ++last;
+    const int count = last - (b - 1) + 1;
+    float m = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    auto row_of = [&](int i) {
+        const int64_t gq = b - 1 + i;
+        return ((2 * gq + (i == 0 ? 1 : 0)) * p.geo.RT + rt) * p.geo.rows + r;
+    };
+    auto empty = [&](int i) {  // a group between may have no tile at all
+        const int64_t gq = b - 1 + i;
+        return total * gq / p.G == total * (gq + 1) / p.G;
+    };
+    if (live) {
+        // the common maximum of this warp's parts first, then one weighted sum
+        for (int i = part + W * lane; i < count; i += W * 32)
+            if (!empty(i)) m = fmaxf(m, p.part_ml[row_of(i)].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+        for (int i = part; i < count; i += W) {
+            if (empty(i)) continue;
+            const int64_t q = row_of(i);
+            const float2 ml = p.part_ml[q];
+            const float f = tc::ex2((ml.x - ms) * c);
+            l += f * ml.y;
+            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + q * kLatent) + lane;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float4 x = __ldcs(src + 32 * v);
+                o[4 * v] += f * x.x;
+                o[4 * v + 1] += f * x.y;
+                o[4 * v + 2] += f * x.z;
+                o[4 * v + 3] += f * x.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<float4 *>(&s_o[rl][part][4 * (32 * v + lane)]) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+    if (lane == 0) s_m[rl][part] = m, s_l[rl][part] = l;
     __syncthreads();
-    float M = -INFINITY, L = 0.f, f[4];
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w]);
-    for (int w = 0; w < 4; ++w) f[w] = s_l[w] == 0.f ? 0.f : expf(s_m[w] - M), L += f[w] * s_l[w];
-    const float inv = bad ? NAN : (L == 0.f ? 0.f : 1.f / L);
-    for (int i = threadIdx.x; i < kLatent; i += 128) {
-        float v = 0.f;
-        for (int w = 0; w < 4; ++w) v += f[w] * s_o[w][i];
-        p.o[row * kLatent + i] = __float2bfloat16(v * inv);
+    if (!live) return;
+    float M = -INFINITY, L = 0.f;
+    for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[rl][i]);
+    const float Ms = M == -INFINITY ? 0.f : M;
+    float f[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        f[i] = tc::ex2((s_m[rl][i] - Ms) * c);
+        L += f[i] * s_l[rl][i];
     }
-    if (p.lse && threadIdx.x == 0) p.lse[row] = bad ? NAN : M + logf(L);
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+    const int64_t row = (int64_t)n * p.geo.R + rr;
+    if (part == 0 && lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M * p.scale + logf(L);
+    for (int x = 2 * (part * 32 + lane); x < kLatent; x += 2 * 32 * W) {
+        float a = 0.f, bb = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            a += f[i] * s_o[rl][i][x];
+            bb += f[i] * s_o[rl][i][x + 1];
+        }
+        *reinterpret_cast<__nv_bfloat162 *>(p.o + row * kLatent + x) = __floats2bfloat162_rn(a * inv, bb * inv);
+    }
+}
+
+constexpr size_t kSmemMax = 232448;
+
+// Row tiles of equal size, as few as 64 rows each allow; the rings take what Q and P leave.
+DecodeGeom geometry(int32_t H, int32_t m) {
+    DecodeGeom q{};
+    q.R = H * m;
+    q.RT = (q.R + kRowTile - 1) / kRowTile;
+    q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
+    q.npad = (q.rows + 15) / 16 * 16;
+    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + (size_t)q.npad * 128;
+    const size_t room = kSmemMax - fixed;
+    q.nr = 2;
+    q.np = (int32_t)((room - q.nr * kChunkB) / kPairB);
+    if (q.np > kMaxPair) q.np = kMaxPair;
+    const size_t extra = room - q.nr * kChunkB - (size_t)q.np * kPairB;
+    if (extra >= kChunkB) ++q.nr;
+    q.smem = (uint32_t)(fixed + (size_t)q.np * kPairB + (size_t)q.nr * kChunkB);
+    return q;
+}
+static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * 64 * 128 >= 8 * kPairB + 2 * kChunkB, "two tiles of 64 rows' rings");
+
+// groups of CTAs that share the list: one CTA an SM
+int32_t groups_of(int32_t RT, int32_t sms) { return sms / RT > 0 ? sms / RT : 1; }
+
+struct DecodeWs {
+    size_t head, ml, o, total;
+};
+DecodeWs decode_ws(const DecodeGeom &q) {
+    DecodeWs w;
+    const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = 2 * G * q.RT * q.rows;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.head = 0;
+    w.ml = up(8 + 16 * G);
+    w.o = w.ml + up(parts * sizeof(float2));
+    w.total = w.o + parts * kLatent * sizeof(float);
+    return w;
+}
+
+template <int W>
+cudaError_t launch_join(const DecodeArgs &a, cudaStream_t st) {
+    const int rows = kJoinThreads / 32 / W;
+    return launch_after(kda_mla_join_kernel<W>, dim3(a.G - 1, (a.geo.R + rows - 1) / rows), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace
@@ -78,7 +734,8 @@ extern "C" {
 
 size_t kda_mla_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens) {
     if (num_seqs < 0 || num_heads < 0 || num_tokens < 0) return 0;
-    return 256;
+    if ((int64_t)num_heads * num_tokens > INT32_MAX / 2 || num_heads == 0 || num_tokens == 0) return 256;
+    return kda::decode_ws(kda::geometry(num_heads, num_tokens)).total;
 }
 
 int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *cache, int64_t page_stride,
@@ -92,6 +749,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (num_seqs < 0 || num_heads <= 0 || num_tokens < 0 || num_heads > 65535 ||
         (int64_t)num_seqs * num_heads * num_tokens > INT32_MAX)
         return KDA_ERR_SHAPE;
+    if (page_stride >= ((int64_t)1 << 38)) return KDA_ERR_SHAPE;
     if (num_seqs == 0 || num_tokens == 0) return KDA_OK;
     if (!q_lat || !q_pe || !cache || !page_table || !cache_lens || !o || !workspace) return KDA_ERR_NULL;
     if (!mla_aligned(q_lat, 16) || !mla_aligned(q_pe, 16) || !mla_aligned(cache, 16) || !mla_aligned(o, 16) ||
@@ -99,20 +757,58 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
         !mla_aligned(workspace, 256))
         return KDA_ERR_ALIGN;
     if (workspace_bytes < kda_mla_decode_workspace_size(num_seqs, num_heads, num_tokens)) return KDA_ERR_WORKSPACE;
-    DecodeArgs a{reinterpret_cast<const __nv_bfloat16 *>(q_lat),
-                 reinterpret_cast<const __nv_bfloat16 *>(q_pe),
-                 {reinterpret_cast<const __nv_bfloat16 *>(cache), page_stride, num_pages, page_size, page_table, max_pages},
-                 cache_lens,
-                 num_seqs,
-                 num_heads,
-                 num_tokens,
-                 scale,
-                 reinterpret_cast<__nv_bfloat16 *>(o),
-                 lse,
-                 status};
-    kda_mla_decode_kernel<<<(unsigned)((int64_t)num_seqs * num_tokens * num_heads), 128, 0,
-                            static_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    int sms = 0, device = 0;
+    rc = device_sms(&sms, &device);
+    if (rc != KDA_OK) return rc;
+    if (device >= 64) return KDA_ERR_DEVICE;
+
+    DecodeArgs a;
+    a.geo = geometry(num_heads, num_tokens);
+    const DecodeWs w = decode_ws(a.geo);
+    a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
+    const uint64_t rows = (uint64_t)num_seqs * a.geo.R;
+    const uint64_t dl[3] = {kLatent, rows, 0}, sl[3] = {1, kLatent, 0}, dp[3] = {kPos, rows, 0}, sp[3] = {1, kPos, 0};
+    // a cache without pages keeps one page of extent: no id is in range, nothing loads from it
+    const uint64_t dc[3] = {kRow, (uint64_t)page_size, (uint64_t)(num_pages > 0 ? num_pages : 1)};
+    const uint64_t sc[3] = {1, kRow, (uint64_t)page_stride};
+    if (!tma::encode(&a.q_lat, q_lat, 2, dl, sl, a.geo.rows, 1) || !tma::encode(&a.q_pe, q_pe, 2, dp, sp, a.geo.rows, 1) ||
+        !tma::encode(&a.cache, cache, 3, dc, sc, a.rb, 1))
+        return KDA_ERR_CUDA;
+    a.table = page_table;
+    a.lens = cache_lens;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.N = num_seqs;
+    a.H = num_heads;
+    a.m = num_tokens;
+    // no more groups than the longest page tables could give tiles to
+    const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
+    a.G = groups_of(a.geo.RT, sms < kMaxGroups ? sms : kMaxGroups);
+    if (a.G > most) a.G = (int32_t)most;
+    a.scale = scale;
+    a.o = reinterpret_cast<__nv_bfloat16 *>(o);
+    a.lse = lse;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.head = reinterpret_cast<int64_t *>(ws + w.head);
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
+    a.status = status;
+    static std::atomic<bool> configured[64];
+    if (!configured[device].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kda_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        configured[device].store(true, std::memory_order_release);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kda_mla_decode_kernel<<<(unsigned)(a.G * a.geo.RT), kDecThreads, a.geo.smem, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    if (a.G > 1) {
+        // sequences of many parts: a block's 16 warps share a row; few parts: four warps a row
+        const cudaError_t e = num_seqs * (int64_t)8 <= a.G ? launch_join<16>(a, st) : launch_join<4>(a, st);
+        if (e != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
 }
 
 }  // extern "C"
