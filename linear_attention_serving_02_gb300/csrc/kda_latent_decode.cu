@@ -8,18 +8,25 @@
 //
 // Work. The sequences' cached rows are cut into tiles of 64; all tiles of the batch form one
 // list, and each of G groups of CTAs takes an equal run of it, so long and short sequences
-// load every SM alike whatever their lengths. The CTAs of a group take up to 64 query rows
+// load every SM alike whatever their lengths. The CTAs of a group take up to 96 query rows
 // each (row tiles) and walk the same tiles at the same time, so all but the first read them
 // from L2. A sequence that a run cuts leaves partial (O, max, sum), joined by a second kernel
 // in list order; the others are finished in place. Nothing waits on another CTA.
 //
 // A tile in a CTA. TMA lays the 64 rows down once as 9 chunks of 64 columns (128-byte
-// swizzle). S = Q K^T: M = 64 query rows, N = 64 cached rows, read K-major. Four softmax warps
-// take S from TMEM, one thread a query row, and write P (bf16) to shared memory. The value
-// product runs transposed, O^T = C^T P^T: M = 128 latents (the same chunks, read MN-major),
-// N = query rows. That way O^T for 64 query rows is 4 x 64 TMEM columns and leaves room for
-// two S tiles, where O itself (64 x 512) would take every column; and a narrow batch pays
-// for its own rows only. Rescaling O^T is rare (rows' maxima must grow by 2^8).
+// swizzle). Both products run transposed, with the cached rows as the A operand: an MMA pays
+// about 30 (M = 64) or 45 (M = 128) cycles for A and 0.48 for each column of N (measured, one
+// CTA), so a narrow batch pays for its own query rows only and up to 96 rows share one read
+// of A. S^T = K Q^T: M = 64 cached rows, N = query rows, K-major. Eight softmax warps take S^T
+// from TMEM, one thread a cached row and up to 48 query rows, and write P (bf16) to shared
+// memory. O^T = C^T P: M = 128 latents (the same chunks, read MN-major), N = query rows.
+// TMEM: O^T takes 4 N columns and S^T N, or 2 N where that fits (N <= 80).
+//
+// A thread of S^T sees one cached row, so a row maximum would be a reduction over lanes. It is
+// not needed: the reference M_r only has to stay within 2^8 of the maximum, so a tile costs a
+// comparison a score, and the reduction runs on a sequence's first tile and where a score
+// passes its reference by 2^8 (then O^T is rescaled too). Each thread keeps its own partial
+// sums of p, reduced once at the end.
 //
 // Shared memory. Q takes 1152 B a row; the rest is a ring of 16 KB pairs of chunks and a
 // ring of 8 KB positional chunks. The MMA warp issues whatever is ready: the next tile's
@@ -38,20 +45,22 @@ namespace kda {
 namespace {
 
 constexpr int kKvTile = 64;                     // cached rows of a tile
-constexpr int kRowTile = 64;                  // query rows of a CTA at most
+constexpr int kRowTile = 96;                  // query rows of a CTA at most
 constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
 constexpr int kMaxPair = 12, kMaxPos = 4;     // ring slots at most
-constexpr int kDecThreads = 192;              // 4 softmax warps, the MMA warp, the TMA warp
+constexpr int kDecThreads = 320;              // 8 softmax warps, the MMA warp, the TMA warp
 constexpr int kMaxGroups = 160;               // CTAs that share the list at most
 constexpr float kGrow = 8.0f;
-constexpr int kSoftmaxThreads = 128;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kGroups = kRowTile / 16 / 2;    // 16-column groups of S^T that a thread takes at most
 
 struct DecodeGeom {
     int32_t R;        // query rows of a sequence: m H
     int32_t RT, rows; // row tiles and query rows of each (a multiple of 8)
-    int32_t npad;     // MMA columns of O^T: rows rounded up to 16
+    int32_t npad;     // MMA columns: rows rounded up to 16
+    int32_t sbufs;    // S^T tiles in TMEM: 2 where they fit, else 1
     int32_t np, nr;   // ring slots
     uint32_t smem;    // dynamic shared memory
 };
@@ -72,16 +81,19 @@ struct DecodeArgs {
 };
 
 struct DecodeSmem {
-    uint64_t q_full, q_empty, s_full[2], p_full, pv_done, drained;
+    uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, drained;
     uint64_t pair_full[kMaxPair], pair_empty[kMaxPair], pos_full[kMaxPos], pos_empty[kMaxPos];
-    float factor[kRowTile];
-    float2 ml[kRowTile];
+    alignas(16) float mb[kRowTile];
+    float m_ref[kRowTile], factor[kRowTile], red[4][kRowTile];
+    int32_t unseen[kRowTile];  // last cached rows that the row's window token does not see
     uint32_t tmem;
     int32_t failed, bad[4];
     int32_t first_seq, first_tile;
     int64_t begin, end;
     int32_t pair_issued, pos_issued, q_issued;
 };
+
+__host__ __device__ constexpr uint32_t p_chunks(int npad) { return npad > 64 ? 2 : 1; }
 
 __device__ __forceinline__ bool bad_len(const DecodeArgs &p, int64_t len) {
     return len < 0 || len > (int64_t)p.max_pages * p.page_size;
@@ -131,7 +143,7 @@ __device__ __forceinline__ bool test_warp(uint64_t *mbar, uint32_t parity) {
 // barrier of the softmax warps that also tells whether any thread's flag is set
 __device__ __forceinline__ bool softmax_any(bool flag) {
     uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 256, p;\nselp.u32 %0, 1, 0, q;\n}\n"
                  : "=r"(r)
                  : "r"((uint32_t)flag)
                  : "memory");
@@ -143,9 +155,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const DecodeGeom &geo = p.geo;
     const uint32_t q_chunk = (uint32_t)geo.rows * 128;
-    uint8_t *s_q = base;                               // 9 chunks of `rows` rows; M = 64 reads run on into what
-    uint8_t *s_p = s_q + 9 * q_chunk;                  // follows, whose rows of S nobody reads
-    uint8_t *s_pair = s_p + (uint32_t)geo.npad * 128;  // P: npad rows of 64 cached rows
+    uint8_t *s_q = base;               // 9 chunks of `rows` rows; N = npad reads up to 8 rows of what follows,
+    uint8_t *s_p = s_q + 9 * q_chunk;  // whose columns of S^T nobody reads
+    uint8_t *s_pair = s_p + p_chunks(geo.npad) * kChunkB;  // P: 64 cached rows of npad query rows, MN-major
     uint8_t *s_pos = s_pair + (uint32_t)geo.np * kPairB;
     DecodeSmem &sm = *reinterpret_cast<DecodeSmem *>(s_pos + (uint32_t)geo.nr * kChunkB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -201,6 +213,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             tc::mbar_init(&sm.q_empty, 1);
             tc::mbar_init(&sm.s_full[0], 1);
             tc::mbar_init(&sm.s_full[1], 1);
+            tc::mbar_init(&sm.s_free[0], kSoftmaxThreads);
+            tc::mbar_init(&sm.s_free[1], kSoftmaxThreads);
             tc::mbar_init(&sm.p_full, kSoftmaxThreads);
             tc::mbar_init(&sm.pv_done, 1);
             tc::mbar_init(&sm.drained, 1);
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1);
             tc::mbar_init_fence();
         }
-    } else if (warp == 4) {
+    } else if (warp == 8) {
         tc::tmem_alloc(&sm.tmem, 512);
     }
     tc::fence_before_sync();
@@ -216,11 +230,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     tc::fence_after_sync();
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
-    const uint32_t t_s = tmem + 256;  // two S tiles of 64 columns behind O^T (4 x npad columns)
+    const uint32_t t_s = tmem + 4 * geo.npad;  // S^T behind O^T
     const int row_first = rt * geo.rows, rows_here = min(geo.rows, geo.R - row_first);
     bool ok = true;
 
-    if (warp == 5) {
+    if (warp == 9) {
         // ---- TMA producer: the warp holds the places of the next 32 boxes of rows ----
         Walk w;
         w.start(p, sm);
@@ -240,7 +254,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             page_next = look(u0 + lane);
             ok = seg == 0 || tma::wait_warp(&sm.q_empty, (seg - 1) & 1);
             if (!ok) break;
-            if (lane == 0) {
+            if (tma::elect()) {
                 sm.bad[seg & 3] = 0;
                 const int row = (int)((int64_t)w.n * geo.R + row_first);
                 tc::mbar_arrive_expect_tx(&sm.q_full, 9 * q_chunk);
@@ -273,7 +287,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 const uint32_t bytes = (uint32_t)boxes * p.rb * 128;
                 ok = tma::wait_warp(&sm.pos_empty[rs], rph ^ 1);
                 if (!ok) break;
-                if (lane == 0) {
+                if (tma::elect()) {
                     tc::mbar_arrive_expect_tx(&sm.pos_full[rs], bytes);
                     for (int b = 0; b < boxes; ++b)
                         tma::load_3d(s_pos + rs * kChunkB + b * p.rb * 128, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 for (int i = 0; i < kPairs && ok; ++i) {
                     ok = tma::wait_warp(&sm.pair_empty[ps], pph ^ 1);
                     if (!ok) break;
-                    if (lane == 0) {
+                    if (tma::elect()) {
                         tc::mbar_arrive_expect_tx(&sm.pair_full[ps], 2 * bytes);
                         for (int c = 0; c < 2; ++c)
                             for (int b = 0; b < boxes; ++b)
@@ -299,9 +313,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             w.skip_idle(p);
         }
         if (!ok) sm.failed = 1;
-    } else if (warp == 4) {
+    } else if (warp == 8) {
         // ---- MMA issuer: whatever is ready ----
-        const uint32_t idS = tma::idesc(64, kKvTile, 0, 0), idO = tma::idesc(128, geo.npad, 1, 0);
+        const uint32_t idS = tma::idesc(kKvTile, geo.npad, 0, 0), idO = tma::idesc(128, geo.npad, 1, 1);
+        const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), pos_lo = tma::lo_k(tc::smem_addr(s_pos));
+        const uint32_t pair_lo = tma::lo_k(tc::smem_addr(s_pair)), vpair_lo = tma::lo_mn(tc::smem_addr(s_pair), kChunkB);
+        const uint32_t p_lo = tma::lo_mn(tc::smem_addr(s_p), kChunkB);
+        const uint32_t q_step = q_chunk >> 4;
         Walk ws, wp;  // of the score products, of the value products
         ws.start(p, sm);
         ws.skip_idle(p);
@@ -309,53 +327,55 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         int js = ws.j0, jp = wp.j0;        // tile of each
         int sk = 0, pk = 0, sseg = 0;      // tiles issued, score stretches opened
         int cs = 0;                        // score chunks of the open tile: 0 positional, 1 .. 4 pairs
+        int sb = 0, sph = 0;               // S^T buffer of the open tile, times the ring of buffers went round
         int s_ps = 0, s_pph = 0, s_rs = 0, s_rph = 0, v_ps = 0;
-        bool q_ready = false;
+        bool s_ready = false;              // the open tile's queries are there and its buffer is free
         uint64_t since = 0;
         uint32_t idle = 0;
         while (!wp.done()) {
             bool moved = false;
-            if (!ws.done() && sk <= pk + 1) {  // the S tile two back has been read
-                if (!q_ready) q_ready = test_warp(&sm.q_full, sseg & 1);
-                if (q_ready) {
+            if (!ws.done()) {
+                if (!s_ready) s_ready = test_warp(&sm.q_full, sseg & 1) && test_warp(&sm.s_free[sb], (sph & 1) ^ 1);
+                if (s_ready) {
                     const bool ready = cs == 0 ? test_warp(&sm.pos_full[s_rs], s_rph) : test_warp(&sm.pair_full[s_ps], s_pph);
                     if (ready) {
                         moved = true;
-                        const uint32_t d = t_s + (sk & 1) * 64;
+                        tc::fence_after_sync();
+                        const uint32_t d = t_s + sb * geo.npad;
                         if (cs == 0) {
-                            if (lane == 0) {
-                                const uint32_t a = tc::smem_addr(s_q + 8 * q_chunk), b = tc::smem_addr(s_pos + s_rs * kChunkB);
+                            if (tma::elect()) {
+                                const uint32_t a = pos_lo + s_rs * (kChunkB >> 4), b = q_lo + 8 * q_step;
 #pragma unroll
-                                for (int s = 0; s < 4; ++s) tc::mma_ss(d, tma::desc_k(a, s), tma::desc_k(b, s), idS, s != 0);
+                                for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, s != 0);
                                 tc::commit(&sm.pos_empty[s_rs]);
                             }
                             if (++s_rs == geo.nr) s_rs = 0, s_rph ^= 1;
                         } else {
-                            if (lane == 0) {
+                            if (tma::elect()) {
+                                const uint32_t a = pair_lo + s_ps * (kPairB >> 4), b = q_lo + 2 * (cs - 1) * q_step;
 #pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    const uint32_t a = tc::smem_addr(s_q + (2 * (cs - 1) + c) * q_chunk);
-                                    const uint32_t b = tc::smem_addr(s_pair + s_ps * kPairB + c * kChunkB);
+                                for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, 1);
 #pragma unroll
-                                    for (int s = 0; s < 4; ++s) tc::mma_ss(d, tma::desc_k(a, s), tma::desc_k(b, s), idS, 1);
-                                }
+                                for (int s = 0; s < 4; ++s)
+                                    tma::mma_ss(d, a + (kChunkB >> 4) + 2 * s, b + q_step + 2 * s, idS, 1);
                             }
                             if (++s_ps == geo.np) s_ps = 0, s_pph ^= 1;
                         }
                         if (++cs == 1 + kPairs) {
                             cs = 0;
                             ++js;
-                            if (lane == 0) {
-                                tc::commit(&sm.s_full[sk & 1]);
+                            if (tma::elect()) {
+                                tc::commit(&sm.s_full[sb]);
                                 if (js == ws.j1) tc::commit(&sm.q_empty);
                             }
                             ++sk;
+                            s_ready = false;
+                            if (++sb == geo.sbufs) sb = 0, ++sph;
                             if (js == ws.j1) {
                                 ws.next(p);
                                 ws.skip_idle(p);
                                 js = ws.j0;
                                 ++sseg;
-                                q_ready = false;
                             }
                         }
                         __syncwarp();
@@ -379,18 +399,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     fence_proxy_async();
                     __syncwarp();
                 }
-                const uint32_t b = tc::smem_addr(s_p);
+                const uint32_t more = jp != wp.j0;
+                uint32_t d = tmem;
                 for (int i = 0; i < kPairs; ++i) {
-                    if (lane == 0) {
-                        const uint32_t a = tc::smem_addr(s_pair + v_ps * kPairB);
-                        for (int s = 0; s < steps; ++s)
-                            tc::mma_ss(tmem + i * geo.npad, tma::desc_mn(a, kChunkB, s), tma::desc_k(b, s), idO,
-                                       (jp != wp.j0) | (s != 0));
+                    if (tma::elect()) {
+                        const uint32_t a = vpair_lo + v_ps * (kPairB >> 4);
+                        if (steps == 4) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 128 * s, idO, s != 0 ? 1 : more);
+                        } else {
+                            for (int s = 0; s < steps; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 128 * s, idO, s != 0 ? 1 : more);
+                        }
                         tc::commit(&sm.pair_empty[v_ps]);
                     }
+                    d += geo.npad;
                     if (++v_ps == geo.np) v_ps = 0;
                 }
-                if (lane == 0) tc::commit(&sm.pv_done);
+                if (tma::elect()) tc::commit(&sm.pv_done);
                 __syncwarp();
                 ++pk;
                 if (++jp == wp.j1) {
@@ -413,140 +438,192 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         }
         if (!ok) sm.failed = 1;
     } else {
-        // ---- softmax: one thread a query row (16 lanes of each warp), then the output ----
-        const int r = warp * 16 + lane;  // this thread's row, when lane < 16
-        const bool owner = lane < 16 && r < rows_here, warp_rows = warp * 16 < rows_here;
-        const int t = (row_first + (owner ? r : 0)) / p.H;  // its window token
-        const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+        // ---- softmax: one thread a cached row (16 lanes of each warp) and its set's column groups; then the output ----
+        const int quarter = warp & 3, set = warp >> 2, groups = geo.npad / 16;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const int tok = quarter * 16 + lane;  // cached row within the tile, when lane < 16
+        const bool row_lane = lane < 16;
         const float c = p.scale * 1.4426950408889634f;
         const uint64_t c2 = pk2(c, c);
-        int k = 0, seg = 0;  // tiles and stretches worked on
+        if (tid < kRowTile) sm.unseen[tid] = p.m - 1 - (row_first + min(tid, rows_here - 1)) / p.H;
+        named_sync(2, kSoftmaxThreads);
+        int k = 0, seg = 0, sb = 0, sph = 0;  // tiles and stretches worked on, S^T buffer and its round
         Walk w;
         for (w.start(p, sm); !w.done() && ok; w.next(p)) {
-            float m_ref = -INFINITY, l = 0.f;
-            const int64_t keys = (int64_t)w.len - p.m + 1 + t;  // cached rows that the row sees
+            uint64_t l2[kGroups][8];  // sums of p: this thread's cached rows, by query row
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) l2[i][e] = 0;
             if (w.work) {
-                for (int j = w.j0; j < w.j1; ++j, ++k) {
-                    ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1);
-                    // a failed wait still meets the barrier below, so that no warp is left in it
+                for (int j = w.j0; j < w.j1; ++j) {
+                    ok = tma::wait_warp(&sm.s_full[sb], sph & 1);
+                    // a failed wait still meets the barriers below, so that no warp is left in them
                     if (ok) tc::fence_after_sync();
-                    uint32_t s[2][32];
-                    float mx = -INFINITY;
-                    if (warp_rows && ok) {
+                    uint32_t s[kGroups][16];
+                    if (ok) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) tc::tmem_ld32_nowait(t_s + quarter + (k & 1) * 64 + 32 * i, s[i]);
+                        for (int i = 0; i < kGroups; ++i)
+                            if (2 * i + set < groups) tma::tmem_ld16_nowait(t_s + lanes + sb * geo.npad + 16 * (2 * i + set), s[i]);
                         tc::tmem_wait_ld();
-                        const int64_t valid = keys - (int64_t)j * kKvTile;
-                        if (__any_sync(0xffffffffu, valid < kKvTile)) {
-                            const int v = (int)max((int64_t)-1, min((int64_t)kKvTile, valid));
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (32 * i + e >= v) s[i][e] = 0xff800000u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])));
+                        tc::fence_before_sync();
                     }
-                    bool grown = owner && (mx - m_ref) * c > kGrow;  // also from -inf to a finite maximum
-                    if (j == w.j0) {
-                        m_ref = mx;
-                        grown = false;
+                    tma::arrive(&sm.s_free[sb]);
+                    if (++sb == geo.sbufs) sb = 0, ++sph;
+                    const int64_t row = (int64_t)j * kKvTile + tok;
+                    if (w.len - (p.m - 1) < ((int64_t)j + 1) * kKvTile) {  // the tile's end is hidden from some row
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i)
+                            if (2 * i + set < groups) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (row >= w.len - sm.unseen[16 * (2 * i + set) + e]) s[i][e] = 0xff800000u;
+                            }
                     }
-                    // one barrier a tile: does any row need its O^T column rescaled, did any wait fail
-                    const bool any = softmax_any(grown || !ok);
-                    const bool wait_pv = k > 0;
-                    if (wait_pv) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                    const bool first = j == w.j0;
+                    float top = -INFINITY;  // how far a score passes its reference, in log2
+                    if (!first) {
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i)
+                            if (2 * i + set < groups) {
+                                const ulonglong2 *mb = reinterpret_cast<const ulonglong2 *>(&sm.mb[16 * (2 * i + set)]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const ulonglong2 b = mb[e];
+                                    const float2 x = upk2(fma2(pk2(__uint_as_float(s[i][4 * e]), __uint_as_float(s[i][4 * e + 1])), c2, b.x));
+                                    const float2 y = upk2(fma2(pk2(__uint_as_float(s[i][4 * e + 2]), __uint_as_float(s[i][4 * e + 3])), c2, b.y));
+                                    top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+                                }
+                            }
+                    }
+                    // one barrier a tile: does a row need a new reference, did a wait fail
+                    const bool any = softmax_any(first || (row_lane && top > kGrow) || !ok);
+                    if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
                     if (any) {
-                        if (lane < 16) {
-                            const float f = grown ? tc::ex2((m_ref - mx) * c) : 1.0f;
-                            sm.factor[r] = f;
-                            l *= f;
-                            if (grown) m_ref = mx;
-                        }
-                        // the flags again, now that everyone's waits are through: all stop together
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i)
+                            if (2 * i + set < groups) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    float x = __uint_as_float(s[i][e]);
+#pragma unroll
+                                    for (int off = 8; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+                                    if (lane == 0) sm.red[quarter][16 * (2 * i + set) + e] = x;
+                                }
+                            }
+                        // all stop together when any wait failed
                         if (softmax_any(!ok)) {
                             ok = false;
                             break;
                         }
-                        tc::fence_after_sync();
-                        for (int i = 0; i < kPairs; ++i)
-                            for (int e = 0; e < geo.npad; e += 16) {
-                                const uint32_t at = tmem + quarter + i * geo.npad + e;
-                                uint32_t x[16];
-                                tc::tmem_ld8_nowait(at, *reinterpret_cast<uint32_t(*)[8]>(&x[0]));
-                                tc::tmem_ld8_nowait(at + 8, *reinterpret_cast<uint32_t(*)[8]>(&x[8]));
-                                tc::tmem_wait_ld();
+                        if (tid < geo.npad) {
+                            const float x = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
+                            const float old = first ? -INFINITY : sm.m_ref[tid];
+                            const bool grown = first || (x - old) * c > kGrow;  // also from -inf to a finite maximum
+                            const float m = grown ? x : old;
+                            sm.factor[tid] = grown ? tc::ex2((old - m) * c) : 1.0f;
+                            sm.m_ref[tid] = m;
+                            sm.mb[tid] = m == -INFINITY ? 0.f : -m * c;
+                        }
+                        named_sync(2, kSoftmaxThreads);
+                        if (!first) {
+                            tc::fence_after_sync();
 #pragma unroll
-                                for (int y = 0; y < 16; ++y)
-                                    x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[e + y]);
-                                tc::tmem_st16(at, x);
-                            }
-                        tc::tmem_wait_st();
+                            for (int i = 0; i < kGroups; ++i)
+                                if (2 * i + set < groups) {
+                                    const uint64_t *f = reinterpret_cast<const uint64_t *>(&sm.factor[16 * (2 * i + set)]);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) l2[i][e] = mul2(l2[i][e], f[e]);
+                                }
+                            for (int i = 2 * set; i < 2 * set + 2; ++i)
+                                for (int e = 0; e < groups; ++e) {
+                                    const uint32_t at = tmem + lanes + i * geo.npad + 16 * e;
+                                    uint32_t x[16];
+                                    tma::tmem_ld16_nowait(at, x);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int y = 0; y < 16; ++y)
+                                        x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[16 * e + y]);
+                                    tc::tmem_st16(at, x);
+                                }
+                            tc::tmem_wait_st();
+                        }
                     }
-                    if (warp_rows && ok) {
-                        const float mb = m_ref == -INFINITY ? 0.f : -m_ref * c;
-                        const uint64_t nmb2 = pk2(mb, mb);
-                        uint64_t l2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
-                        uint8_t *row = s_p + r * 128;
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {  // eight 16-byte units of the row, swizzled
-                            uint32_t h[4];
+                    for (int i = 0; i < kGroups; ++i)
+                        if (2 * i + set < groups) {
+                            const int col = 16 * (2 * i + set);
+                            const ulonglong2 *mb = reinterpret_cast<const ulonglong2 *>(&sm.mb[col]);
+                            uint32_t h[8];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const uint32_t *x = &s[u >> 2][8 * (u & 3) + 2 * e];
-                                const float2 y = upk2(fma2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, nmb2));
-                                const float a = tc::ex2(y.x), b = tc::ex2(y.y);
-                                l2[e & 1] = add2(l2[e & 1], pk2(a, b));
-                                const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
-                                h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                                const ulonglong2 b = mb[e];
+                                const float2 x = upk2(fma2(pk2(__uint_as_float(s[i][4 * e]), __uint_as_float(s[i][4 * e + 1])), c2, b.x));
+                                const float2 y = upk2(fma2(pk2(__uint_as_float(s[i][4 * e + 2]), __uint_as_float(s[i][4 * e + 3])), c2, b.y));
+                                const float p0 = tc::ex2(x.x), p1 = tc::ex2(x.y), p2 = tc::ex2(y.x), p3 = tc::ex2(y.y);
+                                l2[i][2 * e] = add2(l2[i][2 * e], pk2(p0, p1));
+                                l2[i][2 * e + 1] = add2(l2[i][2 * e + 1], pk2(p2, p3));
+                                const __nv_bfloat162 h0 = __floats2bfloat162_rn(p0, p1), h1 = __floats2bfloat162_rn(p2, p3);
+                                h[2 * e] = *reinterpret_cast<const uint32_t *>(&h0);
+                                h[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h1);
                             }
-                            if (lane < 16) *reinterpret_cast<uint4 *>(row + ((u ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            if (row_lane) {  // 16 query rows: two 16-byte units of the cached row's 128 bytes, swizzled
+                                uint8_t *at = s_p + (col >> 6) * kChunkB + tok * 128;
+                                const int u = (col & 63) >> 3, x = tok & 7;
+                                *reinterpret_cast<uint4 *>(at + ((u ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                                *reinterpret_cast<uint4 *>(at + (((u + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                            }
                         }
-                        const float2 ls = upk2(add2(l2[0], l2[1]));
-                        l += ls.x + ls.y;
-                        fence_proxy_async();
-                    }
+                    fence_proxy_async();
                     tc::fence_before_sync();
                     tma::arrive(&sm.p_full);
+                    ++k;
                 }
-                if (ok && !w.done()) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
-                if (softmax_any(!ok)) ok = false;
+                if (ok) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
                 tc::fence_after_sync();
             }
+            // ---- the rows' sums, over this thread's lanes and quarters ----
+            if (w.work) {
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+                    if (2 * i + set < groups) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint64_t x = row_lane ? l2[i][e] : 0;
+#pragma unroll
+                            for (int off = 8; off > 0; off >>= 1) x = add2(x, __shfl_xor_sync(0xffffffffu, x, off));
+                            if (lane == 0) *reinterpret_cast<uint64_t *>(&sm.red[quarter][16 * (2 * i + set) + 2 * e]) = x;
+                        }
+                    }
+            }
+            if (softmax_any(!ok)) ok = false;
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg & 3] != 0);
             if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
             const int64_t row0 = (int64_t)w.n * geo.R + row_first;
             const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.rows;
-            if (lane < 16 && r < kRowTile) {
-                sm.factor[r] = bad ? NAN : (!whole ? 1.0f : (l == 0.f ? 0.f : 1.0f / l));
-                if (owner) {
-                    if (whole) {
-                        if (p.lse) p.lse[row0 + r] = bad ? NAN : (l == 0.f ? -INFINITY : m_ref * p.scale + logf(l));
-                    } else {
-                        p.part_ml[part0 + r] = make_float2(m_ref, bad ? NAN : l);
-                    }
-                }
+            if (tid < rows_here) {
+                const float l = w.work ? (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]) : 0.f;
+                const float m = sm.m_ref[tid];
+                sm.factor[tid] = bad ? NAN : (!whole ? 1.0f : (l == 0.f ? 0.f : 1.0f / l));
+                if (!whole)
+                    p.part_ml[part0 + tid] = make_float2(m, bad ? NAN : l);
+                else if (p.lse)
+                    p.lse[row0 + tid] = bad ? NAN : (l == 0.f ? -INFINITY : m * p.scale + logf(l));
             }
             named_sync(2, kSoftmaxThreads);
-            for (int i = 0; i < kPairs; ++i)
+            for (int i = 2 * set; i < 2 * set + 2; ++i)
                 for (int e = 0; e < rows_here; e += 16) {
                     uint32_t x[16];
                     if (w.work && ok) {
-                        const uint32_t at = tmem + quarter + i * geo.npad + e;
-                        tc::tmem_ld8_nowait(at, *reinterpret_cast<uint32_t(*)[8]>(&x[0]));
-                        tc::tmem_ld8_nowait(at + 8, *reinterpret_cast<uint32_t(*)[8]>(&x[8]));
+                        tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + e, x);
                         tc::tmem_wait_ld();
                     } else {
 #pragma unroll
                         for (int y = 0; y < 16; ++y) x[y] = 0;
                     }
-                    const int lat = 128 * i + 32 * warp + lane;
+                    const int lat = 128 * i + 32 * quarter + lane;
                     if (whole) {
 #pragma unroll
                         for (int y = 0; y < 16; y += 2) {
@@ -574,7 +651,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (sm.failed && warp == 4) {
+    if (sm.failed && warp == 8) {
         // a wait gave up: report it, and let what is in flight land before the memory goes
         if (lane == 0) {
             set_status(p.status, KDA_ERR_CUDA);
@@ -588,7 +665,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         }
         __syncwarp();
     }
-    if (warp == 4) tc::tmem_dealloc(tmem, 512);
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
 // The join of the sequences that a run's border cuts. Block x belongs to the border before
@@ -685,14 +762,15 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 
 constexpr size_t kSmemMax = 232448;
 
-// Row tiles of equal size, as few as 64 rows each allow; the rings take what Q and P leave.
+// Row tiles of equal size, as few as 96 rows each allow; the rings take what Q and P leave.
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
     q.RT = (q.R + kRowTile - 1) / kRowTile;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + (size_t)q.npad * 128;
+    q.sbufs = 6 * q.npad <= 512 ? 2 : 1;
+    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + p_chunks(q.npad) * kChunkB;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
     q.np = (int32_t)((room - q.nr * kChunkB) / kPairB);
@@ -702,7 +780,7 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     q.smem = (uint32_t)(fixed + (size_t)q.np * kPairB + (size_t)q.nr * kChunkB);
     return q;
 }
-static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * 64 * 128 >= 8 * kPairB + 2 * kChunkB, "two tiles of 64 rows' rings");
+static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 9 * 96 * 128 - 2 * kChunkB >= 5 * kPairB + 2 * kChunkB, "96 rows leave a tile's rings");
 
 // groups of CTAs that share the list: one CTA an SM
 int32_t groups_of(int32_t RT, int32_t sms) { return sms / RT > 0 ? sms / RT : 1; }
@@ -715,7 +793,7 @@ DecodeWs decode_ws(const DecodeGeom &q) {
     const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = 2 * G * q.RT * q.rows;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     w.head = 0;
-    w.ml = up(8 + 16 * G);
+    w.ml = up(8 + 16 * kMaxGroups);
     w.o = w.ml + up(parts * sizeof(float2));
     w.total = w.o + parts * kLatent * sizeof(float);
     return w;

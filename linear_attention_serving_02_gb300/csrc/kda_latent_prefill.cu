@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
     } else if (warp == 8) {
         // ---- MMA issuer ----
         constexpr uint32_t idS = tma::idesc(kTileQ, kTileK, 0, 0), idO = tma::idesc(kTileQ, kNope, 0, 1);
+        const uint32_t q_lo = tma::lo_k(tc::smem_addr(sm.q)), k_lo = tma::lo_k(tc::smem_addr(sm.k));
+        const uint32_t v_lo = tma::lo_mn(tc::smem_addr(sm.v), kChunk);
         // S_g(j) = Q_g K(j)^T; chunk c of key tile j is ring entry 3 j + c
         auto scores = [&](int g, int j, bool wait, bool release) {
             const uint32_t d = tmem + g * 128;
@@ -198,14 +200,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                 const int e = 3 * j + c, slot = e % kKSlots, ph = (e / kKSlots) & 1;
                 if (wait) ok = tma::wait_warp(&sm.k_full[slot], ph);
                 if (!ok) return;
-                if (lane == 0) {
-                    const uint32_t a = tc::smem_addr(sm.q[g][c]), b = tc::smem_addr(sm.k[slot]);
+                if (tma::elect()) {
+                    const uint32_t a = q_lo + (g * 3 + c) * (kChunk >> 4), b = k_lo + slot * (kChunk >> 4);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) tc::mma_ss(d, tma::desc_k(a, s), tma::desc_k(b, s), idS, (c | s) != 0);
+                    for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, s != 0 ? 1 : c != 0);
                     if (release) tc::commit(&sm.k_empty[slot]);
                 }
             }
-            if (lane == 0) tc::commit(&sm.s_full[g]);
+            if (tma::elect()) tc::commit(&sm.s_full[g]);
             __syncwarp();
         };
         for (int g = 0; g < 2 && ok; ++g) {
@@ -234,11 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                 ok = tma::wait_warp(&sm.p_full[g], j & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t d = tmem + 256 + g * 128, a = tmem + g * 128, b = tc::smem_addr(sm.v[slot][0]);
+                if (tma::elect()) {
+                    const uint32_t d = tmem + 256 + g * 128, a = tmem + g * 128, b = v_lo + slot * (2 * kChunk >> 4);
 #pragma unroll
-                    for (int s = 0; s < kTileK / 16; ++s)
-                        tc::mma_ts(d, a + 8 * s, tma::desc_mn(b, kChunk, s), idO, (j | s) != 0);
+                    for (int s = 0; s < kTileK / 16; ++s) tma::mma_ts(d, a + 8 * s, b + 128 * s, idO, s != 0 ? 1 : j != 0);
                     tc::commit(&sm.pv_done[g]);
                     if (g == 1 || j >= nt[1]) tc::commit(&sm.v_empty[slot]);
                 }

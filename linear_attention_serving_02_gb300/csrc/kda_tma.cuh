@@ -22,15 +22,36 @@ namespace tma {
 
 constexpr int kChunkCols = 64;  // bf16 columns of a chunk: one 128-byte swizzle row
 
-// descriptor of a K-major chunk, 16-column step s
-__device__ __forceinline__ uint64_t desc_k(uint32_t chunk_saddr, int s) {
-    return (uint64_t)(((chunk_saddr + 32u * s) >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Descriptors as their two halves: the high one is the same for every operand here (8-row
+// groups 1024 B apart, version 1, 128-byte swizzle); the low one holds the address and, for an
+// MN-major operand, the distance of its 64-column chunks. Adding to the low half moves the
+// operand: +2 a 16-column step (K-major), +128 a 16-row step (MN-major), bytes / 16 a chunk.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t lo_k(uint32_t chunk_saddr) { return (chunk_saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t lo_mn(uint32_t chunk_saddr, uint32_t chunk_bytes) {
+    return (chunk_saddr >> 4) | ((chunk_bytes >> 4) << 16);
 }
-// descriptor of an MN-major operand whose 64-column chunks are `chunk_bytes` apart, 16-row step s
-__device__ __forceinline__ uint64_t desc_mn(uint32_t chunk_saddr, uint32_t chunk_bytes, int s) {
-    return (uint64_t)(((chunk_saddr + 2048u * s) >> 4) & 0x3FFF) | ((uint64_t)((chunk_bytes >> 4) & 0x3FFF) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// D[tmem] (+)= A B^T, both in shared memory; issued by one thread
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "n"(kDescHi));
+}
+// the same with A in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(id), "r"(accumulate), "n"(kDescHi));
+}
+// 16 consecutive 32-bit TMEM columns of this thread's lane, without the wait
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 // instruction descriptor: kind::f16, bf16 operands, fp32 accumulator; a_mn / b_mn read that
 // operand MN-major
@@ -56,6 +77,14 @@ __device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, uint6
 // a wait by a whole warp, whose lanes agree on the outcome (what follows is warp-collective)
 __device__ __forceinline__ bool wait_warp(uint64_t *mbar, uint32_t parity) {
     return __all_sync(0xffffffffu, tc::mbar_wait(mbar, parity));
+}
+// true in one lane of a converged warp. Tensor-core and TMA instructions take their operands
+// from uniform registers; under this predicate (unlike `lane == 0`) the compiler knows that
+// one lane runs and moves them there once, instead of in a loop over the active lanes
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ void arrive(uint64_t *mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_addr(mbar)) : "memory");
