@@ -132,14 +132,6 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ bool test_warp(uint64_t *mbar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(done)
-                 : "r"(tc::smem_addr(mbar)), "r"(parity)
-                 : "memory");
-    return __all_sync(0xffffffffu, done != 0);
-}
 // barrier of the softmax warps that also tells whether any thread's flag is set
 __device__ __forceinline__ bool softmax_any(bool flag) {
     uint32_t r;
@@ -332,42 +324,36 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         bool s_ready = false;              // the open tile's queries are there and its buffer is free
         uint64_t since = 0;
         uint32_t idle = 0;
-        while (!wp.done()) {
-            bool moved = false;
-            if (!ws.done()) {
-                if (!s_ready) s_ready = test_warp(&sm.q_full, sseg & 1) && test_warp(&sm.s_free[sb], (sph & 1) ^ 1);
-                if (s_ready) {
-                    const bool ready = cs == 0 ? test_warp(&sm.pos_full[s_rs], s_rph) : test_warp(&sm.pair_full[s_ps], s_pph);
-                    if (ready) {
+        // one thread runs the whole loop: a vote or a warp barrier between the products would cost
+        // more than the products of a narrow batch (an MMA of N = 16 takes 25 to 40 cycles)
+        if (tma::elect()) {
+            while (!wp.done()) {
+                bool moved = false;
+                if (!ws.done()) {
+                    if (!s_ready) s_ready = tma::test(&sm.q_full, sseg & 1) && tma::test(&sm.s_free[sb], (sph & 1) ^ 1);
+                    if (s_ready && (cs == 0 ? tma::test(&sm.pos_full[s_rs], s_rph) : tma::test(&sm.pair_full[s_ps], s_pph))) {
                         moved = true;
                         tc::fence_after_sync();
                         const uint32_t d = t_s + sb * geo.npad;
                         if (cs == 0) {
-                            if (tma::elect()) {
-                                const uint32_t a = pos_lo + s_rs * (kChunkB >> 4), b = q_lo + 8 * q_step;
+                            const uint32_t a = pos_lo + s_rs * (kChunkB >> 4), b = q_lo + 8 * q_step;
 #pragma unroll
-                                for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, s != 0);
-                                tc::commit(&sm.pos_empty[s_rs]);
-                            }
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, s != 0);
+                            tc::commit(&sm.pos_empty[s_rs]);
                             if (++s_rs == geo.nr) s_rs = 0, s_rph ^= 1;
                         } else {
-                            if (tma::elect()) {
-                                const uint32_t a = pair_lo + s_ps * (kPairB >> 4), b = q_lo + 2 * (cs - 1) * q_step;
+                            const uint32_t a = pair_lo + s_ps * (kPairB >> 4), b = q_lo + 2 * (cs - 1) * q_step;
 #pragma unroll
-                                for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, 1);
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, 1);
 #pragma unroll
-                                for (int s = 0; s < 4; ++s)
-                                    tma::mma_ss(d, a + (kChunkB >> 4) + 2 * s, b + q_step + 2 * s, idS, 1);
-                            }
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + (kChunkB >> 4) + 2 * s, b + q_step + 2 * s, idS, 1);
                             if (++s_ps == geo.np) s_ps = 0, s_pph ^= 1;
                         }
                         if (++cs == 1 + kPairs) {
                             cs = 0;
                             ++js;
-                            if (tma::elect()) {
-                                tc::commit(&sm.s_full[sb]);
-                                if (js == ws.j1) tc::commit(&sm.q_empty);
-                            }
+                            tc::commit(&sm.s_full[sb]);
+                            if (js == ws.j1) tc::commit(&sm.q_empty);
                             ++sk;
                             s_ready = false;
                             if (++sb == geo.sbufs) sb = 0, ++sph;
@@ -378,31 +364,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                                 ++sseg;
                             }
                         }
-                        __syncwarp();
                     }
                 }
-            }
-            if (pk < sk && test_warp(&sm.p_full, pk & 1)) {
-                moved = true;
-                tc::fence_after_sync();
-                const int valid = min(kKvTile, wp.len - jp * kKvTile), steps = (valid + 15) / 16;
-                if (valid & 15) {  // value rows behind the sequence in the last step
-                    int slot = v_ps;
-                    const int units = (16 * steps - valid) * 8;
+                if (pk < sk && tma::test(&sm.p_full, pk & 1)) {
+                    moved = true;
+                    tc::fence_after_sync();
+                    const int steps = (min(kKvTile, wp.len - jp * kKvTile) + 15) / 16;
+                    const uint32_t more = jp != wp.j0;
+                    uint32_t d = tmem;
                     for (int i = 0; i < kPairs; ++i) {
-                        for (int c = 0; c < 2; ++c)
-                            for (int u = lane; u < units; u += 32)
-                                reinterpret_cast<uint4 *>(s_pair + slot * kPairB + c * kChunkB)[valid * 8 + u] =
-                                    make_uint4(0, 0, 0, 0);
-                        if (++slot == geo.np) slot = 0;
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                }
-                const uint32_t more = jp != wp.j0;
-                uint32_t d = tmem;
-                for (int i = 0; i < kPairs; ++i) {
-                    if (tma::elect()) {
                         const uint32_t a = vpair_lo + v_ps * (kPairB >> 4);
                         if (steps == 4) {
 #pragma unroll
@@ -411,32 +381,31 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                             for (int s = 0; s < steps; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 128 * s, idO, s != 0 ? 1 : more);
                         }
                         tc::commit(&sm.pair_empty[v_ps]);
+                        d += geo.npad;
+                        if (++v_ps == geo.np) v_ps = 0;
                     }
-                    d += geo.npad;
-                    if (++v_ps == geo.np) v_ps = 0;
+                    tc::commit(&sm.pv_done);
+                    ++pk;
+                    if (++jp == wp.j1) {
+                        wp.next(p);
+                        wp.skip_idle(p);
+                        jp = wp.j0;
+                    }
                 }
-                if (tma::elect()) tc::commit(&sm.pv_done);
-                __syncwarp();
-                ++pk;
-                if (++jp == wp.j1) {
-                    wp.next(p);
-                    wp.skip_idle(p);
-                    jp = wp.j0;
-                }
-            }
-            if (moved) {
-                idle = 0;
-            } else if ((++idle & 63) == 0) {
-                const uint64_t now = tc::globaltimer();
-                if (idle == 64)
-                    since = now;
-                else if (__any_sync(0xffffffffu, now - since > tc::kWaitLimitNs)) {
-                    ok = false;
-                    break;
+                if (moved) {
+                    idle = 0;
+                } else if ((++idle & 63) == 0) {
+                    const uint64_t now = tc::globaltimer();
+                    if (idle == 64) {
+                        since = now;
+                    } else if (now - since > tc::kWaitLimitNs) {
+                        sm.failed = 1;
+                        break;
+                    }
                 }
             }
         }
-        if (!ok) sm.failed = 1;
+        __syncwarp();
     } else {
         // ---- softmax: one thread a cached row (16 lanes of each warp) and its set's column groups; then the output ----
         const int quarter = warp & 3, set = warp >> 2, groups = geo.npad / 16;
@@ -447,7 +416,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         const uint64_t c2 = pk2(c, c);
         if (tid < kRowTile) sm.unseen[tid] = p.m - 1 - (row_first + min(tid, rows_here - 1)) / p.H;
         named_sync(2, kSoftmaxThreads);
-        int k = 0, seg = 0, sb = 0, sph = 0;  // tiles and stretches worked on, S^T buffer and its round
+        int k = 0, seg = 0, sb = 0, sph = 0, ps = 0;  // tiles and stretches worked on, S^T buffer and its round, ring slot
         Walk w;
         for (w.start(p, sm); !w.done() && ok; w.next(p)) {
             uint64_t l2[kGroups][8];  // sums of p: this thread's cached rows, by query row
@@ -574,6 +543,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                                 *reinterpret_cast<uint4 *>(at + (((u + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                             }
                         }
+                    const int valid = min(kKvTile, w.len - j * kKvTile);
+                    if (valid & 15) {  // value rows behind the sequence in the product's last step of 16
+                        const int units = (-valid & 15) * 8;
+                        for (int u = tid; u < 2 * kPairs * units; u += kSoftmaxThreads) {
+                            const int chunk = u / units;
+                            const int slot = (ps + (chunk >> 1)) % geo.np;
+                            reinterpret_cast<uint4 *>(s_pair + slot * kPairB + (chunk & 1) * kChunkB)[valid * 8 + u % units] =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    ps = (ps + kPairs) % geo.np;
                     fence_proxy_async();
                     tc::fence_before_sync();
                     tma::arrive(&sm.p_full);

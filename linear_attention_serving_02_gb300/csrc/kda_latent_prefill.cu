@@ -193,61 +193,47 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
         constexpr uint32_t idS = tma::idesc(kTileQ, kTileK, 0, 0), idO = tma::idesc(kTileQ, kNope, 0, 1);
         const uint32_t q_lo = tma::lo_k(tc::smem_addr(sm.q)), k_lo = tma::lo_k(tc::smem_addr(sm.k));
         const uint32_t v_lo = tma::lo_mn(tc::smem_addr(sm.v), kChunk);
-        // S_g(j) = Q_g K(j)^T; chunk c of key tile j is ring entry 3 j + c
-        auto scores = [&](int g, int j, bool wait, bool release) {
-            const uint32_t d = tmem + g * 128;
-            for (int c = 0; c < 3 && ok; ++c) {
-                const int e = 3 * j + c, slot = e % kKSlots, ph = (e / kKSlots) & 1;
-                if (wait) ok = tma::wait_warp(&sm.k_full[slot], ph);
-                if (!ok) return;
-                if (tma::elect()) {
+        // one thread runs the whole loop: votes between the products would hold up their issue
+        if (tma::elect()) {
+            // S_g(j) = Q_g K(j)^T; chunk c of key tile j is ring entry 3 j + c
+            auto scores = [&](int g, int j, bool release) {
+                const uint32_t d = tmem + g * 128;
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    const int e = 3 * j + c, slot = e % kKSlots, ph = (e / kKSlots) & 1;
+                    if (ok) ok = tc::mbar_wait(&sm.k_full[slot], ph);
+                    if (!ok) return;
                     const uint32_t a = q_lo + (g * 3 + c) * (kChunk >> 4), b = k_lo + slot * (kChunk >> 4);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, s != 0 ? 1 : c != 0);
+                    for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, (c | s) != 0);
                     if (release) tc::commit(&sm.k_empty[slot]);
                 }
-            }
-            if (tma::elect()) tc::commit(&sm.s_full[g]);
-            __syncwarp();
-        };
-        for (int g = 0; g < 2 && ok; ++g) {
-            if (nt[g] == 0) continue;
-            ok = tma::wait_warp(&sm.q_full[g], 0);
-            if (ok) scores(g, 0, true, g == 1 || nt[1] == 0);
-        }
-        for (int j = 0; j < tiles && ok; ++j) {
-            const int slot = j % kVSlots, vph = (j / kVSlots) & 1;
-            bool have_v = false;
+                tc::commit(&sm.s_full[g]);
+            };
             for (int g = 0; g < 2 && ok; ++g) {
-                if (j >= nt[g]) continue;
-                if (!have_v) {
-                    ok = tma::wait_warp(&sm.v_full[slot], vph);
+                if (nt[g] == 0) continue;
+                ok = tc::mbar_wait(&sm.q_full[g], 0);
+                scores(g, 0, g == 1 || nt[1] == 0);
+            }
+            for (int j = 0; j < tiles && ok; ++j) {
+                const int slot = j % kVSlots;
+                ok = tc::mbar_wait(&sm.v_full[slot], (j / kVSlots) & 1);
+                for (int g = 0; g < 2 && ok; ++g) {
+                    if (j >= nt[g]) continue;
+                    ok = tc::mbar_wait(&sm.p_full[g], j & 1);
                     if (!ok) break;
-                    const int valid = nk - j * kTileK;
-                    if (valid < kTileK) {  // value rows behind the sequence
-                        for (int c = 0; c < 2; ++c)
-                            for (int i = valid * 8 + lane; i < kTileK * 8; i += 32)
-                                reinterpret_cast<uint4 *>(sm.v[slot][c])[i] = make_uint4(0, 0, 0, 0);
-                        fence_proxy_async();
-                        __syncwarp();
-                    }
-                    have_v = true;
-                }
-                ok = tma::wait_warp(&sm.p_full[g], j & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (tma::elect()) {
+                    tc::fence_after_sync();
                     const uint32_t d = tmem + 256 + g * 128, a = tmem + g * 128, b = v_lo + slot * (2 * kChunk >> 4);
 #pragma unroll
                     for (int s = 0; s < kTileK / 16; ++s) tma::mma_ts(d, a + 8 * s, b + 128 * s, idO, s != 0 ? 1 : j != 0);
                     tc::commit(&sm.pv_done[g]);
                     if (g == 1 || j >= nt[1]) tc::commit(&sm.v_empty[slot]);
+                    if (j + 1 < nt[g]) scores(g, j + 1, g == 1 || j + 1 >= nt[1]);
                 }
-                __syncwarp();
-                if (j + 1 < nt[g]) scores(g, j + 1, true, g == 1 || j + 1 >= nt[1]);
             }
+            if (!ok) sm.failed = 1;
         }
-        if (!ok) sm.failed = 1;
+        __syncwarp();
     } else {
         // ---- softmax: one thread a query row ----
         const int g = warp >> 2, r = (warp & 3) * 32 + lane, row = row0 + g * kTileQ + r;
@@ -309,6 +295,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                 tc::tmem_st16(s_addr + 16 * i, pr);
             }
             tc::tmem_wait_st();
+            const int there = nk - j * kTileK;
+            if (there < kTileK && (g == 0 || j >= nt[0])) {
+                // value rows behind the sequence; the first query tile that uses them clears them
+                ok = tma::wait_warp(&sm.v_full[j % kVSlots], (j / kVSlots) & 1);
+                if (!ok) break;
+                for (int u = r; u < 2 * (kTileK - there) * 8; u += kTileQ) {
+                    const int chunk = u >= (kTileK - there) * 8, x = u - chunk * (kTileK - there) * 8;
+                    reinterpret_cast<uint4 *>(sm.v[j % kVSlots][chunk])[there * 8 + x] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+            }
             tc::fence_before_sync();
             tma::arrive(&sm.p_full[g]);
         }
