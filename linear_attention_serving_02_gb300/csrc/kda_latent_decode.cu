@@ -14,24 +14,25 @@
 // in list order; the others are finished in place. Nothing waits on another CTA.
 //
 // A tile in a CTA. TMA lays the 64 rows down once as 9 chunks of 64 columns (128-byte
-// swizzle). Both products run transposed, with the cached rows as the A operand: an MMA pays
-// about 30 (M = 64) or 45 (M = 128) cycles for A and 0.48 for each column of N (measured, one
-// CTA), so a narrow batch pays for its own query rows only and up to 96 rows share one read
-// of A. S^T = K Q^T: M = 64 cached rows, N = query rows, K-major. Eight softmax warps take S^T
-// from TMEM, one thread a cached row and up to 48 query rows, and write P (bf16) to shared
-// memory. O^T = C^T P: M = 128 latents (the same chunks, read MN-major), N = query rows.
-// TMEM: O^T takes 4 N columns and S^T N, or 2 N where that fits (N <= 80).
+// swizzle). S = Q K^T: M = 64 or 128 query rows (up to 96 are used), N = 64 cached rows, read
+// K-major. Eight softmax warps take S from TMEM, one thread a query row and half of the tile,
+// and write P (bf16) to shared memory. The value product runs transposed, O^T = C^T P^T:
+// M = 128 latents (the same chunks, read MN-major), N = query rows. An MMA of K = 16 takes
+// N / 2 cycles, but at least 25 with M = 64 and 39 with M = 128 (measured; A's 128 rows are
+// 4 KB of shared memory): 96 rows need 36 x 48 + 16 x 56 cycles a tile, 16 rows
+// 36 x 32 + 16 x 39, where the tile's 72 KB take an SM's share of HBM about 3100. TMEM: O^T
+// takes 4 N columns and two S tiles 128, which fits up to N = 96; O itself (rows x 512) would
+// take every column.
 //
-// A thread of S^T sees one cached row, so a row maximum would be a reduction over lanes. It is
-// not needed: the reference M_r only has to stay within 2^8 of the maximum, so a tile costs a
-// comparison a score, and the reduction runs on a sequence's first tile and where a score
-// passes its reference by 2^8 (then O^T is rescaled too). Each thread keeps its own partial
-// sums of p, reduced once at the end.
+// The reference M_r only has to stay within 2^8 of the row's maximum (P is then far inside
+// bf16 and fp32), so a tile costs a comparison a score and one barrier; the halves' maxima are
+// exchanged, and O^T rescaled, on a sequence's first tile and where a score passes its
+// reference by 2^8.
 //
 // Shared memory. Q takes 1152 B a row; the rest is a ring of 16 KB pairs of chunks and a
-// ring of 8 KB positional chunks. The MMA warp issues whatever is ready: the next tile's
-// scores chunk by chunk as they land, or the value product of the tile whose P is written;
-// each pair of chunks is given back as soon as its 128 latents are done.
+// ring of 8 KB positional chunks. One thread issues the score products chunk by chunk as they
+// land, another the value products as their P is written; each pair of chunks is given back
+// as soon as its 128 latents are done.
 //
 // Rows of a tile behind the sequence's length (the rest of a page, or stale shared memory)
 // may hold anything: their scores are replaced by -inf, the product's 16-row steps past the
@@ -50,17 +51,17 @@ constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
 constexpr int kMaxPair = 12, kMaxPos = 4;     // ring slots at most
-constexpr int kDecThreads = 320;              // 8 softmax warps, the MMA warp, the TMA warp
+constexpr int kDecThreads = 352;              // 8 softmax warps, S issue, value issue, TMA
 constexpr int kMaxGroups = 160;               // CTAs that share the list at most
 constexpr float kGrow = 8.0f;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kGroups = kRowTile / 16 / 2;    // 16-column groups of S^T that a thread takes at most
+constexpr int kHalf = kKvTile / 2;            // cached rows of a tile that a softmax thread takes
 
 struct DecodeGeom {
     int32_t R;        // query rows of a sequence: m H
     int32_t RT, rows; // row tiles and query rows of each (a multiple of 8)
-    int32_t npad;     // MMA columns: rows rounded up to 16
-    int32_t sbufs;    // S^T tiles in TMEM: 2 where they fit, else 1
+    int32_t npad;     // MMA columns of O^T: rows rounded up to 16
+    int32_t ms;       // MMA rows of S: 64 or 128
     int32_t np, nr;   // ring slots
     uint32_t smem;    // dynamic shared memory
 };
@@ -83,17 +84,13 @@ struct DecodeArgs {
 struct DecodeSmem {
     uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, drained;
     uint64_t pair_full[kMaxPair], pair_empty[kMaxPair], pos_full[kMaxPos], pos_empty[kMaxPos];
-    alignas(16) float mb[kRowTile];
-    float m_ref[kRowTile], factor[kRowTile], red[4][kRowTile];
-    int32_t unseen[kRowTile];  // last cached rows that the row's window token does not see
+    float factor[128], half[2][128];  // by query row: scale of O^T, the halves' maxima or sums
     uint32_t tmem;
     int32_t failed, bad[4];
     int32_t first_seq, first_tile;
     int64_t begin, end;
     int32_t pair_issued, pos_issued, q_issued;
 };
-
-__host__ __device__ constexpr uint32_t p_chunks(int npad) { return npad > 64 ? 2 : 1; }
 
 __device__ __forceinline__ bool bad_len(const DecodeArgs &p, int64_t len) {
     return len < 0 || len > (int64_t)p.max_pages * p.page_size;
@@ -147,9 +144,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const DecodeGeom &geo = p.geo;
     const uint32_t q_chunk = (uint32_t)geo.rows * 128;
-    uint8_t *s_q = base;               // 9 chunks of `rows` rows; N = npad reads up to 8 rows of what follows,
-    uint8_t *s_p = s_q + 9 * q_chunk;  // whose columns of S^T nobody reads
-    uint8_t *s_pair = s_p + p_chunks(geo.npad) * kChunkB;  // P: 64 cached rows of npad query rows, MN-major
+    uint8_t *s_q = base;               // 9 chunks of `rows` rows; M = 64 or 128 reads run on into what
+    uint8_t *s_p = s_q + 9 * q_chunk;  // follows (P and the rings are longer), rows of S that nobody reads
+    uint8_t *s_pair = s_p + (uint32_t)geo.npad * 128;  // P: npad rows of 64 cached rows
     uint8_t *s_pos = s_pair + (uint32_t)geo.np * kPairB;
     DecodeSmem &sm = *reinterpret_cast<DecodeSmem *>(s_pos + (uint32_t)geo.nr * kChunkB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             tc::mbar_init(&sm.s_free[1], kSoftmaxThreads);
             tc::mbar_init(&sm.p_full, kSoftmaxThreads);
             tc::mbar_init(&sm.pv_done, 1);
-            tc::mbar_init(&sm.drained, 1);
+            tc::mbar_init(&sm.drained, 2);
             for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.pair_full[i], 1), tc::mbar_init(&sm.pair_empty[i], 1);
             for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1);
             tc::mbar_init_fence();
@@ -222,327 +219,271 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     tc::fence_after_sync();
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
-    const uint32_t t_s = tmem + 4 * geo.npad;  // S^T behind O^T
+    const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
     const int row_first = rt * geo.rows, rows_here = min(geo.rows, geo.R - row_first);
     bool ok = true;
 
-    if (warp == 9) {
-        // ---- TMA producer: the warp holds the places of the next 32 boxes of rows ----
-        Walk w;
-        w.start(p, sm);
-        w.skip_idle(p);
-        int seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
-        const int sub = kKvTile / p.rb;  // boxes of a tile's chunk
-        while (!w.done() && ok) {
-            const int32_t *table = p.table + (int64_t)w.n * p.max_pages;
-            const int64_t u0 = (int64_t)w.j0 * sub;
-            int32_t page_next = 0;
-            auto look = [&](int64_t u) {  // page of box u, num_pages (loads as zeros) when it is bad, 0 past the end
-                const int64_t row = u * p.rb;
-                if (row >= w.len) return 0;
-                const int32_t pg = __ldg(table + row / p.page_size);
-                return pg < 0 || pg >= p.num_pages ? -1 : pg;
-            };
-            page_next = look(u0 + lane);
-            ok = seg == 0 || tma::wait_warp(&sm.q_empty, (seg - 1) & 1);
-            if (!ok) break;
-            if (tma::elect()) {
+    if (warp == 10) {
+        // ---- TMA producer: one thread ----
+        if (tma::elect()) {
+            Walk w;
+            w.start(p, sm);
+            w.skip_idle(p);
+            int seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
+            const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
+            while (!w.done() && ok) {
+                const int32_t *entry = p.table + (int64_t)w.n * p.max_pages;
+                const int64_t row0 = (int64_t)w.j0 * kKvTile;
+                entry += row0 / p.page_size;
+                int32_t at = (int32_t)(row0 % p.page_size);  // row within the page
+                // the places of a tile's boxes, fetched one tile ahead; nothing past the sequence's rows is looked up
+                int32_t pg[4], ry[4], pg_next[4], ry_next[4];
+                auto look = [&](int j) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        pg_next[b] = 0;
+                        ry_next[b] = at;
+                        if (b < sub && j < w.j1 && (int64_t)j * kKvTile + b * p.rb < w.len) {
+                            pg_next[b] = __ldg(entry);
+                            at += p.rb;
+                            if (at == p.page_size) at = 0, ++entry;
+                        }
+                    }
+                };
+                look(w.j0);
+                ok = seg == 0 || tc::mbar_wait(&sm.q_empty, (seg - 1) & 1);
+                if (!ok) break;
                 sm.bad[seg & 3] = 0;
                 const int row = (int)((int64_t)w.n * geo.R + row_first);
                 tc::mbar_arrive_expect_tx(&sm.q_full, 9 * q_chunk);
-                for (int c = 0; c < 8; ++c) tma::load_2d(s_q + c * q_chunk, &p.q_lat, &sm.q_full, 64 * c, row);
                 tma::load_2d(s_q + 8 * q_chunk, &p.q_pe, &sm.q_full, 0, row);
+                for (int c = 0; c < 8; ++c) tma::load_2d(s_q + c * q_chunk, &p.q_lat, &sm.q_full, 64 * c, row);
                 ++sm.q_issued;
-            }
-            int32_t page = 0;
-            for (int j = w.j0; j < w.j1 && ok; ++j) {
-                const int at = (int)(((int64_t)(j - w.j0) * sub) & 31);
-                if (at == 0) {
-                    page = page_next;
-                    if (__any_sync(0xffffffffu, page < 0)) {
-                        // only boxes of this stretch count: another CTA reports its own
-                        const int64_t u = (int64_t)j * sub + lane;
-                        if (__any_sync(0xffffffffu, page < 0 && u < (int64_t)w.j1 * sub) && lane == 0) {
-                            sm.bad[seg & 3] = 1;
-                            set_status(p.status, KDA_ERR_PAGES);
-                        }
+                for (int j = w.j0; j < w.j1 && ok; ++j) {
+                    bool bad = false;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        ry[b] = ry_next[b];
+                        const bool out = (uint32_t)pg_next[b] >= (uint32_t)p.num_pages;
+                        bad |= out;
+                        pg[b] = out ? p.num_pages : pg_next[b];  // loads as zeros
                     }
-                    page_next = look((int64_t)j * sub + 32 + lane);
-                }
-                const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
-                int pg[4], ry[4];
-                for (int b = 0; b < 4; ++b) {
-                    const int x = __shfl_sync(0xffffffffu, page, (at + b) & 31);
-                    pg[b] = x < 0 ? p.num_pages : x;
-                    ry[b] = (int)(((int64_t)j * kKvTile + b * p.rb) % p.page_size);
-                }
-                const uint32_t bytes = (uint32_t)boxes * p.rb * 128;
-                ok = tma::wait_warp(&sm.pos_empty[rs], rph ^ 1);
-                if (!ok) break;
-                if (tma::elect()) {
-                    tc::mbar_arrive_expect_tx(&sm.pos_full[rs], bytes);
-                    for (int b = 0; b < boxes; ++b)
-                        tma::load_3d(s_pos + rs * kChunkB + b * p.rb * 128, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
-                    ++sm.pos_issued;
-                }
-                if (++rs == geo.nr) rs = 0, rph ^= 1;
-                for (int i = 0; i < kPairs && ok; ++i) {
-                    ok = tma::wait_warp(&sm.pair_empty[ps], pph ^ 1);
+                    if (bad) {
+                        sm.bad[seg & 3] = 1;
+                        set_status(p.status, KDA_ERR_PAGES);
+                    }
+                    look(j + 1);
+                    const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
+                    const uint32_t box = (uint32_t)p.rb * 128, bytes = boxes * box;
+                    ok = tc::mbar_wait(&sm.pos_empty[rs], rph ^ 1);
                     if (!ok) break;
-                    if (tma::elect()) {
-                        tc::mbar_arrive_expect_tx(&sm.pair_full[ps], 2 * bytes);
-                        for (int c = 0; c < 2; ++c)
-                            for (int b = 0; b < boxes; ++b)
-                                tma::load_3d(s_pair + ps * kPairB + c * kChunkB + b * p.rb * 128, &p.cache,
-                                             &sm.pair_full[ps], 128 * i + 64 * c, ry[b], pg[b]);
-                        ++sm.pair_issued;
-                    }
-                    if (++ps == geo.np) ps = 0, pph ^= 1;
-                }
-            }
-            ++seg;
-            w.next(p);
-            w.skip_idle(p);
-        }
-        if (!ok) sm.failed = 1;
-    } else if (warp == 8) {
-        // ---- MMA issuer: whatever is ready ----
-        const uint32_t idS = tma::idesc(kKvTile, geo.npad, 0, 0), idO = tma::idesc(128, geo.npad, 1, 1);
-        const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), pos_lo = tma::lo_k(tc::smem_addr(s_pos));
-        const uint32_t pair_lo = tma::lo_k(tc::smem_addr(s_pair)), vpair_lo = tma::lo_mn(tc::smem_addr(s_pair), kChunkB);
-        const uint32_t p_lo = tma::lo_mn(tc::smem_addr(s_p), kChunkB);
-        const uint32_t q_step = q_chunk >> 4;
-        Walk ws, wp;  // of the score products, of the value products
-        ws.start(p, sm);
-        ws.skip_idle(p);
-        wp = ws;
-        int js = ws.j0, jp = wp.j0;        // tile of each
-        int sk = 0, pk = 0, sseg = 0;      // tiles issued, score stretches opened
-        int cs = 0;                        // score chunks of the open tile: 0 positional, 1 .. 4 pairs
-        int sb = 0, sph = 0;               // S^T buffer of the open tile, times the ring of buffers went round
-        int s_ps = 0, s_pph = 0, s_rs = 0, s_rph = 0, v_ps = 0;
-        bool s_ready = false;              // the open tile's queries are there and its buffer is free
-        uint64_t since = 0;
-        uint32_t idle = 0;
-        // one thread runs the whole loop: a vote or a warp barrier between the products would cost
-        // more than the products of a narrow batch (an MMA of N = 16 takes 25 to 40 cycles)
-        if (tma::elect()) {
-            while (!wp.done()) {
-                bool moved = false;
-                if (!ws.done()) {
-                    if (!s_ready) s_ready = tma::test(&sm.q_full, sseg & 1) && tma::test(&sm.s_free[sb], (sph & 1) ^ 1);
-                    if (s_ready && (cs == 0 ? tma::test(&sm.pos_full[s_rs], s_rph) : tma::test(&sm.pair_full[s_ps], s_pph))) {
-                        moved = true;
-                        tc::fence_after_sync();
-                        const uint32_t d = t_s + sb * geo.npad;
-                        if (cs == 0) {
-                            const uint32_t a = pos_lo + s_rs * (kChunkB >> 4), b = q_lo + 8 * q_step;
+                    tc::mbar_arrive_expect_tx(&sm.pos_full[rs], bytes);
 #pragma unroll
-                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, s != 0);
-                            tc::commit(&sm.pos_empty[s_rs]);
-                            if (++s_rs == geo.nr) s_rs = 0, s_rph ^= 1;
-                        } else {
-                            const uint32_t a = pair_lo + s_ps * (kPairB >> 4), b = q_lo + 2 * (cs - 1) * q_step;
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, idS, 1);
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + (kChunkB >> 4) + 2 * s, b + q_step + 2 * s, idS, 1);
-                            if (++s_ps == geo.np) s_ps = 0, s_pph ^= 1;
-                        }
-                        if (++cs == 1 + kPairs) {
-                            cs = 0;
-                            ++js;
-                            tc::commit(&sm.s_full[sb]);
-                            if (js == ws.j1) tc::commit(&sm.q_empty);
-                            ++sk;
-                            s_ready = false;
-                            if (++sb == geo.sbufs) sb = 0, ++sph;
-                            if (js == ws.j1) {
-                                ws.next(p);
-                                ws.skip_idle(p);
-                                js = ws.j0;
-                                ++sseg;
-                            }
-                        }
-                    }
-                }
-                if (pk < sk && tma::test(&sm.p_full, pk & 1)) {
-                    moved = true;
-                    tc::fence_after_sync();
-                    const int steps = (min(kKvTile, wp.len - jp * kKvTile) + 15) / 16;
-                    const uint32_t more = jp != wp.j0;
-                    uint32_t d = tmem;
+                    for (int b = 0; b < 4; ++b)
+                        if (b < boxes) tma::load_3d(s_pos + rs * kChunkB + b * box, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
+                    ++sm.pos_issued;
+                    if (++rs == geo.nr) rs = 0, rph ^= 1;
                     for (int i = 0; i < kPairs; ++i) {
-                        const uint32_t a = vpair_lo + v_ps * (kPairB >> 4);
+                        ok = tc::mbar_wait(&sm.pair_empty[ps], pph ^ 1);
+                        if (!ok) break;
+                        tc::mbar_arrive_expect_tx(&sm.pair_full[ps], 2 * bytes);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b < boxes) {
+                                uint8_t *dst = s_pair + ps * kPairB + b * box;
+                                tma::load_3d(dst, &p.cache, &sm.pair_full[ps], 128 * i, ry[b], pg[b]);
+                                tma::load_3d(dst + kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64, ry[b], pg[b]);
+                            }
+                        ++sm.pair_issued;
+                        if (++ps == geo.np) ps = 0, pph ^= 1;
+                    }
+                }
+                ++seg;
+                w.next(p);
+                w.skip_idle(p);
+            }
+            if (!ok) sm.failed = 1;
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ---- score products: one thread; the value products have a thread of their own, so that
+        // neither polls for the other (a narrow batch's MMA takes less than a look at a barrier) ----
+        if (tma::elect()) {
+            const uint32_t id = tma::idesc(geo.ms, kKvTile, 0, 0);
+            const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), pos_lo = tma::lo_k(tc::smem_addr(s_pos));
+            const uint32_t pair_lo = tma::lo_k(tc::smem_addr(s_pair)), q_step = q_chunk >> 4;
+            Walk w;
+            w.start(p, sm);
+            w.skip_idle(p);
+            int k = 0, seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
+            while (!w.done() && ok) {
+                ok = tc::mbar_wait(&sm.q_full, seg & 1);
+                for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
+                    ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1) && tc::mbar_wait(&sm.pos_full[rs], rph);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t d = t_s + (k & 1) * kKvTile;
+                    {
+                        const uint32_t a = q_lo + 8 * q_step, b = pos_lo + rs * (kChunkB >> 4);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id, s != 0);
+                        tc::commit(&sm.pos_empty[rs]);
+                        if (++rs == geo.nr) rs = 0, rph ^= 1;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        ok = ok && tc::mbar_wait(&sm.pair_full[ps], pph);
+                        if (ok) {
+                            const uint32_t a = q_lo + 2 * i * q_step, b = pair_lo + ps * (kPairB >> 4);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id, 1);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + q_step + 2 * s, b + (kChunkB >> 4) + 2 * s, id, 1);
+                        }
+                        if (++ps == geo.np) ps = 0, pph ^= 1;
+                    }
+                    if (!ok) break;
+                    tc::commit(&sm.s_full[k & 1]);
+                    if (j + 1 == w.j1) tc::commit(&sm.q_empty);
+                }
+                ++seg;
+                w.next(p);
+                w.skip_idle(p);
+            }
+            if (!ok) sm.failed = 1;
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- value products: one thread ----
+        if (tma::elect()) {
+            const uint32_t id = tma::idesc(128, geo.npad, 1, 0);
+            const uint32_t pair_lo = tma::lo_mn(tc::smem_addr(s_pair), kChunkB), p_lo = tma::lo_k(tc::smem_addr(s_p));
+            Walk w;
+            w.start(p, sm);
+            w.skip_idle(p);
+            int k = 0, ps = 0;
+            while (!w.done() && ok) {
+                for (int j = w.j0; j < w.j1; ++j, ++k) {
+                    ok = tc::mbar_wait(&sm.p_full, k & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const int steps = (min(kKvTile, w.len - j * kKvTile) + 15) / 16;
+                    const uint32_t more = j != w.j0;
+                    uint32_t d = tmem;
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        const uint32_t a = pair_lo + ps * (kPairB >> 4);
                         if (steps == 4) {
 #pragma unroll
-                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 128 * s, idO, s != 0 ? 1 : more);
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 2 * s, id, s != 0 ? 1 : more);
                         } else {
-                            for (int s = 0; s < steps; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 128 * s, idO, s != 0 ? 1 : more);
+                            for (int s = 0; s < steps; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 2 * s, id, s != 0 ? 1 : more);
                         }
-                        tc::commit(&sm.pair_empty[v_ps]);
+                        tc::commit(&sm.pair_empty[ps]);
                         d += geo.npad;
-                        if (++v_ps == geo.np) v_ps = 0;
+                        if (++ps == geo.np) ps = 0;
                     }
                     tc::commit(&sm.pv_done);
-                    ++pk;
-                    if (++jp == wp.j1) {
-                        wp.next(p);
-                        wp.skip_idle(p);
-                        jp = wp.j0;
-                    }
                 }
-                if (moved) {
-                    idle = 0;
-                } else if ((++idle & 63) == 0) {
-                    const uint64_t now = tc::globaltimer();
-                    if (idle == 64) {
-                        since = now;
-                    } else if (now - since > tc::kWaitLimitNs) {
-                        sm.failed = 1;
-                        break;
-                    }
-                }
+                w.next(p);
+                w.skip_idle(p);
             }
+            if (!ok) sm.failed = 1;
         }
         __syncwarp();
     } else {
-        // ---- softmax: one thread a cached row (16 lanes of each warp) and its set's column groups; then the output ----
-        const int quarter = warp & 3, set = warp >> 2, groups = geo.npad / 16;
+        // ---- softmax: one thread a query row and half a tile; then the output ----
+        const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const int tok = quarter * 16 + lane;  // cached row within the tile, when lane < 16
-        const bool row_lane = lane < 16;
+        // M = 64 puts rows 16 q .. 16 q + 15 into lanes 32 q .. 32 q + 15 of TMEM
+        const int per_warp = geo.ms / 4, r = quarter * per_warp + lane;
+        const bool owner = lane < per_warp && r < rows_here, warp_rows = quarter * per_warp < rows_here;
+        const int unseen = p.m - 1 - (row_first + (owner ? r : 0)) / p.H;  // last cached rows that the row does not see
         const float c = p.scale * 1.4426950408889634f;
         const uint64_t c2 = pk2(c, c);
-        if (tid < kRowTile) sm.unseen[tid] = p.m - 1 - (row_first + min(tid, rows_here - 1)) / p.H;
-        named_sync(2, kSoftmaxThreads);
-        int k = 0, seg = 0, sb = 0, sph = 0, ps = 0;  // tiles and stretches worked on, S^T buffer and its round, ring slot
+        uint8_t *p_row = s_p + r * 128;
+        int k = 0, seg = 0, ps = 0;  // tiles and stretches worked on, ring slot
         Walk w;
         for (w.start(p, sm); !w.done() && ok; w.next(p)) {
-            uint64_t l2[kGroups][8];  // sums of p: this thread's cached rows, by query row
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) l2[i][e] = 0;
+            float m_ref = -INFINITY, l = 0.f;
             if (w.work) {
                 for (int j = w.j0; j < w.j1; ++j) {
-                    ok = tma::wait_warp(&sm.s_full[sb], sph & 1);
+                    ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1);
                     // a failed wait still meets the barriers below, so that no warp is left in them
                     if (ok) tc::fence_after_sync();
-                    uint32_t s[kGroups][16];
-                    if (ok) {
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i)
-                            if (2 * i + set < groups) tma::tmem_ld16_nowait(t_s + lanes + sb * geo.npad + 16 * (2 * i + set), s[i]);
+                    uint32_t s[kHalf];
+                    const bool first = j == w.j0;
+                    float mb = m_ref == -INFINITY ? 0.f : -m_ref * c, top = -INFINITY;
+                    if (warp_rows && ok) {
+                        tc::tmem_ld32_nowait(t_s + lanes + (k & 1) * kKvTile + set * kHalf, s);
                         tc::tmem_wait_ld();
                         tc::fence_before_sync();
+                        // cached rows of this thread's half that the row sees
+                        const int64_t seen = (int64_t)w.len - unseen - ((int64_t)j * kKvTile + set * kHalf);
+                        if (__any_sync(0xffffffffu, seen < kHalf)) {
+#pragma unroll
+                            for (int e = 0; e < kHalf; ++e)
+                                if (e >= seen) s[e] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < kHalf; e += 2)
+                            top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
                     }
-                    tma::arrive(&sm.s_free[sb]);
-                    if (++sb == geo.sbufs) sb = 0, ++sph;
-                    const int64_t row = (int64_t)j * kKvTile + tok;
-                    if (w.len - (p.m - 1) < ((int64_t)j + 1) * kKvTile) {  // the tile's end is hidden from some row
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i)
-                            if (2 * i + set < groups) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (row >= w.len - sm.unseen[16 * (2 * i + set) + e]) s[i][e] = 0xff800000u;
-                            }
-                    }
-                    const bool first = j == w.j0;
-                    float top = -INFINITY;  // how far a score passes its reference, in log2
-                    if (!first) {
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i)
-                            if (2 * i + set < groups) {
-                                const ulonglong2 *mb = reinterpret_cast<const ulonglong2 *>(&sm.mb[16 * (2 * i + set)]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const ulonglong2 b = mb[e];
-                                    const float2 x = upk2(fma2(pk2(__uint_as_float(s[i][4 * e]), __uint_as_float(s[i][4 * e + 1])), c2, b.x));
-                                    const float2 y = upk2(fma2(pk2(__uint_as_float(s[i][4 * e + 2]), __uint_as_float(s[i][4 * e + 3])), c2, b.y));
-                                    top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
-                                }
-                            }
-                    }
-                    // one barrier a tile: does a row need a new reference, did a wait fail
-                    const bool any = softmax_any(first || (row_lane && top > kGrow) || !ok);
+                    tma::arrive(&sm.s_free[k & 1]);
+                    // one barrier a tile: does a row need a new reference (also from -inf to a finite one), did a wait fail
+                    const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
                     if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
                     if (any) {
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i)
-                            if (2 * i + set < groups) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    float x = __uint_as_float(s[i][e]);
-#pragma unroll
-                                    for (int off = 8; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                                    if (lane == 0) sm.red[quarter][16 * (2 * i + set) + e] = x;
-                                }
-                            }
+                        sm.half[set][quarter * 32 + lane] = top;
                         // all stop together when any wait failed
                         if (softmax_any(!ok)) {
                             ok = false;
                             break;
                         }
-                        if (tid < geo.npad) {
-                            const float x = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
-                            const float old = first ? -INFINITY : sm.m_ref[tid];
-                            const bool grown = first || (x - old) * c > kGrow;  // also from -inf to a finite maximum
-                            const float m = grown ? x : old;
-                            sm.factor[tid] = grown ? tc::ex2((old - m) * c) : 1.0f;
-                            sm.m_ref[tid] = m;
-                            sm.mb[tid] = m == -INFINITY ? 0.f : -m * c;
-                        }
-                        named_sync(2, kSoftmaxThreads);
+                        top = fmaxf(top, sm.half[set ^ 1][quarter * 32 + lane]);
+                        const bool grown = first || (top - m_ref) * c > kGrow;
+                        const float m = grown ? top : m_ref, f = grown ? tc::ex2((m_ref - m) * c) : 1.0f;
                         if (!first) {
+                            l *= f;
+                            if (set == 0 && lane < per_warp) sm.factor[r] = f;
+                            named_sync(2, kSoftmaxThreads);
                             tc::fence_after_sync();
-#pragma unroll
-                            for (int i = 0; i < kGroups; ++i)
-                                if (2 * i + set < groups) {
-                                    const uint64_t *f = reinterpret_cast<const uint64_t *>(&sm.factor[16 * (2 * i + set)]);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) l2[i][e] = mul2(l2[i][e], f[e]);
-                                }
                             for (int i = 2 * set; i < 2 * set + 2; ++i)
-                                for (int e = 0; e < groups; ++e) {
-                                    const uint32_t at = tmem + lanes + i * geo.npad + 16 * e;
+                                for (int e = 0; e < geo.npad; e += 16) {
+                                    const uint32_t at = tmem + lanes + i * geo.npad + e;
                                     uint32_t x[16];
                                     tma::tmem_ld16_nowait(at, x);
                                     tc::tmem_wait_ld();
 #pragma unroll
-                                    for (int y = 0; y < 16; ++y)
-                                        x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[16 * e + y]);
+                                    for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[e + y]);
                                     tc::tmem_st16(at, x);
                                 }
                             tc::tmem_wait_st();
                         }
+                        m_ref = m;
+                        mb = m_ref == -INFINITY ? 0.f : -m_ref * c;
                     }
+                    if (warp_rows && ok) {
+                        const uint64_t mb2 = pk2(mb, mb);
+                        uint64_t l2[2] = {0, 0};
 #pragma unroll
-                    for (int i = 0; i < kGroups; ++i)
-                        if (2 * i + set < groups) {
-                            const int col = 16 * (2 * i + set);
-                            const ulonglong2 *mb = reinterpret_cast<const ulonglong2 *>(&sm.mb[col]);
-                            uint32_t h[8];
+                        for (int u = 0; u < kHalf / 8; ++u) {  // 16-byte units of the row, swizzled
+                            uint32_t h[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const ulonglong2 b = mb[e];
-                                const float2 x = upk2(fma2(pk2(__uint_as_float(s[i][4 * e]), __uint_as_float(s[i][4 * e + 1])), c2, b.x));
-                                const float2 y = upk2(fma2(pk2(__uint_as_float(s[i][4 * e + 2]), __uint_as_float(s[i][4 * e + 3])), c2, b.y));
-                                const float p0 = tc::ex2(x.x), p1 = tc::ex2(x.y), p2 = tc::ex2(y.x), p3 = tc::ex2(y.y);
-                                l2[i][2 * e] = add2(l2[i][2 * e], pk2(p0, p1));
-                                l2[i][2 * e + 1] = add2(l2[i][2 * e + 1], pk2(p2, p3));
-                                const __nv_bfloat162 h0 = __floats2bfloat162_rn(p0, p1), h1 = __floats2bfloat162_rn(p2, p3);
-                                h[2 * e] = *reinterpret_cast<const uint32_t *>(&h0);
-                                h[2 * e + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+                                const uint32_t *x = &s[8 * u + 2 * e];
+                                const float2 y = upk2(fma2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, mb2));
+                                const float a = tc::ex2(y.x), b = tc::ex2(y.y);
+                                l2[e & 1] = add2(l2[e & 1], pk2(a, b));
+                                const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
+                                h[e] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
-                            if (row_lane) {  // 16 query rows: two 16-byte units of the cached row's 128 bytes, swizzled
-                                uint8_t *at = s_p + (col >> 6) * kChunkB + tok * 128;
-                                const int u = (col & 63) >> 3, x = tok & 7;
-                                *reinterpret_cast<uint4 *>(at + ((u ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                                *reinterpret_cast<uint4 *>(at + (((u + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-                            }
+                            if (lane < per_warp && r < geo.npad)
+                                *reinterpret_cast<uint4 *>(p_row + (((4 * set + u) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
+                        const float2 ls = upk2(add2(l2[0], l2[1]));
+                        l += ls.x + ls.y;
+                    }
                     const int valid = min(kKvTile, w.len - j * kKvTile);
                     if (valid & 15) {  // value rows behind the sequence in the product's last step of 16
                         const int units = (-valid & 15) * 8;
@@ -553,7 +494,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                                 make_uint4(0, 0, 0, 0);
                         }
                     }
-                    ps = (ps + kPairs) % geo.np;
+                    ps += kPairs;
+                    if (ps >= geo.np) ps -= geo.np;
                     fence_proxy_async();
                     tc::fence_before_sync();
                     tma::arrive(&sm.p_full);
@@ -562,35 +504,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 if (ok) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
                 tc::fence_after_sync();
             }
-            // ---- the rows' sums, over this thread's lanes and quarters ----
-            if (w.work) {
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    if (2 * i + set < groups) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint64_t x = row_lane ? l2[i][e] : 0;
-#pragma unroll
-                            for (int off = 8; off > 0; off >>= 1) x = add2(x, __shfl_xor_sync(0xffffffffu, x, off));
-                            if (lane == 0) *reinterpret_cast<uint64_t *>(&sm.red[quarter][16 * (2 * i + set) + 2 * e]) = x;
-                        }
-                    }
-            }
+            sm.half[set][quarter * 32 + lane] = l;
             if (softmax_any(!ok)) ok = false;
+            l += sm.half[set ^ 1][quarter * 32 + lane];
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg & 3] != 0);
             if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
             const int64_t row0 = (int64_t)w.n * geo.R + row_first;
             const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.rows;
-            if (tid < rows_here) {
-                const float l = w.work ? (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]) : 0.f;
-                const float m = sm.m_ref[tid];
-                sm.factor[tid] = bad ? NAN : (!whole ? 1.0f : (l == 0.f ? 0.f : 1.0f / l));
-                if (!whole)
-                    p.part_ml[part0 + tid] = make_float2(m, bad ? NAN : l);
-                else if (p.lse)
-                    p.lse[row0 + tid] = bad ? NAN : (l == 0.f ? -INFINITY : m * p.scale + logf(l));
+            if (set == 0 && lane < per_warp) {
+                sm.factor[r] = bad ? NAN : (!whole ? 1.0f : (l == 0.f ? 0.f : 1.0f / l));
+                if (owner) {
+                    if (!whole)
+                        p.part_ml[part0 + r] = make_float2(m_ref, bad ? NAN : l);
+                    else if (p.lse)
+                        p.lse[row0 + r] = bad ? NAN : (l == 0.f ? -INFINITY : m_ref * p.scale + logf(l));
+                }
             }
             named_sync(2, kSoftmaxThreads);
             for (int i = 2 * set; i < 2 * set + 2; ++i)
@@ -631,17 +561,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (sm.failed && warp == 8) {
+    if (sm.failed && (warp == 8 || warp == 9)) {
         // a wait gave up: report it, and let what is in flight land before the memory goes
-        if (lane == 0) {
-            set_status(p.status, KDA_ERR_CUDA);
-            tc::commit(&sm.drained);
-            tc::mbar_wait(&sm.drained, 0);
-            if (sm.q_issued > 0) tc::mbar_wait(&sm.q_full, (sm.q_issued - 1) & 1);
-            for (int e = max(0, sm.pair_issued - geo.np); e < sm.pair_issued; ++e)
-                tc::mbar_wait(&sm.pair_full[e % geo.np], (e / geo.np) & 1);
-            for (int e = max(0, sm.pos_issued - geo.nr); e < sm.pos_issued; ++e)
-                tc::mbar_wait(&sm.pos_full[e % geo.nr], (e / geo.nr) & 1);
+        if (tma::elect()) {
+            tc::commit(&sm.drained);  // each issuing thread's own products
+            if (warp == 8) {
+                set_status(p.status, KDA_ERR_CUDA);
+                tc::mbar_wait(&sm.drained, 0);
+                if (sm.q_issued > 0) tc::mbar_wait(&sm.q_full, (sm.q_issued - 1) & 1);
+                for (int e = max(0, sm.pair_issued - geo.np); e < sm.pair_issued; ++e)
+                    tc::mbar_wait(&sm.pair_full[e % geo.np], (e / geo.np) & 1);
+                for (int e = max(0, sm.pos_issued - geo.nr); e < sm.pos_issued; ++e)
+                    tc::mbar_wait(&sm.pos_full[e % geo.nr], (e / geo.nr) & 1);
+            }
         }
         __syncwarp();
     }
@@ -749,8 +681,8 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     q.RT = (q.R + kRowTile - 1) / kRowTile;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    q.sbufs = 6 * q.npad <= 512 ? 2 : 1;
-    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + p_chunks(q.npad) * kChunkB;
+    q.ms = q.rows <= 64 ? 64 : 128;
+    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + (size_t)q.npad * 128;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
     q.np = (int32_t)((room - q.nr * kChunkB) / kPairB);
@@ -760,7 +692,7 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     q.smem = (uint32_t)(fixed + (size_t)q.np * kPairB + (size_t)q.nr * kChunkB);
     return q;
 }
-static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 9 * 96 * 128 - 2 * kChunkB >= 5 * kPairB + 2 * kChunkB, "96 rows leave a tile's rings");
+static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * 96 * 128 >= 5 * kPairB + 2 * kChunkB, "96 rows leave a tile's rings");
 
 // groups of CTAs that share the list: one CTA an SM
 int32_t groups_of(int32_t RT, int32_t sms) { return sms / RT > 0 ? sms / RT : 1; }
