@@ -68,6 +68,9 @@ struct DecodeGeom {
 
 struct DecodeArgs {
     CUtensorMap q_lat, q_pe, cache;
+    const __nv_bfloat16 *rows;  // the cache again, for the prefetch of a coming tile into L2
+    int64_t page_stride;
+    int32_t ahead;  // prefetch it: the ring holds less than two tiles
     const int32_t *table, *lens;
     int32_t max_pages, num_pages, page_size, rb;  // rb: rows of a TMA box (64, 32 or 16)
     int32_t N, H, m, G;
@@ -153,6 +156,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     const int rt = blockIdx.x % geo.RT, g = blockIdx.x / geo.RT;
 
     // ---- this group's run of the list ----
+    if (warp == 10 && lane == 0) {
+        tma::prefetch_map(&p.q_lat);
+        tma::prefetch_map(&p.q_pe);
+        tma::prefetch_map(&p.cache);
+    }
     if (warp == 0) {
         int64_t total = 0;
         for (int n = lane; n < p.N; n += 32) total += tiles_of(p, __ldg(p.lens + n));
@@ -273,6 +281,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         set_status(p.status, KDA_ERR_PAGES);
                     }
                     look(j + 1);
+                    if (p.ahead && j + 1 < w.j1) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
+                            if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
+                                tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow,
+                                                 (uint32_t)p.rb * kRow * 2);
+                        }
+                    }
                     const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
                     const uint32_t box = (uint32_t)p.rb * 128, bytes = boxes * box;
                     ok = tc::mbar_wait(&sm.pos_empty[rs], rph ^ 1);
@@ -580,8 +597,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
-// The join of the sequences that a run's border cuts. Block x belongs to the border before
-// group x + 1; the first border inside a sequence joins it. W warps share a row's parts,
+// The join of the sequences that a run's border cuts. With fewer sequences than groups block x
+// belongs to sequence x, whose place in the list it adds up itself; with more it belongs to
+// the border before group x + 1, where the main kernel left the place, and the first border
+// inside a sequence joins it. W warps share a row's parts,
 // each lane 16 of the 512 latents; the parts are added in list order within a warp and the
 // warps' sums in warp order, so the result does not depend on timing.
 constexpr int kJoinThreads = 512;
@@ -590,15 +609,41 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     constexpr int kRows = kJoinThreads / 32 / W;  // rows of a block
     __shared__ float s_o[kRows][W][kLatent];
     __shared__ float s_m[kRows][W], s_l[kRows][W];
-    pdl_wait();
-    const int b = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t total = p.head[0];
-    const int32_t *e = reinterpret_cast<const int32_t *>(p.head + 1) + 4 * b;
-    const int64_t at = total * b / p.G;
-    if (at >= total) return;
-    const int32_t n = e[0], inside = e[1], tiles = e[2];
-    const int64_t first = at - inside;  // list index of the sequence's first tile
-    if (inside == 0 || total * (b - 1) / p.G > first) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t n, tiles, b;  // the sequence, its tiles, the first border inside it
+    int64_t total, first; // tiles of the batch; list index of the sequence's first tile
+    if (p.N < p.G) {
+        n = blockIdx.x;
+        int64_t sum = 0, before = 0;
+        for (int i = lane; i < p.N; i += 32) {
+            const int32_t t = tiles_of(p, __ldg(p.lens + i));
+            sum += t;
+            if (i < n) before += t;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            before += __shfl_xor_sync(0xffffffffu, before, off);
+        }
+        total = sum;
+        first = before;
+        tiles = tiles_of(p, __ldg(p.lens + n));
+        // the first group that begins behind the sequence's first tile
+        b = (int32_t)(((first + 1) * p.G + total - 1) / total);
+        if (b >= p.G || total * b / p.G >= first + tiles) return;
+        pdl_wait();
+    } else {
+        b = blockIdx.x + 1;
+        pdl_wait();
+        total = p.head[0];
+        const int32_t *e = reinterpret_cast<const int32_t *>(p.head + 1) + 4 * b;
+        const int64_t at = total * b / p.G;
+        if (at >= total) return;
+        n = e[0];
+        tiles = e[2];
+        first = at - e[1];
+        if (e[1] == 0 || total * (b - 1) / p.G > first) return;
+    }
     const int rl = warp / W, part = warp % W, rr = blockIdx.y * kRows + rl;
     const bool live = rr < p.geo.R;
     const int rt = (live ? rr : 0) / p.geo.rows, r = (live ? rr : 0) % p.geo.rows;
@@ -714,7 +759,8 @@ DecodeWs decode_ws(const DecodeGeom &q) {
 template <int W>
 cudaError_t launch_join(const DecodeArgs &a, cudaStream_t st) {
     const int rows = kJoinThreads / 32 / W;
-    return launch_after(kda_mla_join_kernel<W>, dim3(a.G - 1, (a.geo.R + rows - 1) / rows), dim3(kJoinThreads), 0, st, a);
+    const int cuts = a.N < a.G ? a.N : a.G - 1;
+    return launch_after(kda_mla_join_kernel<W>, dim3(cuts, (a.geo.R + rows - 1) / rows), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace
@@ -764,6 +810,9 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (!tma::encode(&a.q_lat, q_lat, 2, dl, sl, a.geo.rows, 1) || !tma::encode(&a.q_pe, q_pe, 2, dp, sp, a.geo.rows, 1) ||
         !tma::encode(&a.cache, cache, 3, dc, sc, a.rb, 1))
         return KDA_ERR_CUDA;
+    a.rows = reinterpret_cast<const __nv_bfloat16 *>(cache);
+    a.page_stride = page_stride;
+    a.ahead = a.geo.np < 2 * kPairs;
     a.table = page_table;
     a.lens = cache_lens;
     a.max_pages = max_pages;
@@ -795,7 +844,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     if (a.G > 1) {
         // sequences of many parts: a block's 16 warps share a row; few parts: four warps a row
-        const cudaError_t e = num_seqs * (int64_t)8 <= a.G ? launch_join<16>(a, st) : launch_join<4>(a, st);
+        const cudaError_t e = num_seqs * (int64_t)32 <= a.G ? launch_join<16>(a, st) : launch_join<4>(a, st);
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return KDA_OK;

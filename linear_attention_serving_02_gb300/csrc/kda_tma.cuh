@@ -98,6 +98,10 @@ __device__ __forceinline__ bool test(uint64_t *mbar, uint32_t parity) {
 __device__ __forceinline__ void arrive(uint64_t *mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_addr(mbar)) : "memory");
 }
+// ask for bytes (16-byte aligned, a multiple of 16) to be in L2
+__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }

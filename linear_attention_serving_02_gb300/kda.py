@@ -352,29 +352,36 @@ def kda_debug_walk_fault(skip_commit_chunk, wait_limit_ns):
 MLA_LATENT, MLA_POS, MLA_ROW, MLA_NOPE, MLA_QK = 512, 64, 576, 128, 192
 
 
-def _on(device, stream):
-    """Context of a latent-attention or page call: `device` current, and the given stream (or
+# The checks below are on the path of every launch of a decode step; they cost about a third
+# of a microsecond a tensor. The raw handle of the current stream costs 0.1 us where
+# torch.cuda.current_stream() builds an object for 2.9 us.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(index, stream):
+    """Whether a call on device `index` must first make that device, or the given stream, current."""
+    return stream is not None or _current_device() != index
+
+
+def _on(index, stream):
+    """Context of a latent-attention or page call: device `index` current, and the given stream (or
     that device's current one) the one that torch allocates outputs and scratch on, so that
     their memory is not handed out again before the call's work is done."""
-    if stream is not None and stream.device != device:
-        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device)
+    if stream is not None and stream.device.index != index:
+        raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, index))
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(index)
 
 
-def _placed(device, stream):
-    """Whether a call may run as it is: `device` is current and no other stream is asked for."""
-    return stream is None and torch.cuda.current_device() == device.index
-
-
-def _mla_tensor(t, name, dtype, dim, device, tail=0):
+def _mla_tensor(t, name, dtype, dim, index, tail):
     """Type, rank and place of a tensor, and that its last `tail` dimensions are dense."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.dim() != dim:
         raise ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError("%s must be a CUDA tensor%s" % (name, "" if device is None else " on %s" % device))
-    if tail == dim:
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
+    if tail == dim or t.is_contiguous():
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
         return
@@ -385,31 +392,40 @@ def _mla_tensor(t, name, dtype, dim, device, tail=0):
         want *= t.shape[d]
 
 
-def _mla_cache(cache, page_table, num_seqs):
+def _cuda_index(t, name, dtype=None):
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _mla_cache(cache, page_table, num_seqs, index):
     """Checks of a paged cache; returns (page_stride, num_pages, page_size, max_pages)."""
-    _mla_tensor(cache, "cache", torch.bfloat16, 3, None, 2)
-    _mla_tensor(page_table, "page_table", torch.int32, 2, cache.device, 2)
+    _mla_tensor(cache, "cache", torch.bfloat16, 3, index, 2)
+    _mla_tensor(page_table, "page_table", torch.int32, 2, index, 2)
     pages, size, row = cache.shape
     if row != MLA_ROW:
         raise ValueError("cache must be [num_pages, page_size, 576]")
-    if page_table.shape[0] != num_seqs:
+    seqs, max_pages = page_table.shape
+    if seqs != num_seqs:
         raise ValueError("page_table must have a row for each of %d sequences" % num_seqs)
-    return (cache.stride(0) if pages > 1 else size * row), pages, size, page_table.shape[1]
+    return (cache.stride(0) if pages > 1 else size * row), pages, size, max_pages
 
 
-def _mla_ints(t, name, n, device):
-    _mla_tensor(t, name, torch.int32, 1, device, 1)
+def _mla_ints(t, name, n, index):
+    _mla_tensor(t, name, torch.int32, 1, index, 1)
     if t.shape[0] != n:
         raise ValueError("%s must have %d entries, got %d" % (name, n, t.shape[0]))
 
 
-def _mla_status(status, device):
-    if status is not None:
-        _mla_tensor(status, "status", torch.int32, 1, device, 1)
-        if status.shape[0] < 1:
-            raise ValueError("status must hold one int32")
-        return status.data_ptr()
-    return None
+def _mla_status(status, index):
+    if status is None:
+        return None
+    _mla_tensor(status, "status", torch.int32, 1, index, 1)
+    if status.shape[0] < 1:
+        raise ValueError("status must hold one int32")
+    return status.data_ptr()
 
 
 def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm_w=None, eps=1e-6, rope=None,
@@ -423,20 +439,19 @@ def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm
     sines) or None; q_pe: bf16 [T, H, 64], rotated into q_out (allocated, dense, when not given;
     may be q_pe itself).
     """
-    if c.is_cuda and not _placed(c.device, stream):
-        with _on(c.device, stream):
+    dev = _cuda_index(c, "c", torch.bfloat16)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
             return kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens, norm_w, eps, rope,
                                   rope_interleaved, q_pe, q_out, status)
-    _mla_tensor(c, "c", torch.bfloat16, 2, None, 1)
-    dev, T = c.device, c.shape[0]
+    _mla_tensor(c, "c", torch.bfloat16, 2, dev, 1)
+    T = c.shape[0]
     _mla_tensor(k_pe, "k_pe", torch.bfloat16, 2, dev, 1)
     if c.shape[1] != MLA_LATENT or k_pe.shape[0] != T or k_pe.shape[1] != MLA_POS:
         raise ValueError("c must be [T, 512] and k_pe [T, 64]")
     N = cache_lens.shape[0]
     _mla_ints(cache_lens, "cache_lens", N, dev)
-    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N)
-    if cache.device != dev:
-        raise ValueError("cache must be on %s" % dev)
+    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N, dev)
     if cu_seqlens is not None:
         _mla_ints(cu_seqlens, "cu_seqlens", N + 1, dev)
     if norm_w is not None:
@@ -454,9 +469,9 @@ def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm
         _mla_tensor(q_pe, "q_pe", torch.bfloat16, 3, dev, 1)
         H = q_pe.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, H, MLA_POS), dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty((T, H, MLA_POS), dtype=torch.bfloat16, device=c.device)
         _mla_tensor(q_out, "q_out", torch.bfloat16, 3, dev, 1)
-        if q_pe.shape != (T, H, MLA_POS) or q_out.shape != q_pe.shape:
+        if tuple(q_pe.shape) != (T, H, MLA_POS) or q_out.shape != q_pe.shape:
             raise ValueError("q_pe and q_out must be [T, H, 64]")
         qs, qos, qp, qop = q_pe.stride(), q_out.stride(), q_pe.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -468,7 +483,7 @@ def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm
         qp, qs[0], qs[1], qop, qos[0], qos[1], H,
         cu_seqlens.data_ptr() if cu_seqlens is not None else None, cache_lens.data_ptr(), page_table.data_ptr(),
         max_pages, cache.data_ptr(), page_stride, pages, size, T, N, _mla_status(status, dev),
-        torch.cuda.current_stream().cuda_stream)
+        _raw_stream(dev))
     if rc != 0:
         raise KdaError("kda_mla_append", rc)
     return q_out
@@ -477,20 +492,21 @@ def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm
 def kda_mla_gather(cache, page_table, cu_seqlens, total_rows, out=None, status=None, stream=None):
     """Rows of the paged latent cache as dense rows: out row cu_seqlens[n] + i is row i of
     sequence n. cu_seqlens: int32 [N + 1] of the lengths to read. Returns out, bf16 [total_rows, 576]."""
-    if cache.is_cuda and not _placed(cache.device, stream):
-        with _on(cache.device, stream):
+    dev = _cuda_index(cache, "cache", torch.bfloat16)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
             return kda_mla_gather(cache, page_table, cu_seqlens, total_rows, out, status)
-    N, dev, T = page_table.shape[0], cache.device, int(total_rows)
-    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N)
+    N, T = page_table.shape[0], int(total_rows)
+    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N, dev)
     _mla_ints(cu_seqlens, "cu_seqlens", N + 1, dev)
     if out is None:
-        out = torch.empty((T, MLA_ROW), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, MLA_ROW), dtype=torch.bfloat16, device=cache.device)
     _mla_tensor(out, "out", torch.bfloat16, 2, dev, 2)
-    if out.shape != (T, MLA_ROW):
+    if tuple(out.shape) != (T, MLA_ROW):
         raise ValueError("out must be [total_rows, 576]")
     rc = library().kda_mla_gather(cache.data_ptr(), page_stride, pages, size, cu_seqlens.data_ptr(),
                                   page_table.data_ptr(), max_pages, out.data_ptr(), T, N, _mla_status(status, dev),
-                                  torch.cuda.current_stream().cuda_stream)
+                                  _raw_stream(dev))
     if rc != 0:
         raise KdaError("kda_mla_gather", rc)
     return out
@@ -504,15 +520,16 @@ def kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal=True,
     k_pe: bf16 [Tk, 64] (rows may be strided); cu_seqlens_q, cu_seqlens_k: int32 [N + 1]. With
     causal a sequence's queries are its last tokens. o: bf16 [Tq, H, 128]; lse: fp32 [Tq, H].
     """
-    if q.is_cuda and not _placed(q.device, stream):
-        with _on(q.device, stream):
+    dev = _cuda_index(q, "q", torch.bfloat16)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
             return kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal, o, lse, status)
-    _mla_tensor(q, "q", torch.bfloat16, 3, None, 3)
-    dev, (Tq, H, d) = q.device, q.shape
+    _mla_tensor(q, "q", torch.bfloat16, 3, dev, 3)
+    Tq, H, d = q.shape
     _mla_tensor(kv, "kv", torch.bfloat16, 3, dev, 3)
     _mla_tensor(k_pe, "k_pe", torch.bfloat16, 2, dev, 1)
     Tk = kv.shape[0]
-    if d != MLA_QK or kv.shape != (Tk, H, 2 * MLA_NOPE) or k_pe.shape != (Tk, MLA_POS):
+    if d != MLA_QK or tuple(kv.shape) != (Tk, H, 2 * MLA_NOPE) or tuple(k_pe.shape) != (Tk, MLA_POS):
         raise ValueError("q must be [Tq, H, 192], kv [Tk, H, 256] and k_pe [Tk, 64]")
     N = cu_seqlens_q.shape[0] - 1
     if N < 0:
@@ -520,17 +537,17 @@ def kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal=True,
     _mla_ints(cu_seqlens_q, "cu_seqlens_q", N + 1, dev)
     _mla_ints(cu_seqlens_k, "cu_seqlens_k", N + 1, dev)
     if o is None:
-        o = torch.empty((Tq, H, MLA_NOPE), dtype=torch.bfloat16, device=dev)
+        o = torch.empty((Tq, H, MLA_NOPE), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
     _mla_tensor(o, "o", torch.bfloat16, 3, dev, 3)
     _mla_tensor(lse, "lse", torch.float32, 2, dev, 2)
-    if o.shape != (Tq, H, MLA_NOPE) or lse.shape != (Tq, H):
+    if tuple(o.shape) != (Tq, H, MLA_NOPE) or tuple(lse.shape) != (Tq, H):
         raise ValueError("o must be [Tq, H, 128] and lse [Tq, H]")
     rc = library().kda_mla_prefill(q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), k_pe.stride(0) if Tk > 1 else MLA_POS,
                                    cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), Tq, Tk, N, H, 1 if causal else 0,
                                    scale, o.data_ptr(), lse.data_ptr(), _mla_status(status, dev),
-                                   torch.cuda.current_stream().cuda_stream)
+                                   _raw_stream(dev))
     if rc != 0:
         raise KdaError("kda_mla_prefill", rc)
     return o, lse
@@ -550,37 +567,38 @@ def kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens
     last m - 1 - t rows. o: bf16 [N * m, H, 512]; lse: fp32 [N * m, H]. workspace: uint8, at least
     kda_mla_decode_workspace_size bytes (allocated when not given).
     """
-    if cache.is_cuda and not _placed(cache.device, stream):
-        with _on(cache.device, stream):
+    dev = _cuda_index(cache, "cache", torch.bfloat16)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
             return kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse, workspace,
                                   status)
-    m, N, dev = int(num_tokens), cache_lens.shape[0], cache.device
+    m, N = int(num_tokens), cache_lens.shape[0]
     _mla_tensor(q_lat, "q_lat", torch.bfloat16, 3, dev, 3)
     _mla_tensor(q_pe, "q_pe", torch.bfloat16, 3, dev, 3)
-    rows, H = q_lat.shape[0], q_lat.shape[1]
+    rows, H, latent = q_lat.shape
     if m < 0 or rows != N * m:
         raise ValueError("q_lat has %d rows, expected num_seqs * num_tokens = %d" % (rows, N * m))
-    if q_lat.shape[2] != MLA_LATENT or q_pe.shape != (rows, H, MLA_POS):
+    if latent != MLA_LATENT or tuple(q_pe.shape) != (rows, H, MLA_POS):
         raise ValueError("q_lat must be [N * m, H, 512] and q_pe [N * m, H, 64]")
     _mla_ints(cache_lens, "cache_lens", N, dev)
-    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N)
+    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N, dev)
     if o is None:
-        o = torch.empty((rows, H, MLA_LATENT), dtype=torch.bfloat16, device=dev)
+        o = torch.empty_like(q_lat)
     if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((rows, H), dtype=torch.float32, device=cache.device)
     _mla_tensor(o, "o", torch.bfloat16, 3, dev, 3)
     _mla_tensor(lse, "lse", torch.float32, 2, dev, 2)
-    if o.shape != (rows, H, MLA_LATENT) or lse.shape != (rows, H):
+    if o.shape != q_lat.shape or tuple(lse.shape) != (rows, H):
         raise ValueError("o must be [N * m, H, 512] and lse [N * m, H]")
     lib = library()
     if workspace is None:
-        workspace = torch.empty(lib.kda_mla_decode_workspace_size(N, H, m), dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be contiguous and on %s" % dev)
+        workspace = torch.empty(lib.kda_mla_decode_workspace_size(N, H, m), dtype=torch.uint8, device=cache.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on cuda:%d" % dev)
     rc = lib.kda_mla_decode(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), page_stride, pages, size,
                             page_table.data_ptr(), max_pages, cache_lens.data_ptr(), N, H, m, scale, o.data_ptr(),
                             lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                            _mla_status(status, dev), torch.cuda.current_stream().cuda_stream)
+                            _mla_status(status, dev), _raw_stream(dev))
     if rc != 0:
         raise KdaError("kda_mla_decode", rc)
     return o, lse
@@ -590,13 +608,15 @@ def _page_ids(ids, name):
     """A host list of page ids as a contiguous CPU int32 tensor."""
     if not isinstance(ids, torch.Tensor):
         ids = torch.tensor(list(ids), dtype=torch.int64)
-    if ids.is_cuda or ids.dim() != 1 or ids.is_floating_point() or ids.dtype == torch.bool:
+    if ids.dim() != 1 or ids.is_cuda:
         raise ValueError("%s must be a list or a 1-D CPU tensor of page ids" % name)
-    if ids.dtype != torch.int32:
+    if ids.dtype is not torch.int32:
+        if ids.dtype not in (torch.int64, torch.int16, torch.int8, torch.uint8):
+            raise TypeError("%s must hold whole numbers, got %s" % (name, ids.dtype))
         if ids.numel() and (int(ids.min()) < 0 or int(ids.max()) > 0x7FFFFFFF):
             raise KdaError("kda_pages_copy", -9)
         ids = ids.to(torch.int32)
-    return ids.contiguous()
+    return ids if ids.is_contiguous() else ids.contiguous()
 
 
 def kda_pages_copy(pool, src, dst, stream=None):
@@ -607,26 +627,29 @@ def kda_pages_copy(pool, src, dst, stream=None):
     lists or CPU tensors of page ids. KDA states [layers, slots, H, 128, 128] and conv states
     are pools too. Returns pool.
     """
-    if not pool.is_cuda or pool.dim() < 3:
-        raise ValueError("pool must be a CUDA tensor [layers, pages, ...]")
-    if not _placed(pool.device, stream):
-        with _on(pool.device, stream):
+    dev = _cuda_index(pool, "pool")
+    if pool.dim() < 3:
+        raise ValueError("pool must be [layers, pages, ...]")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
             return kda_pages_copy(pool, src, dst)
+    layers, pages, *page = pool.shape
+    strides = pool.stride()
     want = 1
-    for d in range(pool.dim() - 1, 1, -1):
-        if pool.shape[d] > 1 and pool.stride(d) != want:
+    for n, s in zip(reversed(page), reversed(strides)):
+        if n > 1 and s != want:
             raise ValueError("pool must be dense within a page")
-        want *= pool.shape[d]
+        want *= n
     src, dst = _page_ids(src, "src"), _page_ids(dst, "dst")
-    if src.numel() != dst.numel():
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
     es = pool.element_size()
     page_bytes = want * es
-    page_stride = pool.stride(1) * es if pool.shape[1] > 1 else page_bytes
-    layer_stride = pool.stride(0) * es if pool.shape[0] > 1 else page_stride * pool.shape[1]
-    rc = library().kda_pages_copy(pool.data_ptr(), page_stride, page_bytes, pool.shape[1], layer_stride,
-                                  pool.shape[0], src.data_ptr(), dst.data_ptr(), src.numel(),
-                                  torch.cuda.current_stream().cuda_stream)
+    page_stride = strides[1] * es if pages > 1 else page_bytes
+    layer_stride = strides[0] * es if layers > 1 else page_stride * pages
+    rc = library().kda_pages_copy(pool.data_ptr(), page_stride, page_bytes, pages, layer_stride, layers,
+                                  src.data_ptr(), dst.data_ptr(), n, _raw_stream(dev))
     if rc != 0:
         raise KdaError("kda_pages_copy", rc)
     return pool
