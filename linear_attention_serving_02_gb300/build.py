@@ -1,18 +1,23 @@
-"""Build the KDA CUDA library (sm_103a) in-tree.
+"""Build the KDA CUDA library (sm_103a) and its compiled Python binding in-tree.
 
 Compiles every csrc/*.cu with nvcc for sm_103a in parallel and links them into
 _build/libkda_gb300.so, a plain shared library exporting the C ABI of include/kda.h.
+csrc/kda_binding.cpp becomes _build/_kda_binding.so, the binding of the entry points whose
+calls are a few microseconds long (it uses torch's headers and links the library).
 """
 import concurrent.futures
 import glob
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libkda_gb300.so")
+BINDING = os.path.join(OUT_DIR, "_kda_binding.so")
+BINDING_SRC = os.path.join(CSRC, "kda_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
@@ -28,13 +33,13 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    return _sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -46,12 +51,18 @@ def build(force=False, verbose=False, extra_flags=()):
     srcs = _sources()
     objs = [os.path.join(OUT_DIR, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
+    srcs.append(BINDING_SRC)
+    objs.append(os.path.join(OUT_DIR, "kda_binding.o"))
+
     def compile_one(pair):
         src, obj = pair
-        cmd = [nvcc()] + ARCH + FLAGS + list(extra_flags) + ["-c", src, "-o", obj]
+        if src == BINDING_SRC:
+            cmd = ["g++"] + _binding_flags() + ["-c", src, "-o", obj]
+        else:
+            cmd = [nvcc()] + ARCH + FLAGS + list(extra_flags) + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
+            raise RuntimeError("%s failed on %s:\n%s%s" % (os.path.basename(cmd[0]), src, r.stdout, r.stderr))
         return r.stdout + r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
@@ -60,13 +71,37 @@ def build(force=False, verbose=False, extra_flags=()):
         for log in logs:
             if log.strip():
                 print(log)
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    _link([nvcc()] + ARCH + ["-shared"] + objs[:-1] + ["-lcudart"], LIB)
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    _link(["g++", "-shared", objs[-1], "-L" + OUT_DIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + torch_lib,
+           "-Wl,-rpath," + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], BINDING)
+    return LIB
+
+
+def _torch_dir():
+    import torch
+
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _binding_flags():
+    import torch
+
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    dirs = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    # torch's headers as system headers: their warnings are not this file's
+    return ["-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden", "-DAT_PER_OPERATOR_HEADERS",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + d for d in dirs] + [
+            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include")]
+
+
+def _link(cmd, target):
+    tmp = target + ".tmp.%d" % os.getpid()
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, target)
 
 
 if __name__ == "__main__":

@@ -1,12 +1,15 @@
 """Python binding of the KDA C ABI (include/kda.h): argument marshalling only.
 
-Each function here has the name of the C entry point it calls. Tensors are torch
+Each function here has the name of the C entry point it calls (through ctypes, or for the
+latent-attention and page calls through the compiled csrc/kda_binding.cpp). Tensors are torch
 CUDA tensors; the binding checks dtypes and shapes, passes raw pointers, sizes and the
 current CUDA stream, and raises KdaError on a non-zero status. Every step of the
 computation runs in the CUDA library; if the library cannot be built or loaded the
 import fails loudly. There is no other code path.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 
 import torch
 
@@ -349,83 +352,33 @@ def kda_debug_walk_fault(skip_commit_chunk, wait_limit_ns):
 
 
 # ---- latent attention over a paged cache, and the copies of pages (include/kda.h) ----
+# These calls are a few microseconds long and a decode step makes several, so their checks and
+# marshalling are compiled (csrc/kda_binding.cpp); what stands here is their signatures.
 MLA_LATENT, MLA_POS, MLA_ROW, MLA_NOPE, MLA_QK = 512, 64, 576, 128, 192
 
-
-# The checks below are on the path of every launch of a decode step; they cost about a third
-# of a microsecond a tensor. The raw handle of the current stream costs 0.1 us where
-# torch.cuda.current_stream() builds an object for 2.9 us.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_BINDING = None
 
 
-def _elsewhere(index, stream):
-    """Whether a call on device `index` must first make that device, or the given stream, current."""
-    return stream is not None or _current_device() != index
+def binding():
+    """The compiled binding (built in-tree with the library)."""
+    global _BINDING
+    if _BINDING is None:
+        library()
+        loader = importlib.machinery.ExtensionFileLoader("_kda_binding", _build.BINDING)
+        spec = importlib.util.spec_from_file_location("_kda_binding", _build.BINDING, loader=loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        mod.set_error(KdaError)
+        _BINDING = mod
+    return _BINDING
 
 
-def _on(index, stream):
-    """Context of a latent-attention or page call: device `index` current, and the given stream (or
-    that device's current one) the one that torch allocates outputs and scratch on, so that
-    their memory is not handed out again before the call's work is done."""
-    if stream is not None and stream.device.index != index:
-        raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, index))
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(index)
-
-
-def _mla_tensor(t, name, dtype, dim, index, tail):
-    """Type, rank and place of a tensor, and that its last `tail` dimensions are dense."""
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != dim:
-        raise ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
-    if t.get_device() != index:
-        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
-    if tail == dim or t.is_contiguous():
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return
-    want = 1
-    for d in range(dim - 1, dim - 1 - tail, -1):
-        if t.shape[d] > 1 and t.stride(d) != want:
-            raise ValueError("%s must be dense in its last %d dimensions" % (name, tail))
-        want *= t.shape[d]
-
-
-def _cuda_index(t, name, dtype=None):
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    return t.get_device()
-
-
-def _mla_cache(cache, page_table, num_seqs, index):
-    """Checks of a paged cache; returns (page_stride, num_pages, page_size, max_pages)."""
-    _mla_tensor(cache, "cache", torch.bfloat16, 3, index, 2)
-    _mla_tensor(page_table, "page_table", torch.int32, 2, index, 2)
-    pages, size, row = cache.shape
-    if row != MLA_ROW:
-        raise ValueError("cache must be [num_pages, page_size, 576]")
-    seqs, max_pages = page_table.shape
-    if seqs != num_seqs:
-        raise ValueError("page_table must have a row for each of %d sequences" % num_seqs)
-    return (cache.stride(0) if pages > 1 else size * row), pages, size, max_pages
-
-
-def _mla_ints(t, name, n, index):
-    _mla_tensor(t, name, torch.int32, 1, index, 1)
-    if t.shape[0] != n:
-        raise ValueError("%s must have %d entries, got %d" % (name, n, t.shape[0]))
-
-
-def _mla_status(status, index):
-    if status is None:
-        return None
-    _mla_tensor(status, "status", torch.int32, 1, index, 1)
-    if status.shape[0] < 1:
-        raise ValueError("status must hold one int32")
-    return status.data_ptr()
+def _on(stream, t):
+    """Context in which `stream` is the current one, so that torch allocates outputs and scratch on
+    it and their memory is not handed out again before the call's work is done."""
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return torch.cuda.stream(stream)
 
 
 def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm_w=None, eps=1e-6, rope=None,
@@ -439,77 +392,21 @@ def kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm
     sines) or None; q_pe: bf16 [T, H, 64], rotated into q_out (allocated, dense, when not given;
     may be q_pe itself).
     """
-    dev = _cuda_index(c, "c", torch.bfloat16)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, c):
             return kda_mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens, norm_w, eps, rope,
                                   rope_interleaved, q_pe, q_out, status)
-    _mla_tensor(c, "c", torch.bfloat16, 2, dev, 1)
-    T = c.shape[0]
-    _mla_tensor(k_pe, "k_pe", torch.bfloat16, 2, dev, 1)
-    if c.shape[1] != MLA_LATENT or k_pe.shape[0] != T or k_pe.shape[1] != MLA_POS:
-        raise ValueError("c must be [T, 512] and k_pe [T, 64]")
-    N = cache_lens.shape[0]
-    _mla_ints(cache_lens, "cache_lens", N, dev)
-    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N, dev)
-    if cu_seqlens is not None:
-        _mla_ints(cu_seqlens, "cu_seqlens", N + 1, dev)
-    if norm_w is not None:
-        _mla_tensor(norm_w, "norm_w", torch.float32, 1, dev, 1)
-        if norm_w.shape[0] != MLA_LATENT:
-            raise ValueError("norm_w must be [512]")
-    if rope is not None:
-        _mla_tensor(rope, "rope", torch.float32, 2, dev, 2)
-        if rope.shape[1] != MLA_POS:
-            raise ValueError("rope must be [positions, 64]")
-    H, qs, qos, qp, qop = 0, (0, 0), (0, 0), None, None
-    if q_pe is not None:
-        if rope is None:
-            raise ValueError("q_pe is only rotated: it needs rope")
-        _mla_tensor(q_pe, "q_pe", torch.bfloat16, 3, dev, 1)
-        H = q_pe.shape[1]
-        if q_out is None:
-            q_out = torch.empty((T, H, MLA_POS), dtype=torch.bfloat16, device=c.device)
-        _mla_tensor(q_out, "q_out", torch.bfloat16, 3, dev, 1)
-        if tuple(q_pe.shape) != (T, H, MLA_POS) or q_out.shape != q_pe.shape:
-            raise ValueError("q_pe and q_out must be [T, H, 64]")
-        qs, qos, qp, qop = q_pe.stride(), q_out.stride(), q_pe.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out needs q_pe")
-    rc = library().kda_mla_append(
-        c.data_ptr(), c.stride(0) if T > 1 else MLA_LATENT, k_pe.data_ptr(), k_pe.stride(0) if T > 1 else MLA_POS,
-        norm_w.data_ptr() if norm_w is not None else None, eps, rope.data_ptr() if rope is not None else None,
-        rope.shape[0] if rope is not None else 0, 1 if rope_interleaved else 0,
-        qp, qs[0], qs[1], qop, qos[0], qos[1], H,
-        cu_seqlens.data_ptr() if cu_seqlens is not None else None, cache_lens.data_ptr(), page_table.data_ptr(),
-        max_pages, cache.data_ptr(), page_stride, pages, size, T, N, _mla_status(status, dev),
-        _raw_stream(dev))
-    if rc != 0:
-        raise KdaError("kda_mla_append", rc)
-    return q_out
+    return (_BINDING or binding()).mla_append(c, k_pe, cache, page_table, cache_lens, cu_seqlens, norm_w, eps, rope,
+                                              rope_interleaved, q_pe, q_out, status)
 
 
 def kda_mla_gather(cache, page_table, cu_seqlens, total_rows, out=None, status=None, stream=None):
     """Rows of the paged latent cache as dense rows: out row cu_seqlens[n] + i is row i of
     sequence n. cu_seqlens: int32 [N + 1] of the lengths to read. Returns out, bf16 [total_rows, 576]."""
-    dev = _cuda_index(cache, "cache", torch.bfloat16)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, cache):
             return kda_mla_gather(cache, page_table, cu_seqlens, total_rows, out, status)
-    N, T = page_table.shape[0], int(total_rows)
-    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N, dev)
-    _mla_ints(cu_seqlens, "cu_seqlens", N + 1, dev)
-    if out is None:
-        out = torch.empty((T, MLA_ROW), dtype=torch.bfloat16, device=cache.device)
-    _mla_tensor(out, "out", torch.bfloat16, 2, dev, 2)
-    if tuple(out.shape) != (T, MLA_ROW):
-        raise ValueError("out must be [total_rows, 576]")
-    rc = library().kda_mla_gather(cache.data_ptr(), page_stride, pages, size, cu_seqlens.data_ptr(),
-                                  page_table.data_ptr(), max_pages, out.data_ptr(), T, N, _mla_status(status, dev),
-                                  _raw_stream(dev))
-    if rc != 0:
-        raise KdaError("kda_mla_gather", rc)
-    return out
+    return (_BINDING or binding()).mla_gather(cache, page_table, cu_seqlens, total_rows, out, status)
 
 
 def kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal=True, o=None, lse=None, status=None,
@@ -520,37 +417,10 @@ def kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal=True,
     k_pe: bf16 [Tk, 64] (rows may be strided); cu_seqlens_q, cu_seqlens_k: int32 [N + 1]. With
     causal a sequence's queries are its last tokens. o: bf16 [Tq, H, 128]; lse: fp32 [Tq, H].
     """
-    dev = _cuda_index(q, "q", torch.bfloat16)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, q):
             return kda_mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal, o, lse, status)
-    _mla_tensor(q, "q", torch.bfloat16, 3, dev, 3)
-    Tq, H, d = q.shape
-    _mla_tensor(kv, "kv", torch.bfloat16, 3, dev, 3)
-    _mla_tensor(k_pe, "k_pe", torch.bfloat16, 2, dev, 1)
-    Tk = kv.shape[0]
-    if d != MLA_QK or tuple(kv.shape) != (Tk, H, 2 * MLA_NOPE) or tuple(k_pe.shape) != (Tk, MLA_POS):
-        raise ValueError("q must be [Tq, H, 192], kv [Tk, H, 256] and k_pe [Tk, 64]")
-    N = cu_seqlens_q.shape[0] - 1
-    if N < 0:
-        raise ValueError("cu_seqlens_q must hold num_seqs + 1 offsets")
-    _mla_ints(cu_seqlens_q, "cu_seqlens_q", N + 1, dev)
-    _mla_ints(cu_seqlens_k, "cu_seqlens_k", N + 1, dev)
-    if o is None:
-        o = torch.empty((Tq, H, MLA_NOPE), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-    _mla_tensor(o, "o", torch.bfloat16, 3, dev, 3)
-    _mla_tensor(lse, "lse", torch.float32, 2, dev, 2)
-    if tuple(o.shape) != (Tq, H, MLA_NOPE) or tuple(lse.shape) != (Tq, H):
-        raise ValueError("o must be [Tq, H, 128] and lse [Tq, H]")
-    rc = library().kda_mla_prefill(q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), k_pe.stride(0) if Tk > 1 else MLA_POS,
-                                   cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), Tq, Tk, N, H, 1 if causal else 0,
-                                   scale, o.data_ptr(), lse.data_ptr(), _mla_status(status, dev),
-                                   _raw_stream(dev))
-    if rc != 0:
-        raise KdaError("kda_mla_prefill", rc)
-    return o, lse
+    return (_BINDING or binding()).mla_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, scale, causal, o, lse, status)
 
 
 def kda_mla_decode_workspace_size(num_seqs, num_heads, num_tokens=1):
@@ -564,44 +434,15 @@ def kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens
     q_lat: bf16 [N * m, H, 512], q_pe: bf16 [N * m, H, 64] (token t of sequence n at row n * m + t,
     m = num_tokens); cache: bf16 [num_pages, page_size, 576]; page_table: int32 [N, max_pages];
     cache_lens: int32 [N], the lengths with the m new tokens, of which token t sees all but the
-    last m - 1 - t rows. o: bf16 [N * m, H, 512]; lse: fp32 [N * m, H]. workspace: uint8, at least
-    kda_mla_decode_workspace_size bytes (allocated when not given).
+    last m - 1 - t rows. o: bf16 [N * m, H, 512]; lse: fp32 [N * m, H]. workspace: any dense tensor of
+    at least kda_mla_decode_workspace_size bytes (allocated when not given).
     """
-    dev = _cuda_index(cache, "cache", torch.bfloat16)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, q_lat):
             return kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse, workspace,
                                   status)
-    m, N = int(num_tokens), cache_lens.shape[0]
-    _mla_tensor(q_lat, "q_lat", torch.bfloat16, 3, dev, 3)
-    _mla_tensor(q_pe, "q_pe", torch.bfloat16, 3, dev, 3)
-    rows, H, latent = q_lat.shape
-    if m < 0 or rows != N * m:
-        raise ValueError("q_lat has %d rows, expected num_seqs * num_tokens = %d" % (rows, N * m))
-    if latent != MLA_LATENT or tuple(q_pe.shape) != (rows, H, MLA_POS):
-        raise ValueError("q_lat must be [N * m, H, 512] and q_pe [N * m, H, 64]")
-    _mla_ints(cache_lens, "cache_lens", N, dev)
-    page_stride, pages, size, max_pages = _mla_cache(cache, page_table, N, dev)
-    if o is None:
-        o = torch.empty_like(q_lat)
-    if lse is None:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=cache.device)
-    _mla_tensor(o, "o", torch.bfloat16, 3, dev, 3)
-    _mla_tensor(lse, "lse", torch.float32, 2, dev, 2)
-    if o.shape != q_lat.shape or tuple(lse.shape) != (rows, H):
-        raise ValueError("o must be [N * m, H, 512] and lse [N * m, H]")
-    lib = library()
-    if workspace is None:
-        workspace = torch.empty(lib.kda_mla_decode_workspace_size(N, H, m), dtype=torch.uint8, device=cache.device)
-    elif not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError("workspace must be contiguous and on cuda:%d" % dev)
-    rc = lib.kda_mla_decode(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), page_stride, pages, size,
-                            page_table.data_ptr(), max_pages, cache_lens.data_ptr(), N, H, m, scale, o.data_ptr(),
-                            lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                            _mla_status(status, dev), _raw_stream(dev))
-    if rc != 0:
-        raise KdaError("kda_mla_decode", rc)
-    return o, lse
+    return (_BINDING or binding()).mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse,
+                                              workspace, status)
 
 
 def _page_ids(ids, name):
@@ -627,29 +468,7 @@ def kda_pages_copy(pool, src, dst, stream=None):
     lists or CPU tensors of page ids. KDA states [layers, slots, H, 128, 128] and conv states
     are pools too. Returns pool.
     """
-    dev = _cuda_index(pool, "pool")
-    if pool.dim() < 3:
-        raise ValueError("pool must be [layers, pages, ...]")
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None:
+        with _on(stream, pool):
             return kda_pages_copy(pool, src, dst)
-    layers, pages, *page = pool.shape
-    strides = pool.stride()
-    want = 1
-    for n, s in zip(reversed(page), reversed(strides)):
-        if n > 1 and s != want:
-            raise ValueError("pool must be dense within a page")
-        want *= n
-    src, dst = _page_ids(src, "src"), _page_ids(dst, "dst")
-    n = src.shape[0]
-    if dst.shape[0] != n:
-        raise ValueError("src and dst must have the same length")
-    es = pool.element_size()
-    page_bytes = want * es
-    page_stride = strides[1] * es if pages > 1 else page_bytes
-    layer_stride = strides[0] * es if layers > 1 else page_stride * pages
-    rc = library().kda_pages_copy(pool.data_ptr(), page_stride, page_bytes, pages, layer_stride, layers,
-                                  src.data_ptr(), dst.data_ptr(), n, _raw_stream(dev))
-    if rc != 0:
-        raise KdaError("kda_pages_copy", rc)
-    return pool
+    return (_BINDING or binding()).pages_copy(pool, _page_ids(src, "src"), _page_ids(dst, "dst"))
