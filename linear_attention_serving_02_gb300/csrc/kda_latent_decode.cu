@@ -8,21 +8,21 @@
 //
 // Work. The sequences' cached rows are cut into tiles of 64; all tiles of the batch form one
 // list, and each of G groups of CTAs takes an equal run of it, so long and short sequences
-// load every SM alike whatever their lengths. The CTAs of a group take up to 96 query rows
-// each (row tiles) and walk the same tiles at the same time, so all but the first read them
-// from L2. A sequence that a run cuts leaves partial (O, max, sum), joined by a second kernel
-// in list order; the others are finished in place. Nothing waits on another CTA.
+// load every SM alike whatever their lengths. The CTAs of a group take up to 64 query rows
+// each (row tiles) and walk the same tiles; two neighbours form a cluster, each loads half of
+// every tile and TMA multicasts it to both, so a pair reads a tile once from L2. A sequence
+// that a run cuts leaves partial (O, max, sum), joined by a second kernel in list order; the
+// others are finished in place. Only the two CTAs of a cluster wait on each other.
 //
 // A tile in a CTA. TMA lays the 64 rows down once as 9 chunks of 64 columns (128-byte
-// swizzle). S = Q K^T: M = 64 or 128 query rows (up to 96 are used), N = 64 cached rows, read
-// K-major. Eight softmax warps take S from TMEM, one thread a query row and half of the tile,
-// and write P (bf16) to shared memory. The value product runs transposed, O^T = C^T P^T:
-// M = 128 latents (the same chunks, read MN-major), N = query rows. An MMA of K = 16 takes
-// N / 2 cycles, but at least 25 with M = 64 and 39 with M = 128 (measured; A's 128 rows are
-// 4 KB of shared memory): 96 rows need 36 x 48 + 16 x 56 cycles a tile, 16 rows
-// 36 x 32 + 16 x 39, where the tile's 72 KB take an SM's share of HBM about 3100. TMEM: O^T
-// takes 4 N columns and two S tiles 128, which fits up to N = 96; O itself (rows x 512) would
-// take every column.
+// swizzle). S = Q K^T: M = 64 query rows, N = 64 cached rows, read K-major. Eight softmax warps
+// take S from TMEM, one thread a query row and half of the tile, and write P (bf16) to shared
+// memory. The value product runs transposed, O^T = C^T P^T: M = 128 latents (the same chunks,
+// read MN-major), N = query rows. An MMA of K = 16 takes N / 2 cycles, but at least 25 with
+// M = 64 and 39 with M = 128 (measured; A's 128 rows are 4 KB of shared memory): 48 rows need
+// 36 x 32 + 16 x 44 cycles a tile, 16 rows 36 x 32 + 16 x 39, where the tile's 72 KB take an
+// SM's share of HBM about 3100 (a pair's share 1570). TMEM: O^T takes 4 N columns and two S
+// tiles 128; O itself (rows x 512) would take every column.
 //
 // The reference M_r only has to stay within 2^8 of the row's maximum (P is then far inside
 // bf16 and fp32), so a tile costs a comparison a score and one barrier; the halves' maxima are
@@ -30,9 +30,9 @@
 // reference by 2^8.
 //
 // Shared memory. Q takes 1152 B a row; the rest is a ring of 16 KB pairs of chunks and a
-// ring of 8 KB positional chunks. One thread issues the score products chunk by chunk as they
-// land, another the value products as their P is written; each pair of chunks is given back
-// as soon as its 128 latents are done.
+// ring of 8 KB positional chunks, two tiles or more. One thread issues the score products
+// chunk by chunk as they land, another the value products as their P is written; each pair
+// of chunks is given back as soon as its 128 latents are done.
 //
 // Rows of a tile behind the sequence's length (the rest of a page, or stale shared memory)
 // may hold anything: their scores are replaced by -inf, the product's 16-row steps past the
@@ -46,7 +46,7 @@ namespace kda {
 namespace {
 
 constexpr int kKvTile = 64;                     // cached rows of a tile
-constexpr int kRowTile = 96;                  // query rows of a CTA at most
+constexpr int kRowTile = 64;                  // query rows of a CTA at most
 constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
@@ -61,16 +61,12 @@ struct DecodeGeom {
     int32_t R;        // query rows of a sequence: m H
     int32_t RT, rows; // row tiles and query rows of each (a multiple of 8)
     int32_t npad;     // MMA columns of O^T: rows rounded up to 16
-    int32_t ms;       // MMA rows of S: 64 or 128
     int32_t np, nr;   // ring slots
     uint32_t smem;    // dynamic shared memory
 };
 
 struct DecodeArgs {
     CUtensorMap q_lat, q_pe, cache;
-    const __nv_bfloat16 *rows;  // the cache again, for the prefetch of a coming tile into L2
-    int64_t page_stride;
-    int32_t ahead;  // prefetch it: the ring holds less than two tiles
     const int32_t *table, *lens;
     int32_t max_pages, num_pages, page_size, rb;  // rb: rows of a TMA box (64, 32 or 16)
     int32_t N, H, m, G;
@@ -78,8 +74,8 @@ struct DecodeArgs {
     float scale;
     __nv_bfloat16 *o;
     float *lse;
-    float *part_o;   // [2 G, RT, rows, 512]
-    float2 *part_ml; // [2 G, RT, rows] reference maximum (raw scores), sum
+    float *part_o;   // [2 G, RT, npad, 512]
+    float2 *part_ml; // [2 G, RT, npad] reference maximum (raw scores), sum
     int64_t *head;   // [0]: tiles of the batch; then per group {sequence, first tile, tiles of the sequence}
     int32_t *status;
 };
@@ -87,7 +83,7 @@ struct DecodeArgs {
 struct DecodeSmem {
     uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, drained;
     uint64_t pair_full[kMaxPair], pair_empty[kMaxPair], pos_full[kMaxPos], pos_empty[kMaxPos];
-    float factor[128], half[2][128];  // by query row: scale of O^T, the halves' maxima or sums
+    float factor[kRowTile], half[2][kRowTile];  // by query row: scale of O^T, the halves' maxima or sums
     uint32_t tmem;
     int32_t failed, bad[4];
     int32_t first_seq, first_tile;
@@ -142,12 +138,14 @@ __device__ __forceinline__ bool softmax_any(bool flag) {
     return r != 0;
 }
 
+// `two`: clusters of two row tiles; a CTA's rank in its cluster is rt & 1
+template <bool two>
 __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const DecodeGeom &geo = p.geo;
     const uint32_t q_chunk = (uint32_t)geo.rows * 128;
-    uint8_t *s_q = base;               // 9 chunks of `rows` rows; M = 64 or 128 reads run on into what
+    uint8_t *s_q = base;               // 9 chunks of `rows` rows; M = 64 reads run on into what
     uint8_t *s_p = s_q + 9 * q_chunk;  // follows (P and the rings are longer), rows of S that nobody reads
     uint8_t *s_pair = s_p + (uint32_t)geo.npad * 128;  // P: npad rows of 64 cached rows
     uint8_t *s_pos = s_pair + (uint32_t)geo.np * kPairB;
@@ -215,8 +213,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             tc::mbar_init(&sm.p_full, kSoftmaxThreads);
             tc::mbar_init(&sm.pv_done, 1);
             tc::mbar_init(&sm.drained, 2);
-            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.pair_full[i], 1), tc::mbar_init(&sm.pair_empty[i], 1);
-            for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1);
+            // a slot is free when every CTA of the cluster is through with it
+            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.pair_full[i], 1), tc::mbar_init(&sm.pair_empty[i], 1 + two);
+            for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1 + two);
             tc::mbar_init_fence();
         }
     } else if (warp == 8) {
@@ -225,10 +224,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    if (two) tma::cluster_sync();  // the neighbour's barriers are set up before anything reaches them
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
     const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
-    const int row_first = rt * geo.rows, rows_here = min(geo.rows, geo.R - row_first);
+    const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
     if (warp == 10) {
@@ -281,23 +281,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         set_status(p.status, KDA_ERR_PAGES);
                     }
                     look(j + 1);
-                    if (p.ahead && j + 1 < w.j1) {
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
-                            if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
-                                tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow,
-                                                 (uint32_t)p.rb * kRow * 2);
-                        }
-                    }
                     const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
                     const uint32_t box = (uint32_t)p.rb * 128, bytes = boxes * box;
                     ok = tc::mbar_wait(&sm.pos_empty[rs], rph ^ 1);
                     if (!ok) break;
                     tc::mbar_arrive_expect_tx(&sm.pos_full[rs], bytes);
+                    if (!two || ((j ^ rt) & 1)) {  // of a pair, one CTA loads a tile's positions for both
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (b < boxes) tma::load_3d(s_pos + rs * kChunkB + b * box, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
+                        for (int b = 0; b < 4; ++b)
+                            if (b < boxes) {
+                                uint8_t *dst = s_pos + rs * kChunkB + b * box;
+                                if (two)
+                                    tma::load_3d_both(dst, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
+                                else
+                                    tma::load_3d(dst, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
+                            }
+                    }
                     ++sm.pos_issued;
                     if (++rs == geo.nr) rs = 0, rph ^= 1;
                     for (int i = 0; i < kPairs; ++i) {
@@ -308,8 +307,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         for (int b = 0; b < 4; ++b)
                             if (b < boxes) {
                                 uint8_t *dst = s_pair + ps * kPairB + b * box;
-                                tma::load_3d(dst, &p.cache, &sm.pair_full[ps], 128 * i, ry[b], pg[b]);
-                                tma::load_3d(dst + kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64, ry[b], pg[b]);
+                                if (two) {  // each CTA of a pair loads one chunk for both
+                                    const int c = rt & 1;
+                                    tma::load_3d_both(dst + c * kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64 * c, ry[b], pg[b]);
+                                } else {
+                                    tma::load_3d(dst, &p.cache, &sm.pair_full[ps], 128 * i, ry[b], pg[b]);
+                                    tma::load_3d(dst + kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64, ry[b], pg[b]);
+                                }
                             }
                         ++sm.pair_issued;
                         if (++ps == geo.np) ps = 0, pph ^= 1;
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         // ---- score products: one thread; the value products have a thread of their own, so that
         // neither polls for the other (a narrow batch's MMA takes less than a look at a barrier) ----
         if (tma::elect()) {
-            const uint32_t id = tma::idesc(geo.ms, kKvTile, 0, 0);
+            const uint32_t id = tma::idesc(kRowTile, kKvTile, 0, 0);
             const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), pos_lo = tma::lo_k(tc::smem_addr(s_pos));
             const uint32_t pair_lo = tma::lo_k(tc::smem_addr(s_pair)), q_step = q_chunk >> 4;
             Walk w;
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         const uint32_t a = q_lo + 8 * q_step, b = pos_lo + rs * (kChunkB >> 4);
 #pragma unroll
                         for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id, s != 0);
-                        tc::commit(&sm.pos_empty[rs]);
+                        tma::commit_free<two>(&sm.pos_empty[rs]);
                         if (++rs == geo.nr) rs = 0, rph ^= 1;
                     }
 #pragma unroll
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         } else {
                             for (int s = 0; s < steps; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 2 * s, id, s != 0 ? 1 : more);
                         }
-                        tc::commit(&sm.pair_empty[ps]);
+                        tma::commit_free<two>(&sm.pair_empty[ps]);
                         d += geo.npad;
                         if (++ps == geo.np) ps = 0;
                     }
@@ -413,8 +417,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         // M = 64 puts rows 16 q .. 16 q + 15 into lanes 32 q .. 32 q + 15 of TMEM
-        const int per_warp = geo.ms / 4, r = quarter * per_warp + lane;
-        const bool owner = lane < per_warp && r < rows_here, warp_rows = quarter * per_warp < rows_here;
+        const bool low = lane < 16;
+        const int r = quarter * 16 + (lane & 15);
+        const bool owner = low && r < rows_here, warp_rows = quarter * 16 < rows_here;
         const int unseen = p.m - 1 - (row_first + (owner ? r : 0)) / p.H;  // last cached rows that the row does not see
         const float c = p.scale * 1.4426950408889634f;
         const uint64_t c2 = pk2(c, c);
@@ -451,18 +456,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
                     if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
                     if (any) {
-                        sm.half[set][quarter * 32 + lane] = top;
+                        if (low) sm.half[set][r] = top;
                         // all stop together when any wait failed
                         if (softmax_any(!ok)) {
                             ok = false;
                             break;
                         }
-                        top = fmaxf(top, sm.half[set ^ 1][quarter * 32 + lane]);
+                        top = fmaxf(top, sm.half[set ^ 1][r]);
                         const bool grown = first || (top - m_ref) * c > kGrow;
                         const float m = grown ? top : m_ref, f = grown ? tc::ex2((m_ref - m) * c) : 1.0f;
                         if (!first) {
                             l *= f;
-                            if (set == 0 && lane < per_warp) sm.factor[r] = f;
+                            if (set == 0 && low) sm.factor[r] = f;
                             named_sync(2, kSoftmaxThreads);
                             tc::fence_after_sync();
                             for (int i = 2 * set; i < 2 * set + 2; ++i)
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                                 const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
                                 h[e] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
-                            if (lane < per_warp && r < geo.npad)
+                            if (low && r < geo.npad)
                                 *reinterpret_cast<uint4 *>(p_row + (((4 * set + u) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                         const float2 ls = upk2(add2(l2[0], l2[1]));
@@ -521,17 +526,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 if (ok) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
                 tc::fence_after_sync();
             }
-            sm.half[set][quarter * 32 + lane] = l;
+            if (low) sm.half[set][r] = l;
             if (softmax_any(!ok)) ok = false;
-            l += sm.half[set ^ 1][quarter * 32 + lane];
+            l += sm.half[set ^ 1][r];
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg & 3] != 0);
             if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
             const int64_t row0 = (int64_t)w.n * geo.R + row_first;
-            const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.rows;
-            if (set == 0 && lane < per_warp) {
-                sm.factor[r] = bad ? NAN : (!whole ? 1.0f : (l == 0.f ? 0.f : 1.0f / l));
+            const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.npad;
+            if (set == 0 && low) {
+                sm.factor[r] = bad ? NAN : (l == 0.f ? 0.f : 1.0f / l);
                 if (owner) {
                     if (!whole)
                         p.part_ml[part0 + r] = make_float2(m_ref, bad ? NAN : l);
@@ -552,21 +557,21 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     }
                     const int lat = 128 * i + 32 * quarter + lane;
                     if (whole) {
+                        // neighbouring lanes trade a value: each then holds two latents of one row
+                        __nv_bfloat16 *dst = p.o + (row0 + e + (lane & 1)) * kLatent + (lat & ~1);
+                        const int left = rows_here - e - (lane & 1);
 #pragma unroll
                         for (int y = 0; y < 16; y += 2) {
-                            // neighbouring lanes trade a value: each then holds two latents of one row
-                            const float a = __uint_as_float(x[y]) * sm.factor[e + y];
-                            const float b = __uint_as_float(x[y + 1]) * sm.factor[e + y + 1];
+                            const float2 f = *reinterpret_cast<const float2 *>(&sm.factor[e + y]);
+                            const float a = __uint_as_float(x[y]) * f.x, b = __uint_as_float(x[y + 1]) * f.y;
                             const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
                             const __nv_bfloat162 h = (lane & 1) ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-                            const int rr = e + y + (lane & 1);
-                            if (rr < rows_here)
-                                *reinterpret_cast<__nv_bfloat162 *>(p.o + (row0 + rr) * kLatent + (lat & ~1)) = h;
+                            if (y < left) *reinterpret_cast<__nv_bfloat162 *>(dst + y * kLatent) = h;
                         }
-                    } else {
+                    } else {  // rows past the last are written too (their columns of O^T are nobody's): parts are npad rows
+                        float *dst = p.part_o + (part0 + e) * kLatent + lat;
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            if (e + y < rows_here) p.part_o[(part0 + e + y) * kLatent + lat] = __uint_as_float(x[y]) * sm.factor[e + y];
+                        for (int y = 0; y < 16; ++y) dst[y * kLatent] = __uint_as_float(x[y]);
                     }
                 }
             // O^T has been read: the next stretch's P (all threads arrive) lets the MMA warp write it
@@ -593,6 +598,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             }
         }
         __syncwarp();
+    }
+    if (two) {
+        // the neighbour may still load into this CTA's shared memory or free its slots there
+        if (sm.failed && tid == 0) {
+            const uint64_t t0 = tc::globaltimer();
+            while (tc::globaltimer() - t0 < 50000) {  // what it has in flight after a failed wait, 50 us
+            }
+        }
+        __syncthreads();
+        tma::cluster_sync();
     }
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
@@ -657,7 +672,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
     auto row_of = [&](int i) {
         const int64_t gq = b - 1 + i;
-        return ((2 * gq + (i == 0 ? 1 : 0)) * p.geo.RT + rt) * p.geo.rows + r;
+        return ((2 * gq + (i == 0 ? 1 : 0)) * p.geo.RT + rt) * p.geo.npad + r;
     };
     auto empty = [&](int i) {  // a group between may have no tile at all
         const int64_t gq = b - 1 + i;
@@ -719,14 +734,15 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 
 constexpr size_t kSmemMax = 232448;
 
-// Row tiles of equal size, as few as 96 rows each allow; the rings take what Q and P leave.
+// Row tiles of equal size, as few as 64 rows each allow and an even number (clusters of two)
+// where there are several; the rings take what Q and P leave.
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
     q.RT = (q.R + kRowTile - 1) / kRowTile;
+    if (q.RT > 1) q.RT += q.RT & 1;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    q.ms = q.rows <= 64 ? 64 : 128;
     const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + (size_t)q.npad * 128;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
@@ -737,7 +753,7 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     q.smem = (uint32_t)(fixed + (size_t)q.np * kPairB + (size_t)q.nr * kChunkB);
     return q;
 }
-static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * 96 * 128 >= 5 * kPairB + 2 * kChunkB, "96 rows leave a tile's rings");
+static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * kRowTile * 128 >= 8 * kPairB + 2 * kChunkB, "two tiles' rings");
 
 // groups of CTAs that share the list: one CTA an SM
 int32_t groups_of(int32_t RT, int32_t sms) { return sms / RT > 0 ? sms / RT : 1; }
@@ -747,7 +763,7 @@ struct DecodeWs {
 };
 DecodeWs decode_ws(const DecodeGeom &q) {
     DecodeWs w;
-    const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = 2 * G * q.RT * q.rows;
+    const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = 2 * G * q.RT * q.npad;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     w.head = 0;
     w.ml = up(8 + 16 * kMaxGroups);
@@ -755,6 +771,24 @@ DecodeWs decode_ws(const DecodeGeom &q) {
     w.total = w.o + parts * kLatent * sizeof(float);
     return w;
 }
+
+// launch configuration of the main kernel: `cluster` neighbouring CTAs form a cluster
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    Launch(unsigned ctas, unsigned cluster, size_t smem, cudaStream_t st) {
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(kDecThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    Launch(const Launch &) = delete;
+};
 
 template <int W>
 cudaError_t launch_join(const DecodeArgs &a, cudaStream_t st) {
@@ -810,9 +844,6 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (!tma::encode(&a.q_lat, q_lat, 2, dl, sl, a.geo.rows, 1) || !tma::encode(&a.q_pe, q_pe, 2, dp, sp, a.geo.rows, 1) ||
         !tma::encode(&a.cache, cache, 3, dc, sc, a.rb, 1))
         return KDA_ERR_CUDA;
-    a.rows = reinterpret_cast<const __nv_bfloat16 *>(cache);
-    a.page_stride = page_stride;
-    a.ahead = a.geo.np < 2 * kPairs;
     a.table = page_table;
     a.lens = cache_lens;
     a.max_pages = max_pages;
@@ -821,10 +852,6 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     a.N = num_seqs;
     a.H = num_heads;
     a.m = num_tokens;
-    // no more groups than the longest page tables could give tiles to
-    const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
-    a.G = groups_of(a.geo.RT, sms < kMaxGroups ? sms : kMaxGroups);
-    if (a.G > most) a.G = (int32_t)most;
     a.scale = scale;
     a.o = reinterpret_cast<__nv_bfloat16 *>(o);
     a.lse = lse;
@@ -833,15 +860,32 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
     a.part_o = reinterpret_cast<float *>(ws + w.o);
     a.status = status;
-    static std::atomic<bool> configured[64];
-    if (!configured[device].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kda_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
+    // set up once a device: the kernel's shared memory, and how many clusters of two run at a time
+    static std::atomic<int32_t> pairs_at_a_time[64];
+    int32_t pairs = pairs_at_a_time[device].load(std::memory_order_acquire);
+    if (pairs == 0) {
+        if (cudaFuncSetAttribute(kda_mla_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
+            cudaFuncSetAttribute(kda_mla_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
             return KDA_ERR_CUDA;
-        configured[device].store(true, std::memory_order_release);
+        Launch two(2, 2, kSmemMax, nullptr);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<true>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
+        pairs = n;
+        pairs_at_a_time[device].store(pairs, std::memory_order_release);
     }
+    if (a.geo.RT > 1) sms = sms < 2 * pairs ? sms : 2 * pairs;
+    // no more groups than the longest page tables could give tiles to
+    const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
+    a.G = groups_of(a.geo.RT, sms < kMaxGroups ? sms : kMaxGroups);
+    if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    kda_mla_decode_kernel<<<(unsigned)(a.G * a.geo.RT), kDecThreads, a.geo.smem, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    if (a.geo.RT > 1) {
+        const Launch pairs_of((unsigned)(a.G * a.geo.RT), 2, a.geo.smem, st);
+        if (cudaLaunchKernelEx(&pairs_of.cfg, kda_mla_decode_kernel<true>, a) != cudaSuccess) return KDA_ERR_CUDA;
+    } else {
+        kda_mla_decode_kernel<false><<<(unsigned)a.G, kDecThreads, a.geo.smem, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
     if (a.G > 1) {
         // sequences of many parts: a block's 16 warps share a row; few parts: four warps a row
         const cudaError_t e = num_seqs * (int64_t)32 <= a.G ? launch_join<16>(a, st) : launch_join<4>(a, st);
