@@ -4,10 +4,11 @@
 // and rounded once. gather: a copy. Both are bound by their bytes: a token's row is read
 // once and written once (2304 B), a query head's 64 values too (256 B).
 //
-// One warp takes one item of a token: item 0 its row, the others 16 query heads each. A
+// A warp takes a token's row and its first 16 query heads; further heads go 16 to a warp. A
 // lane holds 16 latent values in two 16-byte accesses, so the sum of squares is one warp
-// reduction and nothing passes through shared memory; 8 lanes rotate one head, four pairs a
-// lane. gather gives a warp four rows, nine 16-byte accesses a lane, all in flight at once.
+// reduction and nothing passes through shared memory; four lanes rotate one head, eight pairs a
+// lane in two 16-byte accesses. All of a warp's loads are issued before it looks up where the
+// token goes. gather gives a warp four rows, nine 16-byte accesses a lane, all in flight at once.
 
 #include "kda_latent_common.cuh"
 
@@ -30,7 +31,7 @@ struct AppendArgs {
     int64_t q_ts, q_hs;
     __nv_bfloat16 *q_out;
     int64_t qo_ts, qo_hs;
-    int32_t H, items;  // items of a token: 1 + ceil(H / 16), or 1
+    int32_t H;  // 0 without queries
     const int32_t *cu, *lens;
     PagedRows<__nv_bfloat16> cache;
     int64_t T;
@@ -55,77 +56,69 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 
-// The 64 positional values of one head, by 8 lanes. A lane loads the two 8-byte pieces that
-// hold its four pairs: pairs (i, i + 32) for i = 4 j .. 4 j + 3, or (2 i, 2 i + 1) of the
+// The 64 positional values of one head, by 4 lanes. A lane loads the two 16-byte pieces that
+// hold its eight pairs: pairs (i, i + 32) for i = 8 j .. 8 j + 7, or (2 i, 2 i + 1) of the
 // same i, whose pieces are adjacent.
 struct PosPiece {
-    uint2 a, b;
+    uint4 a, b;
 };
+__device__ __forceinline__ int piece_at(int j, int second, bool interleaved) {
+    return interleaved ? 16 * j + 8 * second : 8 * j + 32 * second;
+}
 __device__ __forceinline__ PosPiece load_pos(const __nv_bfloat16 *p, int j, bool interleaved) {
-    PosPiece v;
-    if (interleaved) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p + 8 * j);
-        v.a = make_uint2(u.x, u.y);
-        v.b = make_uint2(u.z, u.w);
-    } else {
-        v.a = *reinterpret_cast<const uint2 *>(p + 4 * j);
-        v.b = *reinterpret_cast<const uint2 *>(p + 32 + 4 * j);
-    }
-    return v;
+    return PosPiece{*reinterpret_cast<const uint4 *>(p + piece_at(j, 0, interleaved)),
+                    *reinterpret_cast<const uint4 *>(p + piece_at(j, 1, interleaved))};
 }
 __device__ __forceinline__ void store_pos(__nv_bfloat16 *p, int j, bool interleaved, const PosPiece &v) {
-    if (interleaved) {
-        *reinterpret_cast<uint4 *>(p + 8 * j) = make_uint4(v.a.x, v.a.y, v.b.x, v.b.y);
-    } else {
-        *reinterpret_cast<uint2 *>(p + 4 * j) = v.a;
-        *reinterpret_cast<uint2 *>(p + 32 + 4 * j) = v.b;
-    }
+    *reinterpret_cast<uint4 *>(p + piece_at(j, 0, interleaved)) = v.a;
+    *reinterpret_cast<uint4 *>(p + piece_at(j, 1, interleaved)) = v.b;
 }
 __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
     const float x = a * c - b * s;
     b = b * c + a * s;
     a = x;
 }
-__device__ __forceinline__ PosPiece rotate(const PosPiece &v, const float4 &c, const float4 &s, bool interleaved) {
-    float x[8];
-    unpack8(make_uint4(v.a.x, v.a.y, v.b.x, v.b.y), x);
+__device__ __forceinline__ PosPiece rotate(const PosPiece &v, const float (&c)[8], const float (&s)[8], bool interleaved) {
+    float x[8], y[8];
+    unpack8(v.a, x);
+    unpack8(v.b, y);
     if (interleaved) {
-        turn(x[0], x[1], c.x, s.x);
-        turn(x[2], x[3], c.y, s.y);
-        turn(x[4], x[5], c.z, s.z);
-        turn(x[6], x[7], c.w, s.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+            turn(y[2 * i], y[2 * i + 1], c[i + 4], s[i + 4]);
+        }
     } else {
-        turn(x[0], x[4], c.x, s.x);
-        turn(x[1], x[5], c.y, s.y);
-        turn(x[2], x[6], c.z, s.z);
-        turn(x[3], x[7], c.w, s.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i]);
     }
-    const uint4 u = pack8(x);
-    return PosPiece{make_uint2(u.x, u.y), make_uint2(u.z, u.w)};
+    return PosPiece{pack8(x), pack8(y)};
+}
+__device__ __forceinline__ void load8(float (&x)[8], const float *p) {
+    *reinterpret_cast<float4 *>(&x[0]) = __ldg(reinterpret_cast<const float4 *>(p));
+    *reinterpret_cast<float4 *>(&x[4]) = __ldg(reinterpret_cast<const float4 *>(p + 4));
 }
 
 __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __grid_constant__ AppendArgs p) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = item / p.items;
-    const int part = (int)(item - t * p.items);
+    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int part = blockIdx.y;
     if (t >= p.T) return;
 
     // the loads that need no position first
     uint4 lo, hi;
-    PosPiece pe[kHeadsPerItem / 4];
+    PosPiece k_pe, q[kHeadsPerItem / 8];
     const bool il = p.interleaved != 0;
-    const int j = lane & 7, h0 = (part - 1) * kHeadsPerItem + (lane >> 3);
+    const int j = lane & 3, h0 = part * kHeadsPerItem + (lane >> 2);
     if (part == 0) {
         const __nv_bfloat16 *c = p.c + t * p.c_stride;
         lo = *reinterpret_cast<const uint4 *>(c + 8 * lane);
         hi = *reinterpret_cast<const uint4 *>(c + 256 + 8 * lane);
-        if (lane < 8) pe[0] = load_pos(p.k_pe + t * p.k_pe_stride, j, il);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kHeadsPerItem / 4; ++i)
-            if (h0 + 4 * i < p.H) pe[i] = load_pos(p.q_pe + t * p.q_ts + (h0 + 4 * i) * p.q_hs, j, il);
+        if (lane < 4) k_pe = load_pos(p.k_pe + t * p.k_pe_stride, j, il);
     }
+#pragma unroll
+    for (int i = 0; i < kHeadsPerItem / 8; ++i)
+        if (h0 + 8 * i < p.H) q[i] = load_pos(p.q_pe + t * p.q_ts + (h0 + 8 * i) * p.q_hs, j, il);
 
     int n;
     int64_t end;
@@ -139,27 +132,29 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
         end = (n + 1) * p.per_seq;
     }
     const int64_t pos = p.lens[n] - (end - t);
-    const int64_t entry = pos >= 0 ? pos / p.cache.page_size : -1;
-    bool good = entry >= 0 && entry < p.cache.max_pages && (p.rope == nullptr || pos < p.rope_len);
+    const uint32_t entry = (uint32_t)max(pos, (int64_t)0) / (uint32_t)p.cache.page_size;
+    bool good = pos >= 0 && entry < (uint32_t)p.cache.max_pages && (p.rope == nullptr || pos < p.rope_len);
     if (!good && lane == 0) set_status(p.status, KDA_ERR_SEQLENS);
 
-    float4 co = make_float4(1.f, 1.f, 1.f, 1.f), si = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (good && p.rope) {
-        co = *reinterpret_cast<const float4 *>(p.rope + pos * kPos + 4 * j);
-        si = *reinterpret_cast<const float4 *>(p.rope + pos * kPos + kPos / 2 + 4 * j);
-    }
+    float co[8], si[8];
     int32_t page = -1;
-    if (good) page = p.cache.table[(int64_t)n * p.cache.max_pages + entry];
-    if (good && (page < 0 || page >= p.cache.num_pages)) {
-        good = false;
-        if (lane == 0) set_status(p.status, KDA_ERR_PAGES);
+    if (good) {
+        if (p.rope) {
+            load8(co, p.rope + pos * kPos + 8 * j);
+            load8(si, p.rope + pos * kPos + kPos / 2 + 8 * j);
+        }
+        page = p.cache.table[(int64_t)n * p.cache.max_pages + entry];
+        if (page < 0 || page >= p.cache.num_pages) {
+            good = false;
+            if (lane == 0) set_status(p.status, KDA_ERR_PAGES);
+        }
     }
 
-    if (part == 0) {
-        if (!good) return;
-        __nv_bfloat16 *row = p.cache.rows + page * p.cache.page_stride + (pos - entry * p.cache.page_size) * kRow;
+    if (part == 0 && good) {
+        __nv_bfloat16 *row =
+            p.cache.rows + page * p.cache.page_stride + (int64_t)((uint32_t)pos - entry * (uint32_t)p.cache.page_size) * kRow;
         if (p.norm_w) {
-            float x[8], y[8];
+            float x[8], y[8], w[8];
             unpack8(lo, x);
             unpack8(hi, y);
             float ss = 0.f;
@@ -168,28 +163,25 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
             const float r = 1.0f / sqrtf(ss * (1.0f / kLatent) + p.eps);
-            float w[8];
-            *reinterpret_cast<float4 *>(&w[0]) = __ldg(reinterpret_cast<const float4 *>(p.norm_w + 8 * lane));
-            *reinterpret_cast<float4 *>(&w[4]) = __ldg(reinterpret_cast<const float4 *>(p.norm_w + 8 * lane + 4));
+            load8(w, p.norm_w + 8 * lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
             lo = pack8(x);
-            *reinterpret_cast<float4 *>(&w[0]) = __ldg(reinterpret_cast<const float4 *>(p.norm_w + 256 + 8 * lane));
-            *reinterpret_cast<float4 *>(&w[4]) = __ldg(reinterpret_cast<const float4 *>(p.norm_w + 256 + 8 * lane + 4));
+            load8(w, p.norm_w + 256 + 8 * lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
             hi = pack8(y);
         }
         *reinterpret_cast<uint4 *>(row + 8 * lane) = lo;
         *reinterpret_cast<uint4 *>(row + 256 + 8 * lane) = hi;
-        if (lane < 8) store_pos(row + kLatent, j, il, p.rope ? rotate(pe[0], co, si, il) : pe[0]);
-        return;
+        if (lane < 4) store_pos(row + kLatent, j, il, p.rope ? rotate(k_pe, co, si, il) : k_pe);
     }
-    const PosPiece nan{make_uint2(0x7fff7fffu, 0x7fff7fffu), make_uint2(0x7fff7fffu, 0x7fff7fffu)};
+    const uint4 nan4 = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
 #pragma unroll
-    for (int i = 0; i < kHeadsPerItem / 4; ++i)
-        if (h0 + 4 * i < p.H)
-            store_pos(p.q_out + t * p.qo_ts + (h0 + 4 * i) * p.qo_hs, j, il, good ? rotate(pe[i], co, si, il) : nan);
+    for (int i = 0; i < kHeadsPerItem / 8; ++i)
+        if (h0 + 8 * i < p.H)
+            store_pos(p.q_out + t * p.qo_ts + (h0 + 8 * i) * p.qo_hs, j, il,
+                      good ? rotate(q[i], co, si, il) : PosPiece{nan4, nan4});
 }
 
 __global__ void __launch_bounds__(kRowThreads)
@@ -208,15 +200,15 @@ __global__ void __launch_bounds__(kRowThreads)
         src[r] = nullptr;
         while (n + 1 < N && t >= cu[n + 1]) ++n;  // empty sequences are stepped over
         if (n < 0 || t >= T || t >= cu[n + 1] || t < cu[n]) continue;
-        const int64_t i = t - cu[n], entry = i / cache.page_size;
+        const uint32_t i = (uint32_t)(t - cu[n]), entry = i / (uint32_t)cache.page_size;
         int32_t page = -1;
-        if (entry < cache.max_pages) page = cache.table[(int64_t)n * cache.max_pages + entry];
+        if (entry < (uint32_t)cache.max_pages) page = cache.table[(int64_t)n * cache.max_pages + entry];
         if (page < 0 || page >= cache.num_pages) {
             nan_rows |= 1u << r;
-            if (lane == 0) set_status(status, entry < cache.max_pages ? KDA_ERR_PAGES : KDA_ERR_SEQLENS);
+            if (lane == 0) set_status(status, entry < (uint32_t)cache.max_pages ? KDA_ERR_PAGES : KDA_ERR_SEQLENS);
             continue;
         }
-        src[r] = cache.rows + page * cache.page_stride + (i - entry * cache.page_size) * kRow;
+        src[r] = cache.rows + page * cache.page_stride + (int64_t)(i - entry * (uint32_t)cache.page_size) * kRow;
     }
     constexpr int kAcc = kGatherRows * kRowUnits / 32;  // 9
     uint4 v[kAcc];
@@ -290,8 +282,7 @@ int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, in
     a.q_out = reinterpret_cast<__nv_bfloat16 *>(q_out);
     a.qo_ts = q_out_token_stride;
     a.qo_hs = q_out_head_stride;
-    a.H = num_heads;
-    a.items = 1 + (q_pe ? (num_heads + kHeadsPerItem - 1) / kHeadsPerItem : 0);
+    a.H = q_pe ? num_heads : 0;
     a.cu = cu_seqlens;
     a.lens = cache_lens;
     a.cache = {reinterpret_cast<__nv_bfloat16 *>(cache), page_stride, num_pages, page_size, page_table, max_pages};
@@ -299,9 +290,9 @@ int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, in
     a.N = num_seqs;
     a.per_seq = cu_seqlens ? 0 : total_tokens / num_seqs;
     a.status = status;
-    const int64_t blocks = (total_tokens * a.items + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    if (blocks > INT32_MAX) return KDA_ERR_SHAPE;
-    kda_mla_append_kernel<<<(unsigned)blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const int64_t blocks = (total_tokens + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    const int parts = a.H > kHeadsPerItem ? (a.H + kHeadsPerItem - 1) / kHeadsPerItem : 1;
+    kda_mla_append_kernel<<<dim3((unsigned)blocks, (unsigned)parts), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

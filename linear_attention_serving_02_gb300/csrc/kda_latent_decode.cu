@@ -99,6 +99,19 @@ __device__ __forceinline__ int32_t tiles_of(const DecodeArgs &p, int32_t len) {
     return bad_len(p, len) || len == 0 ? 1 : (int32_t)(((int64_t)len + kKvTile - 1) / kKvTile);
 }
 
+// The list's cut into G runs: the first `extra` of them one tile longer than the others.
+struct Runs {
+    int64_t each;
+    int32_t extra;
+    __device__ __forceinline__ Runs(int64_t total, int32_t G) : each(total / G), extra((int32_t)(total - each * G)) {}
+    __device__ __forceinline__ int64_t begin(int32_t g) const { return g * each + min(g, extra); }
+    // the run that holds tile x
+    __device__ __forceinline__ int32_t of(int64_t x) const {
+        const int64_t longer = extra * (each + 1);
+        return (int32_t)(x < longer ? x / (each + 1) : extra + (x - longer) / each);
+    }
+};
+
 // A walk over a run of the list, one stretch of tiles of one sequence after the other.
 struct Walk {
     int32_t n, j0, j1, tiles, len;
@@ -164,7 +177,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         for (int n = lane; n < p.N; n += 32) total += tiles_of(p, __ldg(p.lens + n));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-        const int64_t begin = total * g / p.G, end = total * (g + 1) / p.G;
+        const Runs runs(total, p.G);
+        const int64_t begin = runs.begin(g), end = runs.begin(g + 1);
         int64_t before = 0;
         int seq = p.N - 1;
         int64_t first = 0;
@@ -625,48 +639,48 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     __shared__ float s_o[kRows][W][kLatent];
     __shared__ float s_m[kRows][W], s_l[kRows][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int32_t n, tiles, b;  // the sequence, its tiles, the first border inside it
-    int64_t total, first; // tiles of the batch; list index of the sequence's first tile
+    int32_t n, tiles, b;  // the sequence, its tiles, the run after the one that holds its first tile
+    int64_t first;        // list index of that tile
+    int count;            // parts
     if (p.N < p.G) {
         n = blockIdx.x;
-        int64_t sum = 0, before = 0;
+        int64_t total = 0, before = 0;
         for (int i = lane; i < p.N; i += 32) {
             const int32_t t = tiles_of(p, __ldg(p.lens + i));
-            sum += t;
+            total += t;
             if (i < n) before += t;
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            total += __shfl_xor_sync(0xffffffffu, total, off);
             before += __shfl_xor_sync(0xffffffffu, before, off);
         }
-        total = sum;
+        const Runs runs(total, p.G);
         first = before;
         tiles = tiles_of(p, __ldg(p.lens + n));
-        // the first group that begins behind the sequence's first tile
-        b = (int32_t)(((first + 1) * p.G + total - 1) / total);
-        if (b >= p.G || total * b / p.G >= first + tiles) return;
+        b = runs.of(first) + 1;
+        count = runs.of(first + tiles - 1) - b + 2;
+        if (count == 1) return;
         pdl_wait();
     } else {
         b = blockIdx.x + 1;
         pdl_wait();
-        total = p.head[0];
-        const int32_t *e = reinterpret_cast<const int32_t *>(p.head + 1) + 4 * b;
-        const int64_t at = total * b / p.G;
+        const int64_t total = p.head[0];
+        const Runs runs(total, p.G);
+        const int64_t at = runs.begin(b);
         if (at >= total) return;
+        const int32_t *e = reinterpret_cast<const int32_t *>(p.head + 1) + 4 * b;
         n = e[0];
         tiles = e[2];
         first = at - e[1];
-        if (e[1] == 0 || total * (b - 1) / p.G > first) return;
+        if (e[1] == 0 || runs.of(first) != b - 1) return;
+        count = runs.of(first + tiles - 1) - b + 2;
     }
     const int rl = warp / W, part = warp % W, rr = blockIdx.y * kRows + rl;
     const bool live = rr < p.geo.R;
     const int rt = (live ? rr : 0) / p.geo.rows, r = (live ? rr : 0) % p.geo.rows;
     const float c = p.scale * 1.4426950408889634f;
-    // parts: group b - 1 (slot 1, it holds the sequence's start), then groups b, b + 1, ... while they begin inside
-    int last = b;
-    while (last + 1 < p.G && total * (last + 1) / p.G < first + tiles) ++last;
-    const int count = last - (b - 1) + 1;
+    // parts: run b - 1 (slot 1, it holds the sequence's start), then the following runs (slot 0)
     float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = 0.f;
@@ -674,20 +688,15 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
         const int64_t gq = b - 1 + i;
         return ((2 * gq + (i == 0 ? 1 : 0)) * p.geo.RT + rt) * p.geo.npad + r;
     };
-    auto empty = [&](int i) {  // a group between may have no tile at all
-        const int64_t gq = b - 1 + i;
-        return total * gq / p.G == total * (gq + 1) / p.G;
-    };
     if (live) {
         // the common maximum of this warp's parts first, then one weighted sum
         for (int i = part + W * lane; i < count; i += W * 32)
-            if (!empty(i)) m = fmaxf(m, p.part_ml[row_of(i)].x);
+            m = fmaxf(m, p.part_ml[row_of(i)].x);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
         for (int i = part; i < count; i += W) {
-            if (empty(i)) continue;
             const int64_t q = row_of(i);
             const float2 ml = p.part_ml[q];
             const float f = tc::ex2((ml.x - ms) * c);
@@ -887,8 +896,10 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (a.G > 1) {
-        // sequences of many parts: a block's 16 warps share a row; few parts: four warps a row
-        const cudaError_t e = num_seqs * (int64_t)32 <= a.G ? launch_join<16>(a, st) : launch_join<4>(a, st);
+        // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four,
+        // and two or three are one warp's (256 sequences of 96 heads: XXX us against XXX with four)
+        const int64_t n = num_seqs;
+        const cudaError_t e = n * 32 <= a.G ? launch_join<16>(a, st) : (n * 4 <= a.G ? launch_join<4>(a, st) : launch_join<1>(a, st));
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return KDA_OK;
