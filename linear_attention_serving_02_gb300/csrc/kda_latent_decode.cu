@@ -61,12 +61,14 @@ struct DecodeGeom {
     int32_t R;        // query rows of a sequence: m H
     int32_t RT, rows; // row tiles and query rows of each (a multiple of 8)
     int32_t npad;     // MMA columns of O^T: rows rounded up to 16
+    int32_t qt;       // pairs of Q's latent chunks (128 latents) kept in TMEM; the others in shared memory
     int32_t np, nr;   // ring slots
     uint32_t smem;    // dynamic shared memory
 };
 
 struct DecodeArgs {
     CUtensorMap q_lat, q_pe, cache;
+    const __nv_bfloat16 *q;  // q_lat again
     const int32_t *table, *lens;
     int32_t max_pages, num_pages, page_size, rb;  // rb: rows of a TMA box (64, 32 or 16)
     int32_t N, H, m, G;
@@ -81,7 +83,7 @@ struct DecodeArgs {
 };
 
 struct DecodeSmem {
-    uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, drained;
+    uint64_t q_full, q_empty, q_ready, s_full[2], s_free[2], p_full, pv_done, drained;
     uint64_t pair_full[kMaxPair], pair_empty[kMaxPair], pos_full[kMaxPos], pos_empty[kMaxPos];
     float factor[kRowTile], half[2][kRowTile];  // by query row: scale of O^T, the halves' maxima or sums
     uint32_t tmem;
@@ -151,15 +153,18 @@ __device__ __forceinline__ bool softmax_any(bool flag) {
     return r != 0;
 }
 
-// `two`: clusters of two row tiles; a CTA's rank in its cluster is rt & 1
-template <bool two>
+// QT > 0: clusters of two row tiles, a CTA's rank is rt & 1; the first QT pairs of Q's latent
+// chunks are kept in TMEM (a constant, so that the issue loop has no choice to make)
+template <int QT>
 __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    constexpr bool two = QT > 0;
     const DecodeGeom &geo = p.geo;
     const uint32_t q_chunk = (uint32_t)geo.rows * 128;
-    uint8_t *s_q = base;               // 9 chunks of `rows` rows; M = 64 reads run on into what
-    uint8_t *s_p = s_q + 9 * q_chunk;  // follows (P and the rings are longer), rows of S that nobody reads
+    constexpr int q_chunks = 9 - 2 * QT;      // of Q in shared memory, the positions last
+    uint8_t *s_q = base;                      // chunks of `rows` rows; M = 64 reads run on into what
+    uint8_t *s_p = s_q + q_chunks * q_chunk;  // follows (P and the rings are longer), rows of S that nobody reads
     uint8_t *s_pair = s_p + (uint32_t)geo.npad * 128;  // P: npad rows of 64 cached rows
     uint8_t *s_pos = s_pair + (uint32_t)geo.np * kPairB;
     DecodeSmem &sm = *reinterpret_cast<DecodeSmem *>(s_pos + (uint32_t)geo.nr * kChunkB);
@@ -220,6 +225,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             }
             tc::mbar_init(&sm.q_full, 1);
             tc::mbar_init(&sm.q_empty, 1);
+            tc::mbar_init(&sm.q_ready, kSoftmaxThreads);
             tc::mbar_init(&sm.s_full[0], 1);
             tc::mbar_init(&sm.s_full[1], 1);
             tc::mbar_init(&sm.s_free[0], kSoftmaxThreads);
@@ -242,6 +248,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
     const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
+    const uint32_t t_q = t_s + 2 * kKvTile;    // then Q's first latents, two to a column
     const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
@@ -277,9 +284,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 if (!ok) break;
                 sm.bad[seg & 3] = 0;
                 const int row = (int)((int64_t)w.n * geo.R + row_first);
-                tc::mbar_arrive_expect_tx(&sm.q_full, 9 * q_chunk);
-                tma::load_2d(s_q + 8 * q_chunk, &p.q_pe, &sm.q_full, 0, row);
-                for (int c = 0; c < 8; ++c) tma::load_2d(s_q + c * q_chunk, &p.q_lat, &sm.q_full, 64 * c, row);
+                tc::mbar_arrive_expect_tx(&sm.q_full, q_chunks * q_chunk);
+                tma::load_2d(s_q + (q_chunks - 1) * q_chunk, &p.q_pe, &sm.q_full, 0, row);
+                for (int c = 2 * QT; c < 8; ++c)
+                    tma::load_2d(s_q + (c - 2 * QT) * q_chunk, &p.q_lat, &sm.q_full, 64 * c, row);
                 ++sm.q_issued;
                 for (int j = w.j0; j < w.j1 && ok; ++j) {
                     bool bad = false;
@@ -352,14 +360,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             w.skip_idle(p);
             int k = 0, seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
             while (!w.done() && ok) {
-                ok = tc::mbar_wait(&sm.q_full, seg & 1);
+                ok = tc::mbar_wait(&sm.q_full, seg & 1) && (!two || tc::mbar_wait(&sm.q_ready, seg & 1));
                 for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
                     ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1) && tc::mbar_wait(&sm.pos_full[rs], rph);
                     if (!ok) break;
                     tc::fence_after_sync();
                     const uint32_t d = t_s + (k & 1) * kKvTile;
                     {
-                        const uint32_t a = q_lo + 8 * q_step, b = pos_lo + rs * (kChunkB >> 4);
+                        const uint32_t a = q_lo + (q_chunks - 1) * q_step, b = pos_lo + rs * (kChunkB >> 4);
 #pragma unroll
                         for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id, s != 0);
                         tma::commit_free<two>(&sm.pos_empty[rs]);
@@ -368,8 +376,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i) {
                         ok = ok && tc::mbar_wait(&sm.pair_full[ps], pph);
-                        if (ok) {
-                            const uint32_t a = q_lo + 2 * i * q_step, b = pair_lo + ps * (kPairB >> 4);
+                        if (ok && i < QT) {
+                            const uint32_t a = t_q + 64 * i, b = pair_lo + ps * (kPairB >> 4);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) tma::mma_ts(d, a + 8 * s, b + 2 * s, id, 1);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) tma::mma_ts(d, a + 32 + 8 * s, b + (kChunkB >> 4) + 2 * s, id, 1);
+                        } else if (ok) {
+                            const uint32_t a = q_lo + 2 * (i - QT) * q_step, b = pair_lo + ps * (kPairB >> 4);
 #pragma unroll
                             for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id, 1);
 #pragma unroll
@@ -439,8 +453,33 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         const uint64_t c2 = pk2(c, c);
         uint8_t *p_row = s_p + r * 128;
         int k = 0, seg = 0, ps = 0;  // tiles and stretches worked on, ring slot
+        // Q's first latents into TMEM, in the lanes of S's rows: this thread's row, half of each pair. The
+        // last stretch's score products are through: its last tile was taken
+        auto load_q = [&](const Walk &s) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((int64_t)s.n * geo.R + row_first + max(0, min(r, rows_here - 1))) * kLatent + 64 * set);
+            uint32_t x[2 * QT + 1][16];
+#pragma unroll
+            for (int i = 0; i < 2 * QT; ++i)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 v = __ldg(src + 16 * (i >> 1) + 4 * (i & 1) + u);
+                    x[i][4 * u] = v.x, x[i][4 * u + 1] = v.y, x[i][4 * u + 2] = v.z, x[i][4 * u + 3] = v.w;
+                }
+#pragma unroll
+            for (int i = 0; i < 2 * QT; ++i) tc::tmem_st16(t_q + lanes + 64 * (i >> 1) + 32 * set + 16 * (i & 1), x[i]);
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            tma::arrive(&sm.q_ready);
+        };
         Walk w;
-        for (w.start(p, sm); !w.done() && ok; w.next(p)) {
+        w.start(p, sm);
+        if constexpr (two) {
+            Walk first = w;
+            first.skip_idle(p);
+            if (!first.done()) load_q(first);
+        }
+        for (; !w.done() && ok; w.next(p)) {
             float m_ref = -INFINITY, l = 0.f;
             if (w.work) {
                 for (int j = w.j0; j < w.j1; ++j) {
@@ -536,6 +575,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     tc::fence_before_sync();
                     tma::arrive(&sm.p_full);
                     ++k;
+                }
+                if constexpr (two) {
+                    // the next stretch's queries before this one's output, so that its scores start meanwhile
+                    Walk after = w;
+                    after.next(p);
+                    after.skip_idle(p);
+                    if (ok && !after.done()) load_q(after);
                 }
                 if (ok) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
                 tc::fence_after_sync();
@@ -752,7 +798,8 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     if (q.RT > 1) q.RT += q.RT & 1;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)9 * q.rows * 128 + (size_t)q.npad * 128;
+    q.qt = q.RT > 1 ? (q.npad <= 48 ? 3 : 2) : 0;  // 4 npad + 128 + 64 qt TMEM columns: 512 at both
+    const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)(9 - 2 * q.qt) * q.rows * 128 + (size_t)q.npad * 128;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
     q.np = (int32_t)((room - q.nr * kChunkB) / kPairB);
@@ -853,6 +900,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (!tma::encode(&a.q_lat, q_lat, 2, dl, sl, a.geo.rows, 1) || !tma::encode(&a.q_pe, q_pe, 2, dp, sp, a.geo.rows, 1) ||
         !tma::encode(&a.cache, cache, 3, dc, sc, a.rb, 1))
         return KDA_ERR_CUDA;
+    a.q = reinterpret_cast<const __nv_bfloat16 *>(q_lat);
     a.table = page_table;
     a.lens = cache_lens;
     a.max_pages = max_pages;
@@ -873,12 +921,13 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     static std::atomic<int32_t> pairs_at_a_time[64];
     int32_t pairs = pairs_at_a_time[device].load(std::memory_order_acquire);
     if (pairs == 0) {
-        if (cudaFuncSetAttribute(kda_mla_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
-            cudaFuncSetAttribute(kda_mla_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
+        if (cudaFuncSetAttribute(kda_mla_decode_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
+            cudaFuncSetAttribute(kda_mla_decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
+            cudaFuncSetAttribute(kda_mla_decode_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
             return KDA_ERR_CUDA;
         Launch two(2, 2, kSmemMax, nullptr);
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<true>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
+        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<3>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
         pairs = n;
         pairs_at_a_time[device].store(pairs, std::memory_order_release);
     }
@@ -890,9 +939,10 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a.geo.RT > 1) {
         const Launch pairs_of((unsigned)(a.G * a.geo.RT), 2, a.geo.smem, st);
-        if (cudaLaunchKernelEx(&pairs_of.cfg, kda_mla_decode_kernel<true>, a) != cudaSuccess) return KDA_ERR_CUDA;
+        if (cudaLaunchKernelEx(&pairs_of.cfg, a.geo.qt == 3 ? kda_mla_decode_kernel<3> : kda_mla_decode_kernel<2>, a) != cudaSuccess)
+            return KDA_ERR_CUDA;
     } else {
-        kda_mla_decode_kernel<false><<<(unsigned)a.G, kDecThreads, a.geo.smem, st>>>(a);
+        kda_mla_decode_kernel<0><<<(unsigned)a.G, kDecThreads, a.geo.smem, st>>>(a);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (a.G > 1) {

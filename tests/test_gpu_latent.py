@@ -280,6 +280,12 @@ DECODE = [
     ([20000], 64, 12, 1),
     ([9000, 1, 0, 4000], 64, 16, 2),
     ([100 + 7 * i for i in range(170)], 16, 3, 1),
+    # several row tiles: 384, 130 and 2000 query rows
+    ([300, 0, 71], 64, 96, 4),
+    ([513, 2], 32, 130, 1),
+    ([100, 40], 16, 125, 16),
+    ([40 + 5 * i for i in range(160)], 64, 72, 1),
+    ([6000, 1], 64, 96, 1),
 ]
 
 
