@@ -605,35 +605,38 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 }
             }
             named_sync(2, kSoftmaxThreads);
-            for (int i = 2 * set; i < 2 * set + 2; ++i)
-                for (int e = 0; e < rows_here; e += 16) {
+            for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                const int lat = 128 * i + 32 * quarter + lane;
+                for (int e = 0; 16 * e < rows_here; ++e) {
                     uint32_t x[16];
                     if (w.work && ok) {
-                        tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + e, x);
+                        tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + 16 * e, x);
                         tc::tmem_wait_ld();
                     } else {
 #pragma unroll
                         for (int y = 0; y < 16; ++y) x[y] = 0;
                     }
-                    const int lat = 128 * i + 32 * quarter + lane;
                     if (whole) {
                         // neighbouring lanes trade a value: each then holds two latents of one row
-                        __nv_bfloat16 *dst = p.o + (row0 + e + (lane & 1)) * kLatent + (lat & ~1);
-                        const int left = rows_here - e - (lane & 1);
+                        __nv_bfloat16 *dst = p.o + (row0 + 16 * e + (lane & 1)) * kLatent + (lat & ~1);
+                        const int left = rows_here - 16 * e - (lane & 1);
 #pragma unroll
                         for (int y = 0; y < 16; y += 2) {
-                            const float2 f = *reinterpret_cast<const float2 *>(&sm.factor[e + y]);
-                            const float a = __uint_as_float(x[y]) * f.x, b = __uint_as_float(x[y + 1]) * f.y;
-                            const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
-                            const __nv_bfloat162 h = (lane & 1) ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-                            if (y < left) *reinterpret_cast<__nv_bfloat162 *>(dst + y * kLatent) = h;
+                            const float2 f = *reinterpret_cast<const float2 *>(&sm.factor[16 * e + y]);
+                            const __nv_bfloat162 h =
+                                __floats2bfloat162_rn(__uint_as_float(x[y]) * f.x, __uint_as_float(x[y + 1]) * f.y);
+                            const uint32_t own = *reinterpret_cast<const uint32_t *>(&h);
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                            const uint32_t two_lat = (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                            if (y < left) *reinterpret_cast<uint32_t *>(dst + y * kLatent) = two_lat;
                         }
                     } else {  // rows past the last are written too (their columns of O^T are nobody's): parts are npad rows
-                        float *dst = p.part_o + (part0 + e) * kLatent + lat;
+                        float *dst = p.part_o + (part0 + 16 * e) * kLatent + lat;
 #pragma unroll
                         for (int y = 0; y < 16; ++y) dst[y * kLatent] = __uint_as_float(x[y]);
                     }
                 }
+            }
             // O^T has been read: the next stretch's P (all threads arrive) lets the MMA warp write it
             tc::fence_before_sync();
             named_sync(2, kSoftmaxThreads);
