@@ -36,6 +36,7 @@ constexpr uint32_t kChunk = 128 * 128;  // bytes of a 128-row chunk
 constexpr int kKSlots = 4, kVSlots = 2;
 constexpr int kThreads = 320;  // 2 x 4 softmax warps, the MMA warp, the TMA warp
 constexpr float kRescale = 8.0f;
+constexpr int kParts = 4;  // P of a key tile is handed over in parts of 32 keys
 
 struct PrefillArgs {
     CUtensorMap q, kv, pe;
@@ -53,7 +54,7 @@ struct PrefillSmem {
     uint8_t k[kKSlots][kChunk];
     uint8_t v[kVSlots][2][kChunk];
     uint64_t q_full[2], k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
-    uint64_t s_full[2], p_full[2], pv_done[2], drained;
+    uint64_t s_full[2], p_full[2][kParts], pv_done[2], drained;
     uint32_t tmem;
     int32_t seq, tile, failed;
     int32_t k_issued, v_issued;  // loads the producer started (read after a failed wait only)
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
             for (int i = 0; i < 2; ++i) {
                 tc::mbar_init(&sm.q_full[i], 1);
                 tc::mbar_init(&sm.s_full[i], 1);
-                tc::mbar_init(&sm.p_full[i], kTileQ);
+                for (int k = 0; k < kParts; ++k) tc::mbar_init(&sm.p_full[i][k], kTileQ);
                 tc::mbar_init(&sm.pv_done[i], 1);
             }
             for (int i = 0; i < kKSlots; ++i) tc::mbar_init(&sm.k_full[i], 1), tc::mbar_init(&sm.k_empty[i], 1);
@@ -220,12 +221,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                 ok = tc::mbar_wait(&sm.v_full[slot], (j / kVSlots) & 1);
                 for (int g = 0; g < 2 && ok; ++g) {
                     if (j >= nt[g]) continue;
-                    ok = tc::mbar_wait(&sm.p_full[g], j & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
                     const uint32_t d = tmem + 256 + g * 128, a = tmem + g * 128, b = v_lo + slot * (2 * kChunk >> 4);
 #pragma unroll
-                    for (int s = 0; s < kTileK / 16; ++s) tma::mma_ts(d, a + 8 * s, b + 128 * s, idO, s != 0 ? 1 : j != 0);
+                    for (int k = 0; k < kParts; ++k) {
+                        ok = ok && tc::mbar_wait(&sm.p_full[g][k], j & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int s = k * (kTileK / 16 / kParts); s < (k + 1) * (kTileK / 16 / kParts); ++s)
+                            tma::mma_ts(d, a + 8 * s, b + 128 * s, idO, s != 0 ? 1 : j != 0);
+                    }
+                    if (!ok) break;
                     tc::commit(&sm.pv_done[g]);
                     if (g == 1 || j >= nt[1]) tc::commit(&sm.v_empty[slot]);
                     if (j + 1 < nt[g]) scores(g, j + 1, g == 1 || j + 1 >= nt[1]);
@@ -260,9 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                     for (int k = 0; k < 32; ++k)
                         if (32 * i + k >= valid) s[i][k] = 0xff800000u;
             }
-            float mx = max32(s[0], -INFINITY);
+            float m4[4];  // independent chains
 #pragma unroll
-            for (int i = 1; i < 4; ++i) mx = max32(s[i], mx);
+            for (int i = 0; i < 4; ++i) m4[i] = max32(s[i], -INFINITY);
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const bool grown = (mx - m_ref) * c > kRescale;  // also from -inf to a finite maximum
             if (j == 0) {
                 m_ref = mx;
@@ -288,13 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
             }
             const float mb = m_ref == -INFINITY ? 0.f : -m_ref * c;
             const uint64_t nmb2 = pk2(mb, mb);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t pr[16];
-                exp32(s[i], pr, c2, nmb2, l);
-                tc::tmem_st16(s_addr + 16 * i, pr);
-            }
-            tc::tmem_wait_st();
             const int there = nk - j * kTileK;
             if (there < kTileK && (g == 0 || j >= nt[0])) {
                 // value rows behind the sequence; the first query tile that uses them clears them
@@ -306,8 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                 }
                 fence_proxy_async();
             }
-            tc::fence_before_sync();
-            tma::arrive(&sm.p_full[g]);
+            // the value product starts on the first 32 keys while the others are at their exponentials
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                uint32_t pr[16];
+                exp32(s[i], pr, c2, nmb2, l);
+                tc::tmem_st16(s_addr + 16 * i, pr);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tma::arrive(&sm.p_full[g][i]);
+            }
         }
         if (ok && nt[g] > 0) {
             ok = tma::wait_warp(&sm.pv_done[g], (nt[g] - 1) & 1);
