@@ -124,6 +124,37 @@ __device__ __forceinline__ void commit_free(uint64_t *mbar) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+// ask for a box of a tiled map to be in L2
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n" ::"l"(map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+// 32 bytes in one store: a whole sector of a row that one thread writes (32-byte aligned)
+__device__ __forceinline__ void st_global32(void *dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// Ask for a block of this grid that has not started, to do its work in this one: the 16-byte answer
+// lands at `answer` and counts on mbar. canceled_block reads it: the block's x index, or -1 when
+// none was left (then nothing may be asked for again).
+__device__ __forceinline__ void try_cancel(void *answer, uint64_t *mbar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(
+                     tc::smem_addr(answer)),
+                 "r"(tc::smem_addr(mbar))
+                 : "memory");
+}
+__device__ __forceinline__ int64_t canceled_block(const void *answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n.reg .b128 a;\n.reg .pred p;\nld.shared.b128 a, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n}\n"
+        : "=r"(got), "=r"(x)
+        : "r"(tc::smem_addr(answer))
+        : "memory");
+    return got ? (int64_t)x : -1;
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
