@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         // last stretch's score products are through: its last tile was taken
         auto load_q = [&](const Walk &s) {
             const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + ((int64_t)s.n * geo.R + row_first + max(0, min(r, rows_here - 1))) * kLatent + 64 * set);
+                p.q + ((int64_t)s.n * geo.R + min(row_first + r, geo.R - 1)) * kLatent + 64 * set);
             uint32_t x[2 * QT + 1][16];
 #pragma unroll
             for (int i = 0; i < 2 * QT; ++i)

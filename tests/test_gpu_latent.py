@@ -286,6 +286,9 @@ DECODE = [
     ([100, 40], 16, 125, 16),
     ([40 + 5 * i for i in range(160)], 64, 72, 1),
     ([6000, 1], 64, 96, 1),
+    # eight row tiles of 56 rows, the last one without any (385 and 388 query rows)
+    ([70, 200, 0], 16, 77, 5),
+    ([64], 64, 97, 4),
 ]
 
 
