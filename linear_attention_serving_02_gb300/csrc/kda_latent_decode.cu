@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         ry[b] = ry_next[b];
                         const bool out = (uint32_t)pg_next[b] >= (uint32_t)p.num_pages;
                         bad |= out;
-                        pg[b] = out ? p.num_pages : pg_next[b];  // loads as zeros
+                        pg[b] = out ? INT32_MAX : pg_next[b];  // past every page: loads as zeros
                     }
                     if (bad) {
                         sm.bad[seg & 3] = 1;
@@ -897,7 +897,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
     const uint64_t rows = (uint64_t)num_seqs * a.geo.R;
     const uint64_t dl[3] = {kLatent, rows, 0}, sl[3] = {1, kLatent, 0}, dp[3] = {kPos, rows, 0}, sp[3] = {1, kPos, 0};
-    // a cache without pages keeps one page of extent: no id is in range, nothing loads from it
+    // a cache without pages keeps one page of extent: no id is in range, every load is past it
     const uint64_t dc[3] = {kRow, (uint64_t)page_size, (uint64_t)(num_pages > 0 ? num_pages : 1)};
     const uint64_t sc[3] = {1, kRow, (uint64_t)page_stride};
     if (!tma::encode(&a.q_lat, q_lat, 2, dl, sl, a.geo.rows, 1) || !tma::encode(&a.q_pe, q_pe, 2, dp, sp, a.geo.rows, 1) ||

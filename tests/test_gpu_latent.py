@@ -374,6 +374,20 @@ def test_decode_bad_tables(what, code):
     _check_decode(o, lse, q_lat, q_pe, cache, table, lens, m, SCALE, seqs=(0, 2))
 
 
+def test_decode_of_a_cache_without_pages():
+    g, lens = _gen(35), [40, 0]
+    q_lat, q_pe, cache, table = _decode_inputs(g, lens, 16, 2, 1, tails=False)
+    o, lse, st = torch.zeros(2, 2, LATENT, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 2, device="cuda"), _status()
+    ws = torch.empty(kda.kda_mla_decode_workspace_size(2, 2, 1), dtype=torch.uint8, device="cuda")
+    rc = kda.library().kda_mla_decode(q_lat.data_ptr(), q_pe.data_ptr(), cache.data_ptr(), 16 * ROW, 0, 16,
+                                      table.data_ptr(), table.shape[1], _ints(lens).data_ptr(), 2, 2, 1, SCALE, o.data_ptr(),
+                                      lse.data_ptr(), ws.data_ptr(), ws.numel(), st.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and st.item() == -9
+    assert o[0].isnan().all() and lse[0].isnan().all()
+    assert (o[1] == 0).all() and (lse[1] == -float("inf")).all()
+
+
 def test_decode_gives_the_same_bits_again_and_on_another_stream():
     """A used workspace, another stream and a second call change nothing."""
     g, lens = _gen(35), [5000, 64, 700]
