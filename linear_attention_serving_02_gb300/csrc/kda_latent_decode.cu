@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             float m_ref = -INFINITY, l = 0.f;
             if (w.work) {
                 for (int j = w.j0; j < w.j1; ++j) {
-                    ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1);
+                    ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1) && ok;
                     // a failed wait still meets the barriers below, so that no warp is left in them
                     if (ok) tc::fence_after_sync();
                     uint32_t s[kHalf];
@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
         tiles = tiles_of(p, __ldg(p.lens + n));
         b = runs.of(first) + 1;
         count = runs.of(first + tiles - 1) - b + 2;
+        pdl_wait();  // in every block: a join that ended early would let the next kernel start before the main one's end
         if (count == 1) return;
-        pdl_wait();
     } else {
         b = blockIdx.x + 1;
         pdl_wait();
