@@ -173,8 +173,10 @@ PyObject *mla_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         shape(q_out, "q_out", {T, H, KDA_MLA_POS});
         qp = bf(q);
         qo = bf_out(q_out);
-        qs[0] = q.stride(0), qs[1] = q.stride(1);
-        qos[0] = q_out.stride(0), qos[1] = q_out.stride(1);
+        // the stride of a dimension of one says nothing
+        auto stride = [](const at::Tensor &t, int d) { return t.size(d) > 1 ? t.stride(d) : (int64_t)KDA_MLA_POS; };
+        qs[0] = stride(q, 0), qs[1] = stride(q, 1);
+        qos[0] = stride(q_out, 0), qos[1] = stride(q_out, 1);
     } else {
         TORCH_CHECK_VALUE(a[11] == Py_None, "q_out needs q_pe");
     }

@@ -107,6 +107,24 @@ def test_append_rotates_queries_in_place_and_leaves_padding_alone():
     assert torch.equal(q[..., :NOPE], was[..., :NOPE]) and torch.equal(q[5:], was[5:])
 
 
+def test_append_of_one_token_and_head_with_odd_strides():
+    """A dimension of one has no step: whatever its stride says, the call is taken."""
+    g, rope = _gen(7), _rope(8)
+    down, q = _rand(g, 1, ROW), _rand(g, 1, 1, POS)
+    table, lens = _ints([[0]]), _ints([5])
+    outs = []
+    for odd in (False, True):
+        cache, q_out = torch.zeros(1, 16, ROW, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(q)
+        views = [x.as_strided((1, 1, POS), (1001, 77, 1)) if odd else x for x in (q, q_out)]
+        c, k_pe = down[:, :LATENT], down[:, LATENT:]
+        if odd:
+            c, k_pe = c.as_strided((1, LATENT), (7, 1)), k_pe.as_strided((1, POS), (3, 1), LATENT)
+        kda.kda_mla_append(c, k_pe, cache, table, lens, _ints([0, 1]), rope=rope, q_pe=views[0], q_out=views[1])
+        outs.append((cache, q_out))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert (outs[0][1] != 0).any()
+
+
 @pytest.mark.parametrize("what,code", [("page", -9), ("short", -4), ("long", -4), ("rope", -4)])
 def test_append_bad_tables(what, code):
     g = _gen(5)
