@@ -46,7 +46,8 @@ namespace kda {
 namespace {
 
 constexpr int kKvTile = 64;                     // cached rows of a tile
-constexpr int kRowTile = 64;                  // query rows of a CTA at most
+constexpr int kRowTile = 64;                  // query rows of a CTA of a pair at most
+constexpr int kWideRows = 96;                 // query rows of a CTA of its own at most
 constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
@@ -69,6 +70,8 @@ struct DecodeGeom {
 struct DecodeArgs {
     CUtensorMap q_lat, q_pe, cache;
     const __nv_bfloat16 *q;  // q_lat again
+    const __nv_bfloat16 *rows;  // the cache again, for the prefetch of a coming tile into L2
+    int64_t page_stride;
     const int32_t *table, *lens;
     int32_t max_pages, num_pages, page_size, rb;  // rb: rows of a TMA box (64, 32 or 16)
     int32_t N, H, m, G;
@@ -85,7 +88,7 @@ struct DecodeArgs {
 struct DecodeSmem {
     uint64_t q_full, q_empty, q_ready, s_full[2], s_free[2], p_full, pv_done, drained;
     uint64_t pair_full[kMaxPair], pair_empty[kMaxPair], pos_full[kMaxPos], pos_empty[kMaxPos];
-    float factor[kRowTile], half[2][kRowTile];  // by query row: scale of O^T, the halves' maxima or sums
+    float factor[128], half[2][128];  // by query row: scale of O^T, the halves' maxima or sums
     uint32_t tmem;
     int32_t failed, bad[4];
     int32_t first_seq, first_tile;
@@ -155,11 +158,11 @@ __device__ __forceinline__ bool softmax_any(bool flag) {
 
 // QT > 0: clusters of two row tiles, a CTA's rank is rt & 1; the first QT pairs of Q's latent
 // chunks are kept in TMEM (a constant, so that the issue loop has no choice to make)
-template <int QT>
+template <int MS, int QT, bool two>
 __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    constexpr bool two = QT > 0;
+    constexpr int kS = MS == 128 ? 1 : 2;      // S tiles in TMEM
     const DecodeGeom &geo = p.geo;
     const uint32_t q_chunk = (uint32_t)geo.rows * 128;
     constexpr int q_chunks = 9 - 2 * QT;      // of Q in shared memory, the positions last
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
     const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
-    const uint32_t t_q = t_s + 2 * kKvTile;    // then Q's first latents, two to a column
+    const uint32_t t_q = t_s + kS * kKvTile;    // then Q's first latents, two to a column
     const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
@@ -303,6 +306,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         set_status(p.status, KDA_ERR_PAGES);
                     }
                     look(j + 1);
+                    if (MS == 128 && j + 1 < w.j1) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
+                            if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
+                                tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow,
+                                                 (uint32_t)p.rb * kRow * 2);
+                        }
+                    }
                     const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
                     const uint32_t box = (uint32_t)p.rb * 128, bytes = boxes * box;
                     ok = tc::mbar_wait(&sm.pos_empty[rs], rph ^ 1);
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         // ---- score products: one thread; the value products have a thread of their own, so that
         // neither polls for the other (a narrow batch's MMA takes less than a look at a barrier) ----
         if (tma::elect()) {
-            const uint32_t id = tma::idesc(kRowTile, kKvTile, 0, 0);
+            const uint32_t id = tma::idesc(MS, kKvTile, 0, 0);
             const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), pos_lo = tma::lo_k(tc::smem_addr(s_pos));
             const uint32_t pair_lo = tma::lo_k(tc::smem_addr(s_pair)), q_step = q_chunk >> 4;
             Walk w;
@@ -360,12 +372,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             w.skip_idle(p);
             int k = 0, seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
             while (!w.done() && ok) {
-                ok = tc::mbar_wait(&sm.q_full, seg & 1) && (!two || tc::mbar_wait(&sm.q_ready, seg & 1));
+                ok = tc::mbar_wait(&sm.q_full, seg & 1) && (QT == 0 || tc::mbar_wait(&sm.q_ready, seg & 1));
                 for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
-                    ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1) && tc::mbar_wait(&sm.pos_full[rs], rph);
+                    ok = tc::mbar_wait(&sm.s_free[k % kS], ((k / kS) & 1) ^ 1) && tc::mbar_wait(&sm.pos_full[rs], rph);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t d = t_s + (k & 1) * kKvTile;
+                    const uint32_t d = t_s + (k % kS) * kKvTile;
                     {
                         const uint32_t a = q_lo + (q_chunks - 1) * q_step, b = pos_lo + rs * (kChunkB >> 4);
 #pragma unroll
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         if (++ps == geo.np) ps = 0, pph ^= 1;
                     }
                     if (!ok) break;
-                    tc::commit(&sm.s_full[k & 1]);
+                    tc::commit(&sm.s_full[k % kS]);
                     if (j + 1 == w.j1) tc::commit(&sm.q_empty);
                 }
                 ++seg;
@@ -444,10 +456,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         // ---- softmax: one thread a query row and half a tile; then the output ----
         const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        // M = 64 puts rows 16 q .. 16 q + 15 into lanes 32 q .. 32 q + 15 of TMEM
-        const bool low = lane < 16;
-        const int r = quarter * 16 + (lane & 15);
-        const bool owner = low && r < rows_here, warp_rows = quarter * 16 < rows_here;
+        // M = 64 puts rows 16 q .. 16 q + 15 into lanes 32 q .. 32 q + 15 of TMEM, M = 128 row r into lane r
+        constexpr int kWarpRows = MS / 4;
+        const bool low = lane < kWarpRows;
+        const int r = quarter * kWarpRows + (lane & (kWarpRows - 1));
+        const bool owner = low && r < rows_here, warp_rows = quarter * kWarpRows < rows_here;
         const int unseen = p.m - 1 - (row_first + (owner ? r : 0)) / p.H;  // last cached rows that the row does not see
         const float c = p.scale * 1.4426950408889634f;
         const uint64_t c2 = pk2(c, c);
@@ -474,7 +487,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         };
         Walk w;
         w.start(p, sm);
-        if constexpr (two) {
+        if constexpr (QT > 0) {
             Walk first = w;
             first.skip_idle(p);
             if (!first.done()) load_q(first);
@@ -483,14 +496,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             float m_ref = -INFINITY, l = 0.f;
             if (w.work) {
                 for (int j = w.j0; j < w.j1; ++j) {
-                    ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1) && ok;
+                    ok = tma::wait_warp(&sm.s_full[k % kS], (k / kS) & 1) && ok;
                     // a failed wait still meets the barriers below, so that no warp is left in them
                     if (ok) tc::fence_after_sync();
                     uint32_t s[kHalf];
                     const bool first = j == w.j0;
                     float mb = m_ref == -INFINITY ? 0.f : -m_ref * c, top = -INFINITY;
                     if (warp_rows && ok) {
-                        tc::tmem_ld32_nowait(t_s + lanes + (k & 1) * kKvTile + set * kHalf, s);
+                        tc::tmem_ld32_nowait(t_s + lanes + (k % kS) * kKvTile + set * kHalf, s);
                         tc::tmem_wait_ld();
                         tc::fence_before_sync();
                         // cached rows of this thread's half that the row sees
@@ -504,7 +517,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         for (int e = 0; e < kHalf; e += 2)
                             top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
                     }
-                    tma::arrive(&sm.s_free[k & 1]);
+                    tma::arrive(&sm.s_free[k % kS]);
                     // one barrier a tile: does a row need a new reference (also from -inf to a finite one), did a wait fail
                     const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
                     if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
@@ -576,7 +589,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     tma::arrive(&sm.p_full);
                     ++k;
                 }
-                if constexpr (two) {
+                if constexpr (QT > 0) {
                     // the next stretch's queries before this one's output, so that its scores start meanwhile
                     Walk after = w;
                     after.next(p);
@@ -797,11 +810,11 @@ constexpr size_t kSmemMax = 232448;
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
-    q.RT = (q.R + kRowTile - 1) / kRowTile;
+    q.RT = q.R <= kWideRows ? 1 : (q.R + kRowTile - 1) / kRowTile;
     if (q.RT > 1) q.RT += q.RT & 1;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    q.qt = q.RT > 1 ? (q.npad <= 48 ? 3 : 2) : 0;  // 4 npad + 128 + 64 qt TMEM columns: 512 at both
+    q.qt = q.RT > 1 ? (q.npad <= 48 ? 3 : 2) : (q.R > kRowTile ? 1 : 0);  // 4 npad + 128 + 64 qt TMEM columns: 512 at both
     const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)(9 - 2 * q.qt) * q.rows * 128 + (size_t)q.npad * 128;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
@@ -813,6 +826,7 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     return q;
 }
 static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * kRowTile * 128 >= 8 * kPairB + 2 * kChunkB, "two tiles' rings");
+static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 8 * kWideRows * 128 >= 7 * kPairB + 2 * kChunkB, "96 rows leave 7 pairs");
 
 // groups of CTAs that share the list: one CTA an SM
 int32_t groups_of(int32_t RT, int32_t sms) { return sms / RT > 0 ? sms / RT : 1; }
@@ -822,7 +836,7 @@ struct DecodeWs {
 };
 DecodeWs decode_ws(const DecodeGeom &q) {
     DecodeWs w;
-    const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = 2 * G * q.RT * q.npad;
+    const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = q.RT > 1 && 2 * G * q.RT * q.npad < 2 * (size_t)kMaxGroups * kWideRows ? 2 * (size_t)kMaxGroups * kWideRows : 2 * G * q.RT * q.npad;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     w.head = 0;
     w.ml = up(8 + 16 * kMaxGroups);
@@ -904,6 +918,8 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
         !tma::encode(&a.cache, cache, 3, dc, sc, a.rb, 1))
         return KDA_ERR_CUDA;
     a.q = reinterpret_cast<const __nv_bfloat16 *>(q_lat);
+    a.rows = reinterpret_cast<const __nv_bfloat16 *>(cache);
+    a.page_stride = page_stride;
     a.table = page_table;
     a.lens = cache_lens;
     a.max_pages = max_pages;
@@ -924,13 +940,13 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     static std::atomic<int32_t> pairs_at_a_time[64];
     int32_t pairs = pairs_at_a_time[device].load(std::memory_order_acquire);
     if (pairs == 0) {
-        if (cudaFuncSetAttribute(kda_mla_decode_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
-            cudaFuncSetAttribute(kda_mla_decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
-            cudaFuncSetAttribute(kda_mla_decode_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
-            return KDA_ERR_CUDA;
+        for (auto kernel : {kda_mla_decode_kernel<64, 0, false>, kda_mla_decode_kernel<128, 1, false>,
+                            kda_mla_decode_kernel<64, 2, true>, kda_mla_decode_kernel<64, 3, true>})
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
+                return KDA_ERR_CUDA;
         Launch two(2, 2, kSmemMax, nullptr);
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<3>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
+        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<64, 3, true>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
         pairs = n;
         pairs_at_a_time[device].store(pairs, std::memory_order_release);
     }
@@ -942,10 +958,11 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a.geo.RT > 1) {
         const Launch pairs_of((unsigned)(a.G * a.geo.RT), 2, a.geo.smem, st);
-        if (cudaLaunchKernelEx(&pairs_of.cfg, a.geo.qt == 3 ? kda_mla_decode_kernel<3> : kda_mla_decode_kernel<2>, a) != cudaSuccess)
+        if (cudaLaunchKernelEx(&pairs_of.cfg, a.geo.qt == 3 ? kda_mla_decode_kernel<64, 3, true> : kda_mla_decode_kernel<64, 2, true>, a) != cudaSuccess)
             return KDA_ERR_CUDA;
     } else {
-        kda_mla_decode_kernel<0><<<(unsigned)a.G, kDecThreads, a.geo.smem, st>>>(a);
+        auto kernel = a.geo.qt == 1 ? kda_mla_decode_kernel<128, 1, false> : kda_mla_decode_kernel<64, 0, false>;
+        kernel<<<(unsigned)a.G, kDecThreads, a.geo.smem, st>>>(a);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (a.G > 1) {
