@@ -228,12 +228,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             }
             tc::mbar_init(&sm.q_full, 1);
             tc::mbar_init(&sm.q_empty, 1);
-            tc::mbar_init(&sm.q_ready, kSoftmaxThreads);
+            tc::mbar_init(&sm.q_ready, kSoftmaxThreads / 32);
             tc::mbar_init(&sm.s_full[0], 1);
             tc::mbar_init(&sm.s_full[1], 1);
-            tc::mbar_init(&sm.s_free[0], kSoftmaxThreads);
-            tc::mbar_init(&sm.s_free[1], kSoftmaxThreads);
-            tc::mbar_init(&sm.p_full, kSoftmaxThreads);
+            tc::mbar_init(&sm.s_free[0], kSoftmaxThreads / 32);
+            tc::mbar_init(&sm.s_free[1], kSoftmaxThreads / 32);
+            tc::mbar_init(&sm.p_full, kSoftmaxThreads / 32);
             tc::mbar_init(&sm.pv_done, 1);
             tc::mbar_init(&sm.drained, 2);
             // a slot is free when every CTA of the cluster is through with it
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             for (int i = 0; i < 2 * QT; ++i) tc::tmem_st16(t_q + lanes + 64 * (i >> 1) + 32 * set + 16 * (i & 1), x[i]);
             tc::tmem_wait_st();
             tc::fence_before_sync();
-            tma::arrive(&sm.q_ready);
+            tma::arrive_warp(&sm.q_ready);
         };
         Walk w;
         w.start(p, sm);
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         for (int e = 0; e < kHalf; e += 2)
                             top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
                     }
-                    tma::arrive(&sm.s_free[k % kS]);
+                    tma::arrive_warp(&sm.s_free[k % kS]);
                     // one barrier a tile: does a row need a new reference (also from -inf to a finite one), did a wait fail
                     const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
                     if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     if (ps >= geo.np) ps -= geo.np;
                     fence_proxy_async();
                     tc::fence_before_sync();
-                    tma::arrive(&sm.p_full);
+                    tma::arrive_warp(&sm.p_full);
                     ++k;
                 }
                 if constexpr (QT > 0) {

@@ -190,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
         sm.k_issued = sm.v_issued = sm.q_issued[0] = sm.q_issued[1] = 0;
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sm.item_full[i], 1);
-            tc::mbar_init(&sm.item_empty[i], 2 + 2 * kTileQ);
+            tc::mbar_init(&sm.item_empty[i], 2 + 2 * kTileQ / 32);
             tc::mbar_init(&sm.q_full[i], 1);
             tc::mbar_init(&sm.q_empty[i], 1);
             tc::mbar_init(&sm.s_full[i], 1);
-            for (int k = 0; k < kParts; ++k) tc::mbar_init(&sm.p_full[i][k], kTileQ);
+            for (int k = 0; k < kParts; ++k) tc::mbar_init(&sm.p_full[i][k], kTileQ / 32);
             tc::mbar_init(&sm.pv_done[i], 1);
         }
         tc::mbar_init(&sm.ask, 1);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
             if (!ok) break;
             const Item w = sm.item[n & 1];
             if (w.h < 0) break;
-            tma::arrive(&sm.item_empty[n & 1]);
+            tma::arrive_warp(&sm.item_empty[n & 1]);
             const int row = w.row0 + g * kTileQ + r, nt = g ? w.nt1 : w.nt0;
             const int keys = row < w.nq ? keys_of(w, p.causal, row) : w.nk;
             float m_ref = -INFINITY;  // reference maximum of O and l, in raw scores
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                         tc::tmem_st16(s_addr + 32 * i + 16 * k, pr);
                         tc::tmem_wait_st();
                         tc::fence_before_sync();
-                        tma::arrive(&sm.p_full[g][2 * i + k]);
+                        tma::arrive_warp(&sm.p_full[g][2 * i + k]);
                     }
                 }
             }

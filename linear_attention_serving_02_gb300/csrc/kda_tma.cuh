@@ -99,6 +99,11 @@ __device__ __forceinline__ bool test(uint64_t *mbar, uint32_t parity) {
 __device__ __forceinline__ void arrive(uint64_t *mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_addr(mbar)) : "memory");
 }
+// arrive once for a whole warp, behind what all its lanes did
+__device__ __forceinline__ void arrive_warp(uint64_t *mbar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(mbar);
+}
 // a load that lands at the same place in both CTAs of a cluster of two, and counts on the
 // same barrier in each
 __device__ __forceinline__ void load_3d_both(void *dst, const CUtensorMap *map, uint64_t *mbar, int x, int y, int z) {
