@@ -46,8 +46,7 @@ namespace kda {
 namespace {
 
 constexpr int kKvTile = 64;                     // cached rows of a tile
-constexpr int kRowTile = 64;                  // query rows of a CTA of a pair at most
-constexpr int kWideRows = 96;                 // query rows of a CTA of its own at most
+constexpr int kRowTile = 64, kWideRows = 96;    // query rows of a CTA at most: M = 64, and M = 128 (TMEM holds 96)
 constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
@@ -156,8 +155,9 @@ __device__ __forceinline__ bool softmax_any(bool flag) {
     return r != 0;
 }
 
-// QT > 0: clusters of two row tiles, a CTA's rank is rt & 1; the first QT pairs of Q's latent
-// chunks are kept in TMEM (a constant, so that the issue loop has no choice to make)
+// MS: rows of the score product's M. QT: the first QT pairs of Q's latent chunks are kept in TMEM.
+// two: clusters of two row tiles, a CTA's rank is rt & 1. (Constants, so that the issue loop has
+// no choice to make.)
 template <int MS, int QT, bool two>
 __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
     extern __shared__ uint8_t smem_raw[];
@@ -805,16 +805,19 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 
 constexpr size_t kSmemMax = 232448;
 
-// Row tiles of equal size, as few as 64 rows each allow and an even number (clusters of two)
-// where there are several; the rings take what Q and P leave.
+// Row tiles of equal size, an even number (clusters of two) where there are several; the rings take
+// what Q and P leave. One tile up to 96 rows and two up to 192, with M = 128 past 64 rows: 64 to 128
+// sequences of up to 8000 rows take 291 us (96 rows), 130 (130), 271 (192) where tiles of up to 64
+// rows take 346, 171, 324. From there on as few tiles as 64 rows each allow: 384 rows 243 us and 1024
+// rows 206 us against 254 and 235 with 96.
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
-    q.RT = q.R <= kWideRows ? 1 : (q.R + kRowTile - 1) / kRowTile;
+    q.RT = q.R <= kWideRows ? 1 : (q.R <= 2 * kWideRows ? 2 : (q.R + kRowTile - 1) / kRowTile);
     if (q.RT > 1) q.RT += q.RT & 1;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    q.qt = q.RT > 1 ? (q.npad <= 48 ? 3 : 2) : (q.R > kRowTile ? 1 : 0);  // 4 npad + 128 + 64 qt TMEM columns: 512 at both
+    q.qt = q.rows > kRowTile ? 1 : (q.RT == 1 ? 0 : (q.npad <= 48 ? 3 : 2));  // 4 npad + 128 + 64 qt TMEM columns: 512 at both
     const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)(9 - 2 * q.qt) * q.rows * 128 + (size_t)q.npad * 128;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
@@ -836,7 +839,9 @@ struct DecodeWs {
 };
 DecodeWs decode_ws(const DecodeGeom &q) {
     DecodeWs w;
-    const size_t G = (size_t)groups_of(q.RT, kMaxGroups), parts = q.RT > 1 && 2 * G * q.RT * q.npad < 2 * (size_t)kMaxGroups * kWideRows ? 2 * (size_t)kMaxGroups * kWideRows : 2 * G * q.RT * q.npad;
+    size_t parts = 2 * (size_t)groups_of(q.RT, kMaxGroups) * q.RT * q.npad;
+    const size_t widest = 2 * (size_t)kMaxGroups * kWideRows;
+    if (q.RT > 1 && parts < widest) parts = widest;  // more rows never need less
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     w.head = 0;
     w.ml = up(8 + 16 * kMaxGroups);
@@ -941,7 +946,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     int32_t pairs = pairs_at_a_time[device].load(std::memory_order_acquire);
     if (pairs == 0) {
         for (auto kernel : {kda_mla_decode_kernel<64, 0, false>, kda_mla_decode_kernel<128, 1, false>,
-                            kda_mla_decode_kernel<64, 2, true>, kda_mla_decode_kernel<64, 3, true>})
+                            kda_mla_decode_kernel<64, 2, true>, kda_mla_decode_kernel<64, 3, true>, kda_mla_decode_kernel<128, 1, true>})
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
                 return KDA_ERR_CUDA;
         Launch two(2, 2, kSmemMax, nullptr);
@@ -957,8 +962,9 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a.geo.RT > 1) {
+        auto kernel = a.geo.qt == 3 ? kda_mla_decode_kernel<64, 3, true> : (a.geo.qt == 2 ? kda_mla_decode_kernel<64, 2, true> : kda_mla_decode_kernel<128, 1, true>);
         const Launch pairs_of((unsigned)(a.G * a.geo.RT), 2, a.geo.smem, st);
-        if (cudaLaunchKernelEx(&pairs_of.cfg, a.geo.qt == 3 ? kda_mla_decode_kernel<64, 3, true> : kda_mla_decode_kernel<64, 2, true>, a) != cudaSuccess)
+        if (cudaLaunchKernelEx(&pairs_of.cfg, kernel, a) != cudaSuccess)
             return KDA_ERR_CUDA;
     } else {
         auto kernel = a.geo.qt == 1 ? kda_mla_decode_kernel<128, 1, false> : kda_mla_decode_kernel<64, 0, false>;

@@ -304,6 +304,11 @@ DECODE = [
     ([100, 40], 16, 125, 16),
     ([40 + 5 * i for i in range(160)], 64, 72, 1),
     ([6000, 1], 64, 96, 1),
+    # one and two row tiles of more than 64 rows
+    ([500, 31, 0], 16, 80, 1),
+    ([200, 1, 65], 48, 12, 8),
+    ([300, 40, 0], 64, 96, 2),
+    ([129, 4000], 32, 65, 2),
     # eight row tiles of 56 rows, the last one without any (385 and 388 query rows)
     ([70, 200, 0], 16, 77, 5),
     ([64], 64, 97, 4),
