@@ -382,8 +382,8 @@ int kda_fused_decode(const uint16_t *x_q, const uint16_t *x_k, const uint16_t *x
  *
  * 'status' is a device int32 or NULL. The caller sets it to 0 once; a call whose device
  * tables turn out bad stores a kda_status there (KDA_ERR_SEQLENS for a length or offset,
- * KDA_ERR_PAGES for a page id, KDA_ERR_CUDA for a bounded wait that gave up), and no call
- * clears it. No bad table makes a kernel read or write outside the tensors it was given.
+ * KDA_ERR_PAGES for a page id, KDA_ERR_CUDA for a bounded wait that gave up: that call's
+ * outputs are not to be used), and no call clears it. No bad table makes a kernel read or write outside the tensors it was given.
  * kda_workspace_status(status, stream) reads it.
  * --------------------------------------------------------------------------------- */
 #define KDA_MLA_LATENT 512 /* values of the latent */
@@ -462,9 +462,11 @@ int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages
  *   lse       device fp32 [total_q, H] or NULL: log sum_j exp(s_j)
  * k_pe_stride is a multiple of 8 and at least 64. Rows of o and lse outside every sequence's range are
  * left as they were. Scores, statistics and sums are fp32; the probabilities are rounded
- * to bf16 for the product with the values. A sequence whose offsets fall or leave the
- * tensors is not computed and sets 'status' to KDA_ERR_SEQLENS; its rows are left as they
- * were.
+ * to bf16 for the product with the values. Hidden scores count for nothing whatever they are,
+ * but a NaN or infinite value row inside a sequence can reach rows that do not see it (its
+ * probability there is 0); rows outside the sequence never do. A sequence whose offsets fall
+ * or leave the tensors is not computed and sets 'status' to KDA_ERR_SEQLENS; its rows are
+ * left as they were. Pointers are 16-byte aligned (tables, lse and status: 4).
  */
 int kda_mla_prefill(const uint16_t *q, const uint16_t *kv, const uint16_t *k_pe, int64_t k_pe_stride,
                     const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int64_t total_q, int64_t total_k,
@@ -492,9 +494,10 @@ size_t kda_mla_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_
  *   lse       device fp32 [N * m, H] or NULL
  *   workspace device scratch, kda_mla_decode_workspace_size() bytes, 256-byte aligned; its
  *             contents need no initialisation and are dead after the call
- * Calls that share a workspace must be ordered on one stream. A sequence with a negative
- * length, one past its page table, or a bad page id gets NaN in o and lse and sets
- * 'status'.
+ * Pointers are 16-byte aligned (tables, lse and status: 4). Calls that share a workspace must be
+ * ordered on one stream. A NaN or infinite row of a sequence can reach window tokens that do
+ * not see it; rows outside the sequence never do. A sequence with a negative length, one past
+ * its page table, or a bad page id gets NaN in o and lse and sets 'status'.
  */
 int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *cache, int64_t page_stride,
                    int32_t num_pages, int32_t page_size, const int32_t *page_table, int32_t max_pages,

@@ -8,31 +8,41 @@
 //
 // Work. The sequences' cached rows are cut into tiles of 64; all tiles of the batch form one
 // list, and each of G groups of CTAs takes an equal run of it, so long and short sequences
-// load every SM alike whatever their lengths. The CTAs of a group take up to 64 query rows
-// each (row tiles) and walk the same tiles; two neighbours form a cluster, each loads half of
-// every tile and TMA multicasts it to both, so a pair reads a tile once from L2. A sequence
-// that a run cuts leaves partial (O, max, sum), joined by a second kernel in list order; the
-// others are finished in place. Only the two CTAs of a cluster wait on each other.
+// load every SM alike whatever their lengths. The CTAs of a group take up to 96 query rows
+// each (row tiles) and walk the same tiles; where there are several row tiles, two neighbours
+// form a cluster, each loads half of every tile and TMA multicasts it to both, so a pair reads
+// a tile once from L2. A sequence that a run cuts leaves partial (O, max, sum), joined by a
+// second kernel in list order; the others are finished in place. Only the two CTAs of a cluster
+// wait on each other.
 //
 // A tile in a CTA. TMA lays the 64 rows down once as 9 chunks of 64 columns (128-byte
-// swizzle). S = Q K^T: M = 64 query rows, N = 64 cached rows, read K-major. Eight softmax warps
-// take S from TMEM, one thread a query row and half of the tile, and write P (bf16) to shared
-// memory. The value product runs transposed, O^T = C^T P^T: M = 128 latents (the same chunks,
-// read MN-major), N = query rows. An MMA of K = 16 takes N / 2 cycles, but at least 25 with
-// M = 64 and 39 with M = 128 (measured; A's 128 rows are 4 KB of shared memory): 48 rows need
-// 36 x 32 + 16 x 44 cycles a tile, 16 rows 36 x 32 + 16 x 39, where the tile's 72 KB take an
-// SM's share of HBM about 3100 (a pair's share 1570). TMEM: O^T takes 4 N columns and two S
-// tiles 128; O itself (rows x 512) would take every column.
+// swizzle). S = Q K^T: M = 64 or 128 query rows, N = 64 cached rows, read K-major. Eight softmax
+// warps take S from TMEM, one thread a query row and half of the tile, and write P (bf16) to
+// shared memory. The value product runs transposed, O^T = C^T P^T: M = 128 latents (the same
+// chunks, read MN-major), N = query rows. TMEM: O^T takes 4 N columns (O itself, rows x 512,
+// would take every column), S 64 a tile, two of them with M = 64; past 64 rows of a sequence the
+// rest holds Q's first latents. An MMA of K = 16 takes N / 2 cycles, but at
+// least 25 with M = 64 and 39 with M = 128, or its operands' bytes in shared memory at 128 a
+// cycle: 96 rows need about 28 x 48 + 8 x 32 + 16 x 56 = 2500 cycles a tile and 16 rows 1780, where
+// the tile's 72 KB take an SM's share of HBM about 3100.
+//
+// Measured: 1M cached rows x 12 heads 193 us with the join (6.2 TB/s), bound by the rows' bytes;
+// 256 sequences of up to 8000 rows x 96 heads 294 us (4.3 TB/s). There a tile takes 4000
+// cycles: the ring is a pair short of two tiles, so a tile's last pair is asked for when the
+// last tile's first value product is through, and load 1050, last scores 700, softmax 1200 and
+// the value product follow one another. Clusters of two with 48 rows each took 346, two CTAs
+// that split the columns and trade partial scores 427.
 //
 // The reference M_r only has to stay within 2^8 of the row's maximum (P is then far inside
 // bf16 and fp32), so a tile costs a comparison a score and one barrier; the halves' maxima are
 // exchanged, and O^T rescaled, on a sequence's first tile and where a score passes its
 // reference by 2^8.
 //
-// Shared memory. Q takes 1152 B a row; the rest is a ring of 16 KB pairs of chunks and a
-// ring of 8 KB positional chunks, two tiles or more. One thread issues the score products
-// chunk by chunk as they land, another the value products as their P is written; each pair
-// of chunks is given back as soon as its 128 latents are done.
+// Shared memory. Q takes 1152 B a row less what TMEM holds; the rest is a ring of 16 KB pairs of
+// chunks and a ring of 8 KB positional chunks, two tiles or more, with M = 128 a little less: there
+// the coming tile is asked into L2. One thread issues the score products chunk by chunk as they
+// land, another the value products as their P is written; each pair of chunks is given back as
+// soon as its 128 latents are done.
 //
 // Rows of a tile behind the sequence's length (the rest of a page, or stale shared memory)
 // may hold anything: their scores are replaced by -inf, the product's 16-row steps past the
@@ -693,7 +703,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
 // the border before group x + 1, where the main kernel left the place, and the first border
 // inside a sequence joins it. W warps share a row's parts,
 // each lane 16 of the 512 latents; the parts are added in list order within a warp and the
-// warps' sums in warp order, so the result does not depend on timing.
+// warps' sums in warp order, so the result does not depend on timing. With W = 1 the way through
+// shared memory is not needed, but the 32 KB keep these blocks off the SMs until the main
+// kernel's are through: without them they wait beside it, and 256 x 96 takes 300 us instead of 294.
 constexpr int kJoinThreads = 512;
 template <int W>
 __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid_constant__ DecodeArgs p) {
@@ -972,10 +984,11 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (a.G > 1) {
-        // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four,
-        // and two or three are one warp's (256 sequences of 96 heads: XXX us against XXX with four)
+        // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four, and
+        // two or three are one warp's. With 1, 4 and 16 warps a row: 1M x 12 236, 200 and 193 us; 8 sequences
+        // of 30000 rows x 12 heads 50, 36 and 34; 32 of 8000 x 16 42, 37 and 41; 256 of 8000 x 96 293, 347, 440
         const int64_t n = num_seqs;
-        const cudaError_t e = n * 32 <= a.G ? launch_join<16>(a, st) : (n * 4 <= a.G ? launch_join<4>(a, st) : launch_join<1>(a, st));
+        const cudaError_t e = n * 16 <= a.G ? launch_join<16>(a, st) : (n * 4 <= a.G ? launch_join<4>(a, st) : launch_join<1>(a, st));
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return KDA_OK;
