@@ -28,10 +28,11 @@
 //
 // Measured: 1M cached rows x 12 heads 193 us with the join (6.2 TB/s), bound by the rows' bytes;
 // 256 sequences of up to 8000 rows x 96 heads 294 us (4.3 TB/s). There a tile takes 4000
-// cycles: the ring is a pair short of two tiles, so a tile's last pair is asked for when the
-// last tile's first value product is through, and load 1050, last scores 700, softmax 1200 and
-// the value product follow one another. Clusters of two with 48 rows each took 346, two CTAs
-// that split the columns and trade partial scores 427.
+// cycles, of which shared memory is busy about 3000: the operands' 2500 and 576 for the rows'
+// arrival. In the rest load, last scores, softmax (1200) and value product of a tile follow one
+// another, as the ring holds a little less than two tiles. Tiles of 48 rows, of which it holds two
+// and a quarter, take the same time (296); clusters of two with 48 query rows each 346; two CTAs that
+// split the columns and trade partial scores 427.
 //
 // The reference M_r only has to stay within 2^8 of the row's maximum (P is then far inside
 // bf16 and fp32), so a tile costs a comparison a score and one barrier; the halves' maxima are
