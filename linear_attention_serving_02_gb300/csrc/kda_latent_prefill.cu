@@ -28,7 +28,9 @@
 // 1.54 PFLOP/s; the ragged case, whose tiles do 19% more than its rows need and whose last items
 // end apart, at 1.13. Measured and not taken: two threads a row (176 and 169 us, more handing
 // over), part of the exponentials as polynomials on the FMA pipe (183 us with an eighth of them,
-// 190 with a quarter), clusters of two that share the keys by multicast (183 and 200 us).
+// 190 with a quarter), clusters of two that share the keys by multicast (183 and 200 us), a reference that follows the
+// maximum only where 32 weights sum to more than 2^24 (167 and 155.5, but 272 us instead of 196 where
+// scores spread by 9). 16384 tokens x 16 heads run at 1.77 PFLOP/s.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its last reference
 // (P stays below 2^8, far inside bf16 and fp32), which few tiles do; l sums the fp32 values.

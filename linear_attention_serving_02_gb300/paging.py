@@ -7,8 +7,9 @@ moved returns the moves as (src, dst) lists for kda.kda_pages_copy, to be made b
 next kernel that writes or reads the pages; the page tables that it hands out are already
 the ones after the moves.
 
-KDA states need no pages: a state slot is one page of a pool whose sequences all have
-length page_size = 1.
+A KDA state is one page of a pool with page_size = 1, in a sequence of length 1. It is written
+in place at every step, so a copy of a sequence does not share it: add() and grow() the child's
+slot, and copy the parent's page there.
 """
 import heapq
 

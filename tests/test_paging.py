@@ -108,3 +108,16 @@ def test_table_and_refusals():
         p.fork("c", "d")
     with pytest.raises(ValueError):
         PagePool(1, 0)
+
+
+def test_state_slots_of_a_copied_sequence():
+    """A KDA state's slot: one page of length 1, never shared by a copy."""
+    pool = PagePool(4, 1)
+    pool.add("a")
+    assert pool.grow("a", 1) == ([], [])
+    pool.add("b")
+    assert pool.grow("b", 1) == ([], [])
+    move = pool.pages("a") + pool.pages("b")  # the pair for kda_pages_copy
+    assert len(set(move)) == 2
+    pool.free("a")
+    assert pool.compact() == ([move[1]], [move[0]]) and pool.pages("b") == [move[0]]
