@@ -702,16 +702,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
 // The join of the sequences that a run's border cuts. With fewer sequences than groups block x
 // belongs to sequence x, whose place in the list it adds up itself; with more it belongs to
 // the border before group x + 1, where the main kernel left the place, and the first border
-// inside a sequence joins it. W warps share a row's parts,
-// each lane 16 of the 512 latents; the parts are added in list order within a warp and the
-// warps' sums in warp order, so the result does not depend on timing. With W = 1 the way through
-// shared memory is not needed, but the 32 KB keep these blocks off the SMs until the main
-// kernel's are through: without them they wait beside it, and 256 x 96 takes 300 us instead of 294.
+// inside a sequence joins it. W warps share a row's parts, each lane 16 / Z of the 512 latents, Z
+// blocks a row (1M x 12: 195 us with one, 192 with four); the parts are added in list order within a
+// warp and the warps' sums in warp order, so the result does not depend on timing. With W = 1 the
+// way through shared memory is not needed, but the 32 KB keep these blocks off the SMs until
+// the main kernel's are through: without them they wait beside it, and 256 x 96 takes 300 us
+// instead of 294.
 constexpr int kJoinThreads = 512;
-template <int W>
+template <int W, int Z>
 __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid_constant__ DecodeArgs p) {
     constexpr int kRows = kJoinThreads / 32 / W;  // rows of a block
-    __shared__ float s_o[kRows][W][kLatent];
+    constexpr int kLat = kLatent / Z, kVec = kLat / 128;  // its latents, and float4 of a lane
+    __shared__ float s_o[kRows][W][kLat];
     __shared__ float s_m[kRows][W], s_l[kRows][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t n, tiles, b;  // the sequence, its tiles, the run after the one that holds its first tile
@@ -756,9 +758,10 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     const int rt = (live ? rr : 0) / p.geo.rows, r = (live ? rr : 0) % p.geo.rows;
     const float c = p.scale * 1.4426950408889634f;
     // parts: run b - 1 (slot 1, it holds the sequence's start), then the following runs (slot 0)
-    float m = -INFINITY, l = 0.f, o[16];
+    const int lat0 = blockIdx.z * kLat;
+    float m = -INFINITY, l = 0.f, o[4 * kVec];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    for (int i = 0; i < 4 * kVec; ++i) o[i] = 0.f;
     auto row_of = [&](int i) {
         const int64_t gq = b - 1 + i;
         return ((2 * gq + (i == 0 ? 1 : 0)) * p.geo.RT + rt) * p.geo.npad + r;
@@ -770,15 +773,15 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
+#pragma unroll (Z > 1 ? 8 : 4)
         for (int i = part; i < count; i += W) {
             const int64_t q = row_of(i);
             const float2 ml = p.part_ml[q];
             const float f = tc::ex2((ml.x - ms) * c);
             l += f * ml.y;
-            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + q * kLatent) + lane;
+            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + q * kLatent + lat0) + lane;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
+            for (int v = 0; v < kVec; ++v) {
                 const float4 x = __ldcs(src + 32 * v);
                 o[4 * v] += f * x.x;
                 o[4 * v + 1] += f * x.y;
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
         }
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int v = 0; v < kVec; ++v)
         *reinterpret_cast<float4 *>(&s_o[rl][part][4 * (32 * v + lane)]) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
     if (lane == 0) s_m[rl][part] = m, s_l[rl][part] = l;
     __syncthreads();
@@ -804,15 +807,15 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     }
     const float inv = L == 0.f ? 0.f : 1.0f / L;
     const int64_t row = (int64_t)n * p.geo.R + rr;
-    if (part == 0 && lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M * p.scale + logf(L);
-    for (int x = 2 * (part * 32 + lane); x < kLatent; x += 2 * 32 * W) {
+    if (part == 0 && lane == 0 && blockIdx.z == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M * p.scale + logf(L);
+    for (int x = 2 * (part * 32 + lane); x < kLat; x += 2 * 32 * W) {
         float a = 0.f, bb = 0.f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             a += f[i] * s_o[rl][i][x];
             bb += f[i] * s_o[rl][i][x + 1];
         }
-        *reinterpret_cast<__nv_bfloat162 *>(p.o + row * kLatent + x) = __floats2bfloat162_rn(a * inv, bb * inv);
+        *reinterpret_cast<__nv_bfloat162 *>(p.o + row * kLatent + lat0 + x) = __floats2bfloat162_rn(a * inv, bb * inv);
     }
 }
 
@@ -881,11 +884,11 @@ struct Launch {
     Launch(const Launch &) = delete;
 };
 
-template <int W>
+template <int W, int Z>
 cudaError_t launch_join(const DecodeArgs &a, cudaStream_t st) {
     const int rows = kJoinThreads / 32 / W;
     const int cuts = a.N < a.G ? a.N : a.G - 1;
-    return launch_after(kda_mla_join_kernel<W>, dim3(cuts, (a.geo.R + rows - 1) / rows), dim3(kJoinThreads), 0, st, a);
+    return launch_after(kda_mla_join_kernel<W, Z>, dim3(cuts, (a.geo.R + rows - 1) / rows, Z), dim3(kJoinThreads), 0, st, a);
 }
 
 }  // namespace
@@ -989,7 +992,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
         // two or three are one warp's. With 1, 4 and 16 warps a row: 1M x 12 236, 200 and 193 us; 8 sequences
         // of 30000 rows x 12 heads 50, 36 and 34; 32 of 8000 x 16 42, 37 and 41; 256 of 8000 x 96 293, 347, 440
         const int64_t n = num_seqs;
-        const cudaError_t e = n * 16 <= a.G ? launch_join<16>(a, st) : (n * 4 <= a.G ? launch_join<4>(a, st) : launch_join<1>(a, st));
+        const cudaError_t e = n * 16 <= a.G ? launch_join<16, 4>(a, st) : (n * 4 <= a.G ? launch_join<4, 2>(a, st) : launch_join<1, 1>(a, st));
         if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return KDA_OK;

@@ -87,15 +87,6 @@ __device__ __forceinline__ bool elect() {
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
     return one != 0;
 }
-// whether the phase of the given parity has completed
-__device__ __forceinline__ bool test(uint64_t *mbar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(done)
-                 : "r"(tc::smem_addr(mbar)), "r"(parity)
-                 : "memory");
-    return done != 0;
-}
 __device__ __forceinline__ void arrive(uint64_t *mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_addr(mbar)) : "memory");
 }
