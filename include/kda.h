@@ -383,8 +383,9 @@ int kda_fused_decode(const uint16_t *x_q, const uint16_t *x_k, const uint16_t *x
  * 'status' is a device int32 or NULL. The caller sets it to 0 once; a call whose device
  * tables turn out bad stores a kda_status there (KDA_ERR_SEQLENS for a length or offset,
  * KDA_ERR_PAGES for a page id, KDA_ERR_CUDA for a bounded wait that gave up: that call's
- * outputs are not to be used), and no call clears it. No bad table makes a kernel read or write outside the tensors it was given.
- * kda_workspace_status(status, stream) reads it.
+ * outputs are not to be used), and no call clears it. No bad table makes a kernel read or
+ * write outside the tensors it was given. kda_workspace_status(status, stream) reads it.
+ * Outputs overlap no input unless a call says so.
  * --------------------------------------------------------------------------------- */
 #define KDA_MLA_LATENT 512 /* values of the latent */
 #define KDA_MLA_POS 64     /* values of the positional key */
