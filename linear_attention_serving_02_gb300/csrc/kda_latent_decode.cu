@@ -833,7 +833,7 @@ DecodeGeom geometry(int32_t H, int32_t m) {
     if (q.RT > 1) q.RT += q.RT & 1;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    q.qt = q.rows > kRowTile ? 1 : (q.RT == 1 ? 0 : (q.npad <= 48 ? 3 : 2));  // 4 npad + 128 + 64 qt TMEM columns: 512 at both
+    q.qt = q.rows > kRowTile ? 1 : (q.RT == 1 ? 0 : 2);  // 4 npad + 64 or 128 + 64 qt TMEM columns: 512 at most
     const size_t fixed = 1024 + sizeof(DecodeSmem) + (size_t)(9 - 2 * q.qt) * q.rows * 128 + (size_t)q.npad * 128;
     const size_t room = kSmemMax - fixed;
     q.nr = 2;
@@ -962,12 +962,12 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     int32_t pairs = pairs_at_a_time[device].load(std::memory_order_acquire);
     if (pairs == 0) {
         for (auto kernel : {kda_mla_decode_kernel<64, 0, false>, kda_mla_decode_kernel<128, 1, false>,
-                            kda_mla_decode_kernel<64, 2, true>, kda_mla_decode_kernel<64, 3, true>, kda_mla_decode_kernel<128, 1, true>})
+                            kda_mla_decode_kernel<64, 2, true>, kda_mla_decode_kernel<128, 1, true>})
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
                 return KDA_ERR_CUDA;
         Launch two(2, 2, kSmemMax, nullptr);
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<64, 3, true>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
+        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<64, 2, true>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
         pairs = n;
         pairs_at_a_time[device].store(pairs, std::memory_order_release);
     }
@@ -978,7 +978,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a.geo.RT > 1) {
-        auto kernel = a.geo.qt == 3 ? kda_mla_decode_kernel<64, 3, true> : (a.geo.qt == 2 ? kda_mla_decode_kernel<64, 2, true> : kda_mla_decode_kernel<128, 1, true>);
+        auto kernel = a.geo.qt == 2 ? kda_mla_decode_kernel<64, 2, true> : kda_mla_decode_kernel<128, 1, true>;
         const Launch pairs_of((unsigned)(a.G * a.geo.RT), 2, a.geo.smem, st);
         if (cudaLaunchKernelEx(&pairs_of.cfg, kernel, a) != cudaSuccess)
             return KDA_ERR_CUDA;
