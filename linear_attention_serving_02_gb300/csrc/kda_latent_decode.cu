@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 constexpr size_t kSmemMax = 232448;
 
 // Row tiles of equal size, an even number (clusters of two) where there are several; the rings take
-// what Q and P leave. One tile up to 96 rows and two up to 192, with M = 128 past 64 rows: 64 to 128
+// what Q and P leave. One tile up to 96 rows and two up to 192, with M = 128 past 64 rows: 64 to 256
 // sequences of up to 8000 rows take 291 us (96 rows), 130 (130), 271 (192) where tiles of up to 64
 // rows take 346, 171, 324. From there on as few tiles as 64 rows each allow: 384 rows 243 us and 1024
 // rows 206 us against 254 and 235 with 96.
