@@ -15,6 +15,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <vector>
+
 #include "kda.h"
 
 namespace {
@@ -286,11 +288,52 @@ PyObject *mla_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// pool, and src and dst as contiguous 1-D CPU int32 tensors
+// Page ids: a list or tuple of whole numbers, or a contiguous 1-D CPU int32 tensor.
+struct Ids {
+    std::vector<int32_t> own;
+    const int32_t *p;
+    int64_t n;
+    bool fits = true;  // false: an id is negative or past 32 bits
+    Ids(PyObject *o, const char *name) {
+        if (PyList_CheckExact(o) || PyTuple_CheckExact(o)) {
+            n = PySequence_Fast_GET_SIZE(o);
+            own.resize((size_t)n);
+            for (int64_t i = 0; i < n; ++i) {
+                PyObject *item = PySequence_Fast_GET_ITEM(o, i);
+                int over = 0;
+                const long long v = PyLong_Check(item) ? PyLong_AsLongLongAndOverflow(item, &over) : index(item, name, &over);
+                fits = fits && !over && v >= 0 && v <= INT32_MAX;
+                own[(size_t)i] = (int32_t)v;
+                TORCH_CHECK_VALUE(PySequence_Fast_GET_SIZE(o) == n, name, " changed its length");  // by an item's __index__
+            }
+            p = own.data();
+        } else {
+            const at::Tensor &t = tensor(o, name);
+            TORCH_CHECK_VALUE(t.device().is_cpu() && t.scalar_type() == kI && t.dim() == 1 && t.is_contiguous(), name,
+                              " must be a contiguous 1-D CPU int32 tensor");
+            p = static_cast<const int32_t *>(t.const_data_ptr());
+            n = t.size(0);
+        }
+    }
+    static long long index(PyObject *item, const char *name, int *over) {
+        Py_INCREF(item);  // its own code runs: the list's reference may go
+        PyObject *i = PyNumber_Index(item);
+        Py_DECREF(item);
+        if (!i) {
+            PyErr_Clear();
+            TORCH_CHECK_TYPE(false, name, " must hold whole numbers");
+        }
+        const long long v = PyLong_AsLongLongAndOverflow(i, over);
+        Py_DECREF(i);
+        return v;
+    }
+};
+
 PyObject *pages_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (!args(n, 3, "pages_copy")) return nullptr;
-    const at::Tensor &pool = tensor(a[0], "pool"), &src = tensor(a[1], "src"), &dst = tensor(a[2], "dst");
+    const at::Tensor &pool = tensor(a[0], "pool");
+    const Ids src(a[1], "src"), dst(a[2], "dst");
     TORCH_CHECK_VALUE(pool.is_cuda() && pool.dim() >= 3, "pool must be a CUDA tensor [layers, pages, ...]");
     const int dev = pool.device().index();
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
@@ -299,17 +342,13 @@ PyObject *pages_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(pool.size(d) <= 1 || pool.stride(d) == page, "pool must be dense within a page");
         page *= pool.size(d);
     }
-    for (const at::Tensor *t : {&src, &dst})
-        TORCH_CHECK_VALUE(t->device().is_cpu() && t->scalar_type() == kI && t->dim() == 1 && t->is_contiguous(),
-                          "src and dst must be contiguous 1-D CPU int32 tensors");
-    TORCH_CHECK_VALUE(src.size(0) == dst.size(0), "src and dst must have the same length");
+    TORCH_CHECK_VALUE(src.n == dst.n, "src and dst must have the same length");
+    if (!src.fits || !dst.fits) return fail("kda_pages_copy", KDA_ERR_PAGES);
     const int64_t es = pool.element_size(), layers = pool.size(0), pages = pool.size(1), bytes = page * es;
     const int64_t page_stride = pages > 1 ? pool.stride(1) * es : bytes;
     const int64_t layer_stride = layers > 1 ? pool.stride(0) * es : page_stride * pages;
     const int rc = kda_pages_copy(pool.data_ptr(), page_stride, bytes, extent(pages, "the number of pages"), layer_stride,
-                                  extent(layers, "the number of layers"), static_cast<const int32_t *>(src.const_data_ptr()),
-                                  static_cast<const int32_t *>(dst.const_data_ptr()), extent(src.size(0), "the list"),
-                                  stream_of(dev));
+                                  extent(layers, "the number of layers"), src.p, dst.p, extent(src.n, "the list"), stream_of(dev));
     if (rc != KDA_OK) return fail("kda_pages_copy", rc);
     return Py_NewRef(a[0]);
     END_HANDLE_TH_ERRORS

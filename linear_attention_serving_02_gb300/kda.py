@@ -446,17 +446,17 @@ def kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens
 
 
 def _page_ids(ids, name):
-    """A host list of page ids as a contiguous CPU int32 tensor."""
+    """Page ids as the binding takes them: a list, a tuple or a contiguous CPU int32 tensor."""
+    if isinstance(ids, (list, tuple)):
+        return ids if type(ids) in (list, tuple) else list(ids)
     if not isinstance(ids, torch.Tensor):
-        ids = torch.tensor(list(ids), dtype=torch.int64)
+        return list(ids)
     if ids.dim() != 1 or ids.is_cuda:
         raise ValueError("%s must be a list or a 1-D CPU tensor of page ids" % name)
     if ids.dtype is not torch.int32:
         if ids.dtype not in (torch.int64, torch.int16, torch.int8, torch.uint8):
             raise TypeError("%s must hold whole numbers, got %s" % (name, ids.dtype))
-        if ids.numel() and (int(ids.min()) < 0 or int(ids.max()) > 0x7FFFFFFF):
-            raise KdaError("kda_pages_copy", -9)
-        ids = ids.to(torch.int32)
+        return ids.tolist()
     return ids if ids.is_contiguous() else ids.contiguous()
 
 

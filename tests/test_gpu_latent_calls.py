@@ -177,3 +177,31 @@ def test_the_status_word_is_never_cleared():
     kda.kda_mla_decode(q_lat, q_pe, cache, table, _ints(lens), SCALE, status=st)
     kda.kda_mla_gather(cache, table, _ints(_cu(lens)), 40, status=st)
     assert st.item() == -4
+
+
+def test_page_ids_of_every_kind():
+    g = _gen(58)
+    pool = _rand(g, 2, 9, 16)
+    want = pool.clone()
+    want[:, 5], want[:, 7] = pool[:, 1], pool[:, 2]
+
+    class Id:
+        def __init__(self, v):
+            self.v = v
+
+        def __index__(self):
+            return self.v
+
+    for src, dst in (([1, 2], [5, 7]), ((1, 2), (5, 7)), (range(1, 3), iter([5, 7])), ([Id(1), Id(2)], [5, True + 6]),
+                     (torch.tensor([1, 2]), torch.tensor([5, 7], dtype=torch.uint8)),
+                     (torch.tensor([1, 0, 2, 0], dtype=torch.int32)[::2], torch.tensor([5, 7], dtype=torch.int32))):
+        got = pool.clone()
+        kda.kda_pages_copy(got, src, dst)
+        assert torch.equal(got, want)
+    for bad, error in (([1.0, 2], TypeError), (["1", 2], TypeError), ([1], ValueError), ([1, 2 ** 40], kda.KdaError),
+                       ([1, -2 ** 70], kda.KdaError), ([1, 9], kda.KdaError), (torch.tensor([1.0, 2.0]), TypeError),
+                       (torch.tensor([[1, 2]]), ValueError), (torch.tensor([1, -1]), kda.KdaError)):
+        got = pool.clone()
+        with pytest.raises(error):
+            kda.kda_pages_copy(got, bad, [5, 7])
+        assert torch.equal(got, pool)
