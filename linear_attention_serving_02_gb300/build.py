@@ -74,7 +74,7 @@ def build(force=False, verbose=False, extra_flags=()):
     _link([nvcc()] + ARCH + ["-shared"] + objs[:-1] + ["-lcudart"], LIB)
     torch_lib = os.path.join(_torch_dir(), "lib")
     _link(["g++", "-shared", objs[-1], "-L" + OUT_DIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + torch_lib,
-           "-Wl,-rpath," + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], BINDING)
+           "-Wl,-rpath," + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], BINDING)
     return LIB
 
 

@@ -9,7 +9,7 @@
 
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -128,6 +128,11 @@ Cache paged(PyObject *cache, PyObject *page_table, int64_t seqs, int dev) {
 int64_t row_stride(const at::Tensor &t, int64_t least) { return t.size(0) > 1 ? t.stride(0) : least; }
 void *stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
+// a new dense tensor, without the way through the dispatcher that at::empty takes
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev) {
+    return at::Tensor(at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
+}
+
 bool args(Py_ssize_t n, Py_ssize_t want, const char *fn) {
     if (n == want) return true;
     PyErr_Format(PyExc_TypeError, "%s takes %zd arguments, got %zd", fn, want, n);
@@ -171,7 +176,7 @@ PyObject *mla_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &q = need(a[10], "q_pe", kBf, 3, 1, dev);
         H = extent(q.size(1), "the number of heads");
         shape(q, "q_pe", {T, H, KDA_MLA_POS});
-        q_out = a[11] == Py_None ? at::empty({T, H, KDA_MLA_POS}, q.options()) : need(a[11], "q_out", kBf, 3, 1, dev);
+        q_out = a[11] == Py_None ? fresh({T, H, KDA_MLA_POS}, kBf, dev) : need(a[11], "q_out", kBf, 3, 1, dev);
         shape(q_out, "q_out", {T, H, KDA_MLA_POS});
         qp = bf(q);
         qo = bf_out(q_out);
@@ -203,7 +208,7 @@ PyObject *mla_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Cache cache = paged(a[0], a[1], N, dev);
     const int32_t *cu = ints(a[2], "cu_seqlens", N + 1, dev);
     TORCH_CHECK_VALUE(T >= 0, "total_rows must not be negative");
-    at::Tensor out = a[4] == Py_None ? at::empty({T, KDA_MLA_ROW}, first.options()) : need(a[4], "out", kBf, 2, 2, dev);
+    at::Tensor out = a[4] == Py_None ? fresh({T, KDA_MLA_ROW}, kBf, dev) : need(a[4], "out", kBf, 2, 2, dev);
     shape(out, "out", {T, KDA_MLA_ROW});
     const int rc = kda_mla_gather(bf(first), cache.stride, cache.pages, cache.size, cu, cache.table, cache.max_pages,
                                   bf_out(out), T, extent(N, "the number of sequences"), status_word(a[5], dev), stream_of(dev));
@@ -238,8 +243,8 @@ PyObject *mla_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t N = cu_q.size(0) - 1;
     TORCH_CHECK_VALUE(N >= 0, "cu_seqlens_q must hold num_seqs + 1 offsets");
     const int32_t *cu_k = ints(a[4], "cu_seqlens_k", N + 1, dev);
-    at::Tensor o = a[7] == Py_None ? at::empty({Tq, H, KDA_MLA_NOPE}, q.options()) : need(a[7], "o", kBf, 3, 3, dev);
-    at::Tensor lse = a[8] == Py_None ? at::empty({Tq, H}, q.options().dtype(kF)) : need(a[8], "lse", kF, 2, 2, dev);
+    at::Tensor o = a[7] == Py_None ? fresh({Tq, H, KDA_MLA_NOPE}, kBf, dev) : need(a[7], "o", kBf, 3, 3, dev);
+    at::Tensor lse = a[8] == Py_None ? fresh({Tq, H}, kF, dev) : need(a[8], "lse", kF, 2, 2, dev);
     shape(o, "o", {Tq, H, KDA_MLA_NOPE});
     shape(lse, "lse", {Tq, H});
     const int rc = kda_mla_prefill(bf(q), bf(kv), bf(k_pe), row_stride(k_pe, KDA_MLA_POS),
@@ -266,14 +271,14 @@ PyObject *mla_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor &q_pe = need(a[1], "q_pe", kBf, 3, 3, dev);
     shape(q_pe, "q_pe", {rows, H, KDA_MLA_POS});
     const Cache cache = paged(a[2], a[3], N, dev);
-    at::Tensor o = a[7] == Py_None ? at::empty({rows, H, KDA_MLA_LATENT}, q_lat.options()) : need(a[7], "o", kBf, 3, 3, dev);
-    at::Tensor lse = a[8] == Py_None ? at::empty({rows, H}, q_lat.options().dtype(kF)) : need(a[8], "lse", kF, 2, 2, dev);
+    at::Tensor o = a[7] == Py_None ? fresh({rows, H, KDA_MLA_LATENT}, kBf, dev) : need(a[7], "o", kBf, 3, 3, dev);
+    at::Tensor lse = a[8] == Py_None ? fresh({rows, H}, kF, dev) : need(a[8], "lse", kF, 2, 2, dev);
     shape(o, "o", {rows, H, KDA_MLA_LATENT});
     shape(lse, "lse", {rows, H});
     const int32_t n32 = extent(N, "the number of sequences"), h32 = extent(H, "the number of heads");
     at::Tensor ws;
     if (a[9] == Py_None) {
-        ws = at::empty({(int64_t)kda_mla_decode_workspace_size(n32, h32, m)}, q_lat.options().dtype(at::kByte));
+        ws = fresh({(int64_t)kda_mla_decode_workspace_size(n32, h32, m)}, at::kByte, dev);
     } else {
         ws = tensor(a[9], "workspace");
         TORCH_CHECK_VALUE(ws.is_cuda() && ws.device().index() == dev && ws.is_contiguous(),
