@@ -12,10 +12,11 @@
 // Warps are blocks of their own: with 256 threads a block waits for its slowest token and frees
 // its registers late (65536 tokens x 12 heads 64.7 us, 59.3 us with 32).
 //
-// Measured: append of 65536 tokens x 12 heads 59.3 us (6.2 TB/s), of 256 tokens x 96 heads 3.6 us
-// (a launch and two dependent loads); gather of 108000 rows 40.9 us (6.1 TB/s), of
-// 330 rows 3.6 us (eight rows a warp: 43.7 and 6.0 us).
+// Measured: append of 65536 tokens x 12 heads 59 us (6.3 TB/s), of 256 tokens x 96 heads 3.4 us
+// (a launch and three dependent loads); gather of 108000 rows 40.6 us (6.2 TB/s), of
+// 330 rows 3.3 us (eight rows a warp: 43.7 and 6.0 us).
 
+#include "kda_common.cuh"
 #include "kda_latent_common.cuh"
 
 namespace kda {
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int part = blockIdx.y;
+    pdl_wait();
     if (t >= p.T) return;
 
     // the loads that need no position first
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kRowThreads)
                           __nv_bfloat16 *out, int32_t *status) {
     const int lane = threadIdx.x & 31;
     const int64_t t0 = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kGatherRows;
+    pdl_wait();
     if (t0 >= T) return;
     // the four rows' places: nullptr = none (outside every sequence), NaN rows flagged
     const __nv_bfloat16 *src[kGatherRows];
@@ -298,8 +301,10 @@ int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, in
     a.status = status;
     const int64_t blocks = (total_tokens + kRowThreads / 32 - 1) / (kRowThreads / 32);
     const int parts = a.H > kHeadsPerItem ? (a.H + kHeadsPerItem - 1) / kHeadsPerItem : 1;
-    kda_mla_append_kernel<<<dim3((unsigned)blocks, (unsigned)parts), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return launch_after(kda_mla_append_kernel, dim3((unsigned)blocks, (unsigned)parts), dim3(kRowThreads), 0,
+                        static_cast<cudaStream_t>(stream), a) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
 }
 
 int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
@@ -318,9 +323,10 @@ int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages
     const unsigned blocks = (unsigned)((total_rows + per_block - 1) / per_block);
     const PagedRows<const __nv_bfloat16> pr{reinterpret_cast<const __nv_bfloat16 *>(cache), page_stride, num_pages,
                                             page_size, page_table, max_pages};
-    kda_mla_gather_kernel<<<blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        pr, cu_seqlens, num_seqs, total_rows, reinterpret_cast<__nv_bfloat16 *>(out), status);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return launch_after(kda_mla_gather_kernel, dim3(blocks), dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), pr,
+                        cu_seqlens, num_seqs, total_rows, reinterpret_cast<__nv_bfloat16 *>(out), status) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

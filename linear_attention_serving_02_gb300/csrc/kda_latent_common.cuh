@@ -19,6 +19,13 @@ constexpr int kRow = KDA_MLA_ROW;
 constexpr int kNope = KDA_MLA_NOPE;
 constexpr int kQk = KDA_MLA_QK;
 
+// The kernels are launched so that they may come onto the GPU while the previous kernel on the
+// stream ends, and wait for its end (pdl_wait) before they touch memory: a step of short calls saves
+// about a microsecond a call (256-token append 6.1 -> 4.2 us, 330-row gather 6.1 -> 4.2, two windows of
+// 8 tokens x 12 heads 16.4 -> 14.1, called one after another). None but the decode's main kernel lets
+// its successor start earlier than at its end: in the append that took longer (65536 x 12 70 us, 59
+// without).
+
 // A cache of rows in pages with its page table (pointers of the caller).
 template <typename T>
 struct PagedRows {

@@ -26,8 +26,8 @@
 // cycle: 96 rows need about 28 x 48 + 8 x 32 + 16 x 56 = 2500 cycles a tile and 16 rows 1780, where
 // the tile's 72 KB take an SM's share of HBM about 3100.
 //
-// Measured: 1M cached rows x 12 heads 193 us with the join (6.2 TB/s), bound by the rows' bytes;
-// 256 sequences of up to 8000 rows x 96 heads 294 us (4.3 TB/s). There a tile takes 4000
+// Measured: 1M cached rows x 12 heads 191 us with the join (6.3 TB/s), bound by the rows' bytes;
+// 256 sequences of up to 8000 rows x 96 heads 293 us (4.3 TB/s). There a tile takes 4000
 // cycles, of which shared memory is busy about 3000: the operands' 2500 and 576 for the rows'
 // arrival. In the rest load, last scores, softmax (1200) and value product of a tile follow one
 // another, as the ring holds a little less than two tiles. Tiles of 48 rows, of which it holds two
@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % geo.RT, g = blockIdx.x / geo.RT;
 
+    pdl_wait();
     // ---- this group's run of the list ----
     if (warp == 10 && lane == 0) {
         tma::prefetch_map(&p.q_lat);
@@ -869,7 +870,7 @@ DecodeWs decode_ws(const DecodeGeom &q) {
 // launch configuration of the main kernel: `cluster` neighbouring CTAs form a cluster
 struct Launch {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     Launch(unsigned ctas, unsigned cluster, size_t smem, cudaStream_t st) {
         cfg.gridDim = dim3(ctas);
         cfg.blockDim = dim3(kDecThreads);
@@ -879,7 +880,9 @@ struct Launch {
         attr[0].val.clusterDim.x = cluster;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
     }
     Launch(const Launch &) = delete;
 };
@@ -984,8 +987,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
             return KDA_ERR_CUDA;
     } else {
         auto kernel = a.geo.qt == 1 ? kda_mla_decode_kernel<128, 1, false> : kda_mla_decode_kernel<64, 0, false>;
-        kernel<<<(unsigned)a.G, kDecThreads, a.geo.smem, st>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        if (launch_after(kernel, dim3((unsigned)a.G), dim3(kDecThreads), a.geo.smem, st, a) != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (a.G > 1) {
         // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four, and

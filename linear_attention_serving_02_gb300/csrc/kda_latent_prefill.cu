@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    pdl_wait();
     const uint32_t tmem = sm.tmem;
     bool ok = true;
 
@@ -609,6 +610,8 @@ extern "C" int kda_mla_prefill(const uint16_t *q, const uint16_t *kv, const uint
             return KDA_ERR_CUDA;
         configured[device].store(true, std::memory_order_release);
     }
-    kda_mla_prefill_kernel<<<(unsigned)(slots * num_heads), kThreads, kPrefillSmem, static_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return launch_after(kda_mla_prefill_kernel, dim3((unsigned)(slots * num_heads)), dim3(kThreads), kPrefillSmem,
+                        static_cast<cudaStream_t>(stream), a) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
 }

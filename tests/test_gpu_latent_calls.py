@@ -205,3 +205,54 @@ def test_page_ids_of_every_kind():
         with pytest.raises(error):
             kda.kda_pages_copy(got, bad, [5, 7])
         assert torch.equal(got, pool)
+
+
+@pytest.mark.parametrize("H,m", [(2, 1), (12, 1), (96, 1), (96, 4)])
+def test_calls_that_follow_one_another_wait_for_one_another(H, m):
+    """Each call reads what the one before it wrote, and writes what it read: without any pause between
+    them, and as one graph, they give the bits of calls with a synchronisation behind each."""
+    g, size, lens = _gen(59 + H), 32, [700, 90, 33]
+    N = len(lens)
+    q0, p0, cache0, table = _decode_inputs(g, lens, size, H, m, tails=False)
+    down0, rope, lens_d, cu = _rand(g, N * m, ROW), _rope(800), _ints(lens), _ints(_cu(lens))
+    cu_q = _ints(_cu([m] * N))
+    ws = torch.empty(kda.kda_mla_decode_workspace_size(N, H, m), dtype=torch.uint8, device="cuda")
+    q, cache, down = q0.clone(), cache0.clone(), down0.clone()
+    q_pe, o, lse = p0.clone(), torch.empty_like(q0), torch.empty(N * m, H, device="cuda")
+    rows = torch.empty(sum(lens), ROW, dtype=torch.bfloat16, device="cuda")
+    qx, kv = torch.empty(N * m, 2, QK, dtype=torch.bfloat16, device="cuda"), _rand(g, sum(lens), 2, 2 * NOPE)
+    ox, lx = torch.empty(N * m, 2, NOPE, dtype=torch.bfloat16, device="cuda"), torch.empty(N * m, 2, device="cuda")
+
+    def chain(pause):
+        q.copy_(q0), cache.copy_(cache0), down.copy_(down0), q_pe.copy_(p0)
+        for _ in range(4):
+            steps = [
+                lambda: kda.kda_mla_append(down[:, :LATENT], down[:, LATENT:], cache, table, lens_d, cu_q, rope=rope,
+                                           q_pe=q_pe, q_out=q_pe),
+                lambda: kda.kda_mla_decode(q, q_pe, cache, table, lens_d, SCALE, m, o, lse, ws),
+                lambda: kda.kda_pages_copy(o.view(1, N, -1), [0], [2]),
+                lambda: kda.kda_mla_decode(o, q_pe, cache, table, lens_d, SCALE, m, q, lse, ws),
+                lambda: kda.kda_mla_gather(cache, table, cu, sum(lens), rows),
+                lambda: qx.view(N * m, -1).copy_(q.view(N * m, -1)[:, :2 * QK]),
+                lambda: kda.kda_mla_prefill(qx, kv, rows[:, LATENT:], cu_q, cu, SCALE, o=ox, lse=lx),
+                lambda: down[:, :2 * NOPE].copy_(ox.view(N * m, -1)),
+            ]
+            for step in steps:
+                step()
+                if pause:
+                    torch.cuda.synchronize()
+
+    def state():
+        return [x.clone() for x in (q, cache, down, q_pe, o, lse, rows, ox, lx)]
+
+    chain(True)
+    want = state()
+    assert all(torch.isfinite(x).all() for x in want)
+    for _ in range(5):
+        chain(False)
+        assert all(torch.equal(a, b) for a, b in zip(state(), want))
+    graph, _ = _capture(lambda: chain(False))
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(state(), want))
