@@ -9,11 +9,10 @@
 // Work. The sequences' cached rows are cut into tiles of 64; all tiles of the batch form one
 // list, and each of G groups of CTAs takes an equal run of it, so long and short sequences
 // load every SM alike whatever their lengths. The CTAs of a group take up to 96 query rows
-// each (row tiles) and walk the same tiles; where there are several row tiles, two neighbours
-// form a cluster, each loads half of every tile and TMA multicasts it to both, so a pair reads
-// a tile once from L2. A sequence that a run cuts leaves partial (O, max, sum), joined by a
-// second kernel in list order; the others are finished in place. Only the two CTAs of a cluster
-// wait on each other.
+// each (row tiles) and walk the same tiles, each loading them for itself: the first read brings a
+// tile from HBM, its neighbours' come from L2. A sequence that a run cuts leaves partial (O, max,
+// sum), joined by a second kernel in list order; the others are finished in place. No CTA waits
+// for another.
 //
 // A tile in a CTA. TMA lays the 64 rows down once as 9 chunks of 64 columns (128-byte
 // swizzle). S = Q K^T: M = 64 or 128 query rows, N = 64 cached rows, read K-major. Eight softmax
@@ -31,7 +30,7 @@
 // cycles, of which shared memory is busy about 3000: the operands' 2500 and 576 for the rows'
 // arrival. In the rest load, last scores, softmax (1200) and value product of a tile follow one
 // another, as the ring holds a little less than two tiles. Tiles of 48 rows, of which it holds two
-// and a quarter, take the same time (296); clusters of two with 48 query rows each 346; two CTAs that
+// and a quarter, take the same time (296); two CTAs with 48 query rows each 346; two CTAs that
 // split the columns and trade partial scores 427.
 //
 // The reference M_r only has to stay within 2^8 of the row's maximum (P is then far inside
@@ -167,9 +166,8 @@ __device__ __forceinline__ bool softmax_any(bool flag) {
 }
 
 // MS: rows of the score product's M. QT: the first QT pairs of Q's latent chunks are kept in TMEM.
-// two: clusters of two row tiles, a CTA's rank is rt & 1. (Constants, so that the issue loop has
-// no choice to make.)
-template <int MS, int QT, bool two>
+// (Constants, so that the issue loop has no choice to make.)
+template <int MS, int QT>
 __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __grid_constant__ DecodeArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -248,9 +246,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             tc::mbar_init(&sm.p_full, kSoftmaxThreads / 32);
             tc::mbar_init(&sm.pv_done, 1);
             tc::mbar_init(&sm.drained, 2);
-            // a slot is free when every CTA of the cluster is through with it
-            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.pair_full[i], 1), tc::mbar_init(&sm.pair_empty[i], 1 + two);
-            for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1 + two);
+            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.pair_full[i], 1), tc::mbar_init(&sm.pair_empty[i], 1);
+            for (int i = 0; i < geo.nr; ++i) tc::mbar_init(&sm.pos_full[i], 1), tc::mbar_init(&sm.pos_empty[i], 1);
             tc::mbar_init_fence();
         }
     } else if (warp == 8) {
@@ -259,7 +256,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (two) tma::cluster_sync();  // the neighbour's barriers are set up before anything reaches them
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
     const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
@@ -332,17 +328,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     ok = tc::mbar_wait(&sm.pos_empty[rs], rph ^ 1);
                     if (!ok) break;
                     tc::mbar_arrive_expect_tx(&sm.pos_full[rs], bytes);
-                    if (!two || ((j ^ rt) & 1)) {  // of a pair, one CTA loads a tile's positions for both
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (b < boxes) {
-                                uint8_t *dst = s_pos + rs * kChunkB + b * box;
-                                if (two)
-                                    tma::load_3d_both(dst, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
-                                else
-                                    tma::load_3d(dst, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
-                            }
-                    }
+                    for (int b = 0; b < 4; ++b)
+                        if (b < boxes)
+                            tma::load_3d(s_pos + rs * kChunkB + b * box, &p.cache, &sm.pos_full[rs], kLatent, ry[b], pg[b]);
                     ++sm.pos_issued;
                     if (++rs == geo.nr) rs = 0, rph ^= 1;
                     for (int i = 0; i < kPairs; ++i) {
@@ -353,13 +342,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         for (int b = 0; b < 4; ++b)
                             if (b < boxes) {
                                 uint8_t *dst = s_pair + ps * kPairB + b * box;
-                                if (two) {  // each CTA of a pair loads one chunk for both
-                                    const int c = rt & 1;
-                                    tma::load_3d_both(dst + c * kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64 * c, ry[b], pg[b]);
-                                } else {
-                                    tma::load_3d(dst, &p.cache, &sm.pair_full[ps], 128 * i, ry[b], pg[b]);
-                                    tma::load_3d(dst + kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64, ry[b], pg[b]);
-                                }
+                                tma::load_3d(dst, &p.cache, &sm.pair_full[ps], 128 * i, ry[b], pg[b]);
+                                tma::load_3d(dst + kChunkB, &p.cache, &sm.pair_full[ps], 128 * i + 64, ry[b], pg[b]);
                             }
                         ++sm.pair_issued;
                         if (++ps == geo.np) ps = 0, pph ^= 1;
@@ -394,7 +378,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         const uint32_t a = q_lo + (q_chunks - 1) * q_step, b = pos_lo + rs * (kChunkB >> 4);
 #pragma unroll
                         for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id, s != 0);
-                        tma::commit_free<two>(&sm.pos_empty[rs]);
+                        tc::commit(&sm.pos_empty[rs]);
                         if (++rs == geo.nr) rs = 0, rph ^= 1;
                     }
 #pragma unroll
@@ -452,7 +436,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         } else {
                             for (int s = 0; s < steps; ++s) tma::mma_ss(d, a + 128 * s, p_lo + 2 * s, id, s != 0 ? 1 : more);
                         }
-                        tma::commit_free<two>(&sm.pair_empty[ps]);
+                        tc::commit(&sm.pair_empty[ps]);
                         d += geo.npad;
                         if (++ps == geo.np) ps = 0;
                     }
@@ -687,16 +671,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         }
         __syncwarp();
     }
-    if (two) {
-        // the neighbour may still load into this CTA's shared memory or free its slots there
-        if (sm.failed && tid == 0) {
-            const uint64_t t0 = tc::globaltimer();
-            while (tc::globaltimer() - t0 < 50000) {  // what it has in flight after a failed wait, 50 us
-            }
-        }
-        __syncthreads();
-        tma::cluster_sync();
-    }
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
@@ -822,16 +796,16 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 
 constexpr size_t kSmemMax = 232448;
 
-// Row tiles of equal size, an even number (clusters of two) where there are several; the rings take
-// what Q and P leave. One tile up to 96 rows and two up to 192, with M = 128 past 64 rows: 64 to 256
-// sequences of up to 8000 rows take 291 us (96 rows), 130 (130), 271 (192) where tiles of up to 64
-// rows take 346, 171, 324. From there on as few tiles as 64 rows each allow: 384 rows 243 us and 1024
-// rows 206 us against 254 and 235 with 96.
+// Row tiles of equal size; the rings take what Q and P leave. One tile up to 96 rows and two up to
+// 192, with M = 128 past 64 rows. From there up to 320 rows tiles of up to 64 rows, with M = 64 and four
+// of Q's chunks in TMEM, then of up to 96 again: 64 sequences of up to 8000 rows take 190 us (256 rows),
+// 230 (320), 270 (384), 411 (576), 537 (768) and 715 (1024) with 64, and 211, 240, 267, 382, 496 and 689
+// with 96.
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
-    q.RT = q.R <= kWideRows ? 1 : (q.R <= 2 * kWideRows ? 2 : (q.R + kRowTile - 1) / kRowTile);
-    if (q.RT > 1) q.RT += q.RT & 1;
+    q.RT = (q.R + kWideRows - 1) / kWideRows;
+    if (q.R > 2 * kWideRows && q.R <= 5 * kRowTile) q.RT = (q.R + kRowTile - 1) / kRowTile;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
     q.qt = q.rows > kRowTile ? 1 : (q.RT == 1 ? 0 : 2);  // 4 npad + 64 or 128 + 64 qt TMEM columns: 512 at most
@@ -866,26 +840,6 @@ DecodeWs decode_ws(const DecodeGeom &q) {
     w.total = w.o + parts * kLatent * sizeof(float);
     return w;
 }
-
-// launch configuration of the main kernel: `cluster` neighbouring CTAs form a cluster
-struct Launch {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    Launch(unsigned ctas, unsigned cluster, size_t smem, cudaStream_t st) {
-        cfg.gridDim = dim3(ctas);
-        cfg.blockDim = dim3(kDecThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.numAttrs = 2;
-    }
-    Launch(const Launch &) = delete;
-};
 
 template <int W, int Z>
 cudaError_t launch_join(const DecodeArgs &a, cudaStream_t st) {
@@ -960,35 +914,21 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
     a.part_o = reinterpret_cast<float *>(ws + w.o);
     a.status = status;
-    // set up once a device: the kernel's shared memory, and how many clusters of two run at a time
-    static std::atomic<int32_t> pairs_at_a_time[64];
-    int32_t pairs = pairs_at_a_time[device].load(std::memory_order_acquire);
-    if (pairs == 0) {
-        for (auto kernel : {kda_mla_decode_kernel<64, 0, false>, kda_mla_decode_kernel<128, 1, false>,
-                            kda_mla_decode_kernel<64, 2, true>, kda_mla_decode_kernel<128, 1, true>})
+    static std::atomic<bool> configured[64];  // the kernels' shared memory, set once a device
+    if (!configured[device].load(std::memory_order_acquire)) {
+        for (auto kernel : {kda_mla_decode_kernel<64, 0>, kda_mla_decode_kernel<64, 2>, kda_mla_decode_kernel<128, 1>})
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess)
                 return KDA_ERR_CUDA;
-        Launch two(2, 2, kSmemMax, nullptr);
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kda_mla_decode_kernel<64, 2, true>, &two.cfg) != cudaSuccess || n <= 0) return KDA_ERR_DEVICE;
-        pairs = n;
-        pairs_at_a_time[device].store(pairs, std::memory_order_release);
+        configured[device].store(true, std::memory_order_release);
     }
-    if (a.geo.RT > 1) sms = sms < 2 * pairs ? sms : 2 * pairs;
     // no more groups than the longest page tables could give tiles to
     const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
     a.G = groups_of(a.geo.RT, sms < kMaxGroups ? sms : kMaxGroups);
     if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (a.geo.RT > 1) {
-        auto kernel = a.geo.qt == 2 ? kda_mla_decode_kernel<64, 2, true> : kda_mla_decode_kernel<128, 1, true>;
-        const Launch pairs_of((unsigned)(a.G * a.geo.RT), 2, a.geo.smem, st);
-        if (cudaLaunchKernelEx(&pairs_of.cfg, kernel, a) != cudaSuccess)
-            return KDA_ERR_CUDA;
-    } else {
-        auto kernel = a.geo.qt == 1 ? kda_mla_decode_kernel<128, 1, false> : kda_mla_decode_kernel<64, 0, false>;
-        if (launch_after(kernel, dim3((unsigned)a.G), dim3(kDecThreads), a.geo.smem, st, a) != cudaSuccess) return KDA_ERR_CUDA;
-    }
+    auto kernel = a.geo.qt == 2 ? kda_mla_decode_kernel<64, 2> : (a.geo.qt == 1 ? kda_mla_decode_kernel<128, 1> : kda_mla_decode_kernel<64, 0>);
+    if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(kDecThreads), a.geo.smem, st, a) != cudaSuccess)
+        return KDA_ERR_CUDA;
     if (a.G > 1) {
         // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four, and
         // two or three are one warp's. With 1, 4 and 16 warps a row: 1M x 12 236, 200 and 193 us; 8 sequences

@@ -27,7 +27,7 @@ constexpr int kChunkCols = 64;  // bf16 columns of a chunk: one 128-byte swizzle
 // MN-major operand, the distance of its 64-column chunks. Adding to the low half moves the
 // operand: +2 a 16-column step (K-major), +128 a 16-row step (MN-major), bytes / 16 a chunk.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-// (the address field has 14 bits; in a cluster a shared address has the CTA's rank above them)
+// (the address field has 14 bits)
 __device__ __forceinline__ uint32_t lo_k(uint32_t chunk_saddr) { return ((chunk_saddr >> 4) & 0x3FFF) | (1u << 16); }
 __device__ __forceinline__ uint32_t lo_mn(uint32_t chunk_saddr, uint32_t chunk_bytes) {
     return ((chunk_saddr >> 4) & 0x3FFF) | ((chunk_bytes >> 4) << 16);
@@ -94,31 +94,6 @@ __device__ __forceinline__ void arrive(uint64_t *mbar) {
 __device__ __forceinline__ void arrive_warp(uint64_t *mbar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) arrive(mbar);
-}
-// a load that lands at the same place in both CTAs of a cluster of two, and counts on the
-// same barrier in each
-__device__ __forceinline__ void load_3d_both(void *dst, const CUtensorMap *map, uint64_t *mbar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-        "[%1, {%3, %4, %5}], [%2], %6;\n" ::"r"(tc::smem_addr(dst)),
-        "l"(map), "r"(tc::smem_addr(mbar)), "r"(x), "r"(y), "r"(z), "h"((uint16_t)3)
-        : "memory");
-}
-// arrive once on the mbarrier when every MMA issued so far by this thread has completed; with
-// `both` on the same barrier of each CTA of a cluster of two
-template <bool both>
-__device__ __forceinline__ void commit_free(uint64_t *mbar) {
-    if constexpr (both)
-        asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
-                tc::smem_addr(mbar)),
-            "h"((uint16_t)3));
-    else
-        tc::commit(mbar);
-}
-// all threads of the cluster
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // ask for bytes (16-byte aligned, a multiple of 16) to be in L2
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
