@@ -102,8 +102,8 @@ __device__ __forceinline__ PosPiece rotate(const PosPiece &v, const float (&c)[8
     return PosPiece{pack8(x), pack8(y)};
 }
 __device__ __forceinline__ void load8(float (&x)[8], const float *p) {
-    *reinterpret_cast<float4 *>(&x[0]) = __ldg(reinterpret_cast<const float4 *>(p));
-    *reinterpret_cast<float4 *>(&x[4]) = __ldg(reinterpret_cast<const float4 *>(p + 4));
+    *reinterpret_cast<float4 *>(&x[0]) = *reinterpret_cast<const float4 *>(p);
+    *reinterpret_cast<float4 *>(&x[4]) = *reinterpret_cast<const float4 *>(p + 4);
 }
 
 __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __grid_constant__ AppendArgs p) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads)
         const bool nan = (nan_rows >> r) & 1;
         there[k] = nan || s != nullptr;
         v[k] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-        if (s) v[k] = __ldg(reinterpret_cast<const uint4 *>(s + 8 * c));
+        if (s) v[k] = *reinterpret_cast<const uint4 *>(s + 8 * c);
     }
 #pragma unroll
     for (int k = 0; k < kAcc; ++k)

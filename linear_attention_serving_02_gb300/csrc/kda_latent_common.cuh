@@ -20,11 +20,14 @@ constexpr int kNope = KDA_MLA_NOPE;
 constexpr int kQk = KDA_MLA_QK;
 
 // The kernels are launched so that they may come onto the GPU while the previous kernel on the
-// stream ends, and wait for its end (pdl_wait) before they touch memory: a step of short calls saves
-// about a microsecond a call (256-token append 6.1 -> 4.2 us, 330-row gather 6.1 -> 4.2, two windows of
-// 8 tokens x 12 heads 16.4 -> 14.1, called one after another). None but the decode's main kernel lets
-// its successor start earlier than at its end: in the append that took longer (65536 x 12 70 us, 59
-// without).
+// stream ends, and wait for its end (pdl_wait) before they touch memory (the decode's join says why
+// it may look at the lengths before): a step of short calls saves about a microsecond a call
+// (256-token append 6.1 -> 4.2 us, 330-row gather 6.1 -> 4.2, two windows of 8 tokens x 12 heads
+// 16.4 -> 14.1, called one after another). None but the decode's main kernel lets its successor
+// start earlier than at its end: in the append that took longer (65536 x 12 70 us, 59 without).
+// What they read may thus be written while they are already on the GPU, so they read it with
+// ordinary loads: a load through the read-only path claims that nothing writes the data as long as
+// the kernel lives, and the compiler may move it to before the wait.
 
 // A cache of rows in pages with its page table (pointers of the caller).
 template <typename T>

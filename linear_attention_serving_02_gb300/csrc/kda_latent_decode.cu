@@ -132,7 +132,9 @@ struct Walk {
     int64_t left;
     bool work;  // the sequence has cached rows and a sound length
     __device__ __forceinline__ void open(const DecodeArgs &p) {
-        len = __ldg(p.lens + n);
+        // where it stands and not again: with a load that the compiler may repeat or move, the score loop of
+        // the three-pair variant comes out slower (320 rows 248 us, 230 so)
+        asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(len) : "l"(p.lens + n));
         tiles = tiles_of(p, len);
         j1 = (int32_t)min((int64_t)tiles, j0 + left);
         work = len > 0 && !bad_len(p, len);
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     }
     if (warp == 0) {
         int64_t total = 0;
-        for (int n = lane; n < p.N; n += 32) total += tiles_of(p, __ldg(p.lens + n));
+        for (int n = lane; n < p.N; n += 32) total += tiles_of(p, p.lens[n]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
         const Runs runs(total, p.G);
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         int32_t of = 0;
         for (int n0 = 0; n0 < p.N; n0 += 32) {
             const int n = n0 + lane;
-            const int32_t t = n < p.N ? tiles_of(p, __ldg(p.lens + n)) : 0;
+            const int32_t t = n < p.N ? tiles_of(p, p.lens[n]) : 0;
             int64_t incl = t;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         pg_next[b] = 0;
                         ry_next[b] = at;
                         if (b < sub && j < w.j1 && (int64_t)j * kKvTile + b * p.rb < w.len) {
-                            pg_next[b] = __ldg(entry);
+                            pg_next[b] = *entry;
                             at += p.rb;
                             if (at == p.page_size) at = 0, ++entry;
                         }
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             for (int i = 0; i < 2 * QT; ++i)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const uint4 v = __ldg(src + 16 * (i >> 1) + 4 * (i & 1) + u);
+                    const uint4 v = src[16 * (i >> 1) + 4 * (i & 1) + u];
                     x[i][4 * u] = v.x, x[i][4 * u + 1] = v.y, x[i][4 * u + 2] = v.z, x[i][4 * u + 3] = v.w;
                 }
 #pragma unroll
@@ -695,10 +697,12 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     int64_t first;        // list index of that tile
     int count;            // parts
     if (p.N < p.G) {
+        // The lengths are read before the wait: whatever wrote them had finished before the main kernel
+        // let this one start, which it does behind its own wait. From L2, where that writing is.
         n = blockIdx.x;
         int64_t total = 0, before = 0;
         for (int i = lane; i < p.N; i += 32) {
-            const int32_t t = tiles_of(p, __ldg(p.lens + i));
+            const int32_t t = tiles_of(p, __ldcg(p.lens + i));
             total += t;
             if (i < n) before += t;
         }
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
         }
         const Runs runs(total, p.G);
         first = before;
-        tiles = tiles_of(p, __ldg(p.lens + n));
+        tiles = tiles_of(p, __ldcg(p.lens + n));
         b = runs.of(first) + 1;
         count = runs.of(first + tiles - 1) - b + 2;
         pdl_wait();  // in every block: a join that ended early would let the next kernel start before the main one's end

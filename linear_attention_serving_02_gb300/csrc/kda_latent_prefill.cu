@@ -121,7 +121,7 @@ __device__ __forceinline__ bool find_item(const PrefillArgs &p, int64_t index, P
         int a = 0, b = 0, c = 0, d = 0;
         int64_t tiles = 0;
         if (n < p.N) {
-            a = __ldg(p.cu_q + n), b = __ldg(p.cu_q + n + 1), c = __ldg(p.cu_k + n), d = __ldg(p.cu_k + n + 1);
+            a = p.cu_q[n], b = p.cu_q[n + 1], c = p.cu_k[n], d = p.cu_k[n + 1];
             if (a < 0 || b > p.Tq || b < a || c < 0 || d > p.Tk || d < c)
                 set_status(p.status, KDA_ERR_SEQLENS);  // every CTA that looks finds it: no tiles
             else
