@@ -801,15 +801,17 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
 constexpr size_t kSmemMax = 232448;
 
 // Row tiles of equal size; the rings take what Q and P leave. One tile up to 96 rows and two up to
-// 192, with M = 128 past 64 rows. From there up to 320 rows tiles of up to 64 rows, with M = 64 and four
-// of Q's chunks in TMEM, then of up to 96 again: 64 sequences of up to 8000 rows take 190 us (256 rows),
-// 230 (320), 270 (384), 411 (576), 537 (768) and 715 (1024) with 64, and 211, 240, 267, 382, 496 and 689
-// with 96.
+// 192, with M = 128 past 64 rows. From there on as few as 96 rows each allow, or as 64 do (M = 64, four of
+// Q's chunks in TMEM) where that is less than 13/9 as many: 64 sequences of up to 8000 rows take with tiles
+// of up to 64 and 96 rows 190 and 213 us (256 rows, 4 and 3 tiles), 235 and 213 (288, 5 and 3), 230 and
+// 240 (320, 5 and 4), 270 and 267 (384, 6 and 4), 351 and 384 (512, 8 and 6), 410 and 383 (576, 9 and 6),
+// 436 and 450 (640, 10 and 7), 537 and 496 (768, 12 and 8), 714 and 690 (1024, 16 and 11).
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
     q.RT = (q.R + kWideRows - 1) / kWideRows;
-    if (q.R > 2 * kWideRows && q.R <= 5 * kRowTile) q.RT = (q.R + kRowTile - 1) / kRowTile;
+    const int32_t narrow = (q.R + kRowTile - 1) / kRowTile;
+    if (q.RT > 2 && 9 * (int64_t)narrow < 13 * (int64_t)q.RT) q.RT = narrow;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
     q.qt = q.rows > kRowTile ? 1 : (q.RT == 1 ? 0 : 2);  // 4 npad + 64 or 128 + 64 qt TMEM columns: 512 at most
