@@ -462,7 +462,8 @@ int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages
  *   o         device bf16 [total_q, H, 128] (written)
  *   lse       device fp32 [total_q, H] or NULL: log sum_j exp(s_j)
  * k_pe_stride is a multiple of 8 and at least 64. Rows of o and lse outside every sequence's range are
- * left as they were. Scores, statistics and sums are fp32; the probabilities are rounded
+ * left as they were. Scores, statistics and sums are fp32 (a sum over n_k keys is within about 2^-11 of
+ * itself however long they are); the probabilities are rounded
  * to bf16 for the product with the values. Hidden scores count for nothing whatever they are,
  * but a NaN or infinite value row inside a sequence can reach rows that do not see it (its
  * probability there is 0); rows outside the sequence never do. A sequence whose offsets fall

@@ -33,7 +33,13 @@
 // scores spread by 9). 16384 tokens x 16 heads run at 1.77 PFLOP/s.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its last reference
-// (P stays below 2^8, far inside bf16 and fp32), which few tiles do; l sums the fp32 values.
+// (P stays below 2^8, far inside bf16 and fp32), which few tiles do; l sums the fp32 values, a key
+// tile's for themselves first, so that small weights behind a large one are not lost.
+//
+// The tensor core drops what falls below an accumulator's last bit, always towards zero, so a sum over
+// n keys comes out low by about n / 16 * 0.7 * 2^-23 of itself: 0.5% at a million keys, 17% at 33 million.
+// O therefore sums 512 key tiles at a time (4096 additions, 2^-11 at most); then its row is added to
+// one in local memory, with roundings to nearest. That row is touched behind 65536 keys only.
 //
 // Shared memory: Q 96 KB, K in a ring of four 16 KB chunks (one key tile and the next tile's
 // first chunk), V in a ring of two 32 KB tiles. Rows of a tile that lie behind the sequence
@@ -54,6 +60,7 @@ constexpr int kKSlots = 4, kVSlots = 2;
 constexpr int kThreads = 352;  // 2 x 4 softmax warps, the MMA warp, the TMA warp, the scheduler
 constexpr float kRescale = 8.0f;
 constexpr int kParts = 4;     // P of a key tile is handed over in parts of 32 keys
+constexpr int kFold = 512;    // key tiles that O sums in tensor memory (a power of two)
 constexpr int kAskAhead = 4;  // key tiles before an item's last whose loads ask for the next item
 
 struct PrefillArgs {
@@ -177,6 +184,28 @@ __device__ __forceinline__ void exp32(const uint32_t (&r)[32], uint32_t (&p)[16]
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         p[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
+}
+
+// kept (+)= O of this thread's row, at O's reference m_ref (kept's own stands behind its values); for the
+// output (back) into O instead. A call of its own: in the loop's code it made every tile slower
+// (8192 x 12 170.5 us, 168.5 so).
+__device__ __noinline__ void fold_o(float *kept, uint32_t o_addr, float m_ref, float c, bool first, bool back) {
+    const float f = first || kept[kNope] == m_ref ? 1.0f : tc::ex2((kept[kNope] - m_ref) * c);
+#pragma unroll 1
+    for (int i = 0; i < kNope / 16; ++i) {
+        uint32_t x[16];
+        tma::tmem_ld16_nowait(o_addr + 16 * i, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float y = __uint_as_float(x[k]) + (first ? 0.f : kept[16 * i + k] * f);
+            kept[16 * i + k] = y;
+            x[k] = __float_as_uint(y);
+        }
+        if (back) tc::tmem_st16(o_addr + 16 * i, x);
+    }
+    if (back) tc::tmem_wait_st();
+    kept[kNope] = m_ref;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __grid_constant__ PrefillArgs p) {
@@ -354,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                 early = 0;
                 for (int j = 0; j < tiles && ok; ++j, ++ve) {
                     const int slot = ve % kVSlots;
+                    const uint32_t add = (j & (kFold - 1)) != 0;  // to what O holds
                     ok = tc::mbar_wait(&sm.v_full[slot], (ve / kVSlots) & 1);
                     for (int g = 0; g < 2 && ok; ++g) {
                         const int nt = g ? nt1 : nt0;
@@ -366,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                             tc::fence_after_sync();
 #pragma unroll
                             for (int s = k * (kTileK / 16 / kParts); s < (k + 1) * (kTileK / 16 / kParts); ++s)
-                                tma::mma_ts(d, a + 8 * s, b + 128 * s, idO, s != 0 ? 1 : j != 0);
+                                tma::mma_ts(d, a + 8 * s, b + 128 * s, idO, s != 0 ? 1 : add);
                         }
                         if (!ok) break;
                         ++pe[g];
@@ -409,8 +439,20 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
             const int row = w.row0 + g * kTileQ + r, nt = g ? w.nt1 : w.nt0;
             const int keys = row < w.nq ? keys_of(w, p.causal, row) : w.nk;
             float m_ref = -INFINITY;  // reference maximum of O and l, in raw scores
-            uint64_t l[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
-            for (int j = 0; j < nt; ++j, ++sp) {
+            uint64_t l = pk2(0.f, 0.f);
+            float kept[kNope + 1];  // O of the tiles before the last kFold, and its reference
+            int je = min(nt, kFold);  // the next key tile to stop at
+            for (int j = 0;; ++j, ++sp) {
+                if (j == je) {
+                    if (nt > kFold) {
+                        ok = tma::wait_warp(&sm.pv_done[g], (sp - 1) & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        fold_o(kept, o_addr, m_ref, c, j == kFold, j == nt);
+                    }
+                    if (j == nt) break;
+                    je = min(nt, j + kFold);
+                }
                 ok = tma::wait_warp(&sm.s_full[g], sp & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -439,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                     const float mn = grown ? mx : m_ref;
                     const float f = grown ? tc::ex2((m_ref - mn) * c) : 1.0f;
                     m_ref = mn;
-                    l[0] = mul2(l[0], pk2(f, f));
-                    l[1] = mul2(l[1], pk2(f, f));
+                    l = mul2(l, pk2(f, f));
                     ok = tma::wait_warp(&sm.pv_done[g], (sp - 1) & 1);
                     if (!ok) break;
                     tc::fence_after_sync();
@@ -469,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                     fence_proxy_async();
                 }
                 // the value product starts on the first 32 keys while the others are at their exponentials
+                uint64_t lj[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     tc::tmem_wait_ld();
@@ -476,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t pr[16];
-                        exp32(s[k], pr, c2, nmb2, l);
+                        exp32(s[k], pr, c2, nmb2, lj);
                         if (i == 0) tc::tmem_ld32_nowait(s_addr + 64 + 32 * k, s[k]);
                         tc::tmem_st16(s_addr + 32 * i + 16 * k, pr);
                         tc::tmem_wait_st();
@@ -484,13 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                         tma::arrive_warp(&sm.p_full[g][2 * i + k]);
                     }
                 }
+                l = add2(l, add2(lj[0], lj[1]));
             }
             ve += max(w.nt0, w.nt1);
             if (ok && nt > 0) {
                 ok = tma::wait_warp(&sm.pv_done[g], (sp - 1) & 1);
                 tc::fence_after_sync();
             }
-            const float2 la = upk2(add2(l[0], l[1]));
+            const float2 la = upk2(l);
             const float lt = la.x + la.y;
             const float inv = !ok ? NAN : (lt == 0.f ? 0.f : 1.0f / lt);
             const int64_t at = ((int64_t)(w.q0 + row)) * p.H + w.h;

@@ -1,0 +1,77 @@
+"""Latent attention over millions of keys: sums that stay near the exact ones however long they are.
+
+All keys of a kind are alike, so the answer has a closed form: with n_a keys of weight 2^{s_a} and value v_a,
+o = sum n_a 2^{s_a} v_a / sum n_a 2^{s_a} and lse = ln sum n_a 2^{s_a}. The scale is ln 2 in fp32 and the kernel's
+exponent s scale log2(e) rounds twice, so a weight is off by at most 2 ln 2 |s| 2^-24 < 2^-19 of itself for |s| <= 25.
+The weights are powers of two and the values positive: rounding P changes nothing, and a sum is off by
+  2^-11   at most 4096 additions a part in the tensor core, each low by less than a step 2^-23
+  2^-13   at most 512 parts (2^25 keys of a row) added to nearest, 2^-24 each, and
+          2^-17 of the denominator's additions (a tile's for themselves, then at most 2^18 tiles: where tiles are alike
+          their sums are whole numbers below 2^24 times a power of two, exact)
+and o then is rounded to bf16."""
+import math
+
+import pytest
+import torch
+
+from linear_attention_serving_02_gb300 import kda
+from tests import latent_ref as ref
+from tests.test_gpu_latent import NOPE, POS, QK, _ints
+
+pytestmark = pytest.mark.gpu
+
+LN2 = math.log(2.0)
+TOL_O = ref.U_BF16 + 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -17
+TOL_LSE = 2.0 ** -16
+
+
+def _values(n, kind):
+    """Values of a kind of key: positive, of every last bit of bf16."""
+    return (1 + (torch.arange(n) * (37 + 10 * kind) % 128 + kind) / 128.0 % 1).to(torch.bfloat16)
+
+
+def _want(counts, scores, values):
+    """(o, lse) in 64 bits of counts [.., kinds]."""
+    w = counts.double() * torch.exp2(torch.tensor(scores, dtype=torch.float64))
+    return (w @ values.double()) / w.sum(-1, keepdim=True), w.sum(-1).log()
+
+
+def _close(o, lse, want):
+    o, lse = o.double().cpu(), lse.double().cpu()
+    assert bool(((o - want[0]).abs() <= TOL_O * want[0]).all()), float((o / want[0] - 1).abs().max())
+    assert bool(((lse - want[1]).abs() <= TOL_LSE + 2.0 ** -22 * want[1]).all()), float((lse - want[1]).abs().max())
+
+
+# runs of keys: (kind, length). Scores of the kinds in powers of two.
+MILLION = 1 << 20
+PREFILL = {
+    "alike": ([0.0], [(0, 4 * MILLION + 77)]),
+    "one key of weight 1 before many of 2^-25": ([0.0, -25.0], [(0, 1), (1, 4 * MILLION)]),
+    "a new maximum behind many keys, and small ones again": (
+        [0.0, 9.0, 20.0], [(0, 70000), (1, 3), (0, 131072 + 5), (2, 1), (1, 200000), (0, MILLION)]),
+}
+
+
+@pytest.mark.parametrize("what", list(PREFILL))
+@pytest.mark.parametrize("new", [3, 300])
+def test_prefill_over_millions_of_keys(what, new):
+    """Causal: the last rows see up to 299 keys more than the first; `new` gives one or two query tiles."""
+    scores, runs = PREFILL[what]
+    kind = torch.cat([torch.full((n,), a) for a, n in runs]).cuda()
+    n, H = kind.numel(), 2
+    kv = torch.empty(n, H, 2 * NOPE, dtype=torch.bfloat16, device="cuda")
+    kv[..., :NOPE] = 0
+    for a in range(len(scores)):
+        for h in range(H):
+            kv[kind == a, h, NOPE:] = _values(NOPE, a + 3 * h).cuda()
+    pe = torch.zeros(n, POS, dtype=torch.bfloat16, device="cuda")
+    pe[:, 0] = torch.tensor(scores, device="cuda").to(torch.bfloat16)[kind]
+    q = torch.zeros(new, H, QK, dtype=torch.bfloat16, device="cuda")
+    q[..., NOPE] = 1
+    o, lse = kda.kda_mla_prefill(q, kv, pe, _ints([0, new]), _ints([0, n]), LN2)
+    total = torch.bincount(kind.cpu(), minlength=len(scores))
+    tail = torch.nn.functional.one_hot(kind[n - new + 1:].cpu(), len(scores)).flip(0).cumsum(0).flip(0)  # unseen by a row
+    counts = total - torch.cat([tail, torch.zeros(1, len(scores), dtype=torch.long)])
+    for h in range(H):
+        values = torch.stack([_values(NOPE, a + 3 * h) for a in range(len(scores))])
+        _close(o[:, h], lse[:, h], _want(counts, scores, values))
