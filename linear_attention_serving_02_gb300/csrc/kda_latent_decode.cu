@@ -38,6 +38,11 @@
 // exchanged, and O^T rescaled, on a sequence's first tile and where a score passes its
 // reference by 2^8.
 //
+// The tensor core drops what falls below an accumulator's last bit, always towards zero: a sum over n rows
+// comes out low by about n / 16 * 0.7 * 2^-23 of itself, 0.5% at a million. O^T therefore sums 1024 tiles
+// of a stretch at a time (4096 additions, 2^-11 at most); then it is added, with roundings to nearest, to
+// fp32 rows in the stretch's place among the partials, which a stretch of fewer tiles does not touch.
+//
 // Shared memory. Q takes 1152 B a row less what TMEM holds; the rest is a ring of 16 KB pairs of
 // chunks and a ring of 8 KB positional chunks, two tiles or more, with M = 128 a little less: there
 // the coming tile is asked into L2. One thread issues the score products chunk by chunk as they
@@ -65,6 +70,7 @@ constexpr int kDecThreads = 352;              // 8 softmax warps, S issue, value
 constexpr int kMaxGroups = 160;               // CTAs that share the list at most
 constexpr float kGrow = 8.0f;
 constexpr int kSoftmaxThreads = 256;
+constexpr int kFold = 1024;                   // tiles of a stretch that O^T sums in tensor memory (a power of two)
 constexpr int kHalf = kKvTile / 2;            // cached rows of a tile that a softmax thread takes
 
 struct DecodeGeom {
@@ -133,7 +139,7 @@ struct Walk {
     bool work;  // the sequence has cached rows and a sound length
     __device__ __forceinline__ void open(const DecodeArgs &p) {
         // where it stands and not again: with a load that the compiler may repeat or move, the score loop of
-        // the three-pair variant comes out slower (320 rows 248 us, 230 so)
+        // the variant with two pairs of Q's chunks in TMEM comes out slower (320 rows 248 us, 230 so)
         asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(len) : "l"(p.lens + n));
         tiles = tiles_of(p, len);
         j1 = (int32_t)min((int64_t)tiles, j0 + left);
@@ -165,6 +171,30 @@ __device__ __forceinline__ bool softmax_any(bool flag) {
                  : "r"((uint32_t)flag)
                  : "memory");
     return r != 0;
+}
+
+// kept = factor kept + O^T of this thread's latent, by query row; for the output (back) into O^T instead
+__device__ __forceinline__ void fold_o(float *kept, uint32_t o_addr, int npad, const float *factor, bool start, bool back) {
+    tc::fence_after_sync();
+    for (int e = 0; e < npad; e += 16) {
+        uint32_t x[16];
+        tma::tmem_ld16_nowait(o_addr + e, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+            float *at = kept + (int64_t)(e + y) * kLatent;
+            const float v = __uint_as_float(x[y]) + (start ? 0.f : *at * factor[e + y]);
+            x[y] = __float_as_uint(v);
+            if (!back) *at = v;
+        }
+        if (back) tc::tmem_st16(o_addr + e, x);
+    }
+    if (back) tc::tmem_wait_st();
+}
+// The same as a call: with M = 128 the loop over the tiles is the slower one with fold_o in its code (256 x 96
+// 299 us, 297 so), with two pairs of Q's chunks in TMEM it is the other way round (320 rows 238 us as a call, 223).
+__device__ __noinline__ void fold_o_call(float *kept, uint32_t o_addr, int npad, const float *factor, bool start, bool back) {
+    fold_o(kept, o_addr, npad, factor, start, back);
 }
 
 // MS: rows of the score product's M. QT: the first QT pairs of Q's latent chunks are kept in TMEM.
@@ -427,7 +457,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                     if (!ok) break;
                     tc::fence_after_sync();
                     const int steps = (min(kKvTile, w.len - j * kKvTile) + 15) / 16;
-                    const uint32_t more = j != w.j0;
+                    const uint32_t more = ((j - w.j0) & (kFold - 1)) != 0;
                     uint32_t d = tmem;
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i) {
@@ -492,100 +522,126 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         }
         for (; !w.done() && ok; w.next(p)) {
             float m_ref = -INFINITY, l = 0.f;
+            // the stretch's place among the partials: a run's first stretch, where it continues a sequence, has
+            // the first, the last one, which the run's end cuts, the second; before that any other may use it
+            const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.npad;
+            float m_kept = -INFINITY;  // the reference of O^T's sum over the tiles before the last kFold
             if (w.work) {
-                for (int j = w.j0; j < w.j1; ++j) {
-                    ok = tma::wait_warp(&sm.s_full[k % kS], (k / kS) & 1) && ok;
-                    // a failed wait still meets the barriers below, so that no warp is left in them
-                    if (ok) tc::fence_after_sync();
-                    uint32_t s[kHalf];
-                    const bool first = j == w.j0;
-                    float mb = m_ref == -INFINITY ? 0.f : -m_ref * c, top = -INFINITY;
-                    if (warp_rows && ok) {
-                        tc::tmem_ld32_nowait(t_s + lanes + (k % kS) * kKvTile + set * kHalf, s);
-                        tc::tmem_wait_ld();
-                        tc::fence_before_sync();
-                        // cached rows of this thread's half that the row sees
-                        const int64_t seen = (int64_t)w.len - unseen - ((int64_t)j * kKvTile + set * kHalf);
-                        if (__any_sync(0xffffffffu, seen < kHalf)) {
-#pragma unroll
-                            for (int e = 0; e < kHalf; ++e)
-                                if (e >= seen) s[e] = 0xff800000u;
+                bool stopped = false;
+                for (int js = w.j0; !stopped; js += kFold) {
+                    if (js > w.j0 && w.j1 - w.j0 > kFold) {
+                        // kFold tiles, or the last ones, are in O^T (also with a failed wait: all warps meet these barriers)
+                        ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                        const bool start = js == w.j0 + kFold;
+                        named_sync(2, kSoftmaxThreads);  // the factors have been read
+                        if (set == 0 && low) sm.factor[r] = start || m_kept == m_ref ? 1.0f : tc::ex2((m_kept - m_ref) * c);
+                        named_sync(2, kSoftmaxThreads);
+                        for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                            float *kept = p.part_o + part0 * kLatent + 128 * i + 32 * quarter + lane;
+                            if constexpr (QT == 2)
+                                fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
+                            else
+                                fold_o_call(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
                         }
-#pragma unroll
-                        for (int e = 0; e < kHalf; e += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                        m_kept = m_ref;
                     }
-                    tma::arrive_warp(&sm.s_free[k % kS]);
-                    // one barrier a tile: does a row need a new reference (also from -inf to a finite one), did a wait fail
-                    const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
-                    if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
-                    if (any) {
-                        if (low) sm.half[set][r] = top;
-                        // all stop together when any wait failed
-                        if (softmax_any(!ok)) {
-                            ok = false;
-                            break;
-                        }
-                        top = fmaxf(top, sm.half[set ^ 1][r]);
-                        const bool grown = first || (top - m_ref) * c > kGrow;
-                        const float m = grown ? top : m_ref, f = grown ? tc::ex2((m_ref - m) * c) : 1.0f;
-                        if (!first) {
-                            l *= f;
-                            if (set == 0 && low) sm.factor[r] = f;
-                            named_sync(2, kSoftmaxThreads);
-                            tc::fence_after_sync();
-                            for (int i = 2 * set; i < 2 * set + 2; ++i)
-                                for (int e = 0; e < geo.npad; e += 16) {
-                                    const uint32_t at = tmem + lanes + i * geo.npad + e;
-                                    uint32_t x[16];
-                                    tma::tmem_ld16_nowait(at, x);
-                                    tc::tmem_wait_ld();
+                    if (js >= w.j1) break;
+                    const int je = min(w.j1, js + kFold);
+                    for (int j = js; j < je; ++j) {
+                        ok = tma::wait_warp(&sm.s_full[k % kS], (k / kS) & 1) && ok;
+                        // a failed wait still meets the barriers below, so that no warp is left in them
+                        if (ok) tc::fence_after_sync();
+                        uint32_t s[kHalf];
+                        const bool first = j == w.j0;
+                        float mb = m_ref == -INFINITY ? 0.f : -m_ref * c, top = -INFINITY;
+                        if (warp_rows && ok) {
+                            tc::tmem_ld32_nowait(t_s + lanes + (k % kS) * kKvTile + set * kHalf, s);
+                            tc::tmem_wait_ld();
+                            tc::fence_before_sync();
+                            // cached rows of this thread's half that the row sees
+                            const int64_t seen = (int64_t)w.len - unseen - ((int64_t)j * kKvTile + set * kHalf);
+                            if (__any_sync(0xffffffffu, seen < kHalf)) {
 #pragma unroll
-                                    for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[e + y]);
-                                    tc::tmem_st16(at, x);
-                                }
-                            tc::tmem_wait_st();
-                        }
-                        m_ref = m;
-                        mb = m_ref == -INFINITY ? 0.f : -m_ref * c;
-                    }
-                    if (warp_rows && ok) {
-                        const uint64_t mb2 = pk2(mb, mb);
-                        uint64_t l2[2] = {0, 0};
-#pragma unroll
-                        for (int u = 0; u < kHalf / 8; ++u) {  // 16-byte units of the row, swizzled
-                            uint32_t h[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t *x = &s[8 * u + 2 * e];
-                                const float2 y = upk2(fma2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, mb2));
-                                const float a = tc::ex2(y.x), b = tc::ex2(y.y);
-                                l2[e & 1] = add2(l2[e & 1], pk2(a, b));
-                                const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
-                                h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                                for (int e = 0; e < kHalf; ++e)
+                                    if (e >= seen) s[e] = 0xff800000u;
                             }
-                            if (low && r < geo.npad)
-                                *reinterpret_cast<uint4 *>(p_row + (((4 * set + u) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                            for (int e = 0; e < kHalf; e += 2)
+                                top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
                         }
-                        const float2 ls = upk2(add2(l2[0], l2[1]));
-                        l += ls.x + ls.y;
-                    }
-                    const int valid = min(kKvTile, w.len - j * kKvTile);
-                    if (valid & 15) {  // value rows behind the sequence in the product's last step of 16
-                        const int units = (-valid & 15) * 8;
-                        for (int u = tid; u < 2 * kPairs * units; u += kSoftmaxThreads) {
-                            const int chunk = u / units;
-                            const int slot = (ps + (chunk >> 1)) % geo.np;
-                            reinterpret_cast<uint4 *>(s_pair + slot * kPairB + (chunk & 1) * kChunkB)[valid * 8 + u % units] =
-                                make_uint4(0, 0, 0, 0);
+                        tma::arrive_warp(&sm.s_free[k % kS]);
+                        // one barrier a tile: does a row need a new reference (also from -inf to a finite one), did a wait fail
+                        const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
+                        if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                        if (any) {
+                            if (low) sm.half[set][r] = top;
+                            // all stop together when any wait failed
+                            if (softmax_any(!ok)) {
+                                ok = false;
+                                stopped = true;
+                                break;
+                            }
+                            top = fmaxf(top, sm.half[set ^ 1][r]);
+                            const bool grown = first || (top - m_ref) * c > kGrow;
+                            const float m = grown ? top : m_ref, f = grown ? tc::ex2((m_ref - m) * c) : 1.0f;
+                            if (!first) {
+                                l *= f;
+                                if (set == 0 && low) sm.factor[r] = f;
+                                named_sync(2, kSoftmaxThreads);
+                                tc::fence_after_sync();
+                                for (int i = 2 * set; i < 2 * set + 2; ++i)
+                                    for (int e = 0; e < geo.npad; e += 16) {
+                                        const uint32_t at = tmem + lanes + i * geo.npad + e;
+                                        uint32_t x[16];
+                                        tma::tmem_ld16_nowait(at, x);
+                                        tc::tmem_wait_ld();
+#pragma unroll
+                                        for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * sm.factor[e + y]);
+                                        tc::tmem_st16(at, x);
+                                    }
+                                tc::tmem_wait_st();
+                            }
+                            m_ref = m;
+                            mb = m_ref == -INFINITY ? 0.f : -m_ref * c;
                         }
+                        if (warp_rows && ok) {
+                            const uint64_t mb2 = pk2(mb, mb);
+                            uint64_t l2[2] = {0, 0};
+#pragma unroll
+                            for (int u = 0; u < kHalf / 8; ++u) {  // 16-byte units of the row, swizzled
+                                uint32_t h[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t *x = &s[8 * u + 2 * e];
+                                    const float2 y = upk2(fma2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, mb2));
+                                    const float a = tc::ex2(y.x), b = tc::ex2(y.y);
+                                    l2[e & 1] = add2(l2[e & 1], pk2(a, b));
+                                    const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
+                                    h[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                                }
+                                if (low && r < geo.npad)
+                                    *reinterpret_cast<uint4 *>(p_row + (((4 * set + u) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                            const float2 ls = upk2(add2(l2[0], l2[1]));
+                            l += ls.x + ls.y;
+                        }
+                        const int valid = min(kKvTile, w.len - j * kKvTile);
+                        if (valid & 15) {  // value rows behind the sequence in the product's last step of 16
+                            const int units = (-valid & 15) * 8;
+                            for (int u = tid; u < 2 * kPairs * units; u += kSoftmaxThreads) {
+                                const int chunk = u / units;
+                                const int slot = (ps + (chunk >> 1)) % geo.np;
+                                reinterpret_cast<uint4 *>(s_pair + slot * kPairB + (chunk & 1) * kChunkB)[valid * 8 + u % units] =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        ps += kPairs;
+                        if (ps >= geo.np) ps -= geo.np;
+                        fence_proxy_async();
+                        tc::fence_before_sync();
+                        tma::arrive_warp(&sm.p_full);
+                        ++k;
                     }
-                    ps += kPairs;
-                    if (ps >= geo.np) ps -= geo.np;
-                    fence_proxy_async();
-                    tc::fence_before_sync();
-                    tma::arrive_warp(&sm.p_full);
-                    ++k;
                 }
                 if constexpr (QT > 0) {
                     // the next stretch's queries before this one's output, so that its scores start meanwhile
@@ -605,7 +661,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg & 3] != 0);
             if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
             const int64_t row0 = (int64_t)w.n * geo.R + row_first;
-            const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.npad;
             if (set == 0 && low) {
                 sm.factor[r] = bad ? NAN : (l == 0.f ? 0.f : 1.0f / l);
                 if (owner) {

@@ -5,7 +5,7 @@ o = sum n_a 2^{s_a} v_a / sum n_a 2^{s_a} and lse = ln sum n_a 2^{s_a}. The scal
 exponent s scale log2(e) rounds twice, so a weight is off by at most 2 ln 2 |s| 2^-24 < 2^-19 of itself for |s| <= 25.
 The weights are powers of two and the values positive: rounding P changes nothing, and a sum is off by
   2^-11   at most 4096 additions a part in the tensor core, each low by less than a step 2^-23
-  2^-13   at most 512 parts (2^25 keys of a row) added to nearest, 2^-24 each, and
+  2^-13   at most 512 parts (2^25 keys of a row, or of a thread block's stretch) added to nearest, 2^-24 each, and
           2^-17 of the denominator's additions (a tile's for themselves, then at most 2^18 tiles: where tiles are alike
           their sums are whole numbers below 2^24 times a power of two, exact)
 and o then is rounded to bf16."""
@@ -16,7 +16,7 @@ import torch
 
 from linear_attention_serving_02_gb300 import kda
 from tests import latent_ref as ref
-from tests.test_gpu_latent import NOPE, POS, QK, _ints
+from tests.test_gpu_latent import LATENT, NOPE, POS, QK, ROW, _ints
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,41 @@ def test_prefill_over_millions_of_keys(what, new):
     for h in range(H):
         values = torch.stack([_values(NOPE, a + 3 * h) for a in range(len(scores))])
         _close(o[:, h], lse[:, h], _want(counts, scores, values))
+
+
+DECODE = {
+    # lengths, kinds' scores, pages of each kind in turn, H, m
+    "alike, 13 blocks a list": ([1 << 26, 100], [0.0], [(0, 1)], 64, 16),
+    "alike, 96 rows": ([200 << 20], [0.0], [(0, 1)], 96, 1),
+    "a new maximum behind many rows": ([(1 << 25) + 33], [0.0, 9.0, 18.0], [(0, 1200), (1, 3), (0, 2100), (2, 1), (1, 900)], 64, 16),
+    "whole sequences of many tiles": ([80000 + 31 * n for n in range(170)], [0.0, 9.0], [(0, 1100), (1, 1), (0, 3)], 12, 1),
+}
+
+
+@pytest.mark.parametrize("what", list(DECODE))
+def test_decode_over_millions_of_rows(what):
+    """A page of each kind, which the page tables name again and again."""
+    lens, scores, turns, H, m = DECODE[what]
+    size, kinds, N = 64, len(scores), len(lens)
+    cycle = torch.cat([torch.full((n,), a, dtype=torch.int32) for a, n in turns])
+    most = max(-(-n // size) for n in lens)
+    row = cycle.repeat(-(-most // cycle.numel()))[:most]
+    values = torch.stack([_values(LATENT, a) for a in range(kinds)])
+    cache = torch.zeros(kinds, size, ROW, dtype=torch.bfloat16, device="cuda")
+    cache[..., :LATENT] = values.cuda()[:, None]
+    cache[..., LATENT] = torch.tensor(scores, device="cuda").to(torch.bfloat16)[:, None]
+    q_lat = torch.zeros(N * m, H, LATENT, dtype=torch.bfloat16, device="cuda")
+    q_pe = torch.zeros(N * m, H, POS, dtype=torch.bfloat16, device="cuda")
+    q_pe[..., 0] = 1
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = kda.kda_mla_decode(q_lat, q_pe, cache, row.cuda().repeat(N, 1), _ints(lens), LN2, num_tokens=m, status=st)
+    assert st.item() == 0
+    for n, length in enumerate(lens):
+        for t in range(m):
+            seen = length - (m - 1 - t)
+            full, rest = divmod(seen, size)
+            counts = size * torch.bincount(row[:full], minlength=kinds)
+            if rest:
+                counts[row[full]] += rest
+            wo, wl = _want(counts, scores, values)
+            _close(o[n * m + t], lse[n * m + t], (wo.expand(H, -1), wl.expand(H)))
