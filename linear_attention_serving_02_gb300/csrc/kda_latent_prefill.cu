@@ -242,6 +242,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
     pdl_wait();
     const uint32_t tmem = sm.tmem;
     bool ok = true;
+    // A wait that may last as long as another query tile or role works on an item (10^8 keys take more than a
+    // wait's limit): the limit counts from the last load that the item was seen to make
+    auto wait_while_loading = [&](uint64_t *mbar, uint32_t parity) {
+        auto loads = [&] { return __shfl_sync(0xffffffffu, *(volatile int32_t *)&sm.k_issued, 0); };
+        int seen;
+        bool got;
+        do {
+            seen = loads();
+            got = tma::wait_warp(mbar, parity);
+        } while (!got && loads() != seen);
+        return got;
+    };
 
     if (warp == 9) {
         // ---- TMA producer: one thread ----
@@ -302,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
         // ---- scheduler: this block's item, then those of blocks that have not started, taken over one
         // at a time when the loads of the item at hand come to their end ----
         int64_t index = blockIdx.x;
-        auto loads_seen = [&] { return __shfl_sync(0xffffffffu, *(volatile int32_t *)&sm.k_issued, 0); };
         Place at = {0, 0};
         int n = 0, asked = 0;
         while (ok) {
@@ -323,11 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                     tma::prefetch_3d(&p.q, 64 * (lane % 3), w.h, w.q0 + w.row0 + (lane / 3) * kTileQ);
                 if (n > 0 && lane >= 8 && lane < 12 && max(w.nt0, w.nt1) > 0)
                     tma::prefetch_3d(&p.kv, 64 * (lane - 8), w.h, w.k0);
-                int seen;
-                do {  // an item of 10^8 keys outlasts the limit of a wait, which counts from its last load then
-                    seen = loads_seen();
-                    ok = tma::wait_warp(&sm.ask, n & 1);
-                } while (!ok && loads_seen() != seen);
+                ok = wait_while_loading(&sm.ask, n & 1);
                 ++n;
                 if (!ok) break;
             }
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
         const uint64_t c2 = pk2(c, c);
         int sp = 0, ve = 0;  // score tiles of this query tile so far, V tiles before this item
         for (int n = 0; ok; ++n) {
-            ok = tma::wait_warp(&sm.item_full[n & 1], (n >> 1) & 1);
+            ok = wait_while_loading(&sm.item_full[n & 1], (n >> 1) & 1);  // tile 1 may have no rows
             if (!ok) break;
             const Item w = sm.item[n & 1];
             if (w.h < 0) break;

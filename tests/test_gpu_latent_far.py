@@ -77,6 +77,28 @@ def test_prefill_over_millions_of_keys(what, new):
         _close(o[:, h], lse[:, h], _want(counts, scores, values))
 
 
+def test_prefill_of_one_query_tile_that_takes_longer_than_a_wait():
+    """The warps of the second query tile, which has no rows, wait for the item's end: 1.5 us a key tile, 2.4 s, where
+    a wait gives up after 2. Needs 135 GB for its 2.1e8 keys."""
+    n = 210_000_000
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < n * 2 * (2 * NOPE + POS) + (4 << 30):
+        pytest.skip("not enough free device memory")
+    kv = torch.empty(n, 1, 2 * NOPE, dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros(n, POS, dtype=torch.bfloat16, device="cuda")
+    kv[:] = torch.cat([torch.zeros(NOPE), _values(NOPE, 2)]).to(torch.bfloat16).cuda()
+    q = torch.randn(5, 1, QK, device="cuda").to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = kda.kda_mla_prefill(q, kv, pe, _ints([0, 5]), _ints([0, n]), LN2, causal=False, status=st)
+    assert st.item() == 0
+    # 3205 parts instead of 512, and a denominator of 128 a tile, whole numbers of fewer than 24 bits
+    want = _want(torch.tensor([[n]]), [0.0], _values(NOPE, 2)[None])
+    assert bool(((o[:, 0].double().cpu() - want[0]).abs() <= (TOL_O + 2.0 ** -12) * want[0]).all())
+    assert bool(((lse[:, 0].double().cpu() - want[1]).abs() <= TOL_LSE + 2.0 ** -22 * want[1]).all())
+    del kv, pe
+    torch.cuda.empty_cache()
+
+
 DECODE = {
     # lengths, kinds' scores, pages of each kind in turn, H, m
     "alike, 13 blocks a list": ([1 << 26, 100], [0.0], [(0, 1)], 64, 16),
