@@ -467,7 +467,8 @@ int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages
  * to bf16 for the product with the values. Hidden scores count for nothing whatever they are,
  * but a NaN or infinite value row inside a sequence can reach rows that do not see it (its
  * probability there is 0); rows outside the sequence never do. A sequence whose offsets fall
- * or leave the tensors is not computed and sets 'status' to KDA_ERR_SEQLENS; its rows are
+ * or leave the tensors, or whose queries begin before an earlier one's end (offsets fell between
+ * them), is not computed and sets 'status' to KDA_ERR_SEQLENS; its rows are
  * left as they were. Pointers are 16-byte aligned (tables, lse and status: 4).
  */
 int kda_mla_prefill(const uint16_t *q, const uint16_t *kv, const uint16_t *k_pe, int64_t k_pe_stride,

@@ -108,10 +108,11 @@ __device__ __forceinline__ int key_tiles(const Item &w, int causal, int first) {
     return last < first ? 0 : (int)(((int64_t)keys_of(w, causal, last) + kTileK - 1) / kTileK);
 }
 
-// Where the last item was found: 32 sequences from n0 on, with `before` tiles before them. The blocks that a
-// block takes over come mostly in rising order, so that it reads the list of sequences about once.
+// Where the last item was found: 32 sequences from n0 on, with `before` tiles before them, whose query rows
+// end at `top`. The blocks that a block takes over come mostly in rising order, so that it reads the list of
+// sequences about once.
 struct Place {
-    int32_t n0;
+    int32_t n0, top;
     int64_t before;
 };
 
@@ -120,16 +121,34 @@ struct Place {
 __device__ __forceinline__ bool find_item(const PrefillArgs &p, int64_t index, Place &at, Item &w) {
     const int lane = threadIdx.x & 31;
     const int64_t slot = index / p.H;
-    if (slot < at.before) at = {0, 0};
+    if (slot < at.before) at = {0, 0, 0};
     for (; at.n0 < p.N; at.n0 += 32) {
         const int n0 = at.n0;
         const int64_t before = at.before;
         const int n = n0 + lane;
         int a = 0, b = 0, c = 0, d = 0;
         int64_t tiles = 0;
+        bool sound = true;
         if (n < p.N) {
             a = p.cu_q[n], b = p.cu_q[n + 1], c = p.cu_k[n], d = p.cu_k[n + 1];
-            if (a < 0 || b > p.Tq || b < a || c < 0 || d > p.Tk || d < c)
+            sound = a >= 0 && b <= p.Tq && b >= a && c >= 0 && d <= p.Tk && d >= c;
+        }
+        // where the rows of the sequences before end. Behind offsets that fell a sequence may begin before that:
+        // its rows would be written twice, and the batch have more tiles than the grid has blocks
+        const int32_t end = n < p.N && sound ? b : 0;
+        int32_t top = at.top;
+        if (__any_sync(0xffffffffu, !sound)) {
+            int32_t most = end;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int32_t x = __shfl_up_sync(0xffffffffu, most, off);
+                if (lane >= off) most = max(most, x);
+            }
+            most = __shfl_up_sync(0xffffffffu, most, 1);
+            if (lane > 0) top = max(top, most);
+        }
+        if (n < p.N) {
+            if (!sound || a < top)
                 set_status(p.status, KDA_ERR_SEQLENS);  // every CTA that looks finds it: no tiles
             else
                 tiles = ((int64_t)b - a + kRowsCta - 1) / kRowsCta;
@@ -156,6 +175,7 @@ __device__ __forceinline__ bool find_item(const PrefillArgs &p, int64_t index, P
             return true;
         }
         at.before += __shfl_sync(0xffffffffu, incl, 31);
+        at.top = max(at.top, __reduce_max_sync(0xffffffffu, end));
     }
     return false;
 }
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
         // ---- scheduler: this block's item, then those of blocks that have not started, taken over one
         // at a time when the loads of the item at hand come to their end ----
         int64_t index = blockIdx.x;
-        Place at = {0, 0};
+        Place at = {0, 0, 0};
         int n = 0, asked = 0;
         while (ok) {
             Item w;
