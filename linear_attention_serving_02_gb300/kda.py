@@ -360,12 +360,13 @@ _BINDING = None
 
 
 def binding():
-    """The compiled binding (built in-tree with the library)."""
+    """The compiled binding (built in-tree, for the running Python and torch)."""
     global _BINDING
     if _BINDING is None:
         library()
-        loader = importlib.machinery.ExtensionFileLoader("_kda_binding", _build.BINDING)
-        spec = importlib.util.spec_from_file_location("_kda_binding", _build.BINDING, loader=loader)
+        path = _build.build_binding()
+        loader = importlib.machinery.ExtensionFileLoader("_kda_binding", path)
+        spec = importlib.util.spec_from_file_location("_kda_binding", path, loader=loader)
         mod = importlib.util.module_from_spec(spec)
         loader.exec_module(mod)
         mod.set_error(KdaError)
