@@ -70,7 +70,8 @@ def test_prefill_over_millions_of_keys(what, new):
     q[..., NOPE] = 1
     o, lse = kda.kda_mla_prefill(q, kv, pe, _ints([0, new]), _ints([0, n]), LN2)
     total = torch.bincount(kind.cpu(), minlength=len(scores))
-    tail = torch.nn.functional.one_hot(kind[n - new + 1:].cpu(), len(scores)).flip(0).cumsum(0).flip(0)  # unseen by a row
+    # what a row does not see
+    tail = torch.nn.functional.one_hot(kind[n - new + 1:].cpu(), len(scores)).flip(0).cumsum(0).flip(0)
     counts = total - torch.cat([tail, torch.zeros(1, len(scores), dtype=torch.long)])
     for h in range(H):
         values = torch.stack([_values(NOPE, a + 3 * h) for a in range(len(scores))])
@@ -103,8 +104,10 @@ DECODE = {
     # lengths, kinds' scores, pages of each kind in turn, H, m
     "alike, 13 blocks a list": ([1 << 26, 100], [0.0], [(0, 1)], 64, 16),
     "alike, 96 rows": ([200 << 20], [0.0], [(0, 1)], 96, 1),
-    "a new maximum behind many rows": ([(1 << 25) + 33], [0.0, 9.0, 18.0], [(0, 1200), (1, 3), (0, 2100), (2, 1), (1, 900)], 64, 16),
-    "whole sequences of many tiles": ([80000 + 31 * n for n in range(170)], [0.0, 9.0], [(0, 1100), (1, 1), (0, 3)], 12, 1),
+    "a new maximum behind many rows": ([(1 << 25) + 33], [0.0, 9.0, 18.0],
+                                       [(0, 1200), (1, 3), (0, 2100), (2, 1), (1, 900)], 64, 16),
+    "whole sequences of many tiles": ([80000 + 31 * n for n in range(170)], [0.0, 9.0],
+                                      [(0, 1100), (1, 1), (0, 3)], 12, 1),
 }
 
 

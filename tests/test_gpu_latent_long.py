@@ -36,27 +36,35 @@ def test_decode_of_many_tiles_with_several_row_tiles(H, m, size):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+# one long sequence (all blocks' parts joined by 16 warps a row), some (by four), many (by one)
+COUNTED = [[(1 << 20) + 5], [LATENT * TILE_ROWS, 0, 300011], [900 + 1061 * n for n in range(20)],
+           [LATENT * TILE_ROWS, 0, 20016, 1, 64, 30011, 4500, 127] + [900 + 61 * n for n in range(40)]]
+
+
+@pytest.mark.parametrize("lens", COUNTED, ids=lambda lens: "%d sequences" % len(lens))
 @pytest.mark.parametrize("H,m", [(12, 1), (64, 1), (96, 1), (65, 2), (96, 4), (64, 16)])
-def test_decode_counts_every_tile_once(H, m):
-    """All scores are 0 and row i holds 1 in latent i // 64, so o[d] is the share of the visible rows in tile d:
-    weights of 1 and counts are exact, what is left is the quotient and its rounding."""
+def test_decode_counts_every_tile_once(lens, H, m):
+    """All scores are 0 and row i holds 1 in latent i // 64 % 512, so o[d] is the share of the visible rows in the
+    tiles d, d + 512, ..: weights of 1 and counts are exact, what is left is the quotient and its rounding. Of 32 tiles
+    a latent at most, one too few or too many moves it by 3%."""
     g, size = _gen(60), 64
-    lens = [LATENT * TILE_ROWS, 0, 20000 + m, 1, 64, 30011, 4500, 127] + [900 + 61 * n for n in range(40)]
     table, pages = ref.make_pages(g, lens, size)
     cache = torch.full((pages, size, ROW), float("nan"), dtype=torch.bfloat16, device="cuda")
     for n, k in enumerate(lens):
         i = torch.arange(k)
         at = (table[n, i // size].long() * size + i % size).cuda()
-        cache.view(-1, ROW)[at] = torch.nn.functional.one_hot(i // TILE_ROWS, ROW).to(torch.bfloat16).cuda()
+        one = torch.eye(LATENT, ROW, dtype=torch.bfloat16, device="cuda")
+        cache.view(-1, ROW)[at] = one[(i // TILE_ROWS % LATENT).cuda()]
     N = len(lens)
     q_lat = torch.zeros(N * m, H, LATENT, dtype=torch.bfloat16, device="cuda")
     q_pe = torch.randn(N * m, H, POS, generator=g).to(torch.bfloat16).cuda()
     o, lse = kda.kda_mla_decode(q_lat, q_pe, cache, table.cuda(), _ints(lens), SCALE, num_tokens=m)
-    tiles = TILE_ROWS * torch.arange(LATENT, dtype=torch.float64, device="cuda")
     for n, k in enumerate(lens):
         for t in range(m):
             seen = max(0, k - (m - 1 - t))
-            want = (seen - tiles).clamp(0, TILE_ROWS) / max(1, seen)
+            tiles = LATENT * (1 + k // (TILE_ROWS * LATENT))
+            tiles = TILE_ROWS * torch.arange(tiles, dtype=torch.float64, device="cuda")
+            want = (seen - tiles).clamp(0, TILE_ROWS).view(-1, LATENT).sum(0) / max(1, seen)
             got = o[n * m + t].double()
             assert bool(((got - want).abs() <= (ref.U_BF16 + 2.0 ** -21) * want).all()), (n, t)
             l = torch.tensor(float(seen), dtype=torch.float64).log()
@@ -91,23 +99,25 @@ def test_prefill_of_several_items_a_block(causal):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("new,total,H", [([16384], [16384], 4), ([700, 3000, 257, 5000], [9000, 3000, 16200, 5300], 9)])
+@pytest.mark.parametrize("new,total,H", [([16384], [16384], 4), ([700, 3000, 257, 5000], [9000, 3000, 16200, 5300], 9),
+                                         ([300, 5], [1 << 19, 70001], 2)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_prefill_counts_every_key_tile_once(new, total, H, causal):
-    """All scores are 0 and key j holds 1 in value j // 128: o[d] is the share of the visible keys in tile d."""
+    """All scores are 0 and key j holds 1 in value j // 128 % 128: o[d] is the share of the visible keys in the tiles
+    d, d + 128, .., of 32 at most, so that one moves it by 3%."""
     g, cu_q, cu_k = _gen(62), _cu(new), _cu(total)
     q = torch.zeros(sum(new), H, QK, dtype=torch.bfloat16, device="cuda")
     kv = torch.empty(sum(total), H, 2 * NOPE, dtype=torch.bfloat16, device="cuda")
     kv[..., :NOPE] = torch.randn(H, NOPE, generator=g).to(torch.bfloat16).cuda()
-    j = torch.cat([torch.arange(n) for n in total]).cuda() // TILE_K
-    kv[..., NOPE:] = torch.nn.functional.one_hot(j, NOPE).to(torch.bfloat16)[:, None]
+    j = torch.cat([torch.arange(n) for n in total]).cuda() // TILE_K % NOPE
+    kv[..., NOPE:] = torch.eye(NOPE, dtype=torch.bfloat16, device="cuda")[j][:, None]
     pe = torch.randn(sum(total), POS, generator=g).to(torch.bfloat16).cuda()
     o, lse = kda.kda_mla_prefill(q, kv, pe, _ints(cu_q), _ints(cu_k), SCALE, causal=causal)
-    tiles = TILE_K * torch.arange(NOPE, dtype=torch.float64, device="cuda")
     for n, (k, a) in enumerate(zip(total, new)):
+        tiles = TILE_K * torch.arange(NOPE * (1 + k // (TILE_K * NOPE)), dtype=torch.float64, device="cuda")
         seen = torch.arange(k - a + 1, k + 1, device="cuda", dtype=torch.float64)
         seen = seen if causal else torch.full_like(seen, k)
-        want = ((seen[:, None] - tiles).clamp(0, TILE_K) / seen[:, None])[:, None]
+        want = ((seen[:, None] - tiles).clamp(0, TILE_K).view(a, -1, NOPE).sum(1) / seen[:, None])[:, None]
         got = o[cu_q[n]:cu_q[n + 1]].double()
         assert bool(((got - want).abs() <= (ref.U_BF16 + 2.0 ** -21) * want).all()), n
         l = seen.log()[:, None]

@@ -16,7 +16,10 @@ def test_no_multicast(path):
     assert not re.search(r"multicast\s*::\s*cluster", open(path).read())
 
 
-@pytest.mark.parametrize("path", [p for p in SOURCES if re.search("latent|pages", os.path.basename(p))], ids=os.path.basename)
+EARLY = [p for p in SOURCES if re.search("latent|pages", os.path.basename(p))]
+
+
+@pytest.mark.parametrize("path", EARLY, ids=os.path.basename)
 def test_no_read_only_loads_in_kernels_launched_early(path):
     """These kernels come onto the GPU before the previous one has ended, so what they read is not
     constant for their lifetime: no load may claim that it is, nor a pointer that nothing else writes."""
