@@ -25,13 +25,17 @@
 // cycle: 96 rows need about 28 x 48 + 8 x 32 + 16 x 56 = 2500 cycles a tile and 16 rows 1780, where
 // the tile's 72 KB take an SM's share of HBM about 3100.
 //
-// Measured: 1M cached rows x 12 heads 191 us with the join (6.3 TB/s), bound by the rows' bytes;
-// 256 sequences of up to 8000 rows x 96 heads 293 us (4.3 TB/s). There a tile takes 4000
+// Measured: 1M cached rows x 12 heads 192 us with the join (6.3 TB/s), bound by the rows' bytes;
+// 256 sequences of up to 8000 rows x 96 heads 297 us (4.3 TB/s). There a tile takes 4000
 // cycles, of which shared memory is busy about 3000: the operands' 2500 and 576 for the rows'
 // arrival. In the rest load, last scores, softmax (1200) and value product of a tile follow one
-// another, as the ring holds a little less than two tiles. Tiles of 48 rows, of which it holds two
-// and a quarter, take the same time (296); two CTAs with 48 query rows each 346; two CTAs that
-// split the columns and trade partial scores 427.
+// another, as the ring holds a little less than two tiles; and the join of the parts that the 151
+// borders leave (59 MB written and read) takes 19 us when it runs alone. Tiles of 48 rows, of which
+// the ring holds two and a quarter, take the same time in all; two CTAs with 48 query rows each 346;
+// two CTAs that split the columns and trade partial scores 427.
+//
+// P is rounded to bf16 for the value product, which takes 16-bit operands (two of them a weight would
+// double it); the sum of the weights is that of the fp32 values.
 //
 // The reference M_r only has to stay within 2^8 of the row's maximum (P is then far inside
 // bf16 and fp32), so a tile costs a comparison a score and one barrier; the halves' maxima are
@@ -138,8 +142,8 @@ struct Walk {
     int64_t left;
     bool work;  // the sequence has cached rows and a sound length
     __device__ __forceinline__ void open(const DecodeArgs &p) {
-        // where it stands and not again: with a load that the compiler may repeat or move, the score loop of
-        // the variant with two pairs of Q's chunks in TMEM comes out slower (320 rows 248 us, 230 so)
+        // where it stands and not again: with a load that the compiler may repeat, two tiles of 72 rows take
+        // longer (64 sequences x 130 rows 138 us, 131 so)
         asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(len) : "l"(p.lens + n));
         tiles = tiles_of(p, len);
         j1 = (int32_t)min((int64_t)tiles, j0 + left);
@@ -190,11 +194,6 @@ __device__ __forceinline__ void fold_o(float *kept, uint32_t o_addr, int npad, c
         if (back) tc::tmem_st16(o_addr + e, x);
     }
     if (back) tc::tmem_wait_st();
-}
-// The same as a call: with M = 128 the loop over the tiles is the slower one with fold_o in its code (256 x 96
-// 299 us, 297 so), with two pairs of Q's chunks in TMEM it is the other way round (320 rows 238 us as a call, 223).
-__device__ __noinline__ void fold_o_call(float *kept, uint32_t o_addr, int npad, const float *factor, bool start, bool back) {
-    fold_o(kept, o_addr, npad, factor, start, back);
 }
 
 // MS: rows of the score product's M. QT: the first QT pairs of Q's latent chunks are kept in TMEM.
@@ -538,10 +537,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         named_sync(2, kSoftmaxThreads);
                         for (int i = 2 * set; i < 2 * set + 2; ++i) {
                             float *kept = p.part_o + part0 * kLatent + 128 * i + 32 * quarter + lane;
-                            if constexpr (QT == 2)
-                                fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
-                            else
-                                fold_o_call(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
+                            fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
                         }
                         m_kept = m_ref;
                     }
@@ -738,8 +734,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
 // blocks a row (1M x 12: 195 us with one, 192 with four); the parts are added in list order within a
 // warp and the warps' sums in warp order, so the result does not depend on timing. With W = 1 the
 // way through shared memory is not needed, but the 32 KB keep these blocks off the SMs until
-// the main kernel's are through: without them they wait beside it, and 256 x 96 takes 300 us
-// instead of 294.
+// the main kernel's are through: without them they wait beside it, and 256 x 96 takes 2% longer.
 constexpr int kJoinThreads = 512;
 template <int W, int Z>
 __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid_constant__ DecodeArgs p) {
@@ -857,16 +852,16 @@ constexpr size_t kSmemMax = 232448;
 
 // Row tiles of equal size; the rings take what Q and P leave. One tile up to 96 rows and two up to
 // 192, with M = 128 past 64 rows. From there on as few as 96 rows each allow, or as 64 do (M = 64, four of
-// Q's chunks in TMEM) where that is less than 13/9 as many: 64 sequences of up to 8000 rows take with tiles
-// of up to 64 and 96 rows 190 and 213 us (256 rows, 4 and 3 tiles), 235 and 213 (288, 5 and 3), 230 and
-// 240 (320, 5 and 4), 270 and 267 (384, 6 and 4), 351 and 384 (512, 8 and 6), 410 and 383 (576, 9 and 6),
-// 436 and 450 (640, 10 and 7), 537 and 496 (768, 12 and 8), 714 and 690 (1024, 16 and 11).
+// Q's chunks in TMEM) where that is less than half as many again: 64 sequences of up to 8000 rows take with
+// tiles of up to 64 and 96 rows 188 and 213 us (256 rows, 4 and 3 tiles), 222 and 214 (288, 5 and 3), 225
+// and 229 (320, 5 and 4), 265 and 269 (384, 6 and 4), 342 and 386 (512, 8 and 6), 395 and 384 (576, 9 and 6),
+// 422 and 452 (640, 10 and 7), 512 and 498 (768, 12 and 8), 669 and 694 (1024, 16 and 11).
 DecodeGeom geometry(int32_t H, int32_t m) {
     DecodeGeom q{};
     q.R = H * m;
     q.RT = (q.R + kWideRows - 1) / kWideRows;
     const int32_t narrow = (q.R + kRowTile - 1) / kRowTile;
-    if (q.RT > 2 && 9 * (int64_t)narrow < 13 * (int64_t)q.RT) q.RT = narrow;
+    if (q.RT > 2 && 2 * (int64_t)narrow < 3 * (int64_t)q.RT) q.RT = narrow;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
     q.qt = q.rows > kRowTile ? 1 : (q.RT == 1 ? 0 : 2);  // 4 npad + 64 or 128 + 64 qt TMEM columns: 512 at most

@@ -15,22 +15,26 @@
 // S0(j+1) PV1(j) S1(j+1). TMEM holds exactly S0 S1 O0 O1 (4 x 128 columns). P is handed over in
 // parts of 32 keys, so that P V starts while the rest is at its exponentials.
 //
-// The grid has a block per 256 rows and head, the rows with the most keys first. One block fits an
+// The grid has a block per 256 rows and head, a sequence's rows with the most keys first. One block fits an
 // SM; when its loads come to their end it takes over one that has not started and loads for it
 // while the last products and the output still run: the first scores of the next item are issued
 // before the last value product of this one. Against blocks that start one after another (8192 new
-// tokens x 12 heads, causal; five ragged sequences x 32 heads): 167.8 and 160.5 us against 173.6
-// and 177.5.
+// tokens x 12 heads, causal; five ragged sequences x 32 heads): 167 and 160 us against 173.6 and 177.5.
+// These are times of ten calls replayed from a graph; in a long row of calls, at the clocks that the power
+// limit then leaves, the first two take 177 and 167 us.
 //
 // Bounds: 2 x 1280 cycles of tensor work a key tile at 8192 flop a cycle, and 32 K exponentials,
 // 2048 cycles at 16 a cycle. A key tile takes about 3200 cycles: S to P and back is a chain of
 // 2000 that the other tile's products cover but for their own waits. 8192 x 12 runs at
-// 1.54 PFLOP/s; the ragged case, whose tiles do 19% more than its rows need and whose last items
-// end apart, at 1.13. Measured and not taken: two threads a row (176 and 169 us, more handing
-// over), part of the exponentials as polynomials on the FMA pipe (183 us with an eighth of them,
-// 190 with a quarter), clusters of two that share the keys by multicast (183 and 200 us), a reference that follows the
-// maximum only where 32 weights sum to more than 2^24 (167 and 155.5, but 272 us instead of 196 where
-// scores spread by 9). 16384 tokens x 16 heads run at 1.77 PFLOP/s.
+// 1.54 PFLOP/s (1.45 in a long row); the ragged case, whose tiles do 19% more than its rows need and
+// whose last items end apart, at 1.13 (1.09). Measured and not taken: two threads a row (176 and 169 us,
+// more handing over), part of the exponentials as polynomials on the FMA pipe (183 us with an eighth of
+// them, 190 with a quarter), a reference that follows the maximum only where 32 weights sum to more than
+// 2^24 (167 and 155.5, but 272 us instead of 196 where scores spread by 9). 16384 tokens x 16 heads run at
+// 1.77 PFLOP/s.
+//
+// P is rounded to bf16 for the value product, which takes 16-bit operands (two of them a weight would
+// double it); the sum of the weights is that of the fp32 values.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its last reference
 // (P stays below 2^8, far inside bf16 and fp32), which few tiles do; l sums the fp32 values, a key
