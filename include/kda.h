@@ -462,9 +462,9 @@ int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages
  *   o         device bf16 [total_q, H, 128] (written)
  *   lse       device fp32 [total_q, H] or NULL: log sum_j exp(s_j)
  * k_pe_stride is a multiple of 8 and at least 64. Rows of o and lse outside every sequence's range are
- * left as they were. Scores, statistics and sums are fp32 (a sum over n_k keys is within about 2^-11 of
- * itself however long they are); the probabilities are rounded
- * to bf16 for the product with the values. Hidden scores count for nothing whatever they are,
+ * left as they were. Scores, statistics and sums are fp32 (a sum of values is within about 2^-11 of
+ * itself, however many keys); the probabilities are rounded to bf16 for the product with the
+ * values. Hidden scores count for nothing whatever they are,
  * but a NaN or infinite value row inside a sequence can reach rows that do not see it (its
  * probability there is 0); rows outside the sequence never do. A sequence whose offsets fall
  * or leave the tensors, or whose queries begin before an earlier one's end (offsets fell between
@@ -498,7 +498,9 @@ size_t kda_mla_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_
  *   workspace device scratch, kda_mla_decode_workspace_size() bytes, 256-byte aligned; its
  *             contents need no initialisation and are dead after the call
  * Pointers are 16-byte aligned (tables, lse and status: 4). Calls that share a workspace must be
- * ordered on one stream. A NaN or infinite row of a sequence can reach window tokens that do
+ * ordered on one stream. Scores, statistics, sums and partial outputs are fp32 (a sum is within about
+ * 2^-11 of itself, however many rows); the probabilities are rounded to bf16 for the product with the
+ * rows. A NaN or infinite row of a sequence can reach window tokens that do
  * not see it; rows outside the sequence never do. A sequence with a negative length, one past
  * its page table, or a bad page id gets NaN in o and lse and sets 'status'.
  */

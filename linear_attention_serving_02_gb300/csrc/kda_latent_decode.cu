@@ -30,7 +30,7 @@
 // cycles, of which shared memory is busy about 3000: the operands' 2500 and 576 for the rows'
 // arrival. In the rest load, last scores, softmax (1200) and value product of a tile follow one
 // another, as the ring holds a little less than two tiles; and the join of the parts that the 151
-// borders leave (59 MB written and read) takes 19 us when it runs alone. Tiles of 48 rows, of which
+// borders leave (59 MB written and read) takes 20 us when it runs alone. Tiles of 48 rows, of which
 // the ring holds two and a quarter, take the same time in all; two CTAs with 48 query rows each 346;
 // two CTAs that split the columns and trade partial scores 427.
 //
