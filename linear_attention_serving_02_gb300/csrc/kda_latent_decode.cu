@@ -45,7 +45,8 @@
 // The tensor core drops what falls below an accumulator's last bit, always towards zero: a sum over n rows
 // comes out low by about n / 16 * 0.7 * 2^-23 of itself, 0.5% at a million. O^T therefore sums 1024 tiles
 // of a stretch at a time (4096 additions, 2^-11 at most); then it is added, with roundings to nearest, to
-// fp32 rows in the stretch's place among the partials, which a stretch of fewer tiles does not touch.
+// fp32 rows in the stretch's place among the partials, which a stretch of fewer tiles does not touch, and
+// the denominator, whose roundings go one way too where tiles are alike, to one in a register.
 //
 // Shared memory. Q takes 1152 B a row less what TMEM holds; the rest is a ring of 16 KB pairs of
 // chunks and a ring of 8 KB positional chunks, two tiles or more, with M = 128 a little less: there
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             // the stretch's place among the partials: a run's first stretch, where it continues a sequence, has
             // the first, the last one, which the run's end cuts, the second; before that any other may use it
             const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.npad;
-            float m_kept = -INFINITY;  // the reference of O^T's sum over the tiles before the last kFold
+            float m_kept = -INFINITY, l_kept = 0.f;  // reference and denominator of the tiles before the last kFold
             if (w.work) {
                 bool stopped = false;
                 for (int js = w.j0; !stopped; js += kFold) {
@@ -540,6 +541,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                             fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
                         }
                         m_kept = m_ref;
+                        if (low) l_kept = l_kept * sm.factor[r] + l;
+                        l = js >= w.j1 ? l_kept : 0.f;
                     }
                     if (js >= w.j1) break;
                     const int je = min(w.j1, js + kFold);

@@ -43,7 +43,8 @@
 // The tensor core drops what falls below an accumulator's last bit, always towards zero, so a sum over
 // n keys comes out low by about n / 16 * 0.7 * 2^-23 of itself: 0.5% at a million keys, 17% at 33 million.
 // O therefore sums 512 key tiles at a time (4096 additions, 2^-11 at most); then its row is added to
-// one in local memory, with roundings to nearest. That row is touched behind 65536 keys only.
+// one in local memory, with roundings to nearest, and so is l, whose roundings go one way too where tiles
+// are alike. That row is touched behind 65536 keys only.
 //
 // Shared memory: Q 96 KB, K in a ring of four 16 KB chunks (one key tile and the next tile's
 // first chunk), V in a ring of two 32 KB tiles. Rows of a tile that lie behind the sequence
@@ -210,10 +211,11 @@ __device__ __forceinline__ void exp32(const uint32_t (&r)[32], uint32_t (&p)[16]
     }
 }
 
-// kept (+)= O of this thread's row, at O's reference m_ref (kept's own stands behind its values); for the
-// output (back) into O instead. A call of its own: in the loop's code it made every tile slower
-// (8192 x 12 170.5 us, 168.5 so).
-__device__ __noinline__ void fold_o(float *kept, uint32_t o_addr, float m_ref, float c, bool first, bool back) {
+// kept (+)= O and the denominator l of this thread's row, at their reference m_ref; for the output (back) into
+// O instead. Behind kept's values of O stand its reference and its denominator; returns that. A call of its
+// own: in the loop's code it made every tile slower (8192 x 12 170.5 us, 168.5 so).
+constexpr int kKept = kNope + 2;
+__device__ __noinline__ float fold_o(float *kept, uint32_t o_addr, float l, float m_ref, float c, bool first, bool back) {
     const float f = first || kept[kNope] == m_ref ? 1.0f : tc::ex2((kept[kNope] - m_ref) * c);
 #pragma unroll 1
     for (int i = 0; i < kNope / 16; ++i) {
@@ -230,6 +232,7 @@ __device__ __noinline__ void fold_o(float *kept, uint32_t o_addr, float m_ref, f
     }
     if (back) tc::tmem_wait_st();
     kept[kNope] = m_ref;
+    return kept[kNope + 1] = l + (first ? 0.f : kept[kNope + 1] * f);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __grid_constant__ PrefillArgs p) {
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
             const int keys = row < w.nq ? keys_of(w, p.causal, row) : w.nk;
             float m_ref = -INFINITY;  // reference maximum of O and l, in raw scores
             uint64_t l = pk2(0.f, 0.f);
-            float kept[kNope + 1];  // O of the tiles before the last kFold, and its reference
+            float kept[kKept];  // O, reference and denominator of the tiles before the last kFold
             int je = min(nt, kFold);  // the next key tile to stop at
             for (int j = 0;; ++j, ++sp) {
                 if (j == je) {
@@ -479,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_prefill_kernel(const __gr
                         ok = tma::wait_warp(&sm.pv_done[g], (sp - 1) & 1);
                         if (!ok) break;
                         tc::fence_after_sync();
-                        fold_o(kept, o_addr, m_ref, c, j == kFold, j == nt);
+                        const float2 lk = upk2(l);
+                        const float all = fold_o(kept, o_addr, lk.x + lk.y, m_ref, c, j == kFold, j == nt);
+                        l = pk2(j == nt ? all : 0.f, 0.f);
                     }
                     if (j == nt) break;
                     je = min(nt, j + kFold);
