@@ -509,6 +509,75 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
                    const int32_t *cache_lens, int32_t num_seqs, int32_t num_heads, int32_t num_tokens, float scale,
                    uint16_t *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
 
+/* ---------------------------------------------------------------------------------
+ * The same cache in 8 bits: 644 bytes a token instead of 1152.
+ *
+ * A token's row is KDA_MLA_ROW_FP8 = 640 bytes: its 512 latent values in e4m3, then its 64
+ * positional ones in bf16, both in units of the row's own scale s = 2^e (fp32): e is the least
+ * integer of -40 .. 40 for which the row's largest |latent| is at most 448 s, the largest value
+ * of the type (0 for a row of zeros). Each latent is rounded once, from fp32 to the nearest
+ * e4m3; the scale being a power of two, the positional key is its bf16 rounding, and reading
+ * a row back is exact. The scale is a token's own, since tokens are written one at a time:
+ * a larger one that comes later leaves the written ones as they are.
+ *
+ * A page of page_size rows (a multiple of 16, at most 65536) is page_size * 640 bytes of rows,
+ * then page_size fp32 scales: page_size * KDA_MLA_TOKEN_FP8 bytes, a multiple of 16, at byte
+ * p * page_stride; page_stride counts bytes, is a multiple of 16 and at least that. Page
+ * tables, lengths, 'status' and bad tables are as above, and kda_pages_copy() moves these pages
+ * like any others.
+ * --------------------------------------------------------------------------------- */
+#define KDA_MLA_ROW_FP8 640   /* bytes of a row, its scale apart */
+#define KDA_MLA_TOKEN_FP8 644 /* bytes of a token */
+
+/*
+ * kda_mla_append_fp8 - kda_mla_append() into the 8-bit cache: the same normalisation and
+ * rotation in fp32, then the row's scale and its rounding as above. Arguments as there, but
+ * for cache: device bytes, written.
+ *
+ * Latents past 448 * 2^40 are held as that; a NaN stays one (and counts for nothing in the
+ * scale); a positional value past bf16's range in units of s becomes infinite.
+ */
+int kda_mla_append_fp8(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64_t k_pe_stride,
+                       const float *norm_w, float eps, const float *rope, int32_t rope_len, int32_t rope_interleaved,
+                       const uint16_t *q_pe, int64_t q_token_stride, int64_t q_head_stride,
+                       uint16_t *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t num_heads,
+                       const int32_t *cu_seqlens, const int32_t *cache_lens, const int32_t *page_table, int32_t max_pages,
+                       uint8_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
+                       int64_t total_tokens, int32_t num_seqs, int32_t *status, void *stream);
+
+/*
+ * kda_mla_gather_fp8 - rows of the 8-bit cache as dense bf16 rows, the values that they stand
+ * for: out row cu_seqlens[n] + i is row starts[n] + i of sequence n.
+ *
+ *   cu_seqlens device int32 [num_seqs + 1]; starts device int32 [num_seqs], the first row to
+ *             read of each sequence, or NULL for 0 (a long prefix is expanded a window at a time)
+ *   page_table device int32 [num_seqs, max_pages]; out device bf16 [total_rows, 576]
+ * Rows of out outside every sequence's range are left as they were; a row that is negative, past
+ * the page table or in a bad page becomes NaN and sets 'status'.
+ */
+int kda_mla_gather_fp8(const uint8_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
+                       const int32_t *cu_seqlens, const int32_t *starts, const int32_t *page_table, int32_t max_pages,
+                       uint16_t *out, int64_t total_rows, int32_t num_seqs, int32_t *status, void *stream);
+
+/* Bytes of device workspace for kda_mla_decode_fp8() with these sizes (a bound that depends
+ * on them alone); 0 for a negative argument. */
+size_t kda_mla_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens);
+
+/*
+ * kda_mla_decode_fp8 - kda_mla_decode() over the 8-bit cache:
+ *
+ *   s_rj = scale s_j (q_lat_r . c_j + q_pe_r . p_j),   o_r = sum_j softmax(s_r)_j s_j c_j
+ *
+ * with c_j, p_j the stored values and s_j their scale. Arguments, windows, empty rows, bad tables
+ * and the order of calls that share a workspace are as there, but for
+ *   cache     device bytes
+ *   workspace kda_mla_decode_fp8_workspace_size() bytes, 256-byte aligned
+ */
+int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_t *cache, int64_t page_stride,
+                       int32_t num_pages, int32_t page_size, const int32_t *page_table, int32_t max_pages,
+                       const int32_t *cache_lens, int32_t num_seqs, int32_t num_heads, int32_t num_tokens, float scale,
+                       uint16_t *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
 /*
  * kda_pages_copy - copy pages of a pool in every layer: the device side of forking a
  * sequence (its last page, and its KDA state slot) and of compacting a cache.

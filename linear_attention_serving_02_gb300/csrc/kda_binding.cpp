@@ -55,7 +55,7 @@ const at::Tensor &need(PyObject *o, const char *name, at::ScalarType type, int64
 void shape(const at::Tensor &t, const char *name, std::initializer_list<int64_t> want) {
     TORCH_CHECK_VALUE(t.sizes() == at::IntArrayRef(want), name, " must be ", at::IntArrayRef(want), ", got ", t.sizes());
 }
-constexpr at::ScalarType kBf = at::kBFloat16, kF = at::kFloat, kI = at::kInt;
+constexpr at::ScalarType kBf = at::kBFloat16, kF = at::kFloat, kI = at::kInt, kByte = at::kByte;
 
 const int32_t *ints(PyObject *o, const char *name, int64_t n, int dev) {
     const at::Tensor &t = need(o, name, kI, 1, 1, dev);
@@ -70,6 +70,7 @@ int32_t *status_word(PyObject *o, int dev) {
 }
 const uint16_t *bf(const at::Tensor &t) { return static_cast<const uint16_t *>(t.const_data_ptr()); }
 uint16_t *bf_out(const at::Tensor &t) { return static_cast<uint16_t *>(t.data_ptr()); }
+uint8_t *bytes(const at::Tensor &t) { return static_cast<uint8_t *>(t.data_ptr()); }
 const float *f32(const at::Tensor &t) { return static_cast<const float *>(t.const_data_ptr()); }
 
 int64_t whole(PyObject *o, const char *name) {
@@ -112,15 +113,17 @@ struct Cache {
     int32_t pages, size, max_pages;
     const int32_t *table;
 };
-Cache paged(PyObject *cache, PyObject *page_table, int64_t seqs, int dev) {
+// type: kBf, or kByte for the cache in 8 bits
+Cache paged(PyObject *cache, at::ScalarType type, PyObject *page_table, int64_t seqs, int dev) {
     Cache c;
-    c.t = &need(cache, "cache", kBf, 3, 2, dev);
-    TORCH_CHECK_VALUE(c.t->size(2) == KDA_MLA_ROW, "cache must be [num_pages, page_size, ", KDA_MLA_ROW, "]");
+    const int64_t token = type == kBf ? KDA_MLA_ROW : KDA_MLA_TOKEN_FP8;
+    c.t = &need(cache, "cache", type, 3, 2, dev);
+    TORCH_CHECK_VALUE(c.t->size(2) == token, "cache must be [num_pages, page_size, ", token, "]");
     const at::Tensor &table = need(page_table, "page_table", kI, 2, 2, c.t->device().index());
     TORCH_CHECK_VALUE(table.size(0) == seqs, "page_table must have a row for each of ", seqs, " sequences");
     c.pages = extent(c.t->size(0), "the number of pages");
     c.size = extent(c.t->size(1), "the page size");
-    c.stride = c.pages > 1 ? c.t->stride(0) : (int64_t)c.size * KDA_MLA_ROW;
+    c.stride = c.pages > 1 ? c.t->stride(0) : (int64_t)c.size * token;
     c.max_pages = extent(table.size(1), "the page table");
     c.table = static_cast<const int32_t *>(table.const_data_ptr());
     return c;
@@ -139,9 +142,8 @@ bool args(Py_ssize_t n, Py_ssize_t want, const char *fn) {
     return false;
 }
 
-PyObject *mla_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    if (!args(n, 13, "mla_append")) return nullptr;
+// both forms of append: the cache in bf16 or in 8 bits
+PyObject *append(bool fp8, PyObject *const *a) {
     const at::Tensor &c = need(a[0], "c", kBf, 2, 1, -1);
     const int dev = c.device().index();
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
@@ -151,7 +153,7 @@ PyObject *mla_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     shape(k_pe, "k_pe", {T, KDA_MLA_POS});
     const at::Tensor &lens = need(a[4], "cache_lens", kI, 1, 1, dev);
     const int64_t N = lens.size(0);
-    const Cache cache = paged(a[2], a[3], N, dev);
+    const Cache cache = paged(a[2], fp8 ? kByte : kBf, a[3], N, dev);
     const int32_t *cu = a[5] == Py_None ? nullptr : ints(a[5], "cu_seqlens", N + 1, dev);
     const float *norm_w = nullptr, *rope = nullptr;
     int32_t rope_len = 0;
@@ -187,14 +189,25 @@ PyObject *mla_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
         TORCH_CHECK_VALUE(a[11] == Py_None, "q_out needs q_pe");
     }
-    const int rc = kda_mla_append(bf(c), row_stride(c, KDA_MLA_LATENT), bf(k_pe), row_stride(k_pe, KDA_MLA_POS), norm_w,
-                                  real(a[7], "eps"), rope, rope_len, truth(a[9], "rope_interleaved"), qp, qs[0], qs[1],
-                                  qo, qos[0], qos[1], H, cu, static_cast<const int32_t *>(lens.const_data_ptr()),
-                                  cache.table, cache.max_pages, bf_out(*cache.t), cache.stride, cache.pages, cache.size,
-                                  T, extent(N, "the number of sequences"), status_word(a[12], dev), stream_of(dev));
-    if (rc != KDA_OK) return fail("kda_mla_append", rc);
+    auto call = [&](auto *fn, auto *rows) {
+        return fn(bf(c), row_stride(c, KDA_MLA_LATENT), bf(k_pe), row_stride(k_pe, KDA_MLA_POS), norm_w, real(a[7], "eps"),
+                  rope, rope_len, truth(a[9], "rope_interleaved"), qp, qs[0], qs[1], qo, qos[0], qos[1], H, cu,
+                  static_cast<const int32_t *>(lens.const_data_ptr()), cache.table, cache.max_pages, rows, cache.stride,
+                  cache.pages, cache.size, T, extent(N, "the number of sequences"), status_word(a[12], dev), stream_of(dev));
+    };
+    const int rc = fp8 ? call(kda_mla_append_fp8, bytes(*cache.t)) : call(kda_mla_append, bf_out(*cache.t));
+    if (rc != KDA_OK) return fail(fp8 ? "kda_mla_append_fp8" : "kda_mla_append", rc);
     if (!qo && !q_out.defined()) Py_RETURN_NONE;
     return a[11] == Py_None ? THPVariable_Wrap(std::move(q_out)) : Py_NewRef(a[11]);
+}
+PyObject *mla_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return args(n, 13, "mla_append") ? append(false, a) : nullptr;
+    END_HANDLE_TH_ERRORS
+}
+PyObject *mla_append_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return args(n, 13, "mla_append_fp8") ? append(true, a) : nullptr;
     END_HANDLE_TH_ERRORS
 }
 
@@ -205,7 +218,7 @@ PyObject *mla_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int dev = first.device().index();
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
     const int64_t N = need(a[1], "page_table", kI, 2, 2, dev).size(0), T = whole(a[3], "total_rows");
-    const Cache cache = paged(a[0], a[1], N, dev);
+    const Cache cache = paged(a[0], kBf, a[1], N, dev);
     const int32_t *cu = ints(a[2], "cu_seqlens", N + 1, dev);
     TORCH_CHECK_VALUE(T >= 0, "total_rows must not be negative");
     at::Tensor out = a[4] == Py_None ? fresh({T, KDA_MLA_ROW}, kBf, dev) : need(a[4], "out", kBf, 2, 2, dev);
@@ -214,6 +227,27 @@ PyObject *mla_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                   bf_out(out), T, extent(N, "the number of sequences"), status_word(a[5], dev), stream_of(dev));
     if (rc != KDA_OK) return fail("kda_mla_gather", rc);
     return a[4] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[4]);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *mla_gather_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!args(n, 7, "mla_gather_fp8")) return nullptr;
+    const at::Tensor &first = need(a[0], "cache", kByte, 3, 2, -1);
+    const int dev = first.device().index();
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const int64_t N = need(a[1], "page_table", kI, 2, 2, dev).size(0), T = whole(a[3], "total_rows");
+    const Cache cache = paged(a[0], kByte, a[1], N, dev);
+    const int32_t *cu = ints(a[2], "cu_seqlens", N + 1, dev);
+    const int32_t *starts = a[4] == Py_None ? nullptr : ints(a[4], "starts", N, dev);
+    TORCH_CHECK_VALUE(T >= 0, "total_rows must not be negative");
+    at::Tensor out = a[5] == Py_None ? fresh({T, KDA_MLA_ROW}, kBf, dev) : need(a[5], "out", kBf, 2, 2, dev);
+    shape(out, "out", {T, KDA_MLA_ROW});
+    const int rc = kda_mla_gather_fp8(bytes(first), cache.stride, cache.pages, cache.size, cu, starts, cache.table,
+                                      cache.max_pages, bf_out(out), T, extent(N, "the number of sequences"),
+                                      status_word(a[6], dev), stream_of(dev));
+    if (rc != KDA_OK) return fail("kda_mla_gather_fp8", rc);
+    return a[5] == Py_None ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a[5]);
     END_HANDLE_TH_ERRORS
 }
 
@@ -257,9 +291,8 @@ PyObject *mla_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-PyObject *mla_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    if (!args(n, 11, "mla_decode")) return nullptr;
+// both forms of decode: the cache in bf16 or in 8 bits
+PyObject *decode(bool fp8, PyObject *const *a) {
     const at::Tensor &q_lat = need(a[0], "q_lat", kBf, 3, 3, -1);
     const int dev = q_lat.device().index();
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
@@ -270,7 +303,7 @@ PyObject *mla_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     shape(q_lat, "q_lat", {rows, H, KDA_MLA_LATENT});
     const at::Tensor &q_pe = need(a[1], "q_pe", kBf, 3, 3, dev);
     shape(q_pe, "q_pe", {rows, H, KDA_MLA_POS});
-    const Cache cache = paged(a[2], a[3], N, dev);
+    const Cache cache = paged(a[2], fp8 ? kByte : kBf, a[3], N, dev);
     at::Tensor o = a[7] == Py_None ? fresh({rows, H, KDA_MLA_LATENT}, kBf, dev) : need(a[7], "o", kBf, 3, 3, dev);
     at::Tensor lse = a[8] == Py_None ? fresh({rows, H}, kF, dev) : need(a[8], "lse", kF, 2, 2, dev);
     shape(o, "o", {rows, H, KDA_MLA_LATENT});
@@ -278,18 +311,30 @@ PyObject *mla_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int32_t n32 = extent(N, "the number of sequences"), h32 = extent(H, "the number of heads");
     at::Tensor ws;
     if (a[9] == Py_None) {
-        ws = fresh({(int64_t)kda_mla_decode_workspace_size(n32, h32, m)}, at::kByte, dev);
+        const size_t need = fp8 ? kda_mla_decode_fp8_workspace_size(n32, h32, m) : kda_mla_decode_workspace_size(n32, h32, m);
+        ws = fresh({(int64_t)need}, kByte, dev);
     } else {
         ws = tensor(a[9], "workspace");
         TORCH_CHECK_VALUE(ws.is_cuda() && ws.device().index() == dev && ws.is_contiguous(),
                           "workspace must be contiguous and on cuda:", dev);
     }
-    const int rc = kda_mla_decode(bf(q_lat), bf(q_pe), bf(*cache.t), cache.stride, cache.pages, cache.size, cache.table,
-                                  cache.max_pages, static_cast<const int32_t *>(lens.const_data_ptr()), n32, h32, m,
-                                  real(a[5], "scale"), bf_out(o), static_cast<float *>(lse.data_ptr()), ws.data_ptr(),
-                                  ws.nbytes(), status_word(a[10], dev), stream_of(dev));
-    if (rc != KDA_OK) return fail("kda_mla_decode", rc);
+    auto call = [&](auto *fn, const auto *rows) {
+        return fn(bf(q_lat), bf(q_pe), rows, cache.stride, cache.pages, cache.size, cache.table, cache.max_pages,
+                  static_cast<const int32_t *>(lens.const_data_ptr()), n32, h32, m, real(a[5], "scale"), bf_out(o),
+                  static_cast<float *>(lse.data_ptr()), ws.data_ptr(), ws.nbytes(), status_word(a[10], dev), stream_of(dev));
+    };
+    const int rc = fp8 ? call(kda_mla_decode_fp8, bytes(*cache.t)) : call(kda_mla_decode, bf(*cache.t));
+    if (rc != KDA_OK) return fail(fp8 ? "kda_mla_decode_fp8" : "kda_mla_decode", rc);
     return pair(std::move(o), a[7], std::move(lse), a[8]);
+}
+PyObject *mla_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return args(n, 11, "mla_decode") ? decode(false, a) : nullptr;
+    END_HANDLE_TH_ERRORS
+}
+PyObject *mla_decode_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return args(n, 11, "mla_decode_fp8") ? decode(true, a) : nullptr;
     END_HANDLE_TH_ERRORS
 }
 
@@ -371,6 +416,9 @@ PyMethodDef g_methods[] = {{"mla_append", fast(mla_append), METH_FASTCALL, nullp
                            {"mla_gather", fast(mla_gather), METH_FASTCALL, nullptr},
                            {"mla_prefill", fast(mla_prefill), METH_FASTCALL, nullptr},
                            {"mla_decode", fast(mla_decode), METH_FASTCALL, nullptr},
+                           {"mla_append_fp8", fast(mla_append_fp8), METH_FASTCALL, nullptr},
+                           {"mla_gather_fp8", fast(mla_gather_fp8), METH_FASTCALL, nullptr},
+                           {"mla_decode_fp8", fast(mla_decode_fp8), METH_FASTCALL, nullptr},
                            {"pages_copy", fast(pages_copy), METH_FASTCALL, nullptr},
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

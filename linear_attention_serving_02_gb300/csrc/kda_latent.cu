@@ -27,6 +27,8 @@ constexpr int kHeadsPerItem = 16;
 constexpr int kGatherRows = 4;
 constexpr int kRowUnits = kRow * 2 / 16;  // 16-byte units of a row: 72
 
+// T: the cache's elements, bf16 values or the bytes of its 8-bit form
+template <typename T>
 struct AppendArgs {
     const __nv_bfloat16 *c, *k_pe;
     int64_t c_stride, k_pe_stride;
@@ -40,8 +42,8 @@ struct AppendArgs {
     int64_t qo_ts, qo_hs;
     int32_t H;  // 0 without queries
     const int32_t *cu, *lens;
-    PagedRows<__nv_bfloat16> cache;
-    int64_t T;
+    PagedRows<T> cache;
+    int64_t tokens;
     int32_t N;
     int64_t per_seq;  // tokens of each sequence without cu
     int32_t *status;
@@ -101,17 +103,32 @@ __device__ __forceinline__ PosPiece rotate(const PosPiece &v, const float (&c)[8
     }
     return PosPiece{pack8(x), pack8(y)};
 }
+// eight bf16 values times a power of two
+__device__ __forceinline__ uint4 scaled8(const uint4 &u, float by) {
+    float x[8];
+    unpack8(u, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= by;
+    return pack8(x);
+}
+// eight values times a power of two, each rounded to the nearest e4m3
+__device__ __forceinline__ uint2 e4m3_of8(const float (&x)[8], float by) {
+    return make_uint2(e4m3_of2(x[0] * by, x[1] * by) | (e4m3_of2(x[2] * by, x[3] * by) << 16),
+                      e4m3_of2(x[4] * by, x[5] * by) | (e4m3_of2(x[6] * by, x[7] * by) << 16));
+}
 __device__ __forceinline__ void load8(float (&x)[8], const float *p) {
     *reinterpret_cast<float4 *>(&x[0]) = *reinterpret_cast<const float4 *>(p);
     *reinterpret_cast<float4 *>(&x[4]) = *reinterpret_cast<const float4 *>(p + 4);
 }
 
-__global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __grid_constant__ AppendArgs p) {
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __grid_constant__ AppendArgs<T> p) {
+    constexpr bool kBits8 = sizeof(T) == 1;
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int part = blockIdx.y;
     pdl_wait();
-    if (t >= p.T) return;
+    if (t >= p.tokens) return;
 
     // the loads that need no position first
     uint4 lo, hi;
@@ -159,12 +176,15 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
     }
 
     if (part == 0 && good) {
-        __nv_bfloat16 *row =
-            p.cache.rows + page * p.cache.page_stride + (int64_t)((uint32_t)pos - entry * (uint32_t)p.cache.page_size) * kRow;
-        if (p.norm_w) {
-            float x[8], y[8], w[8];
+        T *page_at = p.cache.rows + page * p.cache.page_stride;
+        const uint32_t r_in_page = (uint32_t)pos - entry * (uint32_t)p.cache.page_size;
+        float x[8], y[8];
+        if (kBits8 || p.norm_w) {
             unpack8(lo, x);
             unpack8(hi, y);
+        }
+        if (p.norm_w) {
+            float w[8];
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
@@ -174,15 +194,41 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
             load8(w, p.norm_w + 8 * lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-            lo = pack8(x);
             load8(w, p.norm_w + 256 + 8 * lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-            hi = pack8(y);
         }
-        *reinterpret_cast<uint4 *>(row + 8 * lane) = lo;
-        *reinterpret_cast<uint4 *>(row + 256 + 8 * lane) = hi;
-        if (lane < 4) store_pos(row + kLatent, j, il, p.rope ? rotate(k_pe, co, si, il) : k_pe);
+        if constexpr (kBits8) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(x[i]), fabsf(y[i])));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const int e = scale_exponent(top);
+            const float inv = exp2_of(-e);
+            uint8_t *row = page_at + (int64_t)r_in_page * kRow8;
+            *reinterpret_cast<uint2 *>(row + 8 * lane) = e4m3_of8(x, inv);
+            *reinterpret_cast<uint2 *>(row + 256 + 8 * lane) = e4m3_of8(y, inv);
+            if (lane < 4) {
+                __nv_bfloat16 *at = reinterpret_cast<__nv_bfloat16 *>(row + kLatent);
+                if (p.rope) {  // a power of two: the angles' products may take it
+                    float cs[8], ss[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) cs[i] = co[i] * inv, ss[i] = si[i] * inv;
+                    store_pos(at, j, il, rotate(k_pe, cs, ss, il));
+                } else {
+                    store_pos(at, j, il, PosPiece{scaled8(k_pe.a, inv), scaled8(k_pe.b, inv)});
+                }
+            }
+            if (lane == 0)
+                *reinterpret_cast<float *>(page_at + (int64_t)p.cache.page_size * kRow8 + 4 * r_in_page) = exp2_of(e);
+        } else {
+            __nv_bfloat16 *row = page_at + (int64_t)r_in_page * kRow;
+            if (p.norm_w) lo = pack8(x), hi = pack8(y);
+            *reinterpret_cast<uint4 *>(row + 8 * lane) = lo;
+            *reinterpret_cast<uint4 *>(row + 256 + 8 * lane) = hi;
+            if (lane < 4) store_pos(row + kLatent, j, il, p.rope ? rotate(k_pe, co, si, il) : k_pe);
+        }
     }
     const uint4 nan4 = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
 #pragma unroll
@@ -236,20 +282,84 @@ __global__ void __launch_bounds__(kRowThreads)
         if (there[k]) reinterpret_cast<uint4 *>(out + t0 * kRow)[k * 32 + lane] = v[k];
 }
 
-}  // namespace
-}  // namespace kda
+// four e4m3 values (a 32-bit word) times s, as two words of bf16 pairs
+__device__ __forceinline__ uint2 bf16_of4(uint32_t v, float s) {
+    const float2 a = values_of2(v), b = values_of2(v >> 16);
+    return make_uint2(pack2(a.x * s, a.y * s), pack2(b.x * s, b.y * s));
+}
 
-extern "C" {
+__global__ void __launch_bounds__(kRowThreads)
+    kda_mla_gather_fp8_kernel(const PagedRows<const uint8_t> cache, const int32_t *cu, const int32_t *starts, int32_t N,
+                              int64_t T, __nv_bfloat16 *out, int32_t *status) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kGatherRows;
+    pdl_wait();
+    if (t0 >= T) return;
+    const uint8_t *src[kGatherRows];
+    const float *scale_at[kGatherRows];
+    unsigned nan_rows = 0;
+    int n = warp_find_seq(cu, N, t0);
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        const int64_t t = t0 + r;
+        src[r] = nullptr;
+        scale_at[r] = nullptr;
+        while (n + 1 < N && t >= cu[n + 1]) ++n;  // empty sequences are stepped over
+        if (n < 0 || t >= T || t >= cu[n + 1] || t < cu[n]) continue;
+        const int64_t i = t - cu[n] + (starts ? starts[n] : 0);
+        const bool there = i >= 0 && i < (int64_t)cache.max_pages * cache.page_size;
+        const uint32_t entry = there ? (uint32_t)i / (uint32_t)cache.page_size : 0;
+        const int32_t page = there ? cache.table[(int64_t)n * cache.max_pages + entry] : -1;
+        if (page < 0 || page >= cache.num_pages) {
+            nan_rows |= 1u << r;
+            if (lane == 0) set_status(status, there ? KDA_ERR_PAGES : KDA_ERR_SEQLENS);
+            continue;
+        }
+        const uint8_t *at = cache.rows + page * cache.page_stride;
+        const uint32_t in_page = (uint32_t)i - entry * (uint32_t)cache.page_size;
+        src[r] = at + (int64_t)in_page * kRow8;
+        scale_at[r] = reinterpret_cast<const float *>(at + (int64_t)cache.page_size * kRow8) + in_page;
+    }
+    // a row's latents are 32 units of 16 bytes, its positional key eight: lane l takes latent unit l of every
+    // row and unit l % 8 of row l / 8's positional key
+    uint4 v[kGatherRows], pe = make_uint4(0, 0, 0, 0);
+    float s[kGatherRows];
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        v[r] = make_uint4(0, 0, 0, 0);
+        s[r] = ((nan_rows >> r) & 1) ? __uint_as_float(0x7fffffffu) : 1.f;
+        if (src[r]) {
+            v[r] = *reinterpret_cast<const uint4 *>(src[r] + 16 * lane);
+            s[r] = *scale_at[r];
+        }
+    }
+    const int pr = lane >> 3;
+    const uint8_t *ps = pr == 0 ? src[0] : (pr == 1 ? src[1] : (pr == 2 ? src[2] : src[3]));
+    if (ps) pe = *reinterpret_cast<const uint4 *>(ps + kLatent + 16 * (lane & 7));
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        if (!src[r] && !((nan_rows >> r) & 1)) continue;
+        const uint2 a = bf16_of4(v[r].x, s[r]), b = bf16_of4(v[r].y, s[r]), c = bf16_of4(v[r].z, s[r]), d = bf16_of4(v[r].w, s[r]);
+        uint4 *dst = reinterpret_cast<uint4 *>(out + (t0 + r) * kRow) + 2 * lane;
+        dst[0] = make_uint4(a.x, a.y, b.x, b.y);
+        dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+    }
+    if (ps || ((nan_rows >> pr) & 1)) {
+        const float sp = pr == 0 ? s[0] : (pr == 1 ? s[1] : (pr == 2 ? s[2] : s[3]));
+        reinterpret_cast<uint4 *>(out + (t0 + pr) * kRow + kLatent)[lane & 7] = scaled8(pe, sp);
+    }
+}
 
-int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64_t k_pe_stride,
-                   const float *norm_w, float eps, const float *rope, int32_t rope_len, int32_t rope_interleaved,
-                   const uint16_t *q_pe, int64_t q_token_stride, int64_t q_head_stride, uint16_t *q_out,
-                   int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t num_heads,
-                   const int32_t *cu_seqlens, const int32_t *cache_lens, const int32_t *page_table, int32_t max_pages,
-                   uint16_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size, int64_t total_tokens,
-                   int32_t num_seqs, int32_t *status, void *stream) {
-    using namespace kda;
-    int rc = check_cache(page_stride, num_pages, page_size, max_pages);
+// The checks and the launch of both forms of append.
+template <typename T>
+int append_call(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64_t k_pe_stride,
+                const float *norm_w, float eps, const float *rope, int32_t rope_len, int32_t rope_interleaved,
+                const uint16_t *q_pe, int64_t q_token_stride, int64_t q_head_stride, uint16_t *q_out,
+                int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t num_heads, const int32_t *cu_seqlens,
+                const int32_t *cache_lens, const int32_t *page_table, int32_t max_pages, T *cache, int64_t page_stride,
+                int32_t num_pages, int32_t page_size, int64_t total_tokens, int32_t num_seqs, int32_t *status,
+                void *stream) {
+    const int rc = check_cache<T>(page_stride, num_pages, page_size, max_pages);
     if (rc != KDA_OK) return rc;
     if (!(eps >= 0.0f) || (rope_interleaved != 0 && rope_interleaved != 1)) return KDA_ERR_UNSUPPORTED;
     if ((q_pe != nullptr) != (q_out != nullptr) || (q_pe && !rope)) return KDA_ERR_UNSUPPORTED;
@@ -275,7 +385,7 @@ int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, in
         !mla_aligned(q_pe, 16) || !mla_aligned(q_out, 16) || !mla_aligned(cache, 16) || !mla_aligned(cu_seqlens, 4) ||
         !mla_aligned(cache_lens, 4) || !mla_aligned(page_table, 4) || !mla_aligned(status, 4))
         return KDA_ERR_ALIGN;
-    AppendArgs a{};
+    AppendArgs<T> a{};
     a.c = reinterpret_cast<const __nv_bfloat16 *>(c);
     a.k_pe = reinterpret_cast<const __nv_bfloat16 *>(k_pe);
     a.c_stride = c_stride;
@@ -294,24 +404,42 @@ int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, in
     a.H = q_pe ? num_heads : 0;
     a.cu = cu_seqlens;
     a.lens = cache_lens;
-    a.cache = {reinterpret_cast<__nv_bfloat16 *>(cache), page_stride, num_pages, page_size, page_table, max_pages};
-    a.T = total_tokens;
+    a.cache = {cache, page_stride, num_pages, page_size, page_table, max_pages};
+    a.tokens = total_tokens;
     a.N = num_seqs;
     a.per_seq = cu_seqlens ? 0 : total_tokens / num_seqs;
     a.status = status;
     const int64_t blocks = (total_tokens + kRowThreads / 32 - 1) / (kRowThreads / 32);
     const int parts = a.H > kHeadsPerItem ? (a.H + kHeadsPerItem - 1) / kHeadsPerItem : 1;
-    return launch_after(kda_mla_append_kernel, dim3((unsigned)blocks, (unsigned)parts), dim3(kRowThreads), 0,
+    return launch_after(kda_mla_append_kernel<T>, dim3((unsigned)blocks, (unsigned)parts), dim3(kRowThreads), 0,
                         static_cast<cudaStream_t>(stream), a) == cudaSuccess
                ? KDA_OK
                : KDA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+int kda_mla_append(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64_t k_pe_stride,
+                   const float *norm_w, float eps, const float *rope, int32_t rope_len, int32_t rope_interleaved,
+                   const uint16_t *q_pe, int64_t q_token_stride, int64_t q_head_stride, uint16_t *q_out,
+                   int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t num_heads,
+                   const int32_t *cu_seqlens, const int32_t *cache_lens, const int32_t *page_table, int32_t max_pages,
+                   uint16_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size, int64_t total_tokens,
+                   int32_t num_seqs, int32_t *status, void *stream) {
+    return kda::append_call(c, c_stride, k_pe, k_pe_stride, norm_w, eps, rope, rope_len, rope_interleaved, q_pe,
+                            q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, num_heads,
+                            cu_seqlens, cache_lens, page_table, max_pages, reinterpret_cast<__nv_bfloat16 *>(cache),
+                            page_stride, num_pages, page_size, total_tokens, num_seqs, status, stream);
 }
 
 int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
                    const int32_t *cu_seqlens, const int32_t *page_table, int32_t max_pages, uint16_t *out,
                    int64_t total_rows, int32_t num_seqs, int32_t *status, void *stream) {
     using namespace kda;
-    int rc = check_cache(page_stride, num_pages, page_size, max_pages);
+    int rc = check_cache<__nv_bfloat16>(page_stride, num_pages, page_size, max_pages);
     if (rc != KDA_OK) return rc;
     if (total_rows < 0 || total_rows > INT32_MAX || num_seqs < 0) return KDA_ERR_SHAPE;
     if (num_seqs == 0 || total_rows == 0) return KDA_OK;
@@ -325,6 +453,40 @@ int kda_mla_gather(const uint16_t *cache, int64_t page_stride, int32_t num_pages
                                             page_size, page_table, max_pages};
     return launch_after(kda_mla_gather_kernel, dim3(blocks), dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), pr,
                         cu_seqlens, num_seqs, total_rows, reinterpret_cast<__nv_bfloat16 *>(out), status) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+int kda_mla_append_fp8(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64_t k_pe_stride,
+                       const float *norm_w, float eps, const float *rope, int32_t rope_len, int32_t rope_interleaved,
+                       const uint16_t *q_pe, int64_t q_token_stride, int64_t q_head_stride, uint16_t *q_out,
+                       int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t num_heads,
+                       const int32_t *cu_seqlens, const int32_t *cache_lens, const int32_t *page_table,
+                       int32_t max_pages, uint8_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
+                       int64_t total_tokens, int32_t num_seqs, int32_t *status, void *stream) {
+    return kda::append_call(c, c_stride, k_pe, k_pe_stride, norm_w, eps, rope, rope_len, rope_interleaved, q_pe,
+                            q_token_stride, q_head_stride, q_out, q_out_token_stride, q_out_head_stride, num_heads,
+                            cu_seqlens, cache_lens, page_table, max_pages, cache, page_stride, num_pages, page_size,
+                            total_tokens, num_seqs, status, stream);
+}
+
+int kda_mla_gather_fp8(const uint8_t *cache, int64_t page_stride, int32_t num_pages, int32_t page_size,
+                       const int32_t *cu_seqlens, const int32_t *starts, const int32_t *page_table, int32_t max_pages,
+                       uint16_t *out, int64_t total_rows, int32_t num_seqs, int32_t *status, void *stream) {
+    using namespace kda;
+    int rc = check_cache<uint8_t>(page_stride, num_pages, page_size, max_pages);
+    if (rc != KDA_OK) return rc;
+    if (total_rows < 0 || total_rows > INT32_MAX || num_seqs < 0) return KDA_ERR_SHAPE;
+    if (num_seqs == 0 || total_rows == 0) return KDA_OK;
+    if (!cache || !cu_seqlens || !page_table || !out) return KDA_ERR_NULL;
+    if (!mla_aligned(cache, 16) || !mla_aligned(out, 16) || !mla_aligned(cu_seqlens, 4) || !mla_aligned(starts, 4) ||
+        !mla_aligned(page_table, 4) || !mla_aligned(status, 4))
+        return KDA_ERR_ALIGN;
+    const int64_t per_block = kGatherRows * (kRowThreads / 32);
+    const unsigned blocks = (unsigned)((total_rows + per_block - 1) / per_block);
+    const PagedRows<const uint8_t> pr{cache, page_stride, num_pages, page_size, page_table, max_pages};
+    return launch_after(kda_mla_gather_fp8_kernel, dim3(blocks), dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), pr,
+                        cu_seqlens, starts, num_seqs, total_rows, reinterpret_cast<__nv_bfloat16 *>(out), status) == cudaSuccess
                ? KDA_OK
                : KDA_ERR_CUDA;
 }

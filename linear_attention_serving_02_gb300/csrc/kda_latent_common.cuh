@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +19,8 @@ constexpr int kPos = KDA_MLA_POS;
 constexpr int kRow = KDA_MLA_ROW;
 constexpr int kNope = KDA_MLA_NOPE;
 constexpr int kQk = KDA_MLA_QK;
+constexpr int kRow8 = KDA_MLA_ROW_FP8;      // bytes of a row of the 8-bit form, its scale apart
+constexpr int kToken8 = KDA_MLA_TOKEN_FP8;  // with its scale
 
 // The kernels are launched so that they may come onto the GPU while the previous kernel on the
 // stream ends, and wait for its end (pdl_wait) before they touch memory (the decode's join says why
@@ -33,11 +36,34 @@ constexpr int kQk = KDA_MLA_QK;
 template <typename T>
 struct PagedRows {
     T *rows;
-    int64_t page_stride;  // elements
+    int64_t page_stride;  // elements of T
     int32_t num_pages, page_size;
     const int32_t *table;  // [num_seqs, max_pages]
     int32_t max_pages;
 };
+
+// ---- the 8-bit form: a row's latents are e4m3, its positional key bf16, both in units of 2^e ----
+
+// 2^e for e of -126 .. 127
+__device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
+// The exponent of a row's scale: the least e of -40 .. 40 with top 2^-e <= 448, the largest e4m3 value, and 0 for
+// a row of zeros. 448 is 1.75 2^8: what exceeds 1.75 carries into the exponent. An infinite top gives 40.
+__device__ __forceinline__ int scale_exponent(float top) {
+    const int e = (int)((__float_as_uint(top) + 0x1FFFFFu) >> 23) - 127 - 8;
+    return top == 0.f ? 0 : max(-40, min(40, e));
+}
+// two values rounded to the nearest e4m3 (a in the low byte); past 448 the nearest is 448, NaN stays NaN
+__device__ __forceinline__ uint32_t e4m3_of2(float a, float b) {
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
+    return v;
+}
+// the values of the two e4m3 in the low half of v
+__device__ __forceinline__ float2 values_of2(uint32_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
 
 // Store a status code in the caller's word (the first bad call wins the race or the last;
 // both are true, and nothing reads it here).
@@ -69,10 +95,12 @@ __device__ __forceinline__ int warp_find_seq(const int32_t *cu, int N, int64_t t
 // ---- host side ----
 inline bool mla_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// The cache's geometry (its pointers apart): KDA_OK, KDA_ERR_UNSUPPORTED or KDA_ERR_SHAPE.
+// The cache's geometry (its pointers apart), T its elements: KDA_OK, KDA_ERR_UNSUPPORTED or KDA_ERR_SHAPE.
+template <typename T>
 inline int check_cache(int64_t page_stride, int32_t num_pages, int32_t page_size, int32_t max_pages) {
     if (page_size <= 0 || page_size % 16 != 0 || page_size > 65536) return KDA_ERR_UNSUPPORTED;
-    if (num_pages < 0 || max_pages < 0 || page_stride < (int64_t)page_size * kRow || page_stride % 8 != 0)
+    constexpr int per_token = sizeof(T) == 1 ? kToken8 : kRow, unit = 16 / sizeof(T);
+    if (num_pages < 0 || max_pages < 0 || page_stride < (int64_t)page_size * per_token || page_stride % unit != 0)
         return KDA_ERR_SHAPE;
     if (page_stride > (INT64_MAX >> 2) / (num_pages > 0 ? num_pages : 1)) return KDA_ERR_SHAPE;
     if ((int64_t)max_pages * page_size > INT32_MAX) return KDA_ERR_SHAPE;  // positions are int32

@@ -923,7 +923,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
                    const int32_t *cache_lens, int32_t num_seqs, int32_t num_heads, int32_t num_tokens, float scale,
                    uint16_t *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *status, void *stream) {
     using namespace kda;
-    int rc = check_cache(page_stride, num_pages, page_size, max_pages);
+    int rc = check_cache<__nv_bfloat16>(page_stride, num_pages, page_size, max_pages);
     if (rc != KDA_OK) return rc;
     if (!(scale > 0.0f) || scale > 3.402823466e38f || num_tokens > KDA_MAX_REPLAY_TOKENS) return KDA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_heads <= 0 || num_tokens < 0 || num_heads > 65535 ||

@@ -77,6 +77,14 @@ def library():
         lib.kda_mla_decode.argtypes = [vp, vp, vp, i64, i32, i32, vp, i32, vp, i32, i32, i32, f32, vp, vp, vp,
                                        ctypes.c_size_t, vp, vp]
         lib.kda_mla_decode.restype = ctypes.c_int
+        lib.kda_mla_append_fp8.argtypes = lib.kda_mla_append.argtypes
+        lib.kda_mla_append_fp8.restype = ctypes.c_int
+        lib.kda_mla_gather_fp8.argtypes = [vp, i64, i32, i32, vp, vp, vp, i32, vp, i64, i32, vp, vp]
+        lib.kda_mla_gather_fp8.restype = ctypes.c_int
+        lib.kda_mla_decode_fp8_workspace_size.argtypes = [i32, i32, i32]
+        lib.kda_mla_decode_fp8_workspace_size.restype = ctypes.c_size_t
+        lib.kda_mla_decode_fp8.argtypes = lib.kda_mla_decode.argtypes
+        lib.kda_mla_decode_fp8.restype = ctypes.c_int
         lib.kda_pages_copy.argtypes = [vp, i64, i64, i32, i64, i32, vp, vp, i32, vp]
         lib.kda_pages_copy.restype = ctypes.c_int
         _LIB = lib
@@ -355,6 +363,7 @@ def kda_debug_walk_fault(skip_commit_chunk, wait_limit_ns):
 # These calls are a few microseconds long and a decode step makes several, so their checks and
 # marshalling are compiled (csrc/kda_binding.cpp); what stands here is their signatures.
 MLA_LATENT, MLA_POS, MLA_ROW, MLA_NOPE, MLA_QK = 512, 64, 576, 128, 192
+MLA_ROW_FP8, MLA_TOKEN_FP8 = 640, 644  # bytes of a row in 8 bits, without and with its scale
 
 _BINDING = None
 
@@ -444,6 +453,45 @@ def kda_mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens
                                   status)
     return (_BINDING or binding()).mla_decode(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse,
                                               workspace, status)
+
+
+def kda_mla_append_fp8(c, k_pe, cache, page_table, cache_lens, cu_seqlens=None, norm_w=None, eps=1e-6, rope=None,
+                       rope_interleaved=False, q_pe=None, q_out=None, status=None, stream=None):
+    """kda_mla_append into a cache in 8 bits: each row's latents are rounded to e4m3 in units of a power of
+    two of their own (include/kda.h). cache: uint8 [num_pages, page_size, 644], written: a page's rows of
+    640 bytes, then its fp32 scales; the other arguments as there. Returns q_out, or None."""
+    if stream is not None:
+        with _on(stream, c):
+            return kda_mla_append_fp8(c, k_pe, cache, page_table, cache_lens, cu_seqlens, norm_w, eps, rope,
+                                      rope_interleaved, q_pe, q_out, status)
+    return (_BINDING or binding()).mla_append_fp8(c, k_pe, cache, page_table, cache_lens, cu_seqlens, norm_w, eps, rope,
+                                                  rope_interleaved, q_pe, q_out, status)
+
+
+def kda_mla_gather_fp8(cache, page_table, cu_seqlens, total_rows, starts=None, out=None, status=None, stream=None):
+    """Rows of the cache in 8 bits as dense rows of the values that they stand for: out row cu_seqlens[n] + i is
+    row starts[n] + i of sequence n. cu_seqlens: int32 [N + 1] of the numbers of rows to read; starts: int32 [N],
+    or None for the first rows. Returns out, bf16 [total_rows, 576]."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_mla_gather_fp8(cache, page_table, cu_seqlens, total_rows, starts, out, status)
+    return (_BINDING or binding()).mla_gather_fp8(cache, page_table, cu_seqlens, total_rows, starts, out, status)
+
+
+def kda_mla_decode_fp8_workspace_size(num_seqs, num_heads, num_tokens=1):
+    return int(library().kda_mla_decode_fp8_workspace_size(int(num_seqs), int(num_heads), int(num_tokens)))
+
+
+def kda_mla_decode_fp8(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens=1, o=None, lse=None,
+                       workspace=None, status=None, stream=None):
+    """kda_mla_decode over a cache in 8 bits, uint8 [num_pages, page_size, 644]; the other arguments as there,
+    the workspace of kda_mla_decode_fp8_workspace_size bytes. Returns (o, lse)."""
+    if stream is not None:
+        with _on(stream, q_lat):
+            return kda_mla_decode_fp8(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse, workspace,
+                                      status)
+    return (_BINDING or binding()).mla_decode_fp8(q_lat, q_pe, cache, page_table, cache_lens, scale, num_tokens, o, lse,
+                                                  workspace, status)
 
 
 def _page_ids(ids, name):
