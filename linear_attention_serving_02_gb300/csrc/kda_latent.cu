@@ -179,11 +179,7 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
         T *page_at = p.cache.rows + page * p.cache.page_stride;
         const uint32_t r_in_page = (uint32_t)pos - entry * (uint32_t)p.cache.page_size;
         float x[8], y[8];
-        if (kBits8 || p.norm_w) {
-            unpack8(lo, x);
-            unpack8(hi, y);
-        }
-        if (p.norm_w) {
+        auto normalise = [&] {
             float w[8];
             float ss = 0.f;
 #pragma unroll
@@ -197,13 +193,16 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
             load8(w, p.norm_w + 256 + 8 * lane);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
-        }
+        };
         if constexpr (kBits8) {
+            unpack8(lo, x);
+            unpack8(hi, y);
+            if (p.norm_w) normalise();
             float top = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(x[i]), fabsf(y[i])));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // magnitudes are in the order of their bits
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
             const int e = scale_exponent(top);
             const float inv = exp2_of(-e);
             uint8_t *row = page_at + (int64_t)r_in_page * kRow8;
@@ -211,20 +210,21 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
             *reinterpret_cast<uint2 *>(row + 256 + 8 * lane) = e4m3_of8(y, inv);
             if (lane < 4) {
                 __nv_bfloat16 *at = reinterpret_cast<__nv_bfloat16 *>(row + kLatent);
-                if (p.rope) {  // a power of two: the angles' products may take it
-                    float cs[8], ss[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) cs[i] = co[i] * inv, ss[i] = si[i] * inv;
-                    store_pos(at, j, il, rotate(k_pe, cs, ss, il));
-                } else {
-                    store_pos(at, j, il, PosPiece{scaled8(k_pe.a, inv), scaled8(k_pe.b, inv)});
-                }
+                const PosPiece turned = p.rope ? rotate(k_pe, co, si, il) : k_pe;
+                // a power of two: the bf16 values stay what they are
+                store_pos(at, j, il, PosPiece{scaled8(turned.a, inv), scaled8(turned.b, inv)});
             }
             if (lane == 0)
                 *reinterpret_cast<float *>(page_at + (int64_t)p.cache.page_size * kRow8 + 4 * r_in_page) = exp2_of(e);
         } else {
             __nv_bfloat16 *row = page_at + (int64_t)r_in_page * kRow;
-            if (p.norm_w) lo = pack8(x), hi = pack8(y);
+            if (p.norm_w) {
+                unpack8(lo, x);
+                unpack8(hi, y);
+                normalise();
+                lo = pack8(x);
+                hi = pack8(y);
+            }
             *reinterpret_cast<uint4 *>(row + 8 * lane) = lo;
             *reinterpret_cast<uint4 *>(row + 256 + 8 * lane) = hi;
             if (lane < 4) store_pos(row + kLatent, j, il, p.rope ? rotate(k_pe, co, si, il) : k_pe);

@@ -1,99 +1,708 @@
 // Latent attention in the absorbed form over the pages of the 8-bit cache: kda_mla_decode_fp8.
 //
-//   s_rj = scale s_j (q_r . row_j),  o_r = sum_j e^{s_rj - M_r} s_j c_j / sum_j e^{s_rj - M_r}
+//   x_rj = log2(e) scale s_j (q_r . row_j),  o_r = sum_j 2^{x_rj} s_j c_j / sum_j 2^{x_rj}
 //
-// A warp takes a query row (one window token and head) and a part of its sequence's cached rows, each
-// lane 16 latents and 2 positional values; scores are warp reductions, the running maximum and sum are
-// kept in fp32. A second kernel joins the parts.
+// with c_j the stored latents and s_j = 2^e_j the row's scale. The work is cut as in the bf16 form: all cached
+// rows of the batch are one list of tiles of 64, cut into equal runs; a CTA takes a run for up to 96 query rows
+// (window token and head), and a second kernel joins the sequences that a run's border cuts.
+//
+// The products take the cache as it lies: e4m3, without unpacking. Their other operands have 16 bits, so each
+// is two 8-bit ones.
+//
+//   Scores. A query row in units of a power of two for which its largest latent is in (224, 448] is e4m3 hi and
+//   e4m3 lo of the rest: 4 bits and, with the rest's sign, 4 bits more are bf16's 8, so q is exact down to 2^-10 of
+//   the unit. Q is M (rows), the cached rows are N and are read K-major; with up to 64 query rows hi and lo
+//   are rows of one product, so that a tile is read once, with more two products. The positional part stays
+//   bf16 (the key is stored in units of s_j, so one accumulator takes both).
+//   Values. The weight w = 2^{x_rj + e_j - m_r} takes the row's scale along; it is e4m3 and, its rest, e5m2, whose
+//   range goes on 2^-7 further down. O^T = C^T W^T: M = 128 latents (the same tile, read MN-major), N = query rows.
+//
+// e4m3's range holds a weight to 2^-9 of the unit, so m_r follows the weights both ways: it is set 2^2.5 below a
+// tile's largest, and set anew, with O^T rescaled, where a tile's largest is over 2^8.75, or the largest of four
+// tiles under 2^-1. (A first token that outweighs all others would else leave these without bits. Four tiles
+// of low weights lose at most 4 64 2^-13 next to the 2^2.5 that set the unit, whatever they hold.) It stays within 2^40
+// of the largest seen, beyond which a tile counts for nothing.
+//
+// Rows of a tile behind the sequence's length may hold anything: their scores are replaced by -inf, the
+// product's 32-row steps past the length are left out, and value rows inside the last step are zeroed in shared
+// memory; their scales are never loaded.
 
-#include "kda_common.cuh"
-#include "kda_latent_common.cuh"
+#include "kda_latent_split.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8, kMaxParts = 64;
+constexpr uint32_t kChunk8 = kKvTile * 128;     // 64 rows of 128 bytes: 128 latents, or the positional key
+constexpr int kChunks = 5;                      // of a tile: the positional key, then 512 latents
+constexpr int kMaxSlots = 24, kScaleSlots = 8, kAhead = 4;
+constexpr int kThreads8 = 384;                  // 8 softmax warps, score issue, value issue, TMA, scales
+constexpr int kMostRows8 = 96;                  // query rows of a CTA
+constexpr float kSet = 2.5f, kHigh = 8.75f, kLow = -1.0f, kReach = 40.0f;
+constexpr int kWindow = 4;                      // tiles over which a row's weights have to be low
+constexpr int kBad = 8;                         // stretches that the loads may be ahead of the output
 
-struct Decode8Args {
-    const __nv_bfloat16 *q_lat, *q_pe;
-    PagedRows<const uint8_t> cache;
-    const int32_t *lens;
-    int32_t N, H, m, R, parts;
-    float scale;
-    __nv_bfloat16 *o;
-    float *lse;
-    float *part_o;    // [parts, N R, 512]
-    float2 *part_ml;  // [parts, N R]
-    int32_t *status;
+struct Geom8 : SplitGeom {
+    int32_t form;  // query rows of a CTA: 0 up to 32, 1 up to 64, 2 up to 96
+    int32_t np;    // ring slots
+    uint32_t smem;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) kda_mla_decode_fp8_kernel(const __grid_constant__ Decode8Args p) {
-    const int lane = threadIdx.x & 31, n = blockIdx.y, r = blockIdx.z * kWarps + (threadIdx.x >> 5);
-    pdl_wait();
-    if (r >= p.R) return;
-    const int64_t len = p.lens[n], row = (int64_t)n * p.R + r, at = blockIdx.x * (int64_t)p.N * p.R + row;
-    bool bad = len < 0 || len > (int64_t)p.cache.max_pages * p.cache.page_size;
-    if (bad && lane == 0) set_status(p.status, KDA_ERR_SEQLENS);
-    float q[16], o[16], qp[2], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __bfloat162float(p.q_lat[row * kLatent + 16 * lane + i]), o[i] = 0.f;
-    qp[0] = __bfloat162float(p.q_pe[row * kPos + 2 * lane]), qp[1] = __bfloat162float(p.q_pe[row * kPos + 2 * lane + 1]);
-    const int64_t seen = len - (p.m - 1 - r / p.H), per = bad ? 0 : (len + p.parts - 1) / p.parts;
-    const int64_t j0 = blockIdx.x * per, j1 = min(seen, j0 + per);
-    for (int64_t j = j0; j < j1; ++j) {
-        const uint32_t entry = (uint32_t)j / (uint32_t)p.cache.page_size, in = (uint32_t)j - entry * (uint32_t)p.cache.page_size;
-        const int32_t page = p.cache.table[(int64_t)n * p.cache.max_pages + entry];
-        if (page < 0 || page >= p.cache.num_pages) {
-            bad = true;
-            if (lane == 0) set_status(p.status, KDA_ERR_PAGES);
-            break;
-        }
-        const uint8_t *base = p.cache.rows + page * p.cache.page_stride, *src = base + (int64_t)in * kRow8;
-        const float s = *(reinterpret_cast<const float *>(base + (int64_t)p.cache.page_size * kRow8) + in);
-        const uint4 u = *reinterpret_cast<const uint4 *>(src + 16 * lane);
-        const __nv_bfloat162 pe = *reinterpret_cast<const __nv_bfloat162 *>(src + kLatent + 4 * lane);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float v[16], dot = qp[0] * __low2float(pe) + qp[1] * __high2float(pe);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 a = values_of2(w[i >> 1] >> (16 * (i & 1)));
-            v[2 * i] = a.x, v[2 * i + 1] = a.y;
-            dot += q[2 * i] * a.x + q[2 * i + 1] * a.y;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        const float x = dot * s * p.scale, top = fmaxf(m, x), f = top == -INFINITY ? 1.f : expf(m - top);
-        const float e = x == -INFINITY ? 0.f : expf(x - top);  // NaN for a NaN
-        l = l * f + e;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = o[i] * f + e * s * v[i];
-        m = top;
-    }
-    if (lane == 0) p.part_ml[at] = make_float2(m, bad ? __int_as_float(0x7fffffff) : l);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p.part_o[at * kLatent + 16 * lane + i] = o[i];
+struct Args8 : SplitArgs {
+    CUtensorMap map;
+    const __nv_bfloat16 *q_lat, *q_pe;
+    const uint8_t *rows;
+    int64_t page_stride;
+    int32_t rb;  // rows of a TMA box (64, 32 or 16)
+    float c;     // log2(e) scale
+    Geom8 geo;
+};
+
+struct Smem8 {
+    uint64_t q_ready, s_full[2], s_free[2], p_full, pv_done, drained;
+    uint64_t full[kMaxSlots], empty[kMaxSlots], sc_full[kScaleSlots], sc_empty[kScaleSlots];
+    float sc[kScaleSlots][3][kKvTile];  // of a tile's rows: scale, its exponent, its reciprocal
+    float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
+    float factor[128];                  // by query row: scale of O^T
+    float2 half[2][128];                // by query row: the halves' maxima (of a tile, and since the last look), or sums
+    uint32_t tmem;
+    int32_t failed, bad[kBad];
+    Run run;
+    int32_t issued;
+};
+
+// kind::f8f6f4, e4m3 times e4m3 (or e5m2 as B), fp32 accumulator; one step takes 32 of the contraction: 32 bytes
+// of a K-major operand, 32 rows of an MN-major one
+__host__ __device__ constexpr uint32_t idesc8(int M, int N, int b_e5m2, int a_mn) {
+    return (1u << 4) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma8(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "n"(tma::kDescHi));
+}
+// 4 bytes global -> shared, in this thread's asynchronous groups
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(tc::smem_addr(dst)), "l"(src) : "memory");
+}
+// Two weights (a first) as two bytes of e4m3 (into the low half of hi) and two of e5m2, their rest
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    uint16_t h, l;
+    asm("{\n.reg .b32 w, v;\ncvt.rn.f16x2.f32 w, %3, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n"
+        "cvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 w, w, v;\ncvt.rn.satfinite.e5m2x2.f16x2 %1, w;\n}\n"
+        : "=h"(h), "=h"(l)
+        : "f"(a), "f"(b));
+    hi = h, lo = l;
 }
 
-__global__ void __launch_bounds__(128) kda_mla_join_fp8_kernel(const __grid_constant__ Decode8Args p) {
+// FORM: query rows of a CTA, as in Geom8
+template <int FORM>
+__global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const __grid_constant__ Args8 p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int MS = FORM == 0 ? 64 : 128;   // M of the score product
+    constexpr bool kStack = FORM < 2;          // hi and lo rows in one product
+    constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, the lane of lo behind hi)
+    constexpr int kCols = kStack ? 16 : 32;    // cached rows of a tile that a softmax thread takes
+    const Geom8 &geo = p.geo;
+    // Q: four chunks of 128 latents of hi (and lo, stacked; else four of lo behind), then the positional part
+    const uint32_t q_chunk = (uint32_t)(kStack ? MS : geo.rows) * 128;
+    constexpr int q_chunks = kStack ? 5 : 9;
+    uint8_t *s_q = base;                          // M = 128 reads of fewer rows run on into what follows,
+    uint8_t *s_p = s_q + q_chunks * q_chunk;      // rows of S that nobody reads
+    uint8_t *s_ring = s_p + (uint32_t)geo.npad * 128;  // W: npad rows of 64 bytes of e4m3, then 64 of e5m2
+    Smem8 &sm = *reinterpret_cast<Smem8 *>(s_ring + (uint32_t)geo.np * kChunk8);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rt = blockIdx.x % geo.RT, g = blockIdx.x / geo.RT;
+
     pdl_wait();
-    const int64_t row = blockIdx.x, rows = (int64_t)p.N * p.R;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < p.parts; ++i) m = fmaxf(m, p.part_ml[i * rows + row].x);
-    for (int i = 0; i < p.parts; ++i) {
-        const float2 ml = p.part_ml[i * rows + row];
-        const float f = ml.x == -INFINITY ? 0.f : expf(ml.x - m);
-        l += ml.y * (ml.y != ml.y ? 1.f : f);
-        for (int k = 0; k < 4; ++k) o[k] += f * p.part_o[(i * rows + row) * kLatent + 4 * threadIdx.x + k];
+    if (warp == 10 && lane == 0) tma::prefetch_map(&p.map);
+    if (warp == 0) {
+        find_run(p, g, rt, sm.run);
+        if (lane == 0) {
+            sm.failed = 0;
+            sm.issued = 0;
+            for (int i = 0; i < kBad; ++i) sm.bad[i] = 0;
+            tc::mbar_init(&sm.q_ready, kSoftmaxThreads / 32);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_free[i], kSoftmaxThreads / 32);
+            tc::mbar_init(&sm.p_full, kSoftmaxThreads / 32);
+            tc::mbar_init(&sm.pv_done, 1);
+            tc::mbar_init(&sm.drained, 2);
+            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 1);
+            for (int i = 0; i < kScaleSlots; ++i)
+                tc::mbar_init(&sm.sc_full[i], 1), tc::mbar_init(&sm.sc_empty[i], kSoftmaxThreads / 32);
+            tc::mbar_init_fence();
+        }
+    } else if (warp == 8) {
+        tc::tmem_alloc(&sm.tmem, 512);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int k = 0; k < 4; ++k) p.o[row * kLatent + 4 * threadIdx.x + k] = __float2bfloat16(l != l ? l : o[k] * inv);
-    if (p.lse && threadIdx.x == 0) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    pdl_trigger();
+    const uint32_t tmem = sm.tmem;
+    const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
+    const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
+    bool ok = true;
+
+    if (warp == 10) {
+        // ---- TMA producer: one thread ----
+        if (tma::elect()) {
+            Walk w;
+            w.start(p, sm.run);
+            w.skip_idle(p);
+            int seg = 0, ps = 0, pph = 0;
+            const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
+            while (!w.done() && ok) {
+                const int32_t *entry = p.table + (int64_t)w.n * p.max_pages;
+                const int64_t row0 = (int64_t)w.j0 * kKvTile;
+                entry += row0 / p.page_size;
+                int32_t at = (int32_t)(row0 % p.page_size);  // row within the page
+                // the places of a tile's boxes, fetched one tile ahead; nothing past the sequence's rows is looked up
+                int32_t pg[4], ry[4], pg_next[4], ry_next[4];
+                auto look = [&](int j) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        pg_next[b] = 0;
+                        ry_next[b] = at;
+                        if (b < sub && j < w.j1 && (int64_t)j * kKvTile + b * p.rb < w.len) {
+                            pg_next[b] = *entry;
+                            at += p.rb;
+                            if (at == p.page_size) at = 0, ++entry;
+                        }
+                    }
+                };
+                look(w.j0);
+                sm.bad[seg % kBad] = 0;
+                for (int j = w.j0; j < w.j1 && ok; ++j) {
+                    bool bad = false;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        ry[b] = ry_next[b];
+                        const bool out = (uint32_t)pg_next[b] >= (uint32_t)p.num_pages;
+                        bad |= out;
+                        pg[b] = out ? INT32_MAX : pg_next[b];  // past every page: loads as zeros
+                    }
+                    if (bad) {
+                        sm.bad[seg % kBad] = 1;
+                        set_status(p.status, KDA_ERR_PAGES);
+                    }
+                    look(j + 1);
+                    if (FORM == 2 && j + 1 < w.j1) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
+                            if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
+                                tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow8,
+                                                 (uint32_t)p.rb * kRow8);
+                        }
+                    }
+                    const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
+                    const uint32_t box = (uint32_t)p.rb * 128;
+                    for (int i = 0; i < kChunks; ++i) {
+                        ok = tc::mbar_wait(&sm.empty[ps], pph ^ 1);
+                        if (!ok) break;
+                        tc::mbar_arrive_expect_tx(&sm.full[ps], boxes * box);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b < boxes)
+                                tma::load_3d(s_ring + ps * kChunk8 + b * box, &p.map, &sm.full[ps], i == 0 ? kLatent : 128 * (i - 1),
+                                             ry[b], pg[b]);
+                        ++sm.issued;
+                        if (++ps == geo.np) ps = 0, pph ^= 1;
+                    }
+                }
+                ++seg;
+                w.next(p);
+                w.skip_idle(p);
+            }
+            if (!ok) sm.failed = 1;
+        }
+        __syncwarp();
+    } else if (warp == 11) {
+        // ---- the rows' scales: kAhead tiles' copies in flight, two rows a lane ----
+        Walk w, done;  // the tile whose copy is issued, and the one that is handed over
+        w.start(p, sm.run);
+        w.skip_idle(p);
+        done = w;
+        int j = w.j0, jd = w.j0, k = 0, kd = 0;
+        auto step = [&](Walk &x, int &at) {
+            if (++at >= x.j1) {
+                x.next(p);
+                x.skip_idle(p);
+                at = x.j0;
+            }
+        };
+        while (!done.done()) {
+            if (!w.done()) {
+                if (ok) ok = tma::wait_warp(&sm.sc_empty[k % kScaleSlots], ((k / kScaleSlots) & 1) ^ 1);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t row = (int64_t)j * kKvTile + 32 * i + lane;
+                    float *dst = &sm.sc[k % kScaleSlots][0][32 * i + lane];
+                    const uint32_t entry = (uint32_t)row / (uint32_t)p.page_size;
+                    const int32_t page = row < w.len ? p.table[(int64_t)w.n * p.max_pages + entry] : -1;
+                    if ((uint32_t)page < (uint32_t)p.num_pages)
+                        copy4(dst, p.rows + page * p.page_stride + (int64_t)p.page_size * kRow8 +
+                                       4 * ((uint32_t)row - entry * (uint32_t)p.page_size));
+                    else
+                        *dst = 1.f;
+                }
+                step(w, j);
+                ++k;
+            }
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+            if (k < kAhead && !w.done()) continue;
+            if (w.done())
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
+            // every lane looks at what it copied itself
+            float(&sc)[3][kKvTile] = sm.sc[kd % kScaleSlots];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = 32 * i + lane;
+                const uint32_t bits = __float_as_uint(sc[0][at]);
+                sc[1][at] = (float)((int)(bits >> 23) - 127);
+                sc[2][at] = __uint_as_float(0x7F000000u - bits);  // 2^-e
+            }
+            tma::arrive_warp(&sm.sc_full[kd % kScaleSlots]);
+            step(done, jd);
+            ++kd;
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        if (!ok && lane == 0) sm.failed = 1;
+    } else if (warp == 8) {
+        // ---- score products: one thread ----
+        if (tma::elect()) {
+            constexpr uint32_t id = idesc8(MS, kKvTile, 0, 0), id_pe = tma::idesc(MS, kKvTile, 0, 0);
+            const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), ring_lo = tma::lo_k(tc::smem_addr(s_ring)), q_step = q_chunk >> 4;
+            Walk w;
+            w.start(p, sm.run);
+            w.skip_idle(p);
+            int k = 0, seg = 0, ps = 0, pph = 0;
+            while (!w.done() && ok) {
+                ok = tc::mbar_wait(&sm.q_ready, seg & 1);
+                for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
+                    ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1);
+                    const uint32_t d = t_s + (k & 1) * kKvTile;
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        ok = ok && tc::mbar_wait(&sm.full[ps], pph);
+                        if (!ok) break;
+                        if (i == 0) tc::fence_after_sync();
+                        const uint32_t b = ring_lo + ps * (kChunk8 >> 4);
+                        if (i == 0) {
+                            const uint32_t a = q_lo + (q_chunks - 1) * q_step;
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id_pe, s != 0);
+                            tc::commit(&sm.empty[ps]);
+                        } else {
+                            const uint32_t a = q_lo + (i - 1) * q_step;
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                mma8(d, a + 2 * s, b + 2 * s, id, 1);
+                                if (!kStack) mma8(d, a + 4 * q_step + 2 * s, b + 2 * s, id, 1);
+                            }
+                        }
+                        if (++ps == geo.np) ps = 0, pph ^= 1;
+                    }
+                    if (!ok) break;
+                    tc::commit(&sm.s_full[k & 1]);
+                }
+                ++seg;
+                w.next(p);
+                w.skip_idle(p);
+            }
+            if (!ok) sm.failed = 1;
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- value products: one thread ----
+        if (tma::elect()) {
+            const uint32_t id_hi = idesc8(128, geo.npad, 0, 1), id_lo = idesc8(128, geo.npad, 1, 1);
+            const uint32_t ring_lo = tma::lo_mn(tc::smem_addr(s_ring), kChunk8), p_lo = tma::lo_k(tc::smem_addr(s_p));
+            Walk w;
+            w.start(p, sm.run);
+            w.skip_idle(p);
+            int k = 0, ps = 0;
+            while (!w.done() && ok) {
+                for (int j = w.j0; j < w.j1; ++j, ++k) {
+                    ok = tc::mbar_wait(&sm.p_full, k & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const bool two = w.len - j * kKvTile > 32;  // steps of 32 cached rows
+                    const uint32_t more = ((j - w.j0) & (kFold - 1)) != 0;
+                    uint32_t d = tmem;
+                    if (++ps == geo.np) ps = 0;  // the positional chunk
+#pragma unroll
+                    for (int i = 0; i < kChunks - 1; ++i) {
+                        const uint32_t a = ring_lo + ps * (kChunk8 >> 4);
+                        mma8(d, a, p_lo, id_hi, more);
+                        mma8(d, a, p_lo + 4, id_lo, 1);
+                        if (two) {
+                            mma8(d, a + 256, p_lo + 2, id_hi, 1);
+                            mma8(d, a + 256, p_lo + 6, id_lo, 1);
+                        }
+                        tc::commit(&sm.empty[ps]);
+                        d += geo.npad;
+                        if (++ps == geo.np) ps = 0;
+                    }
+                    tc::commit(&sm.pv_done);
+                }
+                w.next(p);
+                w.skip_idle(p);
+            }
+            if (!ok) sm.failed = 1;
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: a thread takes a query row and kCols cached rows of a tile; then the output ----
+        const int quarter = warp & 3, set = warp >> 2;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const int i_row = lane & (kRowsQ - 1);                  // row of the quarter
+        const int h = kStack ? (lane >> (FORM == 0 ? 3 : 4)) & 1 : 0;  // stacked: lane of hi or of lo
+        const bool low = FORM != 0 || lane < 16;                // lanes that hold rows of S
+        const bool lead = low && h == 0;                        // one lane a row
+        const int r = quarter * kRowsQ + i_row;
+        const bool owner = low && r < rows_here, warp_rows = quarter * kRowsQ < rows_here;
+        const int unseen = p.m - 1 - (row_first + (owner ? r : 0)) / p.H;  // last cached rows that the row does not see
+        const int col0 = 32 * set + (kStack ? 16 * h : 0);
+        uint8_t *p_row = s_p + r * 128;
+        int k = 0, seg = 0, ps = 0;  // tiles and stretches worked on, ring slot
+        // Q of a stretch, a row a warp at a time; the last stretch's score products are through: its last tile was taken
+        auto load_q = [&](const Walk &s) {
+            const int64_t row0 = (int64_t)s.n * geo.R + row_first;
+            for (int q = warp; q < rows_here; q += 8) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + (row0 + q) * kLatent) + 2 * lane;
+                const uint4 va = src[0], vb = src[1];
+                const uint32_t pe = reinterpret_cast<const uint32_t *>(p.q_pe + (row0 + q) * kPos)[lane];
+                const uint32_t v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+                uint32_t top = 0;  // bits of the largest magnitude, as fp32; NaN is above all
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, max((v[i] << 16) & 0x7fffffffu, v[i] & 0x7fff0000u));
+                top = __reduce_max_sync(0xffffffffu, top);
+                const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
+                // the unit 2^a: the latents' largest in (224, 448]; positional values that dwarf it stay in bf16's range
+                const int a = max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100);
+                const float inv = exp2_of(-min(a, 120));
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t hh[2], ll[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t u = v[2 * i + e];
+                        const float x = __uint_as_float(u << 16) * inv, y = __uint_as_float(u & 0xffff0000u) * inv;
+                        hh[e] = e4m3_of2(x, y);
+                        const float2 back = values_of2(hh[e]);
+                        ll[e] = e4m3_of2(x - back.x, y - back.y);
+                    }
+                    hi[i] = hh[0] | (hh[1] << 16);
+                    lo[i] = ll[0] | (ll[1] << 16);
+                }
+                // rows of the operand: hi and lo of a quarter one behind the other, or the row itself
+                const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
+                uint8_t *at = s_q + (lane >> 3) * q_chunk;
+                *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                at += kStack ? 0 : 4 * q_chunk;
+                *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                const __nv_bfloat162 pes = __floats2bfloat162_rn(__uint_as_float(pe << 16) * inv, __uint_as_float(pe & 0xffff0000u) * inv);
+                at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
+                *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&pes);
+                if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
+                // a row with an infinity or a NaN has no scores
+                if (lane == 0) sm.row_c[q] = max(top, top_pe) >= 0x7f800000u ? NAN : p.c * exp2_of(min(a, 120));
+            }
+            fence_proxy_async();
+            tma::arrive_warp(&sm.q_ready);
+        };
+        Walk w;
+        w.start(p, sm.run);
+        {
+            Walk first = w;
+            first.skip_idle(p);
+            if (!first.done()) load_q(first);
+            named_sync(2, kSoftmaxThreads);
+        }
+        for (; !w.done() && ok; w.next(p)) {
+            float m_ref = -INFINITY, m_top = -INFINITY, l = 0.f;
+            float recent = -INFINITY;  // the largest since the last look at low weights
+            // the stretch's place among the partials: a run's first stretch, where it continues a sequence, has
+            // the first, the last one, which the run's end cuts, the second; before that any other may use it
+            const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.npad;
+            float m_kept = -INFINITY, l_kept = 0.f;  // reference and denominator of the tiles before the last kFold
+            if (w.work) {
+                const float c = owner ? sm.row_c[r] : 0.f;
+                const uint64_t c2 = pk2(c, c);
+                bool stopped = false;
+                for (int js = w.j0; !stopped; js += kFold) {
+                    if (js > w.j0 && w.j1 - w.j0 > kFold) {
+                        // kFold tiles, or the last ones, are in O^T (also with a failed wait: all warps meet these barriers)
+                        ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                        const bool start = js == w.j0 + kFold;
+                        named_sync(2, kSoftmaxThreads);  // the factors have been read
+                        if (set == 0 && lead) sm.factor[r] = start || m_kept == m_ref ? 1.0f : tc::ex2(m_kept - m_ref);
+                        named_sync(2, kSoftmaxThreads);
+                        for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                            float *kept = p.part_o + part0 * kLatent + 128 * i + 32 * quarter + lane;
+                            fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
+                        }
+                        m_kept = m_ref;
+                        if (low) l_kept = l_kept * sm.factor[r] + l;
+                        l = js >= w.j1 ? l_kept : 0.f;
+                    }
+                    if (js >= w.j1) break;
+                    const int je = min(w.j1, js + kFold);
+                    for (int j = js; j < je; ++j) {
+                        const int slot = k % kScaleSlots;
+                        ok = tma::wait_warp(&sm.sc_full[slot], (k / kScaleSlots) & 1) && ok;
+                        ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1) && ok;
+                        // a failed wait still meets the barriers below, so that no warp is left in them
+                        if (ok) tc::fence_after_sync();
+                        uint32_t s[32];
+                        const bool first = j == w.j0;
+                        float top = -INFINITY;
+                        if (warp_rows && ok) {
+                            tc::tmem_ld32_nowait(t_s + lanes + (k & 1) * kKvTile + set * 32, s);
+                            tc::tmem_wait_ld();
+                            tc::fence_before_sync();
+                        }
+                        tma::arrive_warp(&sm.s_free[k & 1]);
+                        if (warp_rows && ok) {
+                            if constexpr (kStack) {
+                                // hi + lo: the lanes trade halves, and each keeps 16 columns
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const float mine = __uint_as_float(h ? s[16 + e] : s[e]), yours = __uint_as_float(h ? s[e] : s[16 + e]);
+                                    s[e] = __float_as_uint(mine + __shfl_xor_sync(0xffffffffu, yours, kRowsQ));
+                                }
+                            }
+                            // x + e: the weight's exponent with its row's scale
+#pragma unroll
+                            for (int e = 0; e < kCols; e += 4) {
+                                const float4 sc = *reinterpret_cast<const float4 *>(&sm.sc[slot][0][col0 + e]);
+                                const float4 ex = *reinterpret_cast<const float4 *>(&sm.sc[slot][1][col0 + e]);
+                                const float2 a = upk2(fma2(mul2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pk2(sc.x, sc.y)), c2, pk2(ex.x, ex.y)));
+                                const float2 b = upk2(fma2(mul2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), pk2(sc.z, sc.w)), c2, pk2(ex.z, ex.w)));
+                                s[e] = __float_as_uint(a.x), s[e + 1] = __float_as_uint(a.y);
+                                s[e + 2] = __float_as_uint(b.x), s[e + 3] = __float_as_uint(b.y);
+                            }
+                            // cached rows of this thread's part that the row sees
+                            const int64_t seen = (int64_t)w.len - unseen - ((int64_t)j * kKvTile + col0);
+                            if (__any_sync(0xffffffffu, seen < kCols)) {
+#pragma unroll
+                                for (int e = 0; e < kCols; ++e)
+                                    if (e >= seen) s[e] = 0xff800000u;
+                            }
+#pragma unroll
+                            for (int e = 0; e < kCols; e += 2)
+                                top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                        }
+                        // one barrier a tile: may a row need a new reference, did a wait fail
+                        const bool look = ((j - w.j0) & (kWindow - 1)) == kWindow - 1;
+                        recent = fmaxf(recent, top);
+                        const bool may = owner && (first || top - m_ref > kHigh ||
+                                                   (look && recent - m_ref < kLow && m_ref > m_top - kReach));
+                        const bool any = softmax_any(may || !ok);
+                        if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                        if (any) {
+                            if constexpr (kStack) {
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, kRowsQ));
+                                recent = fmaxf(recent, __shfl_xor_sync(0xffffffffu, recent, kRowsQ));
+                            }
+                            if (lead) sm.half[set][r] = make_float2(top, recent);
+                            // all stop together when any wait failed
+                            if (softmax_any(!ok)) {
+                                ok = false;
+                                stopped = true;
+                                break;
+                            }
+                            if (low) {
+                                const float2 other = sm.half[set ^ 1][r];
+                                top = fmaxf(top, other.x);
+                                recent = fmaxf(recent, other.y);
+                            }
+                            m_top = fmaxf(m_top, recent);
+                            const bool up = first || top - m_ref > kHigh;
+                            const float to = fmaxf((up ? top : recent) - kSet, m_top - kReach);
+                            const bool anew = up || (look && recent - m_ref < kLow && recent > -INFINITY && to < m_ref);
+                            const float f = anew && !first ? tc::ex2(m_ref - to) : 1.0f;
+                            if (set == 0 && lead) sm.factor[r] = f;
+                            if (anew) m_ref = to;
+                            l *= f;
+                            if (softmax_any(owner && anew && !first)) {
+                                tc::fence_after_sync();
+                                for (int e = 0; e < geo.npad; e += 16) {
+                                    float fs[16];
+                                    bool same = true;
+#pragma unroll
+                                    for (int y = 0; y < 16; ++y) fs[y] = sm.factor[e + y], same &= fs[y] == 1.0f;
+                                    if (same) continue;
+                                    for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                                        const uint32_t at = tmem + lanes + i * geo.npad + e;
+                                        uint32_t x[16];
+                                        tma::tmem_ld16_nowait(at, x);
+                                        tc::tmem_wait_ld();
+#pragma unroll
+                                        for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * fs[y]);
+                                        tc::tmem_st16(at, x);
+                                    }
+                                }
+                                tc::tmem_wait_st();
+                            }
+                        }
+                        if (look) recent = -INFINITY;
+                        if (warp_rows && ok) {
+                            const float mb = m_ref == -INFINITY ? 0.f : -m_ref;
+                            const uint64_t mb2 = pk2(mb, mb);
+                            uint64_t l2[2] = {0, 0};
+#pragma unroll
+                            for (int u = 0; u < kCols / 16; ++u) {  // 16-byte units of the row, swizzled
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t *x = &s[16 * u + 4 * e];
+                                    const float4 inv = *reinterpret_cast<const float4 *>(&sm.sc[slot][2][col0 + 16 * u + 4 * e]);
+                                    const float2 y = upk2(add2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), mb2));
+                                    const float2 z = upk2(add2(pk2(__uint_as_float(x[2]), __uint_as_float(x[3])), mb2));
+                                    const float w0 = tc::ex2(y.x), w1 = tc::ex2(y.y), w2 = tc::ex2(z.x), w3 = tc::ex2(z.y);
+                                    l2[0] = fma2(pk2(w0, w1), pk2(inv.x, inv.y), l2[0]);
+                                    l2[1] = fma2(pk2(w2, w3), pk2(inv.z, inv.w), l2[1]);
+                                    uint32_t h0, h1, l0, l1;
+                                    split2(w0, w1, h0, l0);
+                                    split2(w2, w3, h1, l1);
+                                    hi[e] = h0 | (h1 << 16);
+                                    lo[e] = l0 | (l1 << 16);
+                                }
+                                if (low && r < geo.npad) {
+                                    const int unit = (col0 >> 4) + u;
+                                    *reinterpret_cast<uint4 *>(p_row + ((unit ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                    *reinterpret_cast<uint4 *>(p_row + (((4 + unit) ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                }
+                            }
+                            const float2 ls = upk2(add2(l2[0], l2[1]));
+                            l += ls.x + ls.y;
+                        }
+                        tma::arrive_warp(&sm.sc_empty[slot]);
+                        const int valid = min(kKvTile, w.len - j * kKvTile);
+                        if (valid & 31) {  // value rows behind the sequence in the product's last step of 32
+                            const int units = (-valid & 31) * 8;
+                            for (int u = tid; u < (kChunks - 1) * units; u += kSoftmaxThreads) {
+                                const int at = (ps + 1 + u / units) % geo.np;
+                                reinterpret_cast<uint4 *>(s_ring + at * kChunk8)[valid * 8 + u % units] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        ps += kChunks;
+                        if (ps >= geo.np) ps -= geo.np;
+                        fence_proxy_async();
+                        tc::fence_before_sync();
+                        tma::arrive_warp(&sm.p_full);
+                        ++k;
+                    }
+                }
+                // the next stretch's queries before this one's output, so that its scores start meanwhile
+                Walk after = w;
+                after.next(p);
+                after.skip_idle(p);
+                if (ok && !after.done()) load_q(after);
+                if (ok) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
+                tc::fence_after_sync();
+            }
+            if constexpr (kStack) l += __shfl_xor_sync(0xffffffffu, l, kRowsQ);
+            if (lead) sm.half[set][r].x = l;
+            if (softmax_any(!ok)) ok = false;
+            if (low) l += sm.half[set ^ 1][r].x;
+            // ---- this stretch's part of the sequence: finished, or left for the join ----
+            const bool whole = w.j0 == 0 && w.j1 == w.tiles;
+            const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg % kBad] != 0);
+            if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
+            const int64_t row0 = (int64_t)w.n * geo.R + row_first;
+            if (set == 0 && lead) {
+                sm.factor[r] = bad ? NAN : (l == 0.f ? 0.f : 1.0f / l);
+                if (owner) {
+                    if (!whole)
+                        p.part_ml[part0 + r] = make_float2(m_ref, bad ? NAN : l);
+                    else if (p.lse)
+                        p.lse[row0 + r] = bad ? NAN : (l == 0.f ? -INFINITY : m_ref * p.scale + logf(l));
+                }
+            }
+            named_sync(2, kSoftmaxThreads);
+            for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                const int lat = 128 * i + 32 * quarter + lane;
+                for (int e = 0; 16 * e < rows_here; ++e) {
+                    uint32_t x[16];
+                    if (w.work && ok) {
+                        tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + 16 * e, x);
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) x[y] = 0;
+                    }
+                    if (whole) {
+                        // neighbouring lanes trade a value: each then holds two latents of one row
+                        __nv_bfloat16 *dst = p.o + (row0 + 16 * e + (lane & 1)) * kLatent + (lat & ~1);
+                        const int left = rows_here - 16 * e - (lane & 1);
+#pragma unroll
+                        for (int y = 0; y < 16; y += 2) {
+                            const float2 f = *reinterpret_cast<const float2 *>(&sm.factor[16 * e + y]);
+                            const __nv_bfloat162 h2 =
+                                __floats2bfloat162_rn(__uint_as_float(x[y]) * f.x, __uint_as_float(x[y + 1]) * f.y);
+                            const uint32_t own = *reinterpret_cast<const uint32_t *>(&h2);
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                            const uint32_t two_lat = (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                            if (y < left) *reinterpret_cast<uint32_t *>(dst + y * kLatent) = two_lat;
+                        }
+                    } else {  // rows past the last are written too (their columns of O^T are nobody's): parts are npad rows
+                        float *dst = p.part_o + (part0 + 16 * e) * kLatent + lat;
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) dst[y * kLatent] = __uint_as_float(x[y]);
+                    }
+                }
+            }
+            // O^T has been read: the next stretch's W (all threads arrive) lets the MMA warp write it
+            tc::fence_before_sync();
+            named_sync(2, kSoftmaxThreads);
+            if (w.work) ++seg;
+        }
+        if (!ok) sm.failed = 1;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (sm.failed && (warp == 8 || warp == 9)) {
+        // a wait gave up: report it, and let what is in flight land before the memory goes
+        if (tma::elect()) {
+            tc::commit(&sm.drained);  // each issuing thread's own products
+            if (warp == 8) {
+                set_status(p.status, KDA_ERR_CUDA);
+                tc::mbar_wait(&sm.drained, 0);
+                for (int e = max(0, sm.issued - geo.np); e < sm.issued; ++e) tc::mbar_wait(&sm.full[e % geo.np], (e / geo.np) & 1);
+            }
+        }
+        __syncwarp();
+    }
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
-int parts_of(int64_t N, int64_t R) {
-    const int64_t blocks = N * ((R + kWarps - 1) / kWarps);
-    return (int)max((int64_t)1, min((int64_t)kMaxParts, 608 / blocks));
+constexpr size_t kSmem8 = 232448;
+
+Geom8 geometry8(int32_t H, int32_t m) {
+    Geom8 q{};
+    q.R = H * m;
+    q.RT = (q.R + kMostRows8 - 1) / kMostRows8;
+    q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
+    q.npad = (q.rows + 15) / 16 * 16;
+    q.form = q.rows <= 32 ? 0 : (q.rows <= 64 ? 1 : 2);
+    const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)5 * (q.form == 0 ? 64 : 128) * 128;
+    const size_t fixed = 1024 + sizeof(Smem8) + of_q + (size_t)q.npad * 128;
+    q.np = (int32_t)((kSmem8 - fixed) / kChunk8);
+    if (q.np > kMaxSlots) q.np = kMaxSlots;
+    q.smem = (uint32_t)(fixed + (size_t)q.np * kChunk8);
+    return q;
 }
+static_assert(kSmem8 - 1024 - sizeof(Smem8) - 10 * kMostRows8 * 128 >= 12 * kChunk8, "96 rows leave 12 slots");
+static_assert(kMaxSlots / kChunks + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
 }  // namespace
 }  // namespace kda
@@ -102,9 +711,8 @@ extern "C" {
 
 size_t kda_mla_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens) {
     if (num_seqs < 0 || num_heads < 0 || num_tokens < 0) return 0;
-    const int64_t R = (int64_t)num_heads * num_tokens;
-    if (R > INT32_MAX / 2 || R == 0 || num_seqs == 0) return 256;
-    return (size_t)kda::parts_of(num_seqs, R) * num_seqs * R * (kda::kLatent * 4 + 8);
+    if ((int64_t)num_heads * num_tokens > INT32_MAX / 2 || num_heads == 0 || num_tokens == 0) return 256;
+    return kda::split_ws(kda::geometry8(num_heads, num_tokens), kda::kMostRows8).total;
 }
 
 int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_t *cache, int64_t page_stride,
@@ -126,24 +734,56 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
         !mla_aligned(workspace, 256))
         return KDA_ERR_ALIGN;
     if (workspace_bytes < kda_mla_decode_fp8_workspace_size(num_seqs, num_heads, num_tokens)) return KDA_ERR_WORKSPACE;
-    if (num_seqs > 65535) return KDA_ERR_SHAPE;
-    Decode8Args a{};
+    int sms = 0, device = 0;
+    rc = device_sms(&sms, &device);
+    if (rc != KDA_OK) return rc;
+    if (device >= 64) return KDA_ERR_DEVICE;
+
+    Args8 a;
+    a.geo = geometry8(num_heads, num_tokens);
+    a.split = a.geo;
+    const SplitWs w = split_ws(a.geo, kMostRows8);
+    a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
+    // a cache without pages keeps one page of extent: no id is in range, every load is past it
+    const uint64_t dc[3] = {(uint64_t)kRow8, (uint64_t)page_size, (uint64_t)(num_pages > 0 ? num_pages : 1)};
+    const uint64_t sc[3] = {1, (uint64_t)kRow8, (uint64_t)page_stride};
+    if (!tma::encode_bytes(&a.map, cache, dc, sc, a.rb)) return KDA_ERR_CUDA;
     a.q_lat = reinterpret_cast<const __nv_bfloat16 *>(q_lat);
     a.q_pe = reinterpret_cast<const __nv_bfloat16 *>(q_pe);
-    a.cache = {cache, page_stride, num_pages, page_size, page_table, max_pages};
+    a.rows = cache;
+    a.page_stride = page_stride;
+    a.table = page_table;
     a.lens = cache_lens;
-    a.N = num_seqs, a.H = num_heads, a.m = num_tokens, a.R = num_heads * num_tokens;
-    a.parts = parts_of(a.N, a.R);
-    a.scale = scale;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.N = num_seqs;
+    a.H = num_heads;
+    a.m = num_tokens;
+    a.c = scale * 1.4426950408889634f;
+    a.scale = 0.6931471805599453f;  // the maxima count in powers of two
     a.o = reinterpret_cast<__nv_bfloat16 *>(o);
     a.lse = lse;
-    const int64_t rows = (int64_t)a.N * a.R;
-    a.part_o = static_cast<float *>(workspace);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + a.parts * rows * kLatent);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.head = reinterpret_cast<int64_t *>(ws + w.head);
+    a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
     a.status = status;
+    static std::atomic<bool> configured[64];  // the kernels' shared memory, set once a device
+    if (!configured[device].load(std::memory_order_acquire)) {
+        for (auto kernel : {kda_mla_decode_fp8_kernel<0>, kda_mla_decode_fp8_kernel<1>, kda_mla_decode_fp8_kernel<2>})
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem8) != cudaSuccess)
+                return KDA_ERR_CUDA;
+        configured[device].store(true, std::memory_order_release);
+    }
+    // no more groups than the longest page tables could give tiles to
+    const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
+    a.G = groups_of(a.geo.RT, sms < kMaxGroups ? sms : kMaxGroups);
+    if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_after(kda_mla_decode_fp8_kernel, dim3(a.parts, a.N, (a.R + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, st, a) != cudaSuccess ||
-        launch_after(kda_mla_join_fp8_kernel, dim3((unsigned)rows), dim3(128), 0, st, a) != cudaSuccess)
+    auto kernel = a.geo.form == 0 ? kda_mla_decode_fp8_kernel<0> : (a.geo.form == 1 ? kda_mla_decode_fp8_kernel<1> : kda_mla_decode_fp8_kernel<2>);
+    if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(kThreads8), a.geo.smem, st, a) != cudaSuccess ||
+        join_parts(a, st) != cudaSuccess)
         return KDA_ERR_CUDA;
     return KDA_OK;
 }

@@ -59,50 +59,34 @@
 // length are left out, and value rows inside the last step are zeroed in shared memory.
 
 #include "kda_common.cuh"
-#include "kda_latent_common.cuh"
+#include "kda_latent_split.cuh"
 #include "kda_tma.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kKvTile = 64;                     // cached rows of a tile
 constexpr int kRowTile = 64, kWideRows = 96;    // query rows of a CTA at most: M = 64, and M = 128 (TMEM holds 96)
 constexpr uint32_t kChunkB = kKvTile * 128;     // bytes of a chunk: 8 KB
 constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
 constexpr int kMaxPair = 12, kMaxPos = 4;     // ring slots at most
 constexpr int kDecThreads = 352;              // 8 softmax warps, S issue, value issue, TMA
-constexpr int kMaxGroups = 160;               // CTAs that share the list at most
 constexpr float kGrow = 8.0f;
-constexpr int kSoftmaxThreads = 256;
-constexpr int kFold = 1024;                   // tiles of a stretch that O^T sums in tensor memory (a power of two)
 constexpr int kHalf = kKvTile / 2;            // cached rows of a tile that a softmax thread takes
 
-struct DecodeGeom {
-    int32_t R;        // query rows of a sequence: m H
-    int32_t RT, rows; // row tiles and query rows of each (a multiple of 8)
-    int32_t npad;     // MMA columns of O^T: rows rounded up to 16
+struct DecodeGeom : SplitGeom {
     int32_t qt;       // pairs of Q's latent chunks (128 latents) kept in TMEM; the others in shared memory
     int32_t np, nr;   // ring slots
     uint32_t smem;    // dynamic shared memory
 };
 
-struct DecodeArgs {
+struct DecodeArgs : SplitArgs {
     CUtensorMap q_lat, q_pe, cache;
     const __nv_bfloat16 *q;  // q_lat again
     const __nv_bfloat16 *rows;  // the cache again, for the prefetch of a coming tile into L2
     int64_t page_stride;
-    const int32_t *table, *lens;
-    int32_t max_pages, num_pages, page_size, rb;  // rb: rows of a TMA box (64, 32 or 16)
-    int32_t N, H, m, G;
+    int32_t rb;  // rows of a TMA box (64, 32 or 16)
     DecodeGeom geo;
-    float scale;
-    __nv_bfloat16 *o;
-    float *lse;
-    float *part_o;   // [2 G, RT, npad, 512]
-    float2 *part_ml; // [2 G, RT, npad] reference maximum (raw scores), sum
-    int64_t *head;   // [0]: tiles of the batch; then per group {sequence, first tile, tiles of the sequence}
-    int32_t *status;
 };
 
 struct DecodeSmem {
@@ -111,91 +95,9 @@ struct DecodeSmem {
     float factor[128], half[2][128];  // by query row: scale of O^T, the halves' maxima or sums
     uint32_t tmem;
     int32_t failed, bad[4];
-    int32_t first_seq, first_tile;
-    int64_t begin, end;
+    Run run;
     int32_t pair_issued, pos_issued, q_issued;
 };
-
-__device__ __forceinline__ bool bad_len(const DecodeArgs &p, int64_t len) {
-    return len < 0 || len > (int64_t)p.max_pages * p.page_size;
-}
-// tiles of a sequence in the list: one at least, so that every sequence's output is written
-__device__ __forceinline__ int32_t tiles_of(const DecodeArgs &p, int32_t len) {
-    return bad_len(p, len) || len == 0 ? 1 : (int32_t)(((int64_t)len + kKvTile - 1) / kKvTile);
-}
-
-// The list's cut into G runs: the first `extra` of them one tile longer than the others.
-struct Runs {
-    int64_t each;
-    int32_t extra;
-    __device__ __forceinline__ Runs(int64_t total, int32_t G) : each(total / G), extra((int32_t)(total - each * G)) {}
-    __device__ __forceinline__ int64_t begin(int32_t g) const { return g * each + min(g, extra); }
-    // the run that holds tile x
-    __device__ __forceinline__ int32_t of(int64_t x) const {
-        const int64_t longer = extra * (each + 1);
-        return (int32_t)(x < longer ? x / (each + 1) : extra + (x - longer) / each);
-    }
-};
-
-// A walk over a run of the list, one stretch of tiles of one sequence after the other.
-struct Walk {
-    int32_t n, j0, j1, tiles, len;
-    int64_t left;
-    bool work;  // the sequence has cached rows and a sound length
-    __device__ __forceinline__ void open(const DecodeArgs &p) {
-        // where it stands and not again: with a load that the compiler may repeat, two tiles of 72 rows take
-        // longer (64 sequences x 130 rows 138 us, 131 so)
-        asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(len) : "l"(p.lens + n));
-        tiles = tiles_of(p, len);
-        j1 = (int32_t)min((int64_t)tiles, j0 + left);
-        work = len > 0 && !bad_len(p, len);
-    }
-    __device__ __forceinline__ void start(const DecodeArgs &p, const DecodeSmem &sm) {
-        n = sm.first_seq;
-        j0 = sm.first_tile;
-        left = sm.end - sm.begin;
-        if (left > 0) open(p);
-    }
-    __device__ __forceinline__ bool done() const { return left <= 0; }
-    __device__ __forceinline__ void next(const DecodeArgs &p) {
-        left -= j1 - j0;
-        ++n;
-        j0 = 0;
-        if (left > 0) open(p);
-    }
-    __device__ __forceinline__ void skip_idle(const DecodeArgs &p) {
-        while (!done() && !work) next(p);
-    }
-};
-
-// barrier of the softmax warps that also tells whether any thread's flag is set
-__device__ __forceinline__ bool softmax_any(bool flag) {
-    uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 256, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r)
-                 : "r"((uint32_t)flag)
-                 : "memory");
-    return r != 0;
-}
-
-// kept = factor kept + O^T of this thread's latent, by query row; for the output (back) into O^T instead
-__device__ __forceinline__ void fold_o(float *kept, uint32_t o_addr, int npad, const float *factor, bool start, bool back) {
-    tc::fence_after_sync();
-    for (int e = 0; e < npad; e += 16) {
-        uint32_t x[16];
-        tma::tmem_ld16_nowait(o_addr + e, x);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-            float *at = kept + (int64_t)(e + y) * kLatent;
-            const float v = __uint_as_float(x[y]) + (start ? 0.f : *at * factor[e + y]);
-            x[y] = __float_as_uint(v);
-            if (!back) *at = v;
-        }
-        if (back) tc::tmem_st16(o_addr + e, x);
-    }
-    if (back) tc::tmem_wait_st();
-}
 
 // MS: rows of the score product's M. QT: the first QT pairs of Q's latent chunks are kept in TMEM.
 // (Constants, so that the issue loop has no choice to make.)
@@ -223,51 +125,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         tma::prefetch_map(&p.cache);
     }
     if (warp == 0) {
-        int64_t total = 0;
-        for (int n = lane; n < p.N; n += 32) total += tiles_of(p, p.lens[n]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-        const Runs runs(total, p.G);
-        const int64_t begin = runs.begin(g), end = runs.begin(g + 1);
-        int64_t before = 0;
-        int seq = p.N - 1;
-        int64_t first = 0;
-        int32_t of = 0;
-        for (int n0 = 0; n0 < p.N; n0 += 32) {
-            const int n = n0 + lane;
-            const int32_t t = n < p.N ? tiles_of(p, p.lens[n]) : 0;
-            int64_t incl = t;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += x;
-            }
-            const int64_t lo = before + incl - t;
-            const unsigned mine = __ballot_sync(0xffffffffu, begin >= lo && begin < lo + t);
-            if (mine) {
-                const int src = __ffs(mine) - 1;
-                seq = n0 + src;
-                first = begin - __shfl_sync(0xffffffffu, lo, src);
-                of = __shfl_sync(0xffffffffu, t, src);
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, incl, 31);
-        }
+        find_run(p, g, rt, sm.run);
         if (lane == 0) {
-            sm.first_seq = seq;
-            sm.first_tile = (int32_t)first;
-            sm.begin = begin;
-            sm.end = end;
             sm.failed = 0;
             sm.pair_issued = sm.pos_issued = sm.q_issued = 0;
             for (int i = 0; i < 4; ++i) sm.bad[i] = 0;
-            if (rt == 0) {
-                if (g == 0) p.head[0] = total;
-                int32_t *e = reinterpret_cast<int32_t *>(p.head + 1) + 4 * g;
-                e[0] = seq;
-                e[1] = (int32_t)first;
-                e[2] = of;
-            }
             tc::mbar_init(&sm.q_full, 1);
             tc::mbar_init(&sm.q_empty, 1);
             tc::mbar_init(&sm.q_ready, kSoftmaxThreads / 32);
@@ -299,7 +161,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
         // ---- TMA producer: one thread ----
         if (tma::elect()) {
             Walk w;
-            w.start(p, sm);
+            w.start(p, sm.run);
             w.skip_idle(p);
             int seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
             const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
@@ -396,7 +258,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), pos_lo = tma::lo_k(tc::smem_addr(s_pos));
             const uint32_t pair_lo = tma::lo_k(tc::smem_addr(s_pair)), q_step = q_chunk >> 4;
             Walk w;
-            w.start(p, sm);
+            w.start(p, sm.run);
             w.skip_idle(p);
             int k = 0, seg = 0, ps = 0, pph = 0, rs = 0, rph = 0;
             while (!w.done() && ok) {
@@ -448,7 +310,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             const uint32_t id = tma::idesc(128, geo.npad, 1, 0);
             const uint32_t pair_lo = tma::lo_mn(tc::smem_addr(s_pair), kChunkB), p_lo = tma::lo_k(tc::smem_addr(s_p));
             Walk w;
-            w.start(p, sm);
+            w.start(p, sm.run);
             w.skip_idle(p);
             int k = 0, ps = 0;
             while (!w.done() && ok) {
@@ -514,7 +376,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
             tma::arrive_warp(&sm.q_ready);
         };
         Walk w;
-        w.start(p, sm);
+        w.start(p, sm.run);
         if constexpr (QT > 0) {
             Walk first = w;
             first.skip_idle(p);
@@ -730,127 +592,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
-// The join of the sequences that a run's border cuts. With fewer sequences than groups block x
-// belongs to sequence x, whose place in the list it adds up itself; with more it belongs to
-// the border before group x + 1, where the main kernel left the place, and the first border
-// inside a sequence joins it. W warps share a row's parts, each lane 16 / Z of the 512 latents, Z
-// blocks a row (1M x 12: 195 us with one, 192 with four); the parts are added in list order within a
-// warp and the warps' sums in warp order, so the result does not depend on timing. With W = 1 the
-// way through shared memory is not needed, but the 32 KB keep these blocks off the SMs until
-// the main kernel's are through: without them they wait beside it, and 256 x 96 takes 2% longer.
-constexpr int kJoinThreads = 512;
-template <int W, int Z>
-__global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid_constant__ DecodeArgs p) {
-    constexpr int kRows = kJoinThreads / 32 / W;  // rows of a block
-    constexpr int kLat = kLatent / Z, kVec = kLat / 128;  // its latents, and float4 of a lane
-    __shared__ float s_o[kRows][W][kLat];
-    __shared__ float s_m[kRows][W], s_l[kRows][W];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int32_t n, tiles, b;  // the sequence, its tiles, the run after the one that holds its first tile
-    int64_t first;        // list index of that tile
-    int count;            // parts
-    if (p.N < p.G) {
-        // The lengths are read before the wait: whatever wrote them had finished before the main kernel
-        // let this one start, which it does behind its own wait. From L2, where that writing is.
-        n = blockIdx.x;
-        int64_t total = 0, before = 0;
-        for (int i = lane; i < p.N; i += 32) {
-            const int32_t t = tiles_of(p, __ldcg(p.lens + i));
-            total += t;
-            if (i < n) before += t;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, off);
-            before += __shfl_xor_sync(0xffffffffu, before, off);
-        }
-        const Runs runs(total, p.G);
-        first = before;
-        tiles = tiles_of(p, __ldcg(p.lens + n));
-        b = runs.of(first) + 1;
-        count = runs.of(first + tiles - 1) - b + 2;
-        pdl_wait();  // in every block: a join that ended early would let the next kernel start before the main one's end
-        if (count == 1) return;
-    } else {
-        b = blockIdx.x + 1;
-        pdl_wait();
-        const int64_t total = p.head[0];
-        const Runs runs(total, p.G);
-        const int64_t at = runs.begin(b);
-        if (at >= total) return;
-        const int32_t *e = reinterpret_cast<const int32_t *>(p.head + 1) + 4 * b;
-        n = e[0];
-        tiles = e[2];
-        first = at - e[1];
-        if (e[1] == 0 || runs.of(first) != b - 1) return;
-        count = runs.of(first + tiles - 1) - b + 2;
-    }
-    const int rl = warp / W, part = warp % W, rr = blockIdx.y * kRows + rl;
-    const bool live = rr < p.geo.R;
-    const int rt = (live ? rr : 0) / p.geo.rows, r = (live ? rr : 0) % p.geo.rows;
-    const float c = p.scale * 1.4426950408889634f;
-    // parts: run b - 1 (slot 1, it holds the sequence's start), then the following runs (slot 0)
-    const int lat0 = blockIdx.z * kLat;
-    float m = -INFINITY, l = 0.f, o[4 * kVec];
-#pragma unroll
-    for (int i = 0; i < 4 * kVec; ++i) o[i] = 0.f;
-    auto row_of = [&](int i) {
-        const int64_t gq = b - 1 + i;
-        return ((2 * gq + (i == 0 ? 1 : 0)) * p.geo.RT + rt) * p.geo.npad + r;
-    };
-    if (live) {
-        // the common maximum of this warp's parts first, then one weighted sum
-        for (int i = part + W * lane; i < count; i += W * 32)
-            m = fmaxf(m, p.part_ml[row_of(i)].x);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll (Z > 1 ? 8 : 4)
-        for (int i = part; i < count; i += W) {
-            const int64_t q = row_of(i);
-            const float2 ml = p.part_ml[q];
-            const float f = tc::ex2((ml.x - ms) * c);
-            l += f * ml.y;
-            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + q * kLatent + lat0) + lane;
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                const float4 x = __ldcs(src + 32 * v);
-                o[4 * v] += f * x.x;
-                o[4 * v + 1] += f * x.y;
-                o[4 * v + 2] += f * x.z;
-                o[4 * v + 3] += f * x.w;
-            }
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < kVec; ++v)
-        *reinterpret_cast<float4 *>(&s_o[rl][part][4 * (32 * v + lane)]) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-    if (lane == 0) s_m[rl][part] = m, s_l[rl][part] = l;
-    __syncthreads();
-    if (!live) return;
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[rl][i]);
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float f[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        f[i] = tc::ex2((s_m[rl][i] - Ms) * c);
-        L += f[i] * s_l[rl][i];
-    }
-    const float inv = L == 0.f ? 0.f : 1.0f / L;
-    const int64_t row = (int64_t)n * p.geo.R + rr;
-    if (part == 0 && lane == 0 && blockIdx.z == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M * p.scale + logf(L);
-    for (int x = 2 * (part * 32 + lane); x < kLat; x += 2 * 32 * W) {
-        float a = 0.f, bb = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            a += f[i] * s_o[rl][i][x];
-            bb += f[i] * s_o[rl][i][x + 1];
-        }
-        *reinterpret_cast<__nv_bfloat162 *>(p.o + row * kLatent + lat0 + x) = __floats2bfloat162_rn(a * inv, bb * inv);
-    }
-}
-
 constexpr size_t kSmemMax = 232448;
 
 // Row tiles of equal size; the rings take what Q and P leave. One tile up to 96 rows and two up to
@@ -881,32 +622,6 @@ DecodeGeom geometry(int32_t H, int32_t m) {
 static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 10 * kRowTile * 128 >= 8 * kPairB + 2 * kChunkB, "two tiles' rings");
 static_assert(kSmemMax - 1024 - sizeof(DecodeSmem) - 8 * kWideRows * 128 >= 7 * kPairB + 2 * kChunkB, "96 rows leave 7 pairs");
 
-// groups of CTAs that share the list: one CTA an SM
-int32_t groups_of(int32_t RT, int32_t sms) { return sms / RT > 0 ? sms / RT : 1; }
-
-struct DecodeWs {
-    size_t head, ml, o, total;
-};
-DecodeWs decode_ws(const DecodeGeom &q) {
-    DecodeWs w;
-    size_t parts = 2 * (size_t)groups_of(q.RT, kMaxGroups) * q.RT * q.npad;
-    const size_t widest = 2 * (size_t)kMaxGroups * kWideRows;
-    if (q.RT > 1 && parts < widest) parts = widest;  // more rows never need less
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    w.head = 0;
-    w.ml = up(8 + 16 * kMaxGroups);
-    w.o = w.ml + up(parts * sizeof(float2));
-    w.total = w.o + parts * kLatent * sizeof(float);
-    return w;
-}
-
-template <int W, int Z>
-cudaError_t launch_join(const DecodeArgs &a, cudaStream_t st) {
-    const int rows = kJoinThreads / 32 / W;
-    const int cuts = a.N < a.G ? a.N : a.G - 1;
-    return launch_after(kda_mla_join_kernel<W, Z>, dim3(cuts, (a.geo.R + rows - 1) / rows, Z), dim3(kJoinThreads), 0, st, a);
-}
-
 }  // namespace
 }  // namespace kda
 
@@ -915,7 +630,7 @@ extern "C" {
 size_t kda_mla_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens) {
     if (num_seqs < 0 || num_heads < 0 || num_tokens < 0) return 0;
     if ((int64_t)num_heads * num_tokens > INT32_MAX / 2 || num_heads == 0 || num_tokens == 0) return 256;
-    return kda::decode_ws(kda::geometry(num_heads, num_tokens)).total;
+    return kda::split_ws(kda::geometry(num_heads, num_tokens), kda::kWideRows).total;
 }
 
 int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *cache, int64_t page_stride,
@@ -944,7 +659,8 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
 
     DecodeArgs a;
     a.geo = geometry(num_heads, num_tokens);
-    const DecodeWs w = decode_ws(a.geo);
+    a.split = a.geo;
+    const SplitWs w = split_ws(a.geo, kWideRows);
     a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
     const uint64_t rows = (uint64_t)num_seqs * a.geo.R;
     const uint64_t dl[3] = {kLatent, rows, 0}, sl[3] = {1, kLatent, 0}, dp[3] = {kPos, rows, 0}, sp[3] = {1, kPos, 0};
@@ -988,14 +704,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     auto kernel = a.geo.qt == 2 ? kda_mla_decode_kernel<64, 2> : (a.geo.qt == 1 ? kda_mla_decode_kernel<128, 1> : kda_mla_decode_kernel<64, 0>);
     if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(kDecThreads), a.geo.smem, st, a) != cudaSuccess)
         return KDA_ERR_CUDA;
-    if (a.G > 1) {
-        // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four, and
-        // two or three are one warp's. With 1, 4 and 16 warps a row: 1M x 12 236, 200 and 193 us; 8 sequences
-        // of 30000 rows x 12 heads 50, 36 and 34; 32 of 8000 x 16 42, 37 and 41; 256 of 8000 x 96 293, 347, 440
-        const int64_t n = num_seqs;
-        const cudaError_t e = n * 16 <= a.G ? launch_join<16, 4>(a, st) : (n * 4 <= a.G ? launch_join<4, 2>(a, st) : launch_join<1, 1>(a, st));
-        if (e != cudaSuccess) return KDA_ERR_CUDA;
-    }
+    if (join_parts(a, st) != cudaSuccess) return KDA_ERR_CUDA;
     return KDA_OK;
 }
 

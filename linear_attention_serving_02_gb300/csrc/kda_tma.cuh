@@ -168,5 +168,16 @@ inline bool encode(CUtensorMap *map, const void *base, int rank, const uint64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of a tensor of bytes of three dimensions, innermost first, whose strides count bytes, for boxes of
+// {128, box1, 1}. Out-of-range rows load as zeros.
+inline bool encode_bytes(CUtensorMap *map, const void *base, const uint64_t (&dim)[3], const uint64_t (&stride)[3], uint32_t box1) {
+    const EncodeFn f = encoder();
+    if (!f) return false;
+    const cuuint64_t d[3] = {dim[0], dim[1], dim[2]}, s[2] = {stride[1], stride[2]};
+    const cuuint32_t box[3] = {128, box1, 1}, one[3] = {1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tma
 }  // namespace kda

@@ -6,15 +6,19 @@ Bounds (half steps relative to the value: bf16 2^-8, e4m3 2^-4, e5m2 2^-3, fp16 
            (224, 448]: together they hold a bf16 value exactly, but for what lies below half their last step,
            2^-10 2^a <= 2^-10 / 224 max|q| < 2^-17.8 max|q|. With the sums (576 + 512 terms, and 16 for scaling
            and exponent, a whole step 2^-23 each, as tensor cores may truncate):
-           ds = scale (2^-17.8 max|q_lat| sum|k_lat| + 1104 2^-23 1.07 sum|q k|), k the value with its scale
+           ds = scale (2^-17.8 max|q_lat| sum|k_lat| + 1104 2^-23 1.07 sum|q k|) + 2^-23 max|e|, k the value with
+           its scale 2^e, which is added to the score's exponent
   weights  e^{s - M} is off by 2 ds + 2^-20. For the product with the stored values c = v / s_j the weight
            w = e^{s - M} s_j goes to fp16 and then into an e4m3 and, its remainder, an e5m2: off by at most
            2^-4 2^-3 w + 2^-11 w, and where w is below the e4m3's normal range (2^-6 in the row's unit) by 2^-10 2^-3,
-           or half of e5m2's last step, 2^-17. The unit follows the weights of each tile of 64 cached rows, whose
-           largest one is 2^-1 of it or more: (2^-13 + 2^-17) 2 < 2^-11.9 of the tile's largest weight
+           or half of e5m2's last step, 2^-17: 2^-12.9 of the unit in all. The unit is at most twice the largest
+           weight of the current window of 4 tiles of 64 cached rows or of the one before it (after each window whose
+           largest is less than half of it, it is set to less than that largest), the windows counting from any
+           tile: of the 7 tiles before a tile and the 3 behind it; and at least 2^-43 of the largest weight of all
   sums     2 n 2^-23 in all, n the keys
   o        |do| <= (2^-7 + 2^-11 + 4 ds + 2 n 2^-23 + 2^-18) sum p|v| / sum p
-                   + 2^-11.9 sum_tiles max(p s) sum|c| / sum p + 2^-8 |o|     (1.02 for second-order terms)
+                   + 2^-11.9 sum_tiles (max(p s) of those tiles + 2^-42 of all) sum|c| / sum p + 2^-8 |o|
+           (1.02 for second-order terms)
   lse      |d| <= ds + 2 n 2^-23 + 2^-20 + 2^-22 |lse|
 """
 import torch
@@ -88,6 +92,7 @@ def attend(q, c, s, scale, seen):
     x = torch.where(seen, scale * (q @ k.T), torch.full((), float("-inf"), dtype=torch.float64, device=q.device))
     part = 2.0 ** -17.8 * q[:, :LATENT].abs().amax(1, keepdim=True) * k[:, :LATENT].abs().sum(1)
     ds = scale * torch.where(seen, part + 1104 * 1.07 * STEP32 * (q.abs() @ k.abs().T), torch.zeros_like(x)).amax(1)
+    ds = ds + STEP32 * s.log2().abs().amax()
     top = x.amax(1, keepdim=True)
     any_ = torch.isfinite(top)
     p = torch.exp(x - torch.where(any_, top, torch.zeros_like(top)))
@@ -99,7 +104,8 @@ def attend(q, c, s, scale, seen):
     pad = -n % TILE
     w = torch.nn.functional.pad(p * s, (0, pad)).view(R, -1, TILE).amax(2)
     size = torch.nn.functional.pad(c[:, :LATENT].abs(), (0, 0, 0, pad)).view(-1, TILE, LATENT).sum(1)
-    tiles = (w @ size) / safe
+    near = torch.nn.functional.max_pool1d(torch.nn.functional.pad(w, (7, 3))[:, None], 11, 1)[:, 0]
+    tiles = ((near + 2.0 ** -42 * w.amax(1, keepdim=True)) @ size) / safe
     cnt = seen.sum(1).double()
     bo = 1.02 * ((2.0 ** -7 + 2.0 ** -11 + 4 * ds + 2 * cnt * STEP32 + 2.0 ** -18)[:, None] * ab + 2.0 ** -11.9 * tiles +
                  U_BF16 * o.abs())
