@@ -33,37 +33,44 @@ namespace kda {
 namespace {
 
 constexpr uint32_t kChunk8 = kKvTile * 128;     // 64 rows of 128 bytes: 128 latents, or the positional key
-constexpr int kChunks = 5;                      // of a tile: the positional key, then 512 latents
-constexpr int kMaxSlots = 24, kScaleSlots = 8, kAhead = 4;
-constexpr int kThreads8 = 384;                  // 8 softmax warps, score issue, value issue, TMA, scales
+constexpr int kChunks = 5;                      // of a tile: 512 latents, then the positional key
+constexpr uint32_t kTile8 = kChunks * kChunk8;
+constexpr int kMaxSlots = 4;
+constexpr int kThreads8 = 384;                  // 8 softmax warps, score issue, value issue, TMA, none
+// Registers of a softmax thread and of the others: 384 threads are launched with 168 each, 64512 in all
+constexpr int kRegsSoftmax = 208, kRegsIssue = 80;
+static_assert(256 * kRegsSoftmax + 128 * kRegsIssue <= 384 * 168, "the shares' sum");
 constexpr int kMostRows8 = 96;                  // query rows of a CTA
-constexpr float kSet = 2.5f, kHigh = 8.75f, kLow = -1.0f, kReach = 40.0f;
+constexpr float kSet = 2.5f, kHigh = 8.75f, kReach = 40.0f;  // powers of two
+constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and what is low
 constexpr int kWindow = 4;                      // tiles over which a row's weights have to be low
 constexpr int kBad = 8;                         // stretches that the loads may be ahead of the output
 
 struct Geom8 : SplitGeom {
     int32_t form;  // query rows of a CTA: 0 up to 32, 1 up to 64, 2 up to 96
-    int32_t np;    // ring slots
     uint32_t smem;
 };
+
+// tiles that the ring holds beside Q and W
+constexpr int tiles_in(int form) { return 4 - form; }
 
 struct Args8 : SplitArgs {
     CUtensorMap map;
     const __nv_bfloat16 *q_lat, *q_pe;
     const uint8_t *rows;
     int64_t page_stride;
-    int32_t rb;  // rows of a TMA box (64, 32 or 16)
+    int32_t rb;  // rows of a TMA box: 64 (it then takes all chunks), 32 or 16
     float c;     // log2(e) scale
     Geom8 geo;
 };
 
 struct Smem8 {
-    uint64_t q_ready, s_full[2], s_free[2], p_full, pv_done, drained;
-    uint64_t full[kMaxSlots], empty[kMaxSlots], sc_full[kScaleSlots], sc_empty[kScaleSlots];
-    float sc[kScaleSlots][3][kKvTile];  // of a tile's rows: scale, its exponent, its reciprocal
+    uint64_t q_ready, s_full[2], s_free[2], p_full[2], drained;
+    uint64_t full[kMaxSlots], done[kMaxSlots];  // a tile is there; its products are through
+    float sc[kMaxSlots][kKvTile];       // scales of a tile's rows
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
-    float2 half[2][128];                // by query row: the halves' maxima (of a tile, and since the last look), or sums
+    float half[2][128], recent[2][128]; // by query row: the halves' maxima or sums, and largest weights of a window
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
@@ -81,9 +88,26 @@ __device__ __forceinline__ void mma8(uint32_t d, uint32_t a_lo, uint32_t b_lo, u
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
         "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "n"(tma::kDescHi));
 }
-// 4 bytes global -> shared, in this thread's asynchronous groups
-__device__ __forceinline__ void copy4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(tc::smem_addr(dst)), "l"(src) : "memory");
+// whether the phase of this parity has ended, without waiting: asked for early, used with wait_warp later
+__device__ __forceinline__ bool peek(uint64_t *mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done)
+                 : "r"(tc::smem_addr(mbar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool wait_peeked(bool there, uint64_t *mbar, uint32_t parity) {
+    return __all_sync(0xffffffffu, there) || tma::wait_warp(mbar, parity);
+}
+// 16 TMEM lanes and 32 columns as a warp's fragments: x[4 g + 0, 1] are columns 8 g + 2 (lane % 4) + 0, 1 of TMEM lane
+// lane / 4, x[4 g + 2, 3] the same of TMEM lane 8 + lane / 4. Without the wait
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 // Two weights (a first) as two bytes of e4m3 (into the low half of hi) and two of e5m2, their rest
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -102,16 +126,19 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     constexpr int MS = FORM == 0 ? 64 : 128;   // M of the score product
     constexpr bool kStack = FORM < 2;          // hi and lo rows in one product
-    constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, the lane of lo behind hi)
-    constexpr int kCols = kStack ? 16 : 32;    // cached rows of a tile that a softmax thread takes
+    constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, where lo lies behind hi)
+    constexpr int kR = FORM == 1 ? 2 : 1;          // query rows of a softmax thread,
+    constexpr int kC = kStack ? 8 : 32;            // and cached rows of a tile for each
+    constexpr int kTiles = tiles_in(FORM);
     const Geom8 &geo = p.geo;
     // Q: four chunks of 128 latents of hi (and lo, stacked; else four of lo behind), then the positional part
     const uint32_t q_chunk = (uint32_t)(kStack ? MS : geo.rows) * 128;
     constexpr int q_chunks = kStack ? 5 : 9;
     uint8_t *s_q = base;                          // M = 128 reads of fewer rows run on into what follows,
     uint8_t *s_p = s_q + q_chunks * q_chunk;      // rows of S that nobody reads
-    uint8_t *s_ring = s_p + (uint32_t)geo.npad * 128;  // W: npad rows of 64 bytes of e4m3, then 64 of e5m2
-    Smem8 &sm = *reinterpret_cast<Smem8 *>(s_ring + (uint32_t)geo.np * kChunk8);
+    const uint32_t p_bytes = (uint32_t)geo.npad * 128;  // W, twice: npad rows of 64 bytes of e4m3, then 64 of e5m2
+    uint8_t *s_ring = s_p + 2 * p_bytes;
+    Smem8 &sm = *reinterpret_cast<Smem8 *>(s_ring + kTiles * kTile8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % geo.RT, g = blockIdx.x / geo.RT;
 
@@ -125,12 +152,9 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             for (int i = 0; i < kBad; ++i) sm.bad[i] = 0;
             tc::mbar_init(&sm.q_ready, kSoftmaxThreads / 32);
             for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_free[i], kSoftmaxThreads / 32);
-            tc::mbar_init(&sm.p_full, kSoftmaxThreads / 32);
-            tc::mbar_init(&sm.pv_done, 1);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_full[i], kSoftmaxThreads / 32);
             tc::mbar_init(&sm.drained, 2);
-            for (int i = 0; i < geo.np; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.empty[i], 1);
-            for (int i = 0; i < kScaleSlots; ++i)
-                tc::mbar_init(&sm.sc_full[i], 1), tc::mbar_init(&sm.sc_empty[i], kSoftmaxThreads / 32);
+            for (int i = 0; i < kTiles; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.done[i], 1);
             tc::mbar_init_fence();
         }
     } else if (warp == 8) {
@@ -145,232 +169,190 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
-    if (warp == 10) {
-        // ---- TMA producer: one thread ----
-        if (tma::elect()) {
-            Walk w;
-            w.start(p, sm.run);
-            w.skip_idle(p);
-            int seg = 0, ps = 0, pph = 0;
-            const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
-            while (!w.done() && ok) {
-                const int32_t *entry = p.table + (int64_t)w.n * p.max_pages;
-                const int64_t row0 = (int64_t)w.j0 * kKvTile;
-                entry += row0 / p.page_size;
-                int32_t at = (int32_t)(row0 % p.page_size);  // row within the page
-                // the places of a tile's boxes, fetched one tile ahead; nothing past the sequence's rows is looked up
-                int32_t pg[4], ry[4], pg_next[4], ry_next[4];
-                auto look = [&](int j) {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        pg_next[b] = 0;
-                        ry_next[b] = at;
-                        if (b < sub && j < w.j1 && (int64_t)j * kKvTile + b * p.rb < w.len) {
-                            pg_next[b] = *entry;
-                            at += p.rb;
-                            if (at == p.page_size) at = 0, ++entry;
-                        }
-                    }
-                };
-                look(w.j0);
-                sm.bad[seg % kBad] = 0;
-                for (int j = w.j0; j < w.j1 && ok; ++j) {
-                    bool bad = false;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        ry[b] = ry_next[b];
-                        const bool out = (uint32_t)pg_next[b] >= (uint32_t)p.num_pages;
-                        bad |= out;
-                        pg[b] = out ? INT32_MAX : pg_next[b];  // past every page: loads as zeros
-                    }
-                    if (bad) {
-                        sm.bad[seg % kBad] = 1;
-                        set_status(p.status, KDA_ERR_PAGES);
-                    }
-                    look(j + 1);
-                    if (FORM == 2 && j + 1 < w.j1) {
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsIssue));
+        if (warp == 10) {
+            // ---- TMA producer: one thread ----
+            if (tma::elect()) {
+                Walk w;
+                w.start(p, sm.run);
+                w.skip_idle(p);
+                int seg = 0, ps = 0, pph = 0;
+                const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
+                while (!w.done() && ok) {
+                    const int32_t *entry = p.table + (int64_t)w.n * p.max_pages;
+                    const int64_t row0 = (int64_t)w.j0 * kKvTile;
+                    entry += row0 / p.page_size;
+                    int32_t at = (int32_t)(row0 % p.page_size);  // row within the page
+                    // the places of a tile's boxes, fetched one tile ahead; nothing past the sequence's rows is looked up
+                    int32_t pg[4], ry[4], pg_next[4], ry_next[4];
+                    auto look = [&](int j) {
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
-                            if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
-                                tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow8,
-                                                 (uint32_t)p.rb * kRow8);
-                        }
-                    }
-                    const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
-                    const uint32_t box = (uint32_t)p.rb * 128;
-                    for (int i = 0; i < kChunks; ++i) {
-                        ok = tc::mbar_wait(&sm.empty[ps], pph ^ 1);
-                        if (!ok) break;
-                        tc::mbar_arrive_expect_tx(&sm.full[ps], boxes * box);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (b < boxes)
-                                tma::load_3d(s_ring + ps * kChunk8 + b * box, &p.map, &sm.full[ps], i == 0 ? kLatent : 128 * (i - 1),
-                                             ry[b], pg[b]);
-                        ++sm.issued;
-                        if (++ps == geo.np) ps = 0, pph ^= 1;
-                    }
-                }
-                ++seg;
-                w.next(p);
-                w.skip_idle(p);
-            }
-            if (!ok) sm.failed = 1;
-        }
-        __syncwarp();
-    } else if (warp == 11) {
-        // ---- the rows' scales: kAhead tiles' copies in flight, two rows a lane ----
-        Walk w, done;  // the tile whose copy is issued, and the one that is handed over
-        w.start(p, sm.run);
-        w.skip_idle(p);
-        done = w;
-        int j = w.j0, jd = w.j0, k = 0, kd = 0;
-        auto step = [&](Walk &x, int &at) {
-            if (++at >= x.j1) {
-                x.next(p);
-                x.skip_idle(p);
-                at = x.j0;
-            }
-        };
-        while (!done.done()) {
-            if (!w.done()) {
-                if (ok) ok = tma::wait_warp(&sm.sc_empty[k % kScaleSlots], ((k / kScaleSlots) & 1) ^ 1);
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t row = (int64_t)j * kKvTile + 32 * i + lane;
-                    float *dst = &sm.sc[k % kScaleSlots][0][32 * i + lane];
-                    const uint32_t entry = (uint32_t)row / (uint32_t)p.page_size;
-                    const int32_t page = row < w.len ? p.table[(int64_t)w.n * p.max_pages + entry] : -1;
-                    if ((uint32_t)page < (uint32_t)p.num_pages)
-                        copy4(dst, p.rows + page * p.page_stride + (int64_t)p.page_size * kRow8 +
-                                       4 * ((uint32_t)row - entry * (uint32_t)p.page_size));
-                    else
-                        *dst = 1.f;
-                }
-                step(w, j);
-                ++k;
-            }
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
-            if (k < kAhead && !w.done()) continue;
-            if (w.done())
-                asm volatile("cp.async.wait_all;\n" ::: "memory");
-            else
-                asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
-            // every lane looks at what it copied itself
-            float(&sc)[3][kKvTile] = sm.sc[kd % kScaleSlots];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = 32 * i + lane;
-                const uint32_t bits = __float_as_uint(sc[0][at]);
-                sc[1][at] = (float)((int)(bits >> 23) - 127);
-                sc[2][at] = __uint_as_float(0x7F000000u - bits);  // 2^-e
-            }
-            tma::arrive_warp(&sm.sc_full[kd % kScaleSlots]);
-            step(done, jd);
-            ++kd;
-        }
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-        if (!ok && lane == 0) sm.failed = 1;
-    } else if (warp == 8) {
-        // ---- score products: one thread ----
-        if (tma::elect()) {
-            constexpr uint32_t id = idesc8(MS, kKvTile, 0, 0), id_pe = tma::idesc(MS, kKvTile, 0, 0);
-            const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), ring_lo = tma::lo_k(tc::smem_addr(s_ring)), q_step = q_chunk >> 4;
-            Walk w;
-            w.start(p, sm.run);
-            w.skip_idle(p);
-            int k = 0, seg = 0, ps = 0, pph = 0;
-            while (!w.done() && ok) {
-                ok = tc::mbar_wait(&sm.q_ready, seg & 1);
-                for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
-                    ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1);
-                    const uint32_t d = t_s + (k & 1) * kKvTile;
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        ok = ok && tc::mbar_wait(&sm.full[ps], pph);
-                        if (!ok) break;
-                        if (i == 0) tc::fence_after_sync();
-                        const uint32_t b = ring_lo + ps * (kChunk8 >> 4);
-                        if (i == 0) {
-                            const uint32_t a = q_lo + (q_chunks - 1) * q_step;
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) tma::mma_ss(d, a + 2 * s, b + 2 * s, id_pe, s != 0);
-                            tc::commit(&sm.empty[ps]);
-                        } else {
-                            const uint32_t a = q_lo + (i - 1) * q_step;
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) {
-                                mma8(d, a + 2 * s, b + 2 * s, id, 1);
-                                if (!kStack) mma8(d, a + 4 * q_step + 2 * s, b + 2 * s, id, 1);
+                            pg_next[b] = 0;
+                            ry_next[b] = at;
+                            if (b < sub && j < w.j1 && (int64_t)j * kKvTile + b * p.rb < w.len) {
+                                pg_next[b] = *entry;
+                                at += p.rb;
+                                if (at == p.page_size) at = 0, ++entry;
                             }
                         }
-                        if (++ps == geo.np) ps = 0, pph ^= 1;
-                    }
-                    if (!ok) break;
-                    tc::commit(&sm.s_full[k & 1]);
-                }
-                ++seg;
-                w.next(p);
-                w.skip_idle(p);
-            }
-            if (!ok) sm.failed = 1;
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ---- value products: one thread ----
-        if (tma::elect()) {
-            const uint32_t id_hi = idesc8(128, geo.npad, 0, 1), id_lo = idesc8(128, geo.npad, 1, 1);
-            const uint32_t ring_lo = tma::lo_mn(tc::smem_addr(s_ring), kChunk8), p_lo = tma::lo_k(tc::smem_addr(s_p));
-            Walk w;
-            w.start(p, sm.run);
-            w.skip_idle(p);
-            int k = 0, ps = 0;
-            while (!w.done() && ok) {
-                for (int j = w.j0; j < w.j1; ++j, ++k) {
-                    ok = tc::mbar_wait(&sm.p_full, k & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const bool two = w.len - j * kKvTile > 32;  // steps of 32 cached rows
-                    const uint32_t more = ((j - w.j0) & (kFold - 1)) != 0;
-                    uint32_t d = tmem;
-                    if (++ps == geo.np) ps = 0;  // the positional chunk
+                    };
+                    look(w.j0);
+                    sm.bad[seg % kBad] = 0;
+                    for (int j = w.j0; j < w.j1 && ok; ++j) {
+                        bool bad = false;
 #pragma unroll
-                    for (int i = 0; i < kChunks - 1; ++i) {
-                        const uint32_t a = ring_lo + ps * (kChunk8 >> 4);
-                        mma8(d, a, p_lo, id_hi, more);
-                        mma8(d, a, p_lo + 4, id_lo, 1);
-                        if (two) {
-                            mma8(d, a + 256, p_lo + 2, id_hi, 1);
-                            mma8(d, a + 256, p_lo + 6, id_lo, 1);
+                        for (int b = 0; b < 4; ++b) {
+                            ry[b] = ry_next[b];
+                            const bool out = (uint32_t)pg_next[b] >= (uint32_t)p.num_pages;
+                            bad |= out;
+                            pg[b] = out ? INT32_MAX : pg_next[b];  // past every page: loads as zeros
                         }
-                        tc::commit(&sm.empty[ps]);
-                        d += geo.npad;
-                        if (++ps == geo.np) ps = 0;
+                        if (bad) {
+                            sm.bad[seg % kBad] = 1;
+                            set_status(p.status, KDA_ERR_PAGES);
+                        }
+                        look(j + 1);
+                        if (FORM == 2 && j + 1 < w.j1) {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
+                                if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
+                                    tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow8,
+                                                     (uint32_t)p.rb * kRow8);
+                            }
+                        }
+                        const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
+                        ok = tc::mbar_wait(&sm.done[ps], pph ^ 1);
+                        if (!ok) break;
+                        uint8_t *dst = s_ring + ps * kTile8;
+                        // the rows' scales stand behind the page's rows; of a page that is not there, none are loaded
+                        uint32_t scales = 0;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b < boxes && pg[b] != INT32_MAX) scales += 4 * p.rb;
+                        tc::mbar_arrive_expect_tx(&sm.full[ps], kChunks * boxes * p.rb * 128 + scales);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b < boxes && pg[b] != INT32_MAX)
+                                tc::bulk_g2s(&sm.sc[ps][b * p.rb], p.rows + pg[b] * p.page_stride + (int64_t)p.page_size * kRow8 + 4 * ry[b],
+                                             4 * p.rb, &sm.full[ps]);
+                        if (p.rb == kKvTile) {
+                            tma::load_4d(dst, &p.map, &sm.full[ps], 0, ry[0], 0, pg[0]);
+                        } else {
+                            const uint32_t box = (uint32_t)p.rb * 128;
+                            for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                                for (int b = 0; b < 4; ++b)
+                                    if (b < boxes) tma::load_4d(dst + i * kChunk8 + b * box, &p.map, &sm.full[ps], 0, ry[b], i, pg[b]);
+                        }
+                        ++sm.issued;
+                        if (++ps == kTiles) ps = 0, pph ^= 1;
                     }
-                    tc::commit(&sm.pv_done);
+                    ++seg;
+                    w.next(p);
+                    w.skip_idle(p);
                 }
-                w.next(p);
-                w.skip_idle(p);
+                if (!ok) sm.failed = 1;
             }
-            if (!ok) sm.failed = 1;
+            __syncwarp();
+        } else if (warp == 8) {
+            // ---- score products: one thread ----
+            if (tma::elect()) {
+                constexpr uint32_t id = idesc8(MS, kKvTile, 0, 0), id_pe = tma::idesc(MS, kKvTile, 0, 0);
+                const uint32_t q_lo = tma::lo_k(tc::smem_addr(s_q)), ring_lo = tma::lo_k(tc::smem_addr(s_ring)), q_step = q_chunk >> 4;
+                Walk w;
+                w.start(p, sm.run);
+                w.skip_idle(p);
+                int k = 0, seg = 0, ps = 0, pph = 0;
+                while (!w.done() && ok) {
+                    ok = tc::mbar_wait(&sm.q_ready, seg & 1);
+                    for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
+                        ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1);
+                        const uint32_t d = t_s + (k & 1) * kKvTile;
+                        ok = ok && tc::mbar_wait(&sm.full[ps], pph);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const uint32_t b = ring_lo + ps * (kTile8 >> 4);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            tma::mma_ss(d, q_lo + (q_chunks - 1) * q_step + 2 * s, b + (4 * kChunk8 >> 4) + 2 * s, id_pe, s != 0);
+#pragma unroll
+                        for (int i = 0; i < kChunks - 1; ++i)
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                const uint32_t a = q_lo + i * q_step + 2 * s, bb = b + i * (kChunk8 >> 4) + 2 * s;
+                                mma8(d, a, bb, id, 1);
+                                if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
+                            }
+                        if (++ps == kTiles) ps = 0, pph ^= 1;
+                        tc::commit(&sm.s_full[k & 1]);
+                    }
+                    ++seg;
+                    w.next(p);
+                    w.skip_idle(p);
+                }
+                if (!ok) sm.failed = 1;
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---- value products: one thread ----
+            if (tma::elect()) {
+                const uint32_t id_hi = idesc8(128, geo.npad, 0, 1), id_lo = idesc8(128, geo.npad, 1, 1);
+                const uint32_t ring_lo = tma::lo_mn(tc::smem_addr(s_ring), kChunk8), p_lo = tma::lo_k(tc::smem_addr(s_p));
+                Walk w;
+                w.start(p, sm.run);
+                w.skip_idle(p);
+                int k = 0, ps = 0;
+                while (!w.done() && ok) {
+                    for (int j = w.j0; j < w.j1; ++j, ++k) {
+                        ok = tc::mbar_wait(&sm.p_full[k & 1], (k >> 1) & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const bool two = w.len - j * kKvTile > 32;  // steps of 32 cached rows
+                        const uint32_t more = ((j - w.j0) & (kFold - 1)) != 0;
+                        const uint32_t a0 = ring_lo + ps * (kTile8 >> 4), b = p_lo + (k & 1) * (p_bytes >> 4);
+#pragma unroll
+                        for (int i = 0; i < kChunks - 1; ++i) {
+                            const uint32_t a = a0 + i * (kChunk8 >> 4), d = tmem + i * geo.npad;
+                            mma8(d, a, b, id_hi, more);
+                            mma8(d, a, b + 4, id_lo, 1);
+                            if (two) {
+                                mma8(d, a + 256, b + 2, id_hi, 1);
+                                mma8(d, a + 256, b + 6, id_lo, 1);
+                            }
+                        }
+                        tc::commit(&sm.done[ps]);
+                        if (++ps == kTiles) ps = 0;
+                    }
+                    w.next(p);
+                    w.skip_idle(p);
+                }
+                if (!ok) sm.failed = 1;
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        // ---- softmax: a thread takes a query row and kCols cached rows of a tile; then the output ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsSoftmax));
+        // ---- softmax: a thread takes kC cached rows of a tile for each of kR query rows; then the output ----
         const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const int i_row = lane & (kRowsQ - 1);                  // row of the quarter
-        const int h = kStack ? (lane >> (FORM == 0 ? 3 : 4)) & 1 : 0;  // stacked: lane of hi or of lo
-        const bool low = FORM != 0 || lane < 16;                // lanes that hold rows of S
-        const bool lead = low && h == 0;                        // one lane a row
-        const int r = quarter * kRowsQ + i_row;
-        const bool owner = low && r < rows_here, warp_rows = quarter * kRowsQ < rows_here;
-        const int unseen = p.m - 1 - (row_first + (owner ? r : 0)) / p.H;  // last cached rows that the row does not see
-        const int col0 = 32 * set + (kStack ? 16 * h : 0);
-        uint8_t *p_row = s_p + r * 128;
-        int k = 0, seg = 0, ps = 0;  // tiles and stretches worked on, ring slot
+        const bool lead = !kStack || (lane & 3) == 0;  // one lane a row
+        int r[kR], unseen[kR];                         // the rows, and the last cached rows that each does not see
+        bool owner[kR];
+#pragma unroll
+        for (int y = 0; y < kR; ++y) {
+            r[y] = quarter * kRowsQ + (kStack ? lane / 4 + 8 * y : lane);
+            owner[y] = r[y] < rows_here;
+            unseen[y] = p.m - 1 - (row_first + (owner[y] ? r[y] : 0)) / p.H;
+        }
+        const bool warp_rows = quarter * kRowsQ < rows_here;
+        // column of a tile of value e
+        auto col = [&](int e) { return 32 * set + (kStack ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e); };
+        int k = 0, seg = 0;  // tiles and stretches worked on
+        // the products of tile t are through: waited for in every tile for the one before the last, so that none is passed over
+        auto through = [&](int t) { return tma::wait_warp(&sm.done[t % kTiles], (t / kTiles) & 1); };
         // Q of a stretch, a row a warp at a time; the last stretch's score products are through: its last tile was taken
         auto load_q = [&](const Walk &s) {
             const int64_t row0 = (int64_t)s.n * geo.R + row_first;
@@ -418,6 +400,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             fence_proxy_async();
             tma::arrive_warp(&sm.q_ready);
         };
+        bool tile_there = false, s_there = false;  // the next tile and its scores
         Walk w;
         w.start(p, sm.run);
         {
@@ -427,112 +410,194 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             named_sync(2, kSoftmaxThreads);
         }
         for (; !w.done() && ok; w.next(p)) {
-            float m_ref = -INFINITY, m_top = -INFINITY, l = 0.f;
-            float recent = -INFINITY;  // the largest since the last look at low weights
+            float m_ref[kR], m_top[kR], l[kR];
+            float recent[kR];  // the largest weight of the window, and at its end of the whole row
+            bool faint[kR];    // the last window's weights were low
+            float m_kept[kR], l_kept[kR];  // reference and denominator of the tiles before the last kFold
+#pragma unroll
+            for (int y = 0; y < kR; ++y) m_ref[y] = m_top[y] = m_kept[y] = -INFINITY, l[y] = l_kept[y] = recent[y] = 0.f, faint[y] = false;
             // the stretch's place among the partials: a run's first stretch, where it continues a sequence, has
             // the first, the last one, which the run's end cuts, the second; before that any other may use it
             const int64_t part0 = (((int64_t)2 * g + (w.j0 == 0 ? 1 : 0)) * geo.RT + rt) * geo.npad;
-            float m_kept = -INFINITY, l_kept = 0.f;  // reference and denominator of the tiles before the last kFold
             if (w.work) {
-                const float c = owner ? sm.row_c[r] : 0.f;
-                const uint64_t c2 = pk2(c, c);
+                float c[kR];
+#pragma unroll
+                for (int y = 0; y < kR; ++y) c[y] = owner[y] ? sm.row_c[r[y]] : 0.f;
                 bool stopped = false;
                 for (int js = w.j0; !stopped; js += kFold) {
                     if (js > w.j0 && w.j1 - w.j0 > kFold) {
                         // kFold tiles, or the last ones, are in O^T (also with a failed wait: all warps meet these barriers)
-                        ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
+                        ok = through(k - 1) && ok;
                         const bool start = js == w.j0 + kFold;
                         named_sync(2, kSoftmaxThreads);  // the factors have been read
-                        if (set == 0 && lead) sm.factor[r] = start || m_kept == m_ref ? 1.0f : tc::ex2(m_kept - m_ref);
+#pragma unroll
+                        for (int y = 0; y < kR; ++y)
+                            if (set == 0 && lead) sm.factor[r[y]] = start || m_kept[y] == m_ref[y] ? 1.0f : tc::ex2(m_kept[y] - m_ref[y]);
                         named_sync(2, kSoftmaxThreads);
                         for (int i = 2 * set; i < 2 * set + 2; ++i) {
                             float *kept = p.part_o + part0 * kLatent + 128 * i + 32 * quarter + lane;
                             fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
                         }
-                        m_kept = m_ref;
-                        if (low) l_kept = l_kept * sm.factor[r] + l;
-                        l = js >= w.j1 ? l_kept : 0.f;
+#pragma unroll
+                        for (int y = 0; y < kR; ++y) {
+                            m_kept[y] = m_ref[y];
+                            l_kept[y] = l_kept[y] * sm.factor[r[y]] + l[y];
+                            l[y] = js >= w.j1 ? l_kept[y] : 0.f;
+                        }
                     }
                     if (js >= w.j1) break;
                     const int je = min(w.j1, js + kFold);
                     for (int j = js; j < je; ++j) {
-                        const int slot = k % kScaleSlots;
-                        ok = tma::wait_warp(&sm.sc_full[slot], (k / kScaleSlots) & 1) && ok;
-                        ok = tma::wait_warp(&sm.s_full[k & 1], (k >> 1) & 1) && ok;
+                        const int slot = k % kTiles;
+                        const bool first = j == w.j0;
+                        const bool old_there = k < 2 || peek(&sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1);
+                        ok = wait_peeked(tile_there, &sm.full[slot], (k / kTiles) & 1) && ok;
+                        float sc[kC], v[kR][kC];  // the scales; scores, then weights
+                        auto scales = [&] {
+#pragma unroll
+                            for (int e = 0; e < kC; e += 2) *reinterpret_cast<float2 *>(&sc[e]) = *reinterpret_cast<const float2 *>(&sm.sc[slot][col(e)]);
+                            // behind the sequence they count as one: 0 times what stands there may be NaN
+                            if (w.len - j * kKvTile < kKvTile) {
+#pragma unroll
+                                for (int e = 0; e < kC; ++e)
+                                    if (col(e) >= w.len - j * kKvTile) sc[e] = 1.f;
+                            }
+                        };
+                        scales();
+                        ok = wait_peeked(s_there, &sm.s_full[k & 1], (k >> 1) & 1) && ok;
                         // a failed wait still meets the barriers below, so that no warp is left in them
                         if (ok) tc::fence_after_sync();
-                        uint32_t s[32];
-                        const bool first = j == w.j0;
-                        float top = -INFINITY;
-                        if (warp_rows && ok) {
-                            tc::tmem_ld32_nowait(t_s + lanes + (k & 1) * kKvTile + set * 32, s);
-                            tc::tmem_wait_ld();
-                            tc::fence_before_sync();
-                        }
-                        tma::arrive_warp(&sm.s_free[k & 1]);
-                        if (warp_rows && ok) {
-                            if constexpr (kStack) {
-                                // hi + lo: the lanes trade halves, and each keeps 16 columns
+                        const uint32_t s_at = t_s + lanes + (k & 1) * kKvTile + set * 32;
+                        const bool live = warp_rows && ok;
+                        float sum[kR], most[kR];
+                        auto scores = [&] {  // of this thread's rows, as powers of two; rounded here, so that huge ones still differ by 0 from themselves
+                            if constexpr (FORM == 2) {
+                                uint32_t x[32];
+                                tc::tmem_ld32_nowait(s_at, x);
+                                tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const float mine = __uint_as_float(h ? s[16 + e] : s[e]), yours = __uint_as_float(h ? s[e] : s[16 + e]);
-                                    s[e] = __float_as_uint(mine + __shfl_xor_sync(0xffffffffu, yours, kRowsQ));
+                                for (int e = 0; e < 32; ++e) v[0][e] = __uint_as_float(x[e]);
+                            } else if constexpr (FORM == 1) {
+                                uint32_t hi[16], lo[16];
+                                tmem_ld_16x32(s_at, hi);
+                                tmem_ld_16x32(s_at + (16u << 16), lo);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    v[(e >> 1) & 1][2 * (e >> 2) + (e & 1)] = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
+                            } else {
+                                uint32_t x[16];
+                                tmem_ld_16x32(s_at, x);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    v[0][e] = __uint_as_float(x[4 * (e >> 1) + (e & 1)]) + __uint_as_float(x[4 * (e >> 1) + 2 + (e & 1)]);
+                            }
+                            tc::fence_before_sync();
+#pragma unroll
+                            for (int y = 0; y < kR; ++y) {
+#pragma unroll
+                                for (int e = 0; e < kC; e += 2) {
+                                    const float2 t = upk2(mul2(mul2(pk2(v[y][e], v[y][e + 1]), pk2(sc[e], sc[e + 1])), pk2(c[y], c[y])));
+                                    v[y][e] = t.x, v[y][e + 1] = t.y;
+                                }
+                                const int seen = w.len - j * kKvTile - unseen[y];  // cached rows of the tile that the row sees
+                                if (__any_sync(0xffffffffu, seen < kKvTile)) {
+#pragma unroll
+                                    for (int e = 0; e < kC; ++e)
+                                        if (col(e) >= seen) v[y][e] = -INFINITY;
                                 }
                             }
-                            // x + e: the weight's exponent with its row's scale
+                        };
+                        auto weights = [&] {
 #pragma unroll
-                            for (int e = 0; e < kCols; e += 4) {
-                                const float4 sc = *reinterpret_cast<const float4 *>(&sm.sc[slot][0][col0 + e]);
-                                const float4 ex = *reinterpret_cast<const float4 *>(&sm.sc[slot][1][col0 + e]);
-                                const float2 a = upk2(fma2(mul2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pk2(sc.x, sc.y)), c2, pk2(ex.x, ex.y)));
-                                const float2 b = upk2(fma2(mul2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), pk2(sc.z, sc.w)), c2, pk2(ex.z, ex.w)));
-                                s[e] = __float_as_uint(a.x), s[e + 1] = __float_as_uint(a.y);
-                                s[e + 2] = __float_as_uint(b.x), s[e + 3] = __float_as_uint(b.y);
+                            for (int y = 0; y < kR; ++y) {
+                                const float mb = m_ref[y] == -INFINITY ? 0.f : -m_ref[y];
+                                const uint64_t mb2 = pk2(mb, mb);
+                                uint64_t l2[2] = {0, 0};
+                                most[y] = 0.f;
+#pragma unroll
+                                for (int e = 0; e < kC; e += 2) {
+                                    const float2 x = upk2(add2(pk2(v[y][e], v[y][e + 1]), mb2));
+                                    const uint64_t pp = pk2(tc::ex2(x.x), tc::ex2(x.y));
+                                    l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], pp);
+                                    const float2 ww = upk2(mul2(pp, pk2(sc[e], sc[e + 1])));
+                                    v[y][e] = ww.x, v[y][e + 1] = ww.y;
+                                    most[y] = fmaxf(most[y], fmaxf(ww.x, ww.y));
+                                }
+                                const float2 ls = upk2(add2(l2[0], l2[1]));
+                                sum[y] = ls.x + ls.y;
                             }
-                            // cached rows of this thread's part that the row sees
-                            const int64_t seen = (int64_t)w.len - unseen - ((int64_t)j * kKvTile + col0);
-                            if (__any_sync(0xffffffffu, seen < kCols)) {
+                        };
 #pragma unroll
-                                for (int e = 0; e < kCols; ++e)
-                                    if (e >= seen) s[e] = 0xff800000u;
-                            }
-#pragma unroll
-                            for (int e = 0; e < kCols; e += 2)
-                                top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                        for (int y = 0; y < kR; ++y) sum[y] = most[y] = 0.f;
+                        if (live) {
+                            scores();
+                            if (!first) weights();
                         }
-                        // one barrier a tile: may a row need a new reference, did a wait fail
+                        // one barrier a tile: does a row need a new reference, did a wait fail
                         const bool look = ((j - w.j0) & (kWindow - 1)) == kWindow - 1;
-                        recent = fmaxf(recent, top);
-                        const bool may = owner && (first || top - m_ref > kHigh ||
-                                                   (look && recent - m_ref < kLow && m_ref > m_top - kReach));
-                        const bool any = softmax_any(may || !ok);
-                        if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
-                        if (any) {
-                            if constexpr (kStack) {
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, kRowsQ));
-                                recent = fmaxf(recent, __shfl_xor_sync(0xffffffffu, recent, kRowsQ));
+                        bool may = first || !ok;
+#pragma unroll
+                        for (int y = 0; y < kR; ++y) {
+                            recent[y] = fmaxf(recent[y], most[y]);
+                            may |= owner[y] && (most[y] > kMost || faint[y] || (m_ref[y] == -INFINITY && w.len - j * kKvTile - unseen[y] > 0));
+                            if (look) {
+                                if constexpr (kStack) {
+                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 1));
+                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 2));
+                                }
+                                if (lead) sm.recent[set][r[y]] = recent[y];
                             }
-                            if (lead) sm.half[set][r] = make_float2(top, recent);
+                        }
+                        const bool any = softmax_any(may);
+                        bool again = false, anew[kR];
+#pragma unroll
+                        for (int y = 0; y < kR; ++y) anew[y] = false;
+                        if (k > 1) ok = wait_peeked(old_there, &sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1) && ok;
+                        if (any) {
+                            if (k > 0) ok = through(k - 1) && ok;
+                            // the largest exponent of a weight in this tile, over a row's threads
+                            float top[kR];
+                            scales();
+                            if (live && !first) scores();
+#pragma unroll
+                            for (int y = 0; y < kR; ++y) {
+                                top[y] = -INFINITY;
+                                if (live) {
+#pragma unroll
+                                    for (int e = 0; e < kC; ++e)
+                                        top[y] = fmaxf(top[y], v[y][e] + (float)((int)(__float_as_uint(sc[e]) >> 23) - 127));  // with its row's exponent
+                                }
+                                if constexpr (kStack) {
+                                    top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
+                                    top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
+                                }
+                                if (lead) sm.half[set][r[y]] = top[y];
+                            }
                             // all stop together when any wait failed
                             if (softmax_any(!ok)) {
                                 ok = false;
                                 stopped = true;
                                 break;
                             }
-                            if (low) {
-                                const float2 other = sm.half[set ^ 1][r];
-                                top = fmaxf(top, other.x);
-                                recent = fmaxf(recent, other.y);
+                            again = false;
+#pragma unroll
+                            for (int y = 0; y < kR; ++y) {
+                                top[y] = fmaxf(top[y], sm.half[set ^ 1][r[y]]);
+                                m_top[y] = fmaxf(m_top[y], top[y]);
+                                const bool up = first || top[y] - m_ref[y] > kHigh;
+                                // of low weights, the window's largest, which is still in sm.recent
+                                const float low = m_ref[y] + __log2f(fmaxf(sm.recent[0][r[y]], sm.recent[1][r[y]]));
+                                const float to = fmaxf((up ? top[y] : fmaxf(top[y], low)) - kSet, m_top[y] - kReach);
+                                anew[y] = up || (faint[y] && to < m_ref[y]);
+                                const float f = anew[y] && !first ? tc::ex2(m_ref[y] - to) : 1.0f;
+                                if (set == 0 && lead) sm.factor[r[y]] = f;
+                                if (anew[y]) m_ref[y] = to;
+                                l[y] *= f;
+                                again |= owner[y] && anew[y] && !first;
                             }
-                            m_top = fmaxf(m_top, recent);
-                            const bool up = first || top - m_ref > kHigh;
-                            const float to = fmaxf((up ? top : recent) - kSet, m_top - kReach);
-                            const bool anew = up || (look && recent - m_ref < kLow && recent > -INFINITY && to < m_ref);
-                            const float f = anew && !first ? tc::ex2(m_ref - to) : 1.0f;
-                            if (set == 0 && lead) sm.factor[r] = f;
-                            if (anew) m_ref = to;
-                            l *= f;
-                            if (softmax_any(owner && anew && !first)) {
+                            if (softmax_any(again)) {
                                 tc::fence_after_sync();
                                 for (int e = 0; e < geo.npad; e += 16) {
                                     float fs[16];
@@ -552,53 +617,66 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 }
                                 tc::tmem_wait_st();
                             }
+                            if (live) weights();
+#pragma unroll
+                            for (int y = 0; y < kR; ++y) recent[y] = anew[y] ? most[y] : recent[y];
                         }
-                        if (look) recent = -INFINITY;
-                        if (warp_rows && ok) {
-                            const float mb = m_ref == -INFINITY ? 0.f : -m_ref;
-                            const uint64_t mb2 = pk2(mb, mb);
-                            uint64_t l2[2] = {0, 0};
+                        tma::arrive_warp(&sm.s_free[k & 1]);
 #pragma unroll
-                            for (int u = 0; u < kCols / 16; ++u) {  // 16-byte units of the row, swizzled
-                                uint32_t hi[4], lo[4];
+                        for (int y = 0; y < kR; ++y) {
+                            faint[y] = false;
+                            if (look) {  // (where this tile has set the reference anew, its weights are not low)
+                                const float both = fmaxf(sm.recent[0][r[y]], sm.recent[1][r[y]]);
+                                faint[y] = !anew[y] && both < kLeast && both > 0.f && m_ref[y] > m_top[y] - kReach;
+                                recent[y] = 0.f;
+                            }
+                        }
+                        // what the next tile waits for
+                        tile_there = peek(&sm.full[(k + 1) % kTiles], ((k + 1) / kTiles) & 1);
+                        s_there = peek(&sm.s_full[(k + 1) & 1], ((k + 1) >> 1) & 1);
+                        if (live) {
+                            uint8_t *w_at = s_p + (k & 1) * p_bytes;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t *x = &s[16 * u + 4 * e];
-                                    const float4 inv = *reinterpret_cast<const float4 *>(&sm.sc[slot][2][col0 + 16 * u + 4 * e]);
-                                    const float2 y = upk2(add2(pk2(__uint_as_float(x[0]), __uint_as_float(x[1])), mb2));
-                                    const float2 z = upk2(add2(pk2(__uint_as_float(x[2]), __uint_as_float(x[3])), mb2));
-                                    const float w0 = tc::ex2(y.x), w1 = tc::ex2(y.y), w2 = tc::ex2(z.x), w3 = tc::ex2(z.y);
-                                    l2[0] = fma2(pk2(w0, w1), pk2(inv.x, inv.y), l2[0]);
-                                    l2[1] = fma2(pk2(w2, w3), pk2(inv.z, inv.w), l2[1]);
-                                    uint32_t h0, h1, l0, l1;
-                                    split2(w0, w1, h0, l0);
-                                    split2(w2, w3, h1, l1);
-                                    hi[e] = h0 | (h1 << 16);
-                                    lo[e] = l0 | (l1 << 16);
-                                }
-                                if (low && r < geo.npad) {
-                                    const int unit = (col0 >> 4) + u;
-                                    *reinterpret_cast<uint4 *>(p_row + ((unit ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                                    *reinterpret_cast<uint4 *>(p_row + (((4 + unit) ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            for (int y = 0; y < kR; ++y) {
+                                l[y] += sum[y];
+                                uint32_t hi[kC / 2], lo[kC / 2];  // two columns each
+#pragma unroll
+                                for (int e = 0; e < kC / 2; ++e) split2(v[y][2 * e], v[y][2 * e + 1], hi[e], lo[e]);
+                                uint8_t *row = w_at + r[y] * 128;
+                                // a 16-byte unit u of the row stands at u ^ (row % 8); the rests are four units behind
+                                if (r[y] < geo.npad) {
+                                    if constexpr (kStack) {
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) {
+                                            const int at = ((2 * set + (e >> 1)) ^ (r[y] & 7)) * 16 + 8 * (e & 1) + 2 * (lane & 3);
+                                            *reinterpret_cast<uint16_t *>(row + at) = (uint16_t)hi[e];
+                                            *reinterpret_cast<uint16_t *>(row + (at ^ 64)) = (uint16_t)lo[e];
+                                        }
+                                    } else {
+#pragma unroll
+                                        for (int u = 0; u < 2; ++u) {
+                                            const int at = ((2 * set + u) ^ (r[y] & 7)) * 16;
+                                            auto four = [&](const uint32_t(&x)[kC / 2]) {
+                                                return make_uint4(x[8 * u] | (x[8 * u + 1] << 16), x[8 * u + 2] | (x[8 * u + 3] << 16),
+                                                                  x[8 * u + 4] | (x[8 * u + 5] << 16), x[8 * u + 6] | (x[8 * u + 7] << 16));
+                                            };
+                                            *reinterpret_cast<uint4 *>(row + at) = four(hi);
+                                            *reinterpret_cast<uint4 *>(row + (at ^ 64)) = four(lo);
+                                        }
+                                    }
                                 }
                             }
-                            const float2 ls = upk2(add2(l2[0], l2[1]));
-                            l += ls.x + ls.y;
                         }
-                        tma::arrive_warp(&sm.sc_empty[slot]);
                         const int valid = min(kKvTile, w.len - j * kKvTile);
                         if (valid & 31) {  // value rows behind the sequence in the product's last step of 32
                             const int units = (-valid & 31) * 8;
-                            for (int u = tid; u < (kChunks - 1) * units; u += kSoftmaxThreads) {
-                                const int at = (ps + 1 + u / units) % geo.np;
-                                reinterpret_cast<uint4 *>(s_ring + at * kChunk8)[valid * 8 + u % units] = make_uint4(0, 0, 0, 0);
-                            }
+                            for (int u = tid; u < (kChunks - 1) * units; u += kSoftmaxThreads)
+                                reinterpret_cast<uint4 *>(s_ring + slot * kTile8 + u / units * kChunk8)[valid * 8 + u % units] =
+                                    make_uint4(0, 0, 0, 0);
                         }
-                        ps += kChunks;
-                        if (ps >= geo.np) ps -= geo.np;
                         fence_proxy_async();
                         tc::fence_before_sync();
-                        tma::arrive_warp(&sm.p_full);
+                        tma::arrive_warp(&sm.p_full[k & 1]);
                         ++k;
                     }
                 }
@@ -607,25 +685,34 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                 after.next(p);
                 after.skip_idle(p);
                 if (ok && !after.done()) load_q(after);
-                if (ok) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1);
+                if (ok) ok = through(k - 1);
                 tc::fence_after_sync();
             }
-            if constexpr (kStack) l += __shfl_xor_sync(0xffffffffu, l, kRowsQ);
-            if (lead) sm.half[set][r].x = l;
+#pragma unroll
+            for (int y = 0; y < kR; ++y) {
+                if constexpr (kStack) {
+                    l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+                    l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+                }
+                if (lead) sm.half[set][r[y]] = l[y];
+            }
             if (softmax_any(!ok)) ok = false;
-            if (low) l += sm.half[set ^ 1][r].x;
+#pragma unroll
+            for (int y = 0; y < kR; ++y) l[y] += sm.half[set ^ 1][r[y]];
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg % kBad] != 0);
             if (bad_len(p, w.len) && tid == 0) set_status(p.status, KDA_ERR_SEQLENS);
             const int64_t row0 = (int64_t)w.n * geo.R + row_first;
-            if (set == 0 && lead) {
-                sm.factor[r] = bad ? NAN : (l == 0.f ? 0.f : 1.0f / l);
-                if (owner) {
+#pragma unroll
+            for (int y = 0; y < kR; ++y) {
+                if (set != 0 || !lead) continue;
+                sm.factor[r[y]] = bad ? NAN : (l[y] == 0.f ? 0.f : 1.0f / l[y]);
+                if (owner[y]) {
                     if (!whole)
-                        p.part_ml[part0 + r] = make_float2(m_ref, bad ? NAN : l);
+                        p.part_ml[part0 + r[y]] = make_float2(m_ref[y], bad ? NAN : l[y]);
                     else if (p.lse)
-                        p.lse[row0 + r] = bad ? NAN : (l == 0.f ? -INFINITY : m_ref * p.scale + logf(l));
+                        p.lse[row0 + r[y]] = bad ? NAN : (l[y] == 0.f ? -INFINITY : m_ref[y] * p.scale + logf(l[y]));
                 }
             }
             named_sync(2, kSoftmaxThreads);
@@ -677,7 +764,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             if (warp == 8) {
                 set_status(p.status, KDA_ERR_CUDA);
                 tc::mbar_wait(&sm.drained, 0);
-                for (int e = max(0, sm.issued - geo.np); e < sm.issued; ++e) tc::mbar_wait(&sm.full[e % geo.np], (e / geo.np) & 1);
+                for (int e = max(0, sm.issued - kTiles); e < sm.issued; ++e) tc::mbar_wait(&sm.full[e % kTiles], (e / kTiles) & 1);
             }
         }
         __syncwarp();
@@ -695,14 +782,14 @@ Geom8 geometry8(int32_t H, int32_t m) {
     q.npad = (q.rows + 15) / 16 * 16;
     q.form = q.rows <= 32 ? 0 : (q.rows <= 64 ? 1 : 2);
     const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)5 * (q.form == 0 ? 64 : 128) * 128;
-    const size_t fixed = 1024 + sizeof(Smem8) + of_q + (size_t)q.npad * 128;
-    q.np = (int32_t)((kSmem8 - fixed) / kChunk8);
-    if (q.np > kMaxSlots) q.np = kMaxSlots;
-    q.smem = (uint32_t)(fixed + (size_t)q.np * kChunk8);
+    q.smem = (uint32_t)(1024 + sizeof(Smem8) + of_q + (size_t)q.npad * 256 + (size_t)tiles_in(q.form) * kTile8);
     return q;
 }
-static_assert(kSmem8 - 1024 - sizeof(Smem8) - 10 * kMostRows8 * 128 >= 12 * kChunk8, "96 rows leave 12 slots");
-static_assert(kMaxSlots / kChunks + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
+static_assert(1024 + sizeof(Smem8) + 5 * 64 * 128 + 32 * 256 + tiles_in(0) * kTile8 <= kSmem8, "32 rows");
+static_assert(1024 + sizeof(Smem8) + 5 * 128 * 128 + 64 * 256 + tiles_in(1) * kTile8 <= kSmem8, "64 rows");
+static_assert(1024 + sizeof(Smem8) + 11 * kMostRows8 * 128 + tiles_in(2) * kTile8 <= kSmem8, "96 rows");
+static_assert(tiles_in(0) <= kMaxSlots, "");
+static_assert(kMaxSlots + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
 }  // namespace
 }  // namespace kda
@@ -745,9 +832,10 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     const SplitWs w = split_ws(a.geo, kMostRows8);
     a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
     // a cache without pages keeps one page of extent: no id is in range, every load is past it
-    const uint64_t dc[3] = {(uint64_t)kRow8, (uint64_t)page_size, (uint64_t)(num_pages > 0 ? num_pages : 1)};
-    const uint64_t sc[3] = {1, (uint64_t)kRow8, (uint64_t)page_stride};
-    if (!tma::encode_bytes(&a.map, cache, dc, sc, a.rb)) return KDA_ERR_CUDA;
+    // the chunks of a row are a dimension of their own, outside the rows: a box of all of them lands chunk by chunk
+    const uint64_t dc[4] = {128, (uint64_t)page_size, kChunks, (uint64_t)(num_pages > 0 ? num_pages : 1)};
+    const uint64_t sc[4] = {1, (uint64_t)kRow8, 128, (uint64_t)page_stride};
+    if (!tma::encode_bytes(&a.map, cache, dc, sc, a.rb, a.rb == kKvTile ? kChunks : 1)) return KDA_ERR_CUDA;
     a.q_lat = reinterpret_cast<const __nv_bfloat16 *>(q_lat);
     a.q_pe = reinterpret_cast<const __nv_bfloat16 *>(q_pe);
     a.rows = cache;

@@ -75,6 +75,13 @@ __device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, uint6
         "l"(map), "r"(tc::smem_addr(mbar)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, uint64_t *mbar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];\n" ::"r"(tc::smem_addr(dst)),
+        "l"(map), "r"(tc::smem_addr(mbar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
 // a wait by a whole warp, whose lanes agree on the outcome (what follows is warp-collective)
 __device__ __forceinline__ bool wait_warp(uint64_t *mbar, uint32_t parity) {
     return __all_sync(0xffffffffu, tc::mbar_wait(mbar, parity));
@@ -168,14 +175,15 @@ inline bool encode(CUtensorMap *map, const void *base, int rank, const uint64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of a tensor of bytes of three dimensions, innermost first, whose strides count bytes, for boxes of
-// {128, box1, 1}. Out-of-range rows load as zeros.
-inline bool encode_bytes(CUtensorMap *map, const void *base, const uint64_t (&dim)[3], const uint64_t (&stride)[3], uint32_t box1) {
+// Map of a tensor of bytes of four dimensions, innermost first, whose strides count bytes, for boxes of
+// {128, box1, box2, 1}. Out-of-range rows load as zeros.
+inline bool encode_bytes(CUtensorMap *map, const void *base, const uint64_t (&dim)[4], const uint64_t (&stride)[4],
+                         uint32_t box1, uint32_t box2) {
     const EncodeFn f = encoder();
     if (!f) return false;
-    const cuuint64_t d[3] = {dim[0], dim[1], dim[2]}, s[2] = {stride[1], stride[2]};
-    const cuuint32_t box[3] = {128, box1, 1}, one[3] = {1, 1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t d[4] = {dim[0], dim[1], dim[2], dim[3]}, s[3] = {stride[1], stride[2], stride[3]};
+    const cuuint32_t box[4] = {128, box1, box2, 1}, one[4] = {1, 1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
