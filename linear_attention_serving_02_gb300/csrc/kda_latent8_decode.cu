@@ -36,6 +36,8 @@ constexpr uint32_t kChunk8 = kKvTile * 128;     // 64 rows of 128 bytes: 128 lat
 constexpr int kChunks = 5;                      // of a tile: 512 latents, then the positional key
 constexpr uint32_t kTile8 = kChunks * kChunk8;
 constexpr int kMaxSlots = 4;
+constexpr int kScales = 4;                      // tiles whose scales are kept: a slot is loaded anew behind the score products of the
+                                                // tile two before, which wait until the softmax has taken those of the tile four before
 constexpr int kThreads8 = 384;                  // 8 softmax warps, score issue, value issue, TMA, none
 // Registers of a softmax thread and of the others: 384 threads are launched with 168 each, 64512 in all
 constexpr int kRegsSoftmax = 208, kRegsIssue = 80;
@@ -51,30 +53,35 @@ struct Geom8 : SplitGeom {
     uint32_t smem;
 };
 
-// tiles that the ring holds beside Q and W
+// Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
+// for a wait and a load, which five a tile would make the bound of few rows), or its five chunks where only
+// two tiles fit, each as soon as its products are through.
 constexpr int tiles_in(int form) { return 4 - form; }
+constexpr int pieces_of(int form) { return form < 2 ? 1 : kChunks; }
 
 struct Args8 : SplitArgs {
     CUtensorMap map;
     const __nv_bfloat16 *q_lat, *q_pe;
     const uint8_t *rows;
     int64_t page_stride;
-    int32_t rb;  // rows of a TMA box: 64 (it then takes all chunks), 32 or 16
+    int32_t rb;  // rows of a TMA box: 64 (it then takes all chunks of a tile that is loaded in one piece), 32 or 16
     float c;     // log2(e) scale
     Geom8 geo;
 };
 
 struct Smem8 {
     uint64_t q_ready, s_full[2], s_free[2], p_full[2], drained;
-    uint64_t full[kMaxSlots], done[kMaxSlots];  // a tile is there; its products are through
-    float sc[kMaxSlots][kKvTile];       // scales of a tile's rows
+    uint64_t full[kMaxSlots][kChunks], empty[kMaxSlots][kChunks];  // a piece of a tile is there; may be loaded over
+    uint64_t done[kMaxSlots];           // a tile's products are through
+    uint64_t sc_full[kScales];
+    float sc[kScales][kKvTile];         // scales of a tile's rows
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
     float half[2][128], recent[2][128]; // by query row: the halves' maxima or sums, and largest weights of a window
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
-    int32_t issued;
+    int32_t issued, scaled;  // loads of pieces and of scales
 };
 
 // kind::f8f6f4, e4m3 times e4m3 (or e5m2 as B), fp32 accumulator; one step takes 32 of the contraction: 32 bytes
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, where lo lies behind hi)
     constexpr int kR = FORM == 1 ? 2 : 1;          // query rows of a softmax thread,
     constexpr int kC = kStack ? 8 : 32;            // and cached rows of a tile for each
-    constexpr int kTiles = tiles_in(FORM);
+    constexpr int kTiles = tiles_in(FORM), kPieces = pieces_of(FORM);
     const Geom8 &geo = p.geo;
     // Q: four chunks of 128 latents of hi (and lo, stacked; else four of lo behind), then the positional part
     const uint32_t q_chunk = (uint32_t)(kStack ? MS : geo.rows) * 128;
@@ -148,13 +155,17 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         find_run(p, g, rt, sm.run);
         if (lane == 0) {
             sm.failed = 0;
-            sm.issued = 0;
+            sm.issued = sm.scaled = 0;
+            for (int i = 0; i < kScales; ++i) tc::mbar_init(&sm.sc_full[i], 1);
             for (int i = 0; i < kBad; ++i) sm.bad[i] = 0;
             tc::mbar_init(&sm.q_ready, kSoftmaxThreads / 32);
             for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_free[i], kSoftmaxThreads / 32);
             for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_full[i], kSoftmaxThreads / 32);
             tc::mbar_init(&sm.drained, 2);
-            for (int i = 0; i < kTiles; ++i) tc::mbar_init(&sm.full[i], 1), tc::mbar_init(&sm.done[i], 1);
+            for (int i = 0; i < kTiles; ++i) {
+                tc::mbar_init(&sm.done[i], 1);
+                for (int c = 0; c < kPieces; ++c) tc::mbar_init(&sm.full[i][c], 1), tc::mbar_init(&sm.empty[i][c], 1);
+            }
             tc::mbar_init_fence();
         }
     } else if (warp == 8) {
@@ -218,36 +229,48 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
 #pragma unroll
                             for (int b = 0; b < 4; ++b) {
                                 const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
-                                if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages)
-                                    tma::prefetch_l2(p.rows + pg_next[b] * p.page_stride + (int64_t)ry_next[b] * kRow8,
-                                                     (uint32_t)p.rb * kRow8);
+                                if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages) {
+                                    const uint8_t *page = p.rows + pg_next[b] * p.page_stride;
+                                    tma::prefetch_l2(page + (int64_t)ry_next[b] * kRow8, (uint32_t)p.rb * kRow8);
+                                    tma::prefetch_l2(page + (int64_t)p.page_size * kRow8 + 4 * ry_next[b], 4 * p.rb);
+                                }
                             }
                         }
                         const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
-                        ok = tc::mbar_wait(&sm.done[ps], pph ^ 1);
-                        if (!ok) break;
-                        uint8_t *dst = s_ring + ps * kTile8;
                         // the rows' scales stand behind the page's rows; of a page that is not there, none are loaded
                         uint32_t scales = 0;
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             if (b < boxes && pg[b] != INT32_MAX) scales += 4 * p.rb;
-                        tc::mbar_arrive_expect_tx(&sm.full[ps], kChunks * boxes * p.rb * 128 + scales);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (b < boxes && pg[b] != INT32_MAX)
-                                tc::bulk_g2s(&sm.sc[ps][b * p.rb], p.rows + pg[b] * p.page_stride + (int64_t)p.page_size * kRow8 + 4 * ry[b],
-                                             4 * p.rb, &sm.full[ps]);
-                        if (p.rb == kKvTile) {
-                            tma::load_4d(dst, &p.map, &sm.full[ps], 0, ry[0], 0, pg[0]);
-                        } else {
-                            const uint32_t box = (uint32_t)p.rb * 128;
-                            for (int i = 0; i < kChunks; ++i)
+                        const uint32_t box = (uint32_t)p.rb * 128;
+                        for (int c = 0; c < kPieces; ++c) {  // the positional chunk first
+                            const int chunk = c == 0 ? kChunks - 1 : c - 1;
+                            ok = tc::mbar_wait(kPieces == 1 ? &sm.done[ps] : &sm.empty[ps][c], pph ^ 1);
+                            if (!ok) break;
+                            uint64_t *full = &sm.full[ps][c];
+                            tc::mbar_arrive_expect_tx(full, (kPieces == 1 ? kChunks : 1) * boxes * box);
+                            if (c == 0) {
+                                uint64_t *there = &sm.sc_full[sm.scaled % kScales];
+                                tc::mbar_arrive_expect_tx(there, scales);
 #pragma unroll
                                 for (int b = 0; b < 4; ++b)
-                                    if (b < boxes) tma::load_4d(dst + i * kChunk8 + b * box, &p.map, &sm.full[ps], 0, ry[b], i, pg[b]);
+                                    if (b < boxes && pg[b] != INT32_MAX)
+                                        tc::bulk_g2s(&sm.sc[sm.scaled % kScales][b * p.rb],
+                                                     p.rows + pg[b] * p.page_stride + (int64_t)p.page_size * kRow8 + 4 * ry[b], 4 * p.rb, there);
+                                ++sm.scaled;
+                            }
+                            uint8_t *dst = s_ring + ps * kTile8;
+                            if (kPieces == 1 && p.rb == kKvTile) {
+                                tma::load_4d(dst, &p.map, full, 0, ry[0], 0, pg[0]);
+                            } else {
+                                for (int i = kPieces == 1 ? 0 : chunk; i < (kPieces == 1 ? kChunks : chunk + 1); ++i)
+#pragma unroll
+                                    for (int b = 0; b < 4; ++b)
+                                        if (b < boxes) tma::load_4d(dst + i * kChunk8 + b * box, &p.map, full, 0, ry[b], i, pg[b]);
+                            }
+                            ++sm.issued;
                         }
-                        ++sm.issued;
+                        if (!ok) break;
                         if (++ps == kTiles) ps = 0, pph ^= 1;
                     }
                     ++seg;
@@ -271,21 +294,27 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                     for (int j = w.j0; j < w.j1 && ok; ++j, ++k) {
                         ok = tc::mbar_wait(&sm.s_free[k & 1], ((k >> 1) & 1) ^ 1);
                         const uint32_t d = t_s + (k & 1) * kKvTile;
-                        ok = ok && tc::mbar_wait(&sm.full[ps], pph);
-                        if (!ok) break;
-                        tc::fence_after_sync();
                         const uint32_t b = ring_lo + ps * (kTile8 >> 4);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            tma::mma_ss(d, q_lo + (q_chunks - 1) * q_step + 2 * s, b + (4 * kChunk8 >> 4) + 2 * s, id_pe, s != 0);
-#pragma unroll
-                        for (int i = 0; i < kChunks - 1; ++i)
+                        for (int c = 0; c < kChunks; ++c) {  // the positional chunk first
+                            if (c < kPieces) {
+                                ok = ok && tc::mbar_wait(&sm.full[ps][c], pph);
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                            }
 #pragma unroll
                             for (int s = 0; s < 4; ++s) {
-                                const uint32_t a = q_lo + i * q_step + 2 * s, bb = b + i * (kChunk8 >> 4) + 2 * s;
-                                mma8(d, a, bb, id, 1);
-                                if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
+                                if (c == 0) {
+                                    tma::mma_ss(d, q_lo + (q_chunks - 1) * q_step + 2 * s, b + (4 * kChunk8 >> 4) + 2 * s, id_pe, s != 0);
+                                } else {
+                                    const uint32_t a = q_lo + (c - 1) * q_step + 2 * s, bb = b + (c - 1) * (kChunk8 >> 4) + 2 * s;
+                                    mma8(d, a, bb, id, 1);
+                                    if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
+                                }
                             }
+                            if (c == 0 && kPieces > 1) tc::commit(&sm.empty[ps][0]);
+                        }
+                        if (!ok) break;
                         if (++ps == kTiles) ps = 0, pph ^= 1;
                         tc::commit(&sm.s_full[k & 1]);
                     }
@@ -322,6 +351,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 mma8(d, a + 256, b + 2, id_hi, 1);
                                 mma8(d, a + 256, b + 6, id_lo, 1);
                             }
+                            if (kPieces > 1) tc::commit(&sm.empty[ps][i + 1]);
                         }
                         tc::commit(&sm.done[ps]);
                         if (++ps == kTiles) ps = 0;
@@ -356,51 +386,64 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         // Q of a stretch, a row a warp at a time; the last stretch's score products are through: its last tile was taken
         auto load_q = [&](const Walk &s) {
             const int64_t row0 = (int64_t)s.n * geo.R + row_first;
-            for (int q = warp; q < rows_here; q += 8) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + (row0 + q) * kLatent) + 2 * lane;
-                const uint4 va = src[0], vb = src[1];
-                const uint32_t pe = reinterpret_cast<const uint32_t *>(p.q_pe + (row0 + q) * kPos)[lane];
-                const uint32_t v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-                uint32_t top = 0;  // bits of the largest magnitude, as fp32; NaN is above all
+            // the loads of kBatch rows are on their way before the first is looked at
+            constexpr int kBatch = FORM == 0 ? 4 : 6;
+            for (int q0 = warp; q0 < rows_here; q0 += 8 * kBatch) {
+                uint4 va[kBatch], vb[kBatch];
+                uint32_t vp[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, max((v[i] << 16) & 0x7fffffffu, v[i] & 0x7fff0000u));
-                top = __reduce_max_sync(0xffffffffu, top);
-                const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
-                // the unit 2^a: the latents' largest in (224, 448]; positional values that dwarf it stay in bf16's range
-                const int a = max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100);
-                const float inv = exp2_of(-min(a, 120));
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t hh[2], ll[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t u = v[2 * i + e];
-                        const float x = __uint_as_float(u << 16) * inv, y = __uint_as_float(u & 0xffff0000u) * inv;
-                        hh[e] = e4m3_of2(x, y);
-                        const float2 back = values_of2(hh[e]);
-                        ll[e] = e4m3_of2(x - back.x, y - back.y);
-                    }
-                    hi[i] = hh[0] | (hh[1] << 16);
-                    lo[i] = ll[0] | (ll[1] << 16);
+                for (int b = 0; b < kBatch; ++b) {
+                    const int64_t row = row0 + min(q0 + 8 * b, rows_here - 1);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
+                    va[b] = src[0], vb[b] = src[1];
+                    vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
                 }
-                // rows of the operand: hi and lo of a quarter one behind the other, or the row itself
-                const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
-                uint8_t *at = s_q + (lane >> 3) * q_chunk;
-                *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                at += kStack ? 0 : 4 * q_chunk;
-                *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                const __nv_bfloat162 pes = __floats2bfloat162_rn(__uint_as_float(pe << 16) * inv, __uint_as_float(pe & 0xffff0000u) * inv);
-                at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
-                *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&pes);
-                if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
-                // a row with an infinity or a NaN has no scores
-                if (lane == 0) sm.row_c[q] = max(top, top_pe) >= 0x7f800000u ? NAN : p.c * exp2_of(min(a, 120));
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int q = q0 + 8 * b;
+                    if (q >= rows_here) break;
+                    const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
+                    uint32_t top = 0;  // bits of the largest magnitude, as fp32; NaN is above all
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = max(top, max((v[i] << 16) & 0x7fffffffu, v[i] & 0x7fff0000u));
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
+                    // the unit 2^a: the latents' largest in (224, 448]; positional values that dwarf it stay in bf16's range
+                    const int a = max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100);
+                    const float inv = exp2_of(-min(a, 120));
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t hh[2], ll[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t u = v[2 * i + e];
+                            const float x = __uint_as_float(u << 16) * inv, y = __uint_as_float(u & 0xffff0000u) * inv;
+                            hh[e] = e4m3_of2(x, y);
+                            const float2 back = values_of2(hh[e]);
+                            ll[e] = e4m3_of2(x - back.x, y - back.y);
+                        }
+                        hi[i] = hh[0] | (hh[1] << 16);
+                        lo[i] = ll[0] | (ll[1] << 16);
+                    }
+                    // rows of the operand: hi and lo of a quarter one behind the other, or the row itself
+                    const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
+                    uint8_t *at = s_q + (lane >> 3) * q_chunk;
+                    *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    at += kStack ? 0 : 4 * q_chunk;
+                    *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const __nv_bfloat162 pes = __floats2bfloat162_rn(__uint_as_float(pe << 16) * inv, __uint_as_float(pe & 0xffff0000u) * inv);
+                    at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&pes);
+                    if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
+                    // a row with an infinity or a NaN has no scores
+                    if (lane == 0) sm.row_c[q] = max(top, top_pe) >= 0x7f800000u ? NAN : p.c * exp2_of(min(a, 120));
+                }
             }
             fence_proxy_async();
             tma::arrive_warp(&sm.q_ready);
         };
-        bool tile_there = false, s_there = false;  // the next tile and its scores
+        bool scales_there = false, s_there = false;  // of the next tile
         Walk w;
         w.start(p, sm.run);
         {
@@ -451,11 +494,11 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         const int slot = k % kTiles;
                         const bool first = j == w.j0;
                         const bool old_there = k < 2 || peek(&sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1);
-                        ok = wait_peeked(tile_there, &sm.full[slot], (k / kTiles) & 1) && ok;
+                        ok = wait_peeked(scales_there, &sm.sc_full[k % kScales], (k / kScales) & 1) && ok;
                         float sc[kC], v[kR][kC];  // the scales; scores, then weights
                         auto scales = [&] {
 #pragma unroll
-                            for (int e = 0; e < kC; e += 2) *reinterpret_cast<float2 *>(&sc[e]) = *reinterpret_cast<const float2 *>(&sm.sc[slot][col(e)]);
+                            for (int e = 0; e < kC; e += 2) *reinterpret_cast<float2 *>(&sc[e]) = *reinterpret_cast<const float2 *>(&sm.sc[k % kScales][col(e)]);
                             // behind the sequence they count as one: 0 times what stands there may be NaN
                             if (w.len - j * kKvTile < kKvTile) {
 #pragma unroll
@@ -632,7 +675,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                             }
                         }
                         // what the next tile waits for
-                        tile_there = peek(&sm.full[(k + 1) % kTiles], ((k + 1) / kTiles) & 1);
+                        scales_there = peek(&sm.sc_full[(k + 1) % kScales], ((k + 1) / kScales) & 1);
                         s_there = peek(&sm.s_full[(k + 1) & 1], ((k + 1) >> 1) & 1);
                         if (live) {
                             uint8_t *w_at = s_p + (k & 1) * p_bytes;
@@ -764,7 +807,9 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             if (warp == 8) {
                 set_status(p.status, KDA_ERR_CUDA);
                 tc::mbar_wait(&sm.drained, 0);
-                for (int e = max(0, sm.issued - kTiles); e < sm.issued; ++e) tc::mbar_wait(&sm.full[e % kTiles], (e / kTiles) & 1);
+                for (int e = max(0, sm.scaled - kScales); e < sm.scaled; ++e) tc::mbar_wait(&sm.sc_full[e % kScales], (e / kScales) & 1);
+                for (int e = max(0, sm.issued - kTiles * kPieces); e < sm.issued; ++e)
+                    tc::mbar_wait(&sm.full[e / kPieces % kTiles][e % kPieces], (e / kPieces / kTiles) & 1);
             }
         }
         __syncwarp();
@@ -835,7 +880,7 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     // the chunks of a row are a dimension of their own, outside the rows: a box of all of them lands chunk by chunk
     const uint64_t dc[4] = {128, (uint64_t)page_size, kChunks, (uint64_t)(num_pages > 0 ? num_pages : 1)};
     const uint64_t sc[4] = {1, (uint64_t)kRow8, 128, (uint64_t)page_stride};
-    if (!tma::encode_bytes(&a.map, cache, dc, sc, a.rb, a.rb == kKvTile ? kChunks : 1)) return KDA_ERR_CUDA;
+    if (!tma::encode_bytes(&a.map, cache, dc, sc, a.rb, a.rb == kKvTile && pieces_of(a.geo.form) == 1 ? kChunks : 1)) return KDA_ERR_CUDA;
     a.q_lat = reinterpret_cast<const __nv_bfloat16 *>(q_lat);
     a.q_pe = reinterpret_cast<const __nv_bfloat16 *>(q_pe);
     a.rows = cache;
