@@ -38,10 +38,14 @@ constexpr uint32_t kTile8 = kChunks * kChunk8;
 constexpr int kMaxSlots = 4;
 constexpr int kScales = 4;                      // tiles whose scales are kept: a slot is loaded anew behind the score products of the
                                                 // tile two before, which wait until the softmax has taken those of the tile four before
-constexpr int kThreads8 = 384;                  // 8 softmax warps, score issue, value issue, TMA, none
-// Registers of a softmax thread and of the others: 384 threads are launched with 168 each, 64512 in all
-constexpr int kRegsSoftmax = 208, kRegsIssue = 80;
-static_assert(256 * kRegsSoftmax + 128 * kRegsIssue <= 384 * 168, "the shares' sum");
+constexpr int kSets = 2, kSetCols = kKvTile / kSets;  // the softmax warps of a lane quarter, and the cached rows of a tile that each takes
+constexpr int kSoft = 128 * kSets;              // softmax threads
+constexpr int kIssue = kSoft / 32;              // the warps behind them: score issue, value issue, TMA, none
+constexpr int kThreads8 = kSoft + 128;
+constexpr int kBlocks = kLatent / 128 / kSets;  // of 128 latents of O^T that a softmax warp reads
+// Registers of a softmax thread and of the others, out of those that the block is launched with
+constexpr int kLaunched = kSets == 2 ? 168 : 96, kRegsSoftmax = kSets == 2 ? 208 : 104, kRegsIssue = kSets == 2 ? 80 : 64;
+static_assert(kSoft * kRegsSoftmax + 128 * kRegsIssue <= kThreads8 * kLaunched, "the shares' sum");
 constexpr int kMostRows8 = 96;                  // query rows of a CTA
 constexpr float kSet = 2.5f, kHigh = 8.75f, kReach = 40.0f;  // powers of two
 constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and what is low
@@ -77,7 +81,7 @@ struct Smem8 {
     float sc[kScales][kKvTile];         // scales of a tile's rows
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
-    float half[2][128], recent[2][128]; // by query row: the halves' maxima or sums, and largest weights of a window
+    float part[kSets][128], recent[kSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
@@ -107,22 +111,38 @@ __device__ __forceinline__ bool peek(uint64_t *mbar, uint32_t parity) {
 __device__ __forceinline__ bool wait_peeked(bool there, uint64_t *mbar, uint32_t parity) {
     return __all_sync(0xffffffffu, there) || tma::wait_warp(mbar, parity);
 }
-// 16 TMEM lanes and 32 columns as a warp's fragments: x[4 g + 0, 1] are columns 8 g + 2 (lane % 4) + 0, 1 of TMEM lane
-// lane / 4, x[4 g + 2, 3] the same of TMEM lane 8 + lane / 4. Without the wait
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 TMEM lanes and 16 or 32 columns as a warp's fragments: x[4 g + 0, 1] are columns 8 g + 2 (lane % 4) + 0, 1 of TMEM
+// lane lane / 4, x[4 g + 2, 3] the same of TMEM lane 8 + lane / 4. Without the wait
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// Two weights (a first) as two bytes of e4m3 (into the low half of hi) and two of e5m2, their rest
+// whole rows: 16 or 32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[16]) { tma::tmem_ld16_nowait(taddr, r); }
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[32]) { tc::tmem_ld32_nowait(taddr, r); }
+// Two values (a first) as two bytes of e4m3 (into the low half of hi) and two for their rest: e4m3 for queries, which in
+// fp16 are what they were, and e5m2 for weights, which go on further down
+template <bool QUERY>
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
     uint16_t h, l;
-    asm("{\n.reg .b32 w, v;\ncvt.rn.f16x2.f32 w, %3, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n"
-        "cvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 w, w, v;\ncvt.rn.satfinite.e5m2x2.f16x2 %1, w;\n}\n"
-        : "=h"(h), "=h"(l)
-        : "f"(a), "f"(b));
+    if (QUERY)
+        asm("{\n.reg .b32 w, v;\ncvt.rn.f16x2.f32 w, %3, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n"
+            "cvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 w, w, v;\ncvt.rn.satfinite.e4m3x2.f16x2 %1, w;\n}\n"
+            : "=h"(h), "=h"(l)
+            : "f"(a), "f"(b));
+    else
+        asm("{\n.reg .b32 w, v;\ncvt.rn.f16x2.f32 w, %3, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n"
+            "cvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 w, w, v;\ncvt.rn.satfinite.e5m2x2.f16x2 %1, w;\n}\n"
+            : "=h"(h), "=h"(l)
+            : "f"(a), "f"(b));
     hi = h, lo = l;
 }
 
@@ -135,7 +155,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     constexpr bool kStack = FORM < 2;          // hi and lo rows in one product
     constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, where lo lies behind hi)
     constexpr int kR = FORM == 1 ? 2 : 1;          // query rows of a softmax thread,
-    constexpr int kC = kStack ? 8 : 32;            // and cached rows of a tile for each
+    constexpr int kC = kStack ? kSetCols / 4 : kSetCols;  // and cached rows of a tile for each
     constexpr int kTiles = tiles_in(FORM), kPieces = pieces_of(FORM);
     const Geom8 &geo = p.geo;
     // Q: four chunks of 128 latents of hi (and lo, stacked; else four of lo behind), then the positional part
@@ -150,7 +170,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     const int rt = blockIdx.x % geo.RT, g = blockIdx.x / geo.RT;
 
     pdl_wait();
-    if (warp == 10 && lane == 0) tma::prefetch_map(&p.map);
+    if (warp == kIssue + 2 && lane == 0) tma::prefetch_map(&p.map);
     if (warp == 0) {
         find_run(p, g, rt, sm.run);
         if (lane == 0) {
@@ -158,9 +178,9 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             sm.issued = sm.scaled = 0;
             for (int i = 0; i < kScales; ++i) tc::mbar_init(&sm.sc_full[i], 1);
             for (int i = 0; i < kBad; ++i) sm.bad[i] = 0;
-            tc::mbar_init(&sm.q_ready, kSoftmaxThreads / 32);
-            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_free[i], kSoftmaxThreads / 32);
-            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_full[i], kSoftmaxThreads / 32);
+            tc::mbar_init(&sm.q_ready, kIssue);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_free[i], kIssue);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_full[i], kIssue);
             tc::mbar_init(&sm.drained, 2);
             for (int i = 0; i < kTiles; ++i) {
                 tc::mbar_init(&sm.done[i], 1);
@@ -168,7 +188,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             }
             tc::mbar_init_fence();
         }
-    } else if (warp == 8) {
+    } else if (warp == kIssue) {
         tc::tmem_alloc(&sm.tmem, 512);
     }
     tc::fence_before_sync();
@@ -180,9 +200,9 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
-    if (warp >= 8) {
+    if (warp >= kIssue) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsIssue));
-        if (warp == 10) {
+        if (warp == kIssue + 2) {
             // ---- TMA producer: one thread ----
             if (tma::elect()) {
                 Walk w;
@@ -192,9 +212,9 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                 const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
                 while (!w.done() && ok) {
                     const int32_t *entry = p.table + (int64_t)w.n * p.max_pages;
-                    const int64_t row0 = (int64_t)w.j0 * kKvTile;
-                    entry += row0 / p.page_size;
-                    int32_t at = (int32_t)(row0 % p.page_size);  // row within the page
+                    const uint32_t row0 = (uint32_t)w.j0 * kKvTile, of = row0 / (uint32_t)p.page_size;
+                    entry += of;
+                    int32_t at = (int32_t)(row0 - of * (uint32_t)p.page_size);  // row within the page
                     // the places of a tile's boxes, fetched one tile ahead; nothing past the sequence's rows is looked up
                     int32_t pg[4], ry[4], pg_next[4], ry_next[4];
                     auto look = [&](int j) {
@@ -225,17 +245,6 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                             set_status(p.status, KDA_ERR_PAGES);
                         }
                         look(j + 1);
-                        if (FORM == 2 && j + 1 < w.j1) {
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
-                                if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages) {
-                                    const uint8_t *page = p.rows + pg_next[b] * p.page_stride;
-                                    tma::prefetch_l2(page + (int64_t)ry_next[b] * kRow8, (uint32_t)p.rb * kRow8);
-                                    tma::prefetch_l2(page + (int64_t)p.page_size * kRow8 + 4 * ry_next[b], 4 * p.rb);
-                                }
-                            }
-                        }
                         const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
                         // the rows' scales stand behind the page's rows; of a page that is not there, none are loaded
                         uint32_t scales = 0;
@@ -269,6 +278,18 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                         if (b < boxes) tma::load_4d(dst + i * kChunk8 + b * box, &p.map, full, 0, ry[b], i, pg[b]);
                             }
                             ++sm.issued;
+                            // the next tile into L2, where its pieces will be waited for
+                            if (kPieces > 1 && c == 0 && j + 1 < w.j1) {
+#pragma unroll
+                                for (int b = 0; b < 4; ++b) {
+                                    const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
+                                    if (b < sub && row < w.len && (uint32_t)pg_next[b] < (uint32_t)p.num_pages) {
+                                        const uint8_t *page = p.rows + pg_next[b] * p.page_stride;
+                                        tma::prefetch_l2(page + (int64_t)ry_next[b] * kRow8, (uint32_t)p.rb * kRow8);
+                                        tma::prefetch_l2(page + (int64_t)p.page_size * kRow8 + 4 * ry_next[b], 4 * p.rb);
+                                    }
+                                }
+                            }
                         }
                         if (!ok) break;
                         if (++ps == kTiles) ps = 0, pph ^= 1;
@@ -280,7 +301,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                 if (!ok) sm.failed = 1;
             }
             __syncwarp();
-        } else if (warp == 8) {
+        } else if (warp == kIssue) {
             // ---- score products: one thread ----
             if (tma::elect()) {
                 constexpr uint32_t id = idesc8(MS, kKvTile, 0, 0), id_pe = tma::idesc(MS, kKvTile, 0, 0);
@@ -316,6 +337,11 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         }
                         if (!ok) break;
                         if (++ps == kTiles) ps = 0, pph ^= 1;
+                        // With the scores the softmax may count on the tile's scales, and on the weights of the tile two before
+                        // having been used. One thread waits for these instead of every warp.
+                        ok = tc::mbar_wait(&sm.sc_full[k % kScales], (k / kScales) & 1) &&
+                             (k < 2 || tc::mbar_wait(&sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1));
+                        if (!ok) break;
                         tc::commit(&sm.s_full[k & 1]);
                     }
                     ++seg;
@@ -325,7 +351,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                 if (!ok) sm.failed = 1;
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp == kIssue + 1) {
             // ---- value products: one thread ----
             if (tma::elect()) {
                 const uint32_t id_hi = idesc8(128, geo.npad, 0, 1), id_lo = idesc8(128, geo.npad, 1, 1);
@@ -379,7 +405,14 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         }
         const bool warp_rows = quarter * kRowsQ < rows_here;
         // column of a tile of value e
-        auto col = [&](int e) { return 32 * set + (kStack ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e); };
+        auto col = [&](int e) { return kSetCols * set + (kStack ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e); };
+        // the largest weight of a row's last window
+        auto window = [&](int row) {
+            float x = sm.recent[0][row];
+#pragma unroll
+            for (int i = 1; i < kSets; ++i) x = fmaxf(x, sm.recent[i][row]);
+            return x;
+        };
         int k = 0, seg = 0;  // tiles and stretches worked on
         // the products of tile t are through: waited for in every tile for the one before the last, so that none is passed over
         auto through = [&](int t) { return tma::wait_warp(&sm.done[t % kTiles], (t / kTiles) & 1); };
@@ -387,44 +420,40 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         auto load_q = [&](const Walk &s) {
             const int64_t row0 = (int64_t)s.n * geo.R + row_first;
             // the loads of kBatch rows are on their way before the first is looked at
-            constexpr int kBatch = FORM == 0 ? 4 : 6;
-            for (int q0 = warp; q0 < rows_here; q0 += 8 * kBatch) {
+            constexpr int kBatch = (FORM == 0 ? 4 : 6) * 2 / kSets;
+            for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
                 uint4 va[kBatch], vb[kBatch];
                 uint32_t vp[kBatch];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
-                    const int64_t row = row0 + min(q0 + 8 * b, rows_here - 1);
+                    const int64_t row = row0 + min(q0 + kIssue * b, rows_here - 1);
                     const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
                     va[b] = src[0], vb[b] = src[1];
                     vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
                 }
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
-                    const int q = q0 + 8 * b;
+                    const int q = q0 + kIssue * b;
                     if (q >= rows_here) break;
                     const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
-                    uint32_t top = 0;  // bits of the largest magnitude, as fp32; NaN is above all
+                    // bits of the largest magnitudes, as bf16 and then as fp32; NaN is above all
+                    uint32_t top = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, max((v[i] << 16) & 0x7fffffffu, v[i] & 0x7fff0000u));
-                    top = __reduce_max_sync(0xffffffffu, top);
+                    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
+                    top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
                     const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
                     // the unit 2^a: the latents' largest in (224, 448]; positional values that dwarf it stay in bf16's range
                     const int a = max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100);
                     const float inv = exp2_of(-min(a, 120));
+                    const uint64_t inv2 = pk2(inv, inv);
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t hh[2], ll[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t u = v[2 * i + e];
-                            const float x = __uint_as_float(u << 16) * inv, y = __uint_as_float(u & 0xffff0000u) * inv;
-                            hh[e] = e4m3_of2(x, y);
-                            const float2 back = values_of2(hh[e]);
-                            ll[e] = e4m3_of2(x - back.x, y - back.y);
-                        }
-                        hi[i] = hh[0] | (hh[1] << 16);
-                        lo[i] = ll[0] | (ll[1] << 16);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 x = upk2(mul2(pk2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), inv2));
+                        uint32_t h, l;
+                        split2<true>(x.x, x.y, h, l);
+                        hi[i >> 1] = i & 1 ? hi[i >> 1] | (h << 16) : h;
+                        lo[i >> 1] = i & 1 ? lo[i >> 1] | (l << 16) : l;
                     }
                     // rows of the operand: hi and lo of a quarter one behind the other, or the row itself
                     const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
@@ -443,14 +472,14 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             fence_proxy_async();
             tma::arrive_warp(&sm.q_ready);
         };
-        bool scales_there = false, s_there = false;  // of the next tile
+        bool s_there = false;  // of the next tile
         Walk w;
         w.start(p, sm.run);
         {
             Walk first = w;
             first.skip_idle(p);
             if (!first.done()) load_q(first);
-            named_sync(2, kSoftmaxThreads);
+            named_sync(2, kSoft);
         }
         for (; !w.done() && ok; w.next(p)) {
             float m_ref[kR], m_top[kR], l[kR];
@@ -472,12 +501,12 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         // kFold tiles, or the last ones, are in O^T (also with a failed wait: all warps meet these barriers)
                         ok = through(k - 1) && ok;
                         const bool start = js == w.j0 + kFold;
-                        named_sync(2, kSoftmaxThreads);  // the factors have been read
+                        named_sync(2, kSoft);  // the factors have been read
 #pragma unroll
                         for (int y = 0; y < kR; ++y)
                             if (set == 0 && lead) sm.factor[r[y]] = start || m_kept[y] == m_ref[y] ? 1.0f : tc::ex2(m_kept[y] - m_ref[y]);
-                        named_sync(2, kSoftmaxThreads);
-                        for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                        named_sync(2, kSoft);
+                        for (int i = kBlocks * set; i < kBlocks * (set + 1); ++i) {
                             float *kept = p.part_o + part0 * kLatent + 128 * i + 32 * quarter + lane;
                             fold_o(kept, tmem + lanes + i * geo.npad, geo.npad, sm.factor, start, js >= w.j1);
                         }
@@ -493,8 +522,6 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                     for (int j = js; j < je; ++j) {
                         const int slot = k % kTiles;
                         const bool first = j == w.j0;
-                        const bool old_there = k < 2 || peek(&sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1);
-                        ok = wait_peeked(scales_there, &sm.sc_full[k % kScales], (k / kScales) & 1) && ok;
                         float sc[kC], v[kR][kC];  // the scales; scores, then weights
                         auto scales = [&] {
 #pragma unroll
@@ -506,34 +533,34 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                     if (col(e) >= w.len - j * kKvTile) sc[e] = 1.f;
                             }
                         };
-                        scales();
                         ok = wait_peeked(s_there, &sm.s_full[k & 1], (k >> 1) & 1) && ok;
                         // a failed wait still meets the barriers below, so that no warp is left in them
                         if (ok) tc::fence_after_sync();
-                        const uint32_t s_at = t_s + lanes + (k & 1) * kKvTile + set * 32;
+                        scales();
+                        const uint32_t s_at = t_s + lanes + (k & 1) * kKvTile + set * kSetCols;
                         const bool live = warp_rows && ok;
                         float sum[kR], most[kR];
                         auto scores = [&] {  // of this thread's rows, as powers of two; rounded here, so that huge ones still differ by 0 from themselves
                             if constexpr (FORM == 2) {
-                                uint32_t x[32];
-                                tc::tmem_ld32_nowait(s_at, x);
+                                uint32_t x[kC];
+                                tmem_ld_row(s_at, x);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[0][e] = __uint_as_float(x[e]);
+                                for (int e = 0; e < kC; ++e) v[0][e] = __uint_as_float(x[e]);
                             } else if constexpr (FORM == 1) {
-                                uint32_t hi[16], lo[16];
-                                tmem_ld_16x32(s_at, hi);
-                                tmem_ld_16x32(s_at + (16u << 16), lo);
+                                uint32_t hi[2 * kC], lo[2 * kC];
+                                tmem_ld_fragments(s_at, hi);
+                                tmem_ld_fragments(s_at + (16u << 16), lo);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
+                                for (int e = 0; e < 2 * kC; ++e)
                                     v[(e >> 1) & 1][2 * (e >> 2) + (e & 1)] = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
                             } else {
-                                uint32_t x[16];
-                                tmem_ld_16x32(s_at, x);
+                                uint32_t x[2 * kC];
+                                tmem_ld_fragments(s_at, x);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
+                                for (int e = 0; e < kC; ++e)
                                     v[0][e] = __uint_as_float(x[4 * (e >> 1) + (e & 1)]) + __uint_as_float(x[4 * (e >> 1) + 2 + (e & 1)]);
                             }
                             tc::fence_before_sync();
@@ -579,25 +606,14 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                             if (!first) weights();
                         }
                         // one barrier a tile: does a row need a new reference, did a wait fail
-                        const bool look = ((j - w.j0) & (kWindow - 1)) == kWindow - 1;
                         bool may = first || !ok;
 #pragma unroll
-                        for (int y = 0; y < kR; ++y) {
-                            recent[y] = fmaxf(recent[y], most[y]);
+                        for (int y = 0; y < kR; ++y)
                             may |= owner[y] && (most[y] > kMost || faint[y] || (m_ref[y] == -INFINITY && w.len - j * kKvTile - unseen[y] > 0));
-                            if (look) {
-                                if constexpr (kStack) {
-                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 1));
-                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 2));
-                                }
-                                if (lead) sm.recent[set][r[y]] = recent[y];
-                            }
-                        }
-                        const bool any = softmax_any(may);
+                        const bool any = softmax_any<kSoft>(may);
                         bool again = false, anew[kR];
 #pragma unroll
                         for (int y = 0; y < kR; ++y) anew[y] = false;
-                        if (k > 1) ok = wait_peeked(old_there, &sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1) && ok;
                         if (any) {
                             if (k > 0) ok = through(k - 1) && ok;
                             // the largest exponent of a weight in this tile, over a row's threads
@@ -616,10 +632,10 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                     top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
                                     top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
                                 }
-                                if (lead) sm.half[set][r[y]] = top[y];
+                                if (lead) sm.part[set][r[y]] = top[y];
                             }
                             // all stop together when any wait failed
-                            if (softmax_any(!ok)) {
+                            if (softmax_any<kSoft>(!ok)) {
                                 ok = false;
                                 stopped = true;
                                 break;
@@ -627,11 +643,12 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                             again = false;
 #pragma unroll
                             for (int y = 0; y < kR; ++y) {
-                                top[y] = fmaxf(top[y], sm.half[set ^ 1][r[y]]);
+#pragma unroll
+                                for (int i = 0; i < kSets; ++i) top[y] = fmaxf(top[y], sm.part[i][r[y]]);
                                 m_top[y] = fmaxf(m_top[y], top[y]);
                                 const bool up = first || top[y] - m_ref[y] > kHigh;
                                 // of low weights, the window's largest, which is still in sm.recent
-                                const float low = m_ref[y] + __log2f(fmaxf(sm.recent[0][r[y]], sm.recent[1][r[y]]));
+                                const float low = m_ref[y] + __log2f(window(r[y]));
                                 const float to = fmaxf((up ? top[y] : fmaxf(top[y], low)) - kSet, m_top[y] - kReach);
                                 anew[y] = up || (faint[y] && to < m_ref[y]);
                                 const float f = anew[y] && !first ? tc::ex2(m_ref[y] - to) : 1.0f;
@@ -640,7 +657,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 l[y] *= f;
                                 again |= owner[y] && anew[y] && !first;
                             }
-                            if (softmax_any(again)) {
+                            if (softmax_any<kSoft>(again)) {
                                 tc::fence_after_sync();
                                 for (int e = 0; e < geo.npad; e += 16) {
                                     float fs[16];
@@ -648,7 +665,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
 #pragma unroll
                                     for (int y = 0; y < 16; ++y) fs[y] = sm.factor[e + y], same &= fs[y] == 1.0f;
                                     if (same) continue;
-                                    for (int i = 2 * set; i < 2 * set + 2; ++i) {
+                                    for (int i = kBlocks * set; i < kBlocks * (set + 1); ++i) {
                                         const uint32_t at = tmem + lanes + i * geo.npad + e;
                                         uint32_t x[16];
                                         tma::tmem_ld16_nowait(at, x);
@@ -661,50 +678,34 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 tc::tmem_wait_st();
                             }
                             if (live) weights();
-#pragma unroll
-                            for (int y = 0; y < kR; ++y) recent[y] = anew[y] ? most[y] : recent[y];
                         }
                         tma::arrive_warp(&sm.s_free[k & 1]);
-#pragma unroll
-                        for (int y = 0; y < kR; ++y) {
-                            faint[y] = false;
-                            if (look) {  // (where this tile has set the reference anew, its weights are not low)
-                                const float both = fmaxf(sm.recent[0][r[y]], sm.recent[1][r[y]]);
-                                faint[y] = !anew[y] && both < kLeast && both > 0.f && m_ref[y] > m_top[y] - kReach;
-                                recent[y] = 0.f;
-                            }
-                        }
-                        // what the next tile waits for
-                        scales_there = peek(&sm.sc_full[(k + 1) % kScales], ((k + 1) / kScales) & 1);
-                        s_there = peek(&sm.s_full[(k + 1) & 1], ((k + 1) >> 1) & 1);
                         if (live) {
                             uint8_t *w_at = s_p + (k & 1) * p_bytes;
 #pragma unroll
                             for (int y = 0; y < kR; ++y) {
-                                l[y] += sum[y];
                                 uint32_t hi[kC / 2], lo[kC / 2];  // two columns each
 #pragma unroll
-                                for (int e = 0; e < kC / 2; ++e) split2(v[y][2 * e], v[y][2 * e + 1], hi[e], lo[e]);
+                                for (int e = 0; e < kC / 2; ++e) split2<false>(v[y][2 * e], v[y][2 * e + 1], hi[e], lo[e]);
                                 uint8_t *row = w_at + r[y] * 128;
                                 // a 16-byte unit u of the row stands at u ^ (row % 8); the rests are four units behind
                                 if (r[y] < geo.npad) {
                                     if constexpr (kStack) {
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e) {
-                                            const int at = ((2 * set + (e >> 1)) ^ (r[y] & 7)) * 16 + 8 * (e & 1) + 2 * (lane & 3);
+                                        for (int e = 0; e < kC / 2; ++e) {
+                                            const int byte = col(2 * e), at = ((byte >> 4) ^ (r[y] & 7)) * 16 + (byte & 15);
                                             *reinterpret_cast<uint16_t *>(row + at) = (uint16_t)hi[e];
                                             *reinterpret_cast<uint16_t *>(row + (at ^ 64)) = (uint16_t)lo[e];
                                         }
                                     } else {
 #pragma unroll
-                                        for (int u = 0; u < 2; ++u) {
-                                            const int at = ((2 * set + u) ^ (r[y] & 7)) * 16;
-                                            auto four = [&](const uint32_t(&x)[kC / 2]) {
-                                                return make_uint4(x[8 * u] | (x[8 * u + 1] << 16), x[8 * u + 2] | (x[8 * u + 3] << 16),
-                                                                  x[8 * u + 4] | (x[8 * u + 5] << 16), x[8 * u + 6] | (x[8 * u + 7] << 16));
+                                        for (int u = 0; u < kC / 16; ++u) {
+                                            const int at = ((set * (kC / 16) + u) ^ (r[y] & 7)) * 16;
+                                            auto all = [&](const uint32_t *x) {
+                                                return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
                                             };
-                                            *reinterpret_cast<uint4 *>(row + at) = four(hi);
-                                            *reinterpret_cast<uint4 *>(row + (at ^ 64)) = four(lo);
+                                            *reinterpret_cast<uint4 *>(row + at) = all(hi + 8 * u);
+                                            *reinterpret_cast<uint4 *>(row + (at ^ 64)) = all(lo + 8 * u);
                                         }
                                     }
                                 }
@@ -713,13 +714,33 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         const int valid = min(kKvTile, w.len - j * kKvTile);
                         if (valid & 31) {  // value rows behind the sequence in the product's last step of 32
                             const int units = (-valid & 31) * 8;
-                            for (int u = tid; u < (kChunks - 1) * units; u += kSoftmaxThreads)
+                            for (int u = tid; u < (kChunks - 1) * units; u += kSoft)
                                 reinterpret_cast<uint4 *>(s_ring + slot * kTile8 + u / units * kChunk8)[valid * 8 + u % units] =
                                     make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async();
                         tc::fence_before_sync();
                         tma::arrive_warp(&sm.p_full[k & 1]);
+                        s_there = peek(&sm.s_full[(k + 1) & 1], ((k + 1) >> 1) & 1);
+                        // low weights: a window's largest is left in shared memory behind its last tile, and looked at behind the next
+                        const int of_window = (j - w.j0) & (kWindow - 1);
+#pragma unroll
+                        for (int y = 0; y < kR; ++y) {
+                            l[y] += sum[y];
+                            recent[y] = anew[y] ? most[y] : fmaxf(recent[y], most[y]);
+                            faint[y] = false;
+                            if (of_window == kWindow - 1) {
+                                if constexpr (kStack) {
+                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 1));
+                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 2));
+                                }
+                                if (lead) sm.recent[set][r[y]] = recent[y];
+                                recent[y] = 0.f;
+                            } else if (of_window == 0 && !first && !anew[y]) {  // (a new reference was set by weights that are not low)
+                                const float most_of = window(r[y]);
+                                faint[y] = most_of < kLeast && most_of > 0.f && m_ref[y] > m_top[y] - kReach;
+                            }
+                        }
                         ++k;
                     }
                 }
@@ -737,11 +758,15 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
                     l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
                 }
-                if (lead) sm.half[set][r[y]] = l[y];
+                if (lead) sm.part[set][r[y]] = l[y];
             }
-            if (softmax_any(!ok)) ok = false;
+            if (softmax_any<kSoft>(!ok)) ok = false;
 #pragma unroll
-            for (int y = 0; y < kR; ++y) l[y] += sm.half[set ^ 1][r[y]];
+            for (int y = 0; y < kR; ++y) {
+                l[y] = sm.part[0][r[y]];
+#pragma unroll
+                for (int i = 1; i < kSets; ++i) l[y] += sm.part[i][r[y]];
+            }
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg % kBad] != 0);
@@ -758,8 +783,8 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         p.lse[row0 + r[y]] = bad ? NAN : (l[y] == 0.f ? -INFINITY : m_ref[y] * p.scale + logf(l[y]));
                 }
             }
-            named_sync(2, kSoftmaxThreads);
-            for (int i = 2 * set; i < 2 * set + 2; ++i) {
+            named_sync(2, kSoft);
+            for (int i = kBlocks * set; i < kBlocks * (set + 1); ++i) {
                 const int lat = 128 * i + 32 * quarter + lane;
                 for (int e = 0; 16 * e < rows_here; ++e) {
                     uint32_t x[16];
@@ -793,18 +818,18 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             }
             // O^T has been read: the next stretch's W (all threads arrive) lets the MMA warp write it
             tc::fence_before_sync();
-            named_sync(2, kSoftmaxThreads);
+            named_sync(2, kSoft);
             if (w.work) ++seg;
         }
         if (!ok) sm.failed = 1;
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (sm.failed && (warp == 8 || warp == 9)) {
+    if (sm.failed && (warp == kIssue || warp == kIssue + 1)) {
         // a wait gave up: report it, and let what is in flight land before the memory goes
         if (tma::elect()) {
             tc::commit(&sm.drained);  // each issuing thread's own products
-            if (warp == 8) {
+            if (warp == kIssue) {
                 set_status(p.status, KDA_ERR_CUDA);
                 tc::mbar_wait(&sm.drained, 0);
                 for (int e = max(0, sm.scaled - kScales); e < sm.scaled; ++e) tc::mbar_wait(&sm.sc_full[e % kScales], (e / kScales) & 1);
@@ -814,7 +839,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         }
         __syncwarp();
     }
-    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+    if (warp == kIssue) tc::tmem_dealloc(tmem, 512);
 }
 
 constexpr size_t kSmem8 = 232448;

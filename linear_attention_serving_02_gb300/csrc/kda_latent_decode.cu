@@ -71,6 +71,7 @@ constexpr uint32_t kPairB = 2 * kChunkB;
 constexpr int kPairs = kLatent / 128;         // chunk pairs of a tile's latent: 4
 constexpr int kMaxPair = 12, kMaxPos = 4;     // ring slots at most
 constexpr int kDecThreads = 352;              // 8 softmax warps, S issue, value issue, TMA
+constexpr int kSoftmaxThreads = 256;
 constexpr float kGrow = 8.0f;
 constexpr int kHalf = kKvTile / 2;            // cached rows of a tile that a softmax thread takes
 
@@ -432,12 +433,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                         }
                         tma::arrive_warp(&sm.s_free[k % kS]);
                         // one barrier a tile: does a row need a new reference (also from -inf to a finite one), did a wait fail
-                        const bool any = softmax_any((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
+                        const bool any = softmax_any<kSoftmaxThreads>((owner && (first || (top - m_ref) * c > kGrow)) || !ok);
                         if (k > 0) ok = tma::wait_warp(&sm.pv_done, (k - 1) & 1) && ok;
                         if (any) {
                             if (low) sm.half[set][r] = top;
                             // all stop together when any wait failed
-                            if (softmax_any(!ok)) {
+                            if (softmax_any<kSoftmaxThreads>(!ok)) {
                                 ok = false;
                                 stopped = true;
                                 break;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kda_mla_decode_kernel(const __
                 tc::fence_after_sync();
             }
             if (low) sm.half[set][r] = l;
-            if (softmax_any(!ok)) ok = false;
+            if (softmax_any<kSoftmaxThreads>(!ok)) ok = false;
             l += sm.half[set ^ 1][r];
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;

@@ -12,7 +12,6 @@ namespace {
 
 constexpr int kKvTile = 64;           // cached rows of a tile
 constexpr int kMaxGroups = 160;       // CTAs that share the list at most
-constexpr int kSoftmaxThreads = 256;
 constexpr int kFold = 1024;           // tiles of a stretch that O^T sums in tensor memory (a power of two)
 
 struct SplitGeom {
@@ -47,7 +46,8 @@ __device__ __forceinline__ int32_t tiles_of(const SplitArgs &p, int32_t len) {
 struct Runs {
     int64_t each;
     int32_t extra;
-    __device__ __forceinline__ Runs(int64_t total, int32_t G) : each(total / G), extra((int32_t)(total - each * G)) {}
+    __device__ __forceinline__ Runs(int64_t total, int32_t G)
+        : each(total <= INT32_MAX ? (int32_t)total / G : total / G), extra((int32_t)(total - each * G)) {}
     __device__ __forceinline__ int64_t begin(int32_t g) const { return g * each + min(g, extra); }
     // the run that holds tile x
     __device__ __forceinline__ int32_t of(int64_t x) const {
@@ -58,7 +58,7 @@ struct Runs {
 
 // a run of the list in shared memory: its ends, and where it begins
 struct Run {
-    int32_t first_seq, first_tile;
+    int32_t first_seq, first_tile, first_len;
     int64_t begin, end;
 };
 
@@ -66,7 +66,12 @@ struct Run {
 __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run &run) {
     const int lane = threadIdx.x & 31;
     int64_t total = 0;
-    for (int n = lane; n < p.N; n += 32) total += tiles_of(p, p.lens[n]);
+    int32_t own = 0;  // length of sequence `lane`: with up to 32 of them the second look loads nothing
+    for (int n = lane; n < p.N; n += 32) {
+        const int32_t len = p.lens[n];
+        if (n == lane) own = len;
+        total += tiles_of(p, len);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
     const Runs runs(total, p.G);
@@ -74,10 +79,11 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
     int64_t before = 0;
     int seq = p.N - 1;
     int64_t first = 0;
-    int32_t of = 0;
+    int32_t of = 0, first_len = 0;
     for (int n0 = 0; n0 < p.N; n0 += 32) {
         const int n = n0 + lane;
-        const int32_t t = n < p.N ? tiles_of(p, p.lens[n]) : 0;
+        const int32_t len = n0 == 0 || n >= p.N ? own : p.lens[n];
+        const int32_t t = n < p.N ? tiles_of(p, len) : 0;
         int64_t incl = t;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -91,6 +97,7 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
             seq = n0 + src;
             first = begin - __shfl_sync(0xffffffffu, lo, src);
             of = __shfl_sync(0xffffffffu, t, src);
+            first_len = __shfl_sync(0xffffffffu, len, src);
             break;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -98,6 +105,7 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
     if (lane == 0) {
         run.first_seq = seq;
         run.first_tile = (int32_t)first;
+        run.first_len = first_len;
         run.begin = begin;
         run.end = end;
         if (rt == 0) {
@@ -119,6 +127,9 @@ struct Walk {
         // where it stands and not again: with a load that the compiler may repeat, two tiles of 72 rows take
         // longer (64 sequences x 130 rows 138 us, 131 so)
         asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(len) : "l"(p.lens + n));
+        enter(p);
+    }
+    __device__ __forceinline__ void enter(const SplitArgs &p) {
         tiles = tiles_of(p, len);
         j1 = (int32_t)min((int64_t)tiles, j0 + left);
         work = len > 0 && !bad_len(p, len);
@@ -127,7 +138,8 @@ struct Walk {
         n = run.first_seq;
         j0 = run.first_tile;
         left = run.end - run.begin;
-        if (left > 0) open(p);
+        len = run.first_len;
+        if (left > 0) enter(p);
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
     __device__ __forceinline__ void next(const SplitArgs &p) {
@@ -141,12 +153,13 @@ struct Walk {
     }
 };
 
-// barrier of the softmax warps that also tells whether any thread's flag is set
+// barrier of the softmax warps (N threads) that also tells whether any thread's flag is set
+template <int N>
 __device__ __forceinline__ bool softmax_any(bool flag) {
     uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, 256, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
                  : "=r"(r)
-                 : "r"((uint32_t)flag)
+                 : "r"((uint32_t)flag), "n"(N)
                  : "memory");
     return r != 0;
 }

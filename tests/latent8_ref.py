@@ -12,9 +12,9 @@ Bounds (half steps relative to the value: bf16 2^-8, e4m3 2^-4, e5m2 2^-3, fp16 
            w = e^{s - M} s_j goes to fp16 and then into an e4m3 and, its remainder, an e5m2: off by at most
            2^-4 2^-3 w + 2^-11 w, and where w is below the e4m3's normal range (2^-6 in the row's unit) by 2^-10 2^-3,
            or half of e5m2's last step, 2^-17: 2^-12.9 of the unit in all. The unit is at most twice the largest
-           weight of the current window of 4 tiles of 64 cached rows or of the one before it (after each window whose
-           largest is less than half of it, it is set to less than that largest), the windows counting from any
-           tile: of the 7 tiles before a tile and the 3 behind it; and at least 2^-43 of the largest weight of all
+           weight of the current window of 4 tiles of 64 cached rows or of the one before it (a tile after each window
+           whose largest is less than half of it, it is set to less than that largest), the windows counting from
+           any tile: of the 9 tiles before a tile and the 3 behind it; and at least 2^-43 of the largest weight of all
   sums     2 n 2^-23 in all, n the keys
   o        |do| <= (2^-7 + 2^-11 + 4 ds + 2 n 2^-23 + 2^-18) sum p|v| / sum p
                    + 2^-11.9 sum_tiles (max(p s) of those tiles + 2^-42 of all) sum|c| / sum p + 2^-8 |o|
@@ -104,7 +104,7 @@ def attend(q, c, s, scale, seen):
     pad = -n % TILE
     w = torch.nn.functional.pad(p * s, (0, pad)).view(R, -1, TILE).amax(2)
     size = torch.nn.functional.pad(c[:, :LATENT].abs(), (0, 0, 0, pad)).view(-1, TILE, LATENT).sum(1)
-    near = torch.nn.functional.max_pool1d(torch.nn.functional.pad(w, (7, 3))[:, None], 11, 1)[:, 0]
+    near = torch.nn.functional.max_pool1d(torch.nn.functional.pad(w, (9, 3))[:, None], 13, 1)[:, 0]
     tiles = ((near + 2.0 ** -42 * w.amax(1, keepdim=True)) @ size) / safe
     cnt = seen.sum(1).double()
     bo = 1.02 * ((2.0 ** -7 + 2.0 ** -11 + 4 * ds + 2 * cnt * STEP32 + 2.0 ** -18)[:, None] * ab + 2.0 ** -11.9 * tiles +
