@@ -27,6 +27,8 @@
 // product's 32-row steps past the length are left out, and value rows inside the last step are zeroed in shared
 // memory; their scales are never loaded.
 
+#include <cstddef>
+
 #include "kda_latent_split.cuh"
 
 namespace kda {
@@ -35,9 +37,10 @@ namespace {
 constexpr uint32_t kChunk8 = kKvTile * 128;     // 64 rows of 128 bytes: 128 latents, or the positional key
 constexpr int kChunks = 5;                      // of a tile: 512 latents, then the positional key
 constexpr uint32_t kTile8 = kChunks * kChunk8;
-constexpr int kMaxSlots = 4;
-constexpr int kScales = 4;                      // tiles whose scales are kept: a slot is loaded anew behind the score products of the
-                                                // tile two before, which wait until the softmax has taken those of the tile four before
+constexpr int kMaxSlots = 5;
+constexpr int kScales = 8;                      // tiles whose scales are kept: more than the ring has, so that a slot is loaded anew only when
+                                                // the softmax is through with its tile
+constexpr bool QT1 = false;
 constexpr int kSets = 2, kSetCols = kKvTile / kSets;  // the softmax warps of a lane quarter, and the cached rows of a tile that each takes
 constexpr int kSoft = 128 * kSets;              // softmax threads
 constexpr int kIssue = kSoft / 32;              // the warps behind them: score issue, value issue, TMA, none
@@ -52,16 +55,16 @@ constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and w
 constexpr int kWindow = 4;                      // tiles over which a row's weights have to be low
 constexpr int kBad = 8;                         // stretches that the loads may be ahead of the output
 
+// Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
+// for a wait and a load, which five a tile would make the bound of few rows), or its five chunks where only
+// two tiles fit, each as soon as its products are through.
+constexpr int tiles_in(int form) { return form == 0 ? 4 : (form == 1 ? (QT1 ? 4 : 3) : 2); }
+constexpr int pieces_of(int form) { return form < 2 ? 1 : kChunks; }
+
 struct Geom8 : SplitGeom {
     int32_t form;  // query rows of a CTA: 0 up to 32, 1 up to 64, 2 up to 96
     uint32_t smem;
 };
-
-// Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
-// for a wait and a load, which five a tile would make the bound of few rows), or its five chunks where only
-// two tiles fit, each as soon as its products are through.
-constexpr int tiles_in(int form) { return 4 - form; }
-constexpr int pieces_of(int form) { return form < 2 ? 1 : kChunks; }
 
 struct Args8 : SplitArgs {
     CUtensorMap map;
@@ -78,10 +81,11 @@ struct Smem8 {
     uint64_t full[kMaxSlots][kChunks], empty[kMaxSlots][kChunks];  // a piece of a tile is there; may be loaded over
     uint64_t done[kMaxSlots];           // a tile's products are through
     uint64_t sc_full[kScales];
-    float sc[kScales][kKvTile];         // scales of a tile's rows
+    alignas(16) float sc[kScales][kKvTile];  // scales of a tile's rows (bulk copies land there)
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
     float part[kSets][128], recent[kSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
+    uint2 q_top[kSets][64];             // by query row: its halves' largest magnitudes
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
@@ -98,6 +102,13 @@ __device__ __forceinline__ void mma8(uint32_t d, uint32_t a_lo, uint32_t b_lo, u
         "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
         "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "n"(tma::kDescHi));
+}
+// the same with A in tensor memory: a row a lane, four values a column
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(id), "r"(accumulate), "n"(tma::kDescHi));
 }
 // whether the phase of this parity has ended, without waiting: asked for early, used with wait_warp later
 __device__ __forceinline__ bool peek(uint64_t *mbar, uint32_t parity) {
@@ -128,21 +139,51 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[
 // whole rows: 16 or 32 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[16]) { tma::tmem_ld16_nowait(taddr, r); }
 __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[32]) { tc::tmem_ld32_nowait(taddr, r); }
-// Two values (a first) as two bytes of e4m3 (into the low half of hi) and two for their rest: e4m3 for queries, which in
-// fp16 are what they were, and e5m2 for weights, which go on further down
-template <bool QUERY>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+// two values (a first) as a pair of fp16
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+    asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
+// A pair of fp16 as two bytes of e4m3 and two for the rests: e5m2 for weights, which goes on further down, and e4m3 for
+// queries, whose eight bits the two then hold
+__device__ __forceinline__ void split_weights(uint32_t w, uint16_t &hi, uint16_t &lo) {
+    asm("{\n.reg .b32 v;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, %2;\ncvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 v, %2, v;\n"
+        "cvt.rn.satfinite.e5m2x2.f16x2 %1, v;\n}\n"
+        : "=&h"(hi), "=h"(lo)
+        : "r"(w));
+}
+__device__ __forceinline__ void split_queries(uint32_t w, uint16_t &hi, uint16_t &lo) {
+    asm("{\n.reg .b32 v;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, %2;\ncvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 v, %2, v;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %1, v;\n}\n"
+        : "=&h"(hi), "=h"(lo)
+        : "r"(w));
+}
+
+// The unit 2^a of a query row: its largest latent in (224, 448] of it, unless positional values that dwarf the
+// latents would leave bf16's range. Given the bits of the largest magnitudes as fp32, where NaN is above all.
+struct Unit {
+    int a;
+    float inv;
+    bool sound;  // no infinity, no NaN: a row with one has no scores
+    __device__ __forceinline__ Unit(uint32_t top, uint32_t top_pe)
+        : a(max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100)), inv(exp2_of(-min(a, 120))),
+          sound(max(top, top_pe) < 0x7f800000u) {}
+    __device__ __forceinline__ uint32_t positions(uint32_t two) const {  // in the unit
+        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(two << 16) * inv, __uint_as_float(two & 0xffff0000u) * inv);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    __device__ __forceinline__ float factor(float c) const { return sound ? c * exp2_of(min(a, 120)) : NAN; }
+};
+// two bf16 values in the unit as e4m3 and the e4m3 of their rest (in fp16 they are what they were)
+__device__ __forceinline__ void split_query(uint32_t two, uint64_t inv2, uint32_t &hi, uint32_t &lo) {
+    const float2 x = upk2(mul2(pk2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)), inv2));
     uint16_t h, l;
-    if (QUERY)
-        asm("{\n.reg .b32 w, v;\ncvt.rn.f16x2.f32 w, %3, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n"
-            "cvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 w, w, v;\ncvt.rn.satfinite.e4m3x2.f16x2 %1, w;\n}\n"
-            : "=h"(h), "=h"(l)
-            : "f"(a), "f"(b));
-    else
-        asm("{\n.reg .b32 w, v;\ncvt.rn.f16x2.f32 w, %3, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 %0, w;\n"
-            "cvt.rn.f16x2.e4m3x2 v, %0;\nsub.rn.f16x2 w, w, v;\ncvt.rn.satfinite.e5m2x2.f16x2 %1, w;\n}\n"
-            : "=h"(h), "=h"(l)
-            : "f"(a), "f"(b));
+    split_queries(half2_of(x.x, x.y), h, l);
     hi = h, lo = l;
 }
 
@@ -160,7 +201,8 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     const Geom8 &geo = p.geo;
     // Q: four chunks of 128 latents of hi (and lo, stacked; else four of lo behind), then the positional part
     const uint32_t q_chunk = (uint32_t)(kStack ? MS : geo.rows) * 128;
-    constexpr int q_chunks = kStack ? 5 : 9;
+    constexpr bool kQT = FORM == 1 && QT1;  // Q's latents are in tensor memory
+    constexpr int q_chunks = kQT ? 1 : (kStack ? 5 : 9);
     uint8_t *s_q = base;                          // M = 128 reads of fewer rows run on into what follows,
     uint8_t *s_p = s_q + q_chunks * q_chunk;      // rows of S that nobody reads
     const uint32_t p_bytes = (uint32_t)geo.npad * 128;  // W, twice: npad rows of 64 bytes of e4m3, then 64 of e5m2
@@ -197,6 +239,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
     const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
+    const uint32_t t_q = t_s + 2 * kKvTile;    // and, stacked, the queries' latents in 128
     const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
@@ -208,7 +251,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                 Walk w;
                 w.start(p, sm.run);
                 w.skip_idle(p);
-                int seg = 0, ps = 0, pph = 0;
+                int seg = 0, ps = 0, pph = 0, issued = 0, scaled = 0;
                 const int sub = kKvTile / p.rb;  // boxes of rows of a tile: 1, 2 or 4
                 while (!w.done() && ok) {
                     const int32_t *entry = p.table + (int64_t)w.n * p.max_pages;
@@ -246,40 +289,48 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         }
                         look(j + 1);
                         const int valid = min(kKvTile, w.len - j * kKvTile), boxes = (valid + p.rb - 1) / p.rb;
-                        // the rows' scales stand behind the page's rows; of a page that is not there, none are loaded
-                        uint32_t scales = 0;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (b < boxes && pg[b] != INT32_MAX) scales += 4 * p.rb;
                         const uint32_t box = (uint32_t)p.rb * 128;
+                        uint8_t *dst = s_ring + ps * kTile8;
+#pragma unroll
                         for (int c = 0; c < kPieces; ++c) {  // the positional chunk first
                             const int chunk = c == 0 ? kChunks - 1 : c - 1;
                             ok = tc::mbar_wait(kPieces == 1 ? &sm.done[ps] : &sm.empty[ps][c], pph ^ 1);
                             if (!ok) break;
                             uint64_t *full = &sm.full[ps][c];
-                            tc::mbar_arrive_expect_tx(full, (kPieces == 1 ? kChunks : 1) * boxes * box);
-                            if (c == 0) {
-                                uint64_t *there = &sm.sc_full[sm.scaled % kScales];
-                                tc::mbar_arrive_expect_tx(there, scales);
+                            if (kPieces == 1) {
+                                tc::mbar_arrive_expect_tx(full, kChunks * boxes * box);
+                                if (p.rb == kKvTile) {
+                                    tma::load_4d(dst, &p.map, full, 0, ry[0], 0, pg[0]);
+                                } else {
+                                    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-                                for (int b = 0; b < 4; ++b)
-                                    if (b < boxes && pg[b] != INT32_MAX)
-                                        tc::bulk_g2s(&sm.sc[sm.scaled % kScales][b * p.rb],
-                                                     p.rows + pg[b] * p.page_stride + (int64_t)p.page_size * kRow8 + 4 * ry[b], 4 * p.rb, there);
-                                ++sm.scaled;
-                            }
-                            uint8_t *dst = s_ring + ps * kTile8;
-                            if (kPieces == 1 && p.rb == kKvTile) {
-                                tma::load_4d(dst, &p.map, full, 0, ry[0], 0, pg[0]);
+                                        for (int b = 0; b < 4; ++b)
+                                            if (b < boxes) tma::load_4d(dst + i * kChunk8 + b * box, &p.map, full, 0, ry[b], i, pg[b]);
+                                }
                             } else {
-                                for (int i = kPieces == 1 ? 0 : chunk; i < (kPieces == 1 ? kChunks : chunk + 1); ++i)
+                                tc::mbar_arrive_expect_tx(full, boxes * box);
+                                tma::load_4d(dst + chunk * kChunk8, &p.map, full, 0, ry[0], chunk, pg[0]);
 #pragma unroll
-                                    for (int b = 0; b < 4; ++b)
-                                        if (b < boxes) tma::load_4d(dst + i * kChunk8 + b * box, &p.map, full, 0, ry[b], i, pg[b]);
+                                for (int b = 1; b < 4; ++b)
+                                    if (b < boxes) tma::load_4d(dst + chunk * kChunk8 + b * box, &p.map, full, 0, ry[b], chunk, pg[b]);
                             }
-                            ++sm.issued;
-                            // the next tile into L2, where its pieces will be waited for
-                            if (kPieces > 1 && c == 0 && j + 1 < w.j1) {
+                            ++issued;
+                            if (c > 0) continue;
+                            // the rows' scales stand behind the page's rows; of a page that is not there, none are loaded
+                            uint32_t scales = 0;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (b < boxes && pg[b] != INT32_MAX) scales += 4 * p.rb;
+                            uint64_t *there = &sm.sc_full[scaled % kScales];
+                            tc::mbar_arrive_expect_tx(there, scales);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (b < boxes && pg[b] != INT32_MAX)
+                                    tc::bulk_g2s(&sm.sc[scaled % kScales][b * p.rb],
+                                                 p.rows + pg[b] * p.page_stride + (int64_t)p.page_size * kRow8 + 4 * ry[b], 4 * p.rb, there);
+                            ++scaled;
+                            // the next tile into L2: from HBM its load would take longer than the ring has tiles for
+                            if (j + 1 < w.j1) {
 #pragma unroll
                                 for (int b = 0; b < 4; ++b) {
                                     const int64_t row = ((int64_t)j + 1) * kKvTile + b * p.rb;
@@ -298,6 +349,8 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                     w.next(p);
                     w.skip_idle(p);
                 }
+                sm.issued = issued;
+                sm.scaled = scaled;
                 if (!ok) sm.failed = 1;
             }
             __syncwarp();
@@ -329,8 +382,12 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                     tma::mma_ss(d, q_lo + (q_chunks - 1) * q_step + 2 * s, b + (4 * kChunk8 >> 4) + 2 * s, id_pe, s != 0);
                                 } else {
                                     const uint32_t a = q_lo + (c - 1) * q_step + 2 * s, bb = b + (c - 1) * (kChunk8 >> 4) + 2 * s;
-                                    mma8(d, a, bb, id, 1);
-                                    if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
+                                    if (kQT) {
+                                        mma8_ts(d, t_q + 32 * (c - 1) + 8 * s, bb, id, 1);
+                                    } else {
+                                        mma8(d, a, bb, id, 1);
+                                        if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
+                                    }
                                 }
                             }
                             if (c == 0 && kPieces > 1) tc::commit(&sm.empty[ps][0]);
@@ -406,6 +463,13 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         const bool warp_rows = quarter * kRowsQ < rows_here;
         // column of a tile of value e
         auto col = [&](int e) { return kSetCols * set + (kStack ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e); };
+        uint8_t *w_row[kR];   // the rows of W, and the place of the first weight within
+        uint32_t w_at[kR];
+#pragma unroll
+        for (int y = 0; y < kR; ++y) {
+            w_row[y] = s_p + r[y] * 128;
+            w_at[y] = (((col(0) >> 4) ^ (r[y] & 7)) << 4) | (col(0) & 15);
+        }
         // the largest weight of a row's last window
         auto window = [&](int row) {
             float x = sm.recent[0][row];
@@ -419,54 +483,122 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         // Q of a stretch, a row a warp at a time; the last stretch's score products are through: its last tile was taken
         auto load_q = [&](const Walk &s) {
             const int64_t row0 = (int64_t)s.n * geo.R + row_first;
-            // the loads of kBatch rows are on their way before the first is looked at
-            constexpr int kBatch = (FORM == 0 ? 4 : 6) * 2 / kSets;
-            for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
-                uint4 va[kBatch], vb[kBatch];
-                uint32_t vp[kBatch];
+            if constexpr (kQT) {
+                // A lane's row is its hi or lo part of a query row. Each of the two lanes, of both sets, takes 128 latents and 16
+                // positional values of the row, and they trade what is the other's.
+                const int i = lane & (kRowsQ - 1), lo_lane = (lane / kRowsQ) & 1, q = quarter * kRowsQ + i;
+                uint4 x[16], pe[2];
+                uint32_t top = 0, top_pe = 0;  // bits of the largest magnitudes, of bf16 and then of fp32; NaN is above all
+                if (warp_rows) {
+                    const int64_t row = row0 + min(q, rows_here - 1);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent + 256 * set + 128 * lo_lane);
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int64_t row = row0 + min(q0 + kIssue * b, rows_here - 1);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
-                    va[b] = src[0], vb[b] = src[1];
-                    vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
+                    for (int e = 0; e < 16; ++e) x[e] = src[e];
+                    src = reinterpret_cast<const uint4 *>(p.q_pe + row * kPos + 32 * set + 16 * lo_lane);
+                    pe[0] = src[0], pe[1] = src[1];
+                    auto larger = [](uint32_t t, const uint4 &u) {
+                        return __vmaxu2(__vmaxu2(t, __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu)), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+                    };
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) top = larger(top, x[e]);
+                    top_pe = larger(larger(0, pe[0]), pe[1]);
+                    top = max(top << 16, top & 0xffff0000u), top_pe = max(top_pe << 16, top_pe & 0xffff0000u);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, kRowsQ));
+                    top_pe = max(top_pe, __shfl_xor_sync(0xffffffffu, top_pe, kRowsQ));
+                    if (lo_lane == 0) sm.q_top[set][q] = make_uint2(top, top_pe);
                 }
+                named_sync(2, kSoft);
+                if (warp_rows) {
+                    const uint2 other = sm.q_top[set ^ 1][q];
+                    top = max(top, other.x), top_pe = max(top_pe, other.y);
+                    const Unit unit(top, top_pe);
+                    const uint64_t inv2 = pk2(unit.inv, unit.inv);
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int q = q0 + kIssue * b;
-                    if (q >= rows_here) break;
-                    const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
-                    // bits of the largest magnitudes, as bf16 and then as fp32; NaN is above all
-                    uint32_t top = 0;
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t keep[16], give[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
-                    top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
-                    const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
-                    // the unit 2^a: the latents' largest in (224, 448]; positional values that dwarf it stay in bf16's range
-                    const int a = max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100);
-                    const float inv = exp2_of(-min(a, 120));
-                    const uint64_t inv2 = pk2(inv, inv);
-                    uint32_t hi[4], lo[4];
+                        for (int u = 0; u < 8; ++u) {
+                            const uint32_t w4[4] = {x[8 * e + u].x, x[8 * e + u].y, x[8 * e + u].z, x[8 * e + u].w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 x = upk2(mul2(pk2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), inv2));
-                        uint32_t h, l;
-                        split2<true>(x.x, x.y, h, l);
-                        hi[i >> 1] = i & 1 ? hi[i >> 1] | (h << 16) : h;
-                        lo[i >> 1] = i & 1 ? lo[i >> 1] | (l << 16) : l;
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t hi[2], lo[2];
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) split_query(w4[2 * y + z], inv2, hi[z], lo[z]);
+                                const uint32_t h4 = hi[0] | (hi[1] << 16), l4 = lo[0] | (lo[1] << 16);
+                                keep[2 * u + y] = lo_lane ? l4 : h4;
+                                give[2 * u + y] = lo_lane ? h4 : l4;
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, give[y], kRowsQ);
+                            give[y] = lo_lane ? keep[y] : got;  // columns of the lo lane's latents,
+                            keep[y] = lo_lane ? got : keep[y];  // and of the hi lane's
+                        }
+                        tc::tmem_st16(t_q + lanes + 64 * set + 16 * e, keep);
+                        tc::tmem_st16(t_q + lanes + 64 * set + 32 + 16 * e, give);
                     }
-                    // rows of the operand: hi and lo of a quarter one behind the other, or the row itself
-                    const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
-                    uint8_t *at = s_q + (lane >> 3) * q_chunk;
-                    *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    at += kStack ? 0 : 4 * q_chunk;
-                    *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    const __nv_bfloat162 pes = __floats2bfloat162_rn(__uint_as_float(pe << 16) * inv, __uint_as_float(pe & 0xffff0000u) * inv);
-                    at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&pes);
-                    if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
-                    // a row with an infinity or a NaN has no scores
-                    if (lane == 0) sm.row_c[q] = max(top, top_pe) >= 0x7f800000u ? NAN : p.c * exp2_of(min(a, 120));
+                    // the positional values: the hi row's, and zeros in the lo row
+                    if (FORM != 0 || lane < 16) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int at = 4 * set + 2 * lo_lane + u, m_hi = quarter * 2 * kRowsQ + i, m_lo = m_hi + kRowsQ;
+                            const uint32_t w4[4] = {pe[u].x, pe[u].y, pe[u].z, pe[u].w};
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = unit.positions(w4[e]);
+                            *reinterpret_cast<uint4 *>(s_q + m_hi * 128 + ((at ^ (m_hi & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(s_q + m_lo * 128 + ((at ^ (m_lo & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                        }
+                        if (set == 0 && lo_lane == 0 && q < rows_here) sm.row_c[q] = unit.factor(p.c);
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                }
+            } else {
+                // the loads of kBatch rows are on their way before the first is looked at
+                constexpr int kBatch = (FORM == 0 ? 4 : 6) * 2 / kSets;
+                for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
+                    uint4 va[kBatch], vb[kBatch];
+                    uint32_t vp[kBatch];
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int64_t row = row0 + min(q0 + kIssue * b, rows_here - 1);
+                        const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
+                        va[b] = src[0], vb[b] = src[1];
+                        vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
+                    }
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int q = min(q0 + kIssue * b, rows_here - 1);  // (the last row again: the same values)
+                        const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
+                        // bits of the largest magnitudes, as bf16 and then as fp32; NaN is above all
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
+                        top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
+                        const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
+                        const Unit unit(top, top_pe);
+                        const uint64_t inv2 = pk2(unit.inv, unit.inv);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t h, l;
+                            split_query(v[i], inv2, h, l);
+                            hi[i >> 1] = i & 1 ? hi[i >> 1] | (h << 16) : h;
+                            lo[i >> 1] = i & 1 ? lo[i >> 1] | (l << 16) : l;
+                        }
+                                                // rows of the operand: hi and lo of a quarter one behind the other, or the row itself in chunks of its own
+                        const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
+                        uint8_t *at = s_q + (lane >> 3) * q_chunk;
+                        *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        at += kStack ? 0 : 4 * q_chunk;
+                        *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
+                        *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = unit.positions(pe);
+                        if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
+                        if (lane == 0) sm.row_c[q] = unit.factor(p.c);
+                    }
                 }
             }
             fence_proxy_async();
@@ -522,7 +654,9 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                     for (int j = js; j < je; ++j) {
                         const int slot = k % kTiles;
                         const bool first = j == w.j0;
-                        float sc[kC], v[kR][kC];  // the scales; scores, then weights
+                        float sc[kC];                                    // the rows' scales,
+                        uint64_t x2[kR][kC / 2];                         // the scores as powers of two, by pairs of cached rows,
+                        uint32_t w16[kR][kC / 2];                        // and the weights in fp16
                         auto scales = [&] {
 #pragma unroll
                             for (int e = 0; e < kC; e += 2) *reinterpret_cast<float2 *>(&sc[e]) = *reinterpret_cast<const float2 *>(&sm.sc[k % kScales][col(e)]);
@@ -540,42 +674,47 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         const uint32_t s_at = t_s + lanes + (k & 1) * kKvTile + set * kSetCols;
                         const bool live = warp_rows && ok;
                         float sum[kR], most[kR];
-                        auto scores = [&] {  // of this thread's rows, as powers of two; rounded here, so that huge ones still differ by 0 from themselves
+                        // (scores are rounded before a reference is taken off, so that huge ones still differ by 0 from themselves)
+                        auto scores = [&] {
                             if constexpr (FORM == 2) {
                                 uint32_t x[kC];
                                 tmem_ld_row(s_at, x);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < kC; ++e) v[0][e] = __uint_as_float(x[e]);
+                                for (int e = 0; e < kC / 2; ++e) x2[0][e] = pk2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                             } else if constexpr (FORM == 1) {
                                 uint32_t hi[2 * kC], lo[2 * kC];
                                 tmem_ld_fragments(s_at, hi);
                                 tmem_ld_fragments(s_at + (16u << 16), lo);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 2 * kC; ++e)
-                                    v[(e >> 1) & 1][2 * (e >> 2) + (e & 1)] = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
+                                for (int e = 0; e < kC; ++e)
+                                    x2[e & 1][e >> 1] = add2(pk2(__uint_as_float(hi[2 * e]), __uint_as_float(hi[2 * e + 1])),
+                                                             pk2(__uint_as_float(lo[2 * e]), __uint_as_float(lo[2 * e + 1])));
                             } else {
                                 uint32_t x[2 * kC];
                                 tmem_ld_fragments(s_at, x);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < kC; ++e)
-                                    v[0][e] = __uint_as_float(x[4 * (e >> 1) + (e & 1)]) + __uint_as_float(x[4 * (e >> 1) + 2 + (e & 1)]);
+                                for (int e = 0; e < kC / 2; ++e)
+                                    x2[0][e] = add2(pk2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])),
+                                                    pk2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
                             }
                             tc::fence_before_sync();
 #pragma unroll
-                            for (int y = 0; y < kR; ++y) {
+                            for (int y = 0; y < kR; ++y)
 #pragma unroll
-                                for (int e = 0; e < kC; e += 2) {
-                                    const float2 t = upk2(mul2(mul2(pk2(v[y][e], v[y][e + 1]), pk2(sc[e], sc[e + 1])), pk2(c[y], c[y])));
-                                    v[y][e] = t.x, v[y][e + 1] = t.y;
-                                }
-                                const int seen = w.len - j * kKvTile - unseen[y];  // cached rows of the tile that the row sees
-                                if (__any_sync(0xffffffffu, seen < kKvTile)) {
+                                for (int e = 0; e < kC / 2; ++e)
+                                    x2[y][e] = mul2(mul2(x2[y][e], pk2(sc[2 * e], sc[2 * e + 1])), pk2(c[y], c[y]));
+                            if (w.len - j * kKvTile - (p.m - 1) < kKvTile) {  // a tile of which not every row sees all
 #pragma unroll
-                                    for (int e = 0; e < kC; ++e)
-                                        if (col(e) >= seen) v[y][e] = -INFINITY;
+                                for (int y = 0; y < kR; ++y) {
+                                    const int seen = w.len - j * kKvTile - unseen[y];
+#pragma unroll
+                                    for (int e = 0; e < kC / 2; ++e) {
+                                        const float2 x = upk2(x2[y][e]);
+                                        x2[y][e] = pk2(col(2 * e) >= seen ? -INFINITY : x.x, col(2 * e + 1) >= seen ? -INFINITY : x.y);
+                                    }
                                 }
                             }
                         };
@@ -585,25 +724,27 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 const float mb = m_ref[y] == -INFINITY ? 0.f : -m_ref[y];
                                 const uint64_t mb2 = pk2(mb, mb);
                                 uint64_t l2[2] = {0, 0};
-                                most[y] = 0.f;
+                                uint32_t top = 0;
 #pragma unroll
-                                for (int e = 0; e < kC; e += 2) {
-                                    const float2 x = upk2(add2(pk2(v[y][e], v[y][e + 1]), mb2));
+                                for (int e = 0; e < kC / 2; ++e) {
+                                    const float2 x = upk2(add2(x2[y][e], mb2));
                                     const uint64_t pp = pk2(tc::ex2(x.x), tc::ex2(x.y));
-                                    l2[(e >> 1) & 1] = add2(l2[(e >> 1) & 1], pp);
-                                    const float2 ww = upk2(mul2(pp, pk2(sc[e], sc[e + 1])));
-                                    v[y][e] = ww.x, v[y][e + 1] = ww.y;
-                                    most[y] = fmaxf(most[y], fmaxf(ww.x, ww.y));
+                                    l2[e & 1] = add2(l2[e & 1], pp);
+                                    const float2 ww = upk2(mul2(pp, pk2(sc[2 * e], sc[2 * e + 1])));
+                                    w16[y][e] = half2_of(ww.x, ww.y);
+                                    top = max_half2(top, w16[y][e]);
                                 }
                                 const float2 ls = upk2(add2(l2[0], l2[1]));
                                 sum[y] = ls.x + ls.y;
+                                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&top));
+                                most[y] = fmaxf(t.x, t.y);
                             }
                         };
 #pragma unroll
                         for (int y = 0; y < kR; ++y) sum[y] = most[y] = 0.f;
-                        if (live) {
+                        if (live && !first) {
                             scores();
-                            if (!first) weights();
+                            weights();
                         }
                         // one barrier a tile: does a row need a new reference, did a wait fail
                         bool may = first || !ok;
@@ -619,14 +760,17 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                             // the largest exponent of a weight in this tile, over a row's threads
                             float top[kR];
                             scales();
-                            if (live && !first) scores();
+                            if (live) scores();
 #pragma unroll
                             for (int y = 0; y < kR; ++y) {
                                 top[y] = -INFINITY;
                                 if (live) {
+                                    auto of_scale = [&](int e) { return (float)((int)(__float_as_uint(sc[e]) >> 23) - 127); };  // its exponent
 #pragma unroll
-                                    for (int e = 0; e < kC; ++e)
-                                        top[y] = fmaxf(top[y], v[y][e] + (float)((int)(__float_as_uint(sc[e]) >> 23) - 127));  // with its row's exponent
+                                    for (int e = 0; e < kC / 2; ++e) {
+                                        const float2 x = upk2(x2[y][e]);
+                                        top[y] = fmaxf(top[y], fmaxf(x.x + of_scale(2 * e), x.y + of_scale(2 * e + 1)));
+                                    }
                                 }
                                 if constexpr (kStack) {
                                     top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
@@ -681,32 +825,35 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         }
                         tma::arrive_warp(&sm.s_free[k & 1]);
                         if (live) {
-                            uint8_t *w_at = s_p + (k & 1) * p_bytes;
 #pragma unroll
                             for (int y = 0; y < kR; ++y) {
-                                uint32_t hi[kC / 2], lo[kC / 2];  // two columns each
+                                if (r[y] >= geo.npad) continue;
+                                // the row's 16-byte unit u stands at u ^ (row % 8), the rests four units behind: the bits of a place
+                                // within the row are turned one by one
+                                uint8_t *row = w_row[y] + (k & 1) * p_bytes;
+                                const uint32_t at = w_at[y];
+                                if constexpr (kStack) {
 #pragma unroll
-                                for (int e = 0; e < kC / 2; ++e) split2<false>(v[y][2 * e], v[y][2 * e + 1], hi[e], lo[e]);
-                                uint8_t *row = w_at + r[y] * 128;
-                                // a 16-byte unit u of the row stands at u ^ (row % 8); the rests are four units behind
-                                if (r[y] < geo.npad) {
-                                    if constexpr (kStack) {
+                                    for (int e = 0; e < kC / 2; ++e) {
+                                        uint16_t hi, lo;
+                                        split_weights(w16[y][e], hi, lo);
+                                        *reinterpret_cast<uint16_t *>(row + (at ^ (8 * e))) = hi;
+                                        *reinterpret_cast<uint16_t *>(row + (at ^ (8 * e) ^ 64)) = lo;
+                                    }
+                                } else {
 #pragma unroll
-                                        for (int e = 0; e < kC / 2; ++e) {
-                                            const int byte = col(2 * e), at = ((byte >> 4) ^ (r[y] & 7)) * 16 + (byte & 15);
-                                            *reinterpret_cast<uint16_t *>(row + at) = (uint16_t)hi[e];
-                                            *reinterpret_cast<uint16_t *>(row + (at ^ 64)) = (uint16_t)lo[e];
+                                    for (int u = 0; u < kC / 16; ++u) {
+                                        uint32_t hi[4], lo[4];
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) {
+                                            uint16_t a[4];
+                                            split_weights(w16[y][8 * u + 2 * e], a[0], a[1]);
+                                            split_weights(w16[y][8 * u + 2 * e + 1], a[2], a[3]);
+                                            asm("mov.b32 %0, {%1, %2};" : "=r"(hi[e]) : "h"(a[0]), "h"(a[2]));
+                                            asm("mov.b32 %0, {%1, %2};" : "=r"(lo[e]) : "h"(a[1]), "h"(a[3]));
                                         }
-                                    } else {
-#pragma unroll
-                                        for (int u = 0; u < kC / 16; ++u) {
-                                            const int at = ((set * (kC / 16) + u) ^ (r[y] & 7)) * 16;
-                                            auto all = [&](const uint32_t *x) {
-                                                return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
-                                            };
-                                            *reinterpret_cast<uint4 *>(row + at) = all(hi + 8 * u);
-                                            *reinterpret_cast<uint4 *>(row + (at ^ 64)) = all(lo + 8 * u);
-                                        }
+                                        *reinterpret_cast<uint4 *>(row + (at ^ (16 * u))) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                        *reinterpret_cast<uint4 *>(row + (at ^ (16 * u) ^ 64)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                                     }
                                 }
                             }
@@ -727,7 +874,8 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
 #pragma unroll
                         for (int y = 0; y < kR; ++y) {
                             l[y] += sum[y];
-                            recent[y] = anew[y] ? most[y] : fmaxf(recent[y], most[y]);
+                            // (what fp16 rounds to nothing is there all the same)
+                            recent[y] = fmaxf(anew[y] ? 0.f : recent[y], fmaxf(most[y], sum[y] > 0.f ? 1e-30f : 0.f));
                             faint[y] = false;
                             if (of_window == kWindow - 1) {
                                 if constexpr (kStack) {
@@ -748,6 +896,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                 Walk after = w;
                 after.next(p);
                 after.skip_idle(p);
+                if (softmax_any<kSoft>(!ok)) ok = false;
                 if (ok && !after.done()) load_q(after);
                 if (ok) ok = through(k - 1);
                 tc::fence_after_sync();
@@ -851,14 +1000,15 @@ Geom8 geometry8(int32_t H, int32_t m) {
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
     q.form = q.rows <= 32 ? 0 : (q.rows <= 64 ? 1 : 2);
-    const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)5 * (q.form == 0 ? 64 : 128) * 128;
+    const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)(q.form == 0 ? 5 * 64 : (QT1 ? 1 : 5) * 128) * 128;
     q.smem = (uint32_t)(1024 + sizeof(Smem8) + of_q + (size_t)q.npad * 256 + (size_t)tiles_in(q.form) * kTile8);
     return q;
 }
 static_assert(1024 + sizeof(Smem8) + 5 * 64 * 128 + 32 * 256 + tiles_in(0) * kTile8 <= kSmem8, "32 rows");
-static_assert(1024 + sizeof(Smem8) + 5 * 128 * 128 + 64 * 256 + tiles_in(1) * kTile8 <= kSmem8, "64 rows");
+static_assert(1024 + sizeof(Smem8) + (QT1 ? 1 : 5) * 128 * 128 + 64 * 256 + tiles_in(1) * kTile8 <= kSmem8, "64 rows");
 static_assert(1024 + sizeof(Smem8) + 11 * kMostRows8 * 128 + tiles_in(2) * kTile8 <= kSmem8, "96 rows");
-static_assert(tiles_in(0) <= kMaxSlots, "");
+static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales, "");
+static_assert(offsetof(Smem8, sc) % 16 == 0 && kTile8 % 1024 == 0, "bulk copies");
 static_assert(kMaxSlots + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
 }  // namespace
