@@ -40,15 +40,15 @@ constexpr uint32_t kTile8 = kChunks * kChunk8;
 constexpr int kMaxSlots = 5;
 constexpr int kScales = 8;                      // tiles whose scales are kept: more than the ring has, so that a slot is loaded anew only when
                                                 // the softmax is through with its tile
-constexpr bool QT1 = false;
-constexpr int kSets = 2, kSetCols = kKvTile / kSets;  // the softmax warps of a lane quarter, and the cached rows of a tile that each takes
-constexpr int kSoft = 128 * kSets;              // softmax threads
-constexpr int kIssue = kSoft / 32;              // the warps behind them: score issue, value issue, TMA, none
-constexpr int kThreads8 = kSoft + 128;
-constexpr int kBlocks = kLatent / 128 / kSets;  // of 128 latents of O^T that a softmax warp reads
-// Registers of a softmax thread and of the others, out of those that the block is launched with
-constexpr int kLaunched = kSets == 2 ? 168 : 96, kRegsSoftmax = kSets == 2 ? 208 : 104, kRegsIssue = kSets == 2 ? 80 : 64;
-static_assert(kSoft * kRegsSoftmax + 128 * kRegsIssue <= kThreads8 * kLaunched, "the shares' sum");
+// The softmax warps of a lane quarter by form: each takes its share of a tile's cached rows, and of O^T's blocks of 128
+// latents. Behind them stand four more: score issue, value issue, TMA, none.
+constexpr int kMostSets = 4;
+constexpr int sets_of(int form) { return 2; }
+constexpr int threads_of(int form) { return 128 * sets_of(form) + 128; }
+// Registers that a block is launched with a thread, and how they are shared out
+constexpr int launched_of(int form) { return sets_of(form) == 2 ? 168 : 96; }
+constexpr int softmax_regs(int form) { return sets_of(form) == 2 ? 208 : 104; }
+constexpr int issue_regs(int form) { return sets_of(form) == 2 ? 80 : 64; }
 constexpr int kMostRows8 = 96;                  // query rows of a CTA
 constexpr float kSet = 2.5f, kHigh = 8.75f, kReach = 40.0f;  // powers of two
 constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and what is low
@@ -58,7 +58,7 @@ constexpr int kBad = 8;                         // stretches that the loads may 
 // Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
 // for a wait and a load, which five a tile would make the bound of few rows), or its five chunks where only
 // two tiles fit, each as soon as its products are through.
-constexpr int tiles_in(int form) { return form == 0 ? 4 : (form == 1 ? (QT1 ? 4 : 3) : 2); }
+constexpr int tiles_in(int form) { return 4 - form; }
 constexpr int pieces_of(int form) { return form < 2 ? 1 : kChunks; }
 
 struct Geom8 : SplitGeom {
@@ -84,8 +84,7 @@ struct Smem8 {
     alignas(16) float sc[kScales][kKvTile];  // scales of a tile's rows (bulk copies land there)
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
-    float part[kSets][128], recent[kSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
-    uint2 q_top[kSets][64];             // by query row: its halves' largest magnitudes
+    float part[kMostSets][128], recent[kMostSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
@@ -102,13 +101,6 @@ __device__ __forceinline__ void mma8(uint32_t d, uint32_t a_lo, uint32_t b_lo, u
         "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}\n" ::"r"(d),
         "r"(a_lo), "r"(b_lo), "r"(id), "r"(accumulate), "n"(tma::kDescHi));
-}
-// the same with A in tensor memory: a row a lane, four values a column
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t id, uint32_t accumulate) {
-    asm volatile(
-        "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-        "r"(a_tmem), "r"(b_lo), "r"(id), "r"(accumulate), "n"(tma::kDescHi));
 }
 // whether the phase of this parity has ended, without waiting: asked for early, used with wait_warp later
 __device__ __forceinline__ bool peek(uint64_t *mbar, uint32_t parity) {
@@ -164,6 +156,12 @@ __device__ __forceinline__ void split_queries(uint32_t w, uint16_t &hi, uint16_t
         : "r"(w));
 }
 
+__device__ __forceinline__ void store2(uint32_t at, int more, uint16_t v) {
+    asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(at + more), "h"(v) : "memory");
+}
+__device__ __forceinline__ void store16(uint32_t at, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 // The unit 2^a of a query row: its largest latent in (224, 448] of it, unless positional values that dwarf the
 // latents would leave bf16's range. Given the bits of the largest magnitudes as fp32, where NaN is above all.
 struct Unit {
@@ -189,9 +187,12 @@ __device__ __forceinline__ void split_query(uint32_t two, uint64_t inv2, uint32_
 
 // FORM: query rows of a CTA, as in Geom8
 template <int FORM>
-__global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const __grid_constant__ Args8 p) {
+__global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel(const __grid_constant__ Args8 p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int kSets = sets_of(FORM), kSetCols = kKvTile / kSets, kBlocks = kLatent / 128 / kSets;
+    constexpr int kSoft = 128 * kSets, kIssue = kSoft / 32;  // softmax threads; the first warp behind them
+    static_assert(kSoft * softmax_regs(FORM) + 128 * issue_regs(FORM) <= threads_of(FORM) * launched_of(FORM), "the shares' sum");
     constexpr int MS = FORM == 0 ? 64 : 128;   // M of the score product
     constexpr bool kStack = FORM < 2;          // hi and lo rows in one product
     constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, where lo lies behind hi)
@@ -201,8 +202,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     const Geom8 &geo = p.geo;
     // Q: four chunks of 128 latents of hi (and lo, stacked; else four of lo behind), then the positional part
     const uint32_t q_chunk = (uint32_t)(kStack ? MS : geo.rows) * 128;
-    constexpr bool kQT = FORM == 1 && QT1;  // Q's latents are in tensor memory
-    constexpr int q_chunks = kQT ? 1 : (kStack ? 5 : 9);
+    constexpr int q_chunks = kStack ? 5 : 9;
     uint8_t *s_q = base;                          // M = 128 reads of fewer rows run on into what follows,
     uint8_t *s_p = s_q + q_chunks * q_chunk;      // rows of S that nobody reads
     const uint32_t p_bytes = (uint32_t)geo.npad * 128;  // W, twice: npad rows of 64 bytes of e4m3, then 64 of e5m2
@@ -239,12 +239,11 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
     const uint32_t t_s = tmem + 4 * geo.npad;  // two S tiles of 64 columns behind O^T
-    const uint32_t t_q = t_s + 2 * kKvTile;    // and, stacked, the queries' latents in 128
     const int row_first = rt * geo.rows, rows_here = max(0, min(geo.rows, geo.R - row_first));
     bool ok = true;
 
     if (warp >= kIssue) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsIssue));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(issue_regs(FORM)));
         if (warp == kIssue + 2) {
             // ---- TMA producer: one thread ----
             if (tma::elect()) {
@@ -382,12 +381,8 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                     tma::mma_ss(d, q_lo + (q_chunks - 1) * q_step + 2 * s, b + (4 * kChunk8 >> 4) + 2 * s, id_pe, s != 0);
                                 } else {
                                     const uint32_t a = q_lo + (c - 1) * q_step + 2 * s, bb = b + (c - 1) * (kChunk8 >> 4) + 2 * s;
-                                    if (kQT) {
-                                        mma8_ts(d, t_q + 32 * (c - 1) + 8 * s, bb, id, 1);
-                                    } else {
-                                        mma8(d, a, bb, id, 1);
-                                        if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
-                                    }
+                                    mma8(d, a, bb, id, 1);
+                                    if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
                                 }
                             }
                             if (c == 0 && kPieces > 1) tc::commit(&sm.empty[ps][0]);
@@ -447,7 +442,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsSoftmax));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(softmax_regs(FORM)));
         // ---- softmax: a thread takes kC cached rows of a tile for each of kR query rows; then the output ----
         const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -463,12 +458,18 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         const bool warp_rows = quarter * kRowsQ < rows_here;
         // column of a tile of value e
         auto col = [&](int e) { return kSetCols * set + (kStack ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e); };
-        uint8_t *w_row[kR];   // the rows of W, and the place of the first weight within
+        // Where a thread's first weight of a row goes in W, and how far from there those 16 bytes on and the rests lie: a row's
+        // 16-byte unit u stands at u ^ (row % 8), its rests four units behind
         uint32_t w_at[kR];
+        int w_16[kR], w_64[kR];
+        float limit[kR];
 #pragma unroll
         for (int y = 0; y < kR; ++y) {
-            w_row[y] = s_p + r[y] * 128;
-            w_at[y] = (((col(0) >> 4) ^ (r[y] & 7)) << 4) | (col(0) & 15);
+            const int unit = (col(0) >> 4) ^ (r[y] & 7);
+            w_at[y] = tc::smem_addr(s_p) + r[y] * 128 + 16 * unit + (col(0) & 15);
+            w_16[y] = unit & 1 ? -16 : 16;
+            w_64[y] = unit & 4 ? -64 : 64;
+            limit[y] = owner[y] ? kMost : INFINITY;
         }
         // the largest weight of a row's last window
         auto window = [&](int row) {
@@ -483,122 +484,48 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
         // Q of a stretch, a row a warp at a time; the last stretch's score products are through: its last tile was taken
         auto load_q = [&](const Walk &s) {
             const int64_t row0 = (int64_t)s.n * geo.R + row_first;
-            if constexpr (kQT) {
-                // A lane's row is its hi or lo part of a query row. Each of the two lanes, of both sets, takes 128 latents and 16
-                // positional values of the row, and they trade what is the other's.
-                const int i = lane & (kRowsQ - 1), lo_lane = (lane / kRowsQ) & 1, q = quarter * kRowsQ + i;
-                uint4 x[16], pe[2];
-                uint32_t top = 0, top_pe = 0;  // bits of the largest magnitudes, of bf16 and then of fp32; NaN is above all
-                if (warp_rows) {
-                    const int64_t row = row0 + min(q, rows_here - 1);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent + 256 * set + 128 * lo_lane);
+            // the loads of kBatch rows are on their way before the first is looked at
+            constexpr int kBatch = (FORM == 0 ? 4 : 6) * 2 / kSets;
+            for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
+                uint4 va[kBatch], vb[kBatch];
+                uint32_t vp[kBatch];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = src[e];
-                    src = reinterpret_cast<const uint4 *>(p.q_pe + row * kPos + 32 * set + 16 * lo_lane);
-                    pe[0] = src[0], pe[1] = src[1];
-                    auto larger = [](uint32_t t, const uint4 &u) {
-                        return __vmaxu2(__vmaxu2(t, __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu)), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
-                    };
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) top = larger(top, x[e]);
-                    top_pe = larger(larger(0, pe[0]), pe[1]);
-                    top = max(top << 16, top & 0xffff0000u), top_pe = max(top_pe << 16, top_pe & 0xffff0000u);
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, kRowsQ));
-                    top_pe = max(top_pe, __shfl_xor_sync(0xffffffffu, top_pe, kRowsQ));
-                    if (lo_lane == 0) sm.q_top[set][q] = make_uint2(top, top_pe);
+                for (int b = 0; b < kBatch; ++b) {
+                    const int64_t row = row0 + min(q0 + kIssue * b, rows_here - 1);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
+                    va[b] = src[0], vb[b] = src[1];
+                    vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
                 }
-                named_sync(2, kSoft);
-                if (warp_rows) {
-                    const uint2 other = sm.q_top[set ^ 1][q];
-                    top = max(top, other.x), top_pe = max(top_pe, other.y);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int q = min(q0 + kIssue * b, rows_here - 1);  // (the last row again: the same values)
+                    const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
+                    // bits of the largest magnitudes, as bf16 and then as fp32; NaN is above all
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
+                    top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
+                    const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
                     const Unit unit(top, top_pe);
                     const uint64_t inv2 = pk2(unit.inv, unit.inv);
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t keep[16], give[16];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const uint32_t w4[4] = {x[8 * e + u].x, x[8 * e + u].y, x[8 * e + u].z, x[8 * e + u].w};
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                uint32_t hi[2], lo[2];
-#pragma unroll
-                                for (int z = 0; z < 2; ++z) split_query(w4[2 * y + z], inv2, hi[z], lo[z]);
-                                const uint32_t h4 = hi[0] | (hi[1] << 16), l4 = lo[0] | (lo[1] << 16);
-                                keep[2 * u + y] = lo_lane ? l4 : h4;
-                                give[2 * u + y] = lo_lane ? h4 : l4;
-                            }
-                        }
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, give[y], kRowsQ);
-                            give[y] = lo_lane ? keep[y] : got;  // columns of the lo lane's latents,
-                            keep[y] = lo_lane ? got : keep[y];  // and of the hi lane's
-                        }
-                        tc::tmem_st16(t_q + lanes + 64 * set + 16 * e, keep);
-                        tc::tmem_st16(t_q + lanes + 64 * set + 32 + 16 * e, give);
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t h, l;
+                        split_query(v[i], inv2, h, l);
+                        hi[i >> 1] = i & 1 ? hi[i >> 1] | (h << 16) : h;
+                        lo[i >> 1] = i & 1 ? lo[i >> 1] | (l << 16) : l;
                     }
-                    // the positional values: the hi row's, and zeros in the lo row
-                    if (FORM != 0 || lane < 16) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int at = 4 * set + 2 * lo_lane + u, m_hi = quarter * 2 * kRowsQ + i, m_lo = m_hi + kRowsQ;
-                            const uint32_t w4[4] = {pe[u].x, pe[u].y, pe[u].z, pe[u].w};
-                            uint32_t y[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] = unit.positions(w4[e]);
-                            *reinterpret_cast<uint4 *>(s_q + m_hi * 128 + ((at ^ (m_hi & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4 *>(s_q + m_lo * 128 + ((at ^ (m_lo & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-                        }
-                        if (set == 0 && lo_lane == 0 && q < rows_here) sm.row_c[q] = unit.factor(p.c);
-                    }
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                }
-            } else {
-                // the loads of kBatch rows are on their way before the first is looked at
-                constexpr int kBatch = (FORM == 0 ? 4 : 6) * 2 / kSets;
-                for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
-                    uint4 va[kBatch], vb[kBatch];
-                    uint32_t vp[kBatch];
-#pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int64_t row = row0 + min(q0 + kIssue * b, rows_here - 1);
-                        const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
-                        va[b] = src[0], vb[b] = src[1];
-                        vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
-                    }
-#pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int q = min(q0 + kIssue * b, rows_here - 1);  // (the last row again: the same values)
-                        const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
-                        // bits of the largest magnitudes, as bf16 and then as fp32; NaN is above all
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
-                        top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
-                        const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
-                        const Unit unit(top, top_pe);
-                        const uint64_t inv2 = pk2(unit.inv, unit.inv);
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint32_t h, l;
-                            split_query(v[i], inv2, h, l);
-                            hi[i >> 1] = i & 1 ? hi[i >> 1] | (h << 16) : h;
-                            lo[i >> 1] = i & 1 ? lo[i >> 1] | (l << 16) : l;
-                        }
-                                                // rows of the operand: hi and lo of a quarter one behind the other, or the row itself in chunks of its own
-                        const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
-                        uint8_t *at = s_q + (lane >> 3) * q_chunk;
-                        *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        at += kStack ? 0 : 4 * q_chunk;
-                        *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
-                        *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = unit.positions(pe);
-                        if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
-                        if (lane == 0) sm.row_c[q] = unit.factor(p.c);
-                    }
+                                            // rows of the operand: hi and lo of a quarter one behind the other, or the row itself in chunks of its own
+                    const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
+                    uint8_t *at = s_q + (lane >> 3) * q_chunk;
+                    *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    at += kStack ? 0 : 4 * q_chunk;
+                    *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = unit.positions(pe);
+                    if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
+                    if (lane == 0) sm.row_c[q] = unit.factor(p.c);
                 }
             }
             fence_proxy_async();
@@ -652,20 +579,14 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                     if (js >= w.j1) break;
                     const int je = min(w.j1, js + kFold);
                     for (int j = js; j < je; ++j) {
-                        const int slot = k % kTiles;
                         const bool first = j == w.j0;
+                        const int rem = w.len - j * kKvTile;             // cached rows of the sequence from this tile on
                         float sc[kC];                                    // the rows' scales,
                         uint64_t x2[kR][kC / 2];                         // the scores as powers of two, by pairs of cached rows,
                         uint32_t w16[kR][kC / 2];                        // and the weights in fp16
                         auto scales = [&] {
 #pragma unroll
                             for (int e = 0; e < kC; e += 2) *reinterpret_cast<float2 *>(&sc[e]) = *reinterpret_cast<const float2 *>(&sm.sc[k % kScales][col(e)]);
-                            // behind the sequence they count as one: 0 times what stands there may be NaN
-                            if (w.len - j * kKvTile < kKvTile) {
-#pragma unroll
-                                for (int e = 0; e < kC; ++e)
-                                    if (col(e) >= w.len - j * kKvTile) sc[e] = 1.f;
-                            }
                         };
                         ok = wait_peeked(s_there, &sm.s_full[k & 1], (k >> 1) & 1) && ok;
                         // a failed wait still meets the barriers below, so that no warp is left in them
@@ -706,16 +627,20 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
 #pragma unroll
                                 for (int e = 0; e < kC / 2; ++e)
                                     x2[y][e] = mul2(mul2(x2[y][e], pk2(sc[2 * e], sc[2 * e + 1])), pk2(c[y], c[y]));
-                            if (w.len - j * kKvTile - (p.m - 1) < kKvTile) {  // a tile of which not every row sees all
+                            if (rem - (p.m - 1) < kKvTile) {  // a tile of which not every row sees all
 #pragma unroll
                                 for (int y = 0; y < kR; ++y) {
-                                    const int seen = w.len - j * kKvTile - unseen[y];
+                                    const int seen = rem - unseen[y];
 #pragma unroll
                                     for (int e = 0; e < kC / 2; ++e) {
                                         const float2 x = upk2(x2[y][e]);
                                         x2[y][e] = pk2(col(2 * e) >= seen ? -INFINITY : x.x, col(2 * e + 1) >= seen ? -INFINITY : x.y);
                                     }
                                 }
+                                // scales behind the sequence count as one: 0 times what stands there may be NaN
+#pragma unroll
+                                for (int e = 0; e < kC; ++e)
+                                    if (col(e) >= rem) sc[e] = 1.f;
                             }
                         };
                         auto weights = [&] {
@@ -724,7 +649,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 const float mb = m_ref[y] == -INFINITY ? 0.f : -m_ref[y];
                                 const uint64_t mb2 = pk2(mb, mb);
                                 uint64_t l2[2] = {0, 0};
-                                uint32_t top = 0;
+                                uint32_t top = 0x00010001u;  // (2^-24: what fp16 rounds to nothing is there all the same)
 #pragma unroll
                                 for (int e = 0; e < kC / 2; ++e) {
                                     const float2 x = upk2(add2(x2[y][e], mb2));
@@ -749,8 +674,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                         // one barrier a tile: does a row need a new reference, did a wait fail
                         bool may = first || !ok;
 #pragma unroll
-                        for (int y = 0; y < kR; ++y)
-                            may |= owner[y] && (most[y] > kMost || faint[y] || (m_ref[y] == -INFINITY && w.len - j * kKvTile - unseen[y] > 0));
+                        for (int y = 0; y < kR; ++y) may |= faint[y] || most[y] > limit[y];
                         const bool any = softmax_any<kSoft>(may);
                         bool again = false, anew[kR];
 #pragma unroll
@@ -798,6 +722,8 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 const float f = anew[y] && !first ? tc::ex2(m_ref[y] - to) : 1.0f;
                                 if (set == 0 && lead) sm.factor[r[y]] = f;
                                 if (anew[y]) m_ref[y] = to;
+                                if (anew[y]) recent[y] = 0.f;
+                                faint[y] = owner[y] && m_ref[y] == -INFINITY;  // (a row that has seen nothing yet looks again)
                                 l[y] *= f;
                                 again |= owner[y] && anew[y] && !first;
                             }
@@ -828,17 +754,14 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
 #pragma unroll
                             for (int y = 0; y < kR; ++y) {
                                 if (r[y] >= geo.npad) continue;
-                                // the row's 16-byte unit u stands at u ^ (row % 8), the rests four units behind: the bits of a place
-                                // within the row are turned one by one
-                                uint8_t *row = w_row[y] + (k & 1) * p_bytes;
-                                const uint32_t at = w_at[y];
+                                const uint32_t a = w_at[y] + (k & 1) * p_bytes, b = a + w_16[y], a_lo = a + w_64[y], b_lo = b + w_64[y];
                                 if constexpr (kStack) {
 #pragma unroll
                                     for (int e = 0; e < kC / 2; ++e) {
                                         uint16_t hi, lo;
                                         split_weights(w16[y][e], hi, lo);
-                                        *reinterpret_cast<uint16_t *>(row + (at ^ (8 * e))) = hi;
-                                        *reinterpret_cast<uint16_t *>(row + (at ^ (8 * e) ^ 64)) = lo;
+                                        store2(e < 2 ? a : b, 8 * (e & 1), hi);
+                                        store2(e < 2 ? a_lo : b_lo, 8 * (e & 1), lo);
                                     }
                                 } else {
 #pragma unroll
@@ -846,23 +769,22 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                         uint32_t hi[4], lo[4];
 #pragma unroll
                                         for (int e = 0; e < 4; ++e) {
-                                            uint16_t a[4];
-                                            split_weights(w16[y][8 * u + 2 * e], a[0], a[1]);
-                                            split_weights(w16[y][8 * u + 2 * e + 1], a[2], a[3]);
-                                            asm("mov.b32 %0, {%1, %2};" : "=r"(hi[e]) : "h"(a[0]), "h"(a[2]));
-                                            asm("mov.b32 %0, {%1, %2};" : "=r"(lo[e]) : "h"(a[1]), "h"(a[3]));
+                                            uint16_t q[4];
+                                            split_weights(w16[y][8 * u + 2 * e], q[0], q[1]);
+                                            split_weights(w16[y][8 * u + 2 * e + 1], q[2], q[3]);
+                                            asm("mov.b32 %0, {%1, %2};" : "=r"(hi[e]) : "h"(q[0]), "h"(q[2]));
+                                            asm("mov.b32 %0, {%1, %2};" : "=r"(lo[e]) : "h"(q[1]), "h"(q[3]));
                                         }
-                                        *reinterpret_cast<uint4 *>(row + (at ^ (16 * u))) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                                        *reinterpret_cast<uint4 *>(row + (at ^ (16 * u) ^ 64)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                        store16(u ? b : a, hi);
+                                        store16(u ? b_lo : a_lo, lo);
                                     }
                                 }
                             }
                         }
-                        const int valid = min(kKvTile, w.len - j * kKvTile);
-                        if (valid & 31) {  // value rows behind the sequence in the product's last step of 32
-                            const int units = (-valid & 31) * 8;
+                        if (rem < kKvTile && (rem & 31)) {  // value rows behind the sequence in the product's last step of 32
+                            const int units = (-rem & 31) * 8;
                             for (int u = tid; u < (kChunks - 1) * units; u += kSoft)
-                                reinterpret_cast<uint4 *>(s_ring + slot * kTile8 + u / units * kChunk8)[valid * 8 + u % units] =
+                                reinterpret_cast<uint4 *>(s_ring + k % kTiles * kTile8 + u / units * kChunk8)[rem * 8 + u % units] =
                                     make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async();
@@ -874,9 +796,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
 #pragma unroll
                         for (int y = 0; y < kR; ++y) {
                             l[y] += sum[y];
-                            // (what fp16 rounds to nothing is there all the same)
-                            recent[y] = fmaxf(anew[y] ? 0.f : recent[y], fmaxf(most[y], sum[y] > 0.f ? 1e-30f : 0.f));
-                            faint[y] = false;
+                            recent[y] = fmaxf(recent[y], most[y]);
                             if (of_window == kWindow - 1) {
                                 if constexpr (kStack) {
                                     recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 1));
@@ -885,8 +805,7 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
                                 if (lead) sm.recent[set][r[y]] = recent[y];
                                 recent[y] = 0.f;
                             } else if (of_window == 0 && !first && !anew[y]) {  // (a new reference was set by weights that are not low)
-                                const float most_of = window(r[y]);
-                                faint[y] = most_of < kLeast && most_of > 0.f && m_ref[y] > m_top[y] - kReach;
+                                faint[y] |= owner[y] && window(r[y]) < kLeast && m_ref[y] > m_top[y] - kReach;
                             }
                         }
                         ++k;
@@ -935,33 +854,40 @@ __global__ void __launch_bounds__(kThreads8, 1) kda_mla_decode_fp8_kernel(const 
             named_sync(2, kSoft);
             for (int i = kBlocks * set; i < kBlocks * (set + 1); ++i) {
                 const int lat = 128 * i + 32 * quarter + lane;
-                for (int e = 0; 16 * e < rows_here; ++e) {
-                    uint32_t x[16];
+                for (int e0 = 0; e0 < rows_here; e0 += 32) {
+                    uint32_t x[2][16];
+                    const bool two = e0 + 16 < geo.npad;
                     if (w.work && ok) {
-                        tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + 16 * e, x);
+                        tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + e0, x[0]);
+                        if (two) tma::tmem_ld16_nowait(tmem + lanes + i * geo.npad + e0 + 16, x[1]);
                         tc::tmem_wait_ld();
                     } else {
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) x[y] = 0;
+                        for (int y = 0; y < 16; ++y) x[0][y] = x[1][y] = 0;
                     }
-                    if (whole) {
-                        // neighbouring lanes trade a value: each then holds two latents of one row
-                        __nv_bfloat16 *dst = p.o + (row0 + 16 * e + (lane & 1)) * kLatent + (lat & ~1);
-                        const int left = rows_here - 16 * e - (lane & 1);
 #pragma unroll
-                        for (int y = 0; y < 16; y += 2) {
-                            const float2 f = *reinterpret_cast<const float2 *>(&sm.factor[16 * e + y]);
-                            const __nv_bfloat162 h2 =
-                                __floats2bfloat162_rn(__uint_as_float(x[y]) * f.x, __uint_as_float(x[y + 1]) * f.y);
-                            const uint32_t own = *reinterpret_cast<const uint32_t *>(&h2);
-                            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-                            const uint32_t two_lat = (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-                            if (y < left) *reinterpret_cast<uint32_t *>(dst + y * kLatent) = two_lat;
+                    for (int z = 0; z < 2; ++z) {
+                        const int e = e0 + 16 * z;
+                        if (z && !two) break;
+                        if (whole) {
+                            // neighbouring lanes trade a value: each then holds two latents of one row
+                            __nv_bfloat16 *dst = p.o + (row0 + e + (lane & 1)) * kLatent + (lat & ~1);
+                            const int left = rows_here - e - (lane & 1);
+#pragma unroll
+                            for (int y = 0; y < 16; y += 2) {
+                                const float2 f = *reinterpret_cast<const float2 *>(&sm.factor[e + y]);
+                                const __nv_bfloat162 h2 =
+                                    __floats2bfloat162_rn(__uint_as_float(x[z][y]) * f.x, __uint_as_float(x[z][y + 1]) * f.y);
+                                const uint32_t own = *reinterpret_cast<const uint32_t *>(&h2);
+                                const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                                const uint32_t two_lat = (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                                if (y < left) *reinterpret_cast<uint32_t *>(dst + y * kLatent) = two_lat;
+                            }
+                        } else {  // rows past the last are written too (their columns of O^T are nobody's): parts are npad rows
+                            float *dst = p.part_o + (part0 + e) * kLatent + lat;
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) dst[y * kLatent] = __uint_as_float(x[z][y]);
                         }
-                    } else {  // rows past the last are written too (their columns of O^T are nobody's): parts are npad rows
-                        float *dst = p.part_o + (part0 + 16 * e) * kLatent + lat;
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) dst[y * kLatent] = __uint_as_float(x[y]);
                     }
                 }
             }
@@ -1000,12 +926,12 @@ Geom8 geometry8(int32_t H, int32_t m) {
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
     q.form = q.rows <= 32 ? 0 : (q.rows <= 64 ? 1 : 2);
-    const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)(q.form == 0 ? 5 * 64 : (QT1 ? 1 : 5) * 128) * 128;
+    const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)(q.form == 0 ? 5 * 64 : 5 * 128) * 128;
     q.smem = (uint32_t)(1024 + sizeof(Smem8) + of_q + (size_t)q.npad * 256 + (size_t)tiles_in(q.form) * kTile8);
     return q;
 }
 static_assert(1024 + sizeof(Smem8) + 5 * 64 * 128 + 32 * 256 + tiles_in(0) * kTile8 <= kSmem8, "32 rows");
-static_assert(1024 + sizeof(Smem8) + (QT1 ? 1 : 5) * 128 * 128 + 64 * 256 + tiles_in(1) * kTile8 <= kSmem8, "64 rows");
+static_assert(1024 + sizeof(Smem8) + 5 * 128 * 128 + 64 * 256 + tiles_in(1) * kTile8 <= kSmem8, "64 rows");
 static_assert(1024 + sizeof(Smem8) + 11 * kMostRows8 * 128 + tiles_in(2) * kTile8 <= kSmem8, "96 rows");
 static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales, "");
 static_assert(offsetof(Smem8, sc) % 16 == 0 && kTile8 % 1024 == 0, "bulk copies");
@@ -1090,7 +1016,7 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto kernel = a.geo.form == 0 ? kda_mla_decode_fp8_kernel<0> : (a.geo.form == 1 ? kda_mla_decode_fp8_kernel<1> : kda_mla_decode_fp8_kernel<2>);
-    if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(kThreads8), a.geo.smem, st, a) != cudaSuccess ||
+    if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(threads_of(a.geo.form)), a.geo.smem, st, a) != cudaSuccess ||
         join_parts(a, st) != cudaSuccess)
         return KDA_ERR_CUDA;
     return KDA_OK;
