@@ -937,6 +937,9 @@ static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales, "");
 static_assert(offsetof(Smem8, sc) % 16 == 0 && kTile8 % 1024 == 0, "bulk copies");
 static_assert(kMaxSlots + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
+// What a sequence costs beside its tiles, in tiles: its queries are split and its output written
+int32_t extra8(int form) { return form == 0 ? 4 : (form == 1 ? 6 : 8); }
+
 }  // namespace
 }  // namespace kda
 
@@ -975,6 +978,7 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     Args8 a;
     a.geo = geometry8(num_heads, num_tokens);
     a.split = a.geo;
+    a.extra = extra8(a.geo.form);
     const SplitWs w = split_ws(a.geo, kMostRows8);
     a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
     // a cache without pages keeps one page of extent: no id is in range, every load is past it

@@ -661,6 +661,7 @@ int kda_mla_decode(const uint16_t *q_lat, const uint16_t *q_pe, const uint16_t *
     DecodeArgs a;
     a.geo = geometry(num_heads, num_tokens);
     a.split = a.geo;
+    a.extra = 0;
     const SplitWs w = split_ws(a.geo, kWideRows);
     a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
     const uint64_t rows = (uint64_t)num_seqs * a.geo.R;

@@ -1,6 +1,10 @@
 // What the two decode kernels of latent attention (the cache in bf16 and in 8 bits) share: the cached
 // rows of a batch as one list of tiles that is cut into equal runs, the walk over a run, the sums of
 // long stretches, and the join of the sequences that a run's border cuts.
+//
+// Beginning and ending a sequence costs a run time too. In the list a sequence may therefore stand for
+// some units more than its tiles, in front of them (SplitArgs::extra; one at least, the 8-bit form's cost is
+// measured there), so that a run of many short sequences is given fewer tiles.
 #pragma once
 
 #include "kda_common.cuh"
@@ -24,6 +28,7 @@ struct SplitArgs {
     const int32_t *table, *lens;
     int32_t max_pages, num_pages, page_size;
     int32_t N, H, m, G;
+    int32_t extra;    // units that a sequence counts in front of its tiles, where the runs are long enough (extra_of)
     SplitGeom split;
     float scale;      // what a unit of part_ml's maxima is as a natural logarithm
     __nv_bfloat16 *o;
@@ -42,23 +47,26 @@ __device__ __forceinline__ int32_t tiles_of(const SplitArgs &p, int32_t len) {
     return bad_len(p, len) || len == 0 ? 1 : (int32_t)(((int64_t)len + kKvTile - 1) / kKvTile);
 }
 
-// The list's cut into G runs: the first `extra` of them one tile longer than the others.
+// A run of fewer tiles than four per group gains nothing from evening out.
+__device__ __forceinline__ int32_t extra_of(const SplitArgs &p, int64_t tiles) { return tiles >= 4 * (int64_t)p.G ? p.extra : 0; }
+
+// The list's cut into G runs: the first `longer` of them one unit longer than the others.
 struct Runs {
     int64_t each;
-    int32_t extra;
+    int32_t longer;
     __device__ __forceinline__ Runs(int64_t total, int32_t G)
-        : each(total <= INT32_MAX ? (int32_t)total / G : total / G), extra((int32_t)(total - each * G)) {}
-    __device__ __forceinline__ int64_t begin(int32_t g) const { return g * each + min(g, extra); }
-    // the run that holds tile x
+        : each(total <= INT32_MAX ? (int32_t)total / G : total / G), longer((int32_t)(total - each * G)) {}
+    __device__ __forceinline__ int64_t begin(int32_t g) const { return g * each + min(g, longer); }
+    // the run that holds unit x
     __device__ __forceinline__ int32_t of(int64_t x) const {
-        const int64_t longer = extra * (each + 1);
-        return (int32_t)(x < longer ? x / (each + 1) : extra + (x - longer) / each);
+        const int64_t in_longer = longer * (each + 1);
+        return (int32_t)(x < in_longer ? x / (each + 1) : longer + (x - in_longer) / each);
     }
 };
 
 // a run of the list in shared memory: its ends, and where it begins
 struct Run {
-    int32_t first_seq, first_tile, first_len;
+    int32_t first_seq, first_unit, first_len, extra;  // where it begins: a sequence, a unit of it, its length
     int64_t begin, end;
 };
 
@@ -74,6 +82,8 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    const int32_t extra = extra_of(p, total);
+    total += (int64_t)p.N * extra;
     const Runs runs(total, p.G);
     const int64_t begin = runs.begin(g), end = runs.begin(g + 1);
     int64_t before = 0;
@@ -83,15 +93,15 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
     for (int n0 = 0; n0 < p.N; n0 += 32) {
         const int n = n0 + lane;
         const int32_t len = n0 == 0 || n >= p.N ? own : p.lens[n];
-        const int32_t t = n < p.N ? tiles_of(p, len) : 0;
-        int64_t incl = t;
+        const int32_t t = n < p.N ? tiles_of(p, len) : 0, units = n < p.N ? t + extra : 0;
+        int64_t incl = units;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += x;
         }
-        const int64_t lo = before + incl - t;
-        const unsigned mine = __ballot_sync(0xffffffffu, begin >= lo && begin < lo + t);
+        const int64_t lo = before + incl - units;
+        const unsigned mine = __ballot_sync(0xffffffffu, begin >= lo && begin < lo + units);
         if (mine) {
             const int src = __ffs(mine) - 1;
             seq = n0 + src;
@@ -104,15 +114,16 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
     }
     if (lane == 0) {
         run.first_seq = seq;
-        run.first_tile = (int32_t)first;
+        run.first_unit = (int32_t)first;
         run.first_len = first_len;
+        run.extra = extra;
         run.begin = begin;
         run.end = end;
         if (rt == 0) {
             if (g == 0) p.head[0] = total;
             int32_t *e = reinterpret_cast<int32_t *>(p.head + 1) + 4 * g;
             e[0] = seq;
-            e[1] = (int32_t)first;
+            e[1] = max(0, (int32_t)first - extra);
             e[2] = of;
         }
     }
@@ -120,7 +131,7 @@ __device__ __forceinline__ void find_run(const SplitArgs &p, int g, int rt, Run 
 
 // A walk over a run of the list, one stretch of tiles of one sequence after the other.
 struct Walk {
-    int32_t n, j0, j1, tiles, len;
+    int32_t n, unit, j0, j1, tiles, len, extra;
     int64_t left;
     bool work;  // the sequence has cached rows and a sound length
     __device__ __forceinline__ void open(const SplitArgs &p) {
@@ -131,21 +142,24 @@ struct Walk {
     }
     __device__ __forceinline__ void enter(const SplitArgs &p) {
         tiles = tiles_of(p, len);
-        j1 = (int32_t)min((int64_t)tiles, j0 + left);
+        j0 = max(0, unit - extra);
+        j1 = (int32_t)min((int64_t)tiles, unit - extra + left);
         work = len > 0 && !bad_len(p, len);
+        if (j1 <= j0) left = 0;  // the run ends in front of the sequence's first tile
     }
     __device__ __forceinline__ void start(const SplitArgs &p, const Run &run) {
         n = run.first_seq;
-        j0 = run.first_tile;
+        unit = run.first_unit;
+        extra = run.extra;
         left = run.end - run.begin;
         len = run.first_len;
         if (left > 0) enter(p);
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
     __device__ __forceinline__ void next(const SplitArgs &p) {
-        left -= j1 - j0;
+        left -= j1 + extra - unit;
         ++n;
-        j0 = 0;
+        unit = 0;
         if (left > 0) open(p);
     }
     __device__ __forceinline__ void skip_idle(const SplitArgs &p) {
@@ -200,7 +214,7 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
     __shared__ float s_m[kRows][W], s_l[kRows][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t n, tiles, b;  // the sequence, its tiles, the run after the one that holds its first tile
-    int64_t first;        // list index of that tile
+    int64_t first;        // list index of that tile's unit
     int count;            // parts
     if (p.N < p.G) {
         // The lengths are read before the wait: whatever wrote them had finished before the main kernel
@@ -217,8 +231,9 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
             total += __shfl_xor_sync(0xffffffffu, total, off);
             before += __shfl_xor_sync(0xffffffffu, before, off);
         }
-        const Runs runs(total, p.G);
-        first = before;
+        const int32_t extra = extra_of(p, total);
+        const Runs runs(total + (int64_t)p.N * extra, p.G);
+        first = before + (int64_t)(n + 1) * extra;
         tiles = tiles_of(p, __ldcg(p.lens + n));
         b = runs.of(first) + 1;
         count = runs.of(first + tiles - 1) - b + 2;
