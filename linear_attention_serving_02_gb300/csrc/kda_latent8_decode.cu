@@ -37,19 +37,17 @@ namespace {
 constexpr uint32_t kChunk8 = kKvTile * 128;     // 64 rows of 128 bytes: 128 latents, or the positional key
 constexpr int kChunks = 5;                      // of a tile: 512 latents, then the positional key
 constexpr uint32_t kTile8 = kChunks * kChunk8;
-constexpr int kMaxSlots = 5;
+constexpr int kMaxSlots = 4;
 constexpr int kScales = 8;                      // tiles whose scales are kept: more than the ring has, so that a slot is loaded anew only when
                                                 // the softmax is through with its tile
-// The softmax warps of a lane quarter by form: each takes its share of a tile's cached rows, and of O^T's blocks of 128
-// latents. Behind them stand four more: score issue, value issue, TMA, none.
-constexpr int kMostSets = 4;
-constexpr int sets_of(int form) { return 2; }
-constexpr int threads_of(int form) { return 128 * sets_of(form) + 128; }
+// Two softmax warps a lane quarter: each takes half of a tile's cached rows, and of O^T's blocks of 128 latents. Behind them
+// stand four more: score issue, value issue, TMA, none. (Four a quarter: 32 rows 112 -> 142 us, 96 rows 312 -> 324.)
+constexpr int kSets = 2, kSetCols = kKvTile / kSets, kBlocks = kLatent / 128 / kSets;
+constexpr int kSoft = 128 * kSets, kIssue = kSoft / 32, kThreads = kSoft + 128;  // kIssue: the first warp behind them
 // Registers that a block is launched with a thread, and how they are shared out
-constexpr int launched_of(int form) { return sets_of(form) == 2 ? 168 : 96; }
-constexpr int softmax_regs(int form) { return sets_of(form) == 2 ? 208 : 104; }
-constexpr int issue_regs(int form) { return sets_of(form) == 2 ? 80 : 64; }
-constexpr int kMostRows8 = 96;                  // query rows of a CTA
+constexpr int kLaunched = 168, kSoftRegs = 208, kIssueRegs = 80;
+static_assert(kSoft * kSoftRegs + 128 * kIssueRegs <= kThreads * kLaunched, "the shares' sum");
+constexpr int kRows8 = 64, kMostRows8 = 96;     // query rows of a CTA at most: with hi and lo in one product, and at all
 constexpr float kSet = 2.5f, kHigh = 8.75f, kReach = 40.0f;  // powers of two
 constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and what is low
 constexpr int kWindow = 4;                      // tiles over which a row's weights have to be low
@@ -84,7 +82,7 @@ struct Smem8 {
     alignas(16) float sc[kScales][kKvTile];  // scales of a tile's rows (bulk copies land there)
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
-    float part[kMostSets][128], recent[kMostSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
+    float part[kSets][128], recent[kSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
@@ -114,13 +112,8 @@ __device__ __forceinline__ bool peek(uint64_t *mbar, uint32_t parity) {
 __device__ __forceinline__ bool wait_peeked(bool there, uint64_t *mbar, uint32_t parity) {
     return __all_sync(0xffffffffu, there) || tma::wait_warp(mbar, parity);
 }
-// 16 TMEM lanes and 16 or 32 columns as a warp's fragments: x[4 g + 0, 1] are columns 8 g + 2 (lane % 4) + 0, 1 of TMEM
+// 16 TMEM lanes and 32 columns as a warp's fragments: x[4 g + 0, 1] are columns 8 g + 2 (lane % 4) + 0, 1 of TMEM
 // lane lane / 4, x[4 g + 2, 3] the same of TMEM lane 8 + lane / 4. Without the wait
-__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
@@ -128,9 +121,6 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, uint32_t (&r)[
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// whole rows: 16 or 32 columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[16]) { tma::tmem_ld16_nowait(taddr, r); }
-__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[32]) { tc::tmem_ld32_nowait(taddr, r); }
 // two values (a first) as a pair of fp16
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     uint32_t w;
@@ -162,14 +152,14 @@ __device__ __forceinline__ void store2(uint32_t at, int more, uint16_t v) {
 __device__ __forceinline__ void store16(uint32_t at, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
-// The unit 2^a of a query row: its largest latent in (224, 448] of it, unless positional values that dwarf the
-// latents would leave bf16's range. Given the bits of the largest magnitudes as fp32, where NaN is above all.
+// The unit 2^a of a query row: its largest latent in (224, 448] of it, unless positional values that dwarf the latents would
+// then be over 2^61 (times keys in units of 2^-40 they have to stay in fp32's range). Given the bits of the largest magnitudes as fp32, where NaN is above all.
 struct Unit {
     int a;
     float inv;
     bool sound;  // no infinity, no NaN: a row with one has no scores
     __device__ __forceinline__ Unit(uint32_t top, uint32_t top_pe)
-        : a(max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 227), -100)), inv(exp2_of(-min(a, 120))),
+        : a(max(max((int)((top + 0x1FFFFFu) >> 23) - 135, (int)(top_pe >> 23) - 187), -100)), inv(exp2_of(-min(a, 120))),
           sound(max(top, top_pe) < 0x7f800000u) {}
     __device__ __forceinline__ uint32_t positions(uint32_t two) const {  // in the unit
         const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(two << 16) * inv, __uint_as_float(two & 0xffff0000u) * inv);
@@ -187,12 +177,9 @@ __device__ __forceinline__ void split_query(uint32_t two, uint64_t inv2, uint32_
 
 // FORM: query rows of a CTA, as in Geom8
 template <int FORM>
-__global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel(const __grid_constant__ Args8 p) {
+__global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const __grid_constant__ Args8 p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    constexpr int kSets = sets_of(FORM), kSetCols = kKvTile / kSets, kBlocks = kLatent / 128 / kSets;
-    constexpr int kSoft = 128 * kSets, kIssue = kSoft / 32;  // softmax threads; the first warp behind them
-    static_assert(kSoft * softmax_regs(FORM) + 128 * issue_regs(FORM) <= threads_of(FORM) * launched_of(FORM), "the shares' sum");
     constexpr int MS = FORM == 0 ? 64 : 128;   // M of the score product
     constexpr bool kStack = FORM < 2;          // hi and lo rows in one product
     constexpr int kRowsQ = kStack ? MS / 8 : 32;   // query rows of a lane quarter (and, stacked, where lo lies behind hi)
@@ -243,7 +230,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
     bool ok = true;
 
     if (warp >= kIssue) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(issue_regs(FORM)));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
         if (warp == kIssue + 2) {
             // ---- TMA producer: one thread ----
             if (tma::elect()) {
@@ -442,7 +429,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(softmax_regs(FORM)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
         // ---- softmax: a thread takes kC cached rows of a tile for each of kR query rows; then the output ----
         const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -472,58 +459,58 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
             limit[y] = owner[y] ? kMost : INFINITY;
         }
         // the largest weight of a row's last window
-        auto window = [&](int row) {
-            float x = sm.recent[0][row];
-#pragma unroll
-            for (int i = 1; i < kSets; ++i) x = fmaxf(x, sm.recent[i][row]);
-            return x;
-        };
+        auto window = [&](int row) { return fmaxf(sm.recent[0][row], sm.recent[1][row]); };
         int k = 0, seg = 0;  // tiles and stretches worked on
         // the products of tile t are through: waited for in every tile for the one before the last, so that none is passed over
         auto through = [&](int t) { return tma::wait_warp(&sm.done[t % kTiles], (t / kTiles) & 1); };
         // Q of a stretch, a row a warp at a time; the last stretch's score products are through: its last tile was taken
-        auto load_q = [&](const Walk &s) {
-            const int64_t row0 = (int64_t)s.n * geo.R + row_first;
-            // the loads of kBatch rows are on their way before the first is looked at
-            constexpr int kBatch = (FORM == 0 ? 4 : 6) * 2 / kSets;
+        auto load_q = [&](int n) {
+            const int64_t row0 = (int64_t)n * geo.R + row_first;
+            // The loads of kBatch rows are on their way before the first is looked at. (A few rows at a time: this runs once a
+            // sequence, and long code that seldom runs is fetched anew each time.)
+            constexpr int kBatch = FORM == 0 ? 2 : 4;
+#pragma unroll 1
             for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
-                uint4 va[kBatch], vb[kBatch];
-                uint32_t vp[kBatch];
+                struct {
+                    uint4 a, b;
+                    uint32_t pe;
+                } now[kBatch];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     const int64_t row = row0 + min(q0 + kIssue * b, rows_here - 1);
                     const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * kLatent) + 2 * lane;
-                    va[b] = src[0], vb[b] = src[1];
-                    vp[b] = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
+                    now[b].a = src[0], now[b].b = src[1];
+                    now[b].pe = reinterpret_cast<const uint32_t *>(p.q_pe + row * kPos)[lane];
                 }
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     const int q = min(q0 + kIssue * b, rows_here - 1);  // (the last row again: the same values)
-                    const uint32_t v[8] = {va[b].x, va[b].y, va[b].z, va[b].w, vb[b].x, vb[b].y, vb[b].z, vb[b].w}, pe = vp[b];
+                    const uint32_t v[8] = {now[b].a.x, now[b].a.y, now[b].a.z, now[b].a.w, now[b].b.x, now[b].b.y, now[b].b.z, now[b].b.w};
                     // bits of the largest magnitudes, as bf16 and then as fp32; NaN is above all
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) top = __vmaxu2(top, v[i] & 0x7fff7fffu);
                     top = __reduce_max_sync(0xffffffffu, max(top << 16, top & 0xffff0000u));
-                    const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((pe << 16) & 0x7fffffffu, pe & 0x7fff0000u));
+                    const uint32_t top_pe = __reduce_max_sync(0xffffffffu, max((now[b].pe << 16) & 0x7fffffffu, now[b].pe & 0x7fff0000u));
                     const Unit unit(top, top_pe);
                     const uint64_t inv2 = pk2(unit.inv, unit.inv);
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t h, l;
-                        split_query(v[i], inv2, h, l);
-                        hi[i >> 1] = i & 1 ? hi[i >> 1] | (h << 16) : h;
-                        lo[i >> 1] = i & 1 ? lo[i >> 1] | (l << 16) : l;
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h[2], l[2];
+                        split_query(v[2 * i], inv2, h[0], l[0]);
+                        split_query(v[2 * i + 1], inv2, h[1], l[1]);
+                        hi[i] = h[0] | (h[1] << 16);
+                        lo[i] = l[0] | (l[1] << 16);
                     }
-                                            // rows of the operand: hi and lo of a quarter one behind the other, or the row itself in chunks of its own
+                    // rows of the operand: hi and lo of a quarter one behind the other, or the row itself in chunks of its own
                     const int m_hi = kStack ? (q / kRowsQ) * 2 * kRowsQ + q % kRowsQ : q, m_lo = kStack ? m_hi + kRowsQ : q;
                     uint8_t *at = s_q + (lane >> 3) * q_chunk;
                     *reinterpret_cast<uint4 *>(at + m_hi * 128 + (((lane & 7) ^ (m_hi & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     at += kStack ? 0 : 4 * q_chunk;
                     *reinterpret_cast<uint4 *>(at + m_lo * 128 + (((lane & 7) ^ (m_lo & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     at = s_q + (q_chunks - 1) * q_chunk + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = unit.positions(pe);
+                    *reinterpret_cast<uint32_t *>(at + m_hi * 128 + (((lane >> 2) ^ (m_hi & 7)) << 4)) = unit.positions(now[b].pe);
                     if (kStack) *reinterpret_cast<uint32_t *>(at + m_lo * 128 + (((lane >> 2) ^ (m_lo & 7)) << 4)) = 0;
                     if (lane == 0) sm.row_c[q] = unit.factor(p.c);
                 }
@@ -537,7 +524,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
         {
             Walk first = w;
             first.skip_idle(p);
-            if (!first.done()) load_q(first);
+            if (!first.done()) load_q(first.n);
             named_sync(2, kSoft);
         }
         for (; !w.done() && ok; w.next(p)) {
@@ -554,6 +541,11 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
                 float c[kR];
 #pragma unroll
                 for (int y = 0; y < kR; ++y) c[y] = owner[y] ? sm.row_c[r[y]] : 0.f;
+                // the next sequence with rows
+                Walk after = w;
+                after.next(p);
+                after.skip_idle(p);
+                const int next_n = after.done() ? -1 : after.n;
                 bool stopped = false;
                 for (int js = w.j0; !stopped; js += kFold) {
                     if (js > w.j0 && w.j1 - w.j0 > kFold) {
@@ -599,7 +591,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
                         auto scores = [&] {
                             if constexpr (FORM == 2) {
                                 uint32_t x[kC];
-                                tmem_ld_row(s_at, x);
+                                tc::tmem_ld32_nowait(s_at, x);
                                 tc::tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < kC / 2; ++e) x2[0][e] = pk2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
@@ -711,8 +703,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
                             again = false;
 #pragma unroll
                             for (int y = 0; y < kR; ++y) {
-#pragma unroll
-                                for (int i = 0; i < kSets; ++i) top[y] = fmaxf(top[y], sm.part[i][r[y]]);
+                                top[y] = fmaxf(sm.part[0][r[y]], sm.part[1][r[y]]);
                                 m_top[y] = fmaxf(m_top[y], top[y]);
                                 const bool up = first || top[y] - m_ref[y] > kHigh;
                                 // of low weights, the window's largest, which is still in sm.recent
@@ -812,11 +803,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
                     }
                 }
                 // the next stretch's queries before this one's output, so that its scores start meanwhile
-                Walk after = w;
-                after.next(p);
-                after.skip_idle(p);
                 if (softmax_any<kSoft>(!ok)) ok = false;
-                if (ok && !after.done()) load_q(after);
+                if (ok && next_n >= 0) load_q(next_n);
                 if (ok) ok = through(k - 1);
                 tc::fence_after_sync();
             }
@@ -830,11 +818,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
             }
             if (softmax_any<kSoft>(!ok)) ok = false;
 #pragma unroll
-            for (int y = 0; y < kR; ++y) {
-                l[y] = sm.part[0][r[y]];
-#pragma unroll
-                for (int i = 1; i < kSets; ++i) l[y] += sm.part[i][r[y]];
-            }
+            for (int y = 0; y < kR; ++y) l[y] = sm.part[0][r[y]] + sm.part[1][r[y]];
             // ---- this stretch's part of the sequence: finished, or left for the join ----
             const bool whole = w.j0 == 0 && w.j1 == w.tiles;
             const bool bad = !ok || bad_len(p, w.len) || (w.work && *(volatile int32_t *)&sm.bad[seg % kBad] != 0);
@@ -919,13 +903,20 @@ __global__ void __launch_bounds__(threads_of(FORM), 1) kda_mla_decode_fp8_kernel
 
 constexpr size_t kSmem8 = 232448;
 
+// Row tiles of equal size, as few as 96 rows each allow, or as few as 64 allow, where these are not more than a third
+// more. With tiles of up to 96 and up to 64 rows 64 sequences of up to 8000 rows take 82 and 93 us (96
+// rows, 1 and 2 tiles), 131 and 139 (192, 2 and 3), 171 and 169 (200, 3 and 4), 184 and 171 (256, 3 and 4), 189 and 210
+// (288, 3 and 5), 216 and 210 (320, 4 and 5), 231 and 248 (384, 4 and 6), 320 and 308 (512, 6 and 8), 426 and 479 (768, 8
+// and 12).
 Geom8 geometry8(int32_t H, int32_t m) {
     Geom8 q{};
     q.R = H * m;
     q.RT = (q.R + kMostRows8 - 1) / kMostRows8;
+    const int32_t narrow = (q.R + kRows8 - 1) / kRows8;
+    if (3 * (int64_t)narrow <= 4 * (int64_t)q.RT) q.RT = narrow;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
-    q.form = q.rows <= 32 ? 0 : (q.rows <= 64 ? 1 : 2);
+    q.form = q.rows <= 32 ? 0 : (q.rows <= kRows8 ? 1 : 2);
     const size_t of_q = q.form == 2 ? (size_t)9 * q.rows * 128 : (size_t)(q.form == 0 ? 5 * 64 : 5 * 128) * 128;
     q.smem = (uint32_t)(1024 + sizeof(Smem8) + of_q + (size_t)q.npad * 256 + (size_t)tiles_in(q.form) * kTile8);
     return q;
@@ -937,7 +928,9 @@ static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales, "");
 static_assert(offsetof(Smem8, sc) % 16 == 0 && kTile8 % 1024 == 0, "bulk copies");
 static_assert(kMaxSlots + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
-// What a sequence costs beside its tiles, in tiles: its queries are split and its output written
+// What a sequence costs beside its tiles, in tiles: its queries are split and its output written. (With 0, 0, 0 / 3, 4, 6
+// / 4, 6, 8 units: 32 sequences x 16 heads 31.5 / 26.2 / 26.2 us, 64 x 48 71 / 61.4 / 61.3, 64 x 96, four tokens 243 /
+// 226.5 / 226, 256 x 96 303 / 256 / 255.)
 int32_t extra8(int form) { return form == 0 ? 4 : (form == 1 ? 6 : 8); }
 
 }  // namespace
@@ -1020,7 +1013,7 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto kernel = a.geo.form == 0 ? kda_mla_decode_fp8_kernel<0> : (a.geo.form == 1 ? kda_mla_decode_fp8_kernel<1> : kda_mla_decode_fp8_kernel<2>);
-    if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(threads_of(a.geo.form)), a.geo.smem, st, a) != cudaSuccess ||
+    if (launch_after(kernel, dim3((unsigned)(a.G * a.geo.RT)), dim3(kThreads), a.geo.smem, st, a) != cudaSuccess ||
         join_parts(a, st) != cudaSuccess)
         return KDA_ERR_CUDA;
     return KDA_OK;
