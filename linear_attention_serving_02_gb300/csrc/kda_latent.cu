@@ -1,20 +1,24 @@
-// The rows of the latent cache: kda_mla_append writes them, kda_mla_gather reads them back.
+// The rows of the latent cache: kda_mla_append writes them, kda_mla_gather reads them back; the _fp8 calls are the same
+// for the cache in 8 bits.
 //
 // append: row = ( c / sqrt(mean(c^2) + eps) * w , R(pos) k_pe ), q_out = R(pos) q_pe, in fp32
-// and rounded once. gather: a copy. Both are bound by their bytes: a token's row is read
-// once and written once (2304 B), a query head's 64 values too (256 B).
+// and rounded once; in 8 bits the row is divided by its scale before, the least power of two 2^e with
+// max|latent| 2^-e <= 448, which moves no bit of the bf16 part. gather: a copy, or the values times their scale. All
+// are bound by their bytes: a token's row is read once and written once (2304 B, in 8 bits 1796 B), a query
+// head's 64 values too (256 B).
 //
 // A warp takes a token's row and its first 16 query heads; further heads go 16 to a warp. A
-// lane holds 16 latent values in two 16-byte accesses, so the sum of squares is one warp
-// reduction and nothing passes through shared memory; four lanes rotate one head, eight pairs a
+// lane holds 16 latent values in two 16-byte accesses, so the sum of squares and the largest magnitude are one warp
+// reduction each and nothing passes through shared memory; four lanes rotate one head, eight pairs a
 // lane in two 16-byte accesses. All of a warp's loads are issued before it looks up where the
-// token goes. gather gives a warp four rows, nine 16-byte accesses a lane, all in flight at once.
-// Warps are blocks of their own: with 256 threads a block waits for its slowest token and frees
-// its registers late (65536 tokens x 12 heads 64.7 us, 59.3 us with 32).
+// token goes; the queries, which then wait for nothing more, are through before the row, so that fewer values live
+// at once (65536 tokens x 12 heads in 8 bits: 61.0 us, 59.7 so). gather gives a warp four rows, nine 16-byte
+// accesses a lane, all in flight at once. Blocks are one or two warps: a larger one waits for its slowest token and
+// frees its registers late (append in 8 bits with 1, 2 and 4 warps 59.7, 57.0 and 58.6 us).
 //
-// Measured: append of 65536 tokens x 12 heads 59 us (6.3 TB/s), of 256 tokens x 96 heads 3.4 us
-// (a launch and three dependent loads); gather of 108000 rows 40.6 us (6.2 TB/s), of
-// 330 rows 3.3 us (eight rows a warp: 43.7 and 6.0 us).
+// Measured: append of 65536 tokens x 12 heads 56.4 us (6.2 TB/s), in 8 bits 56.7 (5.6 TB/s: fewer bytes, the same
+// chain of a token's loads), of 256 tokens x 96 heads 3.0 us (a launch and three dependent loads); gather of 108000 rows
+// 40.6 us (6.2 TB/s), in 8 bits 32.9 (5.9 TB/s), of 330 rows 3.3 us (eight rows a warp: 43.7 and 6.0 us).
 
 #include "kda_common.cuh"
 #include "kda_latent_common.cuh"
@@ -22,7 +26,7 @@
 namespace kda {
 namespace {
 
-constexpr int kRowThreads = 32;
+constexpr int kRowThreads = 32, kAppendThreads = 64, kGather8Threads = 64;
 constexpr int kHeadsPerItem = 16;
 constexpr int kGatherRows = 4;
 constexpr int kRowUnits = kRow * 2 / 16;  // 16-byte units of a row: 72
@@ -122,10 +126,10 @@ __device__ __forceinline__ void load8(float (&x)[8], const float *p) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __grid_constant__ AppendArgs<T> p) {
+__global__ void __launch_bounds__(kAppendThreads) kda_mla_append_kernel(const __grid_constant__ AppendArgs<T> p) {
     constexpr bool kBits8 = sizeof(T) == 1;
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int part = blockIdx.y;
     pdl_wait();
     if (t >= p.tokens) return;
@@ -174,6 +178,13 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
             if (lane == 0) set_status(p.status, KDA_ERR_PAGES);
         }
     }
+
+    const uint4 nan4 = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+#pragma unroll
+    for (int i = 0; i < kHeadsPerItem / 8; ++i)
+        if (h0 + 8 * i < p.H)
+            store_pos(p.q_out + t * p.qo_ts + (h0 + 8 * i) * p.qo_hs, j, il,
+                      good ? rotate(q[i], co, si, il) : PosPiece{nan4, nan4});
 
     if (part == 0 && good) {
         T *page_at = p.cache.rows + page * p.cache.page_stride;
@@ -230,12 +241,6 @@ __global__ void __launch_bounds__(kRowThreads) kda_mla_append_kernel(const __gri
             if (lane < 4) store_pos(row + kLatent, j, il, p.rope ? rotate(k_pe, co, si, il) : k_pe);
         }
     }
-    const uint4 nan4 = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-#pragma unroll
-    for (int i = 0; i < kHeadsPerItem / 8; ++i)
-        if (h0 + 8 * i < p.H)
-            store_pos(p.q_out + t * p.qo_ts + (h0 + 8 * i) * p.qo_hs, j, il,
-                      good ? rotate(q[i], co, si, il) : PosPiece{nan4, nan4});
 }
 
 __global__ void __launch_bounds__(kRowThreads)
@@ -288,11 +293,11 @@ __device__ __forceinline__ uint2 bf16_of4(uint32_t v, float s) {
     return make_uint2(pack2(a.x * s, a.y * s), pack2(b.x * s, b.y * s));
 }
 
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kGather8Threads)
     kda_mla_gather_fp8_kernel(const PagedRows<const uint8_t> cache, const int32_t *cu, const int32_t *starts, int32_t N,
                               int64_t T, __nv_bfloat16 *out, int32_t *status) {
     const int lane = threadIdx.x & 31;
-    const int64_t t0 = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kGatherRows;
+    const int64_t t0 = ((int64_t)blockIdx.x * (kGather8Threads / 32) + (threadIdx.x >> 5)) * kGatherRows;
     pdl_wait();
     if (t0 >= T) return;
     const uint8_t *src[kGatherRows];
@@ -320,16 +325,18 @@ __global__ void __launch_bounds__(kRowThreads)
         src[r] = at + (int64_t)in_page * kRow8;
         scale_at[r] = reinterpret_cast<const float *>(at + (int64_t)cache.page_size * kRow8) + in_page;
     }
-    // a row's latents are 32 units of 16 bytes, its positional key eight: lane l takes latent unit l of every
-    // row and unit l % 8 of row l / 8's positional key
-    uint4 v[kGatherRows], pe = make_uint4(0, 0, 0, 0);
+    // lane l takes bytes 8 l and 256 + 8 l of every row's latents, so that a store is 512 bytes in one piece (16 bytes read and 32
+    // written a lane: 108000 rows 35.7 us, 33.8 so, 33.0 with two warps a block), and unit l % 8 of 16 bytes of row l / 8's positional key
+    uint2 v[kGatherRows][2];
+    uint4 pe = make_uint4(0, 0, 0, 0);
     float s[kGatherRows];
 #pragma unroll
     for (int r = 0; r < kGatherRows; ++r) {
-        v[r] = make_uint4(0, 0, 0, 0);
+        v[r][0] = v[r][1] = make_uint2(0, 0);
         s[r] = ((nan_rows >> r) & 1) ? __uint_as_float(0x7fffffffu) : 1.f;
         if (src[r]) {
-            v[r] = *reinterpret_cast<const uint4 *>(src[r] + 16 * lane);
+            v[r][0] = *reinterpret_cast<const uint2 *>(src[r] + 8 * lane);
+            v[r][1] = *reinterpret_cast<const uint2 *>(src[r] + 256 + 8 * lane);
             s[r] = *scale_at[r];
         }
     }
@@ -339,10 +346,11 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int r = 0; r < kGatherRows; ++r) {
         if (!src[r] && !((nan_rows >> r) & 1)) continue;
-        const uint2 a = bf16_of4(v[r].x, s[r]), b = bf16_of4(v[r].y, s[r]), c = bf16_of4(v[r].z, s[r]), d = bf16_of4(v[r].w, s[r]);
-        uint4 *dst = reinterpret_cast<uint4 *>(out + (t0 + r) * kRow) + 2 * lane;
-        dst[0] = make_uint4(a.x, a.y, b.x, b.y);
-        dst[1] = make_uint4(c.x, c.y, d.x, d.y);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint2 a = bf16_of4(v[r][i].x, s[r]), b = bf16_of4(v[r][i].y, s[r]);
+            reinterpret_cast<uint4 *>(out + (t0 + r) * kRow + 256 * i)[lane] = make_uint4(a.x, a.y, b.x, b.y);
+        }
     }
     if (ps || ((nan_rows >> pr) & 1)) {
         const float sp = pr == 0 ? s[0] : (pr == 1 ? s[1] : (pr == 2 ? s[2] : s[3]));
@@ -409,9 +417,9 @@ int append_call(const uint16_t *c, int64_t c_stride, const uint16_t *k_pe, int64
     a.N = num_seqs;
     a.per_seq = cu_seqlens ? 0 : total_tokens / num_seqs;
     a.status = status;
-    const int64_t blocks = (total_tokens + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    const int64_t blocks = (total_tokens + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     const int parts = a.H > kHeadsPerItem ? (a.H + kHeadsPerItem - 1) / kHeadsPerItem : 1;
-    return launch_after(kda_mla_append_kernel<T>, dim3((unsigned)blocks, (unsigned)parts), dim3(kRowThreads), 0,
+    return launch_after(kda_mla_append_kernel<T>, dim3((unsigned)blocks, (unsigned)parts), dim3(kAppendThreads), 0,
                         static_cast<cudaStream_t>(stream), a) == cudaSuccess
                ? KDA_OK
                : KDA_ERR_CUDA;
@@ -482,10 +490,10 @@ int kda_mla_gather_fp8(const uint8_t *cache, int64_t page_stride, int32_t num_pa
     if (!mla_aligned(cache, 16) || !mla_aligned(out, 16) || !mla_aligned(cu_seqlens, 4) || !mla_aligned(starts, 4) ||
         !mla_aligned(page_table, 4) || !mla_aligned(status, 4))
         return KDA_ERR_ALIGN;
-    const int64_t per_block = kGatherRows * (kRowThreads / 32);
+    const int64_t per_block = kGatherRows * (kGather8Threads / 32);
     const unsigned blocks = (unsigned)((total_rows + per_block - 1) / per_block);
     const PagedRows<const uint8_t> pr{cache, page_stride, num_pages, page_size, page_table, max_pages};
-    return launch_after(kda_mla_gather_fp8_kernel, dim3(blocks), dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), pr,
+    return launch_after(kda_mla_gather_fp8_kernel, dim3(blocks), dim3(kGather8Threads), 0, static_cast<cudaStream_t>(stream), pr,
                         cu_seqlens, starts, num_seqs, total_rows, reinterpret_cast<__nv_bfloat16 *>(out), status) == cudaSuccess
                ? KDA_OK
                : KDA_ERR_CUDA;
