@@ -908,12 +908,20 @@ constexpr size_t kSmem8 = 232448;
 // rows, 1 and 2 tiles), 131 and 139 (192, 2 and 3), 171 and 169 (200, 3 and 4), 184 and 171 (256, 3 and 4), 189 and 210
 // (288, 3 and 5), 216 and 210 (320, 4 and 5), 231 and 248 (384, 4 and 6), 320 and 308 (512, 6 and 8), 426 and 479 (768, 8
 // and 12).
-Geom8 geometry8(int32_t H, int32_t m) {
+// Where the tables hold so little (`most` tiles) that every tile is a block's only one, tiles of 32 or 64 rows: a block then has
+// fewer queries to split. 2 x 12 x 8 over 700 rows 16.0 us with one row tile, 11.3 with three; 1 x 96 over 500 and 3000 15.3
+// and 19.9, 10.3 and 16.3 (three and two); 1 x 64 x 16 over 130 20.0, 15.0 (11 and 32).
+Geom8 geometry8(int32_t H, int32_t m, int64_t most, int32_t sms) {
     Geom8 q{};
     q.R = H * m;
     q.RT = (q.R + kMostRows8 - 1) / kMostRows8;
     const int32_t narrow = (q.R + kRows8 - 1) / kRows8;
     if (3 * (int64_t)narrow <= 4 * (int64_t)q.RT) q.RT = narrow;
+    const int32_t least = (q.R + 31) / 32;
+    if (most * least <= sms)
+        q.RT = least;
+    else if (most * narrow <= sms)
+        q.RT = narrow;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
     q.form = q.rows <= 32 ? 0 : (q.rows <= kRows8 ? 1 : 2);
@@ -941,7 +949,7 @@ extern "C" {
 size_t kda_mla_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens) {
     if (num_seqs < 0 || num_heads < 0 || num_tokens < 0) return 0;
     if ((int64_t)num_heads * num_tokens > INT32_MAX / 2 || num_heads == 0 || num_tokens == 0) return 256;
-    return kda::split_ws(kda::geometry8(num_heads, num_tokens), kda::kMostRows8).total;
+    return kda::split_ws(kda::geometry8(num_heads, num_tokens, INT32_MAX, 0), kda::kMostRows8).total;
 }
 
 int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_t *cache, int64_t page_stride,
@@ -969,7 +977,9 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     if (device >= 64) return KDA_ERR_DEVICE;
 
     Args8 a;
-    a.geo = geometry8(num_heads, num_tokens);
+    // the longest page tables' tiles; no more groups than these
+    const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
+    a.geo = geometry8(num_heads, num_tokens, most, sms);
     a.split = a.geo;
     a.extra = extra8(a.geo.form);
     const SplitWs w = split_ws(a.geo, kMostRows8);
@@ -1007,8 +1017,6 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
                 return KDA_ERR_CUDA;
         configured[device].store(true, std::memory_order_release);
     }
-    // no more groups than the longest page tables could give tiles to
-    const int64_t most = (int64_t)num_seqs * (((int64_t)max_pages * page_size + kKvTile - 1) / kKvTile + 1);
     a.G = groups_of(a.geo.RT, sms < kMaxGroups ? sms : kMaxGroups);
     if (a.G > most) a.G = (int32_t)most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

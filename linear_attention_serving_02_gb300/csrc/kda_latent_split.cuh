@@ -201,7 +201,7 @@ __device__ __forceinline__ void fold_o(float *kept, uint32_t o_addr, int npad, c
 // belongs to sequence x, whose place in the list it adds up itself; with more it belongs to
 // the border before group x + 1, where the main kernel left the place, and the first border
 // inside a sequence joins it. W warps share a row's parts, each lane 16 / Z of the 512 latents, Z
-// blocks a row (1M x 12: 195 us with one, 192 with four); the parts are added in list order within a
+// blocks a row; the parts are added in list order within a
 // warp and the warps' sums in warp order, so the result does not depend on timing. With W = 1 the
 // way through shared memory is not needed, but the 32 KB keep these blocks off the SMs until
 // the main kernel's are through: without them they wait beside it, and 256 x 96 takes 2% longer.
@@ -367,11 +367,18 @@ cudaError_t launch_join(const SplitArgs &a, cudaStream_t st) {
 // the join behind the main kernel
 cudaError_t join_parts(const SplitArgs &a, cudaStream_t st) {
     if (a.G <= 1) return cudaSuccess;
-    // a split sequence has about G / N parts: many are shared by a block's 16 warps, a few by four, and
-    // two or three are one warp's. With 1, 4 and 16 warps a row: 1M x 12 236, 200 and 193 us; 8 sequences
-    // of 30000 rows x 12 heads 50, 36 and 34; 32 of 8000 x 16 42, 37 and 41; 256 of 8000 x 96 293, 347, 440
-    const int64_t n = a.N;
-    return n * 16 <= a.G ? launch_join<16, 4>(a, st) : (n * 4 <= a.G ? launch_join<4, 2>(a, st) : launch_join<1, 1>(a, st));
+    // As many warps a row, and blocks a row, as leave about 256 blocks of 16 warps: with fewer a warp goes through its parts
+    // too long, with more the blocks come in waves. In 8 bits, with 1 x 1, 2 x 2, 4 x 2, 8 x 2, 16 x 2 and 16 x 4 warps x
+    // blocks a row: 12 rows of 152 parts (100000 cached rows) -, 49.9, 37.4, 28.9, 25.4 and 24.1 us; 96 of 152 -, 75.2, 54.8,
+    // 47.0, 43.6 and 46.7; 192 of 12 (2 x 12 x 8) 14.6, 11.6, 11.4, 11.4, 13.6 and 18.0; 768 of 19 33.7, 25.9, 26.2, 28.1,
+    // 36.3 and 52.3; 1024 of 9 31.3, 25.9, 28.4, 32.6, 44.4 and 65.9; 2048 of 6 35.6, 37.0, 40.8, 51.3, 74.6 and 115.6.
+    const int64_t rows = (int64_t)(a.N < a.G ? a.N : a.G - 1) * a.split.R;
+    if (rows <= 64) return launch_join<16, 4>(a, st);
+    if (rows <= 128) return launch_join<16, 2>(a, st);
+    if (rows <= 256) return launch_join<8, 2>(a, st);
+    if (rows <= 512) return launch_join<4, 2>(a, st);
+    if (rows <= 1024) return launch_join<2, 2>(a, st);
+    return launch_join<1, 1>(a, st);
 }
 
 }  // namespace
