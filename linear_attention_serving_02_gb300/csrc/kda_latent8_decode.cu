@@ -908,9 +908,11 @@ constexpr size_t kSmem8 = 232448;
 // rows, 1 and 2 tiles), 131 and 139 (192, 2 and 3), 171 and 169 (200, 3 and 4), 184 and 171 (256, 3 and 4), 189 and 210
 // (288, 3 and 5), 216 and 210 (320, 4 and 5), 231 and 248 (384, 4 and 6), 320 and 308 (512, 6 and 8), 426 and 479 (768, 8
 // and 12).
-// Where the tables hold so little (`most` tiles) that every tile is a block's only one, tiles of 32 or 64 rows: a block then has
-// fewer queries to split. 2 x 12 x 8 over 700 rows 16.0 us with one row tile, 11.3 with three; 1 x 96 over 500 and 3000 15.3
-// and 19.9, 10.3 and 16.3 (three and two); 1 x 64 x 16 over 130 20.0, 15.0 (11 and 32).
+// Where the tables hold so little (`most` tiles) that a block has no more than 24 tiles of 32 rows, or 16 of 64, row tiles of
+// these: a block then has fewer queries to split and less to write, which counts for more than reading the tiles more
+// often. With up to 96, 64 and 32 rows: 96 heads over 500 rows 15.3, - and 10.3 us, 12000 23.9, 18.0 and 16.4, 50000 33.1, 30.3
+// and 28.2 (16 tiles), 80000 39.5, 37.4 and 36.6, 120000 47.2, 48.1 and 48.7; 96 x 4 over 20000 35.7, 33.3 (12 tiles) and
+// 36.5; 20 x 96 over 3000 38.0, 35.9 and 34.7. (With fewer than three groups of so many tiles too many SMs would have none.)
 Geom8 geometry8(int32_t H, int32_t m, int64_t most, int32_t sms) {
     Geom8 q{};
     q.R = H * m;
@@ -918,9 +920,9 @@ Geom8 geometry8(int32_t H, int32_t m, int64_t most, int32_t sms) {
     const int32_t narrow = (q.R + kRows8 - 1) / kRows8;
     if (3 * (int64_t)narrow <= 4 * (int64_t)q.RT) q.RT = narrow;
     const int32_t least = (q.R + 31) / 32;
-    if (most * least <= sms)
+    if (least <= sms / 3 && most * least <= 24 * sms)
         q.RT = least;
-    else if (most * narrow <= sms)
+    else if (narrow <= sms / 3 && most * narrow <= 16 * sms)
         q.RT = narrow;
     q.rows = ((q.R + q.RT - 1) / q.RT + 7) / 8 * 8;
     q.npad = (q.rows + 15) / 16 * 16;
