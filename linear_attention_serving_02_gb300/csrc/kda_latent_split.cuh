@@ -202,16 +202,15 @@ __device__ __forceinline__ void fold_o(float *kept, uint32_t o_addr, int npad, c
 // the border before group x + 1, where the main kernel left the place, and the first border
 // inside a sequence joins it. W warps share a row's parts, each lane 16 / Z of the 512 latents, Z
 // blocks a row; the parts are added in list order within a
-// warp and the warps' sums in warp order, so the result does not depend on timing. With W = 1 the
-// way through shared memory is not needed, but the 32 KB keep these blocks off the SMs until
-// the main kernel's are through: without them they wait beside it, and 256 x 96 takes 2% longer.
-constexpr int kJoinThreads = 512;
+// warp and the warps' sums in warp order, so the result does not depend on timing. With W = 1 no
+// shared memory is needed, but 32 KB asked for keep these blocks off the SMs until the main kernel's
+// are through: without them they wait beside it, and 256 x 96 takes 2% longer.
+// (256 threads: 64 x 96 x 4 in 8 bits 226.9 us, with 512 228.4.)
+constexpr int join_threads(int W) { return W == 1 ? 256 : 512; }
 template <int W, int Z>
-__global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid_constant__ SplitArgs p) {
-    constexpr int kRows = kJoinThreads / 32 / W;  // rows of a block
+__global__ void __launch_bounds__(join_threads(W)) kda_mla_join_kernel(const __grid_constant__ SplitArgs p) {
+    constexpr int kRows = join_threads(W) / 32 / W;  // rows of a block
     constexpr int kLat = kLatent / Z, kVec = kLat / 128;  // its latents, and float4 of a lane
-    __shared__ float s_o[kRows][W][kLat];
-    __shared__ float s_m[kRows][W], s_l[kRows][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t n, tiles, b;  // the sequence, its tiles, the run after the one that holds its first tile
     int64_t first;        // list index of that tile's unit
@@ -308,32 +307,47 @@ __global__ void __launch_bounds__(kJoinThreads) kda_mla_join_kernel(const __grid
             }
         }
     }
-#pragma unroll
-    for (int v = 0; v < kVec; ++v)
-        *reinterpret_cast<float4 *>(&s_o[rl][part][4 * (32 * v + lane)]) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-    if (lane == 0) s_m[rl][part] = m, s_l[rl][part] = l;
-    __syncthreads();
-    if (!live) return;
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[rl][i]);
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float f[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        f[i] = tc::ex2((s_m[rl][i] - Ms) * c);
-        L += f[i] * s_l[rl][i];
-    }
-    const float inv = L == 0.f ? 0.f : 1.0f / L;
     const int64_t row = (int64_t)n * p.split.R + rr;
-    if (part == 0 && lane == 0 && blockIdx.z == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M * p.scale + logf(L);
-    for (int x = 2 * (part * 32 + lane); x < kLat; x += 2 * 32 * W) {
-        float a = 0.f, bb = 0.f;
+    if constexpr (W == 1) {
+        if (!live) return;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        if (lane == 0 && blockIdx.z == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(o[4 * v] * inv, o[4 * v + 1] * inv),
+                                 bb = __floats2bfloat162_rn(o[4 * v + 2] * inv, o[4 * v + 3] * inv);
+            *reinterpret_cast<uint2 *>(p.o + row * kLatent + lat0 + 4 * (32 * v + lane)) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&bb));
+        }
+    } else {
+        __shared__ float s_o[kRows][W][kLat];
+        __shared__ float s_m[kRows][W], s_l[kRows][W];
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+            *reinterpret_cast<float4 *>(&s_o[rl][part][4 * (32 * v + lane)]) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        if (lane == 0) s_m[rl][part] = m, s_l[rl][part] = l;
+        __syncthreads();
+        if (!live) return;
+        float M = -INFINITY, L = 0.f;
+        for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[rl][i]);
+        const float Ms = M == -INFINITY ? 0.f : M;
+        float f[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            a += f[i] * s_o[rl][i][x];
-            bb += f[i] * s_o[rl][i][x + 1];
+            f[i] = tc::ex2((s_m[rl][i] - Ms) * c);
+            L += f[i] * s_l[rl][i];
         }
-        *reinterpret_cast<__nv_bfloat162 *>(p.o + row * kLatent + lat0 + x) = __floats2bfloat162_rn(a * inv, bb * inv);
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+        if (part == 0 && lane == 0 && blockIdx.z == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M * p.scale + logf(L);
+        for (int x = 2 * (part * 32 + lane); x < kLat; x += 2 * 32 * W) {
+            float a = 0.f, bb = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                a += f[i] * s_o[rl][i][x];
+                bb += f[i] * s_o[rl][i][x + 1];
+            }
+            *reinterpret_cast<__nv_bfloat162 *>(p.o + row * kLatent + lat0 + x) = __floats2bfloat162_rn(a * inv, bb * inv);
+        }
     }
 }
 
@@ -359,9 +373,10 @@ SplitWs split_ws(const SplitGeom &q, int widest_rows) {
 
 template <int W, int Z>
 cudaError_t launch_join(const SplitArgs &a, cudaStream_t st) {
-    const int rows = kJoinThreads / 32 / W;
+    const int rows = join_threads(W) / 32 / W;
     const int cuts = a.N < a.G ? a.N : a.G - 1;
-    return launch_after(kda_mla_join_kernel<W, Z>, dim3(cuts, (a.split.R + rows - 1) / rows, Z), dim3(kJoinThreads), 0, st, a);
+    return launch_after(kda_mla_join_kernel<W, Z>, dim3(cuts, (a.split.R + rows - 1) / rows, Z), dim3(join_threads(W)),
+                        W == 1 ? 32768 : 0, st, a);
 }
 
 // the join behind the main kernel
