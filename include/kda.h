@@ -570,8 +570,15 @@ size_t kda_mla_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, in
  *
  * with c_j, p_j the stored values and s_j their scale. Arguments, windows, empty rows, bad tables
  * and the order of calls that share a workspace are as there, but for
- *   cache     device bytes
+ *   cache     device bytes; the scales are the powers of two that kda_mla_append_fp8() writes
  *   workspace kda_mla_decode_fp8_workspace_size() bytes, 256-byte aligned
+ *
+ * The cached values enter the products as they lie. The other operands are two 8-bit numbers each: a
+ * query row's latents keep every bf16 bit down to 2^-17.8 of the row's largest; a probability (times s_j) is
+ * off by at most 2^-7 of itself and 2^-11.9 of the largest in the 9 tiles of 64 rows before its own and the 3 behind it.
+ * Scores, statistics, sums and partial outputs are fp32. A query row with an infinity or a NaN gives NaN in
+ * its own row of o and lse. How the rows are cut, and with that the last bits, depends on the lengths, on
+ * num_seqs, num_heads and num_tokens and on max_pages; a call repeated gives the same bits.
  */
 int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_t *cache, int64_t page_stride,
                        int32_t num_pages, int32_t page_size, const int32_t *page_table, int32_t max_pages,
