@@ -37,7 +37,7 @@ namespace {
 constexpr uint32_t kChunk8 = kKvTile * 128;     // 64 rows of 128 bytes: 128 latents, or the positional key
 constexpr int kChunks = 5;                      // of a tile: 512 latents, then the positional key
 constexpr uint32_t kTile8 = kChunks * kChunk8;
-constexpr int kMaxSlots = 4;
+constexpr int kMaxSlots = 4, kMaxPieces = 2 * kChunks;  // of the ring
 constexpr int kScales = 8;                      // tiles whose scales are kept: more than the ring has, so that a slot is loaded anew only when
                                                 // the softmax is through with its tile
 // Two softmax warps a lane quarter: each takes half of a tile's cached rows, and of O^T's blocks of 128 latents. Behind them
@@ -56,6 +56,8 @@ constexpr int kBad = 8;                         // stretches that the loads may 
 // Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
 // for a wait and a load, which five a tile would make the bound of few rows), or its five chunks where only
 // two tiles fit, each as soon as its products are through.
+// (96 rows with one W and a ring of 12 chunks: 256 x 96 257 -> 268 us, the softmax then waits for the tile before; with two and 11
+// chunks 259 to 264, the places of whose chunks take the issuing threads longer to find.)
 constexpr int tiles_in(int form) { return 4 - form; }
 constexpr int pieces_of(int form) { return form < 2 ? 1 : kChunks; }
 
@@ -76,7 +78,7 @@ struct Args8 : SplitArgs {
 
 struct Smem8 {
     uint64_t q_ready, s_full[2], s_free[2], p_full[2], drained;
-    uint64_t full[kMaxSlots][kChunks], empty[kMaxSlots][kChunks];  // a piece of a tile is there; may be loaded over
+    uint64_t full[kMaxPieces], empty[kMaxPieces];  // a piece of a tile is there; may be loaded over
     uint64_t done[kMaxSlots];           // a tile's products are through
     uint64_t sc_full[kScales];
     alignas(16) float sc[kScales][kKvTile];  // scales of a tile's rows (bulk copies land there)
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
             tc::mbar_init(&sm.drained, 2);
             for (int i = 0; i < kTiles; ++i) {
                 tc::mbar_init(&sm.done[i], 1);
-                for (int c = 0; c < kPieces; ++c) tc::mbar_init(&sm.full[i][c], 1), tc::mbar_init(&sm.empty[i][c], 1);
+                for (int c = 0; c < kPieces; ++c) tc::mbar_init(&sm.full[i * kPieces + c], 1), tc::mbar_init(&sm.empty[i * kPieces + c], 1);
             }
             tc::mbar_init_fence();
         }
@@ -280,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
 #pragma unroll
                         for (int c = 0; c < kPieces; ++c) {  // the positional chunk first
                             const int chunk = c == 0 ? kChunks - 1 : c - 1;
-                            ok = tc::mbar_wait(kPieces == 1 ? &sm.done[ps] : &sm.empty[ps][c], pph ^ 1);
+                            ok = tc::mbar_wait(kPieces == 1 ? &sm.done[ps] : &sm.empty[ps * kPieces + c], pph ^ 1);
                             if (!ok) break;
-                            uint64_t *full = &sm.full[ps][c];
+                            uint64_t *full = &sm.full[ps * kPieces + c];
                             if (kPieces == 1) {
                                 tc::mbar_arrive_expect_tx(full, kChunks * boxes * box);
                                 if (p.rb == kKvTile) {
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) {  // the positional chunk first
                             if (c < kPieces) {
-                                ok = ok && tc::mbar_wait(&sm.full[ps][c], pph);
+                                ok = ok && tc::mbar_wait(&sm.full[ps * kPieces + c], pph);
                                 if (!ok) break;
                                 tc::fence_after_sync();
                             }
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                     if (!kStack) mma8(d, a + 4 * q_step, bb, id, 1);
                                 }
                             }
-                            if (c == 0 && kPieces > 1) tc::commit(&sm.empty[ps][0]);
+                            if (c == 0 && kPieces > 1) tc::commit(&sm.empty[ps * kPieces]);
                         }
                         if (!ok) break;
                         if (++ps == kTiles) ps = 0, pph ^= 1;
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                 mma8(d, a + 256, b + 2, id_hi, 1);
                                 mma8(d, a + 256, b + 6, id_lo, 1);
                             }
-                            if (kPieces > 1) tc::commit(&sm.empty[ps][i + 1]);
+                            if (kPieces > 1) tc::commit(&sm.empty[ps * kPieces + i + 1]);
                         }
                         tc::commit(&sm.done[ps]);
                         if (++ps == kTiles) ps = 0;
@@ -893,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                 tc::mbar_wait(&sm.drained, 0);
                 for (int e = max(0, sm.scaled - kScales); e < sm.scaled; ++e) tc::mbar_wait(&sm.sc_full[e % kScales], (e / kScales) & 1);
                 for (int e = max(0, sm.issued - kTiles * kPieces); e < sm.issued; ++e)
-                    tc::mbar_wait(&sm.full[e / kPieces % kTiles][e % kPieces], (e / kPieces / kTiles) & 1);
+                    tc::mbar_wait(&sm.full[e % (kTiles * kPieces)], (e / kPieces / kTiles) & 1);
             }
         }
         __syncwarp();
@@ -934,7 +936,7 @@ Geom8 geometry8(int32_t H, int32_t m, int64_t most, int32_t sms) {
 static_assert(1024 + sizeof(Smem8) + 5 * 64 * 128 + 32 * 256 + tiles_in(0) * kTile8 <= kSmem8, "32 rows");
 static_assert(1024 + sizeof(Smem8) + 5 * 128 * 128 + 64 * 256 + tiles_in(1) * kTile8 <= kSmem8, "64 rows");
 static_assert(1024 + sizeof(Smem8) + 11 * kMostRows8 * 128 + tiles_in(2) * kTile8 <= kSmem8, "96 rows");
-static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales, "");
+static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales && tiles_in(2) * pieces_of(2) <= kMaxPieces, "");
 static_assert(offsetof(Smem8, sc) % 16 == 0 && kTile8 % 1024 == 0, "bulk copies");
 static_assert(kMaxSlots + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
