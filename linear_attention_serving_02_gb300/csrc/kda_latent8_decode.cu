@@ -26,6 +26,18 @@
 // Rows of a tile behind the sequence's length may hold anything: their scores are replaced by -inf, the
 // product's 32-row steps past the length are left out, and value rows inside the last step are zeroed in shared
 // memory; their scales are never loaded.
+//
+// Three forms by the CTA's query rows, each with the longest ring that its Q and W leave room for: up to 32 (M = 64, four
+// tiles), 64 (M = 128, three) and 96 (hi and lo apart, two). Eight softmax warps hold a tile's scores in registers, a thread
+// 8 or 16 cached rows of one or two query rows (with up to 64 rows as the fragments that tcgen05.ld gives, hi and lo added
+// in place) or 32 of one; three warps' elected threads issue score products, value products and loads. S and W are double, so
+// that a tile's scores are computed under the last one's softmax and value product.
+//
+// What bounds it: a tile takes 1500 to 1680 cycles with 12 rows, where its bytes' share of HBM is 1450; 2200 with 48, the
+// softmax's chain (wait, load, 16 exponentials a thread, a barrier, conversions and 16-bit stores); 3100 with 96, of which
+// the products' operands occupy shared memory for 2600. A sequence costs besides what kda_mla_decode_fp8 counts for it
+// (extra8), and the join 3 to 15 us. Measured, whole calls: 1048576 rows x 12 heads 112 us (6.0 TB/s of 6.8), 32 sequences of
+// up to 8000 rows x 16 25.4, 64 x 48 54.3, 256 x 96 252 (0.87 PFLOP/s as a bf16 form counts), 64 x 96 x 4 tokens 222 (0.93).
 
 #include <cstddef>
 
@@ -44,9 +56,13 @@ constexpr int kScales = 8;                      // tiles whose scales are kept: 
 // stand four more: score issue, value issue, TMA, none. (Four a quarter: 32 rows 112 -> 142 us, 96 rows 312 -> 324.)
 constexpr int kSets = 2, kSetCols = kKvTile / kSets, kBlocks = kLatent / 128 / kSets;
 constexpr int kSoft = 128 * kSets, kIssue = kSoft / 32, kThreads = kSoft + 128;  // kIssue: the first warp behind them
-// Registers that a block is launched with a thread, and how they are shared out
-constexpr int kLaunched = 168, kSoftRegs = 208, kIssueRegs = 80;
-static_assert(kSoft * kSoftRegs + 128 * kIssueRegs <= kThreads * kLaunched, "the shares' sum");
+// Registers that a block is launched with a thread, and how they are shared out. (208 and 80: 32 x 16 27.2 us, 1M x 12
+// 112.8, 64 x 48 58.0, 256 x 96 255.8; 200 and 96: 25.4, 111.5, 57.4, 255.4; 184 and 128: 26.4, 113.2, 56.5, 253.6.)
+constexpr int kLaunched = 168;
+constexpr int soft_regs(int form) { return form == 0 ? 200 : 184; }
+constexpr int issue_regs(int form) { return form == 0 ? 96 : 128; }
+static_assert(kSoft * soft_regs(0) + 128 * issue_regs(0) <= kThreads * kLaunched, "the shares' sum");
+static_assert(kSoft * soft_regs(1) + 128 * issue_regs(1) <= kThreads * kLaunched, "the shares' sum");
 constexpr int kRows8 = 64, kMostRows8 = 96;     // query rows of a CTA at most: with hi and lo in one product, and at all
 constexpr float kSet = 2.5f, kHigh = 8.75f, kReach = 40.0f;  // powers of two
 constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and what is low
@@ -232,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
     bool ok = true;
 
     if (warp >= kIssue) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(issue_regs(FORM)));
         if (warp == kIssue + 2) {
             // ---- TMA producer: one thread ----
             if (tma::elect()) {
@@ -431,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(soft_regs(FORM)));
         // ---- softmax: a thread takes kC cached rows of a tile for each of kR query rows; then the output ----
         const int quarter = warp & 3, set = warp >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -469,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
         auto load_q = [&](int n) {
             const int64_t row0 = (int64_t)n * geo.R + row_first;
             // The loads of kBatch rows are on their way before the first is looked at. (A few rows at a time: this runs once a
-            // sequence, and long code that seldom runs is fetched anew each time.)
-            constexpr int kBatch = FORM == 0 ? 2 : 4;
+            // sequence, and long code that seldom runs is fetched anew each time. 64 x 48 with 1, 2 and 4 56.7, 54.3 and 57.2 us, 256 x 96
+            // with 2, 3 and 4 255.3, 252.5 and 254.0.)
+            constexpr int kBatch = FORM < 2 ? 2 : 3;
 #pragma unroll 1
             for (int q0 = warp; q0 < rows_here; q0 += kIssue * kBatch) {
                 struct {
