@@ -957,6 +957,10 @@ static_assert(tiles_in(0) <= kMaxSlots && kMaxSlots + 2 < kScales && tiles_in(2)
 static_assert(offsetof(Smem8, sc) % 16 == 0 && kTile8 % 1024 == 0, "bulk copies");
 static_assert(kMaxSlots + 2 < kBad, "the loads are fewer stretches ahead than flags are kept");
 
+// The workspace of a call, whatever its page tables hold: row tiles chosen by them are narrower than these, and all groups'
+// row tiles are kMaxGroups at most in both.
+SplitWs workspace8(int32_t H, int32_t m) { return split_ws(geometry8(H, m, INT32_MAX, 0), kMostRows8); }
+
 // What a sequence costs beside its tiles, in tiles: its queries are split and its output written. (With 0, 0, 0 / 3, 4, 6
 // / 4, 6, 8 units: 32 sequences x 16 heads 31.5 / 26.2 / 26.2 us, 64 x 48 71 / 61.4 / 61.3, 64 x 96, four tokens 243 /
 // 226.5 / 226, 256 x 96 303 / 256 / 255.)
@@ -970,7 +974,7 @@ extern "C" {
 size_t kda_mla_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_tokens) {
     if (num_seqs < 0 || num_heads < 0 || num_tokens < 0) return 0;
     if ((int64_t)num_heads * num_tokens > INT32_MAX / 2 || num_heads == 0 || num_tokens == 0) return 256;
-    return kda::split_ws(kda::geometry8(num_heads, num_tokens, INT32_MAX, 0), kda::kMostRows8).total;
+    return kda::workspace8(num_heads, num_tokens).total;
 }
 
 int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_t *cache, int64_t page_stride,
@@ -1003,7 +1007,7 @@ int kda_mla_decode_fp8(const uint16_t *q_lat, const uint16_t *q_pe, const uint8_
     a.geo = geometry8(num_heads, num_tokens, most, sms);
     a.split = a.geo;
     a.extra = extra8(a.geo.form);
-    const SplitWs w = split_ws(a.geo, kMostRows8);
+    const SplitWs w = workspace8(num_heads, num_tokens);
     a.rb = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
     // a cache without pages keeps one page of extent: no id is in range, every load is past it
     // the chunks of a row are a dimension of their own, outside the rows: a box of all of them lands chunk by chunk

@@ -208,3 +208,19 @@ def test_calls_that_follow_one_another_wait_for_one_another(H, m):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(state(), want))
+
+
+@pytest.mark.parametrize("H,m,spare", [(12, 1, 0), (33, 1, 0), (40, 1, 5000), (96, 1, 0), (96, 1, 5000), (64, 3, 0), (100, 2, 5000),
+                                       (128, 16, 0)])
+def test_decode_stays_within_its_workspace(H, m, spare):
+    """Every part of the list's cuts is written (one long sequence and short ones): the bytes on both sides of a
+    workspace of just the size that is asked for stay."""
+    g, lens = _gen(60 + H), [12000, 3, 900]
+    q_lat, q_pe, cache, table = _inputs(g, lens, 64, H, m, tails=False)
+    table = torch.cat([table, torch.full((3, spare), -1, dtype=torch.int32, device="cuda")], 1)
+    size, edge = kda.kda_mla_decode_fp8_workspace_size(3, H, m), 1 << 20
+    room = torch.full((size + 2 * edge,), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = kda.kda_mla_decode_fp8(q_lat, q_pe, cache, table, _ints(lens), SCALE, num_tokens=m,
+                                    workspace=room[edge:edge + size])
+    assert bool((room[:edge] == 0x5A).all()) and bool((room[edge + size:] == 0x5A).all())
+    _check(o, lse, q_lat, q_pe, cache, table, lens, m, SCALE, seqs=(1, 2))

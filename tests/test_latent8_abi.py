@@ -90,3 +90,13 @@ def test_reference_quantiser_rounds_to_the_nearest_value_and_keeps_rows_it_made(
     back = (c * s[:, None].double()).float()
     b2, s2 = ref.quantise(back)
     assert torch.equal(ref.codes(b2) * s2[:, None].double(), back.double())
+
+
+def test_decode_workspace_size_grows_with_the_rows():
+    """More heads or tokens never need less, so a workspace for the most serves the others; and it counts no sequences."""
+    size = kda.kda_mla_decode_fp8_workspace_size
+    for m in (1, 2, 16):
+        sizes = [size(4, H, m) for H in range(1, 200)]
+        assert sizes == sorted(sizes)
+    assert all(size(4, H, 1) <= size(4, H, 2) <= size(4, H, 16) for H in range(1, 200))
+    assert size(1, 96, 4) == size(5000, 96, 4)
