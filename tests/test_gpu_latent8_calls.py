@@ -224,3 +224,68 @@ def test_decode_stays_within_its_workspace(H, m, spare):
                                     workspace=room[edge:edge + size])
     assert bool((room[:edge] == 0x5A).all()) and bool((room[edge + size:] == 0x5A).all())
     _check(o, lse, q_lat, q_pe, cache, table, lens, m, SCALE, seqs=(1, 2))
+
+
+@pytest.mark.parametrize("H,m,lens", [(2048, 5, [700, 90, 33]), (65535, 1, [70]), (4000, 16, [100, 0]), (300, 8, [2000, 17, 300])])
+def test_decode_of_very_many_rows(H, m, lens):
+    """More row tiles than SMs: one list for all blocks and no join; and about as many."""
+    g = _gen(H)
+    q_lat, q_pe, cache, table = _inputs(g, lens, 32, H, m)
+    st = _status()
+    o, lse = kda.kda_mla_decode_fp8(q_lat, q_pe, cache, table, _ints(lens), SCALE, num_tokens=m, status=st)
+    assert st.item() == 0
+    _check(o, lse, q_lat, q_pe, cache, table, lens, m, SCALE)
+
+
+@pytest.mark.parametrize("H,m", [(12, 1), (96, 4), (2048, 5)])
+def test_streams_that_fork_and_join(H, m):
+    """main: append, decode, | side: gather of what append wrote; joined: a page copy over both, a decode of the copy.
+    Eagerly without pauses and as a graph they give the bits of calls with a synchronisation behind each."""
+    g, size, lens = _gen(70 + H), 32, [700, 90, 33]
+    N = len(lens)
+    q0, p0, cache0, table = _inputs(g, lens, size, H, m, tails=False)
+    down, rope, lens_d, cu = _rand(g, N * m, ROW), _rope(800), _ints(lens), _ints(_cu(lens))
+    cu_q = _ints(_cu([m] * N))
+    ws = [torch.empty(kda.kda_mla_decode_fp8_workspace_size(N, H, m), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache, q_pe = cache0.clone(), p0.clone()
+    o, lse = torch.empty_like(q0), torch.empty(N * m, H, device="cuda")
+    o2, lse2 = torch.empty_like(q0), torch.empty_like(lse)
+    rows = torch.empty(sum(lens), ROW, dtype=torch.bfloat16, device="cuda")
+    side, src, dst = torch.cuda.Stream(), int(table[1, 0]), int(table[0, 3])
+
+    def step(pause=lambda: None):
+        main = torch.cuda.current_stream()
+        cache.copy_(cache0), q_pe.copy_(p0)
+        kda.kda_mla_append_fp8(down[:, :LATENT], down[:, LATENT:], cache, table, lens_d, cu_q, rope=rope, q_pe=q_pe, q_out=q_pe)
+        pause()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kda.kda_mla_gather_fp8(cache, table, cu, sum(lens), out=rows)
+            pause()
+        kda.kda_mla_decode_fp8(q0, q_pe, cache, table, lens_d, SCALE, m, o, lse, ws[0])
+        pause()
+        main.wait_stream(side)
+        kda.kda_pages_copy(cache[None], [src], [dst])
+        pause()
+        kda.kda_mla_decode_fp8(o, q_pe, cache, table, lens_d, SCALE, m, o2, lse2, ws[1])
+        pause()
+
+    def state():
+        torch.cuda.synchronize()
+        return [x.clone() for x in (cache, q_pe, o, lse, rows, o2, lse2)]
+
+    step(torch.cuda.synchronize)
+    want = state()
+    assert all(bool(torch.isfinite(x.float()).all()) for x in want)
+    for _ in range(5):
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(state(), want))
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=warm):
+        step()
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(state(), want))
