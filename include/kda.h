@@ -574,8 +574,11 @@ size_t kda_mla_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, in
  *   workspace kda_mla_decode_fp8_workspace_size() bytes, 256-byte aligned
  *
  * The cached values enter the products as they lie. The other operands are two 8-bit numbers each: a
- * query row's latents keep every bf16 bit down to 2^-17.8 of the row's largest; a probability (times s_j) is
- * off by at most 2^-7 of itself and 2^-11.9 of the largest in the 9 tiles of 64 rows before its own and the 3 behind it.
+ * query row's latents keep every bf16 bit down to 2^-17.8 of the row's largest; a weight (a probability times s_j) is
+ * off by at most 2^-7.8 of itself (a bf16's rounding is 2^-8), or, where that is more, 2^-13.9 of a unit, and by 2^-53 of
+ * the row's largest weight besides. With the cached rows in tiles of 64 the unit is at most the larger of 2^-2.5 of the largest
+ * weight in the 9 tiles that end with its own and 1/8 of the largest sum of four tiles in a row among them, the weights
+ * of the sequence's first 8 rows counting 2^-6.2 of theirs.
  * Scores, statistics, sums and partial outputs are fp32. A query row with an infinity or a NaN gives NaN in
  * its own row of o and lse. How the rows are cut, and with that the last bits, depends on the lengths, on
  * num_seqs, num_heads and num_tokens and on max_pages; a call repeated gives the same bits.

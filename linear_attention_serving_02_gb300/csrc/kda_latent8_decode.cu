@@ -17,11 +17,18 @@
 //   Values. The weight w = 2^{x_rj + e_j - m_r} takes the row's scale along; it is e4m3 and, its rest, e5m2, whose
 //   range goes on 2^-7 further down. O^T = C^T W^T: M = 128 latents (the same tile, read MN-major), N = query rows.
 //
-// e4m3's range holds a weight to 2^-9 of the unit, so m_r follows the weights both ways: it is set 2^2.5 below a
-// tile's largest, and set anew, with O^T rescaled, where a tile's largest is over 2^8.75, or the largest of four
-// tiles under 2^-1. (A first token that outweighs all others would else leave these without bits. Four tiles
-// of low weights lose at most 4 64 2^-13 next to the 2^2.5 that set the unit, whatever they hold.) It stays within 2^40
-// of the largest seen, beyond which a tile counts for nothing.
+// The two hold a weight of 2^-6 to 448 units as bf16 would, to 2^-8 of itself; a lower one is off by up to 2^-14 units. So
+// m_r follows the weights both ways, and is set anew, with O^T rescaled, where
+//   a tile's largest weight is over 2^8.75: then at 2^6, so that the others keep 12 binary places below it;
+//   four tiles' weights sum to less than 8: then their sum at 2^7 (or the tile's largest at 2^2.5, if that is the larger unit).
+// Tiles of weights that sum to more lose at most 256 2^-14 of 8, 2^-9, whatever they hold. A stretch's first tile has its largest at
+// 2^2.5, which leaves room to grow; but the first 8 rows of a sequence, which often outweigh all others, may be 2^6.2 above
+// that. m_r stays within 2^40 of the largest seen (2^46.2 of those rows), beyond which a tile counts for nothing.
+// The other rows' part of the output beside a first key of 0.95 of the sum is off by 0.2% (rms; bf16 weights 0.23%), beside one of
+// 0.999 by 1.8%; beside a key of 0.9 or 0.99 in the middle by 0.3% and 1.0%, until the unit has followed. (With the largest of four
+// tiles held above 2^-1 by 2^2.5 these were 2.4, 25, 1.0 and 3.7%.) How often the unit is set, emulated: with
+// random scores of a deviation of 1.7 natural units in 5% of the tiles of 96 rows, of 3.0 in 65%, which each take a third longer;
+// another look a tile behind every new maximum would make 0.15% of the 0.3, and 88% of the 65.
 //
 // Rows of a tile behind the sequence's length may hold anything: their scores are replaced by -inf, the
 // product's 32-row steps past the length are left out, and value rows inside the last step are zeroed in shared
@@ -64,9 +71,14 @@ constexpr int issue_regs(int form) { return form == 0 ? 96 : 128; }
 static_assert(kSoft * soft_regs(0) + 128 * issue_regs(0) <= kThreads * kLaunched, "the shares' sum");
 static_assert(kSoft * soft_regs(1) + 128 * issue_regs(1) <= kThreads * kLaunched, "the shares' sum");
 constexpr int kRows8 = 64, kMostRows8 = 96;     // query rows of a CTA at most: with hi and lo in one product, and at all
-constexpr float kSet = 2.5f, kHigh = 8.75f, kReach = 40.0f;  // powers of two
-constexpr float kMost = 430.0f, kLeast = 0.5f;  // weights: below 2^kHigh, and what is low
+// Powers of two: where a unit is set below the largest weight of a stretch's first tile, and of one above the unit's range; how far it
+// is set below the sum of a low window; what the first rows of a sequence may be above the others of their tile
+constexpr float kSet = 2.5f, kSetHigh = 6.0f, kSetLow = 7.0f, kHigh = 8.75f, kEarly = 6.2f, kReach = 40.0f;
+constexpr float kMost = 430.0f;                 // weights: below 2^kHigh
+constexpr float kLeast = 8.0f, kNothing = 0x1p-14f;  // a window's sum: what is low, and what fp16 has nothing left of
 constexpr int kWindow = 4;                      // tiles over which a row's weights have to be low
+constexpr int kEarlyRows = 8;
+static_assert(kSet + kEarly < kHigh, "the first rows stay in range");
 constexpr int kBad = 8;                         // stretches that the loads may be ahead of the output
 
 // Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
@@ -100,7 +112,7 @@ struct Smem8 {
     alignas(16) float sc[kScales][kKvTile];  // scales of a tile's rows (bulk copies land there)
     float row_c[kMostRows8];            // by query row: log2(e) scale times the unit of Q
     float factor[128];                  // by query row: scale of O^T
-    float part[kSets][128], recent[kSets][128];  // by query row: the sets' maxima or sums, and largest weights of a window
+    float part[kSets][128], recent[kSets][128];  // by query row: the sets' maxima or sums, and sums of a window's weights
     uint32_t tmem;
     int32_t failed, bad[kBad];
     Run run;
@@ -147,6 +159,10 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
 }
 __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
     asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
     return a;
 }
 // A pair of fp16 as two bytes of e4m3 and two for the rests: e5m2 for weights, which goes on further down, and e4m3 for
@@ -476,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
             w_64[y] = unit & 4 ? -64 : 64;
             limit[y] = owner[y] ? kMost : INFINITY;
         }
-        // the largest weight of a row's last window
-        auto window = [&](int row) { return fmaxf(sm.recent[0][row], sm.recent[1][row]); };
+        // the sum of the weights of a row's last window
+        auto window = [&](int row) { return sm.recent[0][row] + sm.recent[1][row]; };
         int k = 0, seg = 0;  // tiles and stretches worked on
         // the products of tile t are through: waited for in every tile for the one before the last, so that none is passed over
         auto through = [&](int t) { return tma::wait_warp(&sm.done[t % kTiles], (t / kTiles) & 1); };
@@ -548,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
         }
         for (; !w.done() && ok; w.next(p)) {
             float m_ref[kR], m_top[kR], l[kR];
-            float recent[kR];  // the largest weight of the window, and at its end of the whole row
+            float recent[kR];  // the sum of the window's weights, and at its end of the whole row
             bool faint[kR];    // the last window's weights were low
             float m_kept[kR], l_kept[kR];  // reference and denominator of the tiles before the last kFold
 #pragma unroll
@@ -605,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                         scales();
                         const uint32_t s_at = t_s + lanes + (k & 1) * kKvTile + set * kSetCols;
                         const bool live = warp_rows && ok;
-                        float sum[kR], most[kR];
+                        float sum[kR], most[kR], mass[kR];               // of a row's weights here: without scales, the largest, the sum
                         // (scores are rounded before a reference is taken off, so that huge ones still differ by 0 from themselves)
                         auto scores = [&] {
                             if constexpr (FORM == 2) {
@@ -660,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                 const float mb = m_ref[y] == -INFINITY ? 0.f : -m_ref[y];
                                 const uint64_t mb2 = pk2(mb, mb);
                                 uint64_t l2[2] = {0, 0};
-                                uint32_t top = 0x00010001u;  // (2^-24: what fp16 rounds to nothing is there all the same)
+                                uint32_t top = 0, all = 0;
 #pragma unroll
                                 for (int e = 0; e < kC / 2; ++e) {
                                     const float2 x = upk2(add2(x2[y][e], mb2));
@@ -669,15 +685,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                     const float2 ww = upk2(mul2(pp, pk2(sc[2 * e], sc[2 * e + 1])));
                                     w16[y][e] = half2_of(ww.x, ww.y);
                                     top = max_half2(top, w16[y][e]);
+                                    all = add_half2(all, w16[y][e]);
                                 }
                                 const float2 ls = upk2(add2(l2[0], l2[1]));
                                 sum[y] = ls.x + ls.y;
                                 const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&top));
                                 most[y] = fmaxf(t.x, t.y);
+                                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&all));
+                                mass[y] = a.x + a.y;
                             }
                         };
 #pragma unroll
-                        for (int y = 0; y < kR; ++y) sum[y] = most[y] = 0.f;
+                        for (int y = 0; y < kR; ++y) sum[y] = most[y] = mass[y] = 0.f;
                         if (live && !first) {
                             scores();
                             weights();
@@ -701,10 +720,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                 top[y] = -INFINITY;
                                 if (live) {
                                     auto of_scale = [&](int e) { return (float)((int)(__float_as_uint(sc[e]) >> 23) - 127); };  // its exponent
+                                    const float early = j == 0 && set == 0 ? kEarly : 0.f;
 #pragma unroll
                                     for (int e = 0; e < kC / 2; ++e) {
                                         const float2 x = upk2(x2[y][e]);
-                                        top[y] = fmaxf(top[y], fmaxf(x.x + of_scale(2 * e), x.y + of_scale(2 * e + 1)));
+                                        float t = fmaxf(x.x + of_scale(2 * e), x.y + of_scale(2 * e + 1));
+                                        if (2 * e < (kStack ? kEarlyRows / 4 : kEarlyRows)) t -= early;
+                                        top[y] = fmaxf(top[y], t);
                                     }
                                 }
                                 if constexpr (kStack) {
@@ -725,9 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                 top[y] = fmaxf(sm.part[0][r[y]], sm.part[1][r[y]]);
                                 m_top[y] = fmaxf(m_top[y], top[y]);
                                 const bool up = first || top[y] - m_ref[y] > kHigh;
-                                // of low weights, the window's largest, which is still in sm.recent
-                                const float low = m_ref[y] + __log2f(window(r[y]));
-                                const float to = fmaxf((up ? top[y] : fmaxf(top[y], low)) - kSet, m_top[y] - kReach);
+                                // of low weights, the window's sum, which is still in sm.recent
+                                const float lately = window(r[y]), low = lately < kNothing ? -INFINITY : m_ref[y] + __log2f(lately) - kSetLow;
+                                const float to = fmaxf(up ? top[y] - (first ? kSet : kSetHigh) : fmaxf(top[y] - kSet, low), m_top[y] - kReach);
                                 anew[y] = up || (faint[y] && to < m_ref[y]);
                                 const float f = anew[y] && !first ? tc::ex2(m_ref[y] - to) : 1.0f;
                                 if (set == 0 && lead) sm.factor[r[y]] = f;
@@ -801,16 +823,16 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                         tc::fence_before_sync();
                         tma::arrive_warp(&sm.p_full[k & 1]);
                         s_there = peek(&sm.s_full[(k + 1) & 1], ((k + 1) >> 1) & 1);
-                        // low weights: a window's largest is left in shared memory behind its last tile, and looked at behind the next
+                        // low weights: a window's sum is left in shared memory behind its last tile, and looked at behind the next
                         const int of_window = (j - w.j0) & (kWindow - 1);
 #pragma unroll
                         for (int y = 0; y < kR; ++y) {
                             l[y] += sum[y];
-                            recent[y] = fmaxf(recent[y], most[y]);
+                            recent[y] += mass[y];
                             if (of_window == kWindow - 1) {
                                 if constexpr (kStack) {
-                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 1));
-                                    recent[y] = fmaxf(recent[y], __shfl_xor_sync(0xffffffffu, recent[y], 2));
+                                    recent[y] += __shfl_xor_sync(0xffffffffu, recent[y], 1);
+                                    recent[y] += __shfl_xor_sync(0xffffffffu, recent[y], 2);
                                 }
                                 if (lead) sm.recent[set][r[y]] = recent[y];
                                 recent[y] = 0.f;
