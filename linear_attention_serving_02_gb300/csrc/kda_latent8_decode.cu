@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
             for (int i = 0; i < kScales; ++i) tc::mbar_init(&sm.sc_full[i], 1);
             for (int i = 0; i < kBad; ++i) sm.bad[i] = 0;
             tc::mbar_init(&sm.q_ready, kIssue);
-            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 1), tc::mbar_init(&sm.s_free[i], kIssue);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.s_full[i], 2), tc::mbar_init(&sm.s_free[i], kIssue);
             for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.p_full[i], kIssue);
             tc::mbar_init(&sm.drained, 2);
             for (int i = 0; i < kTiles; ++i) {
@@ -411,11 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                         if (!ok) break;
                         if (++ps == kTiles) ps = 0, pph ^= 1;
                         // With the scores the softmax may count on the tile's scales, and on the weights of the tile two before
-                        // having been used. One thread waits for these instead of every warp.
+                        // having been used. One thread waits for these instead of every warp, and passes them on by an arrival of
+                        // its own: a commit's covers only what the tensor core did.
                         ok = tc::mbar_wait(&sm.sc_full[k % kScales], (k / kScales) & 1) &&
                              (k < 2 || tc::mbar_wait(&sm.done[(k - 2) % kTiles], ((k - 2) / kTiles) & 1));
                         if (!ok) break;
                         tc::commit(&sm.s_full[k & 1]);
+                        tma::arrive(&sm.s_full[k & 1]);
                     }
                     ++seg;
                     w.next(p);
@@ -755,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                 if (set == 0 && lead) sm.factor[r[y]] = f;
                                 if (anew[y]) m_ref[y] = to;
                                 if (anew[y]) recent[y] = 0.f;
-                                // a row that has seen nothing yet looks again; one with a NaN in it never will (in every tile it would, for
-                                // 1.4 to 1.5 times the time of all rows of the block)
+                                // a row that has seen nothing yet looks again; one with a NaN in it never will, and would do so in every tile
+                                // (1.4 to 1.5 times the time, for all rows of the block)
                                 faint[y] = owner[y] && m_ref[y] == -INFINITY && c[y] == c[y];
                                 l[y] *= f;
                                 again |= owner[y] && anew[y] && !first;
