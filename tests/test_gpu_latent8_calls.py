@@ -226,6 +226,19 @@ def test_decode_stays_within_its_workspace(H, m, spare):
     _check(o, lse, q_lat, q_pe, cache, table, lens, m, SCALE, seqs=(1, 2))
 
 
+@pytest.mark.parametrize("H,m,spare", [(12, 1, 0), (33, 1, 0), (40, 1, 5000), (96, 1, 0), (96, 1, 5000), (64, 3, 0), (100, 2, 5000),
+                                       (128, 16, 0)])
+def test_decode_of_a_long_sequence_from_a_workspace_of_its_size(H, m, spare):
+    """The sequence that is cut into many parts, joined from just the workspace that is asked for: parts that overlapped in
+    it would show."""
+    g, lens = _gen(80 + H), [12000, 3, 900]
+    q_lat, q_pe, cache, table = _inputs(g, lens, 64, H, m)
+    table = torch.cat([table, torch.full((3, spare), -1, dtype=torch.int32, device="cuda")], 1)
+    ws = torch.full((kda.kda_mla_decode_fp8_workspace_size(3, H, m),), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = kda.kda_mla_decode_fp8(q_lat, q_pe, cache, table, _ints(lens), SCALE, num_tokens=m, workspace=ws)
+    _check(o, lse, q_lat, q_pe, cache, table, lens, m, SCALE)
+
+
 @pytest.mark.parametrize("H,m,lens", [(2048, 5, [700, 90, 33]), (65535, 1, [70]), (4000, 16, [100, 0]), (300, 8, [2000, 17, 300])])
 def test_decode_of_very_many_rows(H, m, lens):
     """More row tiles than SMs: one list for all blocks and no join; and about as many."""
