@@ -144,3 +144,44 @@ def test_decode_of_positional_scores_alone(H):
     q_pe = torch.randn(1, H, POS, generator=g).to(torch.bfloat16).cuda()
     o, lse = kda.kda_mla_decode_fp8(q_lat, q_pe, cache, table.cuda(), _ints([n]), SCALE)
     _check(o, lse, q_lat, q_pe, cache, table.cuda(), [n], 1, SCALE)
+
+
+@pytest.mark.parametrize("H,m", [(2, 1), (33, 3)])
+def test_the_longest_sequence_and_the_largest_pages(H, m):
+    """Pages of 65,536 rows and the 2,147,418,112 that 32,767 of them hold: rows written and read back at the end, and all of
+    them attended. Half of the pages' rows hold 1 in latent 0, the others' in latent 1, but the last three, the new ones, in 2."""
+    size, pages = 65536, 32767
+    n = size * pages
+    cache = _cache(3, size)
+    rows, scales = ref.parts(cache)
+    one, s = ref.quantise(torch.eye(3, ROW, device="cuda"))
+    for page, kind in ((0, 0), (1, 1), (2, 1)):
+        rows[page], scales[page] = one[kind], s[kind]
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None] % 2
+    table[0, -1] = 2
+    down = torch.zeros(3, ROW, dtype=torch.bfloat16, device="cuda")
+    down[:, 2] = 1
+    st, lens = _status(), _ints([n])
+    kda.kda_mla_append_fp8(down[:, :LATENT], down[:, LATENT:], cache, table, lens, status=st)
+    end = kda.kda_mla_gather_fp8(cache, table, _ints([0, 9]), 9, starts=_ints([n - 9]), status=st)
+    want = torch.zeros(9, ROW, device="cuda")
+    want[:6, 1] = want[6:, 2] = 1
+    assert torch.equal(end.float(), want)
+    q_lat = torch.zeros(m, H, LATENT, dtype=torch.bfloat16, device="cuda")
+    q_pe = torch.zeros(m, H, POS, dtype=torch.bfloat16, device="cuda")
+    q_lat[..., 2] = 16 * LN2  # the new rows score 2^16
+    o, lse = kda.kda_mla_decode_fp8(q_lat, q_pe, cache, table, lens, 1.0, num_tokens=m, status=st)
+    assert st.item() == 0
+    score = float(torch.tensor(16 * LN2).bfloat16())
+    for t in range(m):
+        new = (3 - (m - 1 - t)) * math.exp(score)
+        share = torch.tensor([size * (pages // 2), size * (pages // 2 + 1) - 3, new], dtype=torch.float64)
+        total = share.sum()
+        want = torch.zeros(LATENT, dtype=torch.float64)
+        want[:3] = share / total
+        # (beside the new rows the last nine tiles' weights are off by 2^-13.9 of a unit of 2^-2.5 of theirs: 576 2^-16.4 2^16 in all)
+        more = 576 * 2.0 ** -16.4 * math.exp(score) / total
+        assert bool(((o[t].double().cpu() - want).abs() <= TOL_O * want + more * (want > 0)).all()), t
+        assert bool(((lse[t].double().cpu() - total.log()).abs() <= TOL_LSE + 2.0 ** -22 * total.log()).all()), t
+    far = kda.kda_mla_gather_fp8(cache, table, _ints([0, 2]), 2, starts=_ints([n - 1]), status=st)
+    assert st.item() == -4 and bool(far[1].isnan().all()) and torch.equal(far[0].float(), end[8].float())
