@@ -40,11 +40,13 @@
 // in place) or 32 of one; three warps' elected threads issue score products, value products and loads. S and W are double, so
 // that a tile's scores are computed under the last one's softmax and value product.
 //
-// What bounds it: a tile takes 1500 to 1680 cycles with 12 rows, where its bytes' share of HBM is 1450; 2200 with 48, the
-// softmax's chain (wait, load, 16 exponentials a thread, a barrier, conversions and 16-bit stores); 3100 with 96, of which
-// the products' operands occupy shared memory for 2600. A sequence costs besides what kda_mla_decode_fp8 counts for it
-// (extra8), and the join 3 to 15 us. Measured, whole calls: 1048576 rows x 12 heads 112 us (6.0 TB/s of 6.8), 32 sequences of
-// up to 8000 rows x 16 25.4, 64 x 48 54.3, 256 x 96 252 (0.87 PFLOP/s as a bf16 form counts), 64 x 96 x 4 tokens 222 (0.93).
+// What bounds it (at 2070 MHz): a tile takes 1830 cycles, 0.885 us, with up to 32 rows, which is the rows' arrival (7.1 TB/s); 2360 to 2440
+// with 48, the softmax's chain (wait, load, 16 exponentials a thread, a barrier, conversions and 16-bit stores); 3750 with 96,
+// of which the products' operands occupy shared memory for 2600. A sequence costs besides what kda_mla_decode_fp8 counts for it
+// (extra8), 5 to 16 us, and the join 3 to 16. Measured, whole calls: 1048576 rows x 12 heads 112 us (6.0 TB/s of 6.8), 32
+// sequences of up to 8000 rows x 16 25.3 (pages of 64 rows 23.7), 64 x 48 55.5, 256 x 96 251 to 255 (0.87 PFLOP/s as a bf16 form
+// counts), 64 x 96 x 4 tokens 220 (0.94). With pages of 32 and 16 rows 1048576 x 12 takes 131 and 159 us: ten and twenty loads a
+// tile by one thread.
 
 #include <cstddef>
 
@@ -82,7 +84,7 @@ static_assert(kSet + kEarly < kHigh, "the first rows stay in range");
 constexpr int kBad = 8;                         // stretches that the loads may be ahead of the output
 
 // Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
-// for a wait and a load, which five a tile would make the bound of few rows), or its five chunks where only
+// for a wait and a load, which five a tile would make the bound of few rows, as the small pages' ten and twenty loads do), or its five chunks where only
 // two tiles fit, each as soon as its products are through.
 // (96 rows with one W and a ring of 12 chunks: 256 x 96 257 -> 268 us, the softmax then waits for the tile before; with two and 11
 // chunks 259 to 264, the places of whose chunks take the issuing threads longer to find.)

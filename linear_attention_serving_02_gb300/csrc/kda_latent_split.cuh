@@ -3,8 +3,8 @@
 // long stretches, and the join of the sequences that a run's border cuts.
 //
 // Beginning and ending a sequence costs a run time too. In the list a sequence may therefore stand for
-// some units more than its tiles, in front of them (SplitArgs::extra; one at least, the 8-bit form's cost is
-// measured there), so that a run of many short sequences is given fewer tiles.
+// some units more than its tiles, in front of them (SplitArgs::extra: none in the bf16 form; the 8-bit form's
+// are measured there), so that a run of many short sequences is given fewer tiles.
 #pragma once
 
 #include "kda_common.cuh"
