@@ -40,8 +40,8 @@
 // in place) or 32 of one; three warps' elected threads issue score products, value products and loads. S and W are double, so
 // that a tile's scores are computed under the last one's softmax and value product.
 //
-// What bounds it (at 2070 MHz): a tile takes 1830 cycles, 0.885 us, with up to 32 rows, which is the rows' arrival (7.1 TB/s); 2360 to 2440
-// with 48, the softmax's chain (wait, load, 16 exponentials a thread, a barrier, conversions and 16-bit stores); 3750 with 96,
+// What bounds it (at 2070 MHz): a tile takes 1830 cycles, 0.885 us, with up to 32 rows, which is the rows' arrival (7.1 TB/s); 2360
+// to 2440 with 48, the softmax's chain (wait, load, 16 exponentials a thread, a barrier, conversions and 16-bit stores); 3750 with 96,
 // of which the products' operands occupy shared memory for 2600. A sequence costs besides what kda_mla_decode_fp8 counts for it
 // (extra8), 5 to 16 us, and the join 3 to 16. Measured, whole calls: 1048576 rows x 12 heads 112 us (6.0 TB/s of 6.8), 32
 // sequences of up to 8000 rows x 16 25.3 (pages of 64 rows 23.7), 64 x 48 55.5, 256 x 96 251 to 255 (0.87 PFLOP/s as a bf16 form
@@ -84,8 +84,8 @@ static_assert(kSet + kEarly < kHigh, "the first rows stay in range");
 constexpr int kBad = 8;                         // stretches that the loads may be ahead of the output
 
 // Tiles that the ring holds beside Q and W, and the pieces that a tile is loaded in: one (a thread takes 600 cycles
-// for a wait and a load, which five a tile would make the bound of few rows, as the small pages' ten and twenty loads do), or its five chunks where only
-// two tiles fit, each as soon as its products are through.
+// for a wait and a load, which five a tile would make the bound of few rows, as the small pages' ten and twenty loads do), or
+// its five chunks where only two tiles fit, each as soon as its products are through.
 // (96 rows with one W and a ring of 12 chunks: 256 x 96 257 -> 268 us, the softmax then waits for the tile before; with two and 11
 // chunks 259 to 264, the places of whose chunks take the issuing threads longer to find.)
 constexpr int tiles_in(int form) { return 4 - form; }
@@ -759,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_mla_decode_fp8_kernel(const _
                                 if (set == 0 && lead) sm.factor[r[y]] = f;
                                 if (anew[y]) m_ref[y] = to;
                                 if (anew[y]) recent[y] = 0.f;
-                                // a row that has seen nothing yet looks again; one with a NaN in it never will, and would do so in every tile
-                                // (1.4 to 1.5 times the time, for all rows of the block)
+                                // A row that has seen nothing yet looks again. Not one with a NaN in it, which never sees anything
+                                // and would take all rows of the block through this in every tile (1.4 to 1.5 times the time).
                                 faint[y] = owner[y] && m_ref[y] == -INFINITY && c[y] == c[y];
                                 l[y] *= f;
                                 again |= owner[y] && anew[y] && !first;

@@ -67,7 +67,7 @@ def _sinks(share, count=1, at=0):
 
 
 def _windows(low):
-    """Half of the weights' unit once in four tiles, and a first key that sets the unit."""
+    """One key far above the others in four tiles, and a first key above these."""
     def of(n):
         x = torch.full((n,), -low * math.log(2.0))
         strong = torch.arange(5, n, 4 * TILE)
