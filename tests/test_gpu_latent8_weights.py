@@ -8,7 +8,9 @@ that), by a stretch's first tile (2^-2.5), behind low weights (2^-2.5 of the til
 stays for the next tiles only where four tiles' weights sum to 8 u. Each of these happened in the 9 tiles up to a weight's own,
 so there u <= max(2^-2.5 w, sum of w over 4 tiles / 8). The first 8 rows of a sequence count 2^-6.2 of theirs in its first tile. The
 unit stays above 2^-40 of the largest weight of all (2^-46.2 of those rows'), which adds 2^-53 of it.
-Scores, sums and roundings are as in tests/latent8_ref.py."""
+Scores, sums and roundings are as in tests/latent8_ref.py, whose own term for low weights (2^-11.9 of the largest one near,
+counted for all 64 rows of a tile) follows from a unit held by the largest weight of four tiles: the outputs that it is used
+for stay within it, but what the kernel promises is the bound here."""
 import math
 
 import pytest
